@@ -124,6 +124,50 @@ int paged_kv_write_rope(const pkv_bf16 *k, const pkv_bf16 *v, pkv_bf16 *q, int32
                         pkv_bf16 *v_cache, const pkv_cache_desc *cache, void *stream);
 
 /*
+ * paged_kv_copy_blocks -- pages of the pool copied to other pages of it, in the caches of
+ * every layer: the copy-on-write of sequences that were forked ("mini-vLLM" README,
+ * architecture diagram: a Block Manager hands out the physical blocks; with
+ * pkv_bm_fork several sequences share them, and pkv_bm_append_slots_cow names the
+ * pairs to copy here before the next paged_kv_write).
+ *
+ * k_caches and v_caches are HOST arrays of num_layers device pointers, each to one
+ * layer's cache of the shape `cache`; they are read before the call returns.  For every
+ * pair i < num_pairs (block_pairs is DEVICE int32 [num_pairs][2]: source, destination),
+ * every layer and kv head h, and every row t < n_i:
+ *   k_cache[dst][h][t][:] = k_cache[src][h][t][:]   (bit copy; v alike)
+ * with n_i = num_tokens[i] (DEVICE int32 [num_pairs], clamped to [0, block_size] with
+ * PKV_DEVERR_CONTEXT_LEN) or, where num_tokens is NULL, block_size.  The destination's
+ * other rows are left as they were.  A source may appear in several pairs; a pair with
+ * src == dst does nothing; a pair with a block outside the pool is skipped and raises
+ * PKV_DEVERR_BLOCK_ID.  The copies of a call are not ordered among themselves: a
+ * destination must be neither another pair's source nor its destination, or that block's
+ * rows hold a mix of the values they could have had.  head_dim: any multiple of 8; any
+ * positive block_size; caches 16-byte, block_pairs 8-byte, num_tokens 4-byte aligned.  One launch
+ * per 64 layers.
+ */
+int paged_kv_copy_blocks(pkv_bf16 *const *k_caches, pkv_bf16 *const *v_caches,
+                         int32_t num_layers, const int32_t *block_pairs,
+                         const int32_t *num_tokens, int64_t num_pairs,
+                         const pkv_cache_desc *cache, void *stream);
+
+/*
+ * paged_kv_compact -- the device half of a compaction (pkv_bm_compact plans it): whole
+ * pages moved as by paged_kv_copy_blocks(block_moves [num_moves][2]), and the entries of
+ * block_tables [num_seqs][max_blocks_per_seq] (DEVICE int32, in place) replaced through
+ * block_map (DEVICE int32 [num_blocks]: a block's place after the move):
+ *   block_tables[i] = block_map[block_tables[i]]   for entries >= 0.
+ * Entries outside the pool, or that block_map sends outside it, are left and raise
+ * PKV_DEVERR_BLOCK_ID.  The pages that were moved keep their old contents.  No move's
+ * destination may be another move's source or destination (a plan moves into free
+ * blocks only).  With num_seqs == 0 only pages move.  Applying the same plan twice
+ * changes nothing more.
+ */
+int paged_kv_compact(pkv_bf16 *const *k_caches, pkv_bf16 *const *v_caches, int32_t num_layers,
+                     const int32_t *block_moves, int64_t num_moves, int32_t *block_tables,
+                     int64_t num_seqs, int32_t max_blocks_per_seq, const int32_t *block_map,
+                     const pkv_cache_desc *cache, void *stream);
+
+/*
  * paged_decode_plan -- the launcher's split choice ("vLLM-Style Llama Inference
  * Engine", Features and scope, where split-K decode is the named next step).
  *
@@ -400,10 +444,34 @@ int pkv_bm_add_sequence(pkv_block_manager *m, int64_t seq_id, int64_t num_tokens
  * when a sequence's last block is full.  All or nothing. */
 int pkv_bm_append_slots(pkv_block_manager *m, const int64_t *seq_ids, int32_t n,
                         int64_t *slot_mapping);
-/* A finished sequence releases its blocks. */
+/* A finished sequence releases its blocks; a block that forks share is freed with the
+ * last of them. */
 int pkv_bm_free_sequence(pkv_block_manager *m, int64_t seq_id);
 /* Preempt the most recently admitted sequence (LIFO): release its blocks, report its id. */
 int pkv_bm_preempt_lifo(pkv_block_manager *m, int64_t *seq_id);
+/* Admit child_id as a fork of parent_id: the same length and the same blocks, shared (no
+ * block is allocated).  pkv_bm_append_slots refuses (PKV_ERR_UNSUPPORTED) to append into a
+ * shared, partly filled last block, which it would have to copy first. */
+int pkv_bm_fork(pkv_block_manager *m, int64_t parent_id, int64_t child_id);
+/* pkv_bm_append_slots with copy-on-write: a sequence whose last block is shared and partly
+ * filled gets a block of its own, and (old, new) goes to block_pairs[i][2] with the tokens
+ * to copy to num_tokens[i], *num_pairs of them (at most n; the arrays hold n pairs), for
+ * paged_kv_copy_blocks ahead of the step's write.  All or nothing. */
+int pkv_bm_append_slots_cow(pkv_block_manager *m, const int64_t *seq_ids, int32_t n,
+                            int64_t *slot_mapping, int32_t *block_pairs, int32_t *num_tokens,
+                            int32_t *num_pairs);
+/* Shorten a sequence to num_tokens tokens (at most its length): blocks past them are
+ * released (e.g. the slots of rejected draft tokens). */
+int pkv_bm_truncate(pkv_block_manager *m, int64_t seq_id, int64_t num_tokens);
+/* Sequences that hold this block (0: free), or a negative error code. */
+int32_t pkv_bm_ref_count(pkv_block_manager *m, int32_t block);
+/* Plan a compaction: the blocks in use move to the lowest ids.  Writes the moves (source,
+ * destination; destinations are free blocks) to block_moves [max_moves][2], their count to
+ * *num_moves, and every block's place after them to block_map [num_blocks] (its own id
+ * where it does not move), and moves the manager's own tables.  PKV_ERR_NOSPACE, with the
+ * count wanted in *num_moves and nothing changed, when max_moves is too small. */
+int pkv_bm_compact(pkv_block_manager *m, int32_t *block_moves, int64_t max_moves,
+                   int64_t *num_moves, int32_t *block_map);
 /* Block tables [n][max_blocks_per_seq] (unused entries -1) and context lengths [n] of the
  * listed sequences, ready to copy to the device for paged_decode_attention. */
 int pkv_bm_block_tables(pkv_block_manager *m, const int64_t *seq_ids, int32_t n,

@@ -52,6 +52,10 @@ _lib.paged_kv_write.restype = ctypes.c_int
 _lib.paged_kv_write_rope.argtypes = [_P, _P, _P, _i32, _P, _P, _i64, _P, _i64, _i32, _i32, _P, _P,
                                      _D, _P]
 _lib.paged_kv_write_rope.restype = ctypes.c_int
+_lib.paged_kv_copy_blocks.argtypes = [_P, _P, _i32, _P, _P, _i64, _D, _P]
+_lib.paged_kv_copy_blocks.restype = ctypes.c_int
+_lib.paged_kv_compact.argtypes = [_P, _P, _i32, _P, _i64, _P, _i64, _i32, _P, _D, _P]
+_lib.paged_kv_compact.restype = ctypes.c_int
 _lib.paged_decode_plan.argtypes = [_i32, _i32, _i32, _i32, _i32, _i32]
 _lib.paged_decode_plan.restype = _i32
 _lib.paged_decode_path.argtypes = [_i32, _i32, _i32, _i32, _i32, _i32]
@@ -97,6 +101,16 @@ _lib.pkv_bm_append_slots.argtypes = [_P, _P, _i32, _P]
 _lib.pkv_bm_append_slots.restype = ctypes.c_int
 _lib.pkv_bm_free_sequence.argtypes = [_P, _i64]
 _lib.pkv_bm_free_sequence.restype = ctypes.c_int
+_lib.pkv_bm_fork.argtypes = [_P, _i64, _i64]
+_lib.pkv_bm_fork.restype = ctypes.c_int
+_lib.pkv_bm_append_slots_cow.argtypes = [_P, _P, _i32, _P, _P, _P, ctypes.POINTER(ctypes.c_int32)]
+_lib.pkv_bm_append_slots_cow.restype = ctypes.c_int
+_lib.pkv_bm_truncate.argtypes = [_P, _i64, _i64]
+_lib.pkv_bm_truncate.restype = ctypes.c_int
+_lib.pkv_bm_ref_count.argtypes = [_P, _i32]
+_lib.pkv_bm_ref_count.restype = _i32
+_lib.pkv_bm_compact.argtypes = [_P, _P, _i64, ctypes.POINTER(ctypes.c_int64), _P]
+_lib.pkv_bm_compact.restype = ctypes.c_int
 _lib.pkv_bm_preempt_lifo.argtypes = [_P, ctypes.POINTER(ctypes.c_int64)]
 _lib.pkv_bm_preempt_lifo.restype = ctypes.c_int
 _lib.pkv_bm_block_tables.argtypes = [_P, _P, _i32, _i32, _P, _P]
@@ -188,6 +202,98 @@ def paged_kv_write_rope(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Te
                                     cos_sin.shape[0], r, 1 if neox_style else 0, _ptr(k_cache),
                                     _ptr(v_cache), ctypes.byref(d), _stream(stream)),
            "paged_kv_write_rope")
+
+
+def _one_device(where: torch.Tensor, **tensors) -> None:
+    """The tensors are on one device, which is the current one (the library launches there)."""
+    dev = where.device
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, expected {dev}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, the current device is {torch.cuda.current_device()}")
+
+
+def _layers(k_caches, v_caches, where: str):
+    """(host arrays of the layers' K and V pointers, layer count, one layer's descriptor, a
+    cache tensor) of 4-dim caches (one layer), 5-dim caches [layers, NB, Hkv, BS, D], or
+    sequences of 4-dim caches."""
+    if isinstance(k_caches, torch.Tensor):
+        ndim = k_caches.dim()
+        if ndim not in (4, 5):
+            raise ValueError(f"{where}: k_caches must be [NB, Hkv, BS, D] or [layers, NB, Hkv, BS, D]")
+        _need(k_caches, "k_caches", torch.bfloat16, ndim)
+        if not isinstance(v_caches, torch.Tensor):
+            raise TypeError(f"{where}: k_caches and v_caches must be given alike")
+        _need(v_caches, "v_caches", torch.bfloat16, ndim)
+        if k_caches.shape != v_caches.shape:
+            raise ValueError(f"{where}: k_caches and v_caches shapes differ")
+        _one_device(k_caches, v_caches=v_caches)
+        n = 1 if ndim == 4 else k_caches.shape[0]
+        step = 2 * k_caches.numel() // max(n, 1)
+        k0, v0 = k_caches.data_ptr(), v_caches.data_ptr()
+        kp = (_P * n)(*[k0 + i * step for i in range(n)])
+        vp = (_P * n)(*[v0 + i * step for i in range(n)])
+        NB, Hkv, BS, D = k_caches.shape[-4:]
+        return kp, vp, n, pkv_cache_desc(NB, BS, Hkv, D), k_caches
+    ks, vs = list(k_caches), list(v_caches)
+    if len(ks) != len(vs) or not ks:
+        raise ValueError(f"{where}: k_caches and v_caches need one cache per layer each")
+    for t in ks + vs:
+        _need(t, "a layer's cache", torch.bfloat16, 4)
+        if t.shape != ks[0].shape:
+            raise ValueError(f"{where}: the layers' caches have different shapes")
+        _one_device(ks[0], cache=t)
+    n = len(ks)
+    return ((_P * n)(*[t.data_ptr() for t in ks]), (_P * n)(*[t.data_ptr() for t in vs]), n,
+            cache_desc(ks[0]), ks[0])
+
+
+def paged_kv_copy_blocks(k_caches, v_caches, block_pairs: torch.Tensor,
+                         num_tokens: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Pages block_pairs[:, 0] are copied to pages block_pairs[:, 1] ([n, 2] int32) in every
+    layer; with num_tokens [n] int32 only the first num_tokens[i] rows of pair i.
+
+    The caches: one layer's [NB, Hkv, BS, D], all layers in one [layers, NB, Hkv, BS, D], or
+    a list of the layers' caches.  No destination may be another pair's source or destination.
+    """
+    kp, vp, n, d, first = _layers(k_caches, v_caches, "paged_kv_copy_blocks")
+    _need(block_pairs, "block_pairs", torch.int32, 2)
+    if block_pairs.shape[1] != 2:
+        raise ValueError("block_pairs must be [n, 2]")
+    if num_tokens is not None:
+        _need(num_tokens, "num_tokens", torch.int32, 1)
+        if num_tokens.shape[0] != block_pairs.shape[0]:
+            raise ValueError("num_tokens must have one entry per pair")
+    _one_device(first, block_pairs=block_pairs, num_tokens=num_tokens)
+    _check(_lib.paged_kv_copy_blocks(kp, vp, n, _ptr(block_pairs), _ptr(num_tokens),
+                                     block_pairs.shape[0], ctypes.byref(d), _stream(stream)),
+           "paged_kv_copy_blocks")
+
+
+def paged_kv_compact(k_caches, v_caches, block_moves: torch.Tensor,
+                     block_tables: Optional[torch.Tensor] = None,
+                     block_map: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Pages block_moves[:, 0] move to the free pages block_moves[:, 1] ([n, 2] int32) in
+    every layer, and block_tables [B, M] int32 is rewritten in place through block_map [NB]
+    int32 (BlockManager.compact plans both; caches as in paged_kv_copy_blocks)."""
+    kp, vp, n, d, first = _layers(k_caches, v_caches, "paged_kv_compact")
+    _need(block_moves, "block_moves", torch.int32, 2)
+    if block_moves.shape[1] != 2:
+        raise ValueError("block_moves must be [n, 2]")
+    rows = cols = 0
+    if block_tables is not None:
+        _need(block_tables, "block_tables", torch.int32, 2)
+        if block_map is None:
+            raise ValueError("block_tables need a block_map")
+        _need(block_map, "block_map", torch.int32, 1)
+        if block_map.shape[0] != d.num_blocks:
+            raise ValueError("block_map must have one entry per block")
+        rows, cols = block_tables.shape
+    _one_device(first, block_moves=block_moves, block_tables=block_tables, block_map=block_map)
+    _check(_lib.paged_kv_compact(kp, vp, n, _ptr(block_moves), block_moves.shape[0],
+                                 _ptr(block_tables), rows, cols, _ptr(block_map), ctypes.byref(d),
+                                 _stream(stream)), "paged_kv_compact")
 
 
 PATH_PARTITIONS, PATH_CLUSTER, PATH_PERSISTENT = 1, 2, 3
@@ -464,6 +570,43 @@ class BlockManager:
 
     def free_sequence(self, seq_id: int) -> None:
         _check(_lib.pkv_bm_free_sequence(self._h, int(seq_id)), "pkv_bm_free_sequence")
+
+    def fork(self, parent_id: int, child_id: int) -> None:
+        """Admit child_id sharing every block of parent_id."""
+        _check(_lib.pkv_bm_fork(self._h, int(parent_id), int(child_id)), "pkv_bm_fork")
+
+    def append_slots_cow(self, seq_ids):
+        """append_slots with copy-on-write: (slots [n] int64, block_pairs [p, 2] int32,
+        num_tokens [p] int32); copy the pairs (paged_kv_copy_blocks) before writing the slots."""
+        ids = torch.as_tensor(list(seq_ids), dtype=torch.int64).contiguous()
+        n = len(ids)
+        out = torch.empty(n, dtype=torch.int64)
+        pairs, rows = torch.empty(n, 2, dtype=torch.int32), torch.empty(n, dtype=torch.int32)
+        got = ctypes.c_int32(0)
+        _check(_lib.pkv_bm_append_slots_cow(self._h, ids.data_ptr(), n, out.data_ptr(),
+                                            pairs.data_ptr(), rows.data_ptr(), ctypes.byref(got)),
+               "pkv_bm_append_slots_cow")
+        return out, pairs[:got.value], rows[:got.value]
+
+    def truncate(self, seq_id: int, num_tokens: int) -> None:
+        """Shorten a sequence, releasing the blocks past num_tokens."""
+        _check(_lib.pkv_bm_truncate(self._h, int(seq_id), int(num_tokens)), "pkv_bm_truncate")
+
+    def ref_count(self, block: int) -> int:
+        n = int(_lib.pkv_bm_ref_count(self._h, int(block)))
+        if n < 0:
+            raise PkvError(n, "pkv_bm_ref_count")
+        return n
+
+    def compact(self):
+        """Move the blocks in use to the lowest ids: (block_moves [n, 2] int32, block_map
+        [num_blocks] int32) for paged_kv_compact; the manager's tables are already moved."""
+        moves = torch.empty(self.num_blocks - self.num_free_blocks, 2, dtype=torch.int32)
+        block_map = torch.empty(self.num_blocks, dtype=torch.int32)
+        got = ctypes.c_int64(0)
+        _check(_lib.pkv_bm_compact(self._h, moves.data_ptr(), moves.shape[0], ctypes.byref(got),
+                                   block_map.data_ptr()), "pkv_bm_compact")
+        return moves[:got.value], block_map
 
     def preempt_lifo(self) -> int:
         v = ctypes.c_int64(0)

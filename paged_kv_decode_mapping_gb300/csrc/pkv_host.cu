@@ -185,6 +185,7 @@ PKV_API int pkv_device_errors(uint32_t *flags, int clear) {
   if ((e = read_decode_errors(flags, clear)) != cudaSuccess) return cuda_error(e, "decode error word");
   if ((e = read_prefill_errors(flags, clear)) != cudaSuccess) return cuda_error(e, "prefill error word");
   if ((e = read_write_errors(flags, clear)) != cudaSuccess) return cuda_error(e, "write error word");
+  if ((e = read_page_errors(flags, clear)) != cudaSuccess) return cuda_error(e, "page error word");
   clear_error();
   return PKV_OK;
 }

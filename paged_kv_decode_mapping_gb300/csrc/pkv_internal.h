@@ -104,6 +104,7 @@ int check_decode_attention(const pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf1
 // Device error words of the attention translation units (read + optional clear).
 cudaError_t read_decode_errors(uint32_t *flags, int clear);
 cudaError_t read_prefill_errors(uint32_t *flags, int clear);
+cudaError_t read_page_errors(uint32_t *flags, int clear);
 
 }  // namespace pkv
 
