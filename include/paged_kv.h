@@ -353,6 +353,31 @@ int paged_prefill_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k_
                             const pkv_cache_desc *cache, float scale, void *stream);
 
 /*
+ * prompt_attention -- causal attention over whole prompts packed one after another, K and V
+ * straight from the projections ("vLLM-Style Llama Inference Engine", How it works: prefill
+ * uses causal attention).  A prompt that starts a sequence needs no cache to attend to: this
+ * call and the slot write of the same k and v (paged_kv_write) are independent of each
+ * other.  Prompts behind cached tokens go through paged_prefill_attention.
+ *
+ * Sequence b is rows query_start[b] .. query_start[b+1]-1 (DEVICE int32 [num_seqs + 1],
+ * nondecreasing, within num_tokens) of q, k, v and out; its query i sees its keys 0 .. i:
+ *   out[row][h] = bf16( sum_{t <= i} softmax_t(scale * <q[row][h], k_t>) v_t )
+ * in fp32 arithmetic on bf16 inputs (the weights enter the product with V as bf16).  Query
+ * head h reads kv head h / (num_q_heads / num_kv_heads), any group.  One token's heads are
+ * contiguous; the strides, in elements, lead from one token to the next, so that q, k and v
+ * may be slices of one fused projection (multiples of 8; out 16-byte aligned like q, k, v).
+ * max_query_len >= every length; a longer or misplaced sequence raises
+ * PKV_DEVERR_CONTEXT_LEN and only its first max_query_len rows within the tensors are
+ * computed.  Rows of no sequence are not written, and no sequence reads another's rows;
+ * within a sequence v must be finite (a NaN or infinity may reach rows up to 127 before it).
+ */
+int prompt_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v,
+                     int64_t out_stride, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                     const int32_t *query_start, int64_t num_tokens, int32_t max_query_len,
+                     int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                     int32_t head_dim, float scale, void *stream);
+
+/*
  * paged_decode_split -- flash-decoding partition kernel (split-K over the keys;
  * the FlashAttention-2 online-softmax algebra that the first page references).
  *

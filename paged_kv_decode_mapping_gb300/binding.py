@@ -80,6 +80,9 @@ _lib.paged_decode_step_rope.restype = ctypes.c_int
 _lib.paged_prefill_attention.argtypes = [_P, _P, _P, _P, _P, _i32, _P, _i32, _P, _i32, _i32, _i32,
                                          _D, _f32, _P]
 _lib.paged_prefill_attention.restype = ctypes.c_int
+_lib.prompt_attention.argtypes = [_P, _P, _P, _P, _i64, _i64, _i64, _i64, _P, _i64, _i32, _i32,
+                                  _i32, _i32, _i32, _f32, _P]
+_lib.prompt_attention.restype = ctypes.c_int
 _lib.paged_decode_split.argtypes = [_P, _P, _P, _P, _P, _P, _i32, _P, _i32, _i32, _i32, _D, _f32,
                                     _i32, _P]
 _lib.paged_decode_split.restype = ctypes.c_int
@@ -473,6 +476,39 @@ def paged_prefill_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.T
                                         _ptr(query_start), int(max_query_len), B, q.shape[1],
                                         ctypes.byref(d), float(scale), _stream(stream)),
            "paged_prefill_attention")
+
+
+def prompt_attention(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     query_start: torch.Tensor, max_query_len: int, scale: float,
+                     stream=None) -> None:
+    """Causal attention over whole prompts packed one after another: out, q [T, Hq, D], k, v
+    [T, Hkv, D] bf16 (each token's heads contiguous; the tokens may be strided, e.g. slices
+    of a fused projection), sequence b at rows query_start[b] .. query_start[b+1]-1."""
+    T, Hq, D = q.shape if q.dim() == 3 else (0, 0, 0)
+    for t, name in ((out, "out"), (q, "q"), (k, "k"), (v, "v")):
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+        if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D:
+            raise ValueError(f"{name}: expected [T, heads, D] with q's T and D, got shape {tuple(t.shape)}")
+        if T > 0 and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D)):
+            raise ValueError(f"{name}: a token's heads must be contiguous")
+    if out.shape != q.shape or k.shape != v.shape:
+        raise ValueError("out must have q's shape, and v k's")
+    for t, name in ((out, "out"), (q, "q"), (k, "k"), (v, "v")):
+        if not t.is_cuda:
+            raise ValueError(f"{name}: must be a CUDA tensor")
+    _need(query_start, "query_start", torch.int32, 1)
+    if query_start.shape[0] < 1:
+        raise ValueError("query_start must be [B + 1]")
+    _one_device(q, out=out, k=k, v=v, query_start=query_start)
+
+    def stride(t):  # one token has no next one: any stride will do
+        return t.stride(0) if T > 1 else t.shape[1] * D
+
+    _check(_lib.prompt_attention(_ptr(out), _ptr(q), _ptr(k), _ptr(v), stride(out), stride(q),
+                                 stride(k), stride(v), _ptr(query_start), T, int(max_query_len),
+                                 query_start.shape[0] - 1, Hq, k.shape[1], D, float(scale),
+                                 _stream(stream)), "prompt_attention")
 
 
 def paged_decode_attention_noalloc(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,

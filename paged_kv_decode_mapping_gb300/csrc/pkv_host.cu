@@ -128,6 +128,22 @@ static int tensor_map(const void *cache_ptr, const pkv_cache_desc &c, CUtensorMa
   return PKV_OK;
 }
 
+int packed_map(const pkv_bf16 *x, int64_t tokens, int32_t heads, int32_t d, int64_t stride,
+               int32_t box_tokens, CUtensorMap *out) {
+  const int rc = get_encoder();
+  if (rc) return rc;
+  cuuint64_t dims[4] = {64, (cuuint64_t)tokens, (cuuint64_t)(d / 64), (cuuint64_t)heads};
+  cuuint64_t strides[3] = {(cuuint64_t)stride * 2, 128, (cuuint64_t)d * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)box_tokens, (cuuint32_t)(d / 64), 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  const CUresult r =
+      g_encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<pkv_bf16 *>(x), dims, strides,
+               box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return PKV_OK;
+}
+
 static bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 int ilog2(int x) {
   int r = 0;
@@ -186,6 +202,7 @@ PKV_API int pkv_device_errors(uint32_t *flags, int clear) {
   if ((e = read_prefill_errors(flags, clear)) != cudaSuccess) return cuda_error(e, "prefill error word");
   if ((e = read_write_errors(flags, clear)) != cudaSuccess) return cuda_error(e, "write error word");
   if ((e = read_page_errors(flags, clear)) != cudaSuccess) return cuda_error(e, "page error word");
+  if ((e = read_tile_errors(flags, clear)) != cudaSuccess) return cuda_error(e, "tile error word");
   clear_error();
   return PKV_OK;
 }

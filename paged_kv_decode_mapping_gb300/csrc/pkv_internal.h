@@ -86,6 +86,11 @@ int device_sms(int *sms);
 // attn_mutex().
 int maps_for(const pkv_bf16 *k_cache, const pkv_bf16 *v_cache, const pkv_cache_desc &c,
              CUtensorMap *tmk, CUtensorMap *tmv);
+// Encodes the TMA map of packed rows x [tokens][heads][d] bf16, `stride` elements from one
+// token to the next: box {64 dims, `box_tokens` tokens, d/64 halves, one head}, 128-byte
+// swizzle, zeros past the last token; the caller holds attn_mutex().
+int packed_map(const pkv_bf16 *x, int64_t tokens, int32_t heads, int32_t d, int64_t stride,
+               int32_t box_tokens, CUtensorMap *out);
 // Argument checks shared by the decode and prefill entry points.
 int check_decode(const void *q, const void *k_cache, const void *v_cache, const int32_t *bt,
                  int32_t max_blocks, const int32_t *lens, int32_t max_len, int32_t num_seqs,
@@ -105,6 +110,7 @@ int check_decode_attention(const pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf1
 cudaError_t read_decode_errors(uint32_t *flags, int clear);
 cudaError_t read_prefill_errors(uint32_t *flags, int clear);
 cudaError_t read_page_errors(uint32_t *flags, int clear);
+cudaError_t read_tile_errors(uint32_t *flags, int clear);
 
 }  // namespace pkv
 

@@ -1,0 +1,637 @@
+// pkv_tiles.cu -- attention of many query rows that share keys, on the 5th-generation
+// tensor cores: packed causal prompts (prompt_attention) and the shared prefixes of decode
+// batches (the first half of paged_decode_shared_prefix_attention).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "attn_tc.cuh"
+
+namespace pkv {
+
+// ===========================================================================
+// tile_kernel: a CTA owns one kv head's query rows -- (query token, head of the group)
+// pairs -- as two tiles in ping-pong: while four softmax warps work on one tile's scores
+// (one thread per row), the tensor core works on the other tile.
+//   S_t = Q_t . K_j^T   tcgen05.mma M=128 N=128 K=D, both K-major in shared memory, S_t in TMEM
+//   P_t = exp2(S_t * scale - m)  fp32, rounded to bf16 into TMEM over the upper half of S_t
+//   O_t += P_t . V_j    P_t from TMEM, V_j MN-major in shared memory, O_t in TMEM
+// The row's reference max m moves only when a block raises it by more than kTcRescale;
+// then O_t and the row sum are rescaled.  The row sum adds the bf16-rounded weights that
+// the tensor core multiplies, so the weights stay a convex combination whatever m is.
+// K and V stream through separate rings, each with its producer warp.
+//
+// Two ways of pairing:
+//  * kPrompt: the tiles are 128 query rows each of one packed sequence and share every
+//    K/V block (256 rows per block staged).  Causal: a row of query i sees keys 0 .. i.
+//    K and V rows come straight from the packed projections: one TMA box per block.
+//  * kPrefix: both tiles hold the same 128 rows (queries of a group of sequences) and take
+//    alternate key blocks, so that a few rows over a long prefix still overlap softmax and
+//    tensor core.  The keys come from the pages of the group's first sequence; the CTA
+//    covers one split of them, and each tile writes its softmax-normalised fp32 output and
+//    log-sum-exp for the merge in the decode kernel that follows.
+enum { kPrompt = 0, kPrefix = 1 };
+
+struct TileArgs {
+  const uint16_t *q;
+  uint16_t *out;            // prompt
+  int64_t q_stride, out_stride;  // elements from one query token to the next
+  const int32_t *start;     // [num + 1] first query row of each sequence / group
+  int32_t num, total, max_len;   // sequences or groups, query tokens, longest sequence
+  int32_t num_q_heads, num_kv_heads, group;
+  float scale_log2;
+  // prefix
+  const int32_t *block_tables, *context_lens, *prefix_lens;
+  int64_t num_blocks;
+  int32_t max_blocks, max_prefix, block_size, log2_bs, box_rows;
+  int32_t split_keys;       // keys per split (a multiple of 2 * kTcKeys)
+  int32_t n_rows;           // partial rows per (sequence, head)
+  float *o_part, *lse_part; // [B][Hq][n_rows][D], [B][Hq][n_rows]; rows 2 s, 2 s + 1: split s
+};
+
+constexpr int kTileThreads = 32 * 11;  // 8 softmax warps, K producer, MMA, V producer
+
+template <int D, int MODE>
+struct TileSmem {
+  static constexpr int KS = D == 64 ? 4 : (MODE == kPrompt ? 2 : 3);  // K and V ring stages
+  static constexpr uint32_t kSub = kTcKeys * 128;     // 128 rows x 128 B (64 dims)
+  static constexpr uint32_t kTile = kSub * (D / 64);
+  static constexpr int kQ = MODE == kPrompt ? 2 : 1;  // Q tiles
+  static constexpr uint32_t k = 0;
+  static constexpr uint32_t v = k + KS * kTile;
+  static constexpr uint32_t q = v + KS * kTile;
+  // head_dim 64: a [128 keys][64] tile of ones, read by P.V as 16 more columns of V, so that
+  // the tensor core forms the row sums (O's columns are free in TMEM at 64, not at 128)
+  static constexpr bool kOnes = D == 64;
+  static constexpr uint32_t ones = q + kQ * kTile;
+  static constexpr uint32_t bars = ones + (kOnes ? kSub : 0);
+  // the rings, then s_full/p_full/pv_done per tile, q_ready, mma_done
+  static constexpr int kBars = 4 * KS + 8;
+  static constexpr uint32_t tslot = bars + kBars * 8;
+  static constexpr uint32_t flag = tslot + 8;
+  static constexpr uint32_t total = flag + 8;
+};
+template <int D, int MODE>
+constexpr size_t tile_smem() { return 1024 + TileSmem<D, MODE>::total; }
+static_assert(tile_smem<64, kPrompt>() <= 227 * 1024 && tile_smem<128, kPrompt>() <= 227 * 1024 &&
+                  tile_smem<64, kPrefix>() <= 227 * 1024 && tile_smem<128, kPrefix>() <= 227 * 1024,
+              "the tiles fit a CTA");
+
+// The sequence (or group) whose tiles of `tile_rows` rows hold tile number idx, its first
+// query token, its length and the tile's place in it.  Whole warps; lengths that are
+// negative, past `total` or over max_len are clamped and flagged.
+__device__ __forceinline__ bool locate_tile(const TileArgs &a, int64_t idx, int tile_rows, int lane,
+                                            int &b, int &first, int &n, int &tile, int &ntiles) {
+  int64_t before = 0;
+  for (int c = 0; c < a.num; c += 32) {
+    const int i = c + lane;
+    int s = 0, len = 0;
+    if (i < a.num) {
+      const int s0 = __ldg(a.start + i), e0 = __ldg(a.start + i + 1);
+      s = min(max(s0, 0), a.total);
+      len = min(max(e0, s), a.total) - s;
+      len = min(len, a.max_len);
+      if (s != s0 || s + len != e0) raise_error(PKV_DEVERR_CONTEXT_LEN);
+    }
+    const int64_t mine = ((int64_t)len * a.group + tile_rows - 1) / tile_rows;
+    int64_t upto = mine;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, upto, x);
+      if (lane >= x) upto += y;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + upto > idx);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      b = c + l;
+      first = __shfl_sync(0xffffffffu, s, l);
+      n = __shfl_sync(0xffffffffu, len, l);
+      ntiles = (int)__shfl_sync(0xffffffffu, mine, l);
+      tile = (int)(idx - before - __shfl_sync(0xffffffffu, upto - mine, l));
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return false;
+}
+
+// Loads keys [k0, k0 + nk) of kv head g from the group's pages into a block tile
+// [D/64][128][128 B], one TMA box of min(block_size, 64) rows per lane, completing on `bar`.
+template <int D, uint32_t SUB>
+__device__ __forceinline__ void load_paged_block(const CUtensorMap *tm, uint32_t dst, uint32_t bar,
+                                                 int k0, int nk, int &win, int &tb,
+                                                 const int32_t *trow, int lb_last,
+                                                 const TileArgs &a, int g, int lane,
+                                                 uint64_t policy) {
+  constexpr int kH = D / 64;
+  const int rb = a.box_rows;
+  const int nbox = (nk + rb - 1) / rb;
+  const int lb_hi = (k0 + (nbox - 1) * rb) >> a.log2_bs;
+  if (lb_hi >= win + 32 || (k0 >> a.log2_bs) < win) {
+    win = k0 >> a.log2_bs;
+    tb = (win + lane <= lb_last) ? __ldg(trow + win + lane) : 0;
+  }
+  const int bi = lane / kH, hh = lane % kH;
+  const int key = k0 + bi * rb;
+  const int src = min(max((key >> a.log2_bs) - win, 0), 31);
+  const int64_t phys_raw = __shfl_sync(0xffffffffu, tb, src);
+  if (lane == 0) dev::mbar_arrive_expect_tx(bar, (uint32_t)nbox * rb * 128u * kH);
+  __syncwarp();
+  if (bi < nbox) {
+    int64_t phys = phys_raw;
+    if (phys < 0 || phys >= a.num_blocks) {
+      raise_error(PKV_DEVERR_BLOCK_ID);
+      phys = 0;
+    }
+    const int off = key & (a.block_size - 1);
+    const int32_t row = (int32_t)((phys * a.num_kv_heads + g) * a.block_size + off);
+    const uint32_t d = dst + (uint32_t)(bi * rb) * 128u;
+    if constexpr (D == 64) {
+      dev::tma_load_2d(d, tm, 0, row, bar, policy);
+    } else {
+      asm volatile(
+          "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+          ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(d + hh * SUB),
+          "l"(reinterpret_cast<uint64_t>(tm)), "r"(0), "r"(hh), "r"(row), "r"(bar), "l"(policy)
+          : "memory");
+    }
+  }
+  __syncwarp();
+}
+
+// One whole block tile of packed rows [row, row + 128) of kv head g (rows past the tensor
+// read as zeros): a single box {64 dims, 128 rows, D/64 halves, 1 head}.
+__device__ __forceinline__ void load_packed_block(const CUtensorMap *tm, uint32_t dst, uint32_t bar,
+                                                  uint32_t bytes, int row, int g, uint64_t policy) {
+  dev::mbar_arrive_expect_tx(bar, bytes);
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(0), "r"(row), "r"(0), "r"(g), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    tile_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                const TileArgs a) {
+  using SL = TileSmem<D, MODE>;
+  constexpr int KS = SL::KS;
+  constexpr bool kPaged = MODE == kPrefix;     // keys from pages; partial outputs
+  constexpr bool kShareKeys = MODE == kPrompt; // both tiles take every block
+  constexpr bool kOnes = SL::kOnes;
+  constexpr int kON = D + (kOnes ? 16 : 0);    // O columns per tile (then the row sums)
+  constexpr int kTileRowsCta = kShareKeys ? 2 * kTcRows : kTcRows;
+  constexpr int kProducer = 8, kMma = 9, kProducerV = 10;
+  constexpr uint32_t kPCol = 64;  // P_t's columns within S_t (a thread reads all of its row first)
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = dev::smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *const bp = smem_raw + (base - raw);
+  const uint32_t bars = base + SL::bars;
+  auto k_full = [&](int s) { return bars + 8u * s; };
+  auto k_empty = [&](int s) { return bars + 8u * (KS + s); };
+  auto v_full = [&](int s) { return bars + 8u * (2 * KS + s); };
+  auto v_empty = [&](int s) { return bars + 8u * (3 * KS + s); };
+  auto s_full = [&](int t) { return bars + 8u * (4 * KS + t); };
+  auto p_full = [&](int t) { return bars + 8u * (4 * KS + 2 + t); };
+  auto pv_done = [&](int t) { return bars + 8u * (4 * KS + 4 + t); };
+  const uint32_t q_ready = bars + 8u * (4 * KS + 6);
+  const uint32_t mma_done = bars + 8u * (4 * KS + 7);
+  volatile uint32_t *const s_tmem = reinterpret_cast<volatile uint32_t *>(bp + SL::tslot);
+  volatile int *const s_flag = reinterpret_cast<volatile int *>(bp + SL::flag);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.group;
+  // the decode kernel that merges may start its own part while this one runs
+  if constexpr (kPaged) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int g = blockIdx.x % (unsigned)a.num_kv_heads;
+  int b, first, n, tile, ntiles;
+  if (!locate_tile(a, blockIdx.x / (unsigned)a.num_kv_heads, kTileRowsCta, lane, b, first, n, tile,
+                   ntiles))
+    return;
+  // causal prompts: a sequence's last tiles see the most keys and go first
+  if constexpr (kShareKeys) tile = ntiles - 1 - tile;
+  const int64_t rows = (int64_t)n * G;
+  const int64_t row0 = (int64_t)tile * kTileRowsCta;
+
+  // key0: the CTA's first key; t_end: keys [key0, t_end) are staged, in blocks of kTcKeys;
+  // nb0, nb1: blocks of each tile (block blk(t, i) is its i-th)
+  int key0 = 0, t_end, nblk, nb0, nb1, prefix = 0;
+  if constexpr (kPaged) {
+    prefix = __ldg(a.prefix_lens + b);
+    const int cap = (int)min((int64_t)a.max_blocks * a.block_size, (int64_t)a.max_prefix);
+    if (prefix < 0 || prefix > cap) {
+      if (tid == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
+      prefix = prefix < 0 ? 0 : cap;
+    }
+    prefix = prefix >> a.log2_bs << a.log2_bs;  // whole pages
+    key0 = blockIdx.y * a.split_keys;
+    if (key0 >= prefix) return;
+    t_end = min(key0 + a.split_keys, prefix);
+    nblk = (t_end - key0 + kTcKeys - 1) / kTcKeys;
+    nb0 = (nblk + 1) / 2;
+    nb1 = nblk / 2;
+  } else {
+    const int64_t last0 = min(row0 + kTcRows, rows) - 1, last1 = min(row0 + 2 * kTcRows, rows) - 1;
+    nb0 = ((int)(last0 / G) + kTcKeys) / kTcKeys;
+    nb1 = last1 > last0 ? ((int)(last1 / G) + kTcKeys) / kTcKeys : 0;
+    t_end = (int)(last1 / G) + 1;
+    nblk = max(nb0, nb1);
+  }
+  auto nb_of = [&](int t) { return t ? nb1 : nb0; };
+  auto blk = [&](int t, int i) { return kShareKeys ? i : 2 * i + t; };
+
+  const bool is_producer = warp == kProducer || warp == kProducerV;
+  const int32_t *const trow = kPaged ? a.block_tables + (int64_t)first * a.max_blocks : nullptr;
+  const int lb_last = kPaged ? (t_end - 1) >> a.log2_bs : 0;
+  const int win_first = kPaged ? key0 >> a.log2_bs : 0;
+  int tb = (kPaged && is_producer && win_first + lane <= lb_last) ? __ldg(trow + win_first + lane) : 0;
+
+  if (tid == 0) {
+    for (int i = 0; i < SL::kBars; ++i) {
+      const uint32_t bar = bars + 8u * i;
+      const uint32_t count = bar == p_full(0) || bar == p_full(1) ? 4u
+                             : bar == q_ready ? (kShareKeys ? 8u : 4u) : 1u;
+      dev::mbar_init(bar, count);
+    }
+    *s_flag = 0;
+    dev::fence_mbar_init();
+  }
+  if constexpr (kOnes) {  // bf16 1.0 everywhere; read by the tensor core (async proxy)
+    for (int i = tid; i < (int)(SL::kSub / 16); i += kTileThreads)
+      *reinterpret_cast<uint4 *>(bp + SL::ones + i * 16) =
+          make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    dev::fence_proxy_async_smem();
+  }
+  if (warp == 0) dev::tmem_alloc(base + SL::tslot, 512);
+  dev::tc_fence_before();
+  __syncthreads();
+  dev::tc_fence_after();
+  const uint32_t tmem = *s_tmem;  // S_t at column 128 t, O_t at 256 + kON t
+
+  auto fail = [&](bool ok) {
+    if (!ok) {
+      raise_error(PKV_DEVERR_TIMEOUT);
+      *s_flag = 1;
+    }
+    return ok;
+  };
+  int issued = 0;  // producers: blocks loaded
+
+  if (is_producer) {
+    // ------------------------------------------------- producer warps: K ring, V ring
+    const bool is_k = warp == kProducer;
+    const CUtensorMap *const tm = is_k ? &tmk : &tmv;
+    const uint32_t ring = base + (is_k ? SL::k : SL::v);
+    // a prompt's tiles, and the row tiles of a group, read the same keys: keep them in L2
+    const uint64_t policy = dev::policy_evict_last();
+    int win = win_first;
+    for (int j = 0; j < nblk; ++j) {
+      const int s = j % KS;
+      const uint32_t empty = is_k ? k_empty(s) : v_empty(s), full = is_k ? k_full(s) : v_full(s);
+      if (j >= KS && !__all_sync(0xffffffffu, dev::mbar_wait(empty, ((j / KS) - 1) & 1))) {
+        if (lane == 0) fail(false);
+        break;
+      }
+      const uint32_t dst = ring + s * SL::kTile;
+      if constexpr (kPaged)
+        load_paged_block<D, SL::kSub>(tm, dst, full, key0 + j * kTcKeys,
+                                      min(kTcKeys, t_end - key0 - j * kTcKeys), win, tb, trow,
+                                      lb_last, a, g, lane, policy);
+      else if (lane == 0)
+        load_packed_block(tm, dst, full, SL::kTile, first + j * kTcKeys, g, policy);
+      issued = j + 1;
+    }
+  } else if (warp == kMma) {
+    // ------------------------------------------------- tensor-core issue (one thread)
+    if (lane == 0) {
+      constexpr uint32_t id_s = dev::idesc_bf16_f32(kTcRows, kTcKeys, 0);
+      constexpr uint32_t id_o = dev::idesc_bf16_f32(kTcRows, kON, 1);
+      const uint64_t dq0 = dev::smem_desc(base + SL::q, 16, 1024);
+      const uint64_t dk0 = dev::smem_desc(base + SL::k, 16, 1024);
+      // V stage s as the MN-major B operand: the next 64 columns are V's other half
+      // (head_dim 128) or the tile of ones, `lbo` bytes further on
+      auto dv = [&](int s) {
+        const uint32_t vs = SL::v + s * SL::kTile;
+        return dev::smem_desc(base + vs, kOnes ? SL::ones - vs : SL::kSub, 1024);
+      };
+      // the last tile that reads block blk(t, i) frees its stage
+      auto last_user = [&](int t, int i) { return !kShareKeys || t == 1 || i >= nb1; };
+      auto issue_s = [&](int t, int i) {
+        const int j = blk(t, i), s = j % KS;
+        if (!fail(dev::mbar_wait(k_full(s), (j / KS) & 1))) return false;
+        dev::tc_fence_after();
+        issue_qk<D>(tmem + 128u * t, desc_add(dq0, kShareKeys ? t * SL::kTile : 0),
+                    desc_add(dk0, s * SL::kTile), SL::kSub, id_s);
+        dev::umma_commit(s_full(t));
+        if (last_user(t, i)) dev::umma_commit(k_empty(s));
+        return true;
+      };
+      bool ok = fail(dev::mbar_wait(q_ready, 0));
+      if (ok && nb0 > 0) ok = issue_s(0, 0);
+      if (ok && nb1 > 0) ok = issue_s(1, 0);
+      const int most = max(nb0, nb1);
+      for (int i = 0; ok && i < most; ++i) {
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (i >= nb_of(t)) continue;
+          const int j = blk(t, i), s = j % KS;
+          if (!(ok = fail(dev::mbar_wait(p_full(t), i & 1)))) break;
+          if (!(ok = fail(dev::mbar_wait(v_full(s), (j / KS) & 1)))) break;
+          dev::tc_fence_after();
+          issue_pv_ts(tmem + 256u + (uint32_t)(kON * t), tmem + 128u * t + kPCol, dv(s), id_o,
+                      i > 0 ? 1u : 0u);
+          dev::umma_commit(pv_done(t));
+          if (last_user(t, i)) dev::umma_commit(v_empty(s));
+          // S_t(i+1) over S_t(i) and P_t(i), after the P.V that reads P_t(i): the MMAs of
+          // one thread run in issue order
+          if (i + 1 < nb_of(t)) ok = issue_s(t, i + 1);
+        }
+      }
+      dev::umma_commit(mma_done);
+    }
+  } else {
+    // --------------------------------------------- softmax warps of tile t: row r each
+    const int t = warp >> 2, wq = warp & 3;
+    const int r = 32 * wq + lane;
+    const int64_t gr = row0 + (kShareKeys ? t * kTcRows : 0) + r;
+    const bool valid = gr < rows;
+    const int64_t grc = valid ? gr : rows - 1;
+    const int qi = (int)(grc / G), h = (int)(grc - (int64_t)qi * G);
+    const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
+    const uint32_t sb = tmem + lane_base + 128u * t;
+    const uint32_t ob = tmem + lane_base + 256u + (uint32_t)(kON * t);
+    // keys < see are this row's
+    int see;
+    if constexpr (kPaged)
+      see = min(max(__ldg(a.context_lens + first + qi), 0), t_end);
+    else
+      see = qi + 1;
+    if (kShareKeys || t == 0) {  // the tile's query rows (zeros past the end)
+      const uint4 *src = reinterpret_cast<const uint4 *>(
+          a.q + (int64_t)(first + qi) * a.q_stride + (int64_t)(g * G + h) * D);
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(bp + SL::q + (kShareKeys ? t * SL::kTile : 0u) +
+                                   (c >> 3) * SL::kSub + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
+      }
+      dev::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(q_ready);
+    }
+    const int nb = nb_of(t);
+    float m_ref = -INFINITY, lsum = 0.f;
+    const bool pos_scale = a.scale_log2 > 0.f;
+    bool ok = true;
+    auto rescale_o = [&](float f) {  // O_t (and its row-sum column) and the row sum scale by f
+#pragma unroll 1
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t o[32];
+        dev::tmem_ld32(ob + ch * 32, o);
+        dev::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        dev::tmem_st32(ob + ch * 32, o);
+      }
+      if constexpr (kOnes) {
+        const uint32_t sm = tmem_ld1(ob + D);
+        dev::tmem_wait_ld();
+        tmem_st1(ob + D, __float_as_uint(__uint_as_float(sm) * f));
+      }
+      dev::tmem_wait_st();
+      lsum *= f;
+    };
+    for (int i = 0; i < nb; ++i) {
+      const int j = blk(t, i), k0 = key0 + j * kTcKeys;
+      const int lim = see - 1 - k0;  // columns c <= lim are seen
+      if (!(ok = __all_sync(0xffffffffu, dev::mbar_wait(s_full(t), i & 1)))) break;
+      dev::tc_fence_after();
+      const bool whole = __all_sync(0xffffffffu, lim >= kTcKeys - 1);
+      uint32_t x[128], pk[64];
+      float ls;
+      row_block_load<4>(sb, 0, x);
+      // A row that has seen no key yet has m_ref = -inf: its weights (all masked to 0) are
+      // taken against 0 then.
+      if (i > 0) {
+        // the weights against the reference they start with, and the block's max, in one
+        // pass; the weights again when the block moves the reference.  PV_t(i-1) was issued
+        // before S_t(i) by the same thread, and s_full tracks every MMA issued before its
+        // commit, so O_t is stable here.
+        float bm;
+        ls = row_regs_exp_pk_max<4, !kOnes>(x, 0, lim, whole, pos_scale, a.scale_log2,
+                                            m_ref == -INFINITY ? 0.f : m_ref, pk, &bm);
+        const bool need = bm > m_ref + kTcRescale;
+        if (__any_sync(0xffffffffu, need)) {
+          const float m_new = fmaxf(m_ref, bm);
+          const float f = need ? dev::ex2(m_ref - m_new) : 1.f;
+          if (need) m_ref = m_new;
+          row_block_load<4>(sb, 0, x);
+          ls = row_regs_exp_pk<4, !kOnes>(x, 0, lim, whole, a.scale_log2,
+                                          m_ref == -INFINITY ? 0.f : m_ref, pk);
+          rescale_o(f);
+        }
+      } else {
+        m_ref = row_regs_max<4>(x, 0, lim, whole, pos_scale, a.scale_log2);
+        ls = row_regs_exp_pk<4, !kOnes>(x, 0, lim, whole, a.scale_log2,
+                                        m_ref == -INFINITY ? 0.f : m_ref, pk);
+      }
+      lsum += ls;
+      dev::tmem_st32(sb + kPCol, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+      dev::tmem_st32(sb + kPCol + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+      dev::tmem_wait_st();
+      const int nk = min(kTcKeys, t_end - k0);
+      if (nk < kTcKeys) {  // V rows past the staged keys are stale or another sequence's
+        const int s = j % KS;
+        if (!(ok = __all_sync(0xffffffffu, dev::mbar_wait(v_full(s), (j / KS) & 1)))) break;
+        const uint32_t vt = SL::v + s * SL::kTile;
+        for (int idx = r; idx < (kTcKeys - nk) * (D / 8); idx += kTcRows) {
+          const int row = nk + idx / (D / 8), c = idx % (D / 8);
+          *reinterpret_cast<uint4 *>(bp + vt + (c >> 3) * SL::kSub + row * 128 +
+                                     (((c & 7) ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        dev::fence_proxy_async_smem();
+      }
+      dev::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(p_full(t));
+    }
+    if (!ok && lane == 0) fail(false);
+    if (ok && nb > 0 && !(ok = __all_sync(0xffffffffu, dev::mbar_wait(pv_done(t), (nb - 1) & 1))) &&
+        lane == 0)
+      fail(false);
+    if (ok && nb > 0) {
+      dev::tc_fence_after();
+      if constexpr (kOnes) {
+        lsum = __uint_as_float(tmem_ld1(ob + D));
+        dev::tmem_wait_ld();
+      }
+    }
+    if constexpr (kPaged) {
+      // normalised fp32 partial and its log-sum-exp; no key seen: zeros and -inf
+      const int64_t row = ((int64_t)(first + qi) * a.num_q_heads + g * G + h) * a.n_rows +
+                          2 * blockIdx.y + t;
+      const bool any = nb > 0 && !(lsum == 0.f && m_ref == -INFINITY);
+      const float inv = any ? 1.f / lsum : 0.f;
+      if (ok && valid) a.lse_part[row] = any ? (m_ref + log2f(lsum)) * kLn2 : -INFINITY;
+      float4 *dst = reinterpret_cast<float4 *>(a.o_part + row * D);
+#pragma unroll 1
+      for (int ch = 0; ok && ch < D / 32; ++ch) {
+        uint32_t o[32];
+        if (nb > 0) {
+          dev::tmem_ld32(ob + ch * 32, o);
+          dev::tmem_wait_ld();
+        }
+        if (valid) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            dst[ch * 8 + u] = any ? make_float4(__uint_as_float(o[4 * u]) * inv,
+                                                __uint_as_float(o[4 * u + 1]) * inv,
+                                                __uint_as_float(o[4 * u + 2]) * inv,
+                                                __uint_as_float(o[4 * u + 3]) * inv)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+    } else if (ok && nb > 0) {
+      const float inv = 1.f / lsum;
+      uint4 *dst = reinterpret_cast<uint4 *>(a.out + (int64_t)(first + qi) * a.out_stride +
+                                             (int64_t)(g * G + h) * D);
+#pragma unroll 1
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t o[32];
+        dev::tmem_ld32(ob + ch * 32, o);
+        dev::tmem_wait_ld();
+        if (valid) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t w4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w4[e] = dev::pack_bf16x2(__uint_as_float(o[8 * u + 2 * e]) * inv,
+                                       __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
+            dst[ch * 4 + u] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+          }
+        }
+      }
+    }
+  }
+
+  // ---- teardown: no tensor-core op or copy may still be in flight when TMEM is freed
+  if (tid == 0) (void)dev::mbar_wait(mma_done, 0);
+  __syncthreads();
+  if (is_producer && lane == 0 && *s_flag) {
+    for (int s = 0; s < KS; ++s) {
+      const int last = s + ((issued - 1 - s) / KS) * KS;  // the last block on stage s
+      if (last >= 0 && last < issued)
+        (void)dev::mbar_wait(warp == kProducer ? k_full(s) : v_full(s), (last / KS) & 1);
+    }
+  }
+  dev::tc_fence_before();
+  __syncthreads();
+  dev::tc_fence_after();
+  if (warp == 0) dev::tmem_dealloc(tmem, 512);
+}
+
+cudaError_t read_tile_errors(uint32_t *flags, int clear) { return read_tu_errors(flags, clear); }
+
+namespace {
+
+bool g_tile_attr[kMaxDevices][2][2];  // dynamic smem attribute set: [D 64/128][mode]
+
+template <int D, int MODE>
+int prepare_tile_kernel() {
+  std::lock_guard<std::mutex> lk(attn_mutex());
+  int dev = 0;
+  const int rc = current_device(&dev);
+  if (rc) return rc;
+  bool &set = g_tile_attr[dev][D == 64 ? 0 : 1][MODE];
+  if (!set) {
+    const cudaError_t e = cudaFuncSetAttribute(tile_kernel<D, MODE>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)tile_smem<D, MODE>());
+    if (e != cudaSuccess) return cuda_error(e, "cudaFuncSetAttribute");
+    set = true;
+  }
+  return PKV_OK;
+}
+
+template <int D>
+int launch_prompt(const CUtensorMap &tmk, const CUtensorMap &tmv, const TileArgs &a, unsigned grid,
+                  cudaStream_t stream) {
+  const int rc = prepare_tile_kernel<D, kPrompt>();
+  if (rc) return rc;
+  tile_kernel<D, kPrompt><<<grid, kTileThreads, tile_smem<D, kPrompt>(), stream>>>(tmk, tmv, a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? PKV_OK : cuda_error(e, "tile_kernel launch");
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+PKV_API int prompt_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k,
+                             const pkv_bf16 *v, int64_t out_stride, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const int32_t *query_start,
+                             int64_t num_tokens, int32_t max_query_len, int32_t num_seqs,
+                             int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                             float scale, void *stream) {
+  const char *const fn = "prompt_attention";
+  if (num_seqs < 0 || num_tokens < 0 || max_query_len < 0 || num_q_heads <= 0 || num_kv_heads <= 0)
+    return set_error(PKV_ERR_SHAPE, "%s: bad sizes", fn);
+  if (num_q_heads % num_kv_heads != 0)
+    return set_error(PKV_ERR_SHAPE, "%s: num_q_heads %d is not a multiple of num_kv_heads %d", fn,
+                     num_q_heads, num_kv_heads);
+  if (head_dim != 64 && head_dim != 128)
+    return set_error(PKV_ERR_UNSUPPORTED, "%s: head_dim %d (built: 64, 128)", fn, head_dim);
+  if (num_tokens > 0x7fffff00LL) return set_error(PKV_ERR_UNSUPPORTED, "%s: num_tokens over 2^31", fn);
+  const int64_t qw = (int64_t)num_q_heads * head_dim, kw = (int64_t)num_kv_heads * head_dim;
+  if (q_stride < qw || out_stride < qw || k_stride < kw || v_stride < kw)
+    return set_error(PKV_ERR_SHAPE, "%s: a token stride is shorter than the token's heads", fn);
+  if (q_stride % 8 || out_stride % 8 || k_stride % 8 || v_stride % 8)
+    return set_error(PKV_ERR_ALIGN, "%s: token strides must be multiples of 8 elements", fn);
+  if (q_stride > (1LL << 38) || out_stride > (1LL << 38) || k_stride > (1LL << 38) ||
+      v_stride > (1LL << 38))
+    return set_error(PKV_ERR_UNSUPPORTED, "%s: a token stride is too long", fn);
+  if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) {
+    clear_error();
+    return PKV_OK;
+  }
+  if (!out || !q || !k || !v || !query_start) return set_error(PKV_ERR_NULL, "%s: NULL pointer", fn);
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k) || !aligned16(v))
+    return set_error(PKV_ERR_ALIGN, "%s: out, q, k and v must be 16-byte aligned", fn);
+  if (reinterpret_cast<uintptr_t>(query_start) & 3u)
+    return set_error(PKV_ERR_ALIGN, "%s: query_start must be 4-byte aligned", fn);
+  TileArgs a = {};
+  a.q = q;
+  a.out = out;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.start = query_start;
+  a.num = num_seqs;
+  a.total = (int32_t)num_tokens;
+  a.max_len = max_query_len;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.group = num_q_heads / num_kv_heads;
+  a.scale_log2 = scale * kLog2e;
+  // tiles of all sequences: at most the packed rows' plus one partial tile per sequence
+  const int64_t tiles = num_tokens * a.group / (2 * kTcRows) + std::min<int64_t>(num_seqs, num_tokens);
+  if (tiles > 0x7fffffffLL / num_kv_heads) return set_error(PKV_ERR_UNSUPPORTED, "%s: too many query rows", fn);
+  CUtensorMap tmk, tmv;
+  int rc;
+  {
+    std::lock_guard<std::mutex> lk(attn_mutex());
+    rc = packed_map(k, num_tokens, num_kv_heads, head_dim, k_stride, kTcKeys, &tmk);
+    if (!rc) rc = packed_map(v, num_tokens, num_kv_heads, head_dim, v_stride, kTcKeys, &tmv);
+  }
+  if (rc) return rc;
+  const unsigned grid = (unsigned)(tiles * num_kv_heads);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  rc = head_dim == 64 ? launch_prompt<64>(tmk, tmv, a, grid, s) : launch_prompt<128>(tmk, tmv, a, grid, s);
+  if (!rc) clear_error();
+  return rc;
+}
