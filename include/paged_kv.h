@@ -283,6 +283,43 @@ int paged_decode_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k_c
                            size_t workspace_bytes, void *stream);
 
 /*
+ * paged_decode_shared_prefix_attention -- paged_decode_attention for a batch whose
+ * sequences share long prefixes (forks of one request, or requests behind one system
+ * prompt; "mini-vLLM" README, paged KV-cache paragraph: block tables map positions to
+ * physical blocks, so sequences can map to the same ones).  A shared page is read once for
+ * the group and not once per sequence.
+ *
+ * Group g is the sequences group_start[g] .. group_start[g+1]-1 (DEVICE int32 [num_groups
+ * + 1], nondecreasing, within num_seqs).  The caller states that their first prefix_lens[g]
+ * tokens (DEVICE int32 [num_groups]; only the whole pages of them are taken as shared) lie
+ * in the same pages: their block-table rows agree on those entries, and the first
+ * sequence's row is the one that is read.  The result is that of paged_decode_attention(q,
+ * ..., block_tables, context_lens), to fp32 rounding and the bf16 rounding of the prefix's
+ * weights: each sequence attends to its own first context_lens[b] tokens, even where that
+ * is less than the prefix, and context_lens[b] == 0 gives zeros.  Sequences of no group
+ * are computed without a prefix.
+ *
+ * max_prefix_len >= every prefix_lens[g], and max_suffix_len >= every context_lens[b] less
+ * the whole pages of its group's prefix; both are at most max_blocks_per_seq * block_size.
+ * A longer one is cut there and raises PKV_DEVERR_CONTEXT_LEN, like a group that is
+ * misplaced.  Layouts, supported sizes, alignment, and the rules for the workspace
+ * (zero-filled before its first use, left ready by every call, not shared by calls that
+ * overlap; paged_decode_shared_prefix_workspace_size() bytes) are those of
+ * paged_decode_attention.  All arguments are DEVICE memory.
+ */
+size_t paged_decode_shared_prefix_workspace_size(int32_t num_seqs, int32_t num_q_heads,
+                                                 int32_t num_kv_heads, int32_t head_dim,
+                                                 int32_t num_groups, int32_t max_prefix_len,
+                                                 int32_t max_suffix_len);
+int paged_decode_shared_prefix_attention(
+    pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k_cache, const pkv_bf16 *v_cache,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens,
+    const int32_t *group_start, const int32_t *prefix_lens, int32_t num_groups,
+    int32_t max_prefix_len, int32_t max_suffix_len, int32_t num_seqs, int32_t num_q_heads,
+    const pkv_cache_desc *cache, float scale, void *workspace, size_t workspace_bytes,
+    void *stream);
+
+/*
  * paged_decode_step -- one whole decode step: paged_kv_write(k, v, slot_mapping,
  * num_tokens, ...) into the caches, then paged_decode_attention over the updated
  * caches ("vLLM-Style Llama Inference Engine", How it works: each rank writes its

@@ -71,6 +71,11 @@ _lib.paged_decode_split_workspace_size.restype = _sz
 _lib.paged_decode_attention.argtypes = [_P, _P, _P, _P, _P, _i32, _P, _i32, _i32, _i32, _D, _f32,
                                         _P, _sz, _P]
 _lib.paged_decode_attention.restype = ctypes.c_int
+_lib.paged_decode_shared_prefix_workspace_size.argtypes = [_i32] * 7
+_lib.paged_decode_shared_prefix_workspace_size.restype = _sz
+_lib.paged_decode_shared_prefix_attention.argtypes = [_P, _P, _P, _P, _P, _i32, _P, _P, _P, _i32,
+                                                      _i32, _i32, _i32, _i32, _D, _f32, _P, _sz, _P]
+_lib.paged_decode_shared_prefix_attention.restype = ctypes.c_int
 _lib.paged_decode_step.argtypes = [_P, _P, _P, _P, _P, _i64, _P, _P, _P, _i32, _P, _i32, _i32,
                                    _i32, _D, _f32, _P, _sz, _P]
 _lib.paged_decode_step.restype = ctypes.c_int
@@ -385,6 +390,55 @@ def paged_decode_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Te
                                        _ptr(context_lens), int(max_context_len), B, Hq,
                                        ctypes.byref(d), float(scale), _ptr(workspace), ws_bytes,
                                        _stream(stream)), "paged_decode_attention")
+
+
+def paged_decode_shared_prefix_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
+                                              head_dim: int, num_groups: int, max_prefix_len: int,
+                                              max_suffix_len: int) -> int:
+    return int(_lib.paged_decode_shared_prefix_workspace_size(
+        num_seqs, num_q_heads, num_kv_heads, head_dim, num_groups, max_prefix_len, max_suffix_len))
+
+
+def paged_decode_shared_prefix_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                                         v_cache: torch.Tensor, block_tables: torch.Tensor,
+                                         context_lens: torch.Tensor, group_start: torch.Tensor,
+                                         prefix_lens: torch.Tensor, max_prefix_len: int,
+                                         max_suffix_len: int, scale: float,
+                                         workspace: Optional[torch.Tensor] = None,
+                                         stream=None) -> None:
+    """paged_decode_attention where the sequences group_start[g] .. group_start[g+1]-1 share
+    the pages of their first prefix_lens[g] tokens, which are read once per group.
+
+    max_suffix_len bounds every context_len less the whole pages of its prefix; ``workspace``
+    is as in paged_decode_attention, of ``paged_decode_shared_prefix_workspace_size`` bytes.
+    """
+    _decode_checks(q, k_cache, v_cache, block_tables, context_lens)
+    _need(out, "out", torch.bfloat16, 3)
+    _need(group_start, "group_start", torch.int32, 1)
+    _need(prefix_lens, "prefix_lens", torch.int32, 1)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    groups = prefix_lens.shape[0]
+    if group_start.shape[0] != groups + 1:
+        raise ValueError("group_start must be [G + 1] for prefix_lens [G]")
+    _one_device(q, out=out, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                context_lens=context_lens, group_start=group_start, prefix_lens=prefix_lens,
+                workspace=workspace)
+    B, Hq, D = q.shape
+    NB, Hkv, BS, _ = k_cache.shape
+    if workspace is None:
+        need = paged_decode_shared_prefix_workspace_size(B, Hq, Hkv, D, groups, max_prefix_len,
+                                                         max_suffix_len)
+        workspace = torch.zeros(max(need, 1), dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    d = pkv_cache_desc(NB, BS, Hkv, D)
+    _check(_lib.paged_decode_shared_prefix_attention(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+        block_tables.shape[1], _ptr(context_lens), _ptr(group_start), _ptr(prefix_lens), groups,
+        int(max_prefix_len), int(max_suffix_len), B, Hq, ctypes.byref(d), float(scale),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
+        "paged_decode_shared_prefix_attention")
 
 
 def paged_decode_step(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,

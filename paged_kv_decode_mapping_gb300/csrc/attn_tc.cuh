@@ -29,8 +29,8 @@
 
 namespace pkv {
 
-constexpr int kTcRows = 128;     // query rows of a tile
-constexpr int kTcKeys = 128;     // keys per block
+constexpr int kTcRows = kTileRows;
+constexpr int kTcKeys = kTileKeys;
 // A row's reference max moves only when a block raises it by more than this (base 2).
 constexpr float kTcRescale = 8.f;
 

@@ -203,6 +203,7 @@ PKV_API int pkv_device_errors(uint32_t *flags, int clear) {
   if ((e = read_write_errors(flags, clear)) != cudaSuccess) return cuda_error(e, "write error word");
   if ((e = read_page_errors(flags, clear)) != cudaSuccess) return cuda_error(e, "page error word");
   if ((e = read_tile_errors(flags, clear)) != cudaSuccess) return cuda_error(e, "tile error word");
+  if ((e = read_shared_errors(flags, clear)) != cudaSuccess) return cuda_error(e, "tail error word");
   clear_error();
   return PKV_OK;
 }

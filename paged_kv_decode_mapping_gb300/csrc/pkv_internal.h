@@ -111,6 +111,24 @@ cudaError_t read_decode_errors(uint32_t *flags, int clear);
 cudaError_t read_prefill_errors(uint32_t *flags, int clear);
 cudaError_t read_page_errors(uint32_t *flags, int clear);
 cudaError_t read_tile_errors(uint32_t *flags, int clear);
+cudaError_t read_shared_errors(uint32_t *flags, int clear);
+
+// The shared-prefix half of paged_decode_shared_prefix_attention (pkv_tiles.cu): the
+// partial results of split s of every query row of the groups, in rows 2 s and 2 s + 1 of
+// o_part [B][Hq][n_rows][D] and lse_part [B][Hq][n_rows].  Arguments already checked.
+constexpr int kTileRows = 128;  // query rows of a tile
+constexpr int kTileKeys = 128;  // keys per block
+struct PrefixLaunch {
+  const pkv_bf16 *q;
+  const int32_t *block_tables, *context_lens, *group_start, *prefix_lens;
+  float *o_part, *lse_part;
+  int32_t num_seqs, num_groups, max_blocks, max_prefix, num_q_heads;
+  int32_t split_keys, splits, n_rows;
+  int64_t tiles;  // row tiles over all groups, at most
+  float scale;
+};
+int launch_prefix(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv_cache_desc &c,
+                  const PrefixLaunch &l, cudaStream_t stream);
 
 }  // namespace pkv
 

@@ -47,7 +47,7 @@ struct TileArgs {
   const int32_t *block_tables, *context_lens, *prefix_lens;
   int64_t num_blocks;
   int32_t max_blocks, max_prefix, block_size, log2_bs, box_rows;
-  int32_t split_keys;       // keys per split (a multiple of 2 * kTcKeys)
+  int32_t split_keys;       // keys per split (a multiple of kTcKeys)
   int32_t n_rows;           // partial rows per (sequence, head)
   float *o_part, *lse_part; // [B][Hq][n_rows][D], [B][Hq][n_rows]; rows 2 s, 2 s + 1: split s
 };
@@ -568,7 +568,51 @@ int launch_prompt(const CUtensorMap &tmk, const CUtensorMap &tmv, const TileArgs
   return e == cudaSuccess ? PKV_OK : cuda_error(e, "tile_kernel launch");
 }
 
+template <int D>
+int launch_prefix_tiles(const CUtensorMap &tmk, const CUtensorMap &tmv, const TileArgs &a, dim3 grid,
+                        cudaStream_t stream) {
+  const int rc = prepare_tile_kernel<D, kPrefix>();
+  if (rc) return rc;
+  tile_kernel<D, kPrefix><<<grid, kTileThreads, tile_smem<D, kPrefix>(), stream>>>(tmk, tmv, a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? PKV_OK : cuda_error(e, "tile_kernel launch");
+}
+
 }  // namespace
+
+int launch_prefix(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv_cache_desc &c,
+                  const PrefixLaunch &l, cudaStream_t stream) {
+  TileArgs a = {};
+  a.q = l.q;
+  a.q_stride = (int64_t)l.num_q_heads * c.head_dim;
+  a.start = l.group_start;
+  a.num = l.num_groups;
+  a.total = l.num_seqs;
+  a.max_len = l.num_seqs;
+  a.num_q_heads = l.num_q_heads;
+  a.num_kv_heads = c.num_kv_heads;
+  a.group = l.num_q_heads / c.num_kv_heads;
+  a.scale_log2 = l.scale * kLog2e;
+  a.block_tables = l.block_tables;
+  a.context_lens = l.context_lens;
+  a.prefix_lens = l.prefix_lens;
+  a.num_blocks = c.num_blocks;
+  a.max_blocks = l.max_blocks;
+  a.max_prefix = l.max_prefix;
+  a.block_size = c.block_size;
+  a.log2_bs = ilog2(c.block_size);
+  a.box_rows = std::min(c.block_size, (int32_t)kChunk);
+  a.split_keys = l.split_keys;
+  a.n_rows = l.n_rows;
+  a.o_part = l.o_part;
+  a.lse_part = l.lse_part;
+  if (l.tiles * c.num_kv_heads > 0x7fffffffLL || l.splits > 65535)
+    return set_error(PKV_ERR_UNSUPPORTED, "shared prefix: too many tiles");
+  const dim3 grid((unsigned)(l.tiles * c.num_kv_heads), (unsigned)l.splits);
+  return c.head_dim == 64 ? launch_prefix_tiles<64>(tmk, tmv, a, grid, stream)
+                          : launch_prefix_tiles<128>(tmk, tmv, a, grid, stream);
+}
+
 }  // namespace pkv
 
 using namespace pkv;
