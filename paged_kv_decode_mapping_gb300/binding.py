@@ -9,6 +9,7 @@ the library's kernels; there is no fallback.  Importing this module raises if
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import Optional
@@ -139,8 +140,10 @@ def _check(rc: int, where: str):
 
 
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # torch.cuda.current_stream().cuda_stream without the Stream object (0.2 against 2.8 us)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -214,12 +217,18 @@ def paged_kv_write_rope(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Te
 
 def _one_device(where: torch.Tensor, **tensors) -> None:
     """The tensors are on one device, which is the current one (the library launches there)."""
-    dev = where.device
+    dev = where.get_device()
     for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: on {t.device}, expected {dev}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, the current device is {torch.cuda.current_device()}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name}: on {t.device}, expected {where.device}")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {where.device}, the current device is "
+                         f"{torch.cuda.current_device()}")
+
+
+def _pointers(values) -> array.array:
+    """A host array of device pointers (built faster than a ctypes one)."""
+    return array.array("Q", values)
 
 
 def _layers(k_caches, v_caches, where: str):
@@ -239,11 +248,11 @@ def _layers(k_caches, v_caches, where: str):
         _one_device(k_caches, v_caches=v_caches)
         n = 1 if ndim == 4 else k_caches.shape[0]
         step = 2 * k_caches.numel() // max(n, 1)
-        k0, v0 = k_caches.data_ptr(), v_caches.data_ptr()
-        kp = (_P * n)(*[k0 + i * step for i in range(n)])
-        vp = (_P * n)(*[v0 + i * step for i in range(n)])
         NB, Hkv, BS, D = k_caches.shape[-4:]
-        return kp, vp, n, pkv_cache_desc(NB, BS, Hkv, D), k_caches
+        k0, v0 = k_caches.data_ptr(), v_caches.data_ptr()
+        return (_pointers(range(k0, k0 + n * step, step) if step else [k0] * n),
+                _pointers(range(v0, v0 + n * step, step) if step else [v0] * n), n,
+                pkv_cache_desc(NB, BS, Hkv, D), k_caches)
     ks, vs = list(k_caches), list(v_caches)
     if len(ks) != len(vs) or not ks:
         raise ValueError(f"{where}: k_caches and v_caches need one cache per layer each")
@@ -252,8 +261,7 @@ def _layers(k_caches, v_caches, where: str):
         if t.shape != ks[0].shape:
             raise ValueError(f"{where}: the layers' caches have different shapes")
         _one_device(ks[0], cache=t)
-    n = len(ks)
-    return ((_P * n)(*[t.data_ptr() for t in ks]), (_P * n)(*[t.data_ptr() for t in vs]), n,
+    return (_pointers(t.data_ptr() for t in ks), _pointers(t.data_ptr() for t in vs), len(ks),
             cache_desc(ks[0]), ks[0])
 
 
@@ -274,7 +282,7 @@ def paged_kv_copy_blocks(k_caches, v_caches, block_pairs: torch.Tensor,
         if num_tokens.shape[0] != block_pairs.shape[0]:
             raise ValueError("num_tokens must have one entry per pair")
     _one_device(first, block_pairs=block_pairs, num_tokens=num_tokens)
-    _check(_lib.paged_kv_copy_blocks(kp, vp, n, _ptr(block_pairs), _ptr(num_tokens),
+    _check(_lib.paged_kv_copy_blocks(kp.buffer_info()[0], vp.buffer_info()[0], n, _ptr(block_pairs), _ptr(num_tokens),
                                      block_pairs.shape[0], ctypes.byref(d), _stream(stream)),
            "paged_kv_copy_blocks")
 
@@ -299,7 +307,7 @@ def paged_kv_compact(k_caches, v_caches, block_moves: torch.Tensor,
             raise ValueError("block_map must have one entry per block")
         rows, cols = block_tables.shape
     _one_device(first, block_moves=block_moves, block_tables=block_tables, block_map=block_map)
-    _check(_lib.paged_kv_compact(kp, vp, n, _ptr(block_moves), block_moves.shape[0],
+    _check(_lib.paged_kv_compact(kp.buffer_info()[0], vp.buffer_info()[0], n, _ptr(block_moves), block_moves.shape[0],
                                  _ptr(block_tables), rows, cols, _ptr(block_map), ctypes.byref(d),
                                  _stream(stream)), "paged_kv_compact")
 

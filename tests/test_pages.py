@@ -194,6 +194,9 @@ def test_binding_refuses_tensors_of_another_device(B, monkeypatch):
         def __init__(self, index):
             self.device = torch.device("cuda", index)
 
+        def get_device(self):
+            return self.device.index
+
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     B._one_device(Fake(0), a=Fake(0), b=None)
     with pytest.raises(ValueError, match="current device"):
