@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "attn_tc.cuh"
 
@@ -17,7 +18,7 @@ namespace pkv {
 // pairs -- as two tiles in ping-pong: while four softmax warps work on one tile's scores
 // (one thread per row), the tensor core works on the other tile.
 //   S_t = Q_t . K_j^T   tcgen05.mma M=128 N=128 K=D, both K-major in shared memory, S_t in TMEM
-//   P_t = exp2(S_t * scale - m)  fp32, rounded to bf16 into TMEM over the upper half of S_t
+//   P_t = exp2(S_t * scale - m)  fp32, rounded to bf16 into TMEM over columns of S_t already read
 //   O_t += P_t . V_j    P_t from TMEM, V_j MN-major in shared memory, O_t in TMEM
 // The row's reference max m moves only when a block raises it by more than kTcRescale;
 // then O_t and the row sum are rescaled.  The row sum adds the bf16-rounded weights that
@@ -68,8 +69,8 @@ struct TileSmem {
   static constexpr bool kOnes = D == 64;
   static constexpr uint32_t ones = q + kQ * kTile;
   static constexpr uint32_t bars = ones + (kOnes ? kSub : 0);
-  // the rings, then s_full/p_full/pv_done per tile, q_ready, mma_done
-  static constexpr int kBars = 4 * KS + 8;
+  // the rings, then s_full and pv_done per tile, p_half per tile and half, q_ready, mma_done
+  static constexpr int kBars = 4 * KS + 10;
   static constexpr uint32_t tslot = bars + kBars * 8;
   static constexpr uint32_t flag = tslot + 8;
   static constexpr uint32_t total = flag + 8;
@@ -174,6 +175,58 @@ __device__ __forceinline__ void load_packed_block(const CUtensorMap *tm, uint32_
       : "memory");
 }
 
+// ---------------------------------------------------------------------------
+// The softmax threads' work on one block, in two passes over the row's 128 columns of S_t,
+// 32 at a time out of TMEM.  The second pass is a loop over the two 64-column halves (its
+// straight-line form stalled on instruction fetches), and each half of P is published as
+// soon as it is stored, so that its P.V runs under the other half's exponentials.
+
+// The largest of columns c <= lim (all with kMask = false) of the row, unscaled; -inf if
+// there is none.  Leaves columns 0 .. 31 in x0.
+template <bool kMask>
+__device__ __forceinline__ float row_max(uint32_t sb, int lim, uint32_t (&x0)[32]) {
+  float mx[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
+  uint32_t xb[32];
+  dev::tmem_ld32(sb + 96, xb);
+  tmem_wait_ld_regs(xb);
+#pragma unroll
+  for (int ch = 3; ch >= 0; --ch) {  // the buffers alternate; chunk 0 ends in x0
+    uint32_t(&cur)[32] = (ch & 1) ? xb : x0;
+    uint32_t(&nxt)[32] = (ch & 1) ? x0 : xb;
+    if (ch > 0) dev::tmem_ld32(sb + (ch - 1) * 32, nxt);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int c = ch * 32 + 2 * e;
+      const float a = __uint_as_float(cur[2 * e]), b = __uint_as_float(cur[2 * e + 1]);
+      mx[e & 7] = fmax3(mx[e & 7], !kMask || c <= lim ? a : -INFINITY,
+                        !kMask || c + 1 <= lim ? b : -INFINITY);
+    }
+    if (ch > 0) tmem_wait_ld_regs(nxt);
+  }
+  return fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
+}
+
+// P = exp2(S * scale - m) of the 32 columns x (columns c0 .. of the row) as bf16 pairs, and
+// their sum added to ls.
+template <bool kMask, bool kSum>
+__device__ __forceinline__ void chunk_exp(const uint32_t (&x)[32], int c0, int lim, float scale_log2,
+                                          float m, uint32_t *pk, float (&ls)[4]) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float a0, a1;
+    fma_f32x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), scale_log2, -m, a0, a1);
+    if constexpr (kMask) {
+      a0 = c0 + 2 * e <= lim ? a0 : -INFINITY;
+      a1 = c0 + 2 * e + 1 <= lim ? a1 : -INFINITY;
+    }
+    pk[e] = dev::pack_bf16x2(dev::ex2(a0), dev::ex2(a1));
+    // what the tensor core multiplies: the weights stay a convex combination whatever m is
+    if constexpr (kSum) ls[e & 3] = add_bf16x2(pk[e], ls[e & 3]);
+  }
+}
+
 template <int D, int MODE>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -186,7 +239,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   constexpr int kON = D + (kOnes ? 16 : 0);    // O columns per tile (then the row sums)
   constexpr int kTileRowsCta = kShareKeys ? 2 * kTcRows : kTcRows;
   constexpr int kProducer = 8, kMma = 9, kProducerV = 10;
-  constexpr uint32_t kPCol = 64;  // P_t's columns within S_t (a thread reads all of its row first)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = dev::smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -197,10 +249,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto v_full = [&](int s) { return bars + 8u * (2 * KS + s); };
   auto v_empty = [&](int s) { return bars + 8u * (3 * KS + s); };
   auto s_full = [&](int t) { return bars + 8u * (4 * KS + t); };
-  auto p_full = [&](int t) { return bars + 8u * (4 * KS + 2 + t); };
-  auto pv_done = [&](int t) { return bars + 8u * (4 * KS + 4 + t); };
-  const uint32_t q_ready = bars + 8u * (4 * KS + 6);
-  const uint32_t mma_done = bars + 8u * (4 * KS + 7);
+  auto pv_done = [&](int t) { return bars + 8u * (4 * KS + 2 + t); };
+  auto p_half = [&](int t, int hf) { return bars + 8u * (4 * KS + 4 + 2 * t + hf); };
+  const uint32_t q_ready = bars + 8u * (4 * KS + 8);
+  const uint32_t mma_done = bars + 8u * (4 * KS + 9);
   volatile uint32_t *const s_tmem = reinterpret_cast<volatile uint32_t *>(bp + SL::tslot);
   volatile int *const s_flag = reinterpret_cast<volatile int *>(bp + SL::flag);
 
@@ -254,7 +306,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < SL::kBars; ++i) {
       const uint32_t bar = bars + 8u * i;
-      const uint32_t count = bar == p_full(0) || bar == p_full(1) ? 4u
+      const uint32_t count = i >= 4 * KS + 4 && i < 4 * KS + 8 ? 4u  // p_half: one per warp
                              : bar == q_ready ? (kShareKeys ? 8u : 4u) : 1u;
       dev::mbar_init(bar, count);
     }
@@ -339,11 +391,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int t = 0; t < 2 && ok; ++t) {
           if (i >= nb_of(t)) continue;
           const int j = blk(t, i), s = j % KS;
-          if (!(ok = fail(dev::mbar_wait(p_full(t), i & 1)))) break;
           if (!(ok = fail(dev::mbar_wait(v_full(s), (j / KS) & 1)))) break;
-          dev::tc_fence_after();
-          issue_pv_ts(tmem + 256u + (uint32_t)(kON * t), tmem + 128u * t + kPCol, dv(s), id_o,
-                      i > 0 ? 1u : 0u);
+          const uint64_t dvs = dv(s);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {  // keys 0-63, then 64-127 of the block
+            if (!(ok = fail(dev::mbar_wait(p_half(t, hf), i & 1)))) break;
+            dev::tc_fence_after();
+            const uint32_t p = tmem + 128u * t + 32u * hf;
+            const uint64_t vh = desc_add(dvs, hf * 4 * 2048u);
+            umma4_ts(tmem + 256u + (uint32_t)(kON * t), p, p + 8, p + 16, p + 24, vh,
+                     desc_add(vh, 2048), desc_add(vh, 4096), desc_add(vh, 6144), id_o,
+                     hf > 0 || i > 0 ? 1u : 0u);
+          }
+          if (!ok) break;
           dev::umma_commit(pv_done(t));
           if (last_user(t, i)) dev::umma_commit(v_empty(s));
           // S_t(i+1) over S_t(i) and P_t(i), after the P.V that reads P_t(i): the MMAs of
@@ -370,12 +430,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       see = min(max(__ldg(a.context_lens + first + qi), 0), t_end);
     else
       see = qi + 1;
+    // a negative scale changes the queries' signs, so that the softmax sees none
+    const float scale_log2 = fabsf(a.scale_log2);
+    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
     if (kShareKeys || t == 0) {  // the tile's query rows (zeros past the end)
       const uint4 *src = reinterpret_cast<const uint4 *>(
           a.q + (int64_t)(first + qi) * a.q_stride + (int64_t)(g * G + h) * D);
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
-        const uint4 x = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        uint4 x = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
         *reinterpret_cast<uint4 *>(bp + SL::q + (kShareKeys ? t * SL::kTile : 0u) +
                                    (c >> 3) * SL::kSub + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
       }
@@ -384,8 +448,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (lane == 0) dev::mbar_arrive(q_ready);
     }
     const int nb = nb_of(t);
-    float m_ref = -INFINITY, lsum = 0.f;
-    const bool pos_scale = a.scale_log2 > 0.f;
+    float m_ref = -INFINITY;
+    float ls[4] = {0.f, 0.f, 0.f, 0.f};
     bool ok = true;
     auto rescale_o = [&](float f) {  // O_t (and its row-sum column) and the row sum scale by f
 #pragma unroll 1
@@ -403,50 +467,34 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tmem_st1(ob + D, __float_as_uint(__uint_as_float(sm) * f));
       }
       dev::tmem_wait_st();
-      lsum *= f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) ls[u] *= f;
     };
-    for (int i = 0; i < nb; ++i) {
-      const int j = blk(t, i), k0 = key0 + j * kTcKeys;
-      const int lim = see - 1 - k0;  // columns c <= lim are seen
-      if (!(ok = __all_sync(0xffffffffu, dev::mbar_wait(s_full(t), i & 1)))) break;
-      dev::tc_fence_after();
-      const bool whole = __all_sync(0xffffffffu, lim >= kTcKeys - 1);
-      uint32_t x[128], pk[64];
-      float ls;
-      row_block_load<4>(sb, 0, x);
-      // A row that has seen no key yet has m_ref = -inf: its weights (all masked to 0) are
-      // taken against 0 then.
+    // One block; false when a wait gave up.
+    auto block = [&](auto mask, int i, int j, int k0, int lim) {
+      constexpr bool kMask = decltype(mask)::value;
+      uint32_t xa[32];
+      const float mx = row_max<kMask>(sb, lim, xa);
+      const float bm = mx == -INFINITY ? -INFINITY : mx * scale_log2;
       if (i > 0) {
-        // the weights against the reference they start with, and the block's max, in one
-        // pass; the weights again when the block moves the reference.  PV_t(i-1) was issued
-        // before S_t(i) by the same thread, and s_full tracks every MMA issued before its
-        // commit, so O_t is stable here.
-        float bm;
-        ls = row_regs_exp_pk_max<4, !kOnes>(x, 0, lim, whole, pos_scale, a.scale_log2,
-                                            m_ref == -INFINITY ? 0.f : m_ref, pk, &bm);
+        // The reference moves only when the block raises it by more than kTcRescale.
+        // PV_t(i-1) was issued before S_t(i) by the same thread, and s_full tracks every
+        // MMA issued before its commit, so O_t is stable here.
         const bool need = bm > m_ref + kTcRescale;
         if (__any_sync(0xffffffffu, need)) {
           const float m_new = fmaxf(m_ref, bm);
-          const float f = need ? dev::ex2(m_ref - m_new) : 1.f;
+          rescale_o(need ? dev::ex2(m_ref - m_new) : 1.f);
           if (need) m_ref = m_new;
-          row_block_load<4>(sb, 0, x);
-          ls = row_regs_exp_pk<4, !kOnes>(x, 0, lim, whole, a.scale_log2,
-                                          m_ref == -INFINITY ? 0.f : m_ref, pk);
-          rescale_o(f);
         }
       } else {
-        m_ref = row_regs_max<4>(x, 0, lim, whole, pos_scale, a.scale_log2);
-        ls = row_regs_exp_pk<4, !kOnes>(x, 0, lim, whole, a.scale_log2,
-                                        m_ref == -INFINITY ? 0.f : m_ref, pk);
+        m_ref = bm;
       }
-      lsum += ls;
-      dev::tmem_st32(sb + kPCol, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-      dev::tmem_st32(sb + kPCol + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
-      dev::tmem_wait_st();
+      // a row that has seen no key yet takes its weights, all masked to 0, against 0
+      const float m = m_ref == -INFINITY ? 0.f : m_ref;
       const int nk = min(kTcKeys, t_end - k0);
-      if (nk < kTcKeys) {  // V rows past the staged keys are stale or another sequence's
+      if (kMask && nk < kTcKeys) {  // V rows past the staged keys are stale or another sequence's
         const int s = j % KS;
-        if (!(ok = __all_sync(0xffffffffu, dev::mbar_wait(v_full(s), (j / KS) & 1)))) break;
+        if (!__all_sync(0xffffffffu, dev::mbar_wait(v_full(s), (j / KS) & 1))) return false;
         const uint32_t vt = SL::v + s * SL::kTile;
         for (int idx = r; idx < (kTcKeys - nk) * (D / 8); idx += kTcRows) {
           const int row = nk + idx / (D / 8), c = idx % (D / 8);
@@ -455,10 +503,34 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         dev::fence_proxy_async_smem();
       }
-      dev::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) dev::mbar_arrive(p_full(t));
+#pragma unroll 1
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t xb[32], pk[32];
+        dev::tmem_ld32(sb + 64 * hf + 32, xb);
+        chunk_exp<kMask, !kOnes>(xa, 64 * hf, lim, scale_log2, m, pk, ls);
+        tmem_wait_ld_regs(xb);
+        if (hf == 0) dev::tmem_ld32(sb + 64, xa);
+        chunk_exp<kMask, !kOnes>(xb, 64 * hf + 32, lim, scale_log2, m, pk + 16, ls);
+        if (hf == 0) tmem_wait_ld_regs(xa);
+        dev::tmem_st32(sb + 32 * hf, pk);  // over columns this thread has read
+        dev::tmem_wait_st();
+        dev::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(p_half(t, hf));
+      }
+      return true;
+    };
+    for (int i = 0; i < nb && ok; ++i) {
+      const int j = blk(t, i), k0 = key0 + j * kTcKeys;
+      const int lim = see - 1 - k0;  // columns c <= lim are seen
+      if (!(ok = __all_sync(0xffffffffu, dev::mbar_wait(s_full(t), i & 1)))) break;
+      dev::tc_fence_after();
+      if (__all_sync(0xffffffffu, lim >= kTcKeys - 1))
+        ok = block(std::false_type{}, i, j, k0, lim);
+      else
+        ok = block(std::true_type{}, i, j, k0, lim);
     }
+    float lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
     if (!ok && lane == 0) fail(false);
     if (ok && nb > 0 && !(ok = __all_sync(0xffffffffu, dev::mbar_wait(pv_done(t), (nb - 1) & 1))) &&
         lane == 0)
