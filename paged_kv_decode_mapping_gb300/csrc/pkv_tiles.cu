@@ -23,7 +23,8 @@ namespace pkv {
 // The row's reference max m moves only when a block raises it by more than kTcRescale;
 // then O_t and the row sum are rescaled.  The row sum adds the bf16-rounded weights that
 // the tensor core multiplies, so the weights stay a convex combination whatever m is.
-// K and V stream through separate rings, each with its producer warp.
+// K and V stream through separate rings, each with its producer warp; each tile's MMAs are
+// issued by a thread of their own.
 //
 // Two ways of pairing:
 //  * kPrompt: the tiles are 128 query rows each of one packed sequence and share every
@@ -53,24 +54,30 @@ struct TileArgs {
   float *o_part, *lse_part; // [B][Hq][n_rows][D], [B][Hq][n_rows]; rows 2 s, 2 s + 1: split s
 };
 
-constexpr int kTileThreads = 32 * 11;  // 8 softmax warps, K producer, MMA, V producer
+constexpr int kTileThreads = 32 * 12;  // 8 softmax warps, the K and V producers, an MMA warp per tile
 
 template <int D, int MODE>
 struct TileSmem {
-  static constexpr int KS = D == 64 ? 4 : (MODE == kPrompt ? 2 : 3);  // K and V ring stages
+  // K and V ring stages.  kPrefix: even, so that a stage serves one tile alone (block j is
+  // tile j & 1's): a waiter may trust a barrier's parity only if it saw the phase before,
+  // and a tile's MMA thread sees the phases of its own blocks.
+  static constexpr int KSK = D == 64 ? 4 : (MODE == kPrompt ? 2 : 4);
+  static constexpr int KSV = D == 64 ? 4 : 2;
+  static_assert(MODE == kPrompt || (KSK % 2 == 0 && KSV % 2 == 0), "one tile per stage");
   static constexpr uint32_t kSub = kTcKeys * 128;     // 128 rows x 128 B (64 dims)
   static constexpr uint32_t kTile = kSub * (D / 64);
   static constexpr int kQ = MODE == kPrompt ? 2 : 1;  // Q tiles
   static constexpr uint32_t k = 0;
-  static constexpr uint32_t v = k + KS * kTile;
-  static constexpr uint32_t q = v + KS * kTile;
+  static constexpr uint32_t v = k + KSK * kTile;
+  static constexpr uint32_t q = v + KSV * kTile;
   // head_dim 64: a [128 keys][64] tile of ones, read by P.V as 16 more columns of V, so that
   // the tensor core forms the row sums (O's columns are free in TMEM at 64, not at 128)
   static constexpr bool kOnes = D == 64;
   static constexpr uint32_t ones = q + kQ * kTile;
   static constexpr uint32_t bars = ones + (kOnes ? kSub : 0);
   // the rings, then s_full and pv_done per tile, p_half per tile and half, q_ready, mma_done
-  static constexpr int kBars = 4 * KS + 10;
+  static constexpr int kRings = 2 * KSK + 2 * KSV;  // barriers of the rings
+  static constexpr int kBars = kRings + 10;
   static constexpr uint32_t tslot = bars + kBars * 8;
   static constexpr uint32_t flag = tslot + 8;
   static constexpr uint32_t total = flag + 8;
@@ -232,27 +239,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                 const TileArgs a) {
   using SL = TileSmem<D, MODE>;
-  constexpr int KS = SL::KS;
+  constexpr int KSK = SL::KSK, KSV = SL::KSV, kRings = SL::kRings;
   constexpr bool kPaged = MODE == kPrefix;     // keys from pages; partial outputs
   constexpr bool kShareKeys = MODE == kPrompt; // both tiles take every block
   constexpr bool kOnes = SL::kOnes;
   constexpr int kON = D + (kOnes ? 16 : 0);    // O columns per tile (then the row sums)
   constexpr int kTileRowsCta = kShareKeys ? 2 * kTcRows : kTcRows;
-  constexpr int kProducer = 8, kMma = 9, kProducerV = 10;
+  constexpr int kProducer = 8, kProducerV = 9, kMma = 10;  // kMma + t: tile t's MMA warp
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = dev::smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t *const bp = smem_raw + (base - raw);
   const uint32_t bars = base + SL::bars;
   auto k_full = [&](int s) { return bars + 8u * s; };
-  auto k_empty = [&](int s) { return bars + 8u * (KS + s); };
-  auto v_full = [&](int s) { return bars + 8u * (2 * KS + s); };
-  auto v_empty = [&](int s) { return bars + 8u * (3 * KS + s); };
-  auto s_full = [&](int t) { return bars + 8u * (4 * KS + t); };
-  auto pv_done = [&](int t) { return bars + 8u * (4 * KS + 2 + t); };
-  auto p_half = [&](int t, int hf) { return bars + 8u * (4 * KS + 4 + 2 * t + hf); };
-  const uint32_t q_ready = bars + 8u * (4 * KS + 8);
-  const uint32_t mma_done = bars + 8u * (4 * KS + 9);
+  auto k_empty = [&](int s) { return bars + 8u * (KSK + s); };
+  auto v_full = [&](int s) { return bars + 8u * (2 * KSK + s); };
+  auto v_empty = [&](int s) { return bars + 8u * (2 * KSK + KSV + s); };
+  auto s_full = [&](int t) { return bars + 8u * (kRings + t); };
+  auto pv_done = [&](int t) { return bars + 8u * (kRings + 2 + t); };
+  auto p_half = [&](int t, int hf) { return bars + 8u * (kRings + 4 + 2 * t + hf); };
+  const uint32_t q_ready = bars + 8u * (kRings + 8);
+  const uint32_t mma_done = bars + 8u * (kRings + 9);
   volatile uint32_t *const s_tmem = reinterpret_cast<volatile uint32_t *>(bp + SL::tslot);
   volatile int *const s_flag = reinterpret_cast<volatile int *>(bp + SL::flag);
 
@@ -306,8 +313,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < SL::kBars; ++i) {
       const uint32_t bar = bars + 8u * i;
-      const uint32_t count = i >= 4 * KS + 4 && i < 4 * KS + 8 ? 4u  // p_half: one per warp
-                             : bar == q_ready ? (kShareKeys ? 8u : 4u) : 1u;
+      const uint32_t count = i >= kRings + 4 && i < kRings + 8 ? 4u  // p_half: one per warp
+                             : bar == q_ready ? (kShareKeys ? 8u : 4u)
+                             : bar == mma_done ? 2u
+                             : (i >= KSK && i < 2 * KSK) || (i >= 2 * KSK + KSV && i < kRings)
+                                 ? (kShareKeys && nb1 > 0 ? 2u : 1u)  // empty: its users
+                                 : 1u;
       dev::mbar_init(bar, count);
     }
     *s_flag = 0;
@@ -343,9 +354,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint64_t policy = dev::policy_evict_last();
     int win = win_first;
     for (int j = 0; j < nblk; ++j) {
-      const int s = j % KS;
+      const int ks = is_k ? KSK : KSV, s = j % ks;
       const uint32_t empty = is_k ? k_empty(s) : v_empty(s), full = is_k ? k_full(s) : v_full(s);
-      if (j >= KS && !__all_sync(0xffffffffu, dev::mbar_wait(empty, ((j / KS) - 1) & 1))) {
+      if (j >= ks && !__all_sync(0xffffffffu, dev::mbar_wait(empty, ((j / ks) - 1) & 1))) {
         if (lane == 0) fail(false);
         break;
       }
@@ -358,12 +369,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         load_packed_block(tm, dst, full, SL::kTile, first + j * kTcKeys, g, policy);
       issued = j + 1;
     }
-  } else if (warp == kMma) {
-    // ------------------------------------------------- tensor-core issue (one thread)
+  } else if (warp >= kMma) {
+    // ------------------------------------- tensor-core issue, one thread for each tile:
+    // what one of them does between its MMAs (waits, commits) runs under the other's
+    const int t = warp - kMma;
+    const int nb = t ? nb1 : nb0;
     if (lane == 0) {
       constexpr uint32_t id_s = dev::idesc_bf16_f32(kTcRows, kTcKeys, 0);
       constexpr uint32_t id_o = dev::idesc_bf16_f32(kTcRows, kON, 1);
-      const uint64_t dq0 = dev::smem_desc(base + SL::q, 16, 1024);
+      const uint64_t dq = dev::smem_desc(base + SL::q + (kShareKeys ? t * SL::kTile : 0u), 16, 1024);
       const uint64_t dk0 = dev::smem_desc(base + SL::k, 16, 1024);
       // V stage s as the MN-major B operand: the next 64 columns are V's other half
       // (head_dim 128) or the tile of ones, `lbo` bytes further on
@@ -371,45 +385,44 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t vs = SL::v + s * SL::kTile;
         return dev::smem_desc(base + vs, kOnes ? SL::ones - vs : SL::kSub, 1024);
       };
-      // the last tile that reads block blk(t, i) frees its stage
-      auto last_user = [&](int t, int i) { return !kShareKeys || t == 1 || i >= nb1; };
-      auto issue_s = [&](int t, int i) {
-        const int j = blk(t, i), s = j % KS;
-        if (!fail(dev::mbar_wait(k_full(s), (j / KS) & 1))) return false;
+      const uint32_t s_tm = tmem + 128u * t, o_tm = tmem + 256u + (uint32_t)(kON * t);
+      auto issue_s = [&](int i) {
+        const int j = blk(t, i), s = j % KSK;
+        if (!fail(dev::mbar_wait(k_full(s), (j / KSK) & 1))) return false;
         dev::tc_fence_after();
-        issue_qk<D>(tmem + 128u * t, desc_add(dq0, kShareKeys ? t * SL::kTile : 0),
-                    desc_add(dk0, s * SL::kTile), SL::kSub, id_s);
+        issue_qk<D>(s_tm, dq, desc_add(dk0, s * SL::kTile), SL::kSub, id_s);
         dev::umma_commit(s_full(t));
-        if (last_user(t, i)) dev::umma_commit(k_empty(s));
+        dev::umma_commit(k_empty(s));
         return true;
       };
       bool ok = fail(dev::mbar_wait(q_ready, 0));
-      if (ok && nb0 > 0) ok = issue_s(0, 0);
-      if (ok && nb1 > 0) ok = issue_s(1, 0);
-      const int most = max(nb0, nb1);
-      for (int i = 0; ok && i < most; ++i) {
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (i >= nb_of(t)) continue;
-          const int j = blk(t, i), s = j % KS;
-          if (!(ok = fail(dev::mbar_wait(v_full(s), (j / KS) & 1)))) break;
-          const uint64_t dvs = dv(s);
+      if (ok && nb > 0) ok = issue_s(0);
+      for (int i = 0; ok && i < nb; ++i) {
+        const int j = blk(t, i), s = j % KSV;
+        if (!(ok = fail(dev::mbar_wait(v_full(s), (j / KSV) & 1)))) break;
+        const uint64_t dvs = dv(s);
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {  // keys 0-63, then 64-127 of the block
-            if (!(ok = fail(dev::mbar_wait(p_half(t, hf), i & 1)))) break;
-            dev::tc_fence_after();
-            const uint32_t p = tmem + 128u * t + 32u * hf;
-            const uint64_t vh = desc_add(dvs, hf * 4 * 2048u);
-            umma4_ts(tmem + 256u + (uint32_t)(kON * t), p, p + 8, p + 16, p + 24, vh,
-                     desc_add(vh, 2048), desc_add(vh, 4096), desc_add(vh, 6144), id_o,
-                     hf > 0 || i > 0 ? 1u : 0u);
-          }
-          if (!ok) break;
-          dev::umma_commit(pv_done(t));
-          if (last_user(t, i)) dev::umma_commit(v_empty(s));
-          // S_t(i+1) over S_t(i) and P_t(i), after the P.V that reads P_t(i): the MMAs of
-          // one thread run in issue order
-          if (i + 1 < nb_of(t)) ok = issue_s(t, i + 1);
+        for (int hf = 0; hf < 2; ++hf) {  // keys 0-63, then 64-127 of the block
+          if (!(ok = fail(dev::mbar_wait(p_half(t, hf), i & 1)))) break;
+          dev::tc_fence_after();
+          const uint32_t p = s_tm + 32u * hf;
+          const uint64_t vh = desc_add(dvs, hf * 4 * 2048u);
+          umma4_ts(o_tm, p, p + 8, p + 16, p + 24, vh, desc_add(vh, 2048), desc_add(vh, 4096),
+                   desc_add(vh, 6144), id_o, hf > 0 || i > 0 ? 1u : 0u);
         }
+        if (!ok) break;
+        // S_t(i+1) over S_t(i) and P_t(i), after the P.V that reads P_t(i): the MMAs of
+        // one thread run in issue order
+        if (i + 1 < nb) ok = issue_s(i + 1);
+        else dev::umma_commit(pv_done(t));
+        dev::umma_commit(v_empty(s));
+      }
+      // tile 0 of a prompt ends with fewer blocks: it lets go of tile 1's others unread
+      for (int j = nb; kShareKeys && ok && j < nblk && nb1 > 0; ++j) {
+        if (!(ok = fail(dev::mbar_wait(k_full(j % KSK), (j / KSK) & 1)))) break;
+        dev::mbar_arrive(k_empty(j % KSK));
+        if (!(ok = fail(dev::mbar_wait(v_full(j % KSV), (j / KSV) & 1)))) break;
+        dev::mbar_arrive(v_empty(j % KSV));
       }
       dev::umma_commit(mma_done);
     }
@@ -493,8 +506,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const float m = m_ref == -INFINITY ? 0.f : m_ref;
       const int nk = min(kTcKeys, t_end - k0);
       if (kMask && nk < kTcKeys) {  // V rows past the staged keys are stale or another sequence's
-        const int s = j % KS;
-        if (!__all_sync(0xffffffffu, dev::mbar_wait(v_full(s), (j / KS) & 1))) return false;
+        const int s = j % KSV;
+        if (!__all_sync(0xffffffffu, dev::mbar_wait(v_full(s), (j / KSV) & 1))) return false;
         const uint32_t vt = SL::v + s * SL::kTile;
         for (int idx = r; idx < (kTcKeys - nk) * (D / 8); idx += kTcRows) {
           const int row = nk + idx / (D / 8), c = idx % (D / 8);
@@ -532,8 +545,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     float lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
     if (!ok && lane == 0) fail(false);
-    if (ok && nb > 0 && !(ok = __all_sync(0xffffffffu, dev::mbar_wait(pv_done(t), (nb - 1) & 1))) &&
-        lane == 0)
+    if (ok && nb > 0 && !(ok = __all_sync(0xffffffffu, dev::mbar_wait(pv_done(t), 0))) && lane == 0)
       fail(false);
     if (ok && nb > 0) {
       dev::tc_fence_after();
@@ -595,10 +607,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (tid == 0) (void)dev::mbar_wait(mma_done, 0);
   __syncthreads();
   if (is_producer && lane == 0 && *s_flag) {
-    for (int s = 0; s < KS; ++s) {
-      const int last = s + ((issued - 1 - s) / KS) * KS;  // the last block on stage s
+    const int ks = warp == kProducer ? KSK : KSV;
+    for (int s = 0; s < ks; ++s) {
+      const int last = s + ((issued - 1 - s) / ks) * ks;  // the last block on stage s
       if (last >= 0 && last < issued)
-        (void)dev::mbar_wait(warp == kProducer ? k_full(s) : v_full(s), (last / KS) & 1);
+        (void)dev::mbar_wait(warp == kProducer ? k_full(s) : v_full(s), (last / ks) & 1);
     }
   }
   dev::tc_fence_before();

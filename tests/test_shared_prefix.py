@@ -144,6 +144,22 @@ def test_matches_reference(B, groups, prefixes, suffixes, hq, hkv, d, bs, lead, 
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d,bs", [(64, 16), (128, 16), (128, 32)])
+def test_many_blocks_per_split(B, d, bs):
+    """More groups than the prefix needs splits: every tile CTA walks dozens of key blocks of
+    scattered pages, and its two tiles run apart."""
+    rng = random.Random(d + bs)
+    c = make([2] * 24, [rng.randint(2500, 6500) for _ in range(24)], [3] * 48, 24, 8, d, bs, 13,
+             poison=False)
+    o, amp = reference(c, d ** -0.5)
+    ws = workspace(B, c)
+    B.pkv_device_errors()
+    for _ in range(4):
+        check(call(B, c, d ** -0.5, ws), o, amp)
+    assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d,scale", [(64, 1.0), (128, 1.0), (128, -0.5), (64, 0.0)])
 def test_wide_scores(B, d, scale):
     """Scores of tens, whose maxima jump from block to block and from prefix to tail."""
