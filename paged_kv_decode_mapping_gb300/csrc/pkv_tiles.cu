@@ -75,9 +75,10 @@ struct TileSmem {
   static constexpr bool kOnes = D == 64;
   static constexpr uint32_t ones = q + kQ * kTile;
   static constexpr uint32_t bars = ones + (kOnes ? kSub : 0);
-  // the rings, then s_full and pv_done per tile, p_half per tile and half, q_ready, mma_done
+  // the rings, then s_full and pv_done per tile, p_half per tile and half, turn per tile,
+  // q_ready, mma_done
   static constexpr int kRings = 2 * KSK + 2 * KSV;  // barriers of the rings
-  static constexpr int kBars = kRings + 10;
+  static constexpr int kBars = kRings + 12;
   static constexpr uint32_t tslot = bars + kBars * 8;
   static constexpr uint32_t flag = tslot + 8;
   static constexpr uint32_t total = flag + 8;
@@ -258,8 +259,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto s_full = [&](int t) { return bars + 8u * (kRings + t); };
   auto pv_done = [&](int t) { return bars + 8u * (kRings + 2 + t); };
   auto p_half = [&](int t, int hf) { return bars + 8u * (kRings + 4 + 2 * t + hf); };
-  const uint32_t q_ready = bars + 8u * (kRings + 8);
-  const uint32_t mma_done = bars + 8u * (kRings + 9);
+  auto turn = [&](int t) { return bars + 8u * (kRings + 8 + t); };
+  const uint32_t q_ready = bars + 8u * (kRings + 10);
+  const uint32_t mma_done = bars + 8u * (kRings + 11);
   volatile uint32_t *const s_tmem = reinterpret_cast<volatile uint32_t *>(bp + SL::tslot);
   volatile int *const s_flag = reinterpret_cast<volatile int *>(bp + SL::flag);
 
@@ -371,7 +373,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else if (warp >= kMma) {
     // ------------------------------------- tensor-core issue, one thread for each tile:
-    // what one of them does between its MMAs (waits, commits) runs under the other's
+    // what one of them does between its MMAs (waits, commits) runs under the other's.  They
+    // take turns, P.V and the next S of one tile at a time: left to interleave, both tiles'
+    // scores came at the same moment and both softmaxes ran against each other while the
+    // tensor core idled (4011 against TURNCYC cycles per block pair at head_dim 128).
     const int t = warp - kMma;
     const int nb = t ? nb1 : nb0;
     if (lane == 0) {
@@ -391,6 +396,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (!fail(dev::mbar_wait(k_full(s), (j / KSK) & 1))) return false;
         dev::tc_fence_after();
         issue_qk<D>(s_tm, dq, desc_add(dk0, s * SL::kTile), SL::kSub, id_s);
+        if (i > 0) dev::mbar_arrive(turn(t ^ 1));
         dev::umma_commit(s_full(t));
         dev::umma_commit(k_empty(s));
         return true;
@@ -404,6 +410,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {  // keys 0-63, then 64-127 of the block
           if (!(ok = fail(dev::mbar_wait(p_half(t, hf), i & 1)))) break;
+          // after the other tile's turn: tile 1's i-1st, or tile 0's i-th, if it has one
+          if (hf == 0 && (t ? i < nb0 : i > 0 && i <= nb1) &&
+              !(ok = fail(dev::mbar_wait(turn(t), (t ? i : i - 1) & 1))))
+            break;
           dev::tc_fence_after();
           const uint32_t p = s_tm + 32u * hf;
           const uint64_t vh = desc_add(dvs, hf * 4 * 2048u);
@@ -414,7 +424,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // S_t(i+1) over S_t(i) and P_t(i), after the P.V that reads P_t(i): the MMAs of
         // one thread run in issue order
         if (i + 1 < nb) ok = issue_s(i + 1);
-        else dev::umma_commit(pv_done(t));
+        else {
+          dev::mbar_arrive(turn(t ^ 1));
+          dev::umma_commit(pv_done(t));
+        }
         dev::umma_commit(v_empty(s));
       }
       // tile 0 of a prompt ends with fewer blocks: it lets go of tile 1's others unread
