@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // what one of them does between its MMAs (waits, commits) runs under the other's.  They
     // take turns, P.V and the next S of one tile at a time: left to interleave, both tiles'
     // scores came at the same moment and both softmaxes ran against each other while the
-    // tensor core idled (4011 against TURNCYC cycles per block pair at head_dim 128).
+    // tensor core idled (4011 against 3080 cycles per block pair at head_dim 128).
     const int t = warp - kMma;
     const int nb = t ? nb1 : nb0;
     if (lane == 0) {
@@ -391,40 +391,47 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         return dev::smem_desc(base + vs, kOnes ? SL::ones - vs : SL::kSub, 1024);
       };
       const uint32_t s_tm = tmem + 128u * t, o_tm = tmem + 256u + (uint32_t)(kON * t);
+      auto wait_k = [&](int i) {
+        const int j = blk(t, i);
+        return fail(dev::mbar_wait(k_full(j % KSK), (j / KSK) & 1));
+      };
       auto issue_s = [&](int i) {
-        const int j = blk(t, i), s = j % KSK;
-        if (!fail(dev::mbar_wait(k_full(s), (j / KSK) & 1))) return false;
-        dev::tc_fence_after();
+        const int s = blk(t, i) % KSK;
         issue_qk<D>(s_tm, dq, desc_add(dk0, s * SL::kTile), SL::kSub, id_s);
         if (i > 0) dev::mbar_arrive(turn(t ^ 1));
         dev::umma_commit(s_full(t));
         dev::umma_commit(k_empty(s));
-        return true;
       };
       bool ok = fail(dev::mbar_wait(q_ready, 0));
-      if (ok && nb > 0) ok = issue_s(0);
+      if (ok && nb > 0 && (ok = wait_k(0))) {
+        dev::tc_fence_after();
+        issue_s(0);
+      }
       for (int i = 0; ok && i < nb; ++i) {
         const int j = blk(t, i), s = j % KSV;
+        // every wait but one ahead of the turn, so that the turn is MMAs back to back
         if (!(ok = fail(dev::mbar_wait(v_full(s), (j / KSV) & 1)))) break;
-        const uint64_t dvs = dv(s);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {  // keys 0-63, then 64-127 of the block
-          if (!(ok = fail(dev::mbar_wait(p_half(t, hf), i & 1)))) break;
-          // after the other tile's turn: tile 1's i-1st, or tile 0's i-th, if it has one
-          if (hf == 0 && (t ? i < nb0 : i > 0 && i <= nb1) &&
-              !(ok = fail(dev::mbar_wait(turn(t), (t ? i : i - 1) & 1))))
-            break;
-          dev::tc_fence_after();
-          const uint32_t p = s_tm + 32u * hf;
-          const uint64_t vh = desc_add(dvs, hf * 4 * 2048u);
-          umma4_ts(o_tm, p, p + 8, p + 16, p + 24, vh, desc_add(vh, 2048), desc_add(vh, 4096),
-                   desc_add(vh, 6144), id_o, hf > 0 || i > 0 ? 1u : 0u);
-        }
-        if (!ok) break;
+        if (i + 1 < nb && !(ok = wait_k(i + 1))) break;
+        if (!(ok = fail(dev::mbar_wait(p_half(t, 0), i & 1)))) break;
+        // the other tile's turn: tile 1's i-1st, or tile 0's i-th, if it has one
+        if ((t ? i < nb0 : i > 0 && i <= nb1) &&
+            !(ok = fail(dev::mbar_wait(turn(t), (t ? i : i - 1) & 1))))
+          break;
+        dev::tc_fence_after();
+        const uint64_t vd = dv(s), vh = desc_add(vd, 4 * 2048u);
+        // keys 0-63, then 64-127 of the block (waiting for both halves of P ahead of the
+        // turn measured 9% slower)
+        umma4_ts(o_tm, s_tm, s_tm + 8, s_tm + 16, s_tm + 24, vd, desc_add(vd, 2048),
+                 desc_add(vd, 4096), desc_add(vd, 6144), id_o, i > 0 ? 1u : 0u);
+        if (!(ok = fail(dev::mbar_wait(p_half(t, 1), i & 1)))) break;
+        dev::tc_fence_after();
+        umma4_ts(o_tm, s_tm + 32, s_tm + 40, s_tm + 48, s_tm + 56, vh, desc_add(vh, 2048),
+                 desc_add(vh, 4096), desc_add(vh, 6144), id_o, 1u);
         // S_t(i+1) over S_t(i) and P_t(i), after the P.V that reads P_t(i): the MMAs of
         // one thread run in issue order
-        if (i + 1 < nb) ok = issue_s(i + 1);
-        else {
+        if (i + 1 < nb) {
+          issue_s(i + 1);
+        } else {
           dev::mbar_arrive(turn(t ^ 1));
           dev::umma_commit(pv_done(t));
         }
