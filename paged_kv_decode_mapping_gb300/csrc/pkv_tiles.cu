@@ -21,8 +21,7 @@ namespace pkv {
 //   P_t = exp2(S_t * scale - m)  fp32, rounded to bf16 into TMEM over columns of S_t already read
 //   O_t += P_t . V_j    P_t from TMEM, V_j MN-major in shared memory, O_t in TMEM
 // The row's reference max m moves only when a block raises it by more than kTcRescale;
-// then O_t and the row sum are rescaled.  The row sum adds the bf16-rounded weights that
-// the tensor core multiplies, so the weights stay a convex combination whatever m is.
+// then O_t and the row sum are rescaled.
 // K and V stream through separate rings, each with its producer warp; each tile's MMAs are
 // issued by a thread of their own.
 //
@@ -216,8 +215,17 @@ __device__ __forceinline__ float row_max(uint32_t sb, int lim, uint32_t (&x0)[32
   return fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
 }
 
+__device__ __forceinline__ void add_f32x2(float &a0, float &a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+
 // P = exp2(S * scale - m) of the 32 columns x (columns c0 .. of the row) as bf16 pairs, and
-// their sum added to ls.
+// their sum added to ls: of the weights as they are before the rounding, two to an add (the
+// rounded ones, one to an add, measured 6% slower).  Rounding moves a weight by at most 2^-8
+// of itself, and so the output by at most 2^-8 of sum p |v|.
 template <bool kMask, bool kSum>
 __device__ __forceinline__ void chunk_exp(const uint32_t (&x)[32], int c0, int lim, float scale_log2,
                                           float m, uint32_t *pk, float (&ls)[4]) {
@@ -229,9 +237,9 @@ __device__ __forceinline__ void chunk_exp(const uint32_t (&x)[32], int c0, int l
       a0 = c0 + 2 * e <= lim ? a0 : -INFINITY;
       a1 = c0 + 2 * e + 1 <= lim ? a1 : -INFINITY;
     }
-    pk[e] = dev::pack_bf16x2(dev::ex2(a0), dev::ex2(a1));
-    // what the tensor core multiplies: the weights stay a convex combination whatever m is
-    if constexpr (kSum) ls[e & 3] = add_bf16x2(pk[e], ls[e & 3]);
+    const float p0 = dev::ex2(a0), p1 = dev::ex2(a1);
+    pk[e] = dev::pack_bf16x2(p0, p1);
+    if constexpr (kSum) add_f32x2(ls[2 * (e & 1)], ls[2 * (e & 1) + 1], p0, p1);
   }
 }
 
