@@ -400,7 +400,7 @@ int paged_prefill_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k_
  * nondecreasing, within num_tokens) of q, k, v and out; its query i sees its keys 0 .. i:
  *   out[row][h] = bf16( sum_{t <= i} softmax_t(scale * <q[row][h], k_t>) v_t )
  * in fp32 arithmetic on bf16 inputs (the weights enter the product with V as bf16).  Query
- * head h reads kv head h / (num_q_heads / num_kv_heads), any group.  One token's heads are
+ * head h reads kv head h / (num_q_heads / num_kv_heads), groups of 1 to 128.  One token's heads are
  * contiguous; the strides, in elements, lead from one token to the next, so that q, k and v
  * may be slices of one fused projection (multiples of 8; out 16-byte aligned like q, k, v).
  * max_query_len >= every length; a longer or misplaced sequence raises

@@ -91,6 +91,10 @@ int maps_for(const pkv_bf16 *k_cache, const pkv_bf16 *v_cache, const pkv_cache_d
 // swizzle, zeros past the last token; the caller holds attn_mutex().
 int packed_map(const pkv_bf16 *x, int64_t tokens, int32_t heads, int32_t d, int64_t stride,
                int32_t box_tokens, CUtensorMap *out);
+// The same for query rows [tokens][heads][d], loaded as 3-D boxes {64 dims, `group` heads,
+// `box_tokens` tokens}: the rows of a tile in (token, head) order, 64 dims at a time.
+int query_map(const pkv_bf16 *x, int64_t tokens, int32_t heads, int32_t d, int64_t stride,
+              int32_t group, int32_t box_tokens, CUtensorMap *out);
 // Argument checks shared by the decode and prefill entry points.
 int check_decode(const void *q, const void *k_cache, const void *v_cache, const int32_t *bt,
                  int32_t max_blocks, const int32_t *lens, int32_t max_len, int32_t num_seqs,

@@ -329,10 +329,10 @@ SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int
                        int32_t max_prefix, int32_t max_suffix, int sms) {
   SharedPlan p;
   const int32_t groups = std::min(num_groups, num_seqs);
-  const int64_t rows = (int64_t)num_seqs * (hq / hkv);
-  p.tiles = rows / kTileRows + groups;
+  const int64_t tile_seqs = kTileRows / (hq / hkv);  // sequences of a tile
+  p.tiles = num_seqs / tile_seqs + groups;
   // about one tile CTA per SM: the prefix is cut into as many splits as that takes
-  const int64_t units = std::max<int64_t>((rows + kTileRows - 1) / kTileRows, groups) * hkv;
+  const int64_t units = std::max<int64_t>((num_seqs + tile_seqs - 1) / tile_seqs, groups) * hkv;
   const int64_t want = std::max<int64_t>(1, sms / std::max<int64_t>(units, 1));
   int64_t s = ((int64_t)max_prefix + want - 1) / want;
   s = std::max<int64_t>(kTileKeys, (s + kTileKeys - 1) / kTileKeys * kTileKeys);

@@ -14,22 +14,26 @@
 namespace pkv {
 
 // ===========================================================================
-// tile_kernel: a CTA owns one kv head's query rows -- (query token, head of the group)
-// pairs -- as two tiles in ping-pong: while four softmax warps work on one tile's scores
-// (one thread per row), the tensor core works on the other tile.
+// tile_kernel: a CTA works on one kv head's query rows -- (query token, head of the group)
+// pairs -- as two tiles of up to 128 rows in ping-pong: while four softmax warps work on one
+// tile's scores (one thread per row), the tensor core works on the other tile.
 //   S_t = Q_t . K_j^T   tcgen05.mma M=128 N=128 K=D, both K-major in shared memory, S_t in TMEM
 //   P_t = exp2(S_t * scale - m)  fp32, rounded to bf16 into TMEM over columns of S_t already read
 //   O_t += P_t . V_j    P_t from TMEM, V_j MN-major in shared memory, O_t in TMEM
 // The row's reference max m moves only when a block raises it by more than kTcRescale;
 // then O_t and the row sum are rescaled.
-// K and V stream through separate rings, each with its producer warp; each tile's MMAs are
-// issued by a thread of their own.
+// K and V stream through separate rings, each with its producer warp (the K producer loads the
+// queries too); each tile's MMAs are issued by a thread of their own.
 //
 // Two ways of pairing:
-//  * kPrompt: the tiles are 128 query rows each of one packed sequence and share every
-//    K/V block (256 rows per block staged).  Causal: a row of query i sees keys 0 .. i.
+//  * kPrompt: the tiles are consecutive query rows of one packed sequence and share every
+//    K/V block (up to 256 rows per block staged).  Causal: a row of query i sees keys 0 .. i.
 //    K and V rows come straight from the packed projections: one TMA box per block.
-//  * kPrefix: both tiles hold the same 128 rows (queries of a group of sequences) and take
+//    A CTA goes on to other work items, those of CTAs that have not started yet (cluster
+//    launch control): its rings, queries and scores of the next item fill while the rows of
+//    the last one are written, so that an item costs no launch, set-up and first-copy latency
+//    of its own (about 9 us, the time of six key blocks).
+//  * kPrefix: both tiles hold the same rows (queries of a group of sequences) and take
 //    alternate key blocks, so that a few rows over a long prefix still overlap softmax and
 //    tensor core.  The keys come from the pages of the group's first sequence; the CTA
 //    covers one split of them, and each tile writes its softmax-normalised fp32 output and
@@ -37,12 +41,12 @@ namespace pkv {
 enum { kPrompt = 0, kPrefix = 1 };
 
 struct TileArgs {
-  const uint16_t *q;
   uint16_t *out;            // prompt
-  int64_t q_stride, out_stride;  // elements from one query token to the next
+  int64_t out_stride;       // elements from one query token to the next
   const int32_t *start;     // [num + 1] first query row of each sequence / group
   int32_t num, total, max_len;   // sequences or groups, query tokens, longest sequence
   int32_t num_q_heads, num_kv_heads, group;
+  int32_t tile_tokens;      // query tokens of a tile: 128 / group
   float scale_log2;
   // prefix
   const int32_t *block_tables, *context_lens, *prefix_lens;
@@ -54,6 +58,17 @@ struct TileArgs {
 };
 
 constexpr int kTileThreads = 32 * 12;  // 8 softmax warps, the K and V producers, an MMA warp per tile
+constexpr int kItemReaders = 11;       // warps that read an item: all but the K producer
+
+// One piece of work, handed from the K producer to the other warps.
+struct TileItem {
+  int32_t live;             // 0: no more items
+  int32_t g, first;         // kv head, the sequence's (group's) first query token
+  int32_t tok0, n;          // the tiles' first token and the token count, within the sequence
+  int32_t key0, t_end;      // keys [key0, t_end) are staged, in blocks of kTcKeys
+  int32_t nb0, nb1;         // blocks of each tile
+  int32_t pad[3];
+};
 
 template <int D, int MODE>
 struct TileSmem {
@@ -73,25 +88,51 @@ struct TileSmem {
   // the tensor core forms the row sums (O's columns are free in TMEM at 64, not at 128)
   static constexpr bool kOnes = D == 64;
   static constexpr uint32_t ones = q + kQ * kTile;
-  static constexpr uint32_t bars = ones + (kOnes ? kSub : 0);
-  // the rings, then s_full and pv_done per tile, p_half per tile and half, turn per tile,
-  // q_ready, mma_done
-  static constexpr int kRings = 2 * KSK + 2 * KSV;  // barriers of the rings
-  static constexpr int kBars = kRings + 12;
+  static constexpr uint32_t item = ones + (kOnes ? kSub : 0);  // two items
+  static constexpr uint32_t clc = item + 2 * sizeof(TileItem); // a launch-control answer, 16 B
+  static constexpr uint32_t bars = clc + 16;
+  // the rings, then s_full, pv_done per tile, p_half per tile and half, q_full, q_free, o_free
+  // per tile, item_full, item_empty per slot, clc_full, mma_done
+  static constexpr int kRings = 2 * KSK + 2 * KSV;
+  static constexpr int kBars = kRings + 20;
   static constexpr uint32_t tslot = bars + kBars * 8;
   static constexpr uint32_t flag = tslot + 8;
-  static constexpr uint32_t total = flag + 8;
+  static constexpr uint32_t turns = flag + 8;  // P.V batches issued, per tile
+  static constexpr uint32_t total = turns + 8;
 };
 template <int D, int MODE>
 constexpr size_t tile_smem() { return 1024 + TileSmem<D, MODE>::total; }
 static_assert(tile_smem<64, kPrompt>() <= 227 * 1024 && tile_smem<128, kPrompt>() <= 227 * 1024 &&
                   tile_smem<64, kPrefix>() <= 227 * 1024 && tile_smem<128, kPrefix>() <= 227 * 1024,
               "the tiles fit a CTA");
+static_assert(sizeof(TileItem) == 48, "items keep the answer 16-byte aligned");
 
-// The sequence (or group) whose tiles of `tile_rows` rows hold tile number idx, its first
-// query token, its length and the tile's place in it.  Whole warps; lengths that are
-// negative, past `total` or over max_len are clamped and flagged.
-__device__ __forceinline__ bool locate_tile(const TileArgs &a, int64_t idx, int tile_rows, int lane,
+// Cluster launch control: asks for a CTA of this grid that has not started; the answer (16
+// bytes) completes on `bar`.  Then: whether there was one, and its blockIdx.x.
+__device__ __forceinline__ void clc_try_cancel(uint32_t dst, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+      "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ bool clc_answer(uint32_t src, uint32_t &ctaid) {
+  uint32_t got;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(got), "=r"(ctaid)
+      : "r"(src)
+      : "memory");
+  return got != 0;
+}
+
+// The sequence (or group) whose pieces of `tokens` query tokens hold piece number idx, its
+// first query token, its length, the piece's place in it and its pieces.  Whole warps;
+// lengths that are negative, past `total` or over max_len are clamped and flagged.
+__device__ __forceinline__ bool locate_tile(const TileArgs &a, int64_t idx, int tokens, int lane,
                                             int &b, int &first, int &n, int &tile, int &ntiles) {
   int64_t before = 0;
   for (int c = 0; c < a.num; c += 32) {
@@ -104,11 +145,11 @@ __device__ __forceinline__ bool locate_tile(const TileArgs &a, int64_t idx, int 
       len = min(len, a.max_len);
       if (s != s0 || s + len != e0) raise_error(PKV_DEVERR_CONTEXT_LEN);
     }
-    const int64_t mine = ((int64_t)len * a.group + tile_rows - 1) / tile_rows;
-    int64_t upto = mine;
+    const int mine = (len + tokens - 1) / tokens;
+    int upto = mine;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, upto, x);
+      const int y = __shfl_up_sync(0xffffffffu, upto, x);
       if (lane >= x) upto += y;
     }
     const unsigned past = __ballot_sync(0xffffffffu, before + upto > idx);
@@ -117,13 +158,49 @@ __device__ __forceinline__ bool locate_tile(const TileArgs &a, int64_t idx, int 
       b = c + l;
       first = __shfl_sync(0xffffffffu, s, l);
       n = __shfl_sync(0xffffffffu, len, l);
-      ntiles = (int)__shfl_sync(0xffffffffu, mine, l);
+      ntiles = __shfl_sync(0xffffffffu, mine, l);
       tile = (int)(idx - before - __shfl_sync(0xffffffffu, upto - mine, l));
       return true;
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
   }
   return false;
+}
+
+// The work of CTA (cta_x, cta_y), the same on every lane of the warp; false if it has none.
+template <int MODE>
+__device__ __forceinline__ bool make_item(const TileArgs &a, unsigned cta_x, unsigned cta_y, int lane,
+                                          TileItem &it) {
+  it.live = 1;
+  it.g = (int)(cta_x % (unsigned)a.num_kv_heads);
+  const int tokens = a.tile_tokens * (MODE == kPrompt ? 2 : 1);
+  int b, tile, ntiles;
+  if (!locate_tile(a, cta_x / (unsigned)a.num_kv_heads, tokens, lane, b, it.first, it.n, tile, ntiles))
+    return false;
+  if constexpr (MODE == kPrompt) {
+    it.tok0 = (ntiles - 1 - tile) * tokens;  // a sequence's last tiles see the most keys: first
+    const int e0 = min(it.tok0 + a.tile_tokens, it.n), e1 = min(it.tok0 + tokens, it.n);
+    it.key0 = 0;
+    it.t_end = e1;
+    it.nb0 = (e0 + kTcKeys - 1) / kTcKeys;
+    it.nb1 = e1 > e0 ? (e1 + kTcKeys - 1) / kTcKeys : 0;
+  } else {
+    it.tok0 = tile * tokens;
+    int prefix = __ldg(a.prefix_lens + b);
+    const int cap = (int)min((int64_t)a.max_blocks * a.block_size, (int64_t)a.max_prefix);
+    if (prefix < 0 || prefix > cap) {
+      if (lane == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
+      prefix = prefix < 0 ? 0 : cap;
+    }
+    prefix = prefix >> a.log2_bs << a.log2_bs;  // whole pages
+    it.key0 = (int)cta_y * a.split_keys;
+    if (it.key0 >= prefix) return false;
+    it.t_end = min(it.key0 + a.split_keys, prefix);
+    const int nblk = (it.t_end - it.key0 + kTcKeys - 1) / kTcKeys;
+    it.nb0 = (nblk + 1) / 2;
+    it.nb1 = nblk / 2;
+  }
+  return true;
 }
 
 // Loads keys [k0, k0 + nk) of kv head g from the group's pages into a block tile
@@ -245,15 +322,14 @@ __device__ __forceinline__ void chunk_exp(const uint32_t (&x)[32], int c0, int l
 
 template <int D, int MODE>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    tile_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                const TileArgs a) {
+    tile_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                const __grid_constant__ CUtensorMap tmv, const __grid_constant__ TileArgs a) {
   using SL = TileSmem<D, MODE>;
   constexpr int KSK = SL::KSK, KSV = SL::KSV, kRings = SL::kRings;
-  constexpr bool kPaged = MODE == kPrefix;     // keys from pages; partial outputs
+  constexpr bool kPaged = MODE == kPrefix;     // keys from pages; partial outputs; one item
   constexpr bool kShareKeys = MODE == kPrompt; // both tiles take every block
   constexpr bool kOnes = SL::kOnes;
   constexpr int kON = D + (kOnes ? 16 : 0);    // O columns per tile (then the row sums)
-  constexpr int kTileRowsCta = kShareKeys ? 2 * kTcRows : kTcRows;
   constexpr int kProducer = 8, kProducerV = 9, kMma = 10;  // kMma + t: tile t's MMA warp
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = dev::smem_addr(smem_raw);
@@ -267,79 +343,57 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto s_full = [&](int t) { return bars + 8u * (kRings + t); };
   auto pv_done = [&](int t) { return bars + 8u * (kRings + 2 + t); };
   auto p_half = [&](int t, int hf) { return bars + 8u * (kRings + 4 + 2 * t + hf); };
-  auto turn = [&](int t) { return bars + 8u * (kRings + 8 + t); };
-  const uint32_t q_ready = bars + 8u * (kRings + 10);
-  const uint32_t mma_done = bars + 8u * (kRings + 11);
+  auto q_full = [&](int t) { return bars + 8u * (kRings + 8 + t); };
+  auto q_free = [&](int t) { return bars + 8u * (kRings + 10 + t); };
+  auto o_free = [&](int t) { return bars + 8u * (kRings + 12 + t); };
+  auto item_full = [&](int s) { return bars + 8u * (kRings + 14 + s); };
+  auto item_empty = [&](int s) { return bars + 8u * (kRings + 16 + s); };
+  const uint32_t clc_full = bars + 8u * (kRings + 18);
+  const uint32_t mma_done = bars + 8u * (kRings + 19);
+  volatile int *const s_turn = reinterpret_cast<volatile int *>(bp + SL::turns);
   volatile uint32_t *const s_tmem = reinterpret_cast<volatile uint32_t *>(bp + SL::tslot);
   volatile int *const s_flag = reinterpret_cast<volatile int *>(bp + SL::flag);
+  TileItem *const s_item = reinterpret_cast<TileItem *>(bp + SL::item);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = a.group;
+  const int G = a.group, tile_rows = a.tile_tokens * G;
   // the decode kernel that merges may start its own part while this one runs
   if constexpr (kPaged) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int g = blockIdx.x % (unsigned)a.num_kv_heads;
-  int b, first, n, tile, ntiles;
-  if (!locate_tile(a, blockIdx.x / (unsigned)a.num_kv_heads, kTileRowsCta, lane, b, first, n, tile,
-                   ntiles))
-    return;
-  // causal prompts: a sequence's last tiles see the most keys and go first
-  if constexpr (kShareKeys) tile = ntiles - 1 - tile;
-  const int64_t rows = (int64_t)n * G;
-  const int64_t row0 = (int64_t)tile * kTileRowsCta;
-
-  // key0: the CTA's first key; t_end: keys [key0, t_end) are staged, in blocks of kTcKeys;
-  // nb0, nb1: blocks of each tile (block blk(t, i) is its i-th)
-  int key0 = 0, t_end, nblk, nb0, nb1, prefix = 0;
-  if constexpr (kPaged) {
-    prefix = __ldg(a.prefix_lens + b);
-    const int cap = (int)min((int64_t)a.max_blocks * a.block_size, (int64_t)a.max_prefix);
-    if (prefix < 0 || prefix > cap) {
-      if (tid == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
-      prefix = prefix < 0 ? 0 : cap;
-    }
-    prefix = prefix >> a.log2_bs << a.log2_bs;  // whole pages
-    key0 = blockIdx.y * a.split_keys;
-    if (key0 >= prefix) return;
-    t_end = min(key0 + a.split_keys, prefix);
-    nblk = (t_end - key0 + kTcKeys - 1) / kTcKeys;
-    nb0 = (nblk + 1) / 2;
-    nb1 = nblk / 2;
-  } else {
-    const int64_t last0 = min(row0 + kTcRows, rows) - 1, last1 = min(row0 + 2 * kTcRows, rows) - 1;
-    nb0 = ((int)(last0 / G) + kTcKeys) / kTcKeys;
-    nb1 = last1 > last0 ? ((int)(last1 / G) + kTcKeys) / kTcKeys : 0;
-    t_end = (int)(last1 / G) + 1;
-    nblk = max(nb0, nb1);
-  }
-  auto nb_of = [&](int t) { return t ? nb1 : nb0; };
   auto blk = [&](int t, int i) { return kShareKeys ? i : 2 * i + t; };
 
-  const bool is_producer = warp == kProducer || warp == kProducerV;
-  const int32_t *const trow = kPaged ? a.block_tables + (int64_t)first * a.max_blocks : nullptr;
-  const int lb_last = kPaged ? (t_end - 1) >> a.log2_bs : 0;
-  const int win_first = kPaged ? key0 >> a.log2_bs : 0;
-  int tb = (kPaged && is_producer && win_first + lane <= lb_last) ? __ldg(trow + win_first + lane) : 0;
-
+  // The K producer finds the first item while the others set up.
+  TileItem it = {};
+  bool have = false;
+  if (kPaged || warp == kProducer) have = make_item<MODE>(a, blockIdx.x, blockIdx.y, lane, it);
+  if (kPaged && !have) return;
   if (tid == 0) {
     for (int i = 0; i < SL::kBars; ++i) {
-      const uint32_t bar = bars + 8u * i;
-      const uint32_t count = i >= kRings + 4 && i < kRings + 8 ? 4u  // p_half: one per warp
-                             : bar == q_ready ? (kShareKeys ? 8u : 4u)
-                             : bar == mma_done ? 2u
-                             : (i >= KSK && i < 2 * KSK) || (i >= 2 * KSK + KSV && i < kRings)
-                                 ? (kShareKeys && nb1 > 0 ? 2u : 1u)  // empty: its users
-                                 : 1u;
-      dev::mbar_init(bar, count);
+      const int r = i - kRings;
+      const uint32_t count = (i >= KSK && i < 2 * KSK) || (i >= 2 * KSK + KSV && i < kRings)
+                                 ? (kShareKeys ? 2u : 1u)     // empty: both MMA threads, or one
+                             : r >= 4 && r < 8 ? 4u           // p_half: one per softmax warp
+                             : r == 12 || r == 13 ? 4u        // o_free: alike
+                             : r == 16 || r == 17 ? (uint32_t)kItemReaders
+                             : r == 19 ? 2u                   // mma_done: both MMA threads
+                                       : 1u;
+      dev::mbar_init(bars + 8u * i, count);
     }
     *s_flag = 0;
+    s_turn[0] = s_turn[1] = 0;
     dev::fence_mbar_init();
   }
   if constexpr (kOnes) {  // bf16 1.0 everywhere; read by the tensor core (async proxy)
     for (int i = tid; i < (int)(SL::kSub / 16); i += kTileThreads)
       *reinterpret_cast<uint4 *>(bp + SL::ones + i * 16) =
           make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-    dev::fence_proxy_async_smem();
   }
+  // rows of the Q tiles past the last whole token are never loaded: zeros
+  for (int i = tid; i < SL::kQ * (D / 64) * (kTcRows - tile_rows) * 8; i += kTileThreads) {
+    const int sub = i / ((kTcRows - tile_rows) * 8), o = i - sub * (kTcRows - tile_rows) * 8;
+    *reinterpret_cast<uint4 *>(bp + SL::q + sub * SL::kSub + tile_rows * 128 + o * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+  dev::fence_proxy_async_smem();
   if (warp == 0) dev::tmem_alloc(base + SL::tslot, 512);
   dev::tc_fence_before();
   __syncthreads();
@@ -353,31 +407,126 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     return ok;
   };
+  // Copies `it` number `items` (of the reading warp's count) out of its slot.
+  auto next_item = [&](int items, TileItem &x) {
+    const int s = items & 1;
+    if (!__all_sync(0xffffffffu, dev::mbar_wait(item_full(s), (items >> 1) & 1))) {
+      if (lane == 0) fail(false);
+      return false;
+    }
+    x = s_item[s];
+    __syncwarp();
+    if (lane == 0) dev::mbar_arrive(item_empty(s));
+    return x.live != 0;
+  };
   int issued = 0;  // producers: blocks loaded
 
-  if (is_producer) {
-    // ------------------------------------------------- producer warps: K ring, V ring
-    const bool is_k = warp == kProducer;
-    const CUtensorMap *const tm = is_k ? &tmk : &tmv;
-    const uint32_t ring = base + (is_k ? SL::k : SL::v);
-    // a prompt's tiles, and the row tiles of a group, read the same keys: keep them in L2
-    const uint64_t policy = dev::policy_evict_last();
-    int win = win_first;
-    for (int j = 0; j < nblk; ++j) {
-      const int ks = is_k ? KSK : KSV, s = j % ks;
-      const uint32_t empty = is_k ? k_empty(s) : v_empty(s), full = is_k ? k_full(s) : v_full(s);
-      if (j >= ks && !__all_sync(0xffffffffu, dev::mbar_wait(empty, ((j / ks) - 1) & 1))) {
+  if (warp == kProducer) {
+    // ------------------------------------------------- items, Q tiles and the K ring
+    const uint64_t policy = dev::policy_evict_last();  // other CTAs read the same keys
+    int items = 0, asked = 0, qn[2] = {0, 0};
+    bool ok = true;
+    auto publish = [&](const TileItem &x) {
+      const int s = items & 1;
+      if (items >= 2 &&
+          !__all_sync(0xffffffffu, dev::mbar_wait(item_empty(s), ((items >> 1) - 1) & 1))) {
+        if (lane == 0) fail(false);
+        return false;
+      }
+      if (lane == 0) {
+        s_item[s] = x;
+        dev::mbar_arrive(item_full(s));
+      }
+      ++items;
+      return true;
+    };
+    while (true) {
+      if (kShareKeys && lane == 0) {  // the next item, while this one's copies are issued
+        dev::fence_proxy_async_smem();
+        dev::mbar_arrive_expect_tx(clc_full, 16);
+        clc_try_cancel(base + SL::clc, clc_full);
+      }
+      if (have && (ok = publish(it))) {
+#pragma unroll
+        for (int t = 0; t < SL::kQ; ++t) {
+          if ((t ? it.nb1 : it.nb0) == 0) continue;
+          if (qn[t] > 0 && !(ok = __all_sync(0xffffffffu, dev::mbar_wait(q_free(t), (qn[t] - 1) & 1)))) {
+            if (lane == 0) fail(false);
+            break;
+          }
+          ++qn[t];
+          if (lane == 0) {
+            dev::mbar_arrive_expect_tx(q_full(t), (uint32_t)tile_rows * 128u * (D / 64));
+#pragma unroll
+            for (int hh = 0; hh < D / 64; ++hh)
+              asm volatile(
+                  "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                  " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(base + SL::q + t * SL::kTile + hh * SL::kSub),
+                  "l"(reinterpret_cast<uint64_t>(&tmq)), "r"(hh * 64), "r"(it.g * G),
+                  "r"(it.first + it.tok0 + t * a.tile_tokens), "r"(q_full(t))
+                  : "memory");
+          }
+        }
+        const int nblk = (it.t_end - it.key0 + kTcKeys - 1) / kTcKeys;
+        const int32_t *const trow = kPaged ? a.block_tables + (int64_t)it.first * a.max_blocks : nullptr;
+        const int lb_last = kPaged ? (it.t_end - 1) >> a.log2_bs : 0;
+        int win = kPaged ? it.key0 >> a.log2_bs : 0;
+        int tb = kPaged && win + lane <= lb_last ? __ldg(trow + win + lane) : 0;
+        for (int j = 0; ok && j < nblk; ++j, ++issued) {
+          const int s = issued % KSK;
+          if (issued >= KSK &&
+              !(ok = __all_sync(0xffffffffu, dev::mbar_wait(k_empty(s), ((issued / KSK) - 1) & 1)))) {
+            if (lane == 0) fail(false);
+            break;
+          }
+          const uint32_t dst = base + SL::k + s * SL::kTile;
+          if constexpr (kPaged)
+            load_paged_block<D, SL::kSub>(&tmk, dst, k_full(s), it.key0 + j * kTcKeys,
+                                          min(kTcKeys, it.t_end - it.key0 - j * kTcKeys), win, tb,
+                                          trow, lb_last, a, it.g, lane, policy);
+          else if (lane == 0)
+            load_packed_block(&tmk, dst, k_full(s), SL::kTile, it.first + j * kTcKeys, it.g, policy);
+        }
+      }
+      if constexpr (!kShareKeys) break;
+      // always answered before the CTA may leave
+      if (!__all_sync(0xffffffffu, dev::mbar_wait(clc_full, asked & 1))) {
         if (lane == 0) fail(false);
         break;
       }
-      const uint32_t dst = ring + s * SL::kTile;
-      if constexpr (kPaged)
-        load_paged_block<D, SL::kSub>(tm, dst, full, key0 + j * kTcKeys,
-                                      min(kTcKeys, t_end - key0 - j * kTcKeys), win, tb, trow,
-                                      lb_last, a, g, lane, policy);
-      else if (lane == 0)
-        load_packed_block(tm, dst, full, SL::kTile, first + j * kTcKeys, g, policy);
-      issued = j + 1;
+      ++asked;
+      uint32_t cta = 0;
+      if (!clc_answer(base + SL::clc, cta) || !ok) break;
+      have = make_item<MODE>(a, cta, 0, lane, it);
+      __syncwarp();  // every lane has read the answer: it may be overwritten
+    }
+    it.live = 0;
+    (void)publish(it);
+  } else if (warp == kProducerV) {
+    // ------------------------------------------------- the V ring
+    const uint64_t policy = dev::policy_evict_last();
+    bool ok = true;
+    for (int items = 0; ok && next_item(items, it); ++items) {
+      const int nblk = (it.t_end - it.key0 + kTcKeys - 1) / kTcKeys;
+      const int32_t *const trow = kPaged ? a.block_tables + (int64_t)it.first * a.max_blocks : nullptr;
+      const int lb_last = kPaged ? (it.t_end - 1) >> a.log2_bs : 0;
+      int win = kPaged ? it.key0 >> a.log2_bs : 0;
+      int tb = kPaged && win + lane <= lb_last ? __ldg(trow + win + lane) : 0;
+      for (int j = 0; j < nblk; ++j, ++issued) {
+        const int s = issued % KSV;
+        if (issued >= KSV &&
+            !(ok = __all_sync(0xffffffffu, dev::mbar_wait(v_empty(s), ((issued / KSV) - 1) & 1)))) {
+          if (lane == 0) fail(false);
+          break;
+        }
+        const uint32_t dst = base + SL::v + s * SL::kTile;
+        if constexpr (kPaged)
+          load_paged_block<D, SL::kSub>(&tmv, dst, v_full(s), it.key0 + j * kTcKeys,
+                                        min(kTcKeys, it.t_end - it.key0 - j * kTcKeys), win, tb, trow,
+                                        lb_last, a, it.g, lane, policy);
+        else if (lane == 0)
+          load_packed_block(&tmv, dst, v_full(s), SL::kTile, it.first + j * kTcKeys, it.g, policy);
+      }
     }
   } else if (warp >= kMma) {
     // ------------------------------------- tensor-core issue, one thread for each tile:
@@ -386,255 +535,274 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // scores came at the same moment and both softmaxes ran against each other while the
     // tensor core idled (4011 against 3080 cycles per block pair at head_dim 128).
     const int t = warp - kMma;
-    const int nb = t ? nb1 : nb0;
-    if (lane == 0) {
-      constexpr uint32_t id_s = dev::idesc_bf16_f32(kTcRows, kTcKeys, 0);
-      constexpr uint32_t id_o = dev::idesc_bf16_f32(kTcRows, kON, 1);
-      const uint64_t dq = dev::smem_desc(base + SL::q + (kShareKeys ? t * SL::kTile : 0u), 16, 1024);
-      const uint64_t dk0 = dev::smem_desc(base + SL::k, 16, 1024);
-      // V stage s as the MN-major B operand: the next 64 columns are V's other half
-      // (head_dim 128) or the tile of ones, `lbo` bytes further on
-      auto dv = [&](int s) {
-        const uint32_t vs = SL::v + s * SL::kTile;
-        return dev::smem_desc(base + vs, kOnes ? SL::ones - vs : SL::kSub, 1024);
-      };
-      const uint32_t s_tm = tmem + 128u * t, o_tm = tmem + 256u + (uint32_t)(kON * t);
-      auto wait_k = [&](int i) {
-        const int j = blk(t, i);
-        return fail(dev::mbar_wait(k_full(j % KSK), (j / KSK) & 1));
-      };
-      auto issue_s = [&](int i) {
-        const int s = blk(t, i) % KSK;
-        issue_qk<D>(s_tm, dq, desc_add(dk0, s * SL::kTile), SL::kSub, id_s);
-        if (i > 0) dev::mbar_arrive(turn(t ^ 1));
-        dev::umma_commit(s_full(t));
-        dev::umma_commit(k_empty(s));
-      };
-      bool ok = fail(dev::mbar_wait(q_ready, 0));
-      if (ok && nb > 0 && (ok = wait_k(0))) {
-        dev::tc_fence_after();
-        issue_s(0);
-      }
-      for (int i = 0; ok && i < nb; ++i) {
-        const int j = blk(t, i), s = j % KSV;
-        // every wait but one ahead of the turn, so that the turn is MMAs back to back
-        if (!(ok = fail(dev::mbar_wait(v_full(s), (j / KSV) & 1)))) break;
-        if (i + 1 < nb && !(ok = wait_k(i + 1))) break;
-        if (!(ok = fail(dev::mbar_wait(p_half(t, 0), i & 1)))) break;
-        // the other tile's turn: tile 1's i-1st, or tile 0's i-th, if it has one
-        if ((t ? i < nb0 : i > 0 && i <= nb1) &&
-            !(ok = fail(dev::mbar_wait(turn(t), (t ? i : i - 1) & 1))))
-          break;
-        dev::tc_fence_after();
-        const uint64_t vd = dv(s), vh = desc_add(vd, 4 * 2048u);
-        // keys 0-63, then 64-127 of the block (waiting for both halves of P ahead of the
-        // turn measured 9% slower)
-        umma4_ts(o_tm, s_tm, s_tm + 8, s_tm + 16, s_tm + 24, vd, desc_add(vd, 2048),
-                 desc_add(vd, 4096), desc_add(vd, 6144), id_o, i > 0 ? 1u : 0u);
-        if (!(ok = fail(dev::mbar_wait(p_half(t, 1), i & 1)))) break;
-        dev::tc_fence_after();
-        umma4_ts(o_tm, s_tm + 32, s_tm + 40, s_tm + 48, s_tm + 56, vh, desc_add(vh, 2048),
-                 desc_add(vh, 4096), desc_add(vh, 6144), id_o, 1u);
-        // S_t(i+1) over S_t(i) and P_t(i), after the P.V that reads P_t(i): the MMAs of
-        // one thread run in issue order
-        if (i + 1 < nb) {
-          issue_s(i + 1);
-        } else {
-          dev::mbar_arrive(turn(t ^ 1));
-          dev::umma_commit(pv_done(t));
+    // a negative scale negates the queries instead, so that the softmax sees none
+    const uint32_t id_s =
+        dev::idesc_bf16_f32(kTcRows, kTcKeys, 0) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
+    constexpr uint32_t id_o = dev::idesc_bf16_f32(kTcRows, kON, 1);
+    const uint64_t dq = dev::smem_desc(base + SL::q + (kShareKeys ? t * SL::kTile : 0u), 16, 1024);
+    const uint64_t dk0 = dev::smem_desc(base + SL::k, 16, 1024);
+    // V stage s as the MN-major B operand: the next 64 columns are V's other half
+    // (head_dim 128) or the tile of ones, `lbo` bytes further on
+    auto dv = [&](int s) {
+      const uint32_t vs = SL::v + s * SL::kTile;
+      return dev::smem_desc(base + vs, kOnes ? SL::ones - vs : SL::kSub, 1024);
+    };
+    const uint32_t s_tm = tmem + 128u * t, o_tm = tmem + 256u + (uint32_t)(kON * t);
+    // Running counts over the items: blocks staged before this one (`blocks`), this tile's
+    // score blocks (sc) and live items (on), both tiles' P.V batches (b0, b1).  Every ring
+    // phase is seen by both threads of a prompt, in order.
+    int blocks = 0, sc = 0, on = 0, b0 = 0, b1 = 0;
+    bool ok = true;
+    for (int items = 0; ok && next_item(items, it); ++items) {
+      const int nblk = (it.t_end - it.key0 + kTcKeys - 1) / kTcKeys;
+      const int nb = t ? it.nb1 : it.nb0, nb0 = it.nb0, nb1 = it.nb1;
+      if (lane == 0) {
+        auto wait_k = [&](int i) {
+          const int j = blocks + blk(t, i);
+          return fail(dev::mbar_wait(k_full(j % KSK), (j / KSK) & 1));
+        };
+        auto issue_s = [&](int i) {
+          const int s = (blocks + blk(t, i)) % KSK;
+          issue_qk<D>(s_tm, dq, desc_add(dk0, s * SL::kTile), SL::kSub, id_s);
+          if (i > 0) s_turn[t] = (t ? b1 : b0) + i;
+          dev::umma_commit(s_full(t));
+          dev::umma_commit(k_empty(s));
+          if (kShareKeys && i + 1 == nb) dev::umma_commit(q_free(t));
+        };
+        // Until the other tile has issued this many batches.  Only a matter of order, so it
+        // counts (no phase to mistake) and, past its limit, goes on.
+        auto await_turn = [&](int batches) {
+          if (s_turn[t ^ 1] >= batches) return;
+          const uint64_t t0 = dev::globaltimer_ns();
+          for (uint32_t n = 1; s_turn[t ^ 1] < batches; ++n)
+            if ((n & 255u) == 0 && dev::globaltimer_ns() - t0 > 2000000000ull) return;
+        };
+        if (nb > 0) {
+          ok = fail(dev::mbar_wait(q_full(kShareKeys ? t : 0), on & 1)) && wait_k(0);
+          if (ok) {
+            dev::tc_fence_after();
+            issue_s(0);
+          }
         }
-        dev::umma_commit(v_empty(s));
+        for (int i = 0; ok && i < nb; ++i) {
+          const int j = blocks + blk(t, i), s = j % KSV, ph = (sc + i) & 1;
+          // every wait but one ahead of the turn, so that the turn is MMAs back to back
+          if (!(ok = fail(dev::mbar_wait(v_full(s), (j / KSV) & 1)))) break;
+          if (i + 1 < nb && !(ok = wait_k(i + 1))) break;
+          // the last item's O has been read
+          if (i == 0 && on > 0 && !(ok = fail(dev::mbar_wait(o_free(t), (on - 1) & 1)))) break;
+          if (!(ok = fail(dev::mbar_wait(p_half(t, 0), ph)))) break;
+          // after the other tile's turn: tile 1's i-1st, or tile 0's i-th, if it has one
+          await_turn(t ? b0 + min(i + 1, nb0) : b1 + min(i, nb1));
+          dev::tc_fence_after();
+          const uint64_t vd = dv(s), vh = desc_add(vd, 4 * 2048u);
+          // keys 0-63, then 64-127 of the block (waiting for both halves of P ahead of the
+          // turn measured 9% slower)
+          umma4_ts(o_tm, s_tm, s_tm + 8, s_tm + 16, s_tm + 24, vd, desc_add(vd, 2048),
+                   desc_add(vd, 4096), desc_add(vd, 6144), id_o, i > 0 ? 1u : 0u);
+          if (!(ok = fail(dev::mbar_wait(p_half(t, 1), ph)))) break;
+          dev::tc_fence_after();
+          umma4_ts(o_tm, s_tm + 32, s_tm + 40, s_tm + 48, s_tm + 56, vh, desc_add(vh, 2048),
+                   desc_add(vh, 4096), desc_add(vh, 6144), id_o, 1u);
+          // S_t(i+1) over S_t(i) and P_t(i), after the P.V that reads P_t(i): the MMAs of
+          // one thread run in issue order
+          if (i + 1 < nb) {
+            issue_s(i + 1);
+          } else {
+            s_turn[t] = (t ? b1 : b0) + nb;
+            dev::umma_commit(pv_done(t));
+          }
+          dev::umma_commit(v_empty(s));
+        }
+        // blocks of the other tile alone: seen, and let go of unread
+        for (int i = nb; kShareKeys && ok && i < nblk; ++i) {
+          const int j = blocks + i;
+          if (!(ok = fail(dev::mbar_wait(k_full(j % KSK), (j / KSK) & 1)))) break;
+          dev::mbar_arrive(k_empty(j % KSK));
+          if (!(ok = fail(dev::mbar_wait(v_full(j % KSV), (j / KSV) & 1)))) break;
+          dev::mbar_arrive(v_empty(j % KSV));
+        }
       }
-      // tile 0 of a prompt ends with fewer blocks: it lets go of tile 1's others unread
-      for (int j = nb; kShareKeys && ok && j < nblk && nb1 > 0; ++j) {
-        if (!(ok = fail(dev::mbar_wait(k_full(j % KSK), (j / KSK) & 1)))) break;
-        dev::mbar_arrive(k_empty(j % KSK));
-        if (!(ok = fail(dev::mbar_wait(v_full(j % KSV), (j / KSV) & 1)))) break;
-        dev::mbar_arrive(v_empty(j % KSV));
-      }
-      dev::umma_commit(mma_done);
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      blocks += nblk;
+      sc += nb;
+      on += nb > 0 ? 1 : 0;
+      b0 += nb0;
+      b1 += nb1;
     }
+    if (lane == 0) dev::umma_commit(mma_done);
   } else {
     // --------------------------------------------- softmax warps of tile t: row r each
     const int t = warp >> 2, wq = warp & 3;
     const int r = 32 * wq + lane;
-    const int64_t gr = row0 + (kShareKeys ? t * kTcRows : 0) + r;
-    const bool valid = gr < rows;
-    const int64_t grc = valid ? gr : rows - 1;
-    const int qi = (int)(grc / G), h = (int)(grc - (int64_t)qi * G);
+    const int tok = r / G, h = r - tok * G;  // the row's query token in the tile, its head
     const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
     const uint32_t sb = tmem + lane_base + 128u * t;
     const uint32_t ob = tmem + lane_base + 256u + (uint32_t)(kON * t);
-    // keys < see are this row's
-    int see;
-    if constexpr (kPaged)
-      see = min(max(__ldg(a.context_lens + first + qi), 0), t_end);
-    else
-      see = qi + 1;
-    // a negative scale changes the queries' signs, so that the softmax sees none
     const float scale_log2 = fabsf(a.scale_log2);
-    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-    if (kShareKeys || t == 0) {  // the tile's query rows (zeros past the end)
-      const uint4 *src = reinterpret_cast<const uint4 *>(
-          a.q + (int64_t)(first + qi) * a.q_stride + (int64_t)(g * G + h) * D);
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        uint4 x = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-        x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
-        *reinterpret_cast<uint4 *>(bp + SL::q + (kShareKeys ? t * SL::kTile : 0u) +
-                                   (c >> 3) * SL::kSub + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
-      }
-      dev::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) dev::mbar_arrive(q_ready);
-    }
-    const int nb = nb_of(t);
-    float m_ref = -INFINITY;
-    float ls[4] = {0.f, 0.f, 0.f, 0.f};
+    int blocks = 0, sc = 0, on = 0;  // as in the MMA threads
     bool ok = true;
-    auto rescale_o = [&](float f) {  // O_t (and its row-sum column) and the row sum scale by f
+    for (int items = 0; ok && next_item(items, it); ++items) {
+      const int nb = t ? it.nb1 : it.nb0;
+      const int qi = it.tok0 + (kShareKeys ? t * a.tile_tokens : 0) + tok;  // in its sequence
+      const bool valid = tok < a.tile_tokens && qi < it.n;
+      const int64_t token = it.first + (valid ? qi : 0);
+      // keys < see are this row's
+      int see = it.t_end;
+      if (kPaged && valid) see = min(max(__ldg(a.context_lens + token), 0), it.t_end);
+      if (!kPaged) see = min(qi + 1, it.t_end);
+      float m_ref = -INFINITY;
+      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+      auto rescale_o = [&](float f) {  // O_t (and its row-sum column) and the row sum scale by f
 #pragma unroll 1
-      for (int ch = 0; ch < D / 32; ++ch) {
-        uint32_t o[32];
-        dev::tmem_ld32(ob + ch * 32, o);
-        dev::tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-        dev::tmem_st32(ob + ch * 32, o);
-      }
-      if constexpr (kOnes) {
-        const uint32_t sm = tmem_ld1(ob + D);
-        dev::tmem_wait_ld();
-        tmem_st1(ob + D, __float_as_uint(__uint_as_float(sm) * f));
-      }
-      dev::tmem_wait_st();
-#pragma unroll
-      for (int u = 0; u < 4; ++u) ls[u] *= f;
-    };
-    // One block; false when a wait gave up.
-    auto block = [&](auto mask, int i, int j, int k0, int lim) {
-      constexpr bool kMask = decltype(mask)::value;
-      uint32_t xa[32];
-      const float mx = row_max<kMask>(sb, lim, xa);
-      const float bm = mx == -INFINITY ? -INFINITY : mx * scale_log2;
-      if (i > 0) {
-        // The reference moves only when the block raises it by more than kTcRescale.
-        // PV_t(i-1) was issued before S_t(i) by the same thread, and s_full tracks every
-        // MMA issued before its commit, so O_t is stable here.
-        const bool need = bm > m_ref + kTcRescale;
-        if (__any_sync(0xffffffffu, need)) {
-          const float m_new = fmaxf(m_ref, bm);
-          rescale_o(need ? dev::ex2(m_ref - m_new) : 1.f);
-          if (need) m_ref = m_new;
-        }
-      } else {
-        m_ref = bm;
-      }
-      // a row that has seen no key yet takes its weights, all masked to 0, against 0
-      const float m = m_ref == -INFINITY ? 0.f : m_ref;
-      const int nk = min(kTcKeys, t_end - k0);
-      if (kMask && nk < kTcKeys) {  // V rows past the staged keys are stale or another sequence's
-        const int s = j % KSV;
-        if (!__all_sync(0xffffffffu, dev::mbar_wait(v_full(s), (j / KSV) & 1))) return false;
-        const uint32_t vt = SL::v + s * SL::kTile;
-        for (int idx = r; idx < (kTcKeys - nk) * (D / 8); idx += kTcRows) {
-          const int row = nk + idx / (D / 8), c = idx % (D / 8);
-          *reinterpret_cast<uint4 *>(bp + vt + (c >> 3) * SL::kSub + row * 128 +
-                                     (((c & 7) ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        dev::fence_proxy_async_smem();
-      }
-#pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t xb[32], pk[32];
-        dev::tmem_ld32(sb + 64 * hf + 32, xb);
-        chunk_exp<kMask, !kOnes>(xa, 64 * hf, lim, scale_log2, m, pk, ls);
-        tmem_wait_ld_regs(xb);
-        if (hf == 0) dev::tmem_ld32(sb + 64, xa);
-        chunk_exp<kMask, !kOnes>(xb, 64 * hf + 32, lim, scale_log2, m, pk + 16, ls);
-        if (hf == 0) tmem_wait_ld_regs(xa);
-        dev::tmem_st32(sb + 32 * hf, pk);  // over columns this thread has read
-        dev::tmem_wait_st();
-        dev::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) dev::mbar_arrive(p_half(t, hf));
-      }
-      return true;
-    };
-    for (int i = 0; i < nb && ok; ++i) {
-      const int j = blk(t, i), k0 = key0 + j * kTcKeys;
-      const int lim = see - 1 - k0;  // columns c <= lim are seen
-      if (!(ok = __all_sync(0xffffffffu, dev::mbar_wait(s_full(t), i & 1)))) break;
-      dev::tc_fence_after();
-      if (__all_sync(0xffffffffu, lim >= kTcKeys - 1))
-        ok = block(std::false_type{}, i, j, k0, lim);
-      else
-        ok = block(std::true_type{}, i, j, k0, lim);
-    }
-    float lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
-    if (!ok && lane == 0) fail(false);
-    if (ok && nb > 0 && !(ok = __all_sync(0xffffffffu, dev::mbar_wait(pv_done(t), 0))) && lane == 0)
-      fail(false);
-    if (ok && nb > 0) {
-      dev::tc_fence_after();
-      if constexpr (kOnes) {
-        lsum = __uint_as_float(tmem_ld1(ob + D));
-        dev::tmem_wait_ld();
-      }
-    }
-    if constexpr (kPaged) {
-      // normalised fp32 partial and its log-sum-exp; no key seen: zeros and -inf
-      const int64_t row = ((int64_t)(first + qi) * a.num_q_heads + g * G + h) * a.n_rows +
-                          2 * blockIdx.y + t;
-      const bool any = nb > 0 && !(lsum == 0.f && m_ref == -INFINITY);
-      const float inv = any ? 1.f / lsum : 0.f;
-      if (ok && valid) a.lse_part[row] = any ? (m_ref + log2f(lsum)) * kLn2 : -INFINITY;
-      float4 *dst = reinterpret_cast<float4 *>(a.o_part + row * D);
-#pragma unroll 1
-      for (int ch = 0; ok && ch < D / 32; ++ch) {
-        uint32_t o[32];
-        if (nb > 0) {
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t o[32];
           dev::tmem_ld32(ob + ch * 32, o);
           dev::tmem_wait_ld();
-        }
-        if (valid) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            dst[ch * 8 + u] = any ? make_float4(__uint_as_float(o[4 * u]) * inv,
-                                                __uint_as_float(o[4 * u + 1]) * inv,
-                                                __uint_as_float(o[4 * u + 2]) * inv,
-                                                __uint_as_float(o[4 * u + 3]) * inv)
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+          dev::tmem_st32(ob + ch * 32, o);
+        }
+        if constexpr (kOnes) {
+          const uint32_t sm = tmem_ld1(ob + D);
+          dev::tmem_wait_ld();
+          tmem_st1(ob + D, __float_as_uint(__uint_as_float(sm) * f));
+        }
+        dev::tmem_wait_st();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) ls[u] *= f;
+      };
+      // One block; false when a wait gave up.
+      auto block = [&](auto mask, int i, int k0, int lim) {
+        constexpr bool kMask = decltype(mask)::value;
+        uint32_t xa[32];
+        const float mx = row_max<kMask>(sb, lim, xa);
+        const float bm = mx == -INFINITY ? -INFINITY : mx * scale_log2;
+        if (i > 0) {
+          // The reference moves only when the block raises it by more than kTcRescale.
+          // PV_t(i-1) was issued before S_t(i) by the same thread, and s_full tracks every
+          // MMA issued before its commit, so O_t is stable here.
+          const bool need = bm > m_ref + kTcRescale;
+          if (__any_sync(0xffffffffu, need)) {
+            const float m_new = fmaxf(m_ref, bm);
+            rescale_o(need ? dev::ex2(m_ref - m_new) : 1.f);
+            if (need) m_ref = m_new;
+          }
+        } else {
+          m_ref = bm;
+        }
+        // a row that has seen no key yet takes its weights, all masked to 0, against 0
+        const float m = m_ref == -INFINITY ? 0.f : m_ref;
+        const int nk = min(kTcKeys, it.t_end - k0);
+        if (kMask && nk < kTcKeys) {  // V rows past the staged keys are stale or another sequence's
+          const int j = blocks + blk(t, i), s = j % KSV;
+          if (!__all_sync(0xffffffffu, dev::mbar_wait(v_full(s), (j / KSV) & 1))) return false;
+          const uint32_t vt = SL::v + s * SL::kTile;
+          for (int idx = r; idx < (kTcKeys - nk) * (D / 8); idx += kTcRows) {
+            const int row = nk + idx / (D / 8), c = idx % (D / 8);
+            *reinterpret_cast<uint4 *>(bp + vt + (c >> 3) * SL::kSub + row * 128 +
+                                       (((c & 7) ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          dev::fence_proxy_async_smem();
+        }
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t xb[32], pk[32];
+          dev::tmem_ld32(sb + 64 * hf + 32, xb);
+          chunk_exp<kMask, !kOnes>(xa, 64 * hf, lim, scale_log2, m, pk, ls);
+          tmem_wait_ld_regs(xb);
+          if (hf == 0) dev::tmem_ld32(sb + 64, xa);
+          chunk_exp<kMask, !kOnes>(xb, 64 * hf + 32, lim, scale_log2, m, pk + 16, ls);
+          if (hf == 0) tmem_wait_ld_regs(xa);
+          dev::tmem_st32(sb + 32 * hf, pk);  // over columns this thread has read
+          dev::tmem_wait_st();
+          dev::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) dev::mbar_arrive(p_half(t, hf));
+        }
+        return true;
+      };
+      for (int i = 0; i < nb && ok; ++i) {
+        const int k0 = it.key0 + blk(t, i) * kTcKeys;
+        const int lim = see - 1 - k0;  // columns c <= lim are seen
+        if (!(ok = __all_sync(0xffffffffu, dev::mbar_wait(s_full(t), (sc + i) & 1)))) break;
+        dev::tc_fence_after();
+        if (__all_sync(0xffffffffu, lim >= kTcKeys - 1))
+          ok = block(std::false_type{}, i, k0, lim);
+        else
+          ok = block(std::true_type{}, i, k0, lim);
+      }
+      if (ok && nb > 0) ok = __all_sync(0xffffffffu, dev::mbar_wait(pv_done(t), on & 1));
+      if (!ok) {
+        if (lane == 0) fail(false);
+        break;
+      }
+      float lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      if (nb > 0) {
+        dev::tc_fence_after();
+        if constexpr (kOnes) {
+          lsum = __uint_as_float(tmem_ld1(ob + D));
+          dev::tmem_wait_ld();
         }
       }
-    } else if (ok && nb > 0) {
-      const float inv = 1.f / lsum;
-      uint4 *dst = reinterpret_cast<uint4 *>(a.out + (int64_t)(first + qi) * a.out_stride +
-                                             (int64_t)(g * G + h) * D);
+      if constexpr (kPaged) {
+        // normalised fp32 partial and its log-sum-exp; no key seen: zeros and -inf
+        const int64_t row = (token * a.num_q_heads + it.g * G + h) * a.n_rows + 2 * blockIdx.y + t;
+        const bool any = nb > 0 && !(lsum == 0.f && m_ref == -INFINITY);
+        const float inv = any ? 1.f / lsum : 0.f;
+        if (valid) a.lse_part[row] = any ? (m_ref + log2f(lsum)) * kLn2 : -INFINITY;
+        float4 *dst = reinterpret_cast<float4 *>(a.o_part + row * D);
 #pragma unroll 1
-      for (int ch = 0; ch < D / 32; ++ch) {
-        uint32_t o[32];
-        dev::tmem_ld32(ob + ch * 32, o);
-        dev::tmem_wait_ld();
-        if (valid) {
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t o[32];
+          if (nb > 0) {
+            dev::tmem_ld32(ob + ch * 32, o);
+            dev::tmem_wait_ld();
+          }
+          if (valid) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t w4[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w4[e] = dev::pack_bf16x2(__uint_as_float(o[8 * u + 2 * e]) * inv,
-                                       __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
-            dst[ch * 4 + u] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+            for (int u = 0; u < 8; ++u)
+              dst[ch * 8 + u] = any ? make_float4(__uint_as_float(o[4 * u]) * inv,
+                                                  __uint_as_float(o[4 * u + 1]) * inv,
+                                                  __uint_as_float(o[4 * u + 2]) * inv,
+                                                  __uint_as_float(o[4 * u + 3]) * inv)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
           }
         }
+      } else if (nb > 0) {
+        const float inv = 1.f / lsum;
+        uint4 *dst = reinterpret_cast<uint4 *>(a.out + token * a.out_stride + (int64_t)(it.g * G + h) * D);
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t o[32];
+          dev::tmem_ld32(ob + ch * 32, o);
+          dev::tmem_wait_ld();
+          if (valid) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint32_t w4[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w4[e] = dev::pack_bf16x2(__uint_as_float(o[8 * u + 2 * e]) * inv,
+                                         __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
+              dst[ch * 4 + u] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+            }
+          }
+        }
+        dev::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(o_free(t));  // the next item's P.V may overwrite O_t
       }
+      blocks += (it.t_end - it.key0 + kTcKeys - 1) / kTcKeys;
+      sc += nb;
+      on += nb > 0 ? 1 : 0;
     }
   }
 
   // ---- teardown: no tensor-core op or copy may still be in flight when TMEM is freed
   if (tid == 0) (void)dev::mbar_wait(mma_done, 0);
   __syncthreads();
-  if (is_producer && lane == 0 && *s_flag) {
+  if ((warp == kProducer || warp == kProducerV) && lane == 0 && *s_flag) {
     const int ks = warp == kProducer ? KSK : KSV;
     for (int s = 0; s < ks; ++s) {
       const int last = s + ((issued - 1 - s) / ks) * ks;  // the last block on stage s
@@ -672,21 +840,21 @@ int prepare_tile_kernel() {
 }
 
 template <int D>
-int launch_prompt(const CUtensorMap &tmk, const CUtensorMap &tmv, const TileArgs &a, unsigned grid,
-                  cudaStream_t stream) {
+int launch_prompt(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                  const TileArgs &a, unsigned grid, cudaStream_t stream) {
   const int rc = prepare_tile_kernel<D, kPrompt>();
   if (rc) return rc;
-  tile_kernel<D, kPrompt><<<grid, kTileThreads, tile_smem<D, kPrompt>(), stream>>>(tmk, tmv, a);
+  tile_kernel<D, kPrompt><<<grid, kTileThreads, tile_smem<D, kPrompt>(), stream>>>(tmq, tmk, tmv, a);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? PKV_OK : cuda_error(e, "tile_kernel launch");
 }
 
 template <int D>
-int launch_prefix_tiles(const CUtensorMap &tmk, const CUtensorMap &tmv, const TileArgs &a, dim3 grid,
-                        cudaStream_t stream) {
+int launch_prefix_tiles(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                        const TileArgs &a, dim3 grid, cudaStream_t stream) {
   const int rc = prepare_tile_kernel<D, kPrefix>();
   if (rc) return rc;
-  tile_kernel<D, kPrefix><<<grid, kTileThreads, tile_smem<D, kPrefix>(), stream>>>(tmk, tmv, a);
+  tile_kernel<D, kPrefix><<<grid, kTileThreads, tile_smem<D, kPrefix>(), stream>>>(tmq, tmk, tmv, a);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? PKV_OK : cuda_error(e, "tile_kernel launch");
 }
@@ -696,8 +864,6 @@ int launch_prefix_tiles(const CUtensorMap &tmk, const CUtensorMap &tmv, const Ti
 int launch_prefix(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv_cache_desc &c,
                   const PrefixLaunch &l, cudaStream_t stream) {
   TileArgs a = {};
-  a.q = l.q;
-  a.q_stride = (int64_t)l.num_q_heads * c.head_dim;
   a.start = l.group_start;
   a.num = l.num_groups;
   a.total = l.num_seqs;
@@ -705,6 +871,7 @@ int launch_prefix(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv_cach
   a.num_q_heads = l.num_q_heads;
   a.num_kv_heads = c.num_kv_heads;
   a.group = l.num_q_heads / c.num_kv_heads;
+  a.tile_tokens = kTileRows / a.group;
   a.scale_log2 = l.scale * kLog2e;
   a.block_tables = l.block_tables;
   a.context_lens = l.context_lens;
@@ -721,9 +888,16 @@ int launch_prefix(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv_cach
   a.lse_part = l.lse_part;
   if (l.tiles * c.num_kv_heads > 0x7fffffffLL || l.splits > 65535)
     return set_error(PKV_ERR_UNSUPPORTED, "shared prefix: too many tiles");
+  CUtensorMap tmq;
+  {
+    std::lock_guard<std::mutex> lk(attn_mutex());
+    const int rc = query_map(l.q, l.num_seqs, l.num_q_heads, c.head_dim,
+                             (int64_t)l.num_q_heads * c.head_dim, a.group, a.tile_tokens, &tmq);
+    if (rc) return rc;
+  }
   const dim3 grid((unsigned)(l.tiles * c.num_kv_heads), (unsigned)l.splits);
-  return c.head_dim == 64 ? launch_prefix_tiles<64>(tmk, tmv, a, grid, stream)
-                          : launch_prefix_tiles<128>(tmk, tmv, a, grid, stream);
+  return c.head_dim == 64 ? launch_prefix_tiles<64>(tmq, tmk, tmv, a, grid, stream)
+                          : launch_prefix_tiles<128>(tmq, tmk, tmv, a, grid, stream);
 }
 
 }  // namespace pkv
@@ -742,6 +916,9 @@ PKV_API int prompt_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k
   if (num_q_heads % num_kv_heads != 0)
     return set_error(PKV_ERR_SHAPE, "%s: num_q_heads %d is not a multiple of num_kv_heads %d", fn,
                      num_q_heads, num_kv_heads);
+  if (num_q_heads / num_kv_heads > kTileRows)
+    return set_error(PKV_ERR_UNSUPPORTED, "%s: query group %d > %d", fn, num_q_heads / num_kv_heads,
+                     kTileRows);
   if (head_dim != 64 && head_dim != 128)
     return set_error(PKV_ERR_UNSUPPORTED, "%s: head_dim %d (built: 64, 128)", fn, head_dim);
   if (num_tokens > 0x7fffff00LL) return set_error(PKV_ERR_UNSUPPORTED, "%s: num_tokens over 2^31", fn);
@@ -763,9 +940,7 @@ PKV_API int prompt_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k
   if (reinterpret_cast<uintptr_t>(query_start) & 3u)
     return set_error(PKV_ERR_ALIGN, "%s: query_start must be 4-byte aligned", fn);
   TileArgs a = {};
-  a.q = q;
   a.out = out;
-  a.q_stride = q_stride;
   a.out_stride = out_stride;
   a.start = query_start;
   a.num = num_seqs;
@@ -774,21 +949,24 @@ PKV_API int prompt_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k
   a.num_q_heads = num_q_heads;
   a.num_kv_heads = num_kv_heads;
   a.group = num_q_heads / num_kv_heads;
+  a.tile_tokens = kTileRows / a.group;
   a.scale_log2 = scale * kLog2e;
-  // tiles of all sequences: at most the packed rows' plus one partial tile per sequence
-  const int64_t tiles = num_tokens * a.group / (2 * kTcRows) + std::min<int64_t>(num_seqs, num_tokens);
+  // tiles of all sequences: at most the packed tokens' plus one partial tile per sequence
+  const int64_t tiles = num_tokens / (2 * a.tile_tokens) + std::min<int64_t>(num_seqs, num_tokens);
   if (tiles > 0x7fffffffLL / num_kv_heads) return set_error(PKV_ERR_UNSUPPORTED, "%s: too many query rows", fn);
-  CUtensorMap tmk, tmv;
+  CUtensorMap tmq, tmk, tmv;
   int rc;
   {
     std::lock_guard<std::mutex> lk(attn_mutex());
-    rc = packed_map(k, num_tokens, num_kv_heads, head_dim, k_stride, kTcKeys, &tmk);
+    rc = query_map(q, num_tokens, num_q_heads, head_dim, q_stride, a.group, a.tile_tokens, &tmq);
+    if (!rc) rc = packed_map(k, num_tokens, num_kv_heads, head_dim, k_stride, kTcKeys, &tmk);
     if (!rc) rc = packed_map(v, num_tokens, num_kv_heads, head_dim, v_stride, kTcKeys, &tmv);
   }
   if (rc) return rc;
   const unsigned grid = (unsigned)(tiles * num_kv_heads);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  rc = head_dim == 64 ? launch_prompt<64>(tmk, tmv, a, grid, s) : launch_prompt<128>(tmk, tmv, a, grid, s);
+  rc = head_dim == 64 ? launch_prompt<64>(tmq, tmk, tmv, a, grid, s)
+                      : launch_prompt<128>(tmq, tmk, tmv, a, grid, s);
   if (!rc) clear_error();
   return rc;
 }

@@ -98,6 +98,24 @@ def test_matches_reference(B, lens, hq, hkv, d, fused):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,d", [(24, 8, 128), (8, 8, 64), (10, 2, 128), (16, 2, 64)])
+def test_many_items_per_cta(B, hq, hkv, d):
+    """Far more tiles than SMs: every CTA goes through many items, of sequences of all sizes
+    (none, one token, tiles whose halves end in the same block and in different ones)."""
+    g = torch.Generator().manual_seed(hq + d)
+    lens = torch.randint(0, 420, (150,), generator=g).tolist() + [1, 0, 127, 128, 129, 2000]
+    q, k, v, start = make(lens, hq, hkv, d, True, seed=d)
+    out = torch.empty(q.shape[0], hq, d, dtype=torch.bfloat16, device="cuda")
+    o, amp = reference(q, k, v, start, d ** -0.5)
+    B.pkv_device_errors()
+    for _ in range(3):
+        out.fill_(9.0)
+        B.prompt_attention(out, q, k, v, start.cuda(), max(lens), d ** -0.5)
+        check(out, o, amp)
+    assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("scale", [1.0, -0.7, 0.0])
 def test_wide_scores(B, d, scale):
@@ -213,6 +231,7 @@ def test_argument_errors(B):
         return lib.prompt_attention(out, q, FAKE, FAKE, *st, start, t, longest, n, hq, hkv, d, 0.1, None)
 
     assert call(d=96) == -3 and "head_dim" in B.pkv_last_error()
+    assert call(hq=258, st=(1 << 15, 1 << 15, 128, 128)) == -3 and "group" in B.pkv_last_error()
     assert call(hq=7) == -2 and call(hkv=0) == -2 and call(n=-1) == -2 and call(t=-1) == -2
     assert call(longest=-1) == -2
     assert call(st=(512, 504, 128, 128)) == -2                 # shorter than a token
