@@ -36,9 +36,13 @@ namespace pkv {
 //  * kPrefix: both tiles hold the same rows (queries of a group of sequences) and take
 //    alternate key blocks, so that a few rows over a long prefix still overlap softmax and
 //    tensor core.  The keys come from the pages of the group's first sequence; the CTA
-//    covers one split of them, and each tile writes its softmax-normalised fp32 output and
-//    log-sum-exp for the merge in the decode kernel that follows.
+//    covers one split of them.  The tiles' results are joined through shared memory and those of
+//    a cluster's splits through distributed shared memory: each CTA gathers a share of the
+//    rows and writes one softmax-normalised fp32 row and log-sum-exp per cluster, for the
+//    merge in the decode kernel that follows.  (Written per tile and split, 64 sequences of 3
+//    heads over 8192 keys left 17 MB of partials, half as much as the keys and values.)
 enum { kPrompt = 0, kPrefix = 1 };
+constexpr int kMaxCluster = kPrefixCluster;
 
 struct TileArgs {
   uint16_t *out;            // prompt
@@ -54,7 +58,7 @@ struct TileArgs {
   int32_t max_blocks, max_prefix, block_size, log2_bs, box_rows;
   int32_t split_keys;       // keys per split (a multiple of kTcKeys)
   int32_t n_rows;           // partial rows per (sequence, head)
-  float *o_part, *lse_part; // [B][Hq][n_rows][D], [B][Hq][n_rows]; rows 2 s, 2 s + 1: split s
+  float *o_part, *lse_part; // [B][Hq][n_rows][D], [B][Hq][n_rows]; row s: the s-th cluster of splits
 };
 
 constexpr int kTileThreads = 32 * 12;  // 8 softmax warps, the K and V producers, an MMA warp per tile
@@ -90,11 +94,15 @@ struct TileSmem {
   static constexpr uint32_t ones = q + kQ * kTile;
   static constexpr uint32_t item = ones + (kOnes ? kSub : 0);  // two items
   static constexpr uint32_t clc = item + 2 * sizeof(TileItem); // a launch-control answer, 16 B
-  static constexpr uint32_t bars = clc + 16;
+  // kPrefix, once the rings are done with: the CTA's rows [128][D] fp32, row r's 16-byte chunk
+  // c at c ^ (r & 7); and beside them (max in base 2, sum) per row
+  static constexpr uint32_t rows = 0;
+  static constexpr uint32_t ml = clc + 16;
+  static constexpr uint32_t bars = ml + (MODE == kPrefix ? kTcRows * 8 : 0);
   // the rings, then s_full, pv_done per tile, p_half per tile and half, q_full, q_free, o_free
-  // per tile, item_full, item_empty per slot, clc_full, mma_done
+  // per tile, item_full, item_empty per slot, clc_full, mma_done, tiles_done, rows_left
   static constexpr int kRings = 2 * KSK + 2 * KSV;
-  static constexpr int kBars = kRings + 20;
+  static constexpr int kBars = kRings + 22;
   static constexpr uint32_t tslot = bars + kBars * 8;
   static constexpr uint32_t flag = tslot + 8;
   static constexpr uint32_t turns = flag + 8;  // P.V batches issued, per tile
@@ -193,9 +201,11 @@ __device__ __forceinline__ bool make_item(const TileArgs &a, unsigned cta_x, uns
       prefix = prefix < 0 ? 0 : cap;
     }
     prefix = prefix >> a.log2_bs << a.log2_bs;  // whole pages
+    // a CTA without keys still takes part in its cluster's merge, if any other has some
+    const int cluster0 = (int)(cta_y - dev::cluster_ctarank()) * a.split_keys;
+    if (cluster0 >= prefix) return false;
     it.key0 = (int)cta_y * a.split_keys;
-    if (it.key0 >= prefix) return false;
-    it.t_end = min(it.key0 + a.split_keys, prefix);
+    it.t_end = max(it.key0, min(it.key0 + a.split_keys, prefix));
     const int nblk = (it.t_end - it.key0 + kTcKeys - 1) / kTcKeys;
     it.nb0 = (nblk + 1) / 2;
     it.nb1 = nblk / 2;
@@ -350,6 +360,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto item_empty = [&](int s) { return bars + 8u * (kRings + 16 + s); };
   const uint32_t clc_full = bars + 8u * (kRings + 18);
   const uint32_t mma_done = bars + 8u * (kRings + 19);
+  const uint32_t tiles_done = bars + 8u * (kRings + 20), rows_left = bars + 8u * (kRings + 21);
   volatile int *const s_turn = reinterpret_cast<volatile int *>(bp + SL::turns);
   volatile uint32_t *const s_tmem = reinterpret_cast<volatile uint32_t *>(bp + SL::tslot);
   volatile int *const s_flag = reinterpret_cast<volatile int *>(bp + SL::flag);
@@ -365,7 +376,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   TileItem it = {};
   bool have = false;
   if (kPaged || warp == kProducer) have = make_item<MODE>(a, blockIdx.x, blockIdx.y, lane, it);
-  if (kPaged && !have) return;
+  if (kPaged && !have) return;  // the whole cluster: nothing in its rows or its keys
+  const TileItem first = it;    // kPrefix: the CTA's only one
+  if (kPaged) have = it.t_end > it.key0;
   if (tid == 0) {
     for (int i = 0; i < SL::kBars; ++i) {
       const int r = i - kRings;
@@ -375,6 +388,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                              : r == 12 || r == 13 ? 4u        // o_free: alike
                              : r == 16 || r == 17 ? (uint32_t)kItemReaders
                              : r == 19 ? 2u                   // mma_done: both MMA threads
+                             : r == 20 ? 8u                   // tiles_done: every softmax warp
+                             : r == 21 ? 4u                   // rows_left: tile 1's
                                        : 1u;
       dev::mbar_init(bars + 8u * i, count);
     }
@@ -733,12 +748,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = block(std::true_type{}, i, k0, lim);
       }
       if (ok && nb > 0) ok = __all_sync(0xffffffffu, dev::mbar_wait(pv_done(t), on & 1));
-      if (!ok) {
-        if (lane == 0) fail(false);
-        break;
-      }
+      if (!ok && lane == 0) fail(false);
+      if (!ok && !kPaged) break;
       float lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
-      if (nb > 0) {
+      if (ok && nb > 0) {
         dev::tc_fence_after();
         if constexpr (kOnes) {
           lsum = __uint_as_float(tmem_ld1(ob + D));
@@ -746,29 +759,48 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       if constexpr (kPaged) {
-        // normalised fp32 partial and its log-sum-exp; no key seen: zeros and -inf
-        const int64_t row = (token * a.num_q_heads + it.g * G + h) * a.n_rows + 2 * blockIdx.y + t;
-        const bool any = nb > 0 && !(lsum == 0.f && m_ref == -INFINITY);
-        const float inv = any ? 1.f / lsum : 0.f;
-        if (valid) a.lse_part[row] = any ? (m_ref + log2f(lsum)) * kLn2 : -INFINITY;
-        float4 *dst = reinterpret_cast<float4 *>(a.o_part + row * D);
+        // This tile's (max, sum, unnormalised O) joined with the other's, which has the same
+        // rows: tile 1 leaves its own in shared memory (the rings are done with once both
+        // tiles' MMAs are), tile 0 adds it to its own and leaves the sum there.
+        float *const row_o = reinterpret_cast<float *>(bp + SL::rows + r * D * 4);
+        float2 *const ml = reinterpret_cast<float2 *>(bp + SL::ml) + r;
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(tiles_done);
+        ok = __all_sync(0xffffffffu, dev::mbar_wait(tiles_done, 0)) && ok;
+        const float m1 = nb > 0 ? m_ref : -INFINITY;
+        if (t == 1) *ml = make_float2(m1, nb > 0 ? lsum : 0.f);
+        float w0 = 1.f, w1 = 0.f;
+        if (t == 0) {
+          ok = __all_sync(0xffffffffu, dev::mbar_wait(rows_left, 0)) && ok;
+          const float2 o = *ml;
+          const float m = fmaxf(m1, o.x);
+          w0 = m == -INFINITY ? 1.f : dev::ex2(m1 - m);
+          w1 = m == -INFINITY ? 0.f : dev::ex2(o.x - m);
+          lsum = (nb > 0 ? lsum : 0.f) * w0 + o.y * w1;
+          m_ref = m;
+        }
+        const bool other = t == 0 && __any_sync(0xffffffffu, it.nb1 > 0);
 #pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
+        for (int ch = 0; ch < D / 32 && nb > 0 && ok; ++ch) {
           uint32_t o[32];
-          if (nb > 0) {
-            dev::tmem_ld32(ob + ch * 32, o);
-            dev::tmem_wait_ld();
-          }
-          if (valid) {
+          dev::tmem_ld32(ob + ch * 32, o);
+          dev::tmem_wait_ld();
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-              dst[ch * 8 + u] = any ? make_float4(__uint_as_float(o[4 * u]) * inv,
-                                                  __uint_as_float(o[4 * u + 1]) * inv,
-                                                  __uint_as_float(o[4 * u + 2]) * inv,
-                                                  __uint_as_float(o[4 * u + 3]) * inv)
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int u = 0; u < 8; ++u) {
+            float4 *const at = reinterpret_cast<float4 *>(row_o) + ((ch * 8 + u) ^ (r & 7));
+            float4 x = make_float4(__uint_as_float(o[4 * u]) * w0, __uint_as_float(o[4 * u + 1]) * w0,
+                                   __uint_as_float(o[4 * u + 2]) * w0, __uint_as_float(o[4 * u + 3]) * w0);
+            if (other) {
+              const float4 y = *at;
+              x.x += y.x * w1, x.y += y.y * w1, x.z += y.z * w1, x.w += y.w * w1;
+            }
+            *at = x;
           }
         }
+        __syncwarp();
+        if (t == 1 && lane == 0) dev::mbar_arrive(rows_left);
+        if (!ok && lane == 0) fail(false);
+        if (t == 0) *ml = make_float2(m_ref, lsum);
       } else if (nb > 0) {
         const float inv = 1.f / lsum;
         uint4 *dst = reinterpret_cast<uint4 *>(a.out + token * a.out_stride + (int64_t)(it.g * G + h) * D);
@@ -802,6 +834,55 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   // ---- teardown: no tensor-core op or copy may still be in flight when TMEM is freed
   if (tid == 0) (void)dev::mbar_wait(mma_done, 0);
   __syncthreads();
+  if constexpr (kPaged) {
+    // The cluster's merge: every CTA reads its share of the rows from all of them.  Each
+    // thread arrives after bounded waits only, so both barriers complete; the second keeps
+    // every CTA until its rows have been read.
+    if (!have && tid < kTcRows)
+      reinterpret_cast<float2 *>(bp + SL::ml)[tid] = make_float2(-INFINITY, 0.f);
+    const int n = (int)dev::cluster_nctarank(), rank = (int)dev::cluster_ctarank();
+    dev::cluster_arrive_release();
+    dev::cluster_wait();
+    const int share = (tile_rows + n - 1) / n;
+    for (int r = rank * share + warp; r < min((rank + 1) * share, tile_rows); r += kTileThreads / 32) {
+      const int tok = r / G, h = r - tok * G;
+      const int qi = first.tok0 + tok;
+      if (qi >= first.n) break;
+      float2 ml[kMaxCluster];
+      float4 o[kMaxCluster];
+      float m = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        ml[c] = make_float2(-INFINITY, 0.f);
+        o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < n) {
+          ml[c] = dev::ld_cluster_f2(dev::mapa(base + SL::ml + r * 8, c));
+          if (lane < D / 4)
+            o[c] = dev::ld_cluster_f4(dev::mapa(base + SL::rows + r * D * 4 + ((lane ^ (r & 7)) << 4), c));
+        }
+        m = fmaxf(m, ml[c].x);
+      }
+      float l = 0.f;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        if (ml[c].x == -INFINITY && ml[c].y == 0.f) continue;  // no key seen there: nothing written
+        const float w = dev::ex2(ml[c].x - m);
+        l += w * ml[c].y;
+        x.x += w * o[c].x, x.y += w * o[c].y, x.z += w * o[c].z, x.w += w * o[c].w;
+      }
+      const bool any = m != -INFINITY || l != 0.f;
+      const float inv = any ? 1.f / l : 0.f;
+      const int64_t row = ((int64_t)(first.first + qi) * a.num_q_heads + first.g * G + h) * a.n_rows +
+                          blockIdx.y / n;
+      if (lane < D / 4)
+        reinterpret_cast<float4 *>(a.o_part + row * D)[lane] =
+            make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+      if (lane == 0) a.lse_part[row] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+    }
+    dev::cluster_arrive_release();
+    dev::cluster_wait();
+  }
   if ((warp == kProducer || warp == kProducerV) && lane == 0 && *s_flag) {
     const int ks = warp == kProducer ? KSK : KSV;
     for (int s = 0; s < ks; ++s) {
@@ -851,11 +932,22 @@ int launch_prompt(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensor
 
 template <int D>
 int launch_prefix_tiles(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
-                        const TileArgs &a, dim3 grid, cudaStream_t stream) {
+                        const TileArgs &a, dim3 grid, int cluster, cudaStream_t stream) {
   const int rc = prepare_tile_kernel<D, kPrefix>();
   if (rc) return rc;
-  tile_kernel<D, kPrefix><<<grid, kTileThreads, tile_smem<D, kPrefix>(), stream>>>(tmq, tmk, tmv, a);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kTileThreads, 1, 1);
+  cfg.dynamicSmemBytes = tile_smem<D, kPrefix>();
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = (unsigned)cluster;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tile_kernel<D, kPrefix>, tmq, tmk, tmv, a);
   return e == cudaSuccess ? PKV_OK : cuda_error(e, "tile_kernel launch");
 }
 
@@ -896,8 +988,8 @@ int launch_prefix(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv_cach
     if (rc) return rc;
   }
   const dim3 grid((unsigned)(l.tiles * c.num_kv_heads), (unsigned)l.splits);
-  return c.head_dim == 64 ? launch_prefix_tiles<64>(tmq, tmk, tmv, a, grid, stream)
-                          : launch_prefix_tiles<128>(tmq, tmk, tmv, a, grid, stream);
+  return c.head_dim == 64 ? launch_prefix_tiles<64>(tmq, tmk, tmv, a, grid, l.cluster, stream)
+                          : launch_prefix_tiles<128>(tmq, tmk, tmv, a, grid, l.cluster, stream);
 }
 
 }  // namespace pkv
