@@ -342,9 +342,10 @@ SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int
   for (int32_t c = kPrefixCluster; c > 1; c /= 2) {
     const int64_t fit = (c == 2 ? sms : sms - sms / 19) / c;  // clusters at once
     if (units > fit || blocks < c) continue;
+    const int64_t n = c * std::min(fit / units, blocks / c);
+    if (n <= splits) continue;
     p.cluster = c;
-    splits = c * std::min(fit / units, blocks / c);
-    break;
+    splits = n;
   }
   p.split_keys = (int32_t)std::min<int64_t>(std::max<int64_t>((blocks + splits - 1) / splits, 1) * kTileKeys,
                                             1 << 29);

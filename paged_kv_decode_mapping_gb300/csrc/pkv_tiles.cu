@@ -94,15 +94,16 @@ struct TileSmem {
   static constexpr uint32_t ones = q + kQ * kTile;
   static constexpr uint32_t item = ones + (kOnes ? kSub : 0);  // two items
   static constexpr uint32_t clc = item + 2 * sizeof(TileItem); // a launch-control answer, 16 B
-  // kPrefix, once the rings are done with: the CTA's rows [128][D] fp32, row r's 16-byte chunk
-  // c at c ^ (r & 7); and beside them (max in base 2, sum) per row
+  // kPrefix, once the rings are done with: the tiles' rows [2][128][D] fp32, row r's 16-byte
+  // chunk c at c ^ (r & 7), in the K ring; (max in base 2, sum) per row in the V ring
   static constexpr uint32_t rows = 0;
-  static constexpr uint32_t ml = clc + 16;
-  static constexpr uint32_t bars = ml + (MODE == kPrefix ? kTcRows * 8 : 0);
+  static constexpr uint32_t ml = v;
+  static constexpr uint32_t bars = clc + 16;
+  static_assert(MODE == kPrompt || 2u * kTcRows * D * 4 <= KSK * kTile, "both tiles' rows fit the K ring");
   // the rings, then s_full, pv_done per tile, p_half per tile and half, q_full, q_free, o_free
-  // per tile, item_full, item_empty per slot, clc_full, mma_done, tiles_done, rows_left
+  // per tile, item_full, item_empty per slot, clc_full, mma_done, tiles_done
   static constexpr int kRings = 2 * KSK + 2 * KSV;
-  static constexpr int kBars = kRings + 22;
+  static constexpr int kBars = kRings + 21;
   static constexpr uint32_t tslot = bars + kBars * 8;
   static constexpr uint32_t flag = tslot + 8;
   static constexpr uint32_t turns = flag + 8;  // P.V batches issued, per tile
@@ -138,16 +139,18 @@ __device__ __forceinline__ bool clc_answer(uint32_t src, uint32_t &ctaid) {
 }
 
 // The sequence (or group) whose pieces of `tokens` query tokens hold piece number idx, its
-// first query token, its length, the piece's place in it and its pieces.  Whole warps;
+// first query token, its length, the piece's place in it, its pieces and its prefix.  Whole warps;
 // lengths that are negative, past `total` or over max_len are clamped and flagged.
 __device__ __forceinline__ bool locate_tile(const TileArgs &a, int64_t idx, int tokens, int lane,
-                                            int &b, int &first, int &n, int &tile, int &ntiles) {
+                                            int &first, int &n, int &tile, int &ntiles,
+                                            int &prefix) {
   int64_t before = 0;
   for (int c = 0; c < a.num; c += 32) {
     const int i = c + lane;
-    int s = 0, len = 0;
+    int s = 0, len = 0, p = 0;
     if (i < a.num) {
       const int s0 = __ldg(a.start + i), e0 = __ldg(a.start + i + 1);
+      if (a.prefix_lens) p = __ldg(a.prefix_lens + i);
       s = min(max(s0, 0), a.total);
       len = min(max(e0, s), a.total) - s;
       len = min(len, a.max_len);
@@ -163,7 +166,7 @@ __device__ __forceinline__ bool locate_tile(const TileArgs &a, int64_t idx, int 
     const unsigned past = __ballot_sync(0xffffffffu, before + upto > idx);
     if (past) {
       const int l = __ffs(past) - 1;
-      b = c + l;
+      prefix = __shfl_sync(0xffffffffu, p, l);
       first = __shfl_sync(0xffffffffu, s, l);
       n = __shfl_sync(0xffffffffu, len, l);
       ntiles = __shfl_sync(0xffffffffu, mine, l);
@@ -182,8 +185,8 @@ __device__ __forceinline__ bool make_item(const TileArgs &a, unsigned cta_x, uns
   it.live = 1;
   it.g = (int)(cta_x % (unsigned)a.num_kv_heads);
   const int tokens = a.tile_tokens * (MODE == kPrompt ? 2 : 1);
-  int b, tile, ntiles;
-  if (!locate_tile(a, cta_x / (unsigned)a.num_kv_heads, tokens, lane, b, it.first, it.n, tile, ntiles))
+  int tile, ntiles, prefix;
+  if (!locate_tile(a, cta_x / (unsigned)a.num_kv_heads, tokens, lane, it.first, it.n, tile, ntiles, prefix))
     return false;
   if constexpr (MODE == kPrompt) {
     it.tok0 = (ntiles - 1 - tile) * tokens;  // a sequence's last tiles see the most keys: first
@@ -194,7 +197,6 @@ __device__ __forceinline__ bool make_item(const TileArgs &a, unsigned cta_x, uns
     it.nb1 = e1 > e0 ? (e1 + kTcKeys - 1) / kTcKeys : 0;
   } else {
     it.tok0 = tile * tokens;
-    int prefix = __ldg(a.prefix_lens + b);
     const int cap = (int)min((int64_t)a.max_blocks * a.block_size, (int64_t)a.max_prefix);
     if (prefix < 0 || prefix > cap) {
       if (lane == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto item_empty = [&](int s) { return bars + 8u * (kRings + 16 + s); };
   const uint32_t clc_full = bars + 8u * (kRings + 18);
   const uint32_t mma_done = bars + 8u * (kRings + 19);
-  const uint32_t tiles_done = bars + 8u * (kRings + 20), rows_left = bars + 8u * (kRings + 21);
+  const uint32_t tiles_done = bars + 8u * (kRings + 20);
   volatile int *const s_turn = reinterpret_cast<volatile int *>(bp + SL::turns);
   volatile uint32_t *const s_tmem = reinterpret_cast<volatile uint32_t *>(bp + SL::tslot);
   volatile int *const s_flag = reinterpret_cast<volatile int *>(bp + SL::flag);
@@ -389,7 +391,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                              : r == 16 || r == 17 ? (uint32_t)kItemReaders
                              : r == 19 ? 2u                   // mma_done: both MMA threads
                              : r == 20 ? 8u                   // tiles_done: every softmax warp
-                             : r == 21 ? 4u                   // rows_left: tile 1's
                                        : 1u;
       dev::mbar_init(bars + 8u * i, count);
     }
@@ -759,48 +760,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       if constexpr (kPaged) {
-        // This tile's (max, sum, unnormalised O) joined with the other's, which has the same
-        // rows: tile 1 leaves its own in shared memory (the rings are done with once both
-        // tiles' MMAs are), tile 0 adds it to its own and leaves the sum there.
-        float *const row_o = reinterpret_cast<float *>(bp + SL::rows + r * D * 4);
-        float2 *const ml = reinterpret_cast<float2 *>(bp + SL::ml) + r;
+        // This tile's rows (max, sum, unnormalised O) into shared memory for the cluster's
+        // merge: the rings are done with once both tiles' MMAs are.
         __syncwarp();
         if (lane == 0) dev::mbar_arrive(tiles_done);
         ok = __all_sync(0xffffffffu, dev::mbar_wait(tiles_done, 0)) && ok;
-        const float m1 = nb > 0 ? m_ref : -INFINITY;
-        if (t == 1) *ml = make_float2(m1, nb > 0 ? lsum : 0.f);
-        float w0 = 1.f, w1 = 0.f;
-        if (t == 0) {
-          ok = __all_sync(0xffffffffu, dev::mbar_wait(rows_left, 0)) && ok;
-          const float2 o = *ml;
-          const float m = fmaxf(m1, o.x);
-          w0 = m == -INFINITY ? 1.f : dev::ex2(m1 - m);
-          w1 = m == -INFINITY ? 0.f : dev::ex2(o.x - m);
-          lsum = (nb > 0 ? lsum : 0.f) * w0 + o.y * w1;
-          m_ref = m;
-        }
-        const bool other = t == 0 && __any_sync(0xffffffffu, it.nb1 > 0);
-#pragma unroll 1
+        if (!ok && lane == 0) fail(false);
+        reinterpret_cast<float2 *>(bp + SL::ml)[t * kTcRows + r] =
+            nb > 0 && ok ? make_float2(m_ref, lsum) : make_float2(-INFINITY, 0.f);
+        float4 *const row_o = reinterpret_cast<float4 *>(bp + SL::rows + (t * kTcRows + r) * D * 4);
+#pragma unroll 2
         for (int ch = 0; ch < D / 32 && nb > 0 && ok; ++ch) {
           uint32_t o[32];
           dev::tmem_ld32(ob + ch * 32, o);
           dev::tmem_wait_ld();
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            float4 *const at = reinterpret_cast<float4 *>(row_o) + ((ch * 8 + u) ^ (r & 7));
-            float4 x = make_float4(__uint_as_float(o[4 * u]) * w0, __uint_as_float(o[4 * u + 1]) * w0,
-                                   __uint_as_float(o[4 * u + 2]) * w0, __uint_as_float(o[4 * u + 3]) * w0);
-            if (other) {
-              const float4 y = *at;
-              x.x += y.x * w1, x.y += y.y * w1, x.z += y.z * w1, x.w += y.w * w1;
-            }
-            *at = x;
-          }
+          for (int u = 0; u < 8; ++u)
+            row_o[(ch * 8 + u) ^ (r & 7)] =
+                make_float4(__uint_as_float(o[4 * u]), __uint_as_float(o[4 * u + 1]),
+                            __uint_as_float(o[4 * u + 2]), __uint_as_float(o[4 * u + 3]));
         }
-        __syncwarp();
-        if (t == 1 && lane == 0) dev::mbar_arrive(rows_left);
-        if (!ok && lane == 0) fail(false);
-        if (t == 0) *ml = make_float2(m_ref, lsum);
       } else if (nb > 0) {
         const float inv = 1.f / lsum;
         uint4 *dst = reinterpret_cast<uint4 *>(a.out + token * a.out_stride + (int64_t)(it.g * G + h) * D);
@@ -835,38 +814,42 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (tid == 0) (void)dev::mbar_wait(mma_done, 0);
   __syncthreads();
   if constexpr (kPaged) {
-    // The cluster's merge: every CTA reads its share of the rows from all of them.  Each
-    // thread arrives after bounded waits only, so both barriers complete; the second keeps
-    // every CTA until its rows have been read.
-    if (!have && tid < kTcRows)
+    // The cluster's merge: every CTA reads its share of the rows, both tiles' of every CTA,
+    // one 16-byte chunk per thread with all its loads in flight.  Each thread arrives after
+    // bounded waits only, so both barriers complete; the second keeps every CTA until its
+    // rows have been read.
+    if (!have && tid < 2 * kTcRows)
       reinterpret_cast<float2 *>(bp + SL::ml)[tid] = make_float2(-INFINITY, 0.f);
     const int n = (int)dev::cluster_nctarank(), rank = (int)dev::cluster_ctarank();
     dev::cluster_arrive_release();
     dev::cluster_wait();
-    const int share = (tile_rows + n - 1) / n;
-    for (int r = rank * share + warp; r < min((rank + 1) * share, tile_rows); r += kTileThreads / 32) {
+    const int share = (tile_rows + n - 1) / n, row_end = min((rank + 1) * share, tile_rows);
+    const int c16 = tid % (D / 4);
+#pragma unroll 2
+    for (int r = rank * share + tid / (D / 4); r < row_end; r += kTileThreads / (D / 4)) {
       const int tok = r / G, h = r - tok * G;
       const int qi = first.tok0 + tok;
       if (qi >= first.n) break;
-      float2 ml[kMaxCluster];
-      float4 o[kMaxCluster];
+      float2 ml[2 * kMaxCluster];
+      float4 o[2 * kMaxCluster];
       float m = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < kMaxCluster; ++c) {
+      for (int c = 0; c < 2 * kMaxCluster; ++c) {
         ml[c] = make_float2(-INFINITY, 0.f);
         o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c < n) {
-          ml[c] = dev::ld_cluster_f2(dev::mapa(base + SL::ml + r * 8, c));
-          if (lane < D / 4)
-            o[c] = dev::ld_cluster_f4(dev::mapa(base + SL::rows + r * D * 4 + ((lane ^ (r & 7)) << 4), c));
+        if ((c >> 1) < n) {
+          const uint32_t rr = (uint32_t)((c & 1) * kTcRows + r);
+          ml[c] = dev::ld_cluster_f2(dev::mapa(base + SL::ml + rr * 8, c >> 1));
+          o[c] = dev::ld_cluster_f4(dev::mapa(base + SL::rows + rr * (D * 4) + ((c16 ^ (r & 7)) << 4), c >> 1));
         }
-        m = fmaxf(m, ml[c].x);
       }
+#pragma unroll
+      for (int c = 0; c < 2 * kMaxCluster; ++c) m = fmaxf(m, ml[c].x);
       float l = 0.f;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int c = 0; c < kMaxCluster; ++c) {
-        if (ml[c].x == -INFINITY && ml[c].y == 0.f) continue;  // no key seen there: nothing written
+      for (int c = 0; c < 2 * kMaxCluster; ++c) {
+        if (ml[c].x == -INFINITY && ml[c].y == 0.f) continue;  // no key seen there: no row either
         const float w = dev::ex2(ml[c].x - m);
         l += w * ml[c].y;
         x.x += w * o[c].x, x.y += w * o[c].y, x.z += w * o[c].z, x.w += w * o[c].w;
@@ -875,12 +858,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const float inv = any ? 1.f / l : 0.f;
       const int64_t row = ((int64_t)(first.first + qi) * a.num_q_heads + first.g * G + h) * a.n_rows +
                           blockIdx.y / n;
-      if (lane < D / 4)
-        reinterpret_cast<float4 *>(a.o_part + row * D)[lane] =
-            make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-      if (lane == 0) a.lse_part[row] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+      reinterpret_cast<float4 *>(a.o_part + row * D)[c16] =
+          make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+      if (c16 == 0) a.lse_part[row] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
-    dev::cluster_arrive_release();
+    dev::cluster_arrive_relaxed();  // nothing to publish: the loads above have returned
     dev::cluster_wait();
   }
   if ((warp == kProducer || warp == kProducerV) && lane == 0 && *s_flag) {
