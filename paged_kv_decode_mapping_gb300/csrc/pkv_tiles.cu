@@ -61,8 +61,10 @@ struct TileArgs {
   float *o_part, *lse_part; // [B][Hq][n_rows][D], [B][Hq][n_rows]; row s: the s-th cluster of splits
 };
 
-constexpr int kTileThreads = 32 * 12;  // 8 softmax warps, the K and V producers, an MMA warp per tile
-constexpr int kItemReaders = 11;       // warps that read an item: all but the K producer
+// 8 softmax warps, the K and the V producer (two warps a ring measured neutral), an MMA warp per
+// tile.
+constexpr int kTileThreads = 32 * 12;
+constexpr int kItemReaders = 11;  // kPrompt's warps that read an item: all but the K producer
 
 // One piece of work, handed from the K producer to the other warps.
 struct TileItem {
@@ -79,8 +81,8 @@ struct TileSmem {
   // K and V ring stages.  kPrefix: even, so that a stage serves one tile alone (block j is
   // tile j & 1's): a waiter may trust a barrier's parity only if it saw the phase before,
   // and a tile's MMA thread sees the phases of its own blocks.
-  static constexpr int KSK = D == 64 ? 4 : (MODE == kPrompt ? 2 : 4);
-  static constexpr int KSV = D == 64 ? 4 : 2;
+  static constexpr int KSK = D == 64 ? 4 : 2;
+  static constexpr int KSV = D == 64 ? 4 : (MODE == kPrompt ? 2 : 4);
   static_assert(MODE == kPrompt || (KSK % 2 == 0 && KSV % 2 == 0), "one tile per stage");
   static constexpr uint32_t kSub = kTcKeys * 128;     // 128 rows x 128 B (64 dims)
   static constexpr uint32_t kTile = kSub * (D / 64);
@@ -95,11 +97,11 @@ struct TileSmem {
   static constexpr uint32_t item = ones + (kOnes ? kSub : 0);  // two items
   static constexpr uint32_t clc = item + 2 * sizeof(TileItem); // a launch-control answer, 16 B
   // kPrefix, once the rings are done with: the tiles' rows [2][128][D] fp32, row r's 16-byte
-  // chunk c at c ^ (r & 7), in the K ring; (max in base 2, sum) per row in the V ring
+  // chunk c at c ^ (r & 7), where the rings begin; (max in base 2, sum) per row at their end
   static constexpr uint32_t rows = 0;
-  static constexpr uint32_t ml = v;
+  static constexpr uint32_t ml = q - 2 * kTcRows * 8;
   static constexpr uint32_t bars = clc + 16;
-  static_assert(MODE == kPrompt || 2u * kTcRows * D * 4 <= KSK * kTile, "both tiles' rows fit the K ring");
+  static_assert(MODE == kPrompt || rows + 2u * kTcRows * D * 4 <= ml, "the rows fit the rings");
   // the rings, then s_full, pv_done per tile, p_half per tile and half, q_full, q_free, o_free
   // per tile, item_full, item_empty per slot, clc_full, mma_done, tiles_done
   static constexpr int kRings = 2 * KSK + 2 * KSV;
@@ -216,7 +218,8 @@ __device__ __forceinline__ bool make_item(const TileArgs &a, unsigned cta_x, uns
 }
 
 // Loads keys [k0, k0 + nk) of kv head g from the group's pages into a block tile
-// [D/64][128][128 B], one TMA box of min(block_size, 64) rows per lane, completing on `bar`.
+// [D/64][128][128 B], one TMA box of min(block_size, 64) rows and 64 dims per lane, completing
+// on `bar`.
 template <int D, uint32_t SUB>
 __device__ __forceinline__ void load_paged_block(const CUtensorMap *tm, uint32_t dst, uint32_t bar,
                                                  int k0, int nk, int &win, int &tb,
@@ -425,6 +428,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   };
   // Copies `it` number `items` (of the reading warp's count) out of its slot.
   auto next_item = [&](int items, TileItem &x) {
+    if constexpr (kPaged) return items == 0 && have;  // every warp found its CTA's one item
     const int s = items & 1;
     if (!__all_sync(0xffffffffu, dev::mbar_wait(item_full(s), (items >> 1) & 1))) {
       if (lane == 0) fail(false);
@@ -437,9 +441,54 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   };
   int issued = 0;  // producers: blocks loaded
 
-  if (warp == kProducer) {
-    // ------------------------------------------------- items, Q tiles and the K ring
+  // Loads this warp's part of the item's K or V blocks into its ring; `issued` runs on.
+  auto load_ring = [&](bool is_k, const TileItem &x) {
+    const CUtensorMap *const tm = is_k ? &tmk : &tmv;
+    const int ks = is_k ? KSK : KSV;
     const uint64_t policy = dev::policy_evict_last();  // other CTAs read the same keys
+    const int nblk = (x.t_end - x.key0 + kTcKeys - 1) / kTcKeys;
+    const int32_t *const trow = kPaged ? a.block_tables + (int64_t)x.first * a.max_blocks : nullptr;
+    const int lb_last = kPaged ? (x.t_end - 1) >> a.log2_bs : 0;
+    int win = kPaged ? x.key0 >> a.log2_bs : 0;
+    int tb = kPaged && win + lane <= lb_last ? __ldg(trow + win + lane) : 0;
+    for (int j = 0; j < nblk; ++j, ++issued) {
+      const int s = issued % ks;
+      const uint32_t full = is_k ? k_full(s) : v_full(s), empty = is_k ? k_empty(s) : v_empty(s);
+      if (issued >= ks && !__all_sync(0xffffffffu, dev::mbar_wait(empty, ((issued / ks) - 1) & 1))) {
+        if (lane == 0) fail(false);
+        return false;
+      }
+      const uint32_t dst = base + (is_k ? SL::k : SL::v) + s * SL::kTile;
+      if constexpr (kPaged)
+        load_paged_block<D, SL::kSub>(tm, dst, full, x.key0 + j * kTcKeys,
+                                          min(kTcKeys, x.t_end - x.key0 - j * kTcKeys), win, tb, trow,
+                                          lb_last, a, x.g, lane, policy);
+      else if (lane == 0)
+        load_packed_block(tm, dst, full, SL::kTile, x.first + j * kTcKeys, x.g, policy);
+    }
+    return true;
+  };
+  auto load_q = [&](int t, const TileItem &x) {  // one lane
+    dev::mbar_arrive_expect_tx(q_full(t), (uint32_t)tile_rows * 128u * (D / 64));
+#pragma unroll
+    for (int hh = 0; hh < D / 64; ++hh)
+      asm volatile(
+          "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+          " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(base + SL::q + t * SL::kTile + hh * SL::kSub),
+          "l"(reinterpret_cast<uint64_t>(&tmq)), "r"(hh * 64), "r"(x.g * G),
+          "r"(x.first + x.tok0 + t * a.tile_tokens), "r"(q_full(t))
+          : "memory");
+  };
+
+  if (warp >= kProducer && warp < kMma && kPaged) {
+    // ------------------------------------------------- the Q tile, the K and V rings
+    if (have) {
+      if (warp == kProducer && lane == 0) load_q(0, it);
+      __syncwarp();
+      (void)load_ring(warp == kProducer, it);
+    }
+  } else if (warp == kProducer) {
+    // ------------------------------------------------- items, Q tiles and the K ring
     int items = 0, asked = 0, qn[2] = {0, 0};
     bool ok = true;
     auto publish = [&](const TileItem &x) {
@@ -457,54 +506,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       return true;
     };
     while (true) {
-      if (kShareKeys && lane == 0) {  // the next item, while this one's copies are issued
+      if (lane == 0) {  // the next item, while this one's copies are issued
         dev::fence_proxy_async_smem();
         dev::mbar_arrive_expect_tx(clc_full, 16);
         clc_try_cancel(base + SL::clc, clc_full);
       }
       if (have && (ok = publish(it))) {
 #pragma unroll
-        for (int t = 0; t < SL::kQ; ++t) {
+        for (int t = 0; t < 2; ++t) {
           if ((t ? it.nb1 : it.nb0) == 0) continue;
           if (qn[t] > 0 && !(ok = __all_sync(0xffffffffu, dev::mbar_wait(q_free(t), (qn[t] - 1) & 1)))) {
             if (lane == 0) fail(false);
             break;
           }
           ++qn[t];
-          if (lane == 0) {
-            dev::mbar_arrive_expect_tx(q_full(t), (uint32_t)tile_rows * 128u * (D / 64));
-#pragma unroll
-            for (int hh = 0; hh < D / 64; ++hh)
-              asm volatile(
-                  "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                  " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(base + SL::q + t * SL::kTile + hh * SL::kSub),
-                  "l"(reinterpret_cast<uint64_t>(&tmq)), "r"(hh * 64), "r"(it.g * G),
-                  "r"(it.first + it.tok0 + t * a.tile_tokens), "r"(q_full(t))
-                  : "memory");
-          }
+          if (lane == 0) load_q(t, it);
         }
-        const int nblk = (it.t_end - it.key0 + kTcKeys - 1) / kTcKeys;
-        const int32_t *const trow = kPaged ? a.block_tables + (int64_t)it.first * a.max_blocks : nullptr;
-        const int lb_last = kPaged ? (it.t_end - 1) >> a.log2_bs : 0;
-        int win = kPaged ? it.key0 >> a.log2_bs : 0;
-        int tb = kPaged && win + lane <= lb_last ? __ldg(trow + win + lane) : 0;
-        for (int j = 0; ok && j < nblk; ++j, ++issued) {
-          const int s = issued % KSK;
-          if (issued >= KSK &&
-              !(ok = __all_sync(0xffffffffu, dev::mbar_wait(k_empty(s), ((issued / KSK) - 1) & 1)))) {
-            if (lane == 0) fail(false);
-            break;
-          }
-          const uint32_t dst = base + SL::k + s * SL::kTile;
-          if constexpr (kPaged)
-            load_paged_block<D, SL::kSub>(&tmk, dst, k_full(s), it.key0 + j * kTcKeys,
-                                          min(kTcKeys, it.t_end - it.key0 - j * kTcKeys), win, tb,
-                                          trow, lb_last, a, it.g, lane, policy);
-          else if (lane == 0)
-            load_packed_block(&tmk, dst, k_full(s), SL::kTile, it.first + j * kTcKeys, it.g, policy);
-        }
+        ok = ok && load_ring(true, it);
       }
-      if constexpr (!kShareKeys) break;
       // always answered before the CTA may leave
       if (!__all_sync(0xffffffffu, dev::mbar_wait(clc_full, asked & 1))) {
         if (lane == 0) fail(false);
@@ -520,30 +539,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     (void)publish(it);
   } else if (warp == kProducerV) {
     // ------------------------------------------------- the V ring
-    const uint64_t policy = dev::policy_evict_last();
-    bool ok = true;
-    for (int items = 0; ok && next_item(items, it); ++items) {
-      const int nblk = (it.t_end - it.key0 + kTcKeys - 1) / kTcKeys;
-      const int32_t *const trow = kPaged ? a.block_tables + (int64_t)it.first * a.max_blocks : nullptr;
-      const int lb_last = kPaged ? (it.t_end - 1) >> a.log2_bs : 0;
-      int win = kPaged ? it.key0 >> a.log2_bs : 0;
-      int tb = kPaged && win + lane <= lb_last ? __ldg(trow + win + lane) : 0;
-      for (int j = 0; j < nblk; ++j, ++issued) {
-        const int s = issued % KSV;
-        if (issued >= KSV &&
-            !(ok = __all_sync(0xffffffffu, dev::mbar_wait(v_empty(s), ((issued / KSV) - 1) & 1)))) {
-          if (lane == 0) fail(false);
-          break;
-        }
-        const uint32_t dst = base + SL::v + s * SL::kTile;
-        if constexpr (kPaged)
-          load_paged_block<D, SL::kSub>(&tmv, dst, v_full(s), it.key0 + j * kTcKeys,
-                                        min(kTcKeys, it.t_end - it.key0 - j * kTcKeys), win, tb, trow,
-                                        lb_last, a, it.g, lane, policy);
-        else if (lane == 0)
-          load_packed_block(&tmv, dst, v_full(s), SL::kTile, it.first + j * kTcKeys, it.g, policy);
-      }
-    }
+    for (int items = 0; next_item(items, it); ++items)
+      if (!load_ring(false, it)) break;
   } else if (warp >= kMma) {
     // ------------------------------------- tensor-core issue, one thread for each tile:
     // what one of them does between its MMAs (waits, commits) runs under the other's.  They
@@ -865,12 +862,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     dev::cluster_arrive_relaxed();  // nothing to publish: the loads above have returned
     dev::cluster_wait();
   }
-  if ((warp == kProducer || warp == kProducerV) && lane == 0 && *s_flag) {
-    const int ks = warp == kProducer ? KSK : KSV;
+  if (warp >= kProducer && warp < kMma && lane == 0 && *s_flag) {
+    const int ks = warp < kProducerV ? KSK : KSV;
     for (int s = 0; s < ks; ++s) {
       const int last = s + ((issued - 1 - s) / ks) * ks;  // the last block on stage s
       if (last >= 0 && last < issued)
-        (void)dev::mbar_wait(warp == kProducer ? k_full(s) : v_full(s), (last / ks) & 1);
+        (void)dev::mbar_wait(warp < kProducerV ? k_full(s) : v_full(s), (last / ks) & 1);
     }
   }
   dev::tc_fence_before();
