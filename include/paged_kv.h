@@ -301,11 +301,17 @@ int paged_decode_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k_c
  *
  * max_prefix_len >= every prefix_lens[g], and max_suffix_len >= every context_lens[b] less
  * the whole pages of its group's prefix; both are at most max_blocks_per_seq * block_size.
- * A longer one is cut there and raises PKV_DEVERR_CONTEXT_LEN, like a group that is
- * misplaced.  Layouts, supported sizes, alignment, and the rules for the workspace
- * (zero-filled before its first use, left ready by every call, not shared by calls that
- * overlap; paged_decode_shared_prefix_workspace_size() bytes) are those of
+ * A longer one is cut there, a group that begins inside the one before it or leaves the
+ * batch is moved or cut, and PKV_DEVERR_CONTEXT_LEN is raised.  Layouts, supported sizes,
+ * alignment, and the rules for the workspace (zero-filled before its first use, left ready
+ * by every call for the next one with as many sequences and kv heads, not shared by calls
+ * that overlap; paged_decode_shared_prefix_workspace_size() bytes) are those of
  * paged_decode_attention.  All arguments are DEVICE memory.
+ *
+ * Two launches: the prefixes as matrix products on the tensor cores, and beside them, as a
+ * programmatic dependent, every sequence's own keys and the log-sum-exp merge.  Where too
+ * little would be read twice for that to pay (about 40 MB: see pkv_set_shared_prefix), the
+ * call is paged_decode_attention's one launch, and the groups are not looked at.
  */
 size_t paged_decode_shared_prefix_workspace_size(int32_t num_seqs, int32_t num_q_heads,
                                                  int32_t num_kv_heads, int32_t head_dim,
@@ -318,6 +324,15 @@ int paged_decode_shared_prefix_attention(
     int32_t max_prefix_len, int32_t max_suffix_len, int32_t num_seqs, int32_t num_q_heads,
     const pkv_cache_desc *cache, float scale, void *workspace, size_t workspace_bytes,
     void *stream);
+
+/*
+ * pkv_set_shared_prefix -- whether paged_decode_shared_prefix_attention shares, process-wide:
+ *   PKV_SHARED_AUTO (default): where it pays, by the sizes;
+ *   PKV_SHARED_ALWAYS, PKV_SHARED_NEVER: so that the two can be measured against each other.
+ * Returns the previous mode, or PKV_ERR_UNSUPPORTED for an unknown one.  Host function.
+ */
+enum { PKV_SHARED_AUTO = 0, PKV_SHARED_ALWAYS = 1, PKV_SHARED_NEVER = 2 };
+int32_t pkv_set_shared_prefix(int32_t mode);
 
 /*
  * paged_decode_step -- one whole decode step: paged_kv_write(k, v, slot_mapping,

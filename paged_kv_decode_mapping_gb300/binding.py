@@ -72,6 +72,8 @@ _lib.paged_decode_split_workspace_size.restype = _sz
 _lib.paged_decode_attention.argtypes = [_P, _P, _P, _P, _P, _i32, _P, _i32, _i32, _i32, _D, _f32,
                                         _P, _sz, _P]
 _lib.paged_decode_attention.restype = ctypes.c_int
+_lib.pkv_set_shared_prefix.argtypes = [_i32]
+_lib.pkv_set_shared_prefix.restype = _i32
 _lib.paged_decode_shared_prefix_workspace_size.argtypes = [_i32] * 7
 _lib.paged_decode_shared_prefix_workspace_size.restype = _sz
 _lib.paged_decode_shared_prefix_attention.argtypes = [_P, _P, _P, _P, _P, _i32, _P, _P, _P, _i32,
@@ -398,6 +400,17 @@ def paged_decode_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Te
                                        _ptr(context_lens), int(max_context_len), B, Hq,
                                        ctypes.byref(d), float(scale), _ptr(workspace), ws_bytes,
                                        _stream(stream)), "paged_decode_attention")
+
+
+SHARED_AUTO, SHARED_ALWAYS, SHARED_NEVER = 0, 1, 2
+
+
+def pkv_set_shared_prefix(mode: int) -> int:
+    """Whether paged_decode_shared_prefix_attention shares (SHARED_*); returns the previous mode."""
+    rc = int(_lib.pkv_set_shared_prefix(mode))
+    if rc < 0:
+        _check(rc, "pkv_set_shared_prefix")
+    return rc
 
 
 def paged_decode_shared_prefix_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,

@@ -118,18 +118,18 @@ cudaError_t read_tile_errors(uint32_t *flags, int clear);
 cudaError_t read_shared_errors(uint32_t *flags, int clear);
 
 // The shared-prefix half of paged_decode_shared_prefix_attention (pkv_tiles.cu): the
-// partial results of splits s * cluster .. (s + 1) * cluster - 1 of every query row of the
-// groups, in row s of o_part [B][Hq][n_rows][D] and lse_part [B][Hq][n_rows].  Arguments
-// already checked; splits is a multiple of cluster <= kPrefixCluster.
+// partial results of split s of every query row of the groups, in row s of o_part
+// [B][Hq][n_rows][D] and lse_part [B][Hq][n_rows].  Arguments already checked.
 constexpr int kTileRows = 128;  // query rows of a tile
 constexpr int kTileKeys = 128;  // keys per block
-constexpr int kPrefixCluster = 4;
+struct SharedCut;
 struct PrefixLaunch {
   const pkv_bf16 *q;
   const int32_t *block_tables, *context_lens, *group_start, *prefix_lens;
   float *o_part, *lse_part;
-  int32_t num_seqs, num_groups, max_blocks, max_prefix, num_q_heads;
-  int32_t split_keys, splits, cluster, n_rows;
+  int32_t num_seqs, num_groups, num_q_heads;
+  int32_t split_keys, splits;
+  const SharedCut *cut;
   int64_t tiles;  // row tiles over all groups, at most
   float scale;
 };
@@ -271,6 +271,17 @@ __device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t *p, uint32_t v) 
   return old;
 }
 
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t *p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// Atomic add with release semantics at GPU scope, nothing returned.
+__device__ __forceinline__ void red_add_release(uint32_t *p, uint32_t v) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
 // Plain bulk copy of `bytes` (a multiple of 16; both addresses 16-byte aligned) from
 // global into shared memory, completing on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
@@ -303,25 +314,8 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_arrive_relaxed() {
   asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
 }
-__device__ __forceinline__ void cluster_arrive_release() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-}
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-// Loads from a shared::cluster address (another CTA's shared memory, or this one's).
-__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
 }
 // Stores v at shared::cluster address `addr` (in another CTA of the cluster, or this
 // one) and, once written, counts its 4 bytes off the transaction count of the mbarrier

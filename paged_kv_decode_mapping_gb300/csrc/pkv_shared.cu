@@ -6,16 +6,20 @@
 // The prefix half is a matrix product: the group's query rows (sequence, head of the kv
 // head's group) against the prefix's keys, each page read once for up to 128 rows
 // (pkv_tiles.cu); its splits leave (o, lse) partials.  The other half, tail_kernel below,
-// streams each sequence's own keys like the decode kernel does, and merges.  It is a
-// programmatic dependent of the first: its CTAs fill the SMs as the prefix's leave them,
-// and wait for the prefix's partials only before they merge.
+// streams each sequence's own keys like the decode kernel does.  It is a programmatic
+// dependent of the first, so that its CTAs run beside the prefix's, on the SMs these leave,
+// and only store their parts.  Its last CTAs merge, a warp for a few heads of a sequence: they wait
+// for the prefix's grid and for the sequence's own parts.  (Merged by whichever part came
+// last, by tickets, the last tile CTA of a group had 126 rows to merge alone, 7 us; merged by
+// each tail CTA after waiting for the prefix, the tail held its SMs until the prefix was done.)
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
-#include "decode_device.cuh"
+#include "shared_device.cuh"
 
 namespace pkv {
 
@@ -28,81 +32,25 @@ struct TailArgs {
   float *o_part;                // [B][Hq][n_rows][D]: the prefix's rows, then the tail's
   float *lse_part;              // [B][Hq][n_rows]
   uint16_t *out;                // [B][Hq][D]
-  uint32_t *counters;           // [B][Hkv] tail partitions finished; zero between calls
+  uint32_t *counters;           // [B][Hkv] own parts stored, then runs merged; zero between calls
   int64_t num_blocks;
-  int32_t max_blocks, num_groups, max_prefix, max_suffix, num_q_heads, num_kv_heads, group;
-  int32_t block_size, log2_bs, box_rows, partition_tokens, n_rows;
-  int32_t row_keys;             // prefix keys behind one of its rows
+  int32_t num_seqs, num_groups, num_q_heads, num_kv_heads, group, box_rows;
+  int32_t parts, tail_ctas;     // own parts at most; CTAs ahead of the merging ones
+  int32_t merge_heads;          // heads a merging warp takes at a time
+  int32_t sorted;               // the longest tails first (num_seqs <= kSortSeqs)
   float scale_log2;
+  SharedCut cut;
 };
 
-// The n partition results of one query head (rows of o_rows and lse_rows, as merge_rows
-// takes them) and the CTA's own result (normalised own[v], base-2 own_lse; -inf: none) into
-// bf16 dst[0 .. D).  One warp; 16 rows in flight.  Nothing at all gives zeros.
-template <int D>
-__device__ __forceinline__ void merge_rows_own(uint16_t *dst, const float *o_rows,
-                                               const float *lse_rows, int n, int lane,
-                                               const float (&own)[D / 32], float own_lse) {
-  constexpr int VPL = D / 32, kFly = 16;
-  float M = own_lse, den = own_lse == -INFINITY ? 0.f : 1.f, acc[VPL];
-#pragma unroll
-  for (int v = 0; v < VPL; ++v) acc[v] = own_lse == -INFINITY ? 0.f : own[v];
-  for (int k0 = 0; k0 < n; k0 += kFly) {
-    float lk[kFly], ov[kFly][VPL];
-#pragma unroll
-    for (int u = 0; u < kFly; ++u) {
-      const int k = k0 + u;
-      lk[u] = -INFINITY;
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) ov[u][v] = 0.f;
-      if (k < n) {
-        lk[u] = __ldcg(lse_rows + k) * kLog2e;
-        const float *src = o_rows + (int64_t)k * D + lane * VPL;
-        if constexpr (VPL == 2) {
-          const float2 t = __ldcg(reinterpret_cast<const float2 *>(src));
-          ov[u][0] = t.x;
-          ov[u][1] = t.y;
-        } else {
-          const float4 t = __ldcg(reinterpret_cast<const float4 *>(src));
-          ov[u][0] = t.x;
-          ov[u][1] = t.y;
-          ov[u][2] = t.z;
-          ov[u][3] = t.w;
-        }
-      }
-    }
-    float mb = lk[0];
-#pragma unroll
-    for (int u = 1; u < kFly; ++u) mb = fmaxf(mb, lk[u]);
-    const float Mn = fmaxf(M, mb);
-    if (Mn == -INFINITY) continue;  // rows without keys only, so far
-    const float sc = dev::ex2(M - Mn);
-    den *= sc;
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) acc[v] *= sc;
-#pragma unroll
-    for (int u = 0; u < kFly; ++u) {
-      const float wt = dev::ex2(lk[u] - Mn);
-      den += wt;
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) acc[v] += wt * ov[u][v];
-    }
-    M = Mn;
-  }
-  const float inv = den == 0.f ? 0.f : 1.f / den;
-  uint16_t *d = dst + lane * VPL;
-  if constexpr (VPL == 2) {
-    *reinterpret_cast<uint32_t *>(d) = dev::pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  } else {
-    *reinterpret_cast<uint2 *>(d) = make_uint2(dev::pack_bf16x2(acc[0] * inv, acc[1] * inv),
-                                              dev::pack_bf16x2(acc[2] * inv, acc[3] * inv));
-  }
-}
+constexpr int kSortSeqs = kThreads;  // one sequence per thread
 
 // One CTA per (sequence, kv head, partition of P tokens of the sequence's own keys): the
-// decode kernel's producer ring and consumer warps from the first key past the prefix.
-// The CTA of a sequence held whole, or the last of its partitions to finish (an atomic
-// ticket; nobody waits), merges the prefix's and the tail's results.
+// decode kernel's producer ring and consumer warps from the first key past the prefix; then
+// the CTAs that merge.  These are fewer than the CTAs that fit at once, so that they cannot
+// keep out the ones they wait for, and every wait is bounded.
+//
+// With more CTAs than fit at once the longest sequences go first, so that none of them starts
+// when the others end (64 sequences of 1 to 1024 own keys: SORTUS).
 template <int D, int STAGES>
 __global__ void __launch_bounds__(kThreads, split_occupancy(D))
     tail_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -118,44 +66,113 @@ __global__ void __launch_bounds__(kThreads, split_occupancy(D))
   const uint32_t bar_empty = bar_full + STAGES * 8;
   volatile int *const s_flag =
       reinterpret_cast<volatile int *>(base_ptr + STAGES * kStageBytes + STAGES * 16);
-  volatile int *const s_last = s_flag + 1;
   uint8_t *const q_area = base_ptr + STAGES * kStageBytes + STAGES * 16 + 16;
 
-  const int part = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ __align__(16) uint32_t s_tail[kSortSeqs];
+  __shared__ int s_pick[3];
+  // Length and prefix of sequence `seq`, the same or (each) another one per lane; whole warps.
+  auto sizes = [&](int seq, bool each, int &L, int &skip) {
+    const int given = seq < a.num_seqs ? __ldg(a.context_lens + seq) : 0;
+    skip = 0;
+    for (int c = 0, carry = 0; c < a.num_groups; c += 32) {
+      int s, len;
+      const int p = c + lane < a.num_groups ? __ldg(a.prefix_lens + c + lane) : 0;
+      disjoint_group(a.group_start, a.num_groups, a.num_seqs, a.num_seqs, c, lane, carry, s, len);
+      // the groups that hold it, or (each) all of them in turn
+      unsigned look = __ballot_sync(0xffffffffu, each ? c + lane < a.num_groups : s <= seq && seq < s + len);
+      for (; look; look &= look - 1) {
+        const int i = __ffs(look) - 1;
+        const int si = __shfl_sync(0xffffffffu, s, i), li = __shfl_sync(0xffffffffu, len, i);
+        const int pi = __shfl_sync(0xffffffffu, p, i);
+        if (si <= seq && seq < si + li) skip = shared_pages(a.cut, pi);
+      }
+    }
+    L = shared_len(a.cut, given, skip);
+    return L == given;
+  };
+  if ((int)blockIdx.x >= a.tail_ctas) {
+    // ------------------------------------------------------------- merging CTAs
+    const int first = ((int)blockIdx.x - a.tail_ctas) * (kThreads / 32) + warp;
+    const int step = ((int)gridDim.x - a.tail_ctas) * (kThreads / 32);
+    bool waited = false;
+    const int runs = (a.group + a.merge_heads - 1) / a.merge_heads;  // runs of heads in a unit
+    for (int64_t task = first; task < (int64_t)a.num_seqs * a.num_kv_heads * runs; task += step) {
+      const int unit = (int)(task / runs), h0 = (int)(task % runs) * a.merge_heads;
+      const int heads = min(a.merge_heads, a.group - h0);
+      const int seq = unit / a.num_kv_heads, g = unit - seq * a.num_kv_heads;
+      int L, skip;
+      (void)sizes(seq, false, L, skip);
+      const int n_tail = own_rows(a.cut, L, skip), n = prefix_rows(a.cut, skip) + n_tail;
+      const int64_t row = (int64_t)seq * a.num_q_heads + g * a.group + h0;
+      if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the prefix's rows
+      waited = true;
+      uint32_t *const counter = a.counters + unit;
+      if (n_tail > 0 && dev::ld_acquire(counter) < (unsigned)n_tail) {
+        const uint64_t t0 = dev::globaltimer_ns();
+        uint32_t tries = 0;
+        while (dev::ld_acquire(counter) < (unsigned)n_tail)
+          if ((++tries & 63u) == 0 && dev::globaltimer_ns() - t0 > 2000000000ull) {
+            raise_error(PKV_DEVERR_TIMEOUT);
+            break;
+          }
+      }
+      __syncwarp();
+      uint16_t *const dst = a.out + row * D;
+      const float *const o = a.o_part + row * a.cut.n_rows * D, *const lse = a.lse_part + row * a.cut.n_rows;
+      if (heads > 1 && n <= 32)
+        merge_heads<D>(dst, o, lse, heads, a.cut.n_rows, n, lane);
+      else
+        for (int h = 0; h < heads; ++h)
+          merge_partials<D>(dst + h * D, o + (int64_t)h * a.cut.n_rows * D, lse + h * a.cut.n_rows, n, lane);
+      // the unit's last run to be merged leaves its counter ready for the next call
+      if (n_tail > 0 && lane == 0 && atomicAdd(counter, 1u) + 1 == (unsigned)(n_tail + runs)) *counter = 0u;
+    }
+    // (Every warp here waits for the prefix's grid, so this one does not end before it.)
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  const int part = (int)blockIdx.x % a.parts, g = (int)blockIdx.x / a.parts % a.num_kv_heads;
+  int b = (int)blockIdx.x / (a.parts * a.num_kv_heads), L, skip;
+  bool good;
+  if (a.sorted) {  // the b-th longest tail
+    good = sizes(tid, true, L, skip);
+    // one key each: the chunks, then the first of equals; past the last sequence the least
+    const uint32_t mine = tid < a.num_seqs
+        ? (uint32_t)min((max(L - skip, 0) + kChunk - 1) / kChunk, 0x7fffff) << 8 | (255u - tid)
+        : 0u;
+    s_tail[tid] = mine;
+    __syncthreads();
+    if (tid < a.num_seqs) {
+      int rank = 0;
+#pragma unroll 4
+      for (int i = 0; i < a.num_seqs; i += 4) {
+        const uint4 k = *reinterpret_cast<const uint4 *>(s_tail + i);
+        rank += (k.x > mine) + (k.y > mine) + (k.z > mine) + (k.w > mine);
+      }
+      if (rank == b) {
+        s_pick[0] = tid;
+        s_pick[1] = L;
+        s_pick[2] = skip;
+        if (!good && part == 0 && g == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
+      }
+    }
+    __syncthreads();
+    b = s_pick[0];
+    L = s_pick[1];
+    skip = s_pick[2];
+  } else {
+    good = sizes(b, false, L, skip);
+    if (!good && tid == 0 && part == 0 && g == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
+  }
   const int64_t head0 = (int64_t)b * a.num_q_heads + g * a.group;
-  // the group's query rows into shared memory, and the sequence's sizes, all in flight
-  if (tid < a.group * D / 8)
+  if (tid < a.group * D / 8)  // the group's query rows
     *reinterpret_cast<uint4 *>(q_area + tid * 16) =
         __ldg(reinterpret_cast<const uint4 *>(a.q + head0 * D) + tid);
-  int L = __ldg(a.context_lens + b);
-  int skip = 0;  // the prefix: 0 for a sequence of no group
-  for (int c = 0; c < a.num_groups; c += 32) {
-    const int i = c + lane;
-    int s = 0, e = 0, p = 0;
-    if (i < a.num_groups) {
-      s = __ldg(a.group_start + i);
-      e = __ldg(a.group_start + i + 1);
-      p = __ldg(a.prefix_lens + i);
-    }
-    const unsigned mine = __ballot_sync(0xffffffffu, s <= b && b < e);
-    if (mine) {
-      skip = __shfl_sync(0xffffffffu, p, __ffs(mine) - 1);
-      break;
-    }
-  }
-  const int cap = (int)min((int64_t)a.max_blocks * a.block_size, (int64_t)0x7fffffff);
-  skip = min(max(skip, 0), min(cap, a.max_prefix)) >> a.log2_bs << a.log2_bs;
-  if (L < 0 || L > cap || L - skip > a.max_suffix) {
-    if (tid == 0 && part == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
-    L = L < 0 ? 0 : min(L, min(cap, skip + min(a.max_suffix, 0x7fffffff - skip)));
-  }
-  const int n_pre = (skip + a.row_keys - 1) / a.row_keys;  // the prefix's rows
-  const int n_own = max(L - skip, 0);
-  const int n_tail = (n_own + a.partition_tokens - 1) / a.partition_tokens;
-  if (part >= max(n_tail, 1)) return;
-  const int t_begin = skip + part * a.partition_tokens;
-  const int t_end = min(t_begin + a.partition_tokens, max(L, skip));
+  const int n_pre = prefix_rows(a.cut, skip), n_tail = own_rows(a.cut, L, skip);
+  if (part >= n_tail) return;
+  const int t_begin = skip + part * a.cut.partition_tokens;
+  const int t_end = min(t_begin + a.cut.partition_tokens, L);
   const int n_chunks = (t_end - t_begin + kChunk - 1) / kChunk;
 
   if (tid == 0) {
@@ -165,7 +182,6 @@ __global__ void __launch_bounds__(kThreads, split_occupancy(D))
       dev::mbar_init(bar_empty + 8 * s, kConsumerWarps);
     }
     *s_flag = 0;
-    *s_last = 0;
     dev::fence_mbar_init();
   }
   __syncthreads();
@@ -175,10 +191,10 @@ __global__ void __launch_bounds__(kThreads, split_occupancy(D))
     const uint64_t policy = dev::policy_evict_first();
     const int rb = a.box_rows;
     const uint32_t box_bytes = (uint32_t)rb * 128u;
-    const int32_t *trow = a.block_tables + (int64_t)b * a.max_blocks;
-    const int lb_last = (t_end - 1) >> a.log2_bs;
-    int win = t_begin >> a.log2_bs;
-    int tb = (n_chunks > 0 && win + lane <= lb_last) ? __ldg(trow + win + lane) : 0;
+    const int32_t *trow = a.block_tables + (int64_t)b * a.cut.max_blocks;
+    const int lb_last = (t_end - 1) >> a.cut.log2_bs;
+    int win = t_begin >> a.cut.log2_bs;
+    int tb = win + lane <= lb_last ? __ldg(trow + win + lane) : 0;
     for (int c = 0; c < n_chunks; ++c) {
       const int s = c % STAGES;
       if (c >= STAGES &&
@@ -192,13 +208,13 @@ __global__ void __launch_bounds__(kThreads, split_occupancy(D))
       const int k0 = t_begin + c * kChunk;
       const int nk = min(kChunk, t_end - k0);
       const int nbox = (nk + rb - 1) / rb;
-      const int lb_hi = (k0 + (nbox - 1) * rb) >> a.log2_bs;
+      const int lb_hi = (k0 + (nbox - 1) * rb) >> a.cut.log2_bs;
       if (lb_hi >= win + 32) {  // slide the table window
-        win = k0 >> a.log2_bs;
+        win = k0 >> a.cut.log2_bs;
         tb = (win + lane <= lb_last) ? __ldg(trow + win + lane) : 0;
       }
       const int key = k0 + lane * rb;
-      const int src = min(max((key >> a.log2_bs) - win, 0), 31);
+      const int src = min(max((key >> a.cut.log2_bs) - win, 0), 31);
       const int64_t phys_raw = __shfl_sync(0xffffffffu, tb, src);
       if (lane == 0) dev::mbar_arrive_expect_tx(bar_full + 8 * s, 2u * nbox * box_bytes * (D / 64));
       __syncwarp();
@@ -208,8 +224,8 @@ __global__ void __launch_bounds__(kThreads, split_occupancy(D))
           raise_error(PKV_DEVERR_BLOCK_ID);
           phys = 0;
         }
-        const int off = key & (a.block_size - 1);
-        const int32_t row = (int32_t)((phys * a.num_kv_heads + g) * a.block_size + off);
+        const int off = key & (a.cut.block_size - 1);
+        const int32_t row = (int32_t)((phys * a.num_kv_heads + g) * a.cut.block_size + off);
         const uint32_t dk = base + s * kStageBytes + lane * box_bytes;
         issue_box<D>(dk, dk + kTileBytes, &tmk, &tmv, row, bar_full + 8 * s, policy);
       }
@@ -255,49 +271,16 @@ __global__ void __launch_bounds__(kThreads, split_occupancy(D))
     r.l = r.m + kConsumerWarps * kMaxGroup;
     warp_stash<D>(acc, r, a.group, warp, lane);
     consumer_bar();
-    bool merge = n_tail <= 1;
-    if (!merge) {
-      for (int i = tid; i < a.group * D; i += kConsumers) {
-        const int h = i / D, d = i - h * D;
-        float M2, den;
-        const float val = cta_merge<D>(r, a.group, h, d, &M2, &den);
-        const int64_t row = (head0 + h) * a.n_rows + n_pre + part;
-        a.o_part[row * D + d] = val;
-        if (d == 0) a.lse_part[row] = (M2 + log2f(den)) * kLn2;
-      }
-      consumer_bar();
-      if (tid == 0) {
-        int last = 0;
-        if (!*s_flag) {
-          const unsigned old = dev::atomic_add_acq_rel(a.counters + (int64_t)b * a.num_kv_heads + g, 1u);
-          last = (old + 1 == (unsigned)n_tail);
-        }
-        *s_last = last;
-      }
-      consumer_bar();
-      merge = *s_last != 0;
-      if (merge && tid == 0) a.counters[(int64_t)b * a.num_kv_heads + g] = 0u;
+    for (int i = tid; i < a.group * D; i += kConsumers) {
+      const int h = i / D, d = i - h * D;
+      float M2, den;
+      const float val = cta_merge<D>(r, a.group, h, d, &M2, &den);
+      const int64_t row = (head0 + h) * a.cut.n_rows + n_pre + part;
+      a.o_part[row * D + d] = val;
+      if (d == 0) a.lse_part[row] = (M2 + log2f(den)) * kLn2;
     }
-    // the prefix's partials are complete and visible past this point
-    if (merge) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      constexpr int VPL = D / 32;
-      for (int h = warp; h < a.group; h += kConsumerWarps) {
-        float own[VPL], own_lse = -INFINITY;
-        if (n_tail == 1) {
-          float M2, den;
-#pragma unroll
-          for (int v = 0; v < VPL; ++v) own[v] = cta_merge<D>(r, a.group, h, lane * VPL + v, &M2, &den);
-          own_lse = M2 + log2f(den);
-        } else {
-#pragma unroll
-          for (int v = 0; v < VPL; ++v) own[v] = 0.f;
-        }
-        merge_rows_own<D>(a.out + (head0 + h) * D, a.o_part + (head0 + h) * a.n_rows * D,
-                          a.lse_part + (head0 + h) * a.n_rows, n_pre + (n_tail > 1 ? n_tail : 0),
-                          lane, own, own_lse);
-      }
-    }
+    consumer_bar();  // orders every thread's stores before the release
+    if (tid == 0 && !*s_flag) dev::red_add_release(a.counters + (int64_t)b * a.num_kv_heads + g, 1u);
   }
 
   // ---- a timed-out wait leaves copies possibly in flight: wait for them (bounded)
@@ -315,13 +298,14 @@ cudaError_t read_shared_errors(uint32_t *flags, int clear) { return read_tu_erro
 namespace {
 
 bool g_tail_attr[kMaxDevices][2];
+std::atomic<int> g_mode{PKV_SHARED_AUTO};  // PKV_SHARED_*, process-wide
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // How a call is cut: split_keys prefix keys per tile CTA, partition_tokens tail tokens per
 // tail CTA, and the workspace.
 struct SharedPlan {
-  int32_t split_keys, splits, cluster, partition_tokens, parts, n_rows;
+  int32_t split_keys, splits, partition_tokens, parts, n_rows, sorted, merge_ctas, merge_heads, plain, plain_len;
   int64_t tiles;  // row tiles over all groups, at most
   size_t o_part, lse_part, total;
 };
@@ -331,33 +315,60 @@ SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int
   SharedPlan p;
   const int32_t groups = std::min(num_groups, num_seqs);
   const int64_t tile_seqs = kTileRows / (hq / hkv);  // sequences of a tile
-  p.tiles = num_seqs / tile_seqs + groups;
-  // About one tile CTA per SM: the prefix is cut into as many splits as that takes, in
-  // clusters (measured on 152 SMs with 1 CTA each: 36 clusters of 4 fit at once, 76 of 2,
-  // but only 15 of 8).
-  const int64_t units = std::max<int64_t>((num_seqs + tile_seqs - 1) / tile_seqs, groups) * hkv;
+  p.tiles = groups > 0 ? (num_seqs - groups) / tile_seqs + groups : 0;  // at most, however they are cut
+  const int64_t units = p.tiles * hkv;
   const int64_t blocks = ((int64_t)max_prefix + kTileKeys - 1) / kTileKeys;
-  p.cluster = 1;
-  int64_t splits = 1;
-  for (int32_t c = kPrefixCluster; c > 1; c /= 2) {
-    const int64_t fit = (c == 2 ? sms : sms - sms / 19) / c;  // clusters at once
-    if (units > fit || blocks < c) continue;
-    const int64_t n = c * std::min(fit / units, blocks / c);
-    if (n <= splits) continue;
-    p.cluster = c;
-    splits = n;
-  }
-  p.split_keys = (int32_t)std::min<int64_t>(std::max<int64_t>((blocks + splits - 1) / splits, 1) * kTileKeys,
-                                            1 << 29);
-  p.splits = (int32_t)splits;
   const int32_t mlen = std::max(max_suffix, 1);
   p.partition_tokens = paged_decode_plan(num_seqs, hq, hkv, d, mlen, sms);
   p.parts = (mlen + p.partition_tokens - 1) / p.partition_tokens;
-  p.n_rows = p.splits / p.cluster + p.parts;
+  // The prefix's CTAs take an SM each; the tail's run beside them on the others, and take
+  // theirs over.  So: as many splits as make the longer of a tile CTA's time and of the whole
+  // work over the SMs the shortest.  Measured, in us: a tile CTA 8.5 and, per block of 128
+  // keys, what the TMA unit needs for its boxes of 16 rows (63 cycles each and 64 bytes a
+  // cycle at 1.93 GHz) or the HBM for all CTAs' (6.5 TB/s); a tail CTA 4.5 and 34 KB a us, 2 or
+  // 3 to an SM.  Own lengths are taken at half the longest.
+  const int occ = split_occupancy(d);
+  const double tail_ctas = (double)num_seqs * hkv * p.parts;
+  const double tail = tail_ctas * (4.5 + 0.5 * mlen / p.parts * d * 4 / 34e3) / occ;
+  const double tma = d == 64 ? 0.79 : 1.57;
+  double best = 0;
+  p.splits = 1;
+  for (int64_t n = 1; n <= std::min<int64_t>(blocks, 1024); ++n) {
+    const double ctas = (double)units * n;
+    if (n > 1 && ctas > sms) break;
+    const double hbm = (double)groups * hkv * n * kTileKeys * d * 4 / 6.5e6;
+    const double tile = 8.5 + (double)((blocks + n - 1) / n) * std::max(tma, hbm);
+    const double fits = ctas + tail_ctas / occ <= sms ? 0 : 5;  // or the tail begins after it
+    const double t = std::max(tile, (tail + std::min<double>(ctas, sms) * tile) / sms) + fits;
+    if (n == 1 || t < best) {
+      best = t;
+      p.splits = (int32_t)n;
+    }
+  }
+  p.split_keys = (int32_t)std::min<int64_t>(
+      std::max<int64_t>((blocks + p.splits - 1) / p.splits, 1) * kTileKeys, 1 << 29);
+  p.sorted = num_seqs <= kSortSeqs && mlen >= 512 && units * p.splits + tail_ctas / occ > sms;
+  p.n_rows = p.splits + p.parts;
+  // A warp per head, or per as many heads as keep the merging CTAs within half of those that
+  // fit at once.
+  const int64_t warps = kThreads / 32, cap = (int64_t)sms * occ / 2 * warps;
+  const int32_t group = hq / hkv;
+  int64_t tasks;
+  for (p.merge_heads = 1;; ++p.merge_heads) {
+    tasks = (int64_t)num_seqs * hkv * ((group + p.merge_heads - 1) / p.merge_heads);
+    if (tasks <= cap || p.merge_heads == group) break;
+  }
+  p.merge_ctas = (int32_t)((std::min(tasks, cap) + warps - 1) / warps);
   const size_t prow = (size_t)num_seqs * hq * p.n_rows;
-  p.o_part = up256((size_t)num_seqs * hkv * 4);
+  p.o_part = up256((size_t)num_seqs * hkv * 4 + 8);  // behind the plain decode's words too
   p.lse_part = p.o_part + up256(prow * d * sizeof(float));
   p.total = p.lse_part + up256(prow * sizeof(float));
+  p.plain_len = (int32_t)std::min<int64_t>((int64_t)max_prefix + max_suffix, 0x7fffffff);
+  p.total = std::max(p.total, paged_decode_workspace_size(num_seqs, hq, hkv, d, p.plain_len));
+  // Little is read twice: the plain decode, one launch, is the faster one.  Measured, shared
+  // against plain: 3 sequences over 512 tokens (2 MB saved) 8.3 against 7.5 us, 16 over 2048
+  // (63 MB) 10.6 against 12.7 us, 64 over 8192 (1 GB) 43 against 258 us.
+  p.plain = (double)(num_seqs - groups) * max_prefix * hkv * d * 4 < 40e6;
   return p;
 }
 
@@ -404,6 +415,13 @@ int sm_count(int *sms) {
 
 using namespace pkv;
 
+PKV_API int32_t pkv_set_shared_prefix(int32_t mode) {
+  if (mode != PKV_SHARED_AUTO && mode != PKV_SHARED_ALWAYS && mode != PKV_SHARED_NEVER)
+    return set_error(PKV_ERR_UNSUPPORTED, "pkv_set_shared_prefix: unknown mode %d", mode);
+  clear_error();
+  return g_mode.exchange(mode);
+}
+
 PKV_API size_t paged_decode_shared_prefix_workspace_size(int32_t num_seqs, int32_t num_q_heads,
                                                          int32_t num_kv_heads, int32_t head_dim,
                                                          int32_t num_groups, int32_t max_prefix_len,
@@ -448,6 +466,18 @@ PKV_API int paged_decode_shared_prefix_attention(
                      p.total);
   if (!aligned16(workspace))
     return set_error(PKV_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+  const int64_t tail_ctas = (int64_t)p.parts * hkv * num_seqs;
+  if (tail_ctas > 0x7fff0000LL || (int64_t)num_seqs * num_q_heads > 0x7fffffffLL)
+    return set_error(PKV_ERR_UNSUPPORTED, "%s: too many parts", fn);
+  const int mode = g_mode.load(std::memory_order_relaxed);
+  if (mode == PKV_SHARED_NEVER || (mode == PKV_SHARED_AUTO && p.plain)) {
+    const int64_t cap = (int64_t)max_blocks_per_seq * cache->block_size;
+    const int32_t len = (int32_t)std::min<int64_t>(p.plain_len, cap);
+    if (workspace_bytes >= paged_decode_workspace_size(num_seqs, num_q_heads, hkv, D, len))
+      return paged_decode_attention(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                                    context_lens, len, num_seqs, num_q_heads, cache, scale, workspace,
+                                    workspace_bytes, stream);
+  }
   CUtensorMap tmk, tmv;
   {
     std::lock_guard<std::mutex> lk(attn_mutex());
@@ -465,20 +495,22 @@ PKV_API int paged_decode_shared_prefix_attention(
   a.out = out;
   a.counters = reinterpret_cast<uint32_t *>(ws);
   a.num_blocks = cache->num_blocks;
-  a.max_blocks = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
   a.num_groups = num_groups;
-  a.max_prefix = max_prefix_len;
-  a.max_suffix = max_suffix_len;
   a.num_q_heads = num_q_heads;
   a.num_kv_heads = hkv;
   a.group = num_q_heads / hkv;
-  a.block_size = cache->block_size;
-  a.log2_bs = ilog2(cache->block_size);
   a.box_rows = std::min(cache->block_size, (int32_t)kChunk);
-  a.partition_tokens = p.partition_tokens;
-  a.n_rows = p.n_rows;
-  a.row_keys = p.split_keys * p.cluster;
   a.scale_log2 = scale * kLog2e;
+  a.cut.max_blocks = max_blocks_per_seq;
+  a.cut.block_size = cache->block_size;
+  a.cut.log2_bs = ilog2(cache->block_size);
+  a.cut.max_prefix = max_prefix_len;
+  a.cut.max_suffix = max_suffix_len;
+  a.sorted = p.sorted;
+  a.cut.split_keys = p.split_keys;
+  a.cut.partition_tokens = p.partition_tokens;
+  a.cut.n_rows = p.n_rows;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool prefix = num_groups > 0 && max_prefix_len >= cache->block_size;
   if (prefix) {
@@ -492,18 +524,18 @@ PKV_API int paged_decode_shared_prefix_attention(
     l.lse_part = a.lse_part;
     l.num_seqs = num_seqs;
     l.num_groups = num_groups;
-    l.max_blocks = max_blocks_per_seq;
-    l.max_prefix = max_prefix_len;
     l.num_q_heads = num_q_heads;
     l.split_keys = p.split_keys;
     l.splits = p.splits;
-    l.cluster = p.cluster;
-    l.n_rows = p.n_rows;
     l.tiles = p.tiles;
     l.scale = scale;
+    l.cut = &a.cut;
     if ((rc = launch_prefix(tmk, tmv, *cache, l, s))) return rc;
   }
-  const dim3 grid((unsigned)p.parts, (unsigned)hkv, (unsigned)num_seqs);
+  a.parts = p.parts;
+  a.merge_heads = p.merge_heads;
+  a.tail_ctas = (int32_t)tail_ctas;
+  const dim3 grid((unsigned)(tail_ctas + p.merge_ctas));
   rc = D == 64 ? launch_tail<64>(tmk, tmv, a, grid, prefix, s) : launch_tail<128>(tmk, tmv, a, grid, prefix, s);
   if (!rc) clear_error();
   return rc;

@@ -10,6 +10,7 @@
 #include <type_traits>
 
 #include "attn_tc.cuh"
+#include "shared_device.cuh"
 
 namespace pkv {
 
@@ -36,13 +37,11 @@ namespace pkv {
 //  * kPrefix: both tiles hold the same rows (queries of a group of sequences) and take
 //    alternate key blocks, so that a few rows over a long prefix still overlap softmax and
 //    tensor core.  The keys come from the pages of the group's first sequence; the CTA
-//    covers one split of them.  The tiles' results are joined through shared memory and those of
-//    a cluster's splits through distributed shared memory: each CTA gathers a share of the
-//    rows and writes one softmax-normalised fp32 row and log-sum-exp per cluster, for the
-//    merge in the decode kernel that follows.  (Written per tile and split, 64 sequences of 3
-//    heads over 8192 keys left 17 MB of partials, half as much as the keys and values.)
+//    covers one split of them, joins its tiles' results through shared memory and writes one
+//    softmax-normalised fp32 row and log-sum-exp per query row.  (A cluster's splits joined
+//    through distributed shared memory wrote a quarter of the rows, but took 3.5 us to read
+//    them against 1 us to write them all.)
 enum { kPrompt = 0, kPrefix = 1 };
-constexpr int kMaxCluster = kPrefixCluster;
 
 struct TileArgs {
   uint16_t *out;            // prompt
@@ -55,10 +54,10 @@ struct TileArgs {
   // prefix
   const int32_t *block_tables, *context_lens, *prefix_lens;
   int64_t num_blocks;
-  int32_t max_blocks, max_prefix, block_size, log2_bs, box_rows;
+  int32_t box_rows;
   int32_t split_keys;       // keys per split (a multiple of kTcKeys)
-  int32_t n_rows;           // partial rows per (sequence, head)
-  float *o_part, *lse_part; // [B][Hq][n_rows][D], [B][Hq][n_rows]; row s: the s-th cluster of splits
+  float *o_part, *lse_part; // [B][Hq][n_rows][D], [B][Hq][n_rows]; row s: the s-th split
+  SharedCut cut;
 };
 
 // 8 softmax warps, the K and the V producer (two warps a ring measured neutral), an MMA warp per
@@ -73,7 +72,8 @@ struct TileItem {
   int32_t tok0, n;          // the tiles' first token and the token count, within the sequence
   int32_t key0, t_end;      // keys [key0, t_end) are staged, in blocks of kTcKeys
   int32_t nb0, nb1;         // blocks of each tile
-  int32_t pad[3];
+  int32_t prefix;           // kPrefix: the whole pages of the group's prefix
+  int32_t pad[2];
 };
 
 template <int D, int MODE>
@@ -141,23 +141,16 @@ __device__ __forceinline__ bool clc_answer(uint32_t src, uint32_t &ctaid) {
 }
 
 // The sequence (or group) whose pieces of `tokens` query tokens hold piece number idx, its
-// first query token, its length, the piece's place in it, its pieces and its prefix.  Whole warps;
-// lengths that are negative, past `total` or over max_len are clamped and flagged.
+// first query token, its length, the piece's place in it, its pieces and its prefix.  Whole
+// warps; misplaced and over-long sequences are moved, cut and flagged.
 __device__ __forceinline__ bool locate_tile(const TileArgs &a, int64_t idx, int tokens, int lane,
                                             int &first, int &n, int &tile, int &ntiles,
                                             int &prefix) {
   int64_t before = 0;
-  for (int c = 0; c < a.num; c += 32) {
-    const int i = c + lane;
-    int s = 0, len = 0, p = 0;
-    if (i < a.num) {
-      const int s0 = __ldg(a.start + i), e0 = __ldg(a.start + i + 1);
-      if (a.prefix_lens) p = __ldg(a.prefix_lens + i);
-      s = min(max(s0, 0), a.total);
-      len = min(max(e0, s), a.total) - s;
-      len = min(len, a.max_len);
-      if (s != s0 || s + len != e0) raise_error(PKV_DEVERR_CONTEXT_LEN);
-    }
+  for (int c = 0, carry = 0; c < a.num; c += 32) {
+    int s, len;
+    const int p = a.prefix_lens && c + lane < a.num ? __ldg(a.prefix_lens + c + lane) : 0;
+    disjoint_group(a.start, a.num, a.total, a.max_len, c, lane, carry, s, len);
     const int mine = (len + tokens - 1) / tokens;
     int upto = mine;
 #pragma unroll
@@ -199,17 +192,15 @@ __device__ __forceinline__ bool make_item(const TileArgs &a, unsigned cta_x, uns
     it.nb1 = e1 > e0 ? (e1 + kTcKeys - 1) / kTcKeys : 0;
   } else {
     it.tok0 = tile * tokens;
-    const int cap = (int)min((int64_t)a.max_blocks * a.block_size, (int64_t)a.max_prefix);
-    if (prefix < 0 || prefix > cap) {
-      if (lane == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
-      prefix = prefix < 0 ? 0 : cap;
-    }
-    prefix = prefix >> a.log2_bs << a.log2_bs;  // whole pages
-    // a CTA without keys still takes part in its cluster's merge, if any other has some
-    const int cluster0 = (int)(cta_y - dev::cluster_ctarank()) * a.split_keys;
-    if (cluster0 >= prefix) return false;
+    const int pages = shared_pages(a.cut, prefix);
+    if ((prefix < 0 || prefix > min((int64_t)a.cut.max_blocks * a.cut.block_size, (int64_t)a.cut.max_prefix)) &&
+        lane == 0)
+      raise_error(PKV_DEVERR_CONTEXT_LEN);
+    prefix = pages;
+    it.prefix = prefix;
     it.key0 = (int)cta_y * a.split_keys;
-    it.t_end = max(it.key0, min(it.key0 + a.split_keys, prefix));
+    if (it.key0 >= prefix) return false;
+    it.t_end = min(it.key0 + a.split_keys, prefix);
     const int nblk = (it.t_end - it.key0 + kTcKeys - 1) / kTcKeys;
     it.nb0 = (nblk + 1) / 2;
     it.nb1 = nblk / 2;
@@ -229,14 +220,14 @@ __device__ __forceinline__ void load_paged_block(const CUtensorMap *tm, uint32_t
   constexpr int kH = D / 64;
   const int rb = a.box_rows;
   const int nbox = (nk + rb - 1) / rb;
-  const int lb_hi = (k0 + (nbox - 1) * rb) >> a.log2_bs;
-  if (lb_hi >= win + 32 || (k0 >> a.log2_bs) < win) {
-    win = k0 >> a.log2_bs;
+  const int lb_hi = (k0 + (nbox - 1) * rb) >> a.cut.log2_bs;
+  if (lb_hi >= win + 32 || (k0 >> a.cut.log2_bs) < win) {
+    win = k0 >> a.cut.log2_bs;
     tb = (win + lane <= lb_last) ? __ldg(trow + win + lane) : 0;
   }
   const int bi = lane / kH, hh = lane % kH;
   const int key = k0 + bi * rb;
-  const int src = min(max((key >> a.log2_bs) - win, 0), 31);
+  const int src = min(max((key >> a.cut.log2_bs) - win, 0), 31);
   const int64_t phys_raw = __shfl_sync(0xffffffffu, tb, src);
   if (lane == 0) dev::mbar_arrive_expect_tx(bar, (uint32_t)nbox * rb * 128u * kH);
   __syncwarp();
@@ -246,8 +237,8 @@ __device__ __forceinline__ void load_paged_block(const CUtensorMap *tm, uint32_t
       raise_error(PKV_DEVERR_BLOCK_ID);
       phys = 0;
     }
-    const int off = key & (a.block_size - 1);
-    const int32_t row = (int32_t)((phys * a.num_kv_heads + g) * a.block_size + off);
+    const int off = key & (a.cut.block_size - 1);
+    const int32_t row = (int32_t)((phys * a.num_kv_heads + g) * a.cut.block_size + off);
     const uint32_t d = dst + (uint32_t)(bi * rb) * 128u;
     if constexpr (D == 64) {
       dev::tma_load_2d(d, tm, 0, row, bar, policy);
@@ -381,9 +372,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   TileItem it = {};
   bool have = false;
   if (kPaged || warp == kProducer) have = make_item<MODE>(a, blockIdx.x, blockIdx.y, lane, it);
-  if (kPaged && !have) return;  // the whole cluster: nothing in its rows or its keys
-  const TileItem first = it;    // kPrefix: the CTA's only one
-  if (kPaged) have = it.t_end > it.key0;
+  if (kPaged && !have) return;
+  const TileItem first = it;  // kPrefix: the CTA's only one
   if (tid == 0) {
     for (int i = 0; i < SL::kBars; ++i) {
       const int r = i - kRings;
@@ -447,9 +437,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int ks = is_k ? KSK : KSV;
     const uint64_t policy = dev::policy_evict_last();  // other CTAs read the same keys
     const int nblk = (x.t_end - x.key0 + kTcKeys - 1) / kTcKeys;
-    const int32_t *const trow = kPaged ? a.block_tables + (int64_t)x.first * a.max_blocks : nullptr;
-    const int lb_last = kPaged ? (x.t_end - 1) >> a.log2_bs : 0;
-    int win = kPaged ? x.key0 >> a.log2_bs : 0;
+    const int32_t *const trow = kPaged ? a.block_tables + (int64_t)x.first * a.cut.max_blocks : nullptr;
+    const int lb_last = kPaged ? (x.t_end - 1) >> a.cut.log2_bs : 0;
+    int win = kPaged ? x.key0 >> a.cut.log2_bs : 0;
     int tb = kPaged && win + lane <= lb_last ? __ldg(trow + win + lane) : 0;
     for (int j = 0; j < nblk; ++j, ++issued) {
       const int s = issued % ks;
@@ -757,8 +747,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       }
       if constexpr (kPaged) {
-        // This tile's rows (max, sum, unnormalised O) into shared memory for the cluster's
-        // merge: the rings are done with once both tiles' MMAs are.
+        // This tile's rows (max, sum, unnormalised O) into shared memory, to be joined with the
+        // other's below: the rings are done with once both tiles' MMAs are.
         __syncwarp();
         if (lane == 0) dev::mbar_arrive(tiles_done);
         ok = __all_sync(0xffffffffu, dev::mbar_wait(tiles_done, 0)) && ok;
@@ -811,56 +801,39 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (tid == 0) (void)dev::mbar_wait(mma_done, 0);
   __syncthreads();
   if constexpr (kPaged) {
-    // The cluster's merge: every CTA reads its share of the rows, both tiles' of every CTA,
-    // one 16-byte chunk per thread with all its loads in flight.  Each thread arrives after
-    // bounded waits only, so both barriers complete; the second keeps every CTA until its
-    // rows have been read.
-    if (!have && tid < 2 * kTcRows)
-      reinterpret_cast<float2 *>(bp + SL::ml)[tid] = make_float2(-INFINITY, 0.f);
-    const int n = (int)dev::cluster_nctarank(), rank = (int)dev::cluster_ctarank();
-    dev::cluster_arrive_release();
-    dev::cluster_wait();
-    const int share = (tile_rows + n - 1) / n, row_end = min((rank + 1) * share, tile_rows);
-    const int c16 = tid % (D / 4);
-#pragma unroll 2
-    for (int r = rank * share + tid / (D / 4); r < row_end; r += kTileThreads / (D / 4)) {
-      const int tok = r / G, h = r - tok * G;
-      const int qi = first.tok0 + tok;
-      if (qi >= first.n) break;
-      float2 ml[2 * kMaxCluster];
-      float4 o[2 * kMaxCluster];
-      float m = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < 2 * kMaxCluster; ++c) {
-        ml[c] = make_float2(-INFINITY, 0.f);
-        o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if ((c >> 1) < n) {
-          const uint32_t rr = (uint32_t)((c & 1) * kTcRows + r);
-          ml[c] = dev::ld_cluster_f2(dev::mapa(base + SL::ml + rr * 8, c >> 1));
-          o[c] = dev::ld_cluster_f4(dev::mapa(base + SL::rows + rr * (D * 4) + ((c16 ^ (r & 7)) << 4), c >> 1));
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < 2 * kMaxCluster; ++c) m = fmaxf(m, ml[c].x);
-      float l = 0.f;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int c = 0; c < 2 * kMaxCluster; ++c) {
-        if (ml[c].x == -INFINITY && ml[c].y == 0.f) continue;  // no key seen there: no row either
-        const float w = dev::ex2(ml[c].x - m);
-        l += w * ml[c].y;
-        x.x += w * o[c].x, x.y += w * o[c].y, x.z += w * o[c].z, x.w += w * o[c].w;
-      }
-      const bool any = m != -INFINITY || l != 0.f;
-      const float inv = any ? 1.f / l : 0.f;
-      const int64_t row = ((int64_t)(first.first + qi) * a.num_q_heads + first.g * G + h) * a.n_rows +
-                          blockIdx.y / n;
-      reinterpret_cast<float4 *>(a.o_part + row * D)[c16] =
-          make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-      if (c16 == 0) a.lse_part[row] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+    // Both tiles' rows of a query row joined and written: the weights and the place of each row
+    // first, then 16 bytes per thread.
+    const int toks = min(a.tile_tokens, first.n - first.tok0), nrows = toks * G;  // tokens: sequences
+    const int c16 = tid % (D / 4), r_first = tid / (D / 4);
+    constexpr int kStep = kTileThreads / (D / 4);
+    const float2 *const s_ml = reinterpret_cast<const float2 *>(bp + SL::ml);
+    const float4 *const s_rows = reinterpret_cast<const float4 *>(bp + SL::rows);
+    float2 *const s_join = reinterpret_cast<float2 *>(bp + SL::q);                 // per row: the tiles' weights
+    int *const s_row = reinterpret_cast<int *>(bp + SL::q + kTcRows * 8);          // per row: b * Hq + h
+    if (tid < nrows) {
+      const int tok = tid / G;
+      const int row = (first.first + first.tok0 + tok) * a.num_q_heads + first.g * G + (tid - tok * G);
+      const float2 a0 = s_ml[tid], a1 = s_ml[kTcRows + tid];
+      // a tile without keys wrote no row (weight -1 below); no key at all gives zeros and -inf
+      const bool any0 = a0.x != -INFINITY || a0.y != 0.f, any1 = a1.x != -INFINITY || a1.y != 0.f;
+      const float m = fmaxf(a0.x, a1.x);
+      const float w0 = any0 ? dev::ex2(a0.x - m) : 0.f, w1 = any1 ? dev::ex2(a1.x - m) : 0.f;
+      const float l = (any0 ? w0 * a0.y : 0.f) + (any1 ? w1 * a1.y : 0.f);
+      s_join[tid] = make_float2(any0 ? w0 / l : -1.f, any1 ? w1 / l : -1.f);
+      s_row[tid] = row;
+      a.lse_part[(int64_t)row * a.cut.n_rows + blockIdx.y] =
+          any0 || any1 ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
-    dev::cluster_arrive_relaxed();  // nothing to publish: the loads above have returned
-    dev::cluster_wait();
+    __syncthreads();
+#pragma unroll 4
+    for (int r = r_first; r < nrows; r += kStep) {
+      const float2 w = s_join[r];
+      const int at = r * (D / 4) + (c16 ^ (r & 7));
+      const float4 x0 = s_rows[at], x1 = s_rows[kTcRows * (D / 4) + at];
+      auto join = [&](float u, float v) { return (w.x == -1.f ? 0.f : w.x * u) + (w.y == -1.f ? 0.f : w.y * v); };
+      reinterpret_cast<float4 *>(a.o_part + ((int64_t)s_row[r] * a.cut.n_rows + blockIdx.y) * D)[c16] =
+          make_float4(join(x0.x, x1.x), join(x0.y, x1.y), join(x0.z, x1.z), join(x0.w, x1.w));
+    }
   }
   if (warp >= kProducer && warp < kMma && lane == 0 && *s_flag) {
     const int ks = warp < kProducerV ? KSK : KSV;
@@ -911,22 +884,11 @@ int launch_prompt(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensor
 
 template <int D>
 int launch_prefix_tiles(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
-                        const TileArgs &a, dim3 grid, int cluster, cudaStream_t stream) {
+                        const TileArgs &a, dim3 grid, cudaStream_t stream) {
   const int rc = prepare_tile_kernel<D, kPrefix>();
   if (rc) return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kTileThreads, 1, 1);
-  cfg.dynamicSmemBytes = tile_smem<D, kPrefix>();
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = (unsigned)cluster;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, tile_kernel<D, kPrefix>, tmq, tmk, tmv, a);
+  tile_kernel<D, kPrefix><<<grid, kTileThreads, tile_smem<D, kPrefix>(), stream>>>(tmq, tmk, tmv, a);
+  const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? PKV_OK : cuda_error(e, "tile_kernel launch");
 }
 
@@ -948,15 +910,11 @@ int launch_prefix(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv_cach
   a.context_lens = l.context_lens;
   a.prefix_lens = l.prefix_lens;
   a.num_blocks = c.num_blocks;
-  a.max_blocks = l.max_blocks;
-  a.max_prefix = l.max_prefix;
-  a.block_size = c.block_size;
-  a.log2_bs = ilog2(c.block_size);
   a.box_rows = std::min(c.block_size, (int32_t)kChunk);
   a.split_keys = l.split_keys;
-  a.n_rows = l.n_rows;
   a.o_part = l.o_part;
   a.lse_part = l.lse_part;
+  a.cut = *l.cut;
   if (l.tiles * c.num_kv_heads > 0x7fffffffLL || l.splits > 65535)
     return set_error(PKV_ERR_UNSUPPORTED, "shared prefix: too many tiles");
   CUtensorMap tmq;
@@ -967,8 +925,8 @@ int launch_prefix(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv_cach
     if (rc) return rc;
   }
   const dim3 grid((unsigned)(l.tiles * c.num_kv_heads), (unsigned)l.splits);
-  return c.head_dim == 64 ? launch_prefix_tiles<64>(tmq, tmk, tmv, a, grid, l.cluster, stream)
-                          : launch_prefix_tiles<128>(tmq, tmk, tmv, a, grid, l.cluster, stream);
+  return c.head_dim == 64 ? launch_prefix_tiles<64>(tmq, tmk, tmv, a, grid, stream)
+                          : launch_prefix_tiles<128>(tmq, tmk, tmv, a, grid, stream);
 }
 
 }  // namespace pkv

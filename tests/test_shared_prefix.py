@@ -26,6 +26,14 @@ def B():
     return binding
 
 
+@pytest.fixture(autouse=True)
+def always_shared(B):
+    """The shared path at every size; test_modes_agree takes the others."""
+    before = B.pkv_set_shared_prefix(B.SHARED_ALWAYS)
+    yield
+    B.pkv_set_shared_prefix(before)
+
+
 def make(groups, prefixes, suffixes, hq, hkv, d, bs, seed, lead=0, tail=0, poison=True):
     """`groups`: sizes; one prefix each; one suffix per sequence.  `lead`/`tail` sequences of
     no group come before and after (their suffix is their whole context).  Slots that no
@@ -183,6 +191,19 @@ def test_contexts_shorter_than_the_prefix(B, d):
 
 
 @pytest.mark.gpu
+def test_modes_agree(B):
+    """Shared, plain and by size, in turn on one workspace."""
+    c = make([20, 4], [1000, 2500], list(range(24)), 32, 8, 64, 16, 1)
+    o, amp = reference(c, 0.125)
+    ws = workspace(B, c)
+    B.pkv_device_errors()
+    for mode in (B.SHARED_ALWAYS, B.SHARED_NEVER, B.SHARED_AUTO, B.SHARED_ALWAYS, B.SHARED_NEVER):
+        B.pkv_set_shared_prefix(mode)
+        check(call(B, c, 0.125, ws), o, amp, f"mode {mode}")
+    assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.gpu
 def test_equals_plain_decode(B):
     c = make([20, 4], [1000, 2500], list(range(24)), 32, 8, 64, 16, 1)
     a, b = call(B, c, 0.125), torch.empty_like(c["q"])
@@ -318,6 +339,12 @@ def test_argument_errors(B):
     assert run(out=None) == -1 and run(start=None) == -1 and run(prefix=None) == -1
     assert run(out=ctypes.c_void_p((1 << 20) + 2)) == -5
     assert run(n=0) == 0
+
+
+def test_unknown_mode(B):
+    assert B.lib().pkv_set_shared_prefix(3) == -3 and B.lib().pkv_set_shared_prefix(-1) == -3
+    with pytest.raises(B.PkvError):
+        B.pkv_set_shared_prefix(7)
 
 
 def test_workspace_size(B):
