@@ -141,11 +141,11 @@ def _check(rc: int, where: str):
         raise PkvError(rc, where)
 
 
-def _stream(stream: Optional[torch.cuda.Stream]) -> int:
+def _stream(stream: Optional[torch.cuda.Stream], dev: Optional[int] = None) -> int:
     if stream is not None:
         return stream.cuda_stream
     # torch.cuda.current_stream().cuda_stream without the Stream object (0.2 against 2.8 us)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -228,12 +228,27 @@ def _one_device(where: torch.Tensor, **tensors) -> None:
                          f"{torch.cuda.current_device()}")
 
 
+def _home(t: torch.Tensor) -> int:
+    """The device of t if it is the current one, else -2, which no tensor is on."""
+    dev = t.get_device()
+    return dev if dev >= 0 and dev == torch.cuda.current_device() else -2
+
+
+def _fine(dev: int, dtype, *tensors) -> bool:
+    """Whether the tensors are contiguous, of `dtype` and on device `dev` (None: not given).  The
+    checks that name what is wrong cost 0.5 us a tensor; a call makes them where this fails."""
+    for t in tensors:
+        if t is not None and (t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()):
+            return False
+    return True
+
+
 def _pointers(values) -> array.array:
     """A host array of device pointers (built faster than a ctypes one)."""
     return array.array("Q", values)
 
 
-def _layers(k_caches, v_caches, where: str):
+def _layers(k_caches, v_caches, dev: int, where: str):
     """(host arrays of the layers' K and V pointers, layer count, one layer's descriptor, a
     cache tensor) of 4-dim caches (one layer), 5-dim caches [layers, NB, Hkv, BS, D], or
     sequences of 4-dim caches."""
@@ -241,16 +256,16 @@ def _layers(k_caches, v_caches, where: str):
         ndim = k_caches.dim()
         if ndim not in (4, 5):
             raise ValueError(f"{where}: k_caches must be [NB, Hkv, BS, D] or [layers, NB, Hkv, BS, D]")
-        _need(k_caches, "k_caches", torch.bfloat16, ndim)
         if not isinstance(v_caches, torch.Tensor):
             raise TypeError(f"{where}: k_caches and v_caches must be given alike")
-        _need(v_caches, "v_caches", torch.bfloat16, ndim)
+        if not _fine(dev, torch.bfloat16, k_caches, v_caches):
+            _need(k_caches, "k_caches", torch.bfloat16, ndim)
+            _need(v_caches, "v_caches", torch.bfloat16, ndim)
+            _one_device(k_caches, v_caches=v_caches)
         if k_caches.shape != v_caches.shape:
             raise ValueError(f"{where}: k_caches and v_caches shapes differ")
-        _one_device(k_caches, v_caches=v_caches)
-        n = 1 if ndim == 4 else k_caches.shape[0]
-        step = 2 * k_caches.numel() // max(n, 1)
-        NB, Hkv, BS, D = k_caches.shape[-4:]
+        n, NB, Hkv, BS, D = k_caches.shape if ndim == 5 else (1, *k_caches.shape)
+        step = 2 * NB * Hkv * BS * D
         k0, v0 = k_caches.data_ptr(), v_caches.data_ptr()
         return (_pointers(range(k0, k0 + n * step, step) if step else [k0] * n),
                 _pointers(range(v0, v0 + n * step, step) if step else [v0] * n), n,
@@ -258,12 +273,14 @@ def _layers(k_caches, v_caches, where: str):
     ks, vs = list(k_caches), list(v_caches)
     if len(ks) != len(vs) or not ks:
         raise ValueError(f"{where}: k_caches and v_caches need one cache per layer each")
-    for t in ks + vs:
-        _need(t, "a layer's cache", torch.bfloat16, 4)
-        if t.shape != ks[0].shape:
-            raise ValueError(f"{where}: the layers' caches have different shapes")
-        _one_device(ks[0], cache=t)
-    return (_pointers(t.data_ptr() for t in ks), _pointers(t.data_ptr() for t in vs), len(ks),
+    if not _fine(dev, torch.bfloat16, *ks, *vs):
+        for t in ks + vs:
+            _need(t, "a layer's cache", torch.bfloat16, 4)
+            _one_device(ks[0], cache=t)
+    shape = ks[0].shape
+    if len(shape) != 4 or any(t.shape != shape for t in ks + vs):
+        raise ValueError(f"{where}: the layers' caches must have one shape [NB, Hkv, BS, D]")
+    return (_pointers([t.data_ptr() for t in ks]), _pointers([t.data_ptr() for t in vs]), len(ks),
             cache_desc(ks[0]), ks[0])
 
 
@@ -275,18 +292,21 @@ def paged_kv_copy_blocks(k_caches, v_caches, block_pairs: torch.Tensor,
     The caches: one layer's [NB, Hkv, BS, D], all layers in one [layers, NB, Hkv, BS, D], or
     a list of the layers' caches.  No destination may be another pair's source or destination.
     """
-    kp, vp, n, d, first = _layers(k_caches, v_caches, "paged_kv_copy_blocks")
-    _need(block_pairs, "block_pairs", torch.int32, 2)
-    if block_pairs.shape[1] != 2:
+    dev = _home(block_pairs)
+    kp, vp, n, d, first = _layers(k_caches, v_caches, dev, "paged_kv_copy_blocks")
+    if not _fine(dev, torch.int32, block_pairs, num_tokens):
+        _need(block_pairs, "block_pairs", torch.int32, 2)
+        if num_tokens is not None:
+            _need(num_tokens, "num_tokens", torch.int32, 1)
+        _one_device(first, block_pairs=block_pairs, num_tokens=num_tokens)
+    shape = block_pairs.shape
+    if len(shape) != 2 or shape[1] != 2:
         raise ValueError("block_pairs must be [n, 2]")
-    if num_tokens is not None:
-        _need(num_tokens, "num_tokens", torch.int32, 1)
-        if num_tokens.shape[0] != block_pairs.shape[0]:
-            raise ValueError("num_tokens must have one entry per pair")
-    _one_device(first, block_pairs=block_pairs, num_tokens=num_tokens)
-    _check(_lib.paged_kv_copy_blocks(kp.buffer_info()[0], vp.buffer_info()[0], n, _ptr(block_pairs), _ptr(num_tokens),
-                                     block_pairs.shape[0], ctypes.byref(d), _stream(stream)),
-           "paged_kv_copy_blocks")
+    if num_tokens is not None and num_tokens.shape != shape[:1]:
+        raise ValueError("num_tokens must have one entry per pair")
+    _check(_lib.paged_kv_copy_blocks(kp.buffer_info()[0], vp.buffer_info()[0], n,
+                                     block_pairs.data_ptr(), _ptr(num_tokens), shape[0],
+                                     ctypes.byref(d), _stream(stream, dev)), "paged_kv_copy_blocks")
 
 
 def paged_kv_compact(k_caches, v_caches, block_moves: torch.Tensor,
@@ -295,23 +315,29 @@ def paged_kv_compact(k_caches, v_caches, block_moves: torch.Tensor,
     """Pages block_moves[:, 0] move to the free pages block_moves[:, 1] ([n, 2] int32) in
     every layer, and block_tables [B, M] int32 is rewritten in place through block_map [NB]
     int32 (BlockManager.compact plans both; caches as in paged_kv_copy_blocks)."""
-    kp, vp, n, d, first = _layers(k_caches, v_caches, "paged_kv_compact")
-    _need(block_moves, "block_moves", torch.int32, 2)
-    if block_moves.shape[1] != 2:
+    dev = _home(block_moves)
+    kp, vp, n, d, first = _layers(k_caches, v_caches, dev, "paged_kv_compact")
+    if not _fine(dev, torch.int32, block_moves, block_tables, block_map):
+        _need(block_moves, "block_moves", torch.int32, 2)
+        if block_tables is not None:
+            _need(block_tables, "block_tables", torch.int32, 2)
+        if block_map is not None:
+            _need(block_map, "block_map", torch.int32, 1)
+        _one_device(first, block_moves=block_moves, block_tables=block_tables, block_map=block_map)
+    shape = block_moves.shape
+    if len(shape) != 2 or shape[1] != 2:
         raise ValueError("block_moves must be [n, 2]")
     rows = cols = 0
     if block_tables is not None:
-        _need(block_tables, "block_tables", torch.int32, 2)
-        if block_map is None:
-            raise ValueError("block_tables need a block_map")
-        _need(block_map, "block_map", torch.int32, 1)
-        if block_map.shape[0] != d.num_blocks:
-            raise ValueError("block_map must have one entry per block")
+        if block_tables.dim() != 2:
+            raise ValueError("block_tables must be [B, M]")
+        if block_map is None or block_map.shape != (d.num_blocks,):
+            raise ValueError("block_tables need a block_map with one entry per block")
         rows, cols = block_tables.shape
-    _one_device(first, block_moves=block_moves, block_tables=block_tables, block_map=block_map)
-    _check(_lib.paged_kv_compact(kp.buffer_info()[0], vp.buffer_info()[0], n, _ptr(block_moves), block_moves.shape[0],
-                                 _ptr(block_tables), rows, cols, _ptr(block_map), ctypes.byref(d),
-                                 _stream(stream)), "paged_kv_compact")
+    _check(_lib.paged_kv_compact(kp.buffer_info()[0], vp.buffer_info()[0], n,
+                                 block_moves.data_ptr(), shape[0], _ptr(block_tables), rows, cols,
+                                 _ptr(block_map), ctypes.byref(d), _stream(stream, dev)),
+           "paged_kv_compact")
 
 
 PATH_PARTITIONS, PATH_CLUSTER, PATH_PERSISTENT = 1, 2, 3
@@ -433,33 +459,42 @@ def paged_decode_shared_prefix_attention(out: torch.Tensor, q: torch.Tensor, k_c
     max_suffix_len bounds every context_len less the whole pages of its prefix; ``workspace``
     is as in paged_decode_attention, of ``paged_decode_shared_prefix_workspace_size`` bytes.
     """
-    _decode_checks(q, k_cache, v_cache, block_tables, context_lens)
-    _need(out, "out", torch.bfloat16, 3)
-    _need(group_start, "group_start", torch.int32, 1)
-    _need(prefix_lens, "prefix_lens", torch.int32, 1)
+    dev = _home(q)
+    if not (_fine(dev, torch.bfloat16, q, out, k_cache, v_cache) and
+            _fine(dev, torch.int32, block_tables, context_lens, group_start, prefix_lens)):
+        _decode_checks(q, k_cache, v_cache, block_tables, context_lens)
+        _need(out, "out", torch.bfloat16, 3)
+        _need(group_start, "group_start", torch.int32, 1)
+        _need(prefix_lens, "prefix_lens", torch.int32, 1)
+        _one_device(q, out=out, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                    context_lens=context_lens, group_start=group_start, prefix_lens=prefix_lens)
+    if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2 or prefix_lens.dim() != 1:
+        raise ValueError("q [B, Hq, D], cache [NB, Hkv, BS, D], block_tables [B, M], prefix_lens [G]")
+    B, Hq, D = q.shape
+    NB, Hkv, BS, Dk = k_cache.shape
+    rows, cols = block_tables.shape
+    groups = prefix_lens.shape[0]
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache shapes differ")
+    if rows != B or Dk != D or context_lens.shape != (B,):
+        raise ValueError("q [B, Hq, D], block_tables [B, M], context_lens [B], cache [NB, Hkv, BS, D] disagree")
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    groups = prefix_lens.shape[0]
-    if group_start.shape[0] != groups + 1:
+    if group_start.shape != (groups + 1,):
         raise ValueError("group_start must be [G + 1] for prefix_lens [G]")
-    _one_device(q, out=out, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                context_lens=context_lens, group_start=group_start, prefix_lens=prefix_lens,
-                workspace=workspace)
-    B, Hq, D = q.shape
-    NB, Hkv, BS, _ = k_cache.shape
     if workspace is None:
         need = paged_decode_shared_prefix_workspace_size(B, Hq, Hkv, D, groups, max_prefix_len,
                                                          max_suffix_len)
         workspace = torch.zeros(max(need, 1), dtype=torch.uint8, device=q.device)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace: must be contiguous")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous and on the current device")
     d = pkv_cache_desc(NB, BS, Hkv, D)
     _check(_lib.paged_decode_shared_prefix_attention(
-        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-        block_tables.shape[1], _ptr(context_lens), _ptr(group_start), _ptr(prefix_lens), groups,
-        int(max_prefix_len), int(max_suffix_len), B, Hq, ctypes.byref(d), float(scale),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
-        "paged_decode_shared_prefix_attention")
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        block_tables.data_ptr(), cols, context_lens.data_ptr(), group_start.data_ptr(),
+        prefix_lens.data_ptr(), groups, max_prefix_len, max_suffix_len, B, Hq, ctypes.byref(d),
+        scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream(stream, dev)), "paged_decode_shared_prefix_attention")
 
 
 def paged_decode_step(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -559,31 +594,35 @@ def prompt_attention(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: tor
     """Causal attention over whole prompts packed one after another: out, q [T, Hq, D], k, v
     [T, Hkv, D] bf16 (each token's heads contiguous; the tokens may be strided, e.g. slices
     of a fused projection), sequence b at rows query_start[b] .. query_start[b+1]-1."""
+    dev = _home(q)
     T, Hq, D = q.shape if q.dim() == 3 else (0, 0, 0)
+    row = []  # elements from one token to the next
     for t, name in ((out, "out"), (q, "q"), (k, "k"), (v, "v")):
-        if t.dtype != torch.bfloat16:
+        if t.dtype is not torch.bfloat16:
             raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-        if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D:
-            raise ValueError(f"{name}: expected [T, heads, D] with q's T and D, got shape {tuple(t.shape)}")
-        if T > 0 and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D)):
+        shape = t.shape
+        if len(shape) != 3 or shape[0] != T or shape[2] != D:
+            raise ValueError(f"{name}: expected [T, heads, D] with q's T and D, got shape {tuple(shape)}")
+        step, head, one = t.stride()
+        if T > 0 and (one != 1 or (shape[1] > 1 and head != D)):
             raise ValueError(f"{name}: a token's heads must be contiguous")
+        row.append(step if T > 1 else shape[1] * D)  # one token has no next one: any will do
     if out.shape != q.shape or k.shape != v.shape:
         raise ValueError("out must have q's shape, and v k's")
-    for t, name in ((out, "out"), (q, "q"), (k, "k"), (v, "v")):
-        if not t.is_cuda:
-            raise ValueError(f"{name}: must be a CUDA tensor")
-    _need(query_start, "query_start", torch.int32, 1)
-    if query_start.shape[0] < 1:
+    if not (out.get_device() == dev == k.get_device() == v.get_device() and
+            _fine(dev, torch.int32, query_start)):
+        _need(query_start, "query_start", torch.int32, 1)
+        if not q.is_cuda:
+            raise ValueError("q: must be a CUDA tensor")
+        _one_device(q, out=out, k=k, v=v, query_start=query_start)
+    if query_start.dim() != 1:
         raise ValueError("query_start must be [B + 1]")
-    _one_device(q, out=out, k=k, v=v, query_start=query_start)
-
-    def stride(t):  # one token has no next one: any stride will do
-        return t.stride(0) if T > 1 else t.shape[1] * D
-
-    _check(_lib.prompt_attention(_ptr(out), _ptr(q), _ptr(k), _ptr(v), stride(out), stride(q),
-                                 stride(k), stride(v), _ptr(query_start), T, int(max_query_len),
-                                 query_start.shape[0] - 1, Hq, k.shape[1], D, float(scale),
-                                 _stream(stream)), "prompt_attention")
+    seqs = query_start.shape[0] - 1
+    if seqs < 0:
+        raise ValueError("query_start must be [B + 1]")
+    _check(_lib.prompt_attention(out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), *row,
+                                 query_start.data_ptr(), T, max_query_len, seqs, Hq, k.shape[1], D,
+                                 scale, _stream(stream, dev)), "prompt_attention")
 
 
 def paged_decode_attention_noalloc(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
