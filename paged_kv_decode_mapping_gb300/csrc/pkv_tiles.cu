@@ -140,48 +140,56 @@ __device__ __forceinline__ bool clc_answer(uint32_t src, uint32_t &ctaid) {
   return got != 0;
 }
 
+// Where a search through the sequences stands: 32 of them from number `c`, one per lane, and
+// what lies before them.
+struct TileCursor {
+  int c = -32, carry = 0, next_carry = 0;  // the furthest end before these, and with them
+  int64_t before = 0;                      // pieces before these
+  int s = 0, len = 0, mine = 0, upto = 0, prefix = 0;
+};
+
 // The sequence (or group) whose pieces of `tokens` query tokens hold piece number idx, its
 // first query token, its length, the piece's place in it, its pieces and its prefix.  Whole
-// warps; misplaced and over-long sequences are moved, cut and flagged.
-__device__ __forceinline__ bool locate_tile(const TileArgs &a, int64_t idx, int tokens, int lane,
-                                            int &first, int &n, int &tile, int &ntiles,
+// warps; misplaced and over-long sequences are moved, cut and flagged.  The search goes on from
+// where the last one ended (from the beginning, 512 sequences of 84 tokens took 15 us an item).
+__device__ __forceinline__ bool locate_tile(const TileArgs &a, TileCursor &at, int64_t idx, int tokens,
+                                            int lane, int &first, int &n, int &tile, int &ntiles,
                                             int &prefix) {
-  int64_t before = 0;
-  for (int c = 0, carry = 0; c < a.num; c += 32) {
-    int s, len;
-    const int p = a.prefix_lens && c + lane < a.num ? __ldg(a.prefix_lens + c + lane) : 0;
-    disjoint_group(a.start, a.num, a.total, a.max_len, c, lane, carry, s, len);
-    const int mine = (len + tokens - 1) / tokens;
-    int upto = mine;
+  if (idx < at.before) at = TileCursor();
+  while (true) {
+    const int64_t total = at.before + __shfl_sync(0xffffffffu, at.upto, 31);
+    if (idx < total) break;
+    if (at.c + 32 >= a.num) return false;
+    at.c += 32;
+    at.before = total;
+    at.carry = at.next_carry;
+    at.prefix = a.prefix_lens && at.c + lane < a.num ? __ldg(a.prefix_lens + at.c + lane) : 0;
+    disjoint_group(a.start, a.num, a.total, a.max_len, at.c, lane, at.next_carry, at.s, at.len);
+    at.mine = at.upto = (at.len + tokens - 1) / tokens;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, upto, x);
-      if (lane >= x) upto += y;
+      const int y = __shfl_up_sync(0xffffffffu, at.upto, x);
+      if (lane >= x) at.upto += y;
     }
-    const unsigned past = __ballot_sync(0xffffffffu, before + upto > idx);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      prefix = __shfl_sync(0xffffffffu, p, l);
-      first = __shfl_sync(0xffffffffu, s, l);
-      n = __shfl_sync(0xffffffffu, len, l);
-      ntiles = __shfl_sync(0xffffffffu, mine, l);
-      tile = (int)(idx - before - __shfl_sync(0xffffffffu, upto - mine, l));
-      return true;
-    }
-    before += __shfl_sync(0xffffffffu, upto, 31);
   }
-  return false;
+  const int l = __ffs(__ballot_sync(0xffffffffu, at.before + at.upto > idx)) - 1;
+  prefix = __shfl_sync(0xffffffffu, at.prefix, l);
+  first = __shfl_sync(0xffffffffu, at.s, l);
+  n = __shfl_sync(0xffffffffu, at.len, l);
+  ntiles = __shfl_sync(0xffffffffu, at.mine, l);
+  tile = (int)(idx - at.before - __shfl_sync(0xffffffffu, at.upto - at.mine, l));
+  return true;
 }
 
 // The work of CTA (cta_x, cta_y), the same on every lane of the warp; false if it has none.
 template <int MODE>
-__device__ __forceinline__ bool make_item(const TileArgs &a, unsigned cta_x, unsigned cta_y, int lane,
-                                          TileItem &it) {
+__device__ __forceinline__ bool make_item(const TileArgs &a, TileCursor &at, unsigned cta_x, unsigned cta_y,
+                                          int lane, TileItem &it) {
   it.live = 1;
   it.g = (int)(cta_x % (unsigned)a.num_kv_heads);
   const int tokens = a.tile_tokens * (MODE == kPrompt ? 2 : 1);
   int tile, ntiles, prefix;
-  if (!locate_tile(a, cta_x / (unsigned)a.num_kv_heads, tokens, lane, it.first, it.n, tile, ntiles, prefix))
+  if (!locate_tile(a, at, cta_x / (unsigned)a.num_kv_heads, tokens, lane, it.first, it.n, tile, ntiles, prefix))
     return false;
   if constexpr (MODE == kPrompt) {
     it.tok0 = (ntiles - 1 - tile) * tokens;  // a sequence's last tiles see the most keys: first
@@ -371,7 +379,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   // The K producer finds the first item while the others set up.
   TileItem it = {};
   bool have = false;
-  if (kPaged || warp == kProducer) have = make_item<MODE>(a, blockIdx.x, blockIdx.y, lane, it);
+  TileCursor at;
+  if (kPaged || warp == kProducer) have = make_item<MODE>(a, at, blockIdx.x, blockIdx.y, lane, it);
   if (kPaged && !have) return;
   const TileItem first = it;  // kPrefix: the CTA's only one
   if (tid == 0) {
@@ -430,9 +439,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     return x.live != 0;
   };
   int issued = 0;  // producers: blocks loaded
+  auto nothing = [](int, int) {};
 
-  // Loads this warp's part of the item's K or V blocks into its ring; `issued` runs on.
-  auto load_ring = [&](bool is_k, const TileItem &x) {
+  // Loads this warp's part of the item's K or V blocks into its ring, between
+  // before(block, blocks) and after(block, blocks); `issued` runs on.
+  auto load_ring = [&](bool is_k, const TileItem &x, auto before, auto after) {
     const CUtensorMap *const tm = is_k ? &tmk : &tmv;
     const int ks = is_k ? KSK : KSV;
     const uint64_t policy = dev::policy_evict_last();  // other CTAs read the same keys
@@ -442,6 +453,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     int win = kPaged ? x.key0 >> a.cut.log2_bs : 0;
     int tb = kPaged && win + lane <= lb_last ? __ldg(trow + win + lane) : 0;
     for (int j = 0; j < nblk; ++j, ++issued) {
+      before(j, nblk);
       const int s = issued % ks;
       const uint32_t full = is_k ? k_full(s) : v_full(s), empty = is_k ? k_empty(s) : v_empty(s);
       if (issued >= ks && !__all_sync(0xffffffffu, dev::mbar_wait(empty, ((issued / ks) - 1) & 1))) {
@@ -455,6 +467,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                           lb_last, a, x.g, lane, policy);
       else if (lane == 0)
         load_packed_block(tm, dst, full, SL::kTile, x.first + j * kTcKeys, x.g, policy);
+      after(j, nblk);
     }
     return true;
   };
@@ -475,7 +488,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (have) {
       if (warp == kProducer && lane == 0) load_q(0, it);
       __syncwarp();
-      (void)load_ring(warp == kProducer, it);
+      (void)load_ring(warp == kProducer, it, nothing, nothing);
     }
   } else if (warp == kProducer) {
     // ------------------------------------------------- items, Q tiles and the K ring
@@ -495,13 +508,36 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       ++items;
       return true;
     };
-    while (true) {
-      if (lane == 0) {  // the next item, while this one's copies are issued
+    // The next item is asked for four blocks before this one's end and found two before it, so
+    // that its queries follow this one's last scores.
+    TileItem next = {};
+    bool more = false;
+    int asks = 0;
+    auto ask = [&] {
+      ++asks;
+      if (lane == 0) {
         dev::fence_proxy_async_smem();
         dev::mbar_arrive_expect_tx(clc_full, 16);
         clc_try_cancel(base + SL::clc, clc_full);
       }
-      if (have && (ok = publish(it))) {
+    };
+    auto find = [&] {
+      more = false;
+      if (!(ok = __all_sync(0xffffffffu, dev::mbar_wait(clc_full, asked & 1)) && ok)) {
+        if (lane == 0) fail(false);
+        return;
+      }
+      ++asked;
+      uint32_t cta = 0;
+      if (clc_answer(base + SL::clc, cta)) {
+        more = true;
+        have = make_item<MODE>(a, at, cta, 0, lane, next);
+      }
+      __syncwarp();  // every lane has read the answer: it may be overwritten
+    };
+    while (true) {
+      if (have) {
+        if (!(ok = publish(it))) break;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if ((t ? it.nb1 : it.nb0) == 0) continue;
@@ -512,25 +548,28 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ++qn[t];
           if (lane == 0) load_q(t, it);
         }
-        ok = ok && load_ring(true, it);
+        if (!ok) break;
+        auto early = [&](int j, int nblk) {
+          if (j == max(nblk - 4, 0)) ask();
+        };
+        auto late = [&](int j, int nblk) {  // the ring's free stages first
+          if (j == min(nblk - 1, max(nblk - 3, KSK - 1))) find();
+        };
+        ok = load_ring(true, it, early, late) && ok;
+      } else {
+        ask();
+        find();
       }
-      // always answered before the CTA may leave
-      if (!__all_sync(0xffffffffu, dev::mbar_wait(clc_full, asked & 1))) {
-        if (lane == 0) fail(false);
-        break;
-      }
-      ++asked;
-      uint32_t cta = 0;
-      if (!clc_answer(base + SL::clc, cta) || !ok) break;
-      have = make_item<MODE>(a, cta, 0, lane, it);
-      __syncwarp();  // every lane has read the answer: it may be overwritten
+      if (!ok || !more) break;
+      it = next;
     }
+    if (asks > asked) (void)dev::mbar_wait(clc_full, asked & 1);  // answered before the CTA may leave
     it.live = 0;
     (void)publish(it);
   } else if (warp == kProducerV) {
     // ------------------------------------------------- the V ring
     for (int items = 0; next_item(items, it); ++items)
-      if (!load_ring(false, it)) break;
+      if (!load_ring(false, it, nothing, nothing)) break;
   } else if (warp >= kMma) {
     // ------------------------------------- tensor-core issue, one thread for each tile:
     // what one of them does between its MMAs (waits, commits) runs under the other's.  They
@@ -696,8 +735,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         // a row that has seen no key yet takes its weights, all masked to 0, against 0
         const float m = m_ref == -INFINITY ? 0.f : m_ref;
-        const int nk = min(kTcKeys, it.t_end - k0);
-        if (kMask && nk < kTcKeys) {  // V rows past the staged keys are stale or another sequence's
+        // V rows past the prefix are stale, past the sequence another's
+        const int nk = (kPaged ? it.t_end : it.n) - k0;
+        if (kMask && nk < kTcKeys) {
           const int j = blocks + blk(t, i), s = j % KSV;
           if (!__all_sync(0xffffffffu, dev::mbar_wait(v_full(s), (j / KSV) & 1))) return false;
           const uint32_t vt = SL::v + s * SL::kTile;
