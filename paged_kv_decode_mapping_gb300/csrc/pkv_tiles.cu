@@ -94,7 +94,9 @@ struct TileSmem {
   // the tensor core forms the row sums (O's columns are free in TMEM at 64, not at 128)
   static constexpr bool kOnes = D == 64;
   static constexpr uint32_t ones = q + kQ * kTile;
-  static constexpr uint32_t item = ones + (kOnes ? kSub : 0);  // two items
+  // kPrompt: 64 dims of each softmax warp's 32 output rows, row r's 16-byte chunk c at c ^ (r & 7)
+  static constexpr uint32_t stage = ones + (kOnes ? kSub : 0);
+  static constexpr uint32_t item = stage + (MODE == kPrompt ? 2 * kTcRows * 128 : 0);  // two items
   static constexpr uint32_t clc = item + 2 * sizeof(TileItem); // a launch-control answer, 16 B
   // kPrefix, once the rings are done with: the tiles' rows [2][128][D] fp32, row r's 16-byte
   // chunk c at c ^ (r & 7), where the rings begin; (max in base 2, sum) per row at their end
@@ -279,13 +281,33 @@ __device__ __forceinline__ void load_packed_block(const CUtensorMap *tm, uint32_
 // straight-line form stalled on instruction fetches), and each half of P is published as
 // soon as it is stored, so that its P.V runs under the other half's exponentials.
 
-// The largest of columns c <= lim (all with kMask = false) of the row, unscaled; -inf if
-// there is none.  Leaves columns 0 .. 31 in x0.
+// A masked block's row sees the columns c <= lim; lo and hi are the least and the largest lim
+// of the warp, so that 32 columns that all its rows see, or none, cost no compares, the
+// latter no exponentials either (compares throughout: MASKUS).
+struct Limits {
+  int lim, lo, hi;
+};
+
+// The largest of the row's columns (with kMask: of those it sees), unscaled; -inf if there is
+// none.  Leaves columns 0 .. 31 in x0.
 template <bool kMask>
-__device__ __forceinline__ float row_max(uint32_t sb, int lim, uint32_t (&x0)[32]) {
+__device__ __forceinline__ float row_max(uint32_t sb, const Limits &l, uint32_t (&x0)[32]) {
   float mx[8];
 #pragma unroll
   for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
+  if constexpr (kMask) {
+#pragma unroll 1
+    for (int c0 = max(min(l.hi, kTcKeys - 1), 0) & ~31; c0 >= 0; c0 -= 32) {
+      dev::tmem_ld32(sb + c0, x0);
+      tmem_wait_ld_regs(x0);
+      const int lim = l.lo >= c0 + 31 ? 31 : l.lim - c0;
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        mx[e & 7] = fmax3(mx[e & 7], 2 * e <= lim ? __uint_as_float(x0[2 * e]) : -INFINITY,
+                          2 * e + 1 <= lim ? __uint_as_float(x0[2 * e + 1]) : -INFINITY);
+    }
+    return fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
+  }
   uint32_t xb[32];
   dev::tmem_ld32(sb + 96, xb);
   tmem_wait_ld_regs(xb);
@@ -296,10 +318,7 @@ __device__ __forceinline__ float row_max(uint32_t sb, int lim, uint32_t (&x0)[32
     if (ch > 0) dev::tmem_ld32(sb + (ch - 1) * 32, nxt);
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const int c = ch * 32 + 2 * e;
-      const float a = __uint_as_float(cur[2 * e]), b = __uint_as_float(cur[2 * e + 1]);
-      mx[e & 7] = fmax3(mx[e & 7], !kMask || c <= lim ? a : -INFINITY,
-                        !kMask || c + 1 <= lim ? b : -INFINITY);
+      mx[e & 7] = fmax3(mx[e & 7], __uint_as_float(cur[2 * e]), __uint_as_float(cur[2 * e + 1]));
     }
     if (ch > 0) tmem_wait_ld_regs(nxt);
   }
@@ -715,10 +734,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int u = 0; u < 4; ++u) ls[u] *= f;
       };
       // One block; false when a wait gave up.
-      auto block = [&](auto mask, int i, int k0, int lim) {
+      auto block = [&](auto mask, int i, int k0, const Limits &l) {
         constexpr bool kMask = decltype(mask)::value;
+        auto weights = [&](const uint32_t(&x)[32], int c0, uint32_t *pk, float m) {
+          if (!kMask || l.lo >= c0 + 31) {
+            chunk_exp<false, !kOnes>(x, c0, 0, scale_log2, m, pk, ls);
+          } else if (l.hi < c0) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[e] = 0u;
+          } else {
+            chunk_exp<true, !kOnes>(x, c0, l.lim, scale_log2, m, pk, ls);
+          }
+        };
         uint32_t xa[32];
-        const float mx = row_max<kMask>(sb, lim, xa);
+        const float mx = row_max<kMask>(sb, l, xa);
         const float bm = mx == -INFINITY ? -INFINITY : mx * scale_log2;
         if (i > 0) {
           // The reference moves only when the block raises it by more than kTcRescale.
@@ -752,10 +781,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int hf = 0; hf < 2; ++hf) {
           uint32_t xb[32], pk[32];
           dev::tmem_ld32(sb + 64 * hf + 32, xb);
-          chunk_exp<kMask, !kOnes>(xa, 64 * hf, lim, scale_log2, m, pk, ls);
+          weights(xa, 64 * hf, pk, m);
           tmem_wait_ld_regs(xb);
           if (hf == 0) dev::tmem_ld32(sb + 64, xa);
-          chunk_exp<kMask, !kOnes>(xb, 64 * hf + 32, lim, scale_log2, m, pk + 16, ls);
+          weights(xb, 64 * hf + 32, pk + 16, m);
           if (hf == 0) tmem_wait_ld_regs(xa);
           dev::tmem_st32(sb + 32 * hf, pk);  // over columns this thread has read
           dev::tmem_wait_st();
@@ -770,10 +799,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int lim = see - 1 - k0;  // columns c <= lim are seen
         if (!(ok = __all_sync(0xffffffffu, dev::mbar_wait(s_full(t), (sc + i) & 1)))) break;
         dev::tc_fence_after();
-        if (__all_sync(0xffffffffu, lim >= kTcKeys - 1))
-          ok = block(std::false_type{}, i, k0, lim);
-        else
-          ok = block(std::true_type{}, i, k0, lim);
+        const Limits l{lim, __reduce_min_sync(0xffffffffu, lim), __reduce_max_sync(0xffffffffu, lim)};
+        ok = l.lo >= kTcKeys - 1 ? block(std::false_type{}, i, k0, l) : block(std::true_type{}, i, k0, l);
       }
       if (ok && nb > 0) ok = __all_sync(0xffffffffu, dev::mbar_wait(pv_done(t), on & 1));
       if (!ok && lane == 0) fail(false);
@@ -809,23 +836,41 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
       } else if (nb > 0) {
         const float inv = 1.f / lsum;
-        uint4 *dst = reinterpret_cast<uint4 *>(a.out + token * a.out_stride + (int64_t)(it.g * G + h) * D);
+        // through shared memory, so that 8 lanes write 128 bytes of a row (a row per lane, 16
+        // bytes at a time, was a line per lane: EPIUS)
+        const uint64_t dst = valid ? reinterpret_cast<uint64_t>(
+                                         a.out + token * a.out_stride + (int64_t)(it.g * G + h) * D)
+                                   : 0;
+        uint8_t *const stage = bp + SL::stage + warp * 4096;
 #pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t o[32];
-          dev::tmem_ld32(ob + ch * 32, o);
+        for (int hf = 0; hf < D / 64; ++hf) {
+          uint32_t o[32], o2[32];
+          dev::tmem_ld32(ob + hf * 64, o);
+          dev::tmem_ld32(ob + hf * 64 + 32, o2);
           dev::tmem_wait_ld();
-          if (valid) {
+          auto put = [&](const uint32_t(&x)[32], int c0) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               uint32_t w4[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                w4[e] = dev::pack_bf16x2(__uint_as_float(o[8 * u + 2 * e]) * inv,
-                                         __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
-              dst[ch * 4 + u] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                w4[e] = dev::pack_bf16x2(__uint_as_float(x[8 * u + 2 * e]) * inv,
+                                         __uint_as_float(x[8 * u + 2 * e + 1]) * inv);
+              *reinterpret_cast<uint4 *>(stage + lane * 128 + (((c0 + u) ^ (lane & 7)) << 4)) =
+                  make_uint4(w4[0], w4[1], w4[2], w4[3]);
             }
+          };
+          put(o, 0);
+          put(o2, 4);
+          __syncwarp();
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int row = 4 * u + (lane >> 3), c = lane & 7;
+            const uint64_t to = __shfl_sync(0xffffffffu, dst, row);
+            const uint4 x = *reinterpret_cast<const uint4 *>(stage + row * 128 + ((c ^ (row & 7)) << 4));
+            if (to) *reinterpret_cast<uint4 *>(to + hf * 128 + c * 16) = x;
           }
+          __syncwarp();  // read before it is overwritten
         }
         dev::tc_fence_before();
         __syncwarp();
