@@ -61,7 +61,9 @@ struct TileArgs {
 };
 
 // 8 softmax warps, the K and the V producer (two warps a ring measured neutral), an MMA warp per
-// tile.
+// tile.  (Four more warps that write the output while the softmax warps go on to the next item:
+// two documents of 7000 and 8192 tokens 1% faster, prompts of 336 tokens 6% slower, and 8% at
+// head_dim 64: O_t has no second buffer in TMEM, so the next item's P.V waits all the same.)
 constexpr int kTileThreads = 32 * 12;
 constexpr int kItemReaders = 11;  // kPrompt's warps that read an item: all but the K producer
 
@@ -94,9 +96,10 @@ struct TileSmem {
   // the tensor core forms the row sums (O's columns are free in TMEM at 64, not at 128)
   static constexpr bool kOnes = D == 64;
   static constexpr uint32_t ones = q + kQ * kTile;
-  // kPrompt: 64 dims of each softmax warp's 32 output rows, row r's 16-byte chunk c at c ^ (r & 7)
+  // kPrompt: 32 dims of each softmax warp's 32 output rows, row r's 16-byte chunk c at
+  // c ^ (r / 2 & 3)
   static constexpr uint32_t stage = ones + (kOnes ? kSub : 0);
-  static constexpr uint32_t item = stage + (MODE == kPrompt ? 2 * kTcRows * 128 : 0);  // two items
+  static constexpr uint32_t item = stage + (MODE == kPrompt ? 2 * kTcRows * 64 : 0);  // two items
   static constexpr uint32_t clc = item + 2 * sizeof(TileItem); // a launch-control answer, 16 B
   // kPrefix, once the rings are done with: the tiles' rows [2][128][D] fp32, row r's 16-byte
   // chunk c at c ^ (r & 7), where the rings begin; (max in base 2, sum) per row at their end
@@ -275,6 +278,35 @@ __device__ __forceinline__ void load_packed_block(const CUtensorMap *tm, uint32_
       : "memory");
 }
 
+// dev::mbar_wait in as few instructions as it takes: the kernel waits in forty places, and
+// with 90 KB of code its warps spent a quarter of their time waiting for instructions
+// (128 prompts of 336 tokens, 217 us; with 57 KB 155 us).
+__device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity) {
+  uint64_t since = 0;
+#pragma unroll 1
+  while (!dev::mbar_try_wait(bar, parity)) {
+    const uint64_t now = dev::globaltimer_ns();
+    if (since == 0) since = now;
+    if (now - since > 2000000000ull) return false;
+  }
+  return true;
+}
+// __syncthreads from more than one place of the code.
+__device__ __forceinline__ void cta_sync() { asm volatile("bar.sync 0;" ::: "memory"); }
+// The whole warp's: true on every lane, or on none.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, tile_wait(bar, parity));
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // The softmax threads' work on one block, in two passes over the row's 128 columns of S_t,
 // 32 at a time out of TMEM.  The second pass is a loop over the two 64-column halves (its
@@ -283,7 +315,8 @@ __device__ __forceinline__ void load_packed_block(const CUtensorMap *tm, uint32_
 
 // A masked block's row sees the columns c <= lim; lo and hi are the least and the largest lim
 // of the warp, so that 32 columns that all its rows see, or none, cost no compares, the
-// latter no exponentials either (compares throughout: MASKUS).
+// latter no exponentials either (compares throughout: 512 prompts of 84
+// tokens 124 against 119 us).
 struct Limits {
   int lim, lo, hi;
 };
@@ -395,16 +428,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if constexpr (kPaged) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   auto blk = [&](int t, int i) { return kShareKeys ? i : 2 * i + t; };
 
-  // The K producer finds the first item while the others set up.
+  // kPrompt: the K producer looks for the first item while the others set up.
   TileItem it = {};
-  bool have = false;
   TileCursor at;
-  if (kPaged || warp == kProducer) have = make_item<MODE>(a, at, blockIdx.x, blockIdx.y, lane, it);
-  if (kPaged && !have) return;
+  bool have = false;
+  if (kPaged) {
+    have = make_item<MODE>(a, at, blockIdx.x, blockIdx.y, lane, it);
+    if (!have) return;
+  }
   const TileItem first = it;  // kPrefix: the CTA's only one
-  if (tid == 0) {
-    for (int i = 0; i < SL::kBars; ++i) {
-      const int r = i - kRings;
+  if (kPaged || warp != kProducer) {
+    if (tid < SL::kBars) {
+      const int i = tid, r = i - kRings;
       const uint32_t count = (i >= KSK && i < 2 * KSK) || (i >= 2 * KSK + KSV && i < kRings)
                                  ? (kShareKeys ? 2u : 1u)     // empty: both MMA threads, or one
                              : r >= 4 && r < 8 ? 4u           // p_half: one per softmax warp
@@ -414,27 +449,34 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                              : r == 20 ? 8u                   // tiles_done: every softmax warp
                                        : 1u;
       dev::mbar_init(bars + 8u * i, count);
+      dev::fence_mbar_init();
     }
-    *s_flag = 0;
-    s_turn[0] = s_turn[1] = 0;
-    dev::fence_mbar_init();
+    if (tid == 0) {
+      *s_flag = 0;
+      s_turn[0] = s_turn[1] = 0;
+    }
+    if (kOnes && tid < 256) {  // bf16 1.0 everywhere; read by the tensor core (async proxy)
+#pragma unroll 1
+      for (int i = tid; i < (int)(SL::kSub / 16); i += 256)
+        *reinterpret_cast<uint4 *>(bp + SL::ones + i * 16) =
+            make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    }
+    // rows of the Q tiles past the last whole token are never loaded: zeros
+    if (tid < 256) {
+      const int pad = (kTcRows - tile_rows) * 8;  // 16-byte pieces
+#pragma unroll 1
+      for (int sub = 0; sub < SL::kQ * (D / 64); ++sub)
+#pragma unroll 1
+        for (int i = tid; i < pad; i += 256)
+          *reinterpret_cast<uint4 *>(bp + SL::q + sub * SL::kSub + tile_rows * 128 + i * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+    }
+    dev::fence_proxy_async_smem();
+    if (warp == 0) dev::tmem_alloc(base + SL::tslot, 512);
+    dev::tc_fence_before();
+    cta_sync();
+    dev::tc_fence_after();
   }
-  if constexpr (kOnes) {  // bf16 1.0 everywhere; read by the tensor core (async proxy)
-    for (int i = tid; i < (int)(SL::kSub / 16); i += kTileThreads)
-      *reinterpret_cast<uint4 *>(bp + SL::ones + i * 16) =
-          make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-  }
-  // rows of the Q tiles past the last whole token are never loaded: zeros
-  for (int i = tid; i < SL::kQ * (D / 64) * (kTcRows - tile_rows) * 8; i += kTileThreads) {
-    const int sub = i / ((kTcRows - tile_rows) * 8), o = i - sub * (kTcRows - tile_rows) * 8;
-    *reinterpret_cast<uint4 *>(bp + SL::q + sub * SL::kSub + tile_rows * 128 + o * 16) =
-        make_uint4(0u, 0u, 0u, 0u);
-  }
-  dev::fence_proxy_async_smem();
-  if (warp == 0) dev::tmem_alloc(base + SL::tslot, 512);
-  dev::tc_fence_before();
-  __syncthreads();
-  dev::tc_fence_after();
   const uint32_t tmem = *s_tmem;  // S_t at column 128 t, O_t at 256 + kON t
 
   auto fail = [&](bool ok) {
@@ -448,7 +490,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto next_item = [&](int items, TileItem &x) {
     if constexpr (kPaged) return items == 0 && have;  // every warp found its CTA's one item
     const int s = items & 1;
-    if (!__all_sync(0xffffffffu, dev::mbar_wait(item_full(s), (items >> 1) & 1))) {
+    if (!warp_wait(item_full(s), (items >> 1) & 1)) {
       if (lane == 0) fail(false);
       return false;
     }
@@ -458,38 +500,35 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     return x.live != 0;
   };
   int issued = 0;  // producers: blocks loaded
-  auto nothing = [](int, int) {};
 
-  // Loads this warp's part of the item's K or V blocks into its ring, between
-  // before(block, blocks) and after(block, blocks); `issued` runs on.
-  auto load_ring = [&](bool is_k, const TileItem &x, auto before, auto after) {
+  // Loads blocks [from, to) of the item's K or V into this warp's ring, each after
+  // before(block); `issued` runs on.
+  auto load_ring = [&](bool is_k, const TileItem &x, int from, int to, auto before) {
     const CUtensorMap *const tm = is_k ? &tmk : &tmv;
     const int ks = is_k ? KSK : KSV;
     const uint64_t policy = dev::policy_evict_last();  // other CTAs read the same keys
-    const int nblk = (x.t_end - x.key0 + kTcKeys - 1) / kTcKeys;
     const int32_t *const trow = kPaged ? a.block_tables + (int64_t)x.first * a.cut.max_blocks : nullptr;
     const int lb_last = kPaged ? (x.t_end - 1) >> a.cut.log2_bs : 0;
-    int win = kPaged ? x.key0 >> a.cut.log2_bs : 0;
-    int tb = kPaged && win + lane <= lb_last ? __ldg(trow + win + lane) : 0;
-    for (int j = 0; j < nblk; ++j, ++issued) {
-      before(j, nblk);
+    [[maybe_unused]] int win = kPaged ? x.key0 >> a.cut.log2_bs : 0;
+    [[maybe_unused]] int tb = kPaged && win + lane <= lb_last ? __ldg(trow + win + lane) : 0;
+#pragma unroll 1
+    for (int j = from; j < to; ++j, ++issued) {
+      before(j);
       const int s = issued % ks;
       const uint32_t full = is_k ? k_full(s) : v_full(s), empty = is_k ? k_empty(s) : v_empty(s);
-      if (issued >= ks && !__all_sync(0xffffffffu, dev::mbar_wait(empty, ((issued / ks) - 1) & 1))) {
-        if (lane == 0) fail(false);
-        return false;
-      }
+      if (issued >= ks && !warp_wait(empty, ((issued / ks) - 1) & 1)) return false;
       const uint32_t dst = base + (is_k ? SL::k : SL::v) + s * SL::kTile;
       if constexpr (kPaged)
         load_paged_block<D, SL::kSub>(tm, dst, full, x.key0 + j * kTcKeys,
-                                          min(kTcKeys, x.t_end - x.key0 - j * kTcKeys), win, tb, trow,
-                                          lb_last, a, x.g, lane, policy);
+                                      min(kTcKeys, x.t_end - x.key0 - j * kTcKeys), win, tb, trow,
+                                      lb_last, a, x.g, lane, policy);
       else if (lane == 0)
         load_packed_block(tm, dst, full, SL::kTile, x.first + j * kTcKeys, x.g, policy);
-      after(j, nblk);
     }
     return true;
   };
+  auto nothing = [](int) {};
+  auto item_blocks = [](const TileItem &x) { return (x.t_end - x.key0 + kTcKeys - 1) / kTcKeys; };
   auto load_q = [&](int t, const TileItem &x) {  // one lane
     dev::mbar_arrive_expect_tx(q_full(t), (uint32_t)tile_rows * 128u * (D / 64));
 #pragma unroll
@@ -502,201 +541,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           : "memory");
   };
 
-  if (warp >= kProducer && warp < kMma && kPaged) {
-    // ------------------------------------------------- the Q tile, the K and V rings
-    if (have) {
-      if (warp == kProducer && lane == 0) load_q(0, it);
-      __syncwarp();
-      (void)load_ring(warp == kProducer, it, nothing, nothing);
-    }
-  } else if (warp == kProducer) {
-    // ------------------------------------------------- items, Q tiles and the K ring
-    int items = 0, asked = 0, qn[2] = {0, 0};
-    bool ok = true;
-    auto publish = [&](const TileItem &x) {
-      const int s = items & 1;
-      if (items >= 2 &&
-          !__all_sync(0xffffffffu, dev::mbar_wait(item_empty(s), ((items >> 1) - 1) & 1))) {
-        if (lane == 0) fail(false);
-        return false;
-      }
-      if (lane == 0) {
-        s_item[s] = x;
-        dev::mbar_arrive(item_full(s));
-      }
-      ++items;
-      return true;
-    };
-    // The next item is asked for four blocks before this one's end and found two before it, so
-    // that its queries follow this one's last scores.
-    TileItem next = {};
-    bool more = false;
-    int asks = 0;
-    auto ask = [&] {
-      ++asks;
-      if (lane == 0) {
-        dev::fence_proxy_async_smem();
-        dev::mbar_arrive_expect_tx(clc_full, 16);
-        clc_try_cancel(base + SL::clc, clc_full);
-      }
-    };
-    auto find = [&] {
-      more = false;
-      if (!(ok = __all_sync(0xffffffffu, dev::mbar_wait(clc_full, asked & 1)) && ok)) {
-        if (lane == 0) fail(false);
-        return;
-      }
-      ++asked;
-      uint32_t cta = 0;
-      if (clc_answer(base + SL::clc, cta)) {
-        more = true;
-        have = make_item<MODE>(a, at, cta, 0, lane, next);
-      }
-      __syncwarp();  // every lane has read the answer: it may be overwritten
-    };
-    while (true) {
-      if (have) {
-        if (!(ok = publish(it))) break;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if ((t ? it.nb1 : it.nb0) == 0) continue;
-          if (qn[t] > 0 && !(ok = __all_sync(0xffffffffu, dev::mbar_wait(q_free(t), (qn[t] - 1) & 1)))) {
-            if (lane == 0) fail(false);
-            break;
-          }
-          ++qn[t];
-          if (lane == 0) load_q(t, it);
-        }
-        if (!ok) break;
-        auto early = [&](int j, int nblk) {
-          if (j == max(nblk - 4, 0)) ask();
-        };
-        auto late = [&](int j, int nblk) {  // the ring's free stages first
-          if (j == min(nblk - 1, max(nblk - 3, KSK - 1))) find();
-        };
-        ok = load_ring(true, it, early, late) && ok;
-      } else {
-        ask();
-        find();
-      }
-      if (!ok || !more) break;
-      it = next;
-    }
-    if (asks > asked) (void)dev::mbar_wait(clc_full, asked & 1);  // answered before the CTA may leave
-    it.live = 0;
-    (void)publish(it);
-  } else if (warp == kProducerV) {
-    // ------------------------------------------------- the V ring
-    for (int items = 0; next_item(items, it); ++items)
-      if (!load_ring(false, it, nothing, nothing)) break;
-  } else if (warp >= kMma) {
-    // ------------------------------------- tensor-core issue, one thread for each tile:
-    // what one of them does between its MMAs (waits, commits) runs under the other's.  They
-    // take turns, P.V and the next S of one tile at a time: left to interleave, both tiles'
-    // scores came at the same moment and both softmaxes ran against each other while the
-    // tensor core idled (4011 against 3080 cycles per block pair at head_dim 128).
-    const int t = warp - kMma;
-    // a negative scale negates the queries instead, so that the softmax sees none
-    const uint32_t id_s =
-        dev::idesc_bf16_f32(kTcRows, kTcKeys, 0) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
-    constexpr uint32_t id_o = dev::idesc_bf16_f32(kTcRows, kON, 1);
-    const uint64_t dq = dev::smem_desc(base + SL::q + (kShareKeys ? t * SL::kTile : 0u), 16, 1024);
-    const uint64_t dk0 = dev::smem_desc(base + SL::k, 16, 1024);
-    // V stage s as the MN-major B operand: the next 64 columns are V's other half
-    // (head_dim 128) or the tile of ones, `lbo` bytes further on
-    auto dv = [&](int s) {
-      const uint32_t vs = SL::v + s * SL::kTile;
-      return dev::smem_desc(base + vs, kOnes ? SL::ones - vs : SL::kSub, 1024);
-    };
-    const uint32_t s_tm = tmem + 128u * t, o_tm = tmem + 256u + (uint32_t)(kON * t);
-    // Running counts over the items: blocks staged before this one (`blocks`), this tile's
-    // score blocks (sc) and live items (on), both tiles' P.V batches (b0, b1).  Every ring
-    // phase is seen by both threads of a prompt, in order.
-    int blocks = 0, sc = 0, on = 0, b0 = 0, b1 = 0;
-    bool ok = true;
-    for (int items = 0; ok && next_item(items, it); ++items) {
-      const int nblk = (it.t_end - it.key0 + kTcKeys - 1) / kTcKeys;
-      const int nb = t ? it.nb1 : it.nb0, nb0 = it.nb0, nb1 = it.nb1;
-      if (lane == 0) {
-        auto wait_k = [&](int i) {
-          const int j = blocks + blk(t, i);
-          return fail(dev::mbar_wait(k_full(j % KSK), (j / KSK) & 1));
-        };
-        auto issue_s = [&](int i) {
-          const int s = (blocks + blk(t, i)) % KSK;
-          issue_qk<D>(s_tm, dq, desc_add(dk0, s * SL::kTile), SL::kSub, id_s);
-          if (i > 0) s_turn[t] = (t ? b1 : b0) + i;
-          dev::umma_commit(s_full(t));
-          dev::umma_commit(k_empty(s));
-          if (kShareKeys && i + 1 == nb) dev::umma_commit(q_free(t));
-        };
-        // Until the other tile has issued this many batches.  Only a matter of order, so it
-        // counts (no phase to mistake) and, past its limit, goes on.
-        auto await_turn = [&](int batches) {
-          if (s_turn[t ^ 1] >= batches) return;
-          const uint64_t t0 = dev::globaltimer_ns();
-          for (uint32_t n = 1; s_turn[t ^ 1] < batches; ++n)
-            if ((n & 255u) == 0 && dev::globaltimer_ns() - t0 > 2000000000ull) return;
-        };
-        if (nb > 0) {
-          ok = fail(dev::mbar_wait(q_full(kShareKeys ? t : 0), on & 1)) && wait_k(0);
-          if (ok) {
-            dev::tc_fence_after();
-            issue_s(0);
-          }
-        }
-        for (int i = 0; ok && i < nb; ++i) {
-          const int j = blocks + blk(t, i), s = j % KSV, ph = (sc + i) & 1;
-          // every wait but one ahead of the turn, so that the turn is MMAs back to back
-          if (!(ok = fail(dev::mbar_wait(v_full(s), (j / KSV) & 1)))) break;
-          if (i + 1 < nb && !(ok = wait_k(i + 1))) break;
-          // the last item's O has been read
-          if (i == 0 && on > 0 && !(ok = fail(dev::mbar_wait(o_free(t), (on - 1) & 1)))) break;
-          if (!(ok = fail(dev::mbar_wait(p_half(t, 0), ph)))) break;
-          // after the other tile's turn: tile 1's i-1st, or tile 0's i-th, if it has one
-          await_turn(t ? b0 + min(i + 1, nb0) : b1 + min(i, nb1));
-          dev::tc_fence_after();
-          const uint64_t vd = dv(s), vh = desc_add(vd, 4 * 2048u);
-          // keys 0-63, then 64-127 of the block (waiting for both halves of P ahead of the
-          // turn measured 9% slower)
-          umma4_ts(o_tm, s_tm, s_tm + 8, s_tm + 16, s_tm + 24, vd, desc_add(vd, 2048),
-                   desc_add(vd, 4096), desc_add(vd, 6144), id_o, i > 0 ? 1u : 0u);
-          if (!(ok = fail(dev::mbar_wait(p_half(t, 1), ph)))) break;
-          dev::tc_fence_after();
-          umma4_ts(o_tm, s_tm + 32, s_tm + 40, s_tm + 48, s_tm + 56, vh, desc_add(vh, 2048),
-                   desc_add(vh, 4096), desc_add(vh, 6144), id_o, 1u);
-          // S_t(i+1) over S_t(i) and P_t(i), after the P.V that reads P_t(i): the MMAs of
-          // one thread run in issue order
-          if (i + 1 < nb) {
-            issue_s(i + 1);
-          } else {
-            s_turn[t] = (t ? b1 : b0) + nb;
-            dev::umma_commit(pv_done(t));
-          }
-          dev::umma_commit(v_empty(s));
-        }
-        // blocks of the other tile alone: seen, and let go of unread
-        for (int i = nb; kShareKeys && ok && i < nblk; ++i) {
-          const int j = blocks + i;
-          if (!(ok = fail(dev::mbar_wait(k_full(j % KSK), (j / KSK) & 1)))) break;
-          dev::mbar_arrive(k_empty(j % KSK));
-          if (!(ok = fail(dev::mbar_wait(v_full(j % KSV), (j / KSV) & 1)))) break;
-          dev::mbar_arrive(v_empty(j % KSV));
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-      blocks += nblk;
-      sc += nb;
-      on += nb > 0 ? 1 : 0;
-      b0 += nb0;
-      b1 += nb1;
-    }
-    if (lane == 0) dev::umma_commit(mma_done);
-  } else {
+  if (warp < kProducer) {
     // --------------------------------------------- softmax warps of tile t: row r each
     const int t = warp >> 2, wq = warp & 3;
     const int r = 32 * wq + lane;
-    const int tok = r / G, h = r - tok * G;  // the row's query token in the tile, its head
+    [[maybe_unused]] const int tok = r / G, h = r - tok * G;  // the row's query token in the tile, its head
     const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
     const uint32_t sb = tmem + lane_base + 128u * t;
     const uint32_t ob = tmem + lane_base + 256u + (uint32_t)(kON * t);
@@ -733,21 +582,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int u = 0; u < 4; ++u) ls[u] *= f;
       };
-      // One block; false when a wait gave up.
-      auto block = [&](auto mask, int i, int k0, const Limits &l) {
-        constexpr bool kMask = decltype(mask)::value;
-        auto weights = [&](const uint32_t(&x)[32], int c0, uint32_t *pk, float m) {
-          if (!kMask || l.lo >= c0 + 31) {
-            chunk_exp<false, !kOnes>(x, c0, 0, scale_log2, m, pk, ls);
-          } else if (l.hi < c0) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) pk[e] = 0u;
-          } else {
-            chunk_exp<true, !kOnes>(x, c0, l.lim, scale_log2, m, pk, ls);
-          }
-        };
+      for (int i = 0; i < nb && ok; ++i) {
+        const int k0 = it.key0 + blk(t, i) * kTcKeys;
+        const int lim = see - 1 - k0;  // columns c <= lim are seen
+        if (!(ok = warp_wait(s_full(t), (sc + i) & 1))) break;
+        dev::tc_fence_after();
+        const Limits l{lim, __reduce_min_sync(0xffffffffu, lim), __reduce_max_sync(0xffffffffu, lim)};
+        const bool masked = l.lo < kTcKeys - 1;
         uint32_t xa[32];
-        const float mx = row_max<kMask>(sb, l, xa);
+        const float mx = masked ? row_max<true>(sb, l, xa) : row_max<false>(sb, l, xa);
         const float bm = mx == -INFINITY ? -INFINITY : mx * scale_log2;
         if (i > 0) {
           // The reference moves only when the block raises it by more than kTcRescale.
@@ -764,45 +607,61 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         // a row that has seen no key yet takes its weights, all masked to 0, against 0
         const float m = m_ref == -INFINITY ? 0.f : m_ref;
-        // V rows past the prefix are stale, past the sequence another's
-        const int nk = (kPaged ? it.t_end : it.n) - k0;
-        if (kMask && nk < kTcKeys) {
-          const int j = blocks + blk(t, i), s = j % KSV;
-          if (!__all_sync(0xffffffffu, dev::mbar_wait(v_full(s), (j / KSV) & 1))) return false;
-          const uint32_t vt = SL::v + s * SL::kTile;
-          for (int idx = r; idx < (kTcKeys - nk) * (D / 8); idx += kTcRows) {
-            const int row = nk + idx / (D / 8), c = idx % (D / 8);
-            *reinterpret_cast<uint4 *>(bp + vt + (c >> 3) * SL::kSub + row * 128 +
-                                       (((c & 7) ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          dev::fence_proxy_async_smem();
-        }
-#pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t xb[32], pk[32];
-          dev::tmem_ld32(sb + 64 * hf + 32, xb);
-          weights(xa, 64 * hf, pk, m);
-          tmem_wait_ld_regs(xb);
-          if (hf == 0) dev::tmem_ld32(sb + 64, xa);
-          weights(xb, 64 * hf + 32, pk + 16, m);
-          if (hf == 0) tmem_wait_ld_regs(xa);
-          dev::tmem_st32(sb + 32 * hf, pk);  // over columns this thread has read
+        auto publish_half = [&](int hf) {
           dev::tmem_wait_st();
           dev::tc_fence_before();
           __syncwarp();
           if (lane == 0) dev::mbar_arrive(p_half(t, hf));
+        };
+        if (masked) {
+          // V rows past the prefix are stale, past the sequence another's
+          const int nk = (kPaged ? it.t_end : it.n) - k0;
+          if (nk < kTcKeys) {
+            const int j = blocks + blk(t, i), s = j % KSV;
+            if (!(ok = warp_wait(v_full(s), (j / KSV) & 1))) break;
+            const uint32_t vt = SL::v + s * SL::kTile;
+#pragma unroll 1
+            for (int idx = r; idx < (kTcKeys - nk) * (D / 8); idx += kTcRows) {
+              const int row = nk + idx / (D / 8), c = idx % (D / 8);
+              *reinterpret_cast<uint4 *>(bp + vt + (c >> 3) * SL::kSub + row * 128 +
+                                         (((c & 7) ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            dev::fence_proxy_async_smem();
+          }
+#pragma unroll 1
+          for (int c0 = 0; c0 < kTcKeys; c0 += 32) {
+            uint32_t pk[16];
+            if (c0 > 0) {
+              dev::tmem_ld32(sb + c0, xa);
+              tmem_wait_ld_regs(xa);
+            }
+            if (l.lo >= c0 + 31) {
+              chunk_exp<false, !kOnes>(xa, 0, 0, scale_log2, m, pk, ls);
+            } else if (l.hi < c0) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pk[e] = 0u;
+            } else {
+              chunk_exp<true, !kOnes>(xa, 0, l.lim - c0, scale_log2, m, pk, ls);
+            }
+            tmem_st16(sb + c0 / 2, pk);  // over columns this thread has read
+            if (c0 & 32) publish_half(c0 >> 6);
+          }
+        } else {
+#pragma unroll 1
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t xb[32], pk[32];
+            dev::tmem_ld32(sb + 64 * hf + 32, xb);
+            chunk_exp<false, !kOnes>(xa, 0, 0, scale_log2, m, pk, ls);
+            tmem_wait_ld_regs(xb);
+            if (hf == 0) dev::tmem_ld32(sb + 64, xa);
+            chunk_exp<false, !kOnes>(xb, 0, 0, scale_log2, m, pk + 16, ls);
+            if (hf == 0) tmem_wait_ld_regs(xa);
+            dev::tmem_st32(sb + 32 * hf, pk);  // over columns this thread has read
+            publish_half(hf);
+          }
         }
-        return true;
-      };
-      for (int i = 0; i < nb && ok; ++i) {
-        const int k0 = it.key0 + blk(t, i) * kTcKeys;
-        const int lim = see - 1 - k0;  // columns c <= lim are seen
-        if (!(ok = __all_sync(0xffffffffu, dev::mbar_wait(s_full(t), (sc + i) & 1)))) break;
-        dev::tc_fence_after();
-        const Limits l{lim, __reduce_min_sync(0xffffffffu, lim), __reduce_max_sync(0xffffffffu, lim)};
-        ok = l.lo >= kTcKeys - 1 ? block(std::false_type{}, i, k0, l) : block(std::true_type{}, i, k0, l);
       }
-      if (ok && nb > 0) ok = __all_sync(0xffffffffu, dev::mbar_wait(pv_done(t), on & 1));
+      if (ok && nb > 0) ok = warp_wait(pv_done(t), on & 1);
       if (!ok && lane == 0) fail(false);
       if (!ok && !kPaged) break;
       float lsum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
@@ -813,12 +672,56 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           dev::tmem_wait_ld();
         }
       }
+      if (!kPaged && nb > 0) {
+        // through shared memory, so that 4 lanes write 64 bytes of a row (a row per lane, 16
+        // bytes at a time, was a line per lane: 512 sequences of 84 tokens 167 against 124 us)
+        const float inv = 1.f / lsum;
+        const uint64_t dst = valid ? reinterpret_cast<uint64_t>(
+                                         a.out + token * a.out_stride + (int64_t)(it.g * G + h) * D)
+                                   : 0;  // the lane's row
+        uint8_t *const stage = bp + SL::stage + warp * 2048;
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t o[32];
+          dev::tmem_ld32(ob + ch * 32, o);
+          dev::tmem_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t w4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w4[e] = dev::pack_bf16x2(__uint_as_float(o[8 * u + 2 * e]) * inv,
+                                       __uint_as_float(o[8 * u + 2 * e + 1]) * inv);
+            *reinterpret_cast<uint4 *>(stage + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(w4[0], w4[1], w4[2], w4[3]);
+          }
+          if (ch == D / 32 - 1) dev::tc_fence_before();
+          __syncwarp();
+          // the next item's P.V may overwrite O_t
+          if (ch == D / 32 - 1 && lane == 0) dev::mbar_arrive(o_free(t));
+          uint4 x[4];  // all loads ahead of the stores, which they may not pass
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int row = 8 * u + (lane >> 2), c = lane & 3;
+            x[u] = *reinterpret_cast<const uint4 *>(stage + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint64_t to = __shfl_sync(0xffffffffu, dst, 8 * u + (lane >> 2));
+            if (to)
+              asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(to + ch * 64 + (lane & 3) * 16),
+                           "r"(x[u].x), "r"(x[u].y), "r"(x[u].z), "r"(x[u].w)
+                           : "memory");
+          }
+          __syncwarp();  // read before it is overwritten
+        }
+      }
       if constexpr (kPaged) {
         // This tile's rows (max, sum, unnormalised O) into shared memory, to be joined with the
         // other's below: the rings are done with once both tiles' MMAs are.
         __syncwarp();
         if (lane == 0) dev::mbar_arrive(tiles_done);
-        ok = __all_sync(0xffffffffu, dev::mbar_wait(tiles_done, 0)) && ok;
+        ok = warp_wait(tiles_done, 0) && ok;
         if (!ok && lane == 0) fail(false);
         reinterpret_cast<float2 *>(bp + SL::ml)[t * kTcRows + r] =
             nb > 0 && ok ? make_float2(m_ref, lsum) : make_float2(-INFINITY, 0.f);
@@ -834,56 +737,205 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 make_float4(__uint_as_float(o[4 * u]), __uint_as_float(o[4 * u + 1]),
                             __uint_as_float(o[4 * u + 2]), __uint_as_float(o[4 * u + 3]));
         }
-      } else if (nb > 0) {
-        const float inv = 1.f / lsum;
-        // through shared memory, so that 8 lanes write 128 bytes of a row (a row per lane, 16
-        // bytes at a time, was a line per lane: EPIUS)
-        const uint64_t dst = valid ? reinterpret_cast<uint64_t>(
-                                         a.out + token * a.out_stride + (int64_t)(it.g * G + h) * D)
-                                   : 0;
-        uint8_t *const stage = bp + SL::stage + warp * 4096;
-#pragma unroll 1
-        for (int hf = 0; hf < D / 64; ++hf) {
-          uint32_t o[32], o2[32];
-          dev::tmem_ld32(ob + hf * 64, o);
-          dev::tmem_ld32(ob + hf * 64 + 32, o2);
-          dev::tmem_wait_ld();
-          auto put = [&](const uint32_t(&x)[32], int c0) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              uint32_t w4[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w4[e] = dev::pack_bf16x2(__uint_as_float(x[8 * u + 2 * e]) * inv,
-                                         __uint_as_float(x[8 * u + 2 * e + 1]) * inv);
-              *reinterpret_cast<uint4 *>(stage + lane * 128 + (((c0 + u) ^ (lane & 7)) << 4)) =
-                  make_uint4(w4[0], w4[1], w4[2], w4[3]);
-            }
-          };
-          put(o, 0);
-          put(o2, 4);
-          __syncwarp();
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int row = 4 * u + (lane >> 3), c = lane & 7;
-            const uint64_t to = __shfl_sync(0xffffffffu, dst, row);
-            const uint4 x = *reinterpret_cast<const uint4 *>(stage + row * 128 + ((c ^ (row & 7)) << 4));
-            if (to) *reinterpret_cast<uint4 *>(to + hf * 128 + c * 16) = x;
-          }
-          __syncwarp();  // read before it is overwritten
-        }
-        dev::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) dev::mbar_arrive(o_free(t));  // the next item's P.V may overwrite O_t
       }
       blocks += (it.t_end - it.key0 + kTcKeys - 1) / kTcKeys;
       sc += nb;
       on += nb > 0 ? 1 : 0;
     }
+  } else {
+    if (kPaged && warp < kMma) {
+      // ----------------------------------------------- the Q tile, the K and V rings
+      if (warp == kProducer && lane == 0) load_q(0, it);
+      __syncwarp();
+      if (!load_ring(warp == kProducer, it, 0, item_blocks(it), nothing) && lane == 0) fail(false);
+    } else if (warp == kProducer) {
+      // ----------------------------------------------- items, Q tiles and the K ring
+      // The next item is asked for four blocks before this one's end and found two before it, so
+      // that its queries follow this one's last scores.
+      TileItem next = {};
+      uint32_t cta = blockIdx.x;                     // the piece to look for next, if there is
+      bool more = true, begun = false, found = false, ok = true;  // one; set up; looked for
+      int items = 0, asks = 0, answers = 0, qn0 = 0, qn1 = 0;
+      int j = 0, nblk = 0, split = 0;                // next block; blocks, those before `next`
+      auto publish = [&](const TileItem &x) {
+        const int s = items & 1;
+        if (items >= 2 && !warp_wait(item_empty(s), ((items >> 1) - 1) & 1)) return false;
+        if (lane == 0) {
+          s_item[s] = x;
+          dev::mbar_arrive(item_full(s));
+        }
+        ++items;
+        return true;
+      };
+      auto ask = [&] {
+        ++asks;
+        if (lane == 0) {
+          dev::fence_proxy_async_smem();
+          dev::mbar_arrive_expect_tx(clc_full, 16);
+          clc_try_cancel(base + SL::clc, clc_full);
+        }
+      };
+      while (true) {
+        const int stop = found ? nblk : split;
+        ok = load_ring(true, it, j, stop, [&](int b) {
+          if (b == max(nblk - 4, 0)) ask();
+        });
+        if (!ok) break;
+        j = stop;
+        if (!found) {
+          if (begun) {
+            if (!(ok = warp_wait(clc_full, answers & 1))) break;
+            ++answers;
+            more = clc_answer(base + SL::clc, cta);
+          }
+          have = more && make_item<MODE>(a, at, cta, 0, lane, next);
+          __syncwarp();  // every lane has read the answer: it may be overwritten
+          if (!begun) cta_sync();
+          begun = found = true;
+          continue;
+        }
+        if (!more) break;
+        found = false;
+        j = nblk = split = 0;
+        if (!have) {  // past the last sequence's
+          ask();
+          continue;
+        }
+        it = next;
+        if (!(ok = publish(it))) break;
+#pragma unroll 1
+        for (int t = 0; ok && t < 2; ++t) {
+          if ((t ? it.nb1 : it.nb0) == 0) continue;
+          const int n = t ? qn1++ : qn0++;
+          ok = n == 0 || warp_wait(q_free(t), (n - 1) & 1);
+          if (ok && lane == 0) load_q(t, it);
+        }
+        if (!ok) break;
+        nblk = item_blocks(it);
+        split = min(nblk, max(nblk - 2, KSK));       // the ring's free stages first
+      }
+      if (asks > answers) ok = warp_wait(clc_full, answers & 1) && ok;  // before the CTA may leave
+      it.live = 0;
+      ok = publish(it) && ok;
+      if (!ok && lane == 0) fail(false);
+    } else if (warp == kProducerV) {
+      // ----------------------------------------------- the V ring
+      bool ok = true;
+      for (int items = 0; ok && next_item(items, it); ++items)
+        ok = load_ring(false, it, 0, item_blocks(it), nothing);
+      if (!ok && lane == 0) fail(false);
+    } else {
+      // ----------------------------------- tensor-core issue, one thread for each tile:
+      // what one of them does between its MMAs (waits, commits) runs under the other's.  They
+      // take turns, P.V and the next S of one tile at a time: left to interleave, both tiles'
+      // scores came at the same moment and both softmaxes ran against each other while the
+      // tensor core idled (4011 against 3080 cycles per block pair at head_dim 128).
+      const int t = warp - kMma;
+      // a negative scale negates the queries instead, so that the softmax sees none
+      const uint32_t id_s =
+          dev::idesc_bf16_f32(kTcRows, kTcKeys, 0) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
+      constexpr uint32_t id_o = dev::idesc_bf16_f32(kTcRows, kON, 1);
+      const uint64_t dq = dev::smem_desc(base + SL::q + (kShareKeys ? t * SL::kTile : 0u), 16, 1024);
+      const uint64_t dk0 = dev::smem_desc(base + SL::k, 16, 1024);
+      // V stage s as the MN-major B operand: the next 64 columns are V's other half
+      // (head_dim 128) or the tile of ones, `lbo` bytes further on
+      auto dv = [&](int s) {
+        const uint32_t vs = SL::v + s * SL::kTile;
+        return dev::smem_desc(base + vs, kOnes ? SL::ones - vs : SL::kSub, 1024);
+      };
+      const uint32_t s_tm = tmem + 128u * t, o_tm = tmem + 256u + (uint32_t)(kON * t);
+      // Running counts over the items: blocks staged before this one (`blocks`), this tile's
+      // score blocks (sc) and live items (on), both tiles' P.V batches (b0, b1).  Every ring
+      // phase is seen by both threads of a prompt, in order.
+      int blocks = 0, sc = 0, on = 0, b0 = 0, b1 = 0;
+      bool ok = true;
+      for (int items = 0; ok && next_item(items, it); ++items) {
+        const int nblk = item_blocks(it);
+        const int nb = t ? it.nb1 : it.nb0, nb0 = it.nb0, nb1 = it.nb1;
+        if (lane == 0) {
+          // Until the other tile has issued this many batches.  Only a matter of order, so it
+          // counts (no phase to mistake) and, past its limit, goes on.
+          auto await_turn = [&](int batches) {
+            if (s_turn[t ^ 1] >= batches) return;
+            const uint64_t t0 = dev::globaltimer_ns();
+            for (uint32_t n = 1; s_turn[t ^ 1] < batches; ++n)
+              if ((n & 255u) == 0 && dev::globaltimer_ns() - t0 > 2000000000ull) return;
+          };
+          auto wait_k = [&](int i) {
+            const int j = blocks + blk(t, i);
+            return tile_wait(k_full(j % KSK), (j / KSK) & 1);
+          };
+          auto issue_s = [&](int i) {
+            const int s = (blocks + blk(t, i)) % KSK;
+            issue_qk<D>(s_tm, dq, desc_add(dk0, s * SL::kTile), SL::kSub, id_s);
+            if (i > 0) s_turn[t] = (t ? b1 : b0) + i;
+            dev::umma_commit(s_full(t));
+            dev::umma_commit(k_empty(s));
+            if (kShareKeys && i + 1 == nb) dev::umma_commit(q_free(t));
+          };
+          if (nb > 0) {
+            ok = tile_wait(q_full(kShareKeys ? t : 0), on & 1) && wait_k(0);
+            if (ok) {
+              dev::tc_fence_after();
+              issue_s(0);
+            }
+          }
+          for (int i = 0; ok && i < nb; ++i) {
+            const int j = blocks + blk(t, i), s = j % KSV, ph = (sc + i) & 1;
+            // every wait but one ahead of the turn, so that the turn is MMAs back to back
+            if (!(ok = tile_wait(v_full(s), (j / KSV) & 1))) break;
+            if (i + 1 < nb && !(ok = wait_k(i + 1))) break;
+            // the last item's O has been read
+            if (i == 0 && on > 0 && !(ok = tile_wait(o_free(t), (on - 1) & 1))) break;
+            if (!(ok = tile_wait(p_half(t, 0), ph))) break;
+            // after the other tile's turn: tile 1's i-1st, or tile 0's i-th, if it has one
+            await_turn(t ? b0 + min(i + 1, nb0) : b1 + min(i, nb1));
+            dev::tc_fence_after();
+            const uint64_t vd = dv(s), vh = desc_add(vd, 4 * 2048u);
+            // keys 0-63, then 64-127 of the block (waiting for both halves of P ahead of the
+            // turn measured 9% slower)
+            umma4_ts(o_tm, s_tm, s_tm + 8, s_tm + 16, s_tm + 24, vd, desc_add(vd, 2048),
+                     desc_add(vd, 4096), desc_add(vd, 6144), id_o, i > 0 ? 1u : 0u);
+            if (!(ok = tile_wait(p_half(t, 1), ph))) break;
+            dev::tc_fence_after();
+            umma4_ts(o_tm, s_tm + 32, s_tm + 40, s_tm + 48, s_tm + 56, vh, desc_add(vh, 2048),
+                     desc_add(vh, 4096), desc_add(vh, 6144), id_o, 1u);
+            // S_t(i+1) over S_t(i) and P_t(i), after the P.V that reads P_t(i): the MMAs of
+            // one thread run in issue order
+            if (i + 1 < nb) {
+              issue_s(i + 1);
+            } else {
+              s_turn[t] = (t ? b1 : b0) + nb;
+              dev::umma_commit(pv_done(t));
+            }
+            dev::umma_commit(v_empty(s));
+          }
+          // blocks of the other tile alone: seen, and let go of unread
+#pragma unroll 1
+          for (int i = nb; kShareKeys && ok && i < nblk; ++i) {
+            const int j = blocks + i;
+            if (!(ok = tile_wait(k_full(j % KSK), (j / KSK) & 1))) break;
+            dev::mbar_arrive(k_empty(j % KSK));
+            if (!(ok = tile_wait(v_full(j % KSV), (j / KSV) & 1))) break;
+            dev::mbar_arrive(v_empty(j % KSV));
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        blocks += nblk;
+        sc += nb;
+        on += nb > 0 ? 1 : 0;
+        b0 += nb0;
+        b1 += nb1;
+      }
+      if (lane == 0) {
+        if (!ok) fail(false);
+        dev::umma_commit(mma_done);
+      }
+    }
   }
 
   // ---- teardown: no tensor-core op or copy may still be in flight when TMEM is freed
-  if (tid == 0) (void)dev::mbar_wait(mma_done, 0);
+  if (tid == 0) (void)tile_wait(mma_done, 0);
   __syncthreads();
   if constexpr (kPaged) {
     // Both tiles' rows of a query row joined and written: the weights and the place of each row
@@ -948,9 +1000,9 @@ int prepare_tile_kernel() {
   if (rc) return rc;
   bool &set = g_tile_attr[dev][D == 64 ? 0 : 1][MODE];
   if (!set) {
-    const cudaError_t e = cudaFuncSetAttribute(tile_kernel<D, MODE>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)tile_smem<D, MODE>());
+    cudaError_t e = cudaFuncSetAttribute(tile_kernel<D, MODE>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)tile_smem<D, MODE>());
     if (e != cudaSuccess) return cuda_error(e, "cudaFuncSetAttribute");
     set = true;
   }
