@@ -492,8 +492,8 @@ def paged_decode_shared_prefix_attention(out: torch.Tensor, q: torch.Tensor, k_c
     _check(_lib.paged_decode_shared_prefix_attention(
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         block_tables.data_ptr(), cols, context_lens.data_ptr(), group_start.data_ptr(),
-        prefix_lens.data_ptr(), groups, max_prefix_len, max_suffix_len, B, Hq, ctypes.byref(d),
-        scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        prefix_lens.data_ptr(), groups, int(max_prefix_len), int(max_suffix_len), B, Hq,
+        ctypes.byref(d), float(scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         _stream(stream, dev)), "paged_decode_shared_prefix_attention")
 
 
@@ -621,8 +621,8 @@ def prompt_attention(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: tor
     if seqs < 0:
         raise ValueError("query_start must be [B + 1]")
     _check(_lib.prompt_attention(out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), *row,
-                                 query_start.data_ptr(), T, max_query_len, seqs, Hq, k.shape[1], D,
-                                 scale, _stream(stream, dev)), "prompt_attention")
+                                 query_start.data_ptr(), T, int(max_query_len), seqs, Hq, k.shape[1],
+                                 D, float(scale), _stream(stream, dev)), "prompt_attention")
 
 
 def paged_decode_attention_noalloc(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,

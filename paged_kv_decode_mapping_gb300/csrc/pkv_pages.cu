@@ -144,7 +144,7 @@ int launch_pages(pkv_bf16 *const *k_caches, pkv_bf16 *const *v_caches, int32_t n
     a.tables = remap ? tables : nullptr;
     a.entries = remap ? entries : 0;
     a.block_map = block_map;
-    int64_t x = num_pairs * a.chunks;
+    int64_t x = num_layers > 0 ? num_pairs * a.chunks : 0;
     if (x == 0) x = std::min<int64_t>((entries + kPageThreads - 1) / kPageThreads, 4096);
     const unsigned y = (unsigned)(a.planes + (remap ? 1 : 0));
     if (y > 0) {

@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (lane == 0) dev::mbar_arrive(item_empty(s));
     return x.live != 0;
   };
-  int issued = 0;  // producers: blocks loaded
+  int issued = 0, qn0 = 0, qn1 = 0;  // producers: blocks loaded, Q tiles of either tile
 
   // Loads blocks [from, to) of the item's K or V into this warp's ring, each after
   // before(block); `issued` runs on.
@@ -745,7 +745,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   } else {
     if (kPaged && warp < kMma) {
       // ----------------------------------------------- the Q tile, the K and V rings
-      if (warp == kProducer && lane == 0) load_q(0, it);
+      if (warp == kProducer) {
+        if (lane == 0) load_q(0, it);
+        ++qn0;
+      }
       __syncwarp();
       if (!load_ring(warp == kProducer, it, 0, item_blocks(it), nothing) && lane == 0) fail(false);
     } else if (warp == kProducer) {
@@ -755,7 +758,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       TileItem next = {};
       uint32_t cta = blockIdx.x;                     // the piece to look for next, if there is
       bool more = true, begun = false, found = false, ok = true;  // one; set up; looked for
-      int items = 0, asks = 0, answers = 0, qn0 = 0, qn1 = 0;
+      int items = 0, asks = 0, answers = 0;
       int j = 0, nblk = 0, split = 0;                // next block; blocks, those before `next`
       auto publish = [&](const TileItem &x) {
         const int s = items & 1;
@@ -806,9 +809,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll 1
         for (int t = 0; ok && t < 2; ++t) {
           if ((t ? it.nb1 : it.nb0) == 0) continue;
-          const int n = t ? qn1++ : qn0++;
-          ok = n == 0 || warp_wait(q_free(t), (n - 1) & 1);
-          if (ok && lane == 0) load_q(t, it);
+          const int n = t ? qn1 : qn0;
+          if (n > 0 && !(ok = warp_wait(q_free(t), (n - 1) & 1))) break;
+          (t ? qn1 : qn0) = n + 1;
+          if (lane == 0) load_q(t, it);
         }
         if (!ok) break;
         nblk = item_blocks(it);
@@ -972,12 +976,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           make_float4(join(x0.x, x1.x), join(x0.y, x1.y), join(x0.z, x1.z), join(x0.w, x1.w));
     }
   }
+  // a wait that gave up leaves copies possibly in flight: waited for (bounded)
   if (warp >= kProducer && warp < kMma && lane == 0 && *s_flag) {
+    if (qn0 > 0) (void)tile_wait(q_full(0), (qn0 - 1) & 1);
+    if (qn1 > 0) (void)tile_wait(q_full(1), (qn1 - 1) & 1);
     const int ks = warp < kProducerV ? KSK : KSV;
     for (int s = 0; s < ks; ++s) {
       const int last = s + ((issued - 1 - s) / ks) * ks;  // the last block on stage s
       if (last >= 0 && last < issued)
-        (void)dev::mbar_wait(warp < kProducerV ? k_full(s) : v_full(s), (last / ks) & 1);
+        (void)tile_wait(warp < kProducerV ? k_full(s) : v_full(s), (last / ks) & 1);
     }
   }
   dev::tc_fence_before();

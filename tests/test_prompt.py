@@ -2,8 +2,8 @@
 
 The allowed difference of an output o = sum p_t v_t, with A = sum p_t |v_t|: rounding it to
 bf16 moves it by at most 2^-8 |o|; the weights enter the product as bf16, each off by at
-most 2^-8 of itself, and are divided by the sum of the rounded weights, so the quotient
-moves by at most 2 * 2^-8 A; fp32 scores of 128 products and the hardware exp2 add less than
+most 2^-8 of itself, and are divided by the sum of the weights (of the rounded ones at
+head_dim 64, of the unrounded ones at 128), so the quotient moves by at most 2 * 2^-8 A; fp32 scores of 128 products and the hardware exp2 add less than
 2^-12 A (128 * 2^-24 of |scale q k| <= 30 in the exponent, plus 2^-22 per weight).
 """
 
@@ -113,6 +113,57 @@ def test_many_items_per_cta(B, hq, hkv, d):
         B.prompt_attention(out, q, k, v, start.cuda(), max(lens), d ** -0.5)
         check(out, o, amp)
     assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_short_sequences(B, d):
+    """Hundreds of sequences of a few tokens or none: a CTA's items lie far apart in the list,
+    and the grid holds many more pieces than there are."""
+    g = torch.Generator().manual_seed(d)
+    lens = torch.randint(-20, 30, (1100,), generator=g).clamp(min=0).tolist() + [0] * 200 + [50]
+    q, k, v, start = make(lens, 8, 2, d, True, seed=d)
+    out = torch.empty(q.shape[0], 8, d, dtype=torch.bfloat16, device="cuda")
+    o, amp = reference(q, k, v, start, d ** -0.5)
+    B.pkv_device_errors()
+    B.prompt_attention(out, q, k, v, start.cuda(), max(lens), d ** -0.5)
+    check(out, o, amp)
+    assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_past_4_gb(B, d):
+    """Token strides of 8 MB: the last rows lie past 2^31 elements and 2^32 bytes."""
+    step, lens = 1 << 22, [200, 370]
+    q, k, v, start = make(lens, 4, 2, d, False, seed=8)
+    base = torch.empty(4, sum(lens) * step, dtype=torch.bfloat16, device="cuda")
+    far = []
+    for x, t in zip((q, k, v, q), base):
+        y = t.as_strided((x.shape[0], x.shape[1], d), (step, d, 1))
+        far.append(y.copy_(x))
+    B.prompt_attention(far[3], far[0], far[1], far[2], start.cuda(), 370, d ** -0.5)
+    check(far[3], *reference(q, k, v, start, d ** -0.5))
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once(B):
+    """Two streams' calls beside each other, many times over."""
+    sets = [make([700, 90, 1300], 12, 4, 128, True, seed=1), make([33] * 60, 8, 2, 64, False, seed=2)]
+    refs = [reference(*x, 0.1) for x in sets]
+    starts = [x[3].cuda() for x in sets]
+    outs = [[torch.empty_like(x[0]) for _ in range(6)] for x in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for i in range(6):
+        for j, (q, k, v, start) in enumerate(sets):
+            with torch.cuda.stream(streams[j]):
+                B.prompt_attention(outs[j][i], q, k, v, starts[j], 1300, 0.1)
+    torch.cuda.synchronize()
+    for out, ref in zip(outs, refs):
+        for x in out:
+            check(x, *ref)
 
 
 @pytest.mark.gpu

@@ -2,8 +2,8 @@
 
 The allowed difference of an output o = sum p_t v_t, with A = sum p_t |v_t|: rounding it to
 bf16 moves it by at most 2^-8 |o|; the prefix's weights enter the product with V as bf16,
-each off by at most 2^-8 of itself, and are divided by the sum of the rounded weights, so
-that half moves by at most 2 * 2^-8 of its A (the tail's weights keep 16 bits); fp32
+each off by at most 2^-8 of itself, and are divided by the sum of the weights (of the
+rounded ones at head_dim 64, of the unrounded ones at 128), so that half moves by at most 2 * 2^-8 of its A (the tail's weights keep 16 bits); fp32
 scores, the hardware exp2 and the fp32 merge add less than 2^-12 A.
 """
 
@@ -201,6 +201,42 @@ def test_modes_agree(B):
         B.pkv_set_shared_prefix(mode)
         check(call(B, c, 0.125, ws), o, amp, f"mode {mode}")
     assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.gpu
+def test_pages_past_4_gb(B):
+    c = make([5], [700], [40] * 5, 16, 8, 128, 16, 6, poison=False)
+    o, amp = reference(c, 0.09)
+    nb, off = 135000, 135000 - c["k"].shape[0]  # 32 KB a page and head set
+    for x in ("k", "v"):
+        pool = torch.empty(nb, *c[x].shape[1:], dtype=torch.bfloat16, device="cuda")
+        pool[off:] = c[x]
+        c[x] = pool
+    c["tables"] = torch.where(c["tables"] >= 0, c["tables"] + off, c["tables"])
+    B.pkv_device_errors()
+    check(call(B, c, 0.09), o, amp)
+    assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once(B):
+    """Two streams, each with a workspace of its own, beside each other."""
+    sets = [make([30, 9], [2100, 900], [64] * 39, 16, 4, 64, 16, 3),
+            make([12], [3000], list(range(0, 600, 50)), 24, 8, 128, 32, 4)]
+    refs = [reference(c, 0.1) for c in sets]
+    spaces = [workspace(B, c) for c in sets]
+    outs = [[torch.empty_like(c["q"]) for _ in range(6)] for c in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for i in range(6):
+        for j, c in enumerate(sets):
+            with torch.cuda.stream(streams[j]):
+                call(B, c, 0.1, spaces[j], outs[j][i])
+    torch.cuda.synchronize()
+    for out, ref in zip(outs, refs):
+        for x in out:
+            check(x, *ref)
 
 
 @pytest.mark.gpu
