@@ -8,8 +8,10 @@
 // (pkv_tiles.cu); its splits leave (o, lse) partials.  The other half, tail_kernel below,
 // streams each sequence's own keys like the decode kernel does.  It is a programmatic
 // dependent of the first, so that its CTAs run beside the prefix's, on the SMs these leave,
-// and only store their parts.  Its last CTAs merge, a warp for a few heads of a sequence: they wait
-// for the prefix's grid and for the sequence's own parts.  (Merged by whichever part came
+// and only store their parts.  Its last CTAs merge, a warp for a few heads of a sequence: they
+// wait for the prefix's grid and for the sequence's own parts.  Measured: 64 sequences of 1 to
+// 1024 own keys over 8192 shared ones (24 / 8 heads of 128) 42.7 us, of which the prefix's
+// CTAs, 64 of them, run for 29 and the own keys' until 37; without sharing 258 us.  (Merged by whichever part came
 // last, by tickets, the last tile CTA of a group had 126 rows to merge alone, 7 us; merged by
 // each tail CTA after waiting for the prefix, the tail held its SMs until the prefix was done.)
 #include <cuda.h>
