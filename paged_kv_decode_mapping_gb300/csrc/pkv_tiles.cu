@@ -36,7 +36,7 @@ namespace pkv {
 //    of its own (about 9 us, the time of six key blocks).
 //    Measured: 8192 tokens of 24 / 8 heads of 128 at 1560 TFLOP/s, the tensor pipe 67% busy
 //    (a block pair takes 3080 cycles, 2080 of them MMAs; the exponentials and their rounding
-//    are the rest); 8192 of 32 / 8 heads of 64 at 920, the tensor pipe 42% busy: half the MMAs
+//    are the rest); 8192 of 32 / 8 heads of 64 at 900, the tensor pipe 42% busy: half the MMAs
 //    for the same softmax.  Short prompts end in what an item costs beside its blocks (an
 //    epilogue of 2000 cycles, the last P.V, the first S: about 2.6 us).
 //  * kPrefix: both tiles hold the same rows (queries of a group of sequences) and take
