@@ -10,10 +10,10 @@
 // dependent of the first, so that its CTAs run beside the prefix's, on the SMs these leave,
 // and only store their parts.  Its last CTAs merge, a warp for a few heads of a sequence: they
 // wait for the prefix's grid and for the sequence's own parts.  Measured: 64 sequences of 1 to
-// 1024 own keys over 8192 shared ones (24 / 8 heads of 128) 42.7 us, of which the prefix's
-// CTAs, 64 of them, run for 29 and the own keys' until 37; without sharing 258 us.  (Merged by whichever part came
-// last, by tickets, the last tile CTA of a group had 126 rows to merge alone, 7 us; merged by
-// each tail CTA after waiting for the prefix, the tail held its SMs until the prefix was done.)
+// 1024 own keys over 8192 shared ones (24 / 8 heads of 128) 37.6 us, of which the prefix's
+// CTAs, 64 of them, run for 29; without sharing 258 us.  (Merged by whichever part came last,
+// by tickets, the last tile CTA of a group had 126 rows to merge alone, 7 us; merged by each
+// tail CTA after waiting for the prefix, the tail held its SMs until the prefix was done.)
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -44,6 +44,21 @@ struct TailArgs {
   SharedCut cut;
 };
 
+// Stages of the ring and CTAs per SM.  At head_dim 128 three stages and two CTAs; with more
+// CTAs than those hold at once, two stages and three: their starts and ends, 5 us of 12, lie
+// under the others' streams (64 sequences of 1 to 1024 own keys over 8192: 42.6 against 37.6
+// us; 16 of 1 to 256, which all fit: 55.0 against 56.3 us).
+constexpr int tail_stages(int d, bool many) { return d == 64 ? 4 : many ? 2 : 3; }
+constexpr int tail_occupancy(int d, int stages) { return d == 64 || stages == 2 ? 3 : 2; }
+constexpr size_t tail_smem(int d, int stages) {
+  return 1024 + (size_t)stages * 2 * kChunk * d * 2 + stages * 16 + 16 + (size_t)kMaxGroup * d * 2;
+}
+constexpr size_t kTailStatic = 1024;  // of the kernel's own, at most
+static_assert(3 * (tail_smem(64, 4) + kTailStatic + 1024) <= 228 * 1024 &&
+                  3 * (tail_smem(128, 2) + kTailStatic + 1024) <= 228 * 1024 &&
+                  2 * (tail_smem(128, 3) + kTailStatic + 1024) <= 228 * 1024,
+              "tail CTAs per SM");
+
 constexpr int kSortSeqs = kThreads;  // one sequence per thread
 
 // One CTA per (sequence, kv head, partition of P tokens of the sequence's own keys): the
@@ -52,10 +67,10 @@ constexpr int kSortSeqs = kThreads;  // one sequence per thread
 // keep out the ones they wait for, and every wait is bounded.
 //
 // With more CTAs than fit at once the longest sequences go first, so that none of them starts
-// when the others end (64 sequences of 1 to 1024 own keys over 8192 shared ones: 47.5 against
-// 42.5 us).
+// when the others end (64 sequences of 1 to 1024 own keys over 8192 shared ones: 42.6 against
+// 37.7 us).
 template <int D, int STAGES>
-__global__ void __launch_bounds__(kThreads, split_occupancy(D))
+__global__ void __launch_bounds__(kThreads, tail_occupancy(D, STAGES))
     tail_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                 const TailArgs a) {
   constexpr int kTileBytes = kChunk * D * 2;
@@ -300,7 +315,7 @@ cudaError_t read_shared_errors(uint32_t *flags, int clear) { return read_tu_erro
 
 namespace {
 
-bool g_tail_attr[kMaxDevices][2];
+bool g_tail_attr[kMaxDevices][3];
 std::atomic<int> g_mode{PKV_SHARED_AUTO};  // PKV_SHARED_*, process-wide
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -309,6 +324,7 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 // tail CTA, and the workspace.
 struct SharedPlan {
   int32_t split_keys, splits, partition_tokens, parts, n_rows, sorted, merge_ctas, merge_heads, plain, plain_len;
+  int32_t stages;  // of the tail's ring
   int64_t tiles;  // row tiles over all groups, at most
   size_t o_part, lse_part, total;
 };
@@ -329,10 +345,12 @@ SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int
   // work over the SMs the shortest.  Measured, in us: a tile CTA 8.5 and, per block of 128
   // keys, what the TMA unit needs for its boxes of 16 rows (63 cycles each and 64 bytes a
   // cycle at 1.93 GHz) or the HBM for all CTAs' (6.5 TB/s); a tail CTA 4.5 and 34 KB a us, 2 or
-  // 3 to an SM.  Own lengths are taken at half the longest.
-  const int occ = split_occupancy(d);
+  // 3 to an SM, all of them at most the HBM's.  Own lengths are taken at half the longest.
   const double tail_ctas = (double)num_seqs * hkv * p.parts;
-  const double tail = tail_ctas * (4.5 + 0.5 * mlen / p.parts * d * 4 / 34e3) / occ;
+  p.stages = tail_stages(d, tail_ctas > (double)sms * tail_occupancy(d, tail_stages(d, false)));
+  const int occ = tail_occupancy(d, p.stages);
+  const double own = 0.5 * mlen / p.parts * d * 4;  // bytes of a tail CTA
+  const double tail = std::max(tail_ctas * (4.5 + own / 34e3) / occ, tail_ctas * own / 6.5e6 * sms);
   const double tma = d == 64 ? 0.79 : 1.57;
   double best = 0;
   p.splits = 1;
@@ -370,24 +388,23 @@ SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int
   p.total = std::max(p.total, paged_decode_workspace_size(num_seqs, hq, hkv, d, p.plain_len));
   // Little is read twice: the plain decode, one launch, is the faster one.  Measured, shared
   // against plain: 3 sequences over 512 tokens (2 MB saved) 8.3 against 7.5 us, 16 over 2048
-  // (63 MB) 10.6 against 12.7 us, 64 over 8192 (1 GB) 43 against 258 us.
+  // (63 MB) 10.9 against 12.7 us, 64 over 8192 (1 GB) 38 against 258 us.
   p.plain = (double)(num_seqs - groups) * max_prefix * hkv * d * 4 < 40e6;
   return p;
 }
 
-template <int D>
+template <int D, int S>
 int launch_tail(const CUtensorMap &tmk, const CUtensorMap &tmv, const TailArgs &a, dim3 grid,
                 bool programmatic, cudaStream_t stream) {
-  constexpr int S = split_stages(D);
   {
     std::lock_guard<std::mutex> lk(attn_mutex());
     int dev = 0;
     const int rc = current_device(&dev);
     if (rc) return rc;
-    bool &set = g_tail_attr[dev][D == 64 ? 0 : 1];
+    bool &set = g_tail_attr[dev][D == 64 ? 0 : S - 1];
     if (!set) {
       cudaError_t e = cudaFuncSetAttribute(tail_kernel<D, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)split_smem(D));
+                                           (int)tail_smem(D, S));
       if (e != cudaSuccess) return cuda_error(e, "cudaFuncSetAttribute");
       e = cudaFuncSetAttribute(tail_kernel<D, S>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
       if (e != cudaSuccess) return cuda_error(e, "cudaFuncSetAttribute(carveout)");
@@ -397,7 +414,7 @@ int launch_tail(const CUtensorMap &tmk, const CUtensorMap &tmv, const TailArgs &
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = split_smem(D);
+  cfg.dynamicSmemBytes = tail_smem(D, S);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -539,7 +556,9 @@ PKV_API int paged_decode_shared_prefix_attention(
   a.merge_heads = p.merge_heads;
   a.tail_ctas = (int32_t)tail_ctas;
   const dim3 grid((unsigned)(tail_ctas + p.merge_ctas));
-  rc = D == 64 ? launch_tail<64>(tmk, tmv, a, grid, prefix, s) : launch_tail<128>(tmk, tmv, a, grid, prefix, s);
+  rc = D == 64         ? launch_tail<64, 4>(tmk, tmv, a, grid, prefix, s)
+       : p.stages == 2 ? launch_tail<128, 2>(tmk, tmv, a, grid, prefix, s)
+                       : launch_tail<128, 3>(tmk, tmv, a, grid, prefix, s);
   if (!rc) clear_error();
   return rc;
 }

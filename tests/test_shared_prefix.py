@@ -168,6 +168,23 @@ def test_many_blocks_per_split(B, d, bs):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n,hkv,d,bs,most", [(50, 8, 128, 16, 900), (170, 4, 128, 32, 700),
+                                             (170, 4, 64, 16, 900), (36, 8, 128, 16, 300)])
+def test_many_tails(B, n, hkv, d, bs, most):
+    """More own parts than fit on the GPU at once, and (the last) just fewer; own lengths from
+    none to many ring stages, with and without the sort by length."""
+    rng = random.Random(n + d)
+    suffixes = [rng.choice([0, 1, 63, 64, 65, 129, rng.randint(0, most), most]) for _ in range(n)]
+    c = make([n // 2, n - n // 2], [600, 350], suffixes, 2 * hkv, hkv, d, bs, n, poison=False)
+    o, amp = reference(c, d ** -0.5)
+    ws = workspace(B, c)
+    B.pkv_device_errors()
+    for _ in range(3):
+        check(call(B, c, d ** -0.5, ws), o, amp)
+    assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d,scale", [(64, 1.0), (128, 1.0), (128, -0.5), (64, 0.0)])
 def test_wide_scores(B, d, scale):
     """Scores of tens, whose maxima jump from block to block and from prefix to tail."""
