@@ -310,9 +310,10 @@ int paged_decode_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k_c
  * paged_decode_attention.  All arguments are DEVICE memory.
  *
  * Two launches: the prefixes as matrix products on the tensor cores, and beside them, as a
- * programmatic dependent, every sequence's own keys and the log-sum-exp merge.  Where too
- * little would be read twice for that to pay (about 40 MB: see pkv_set_shared_prefix), the
- * call is paged_decode_attention's one launch, and the groups are not looked at.
+ * programmatic dependent, every sequence's own keys and the log-sum-exp merge.  Where that
+ * does not pay by the sizes (little is read twice, or there are hundreds of small groups with
+ * short prefixes: see pkv_set_shared_prefix), the call is paged_decode_attention's one launch,
+ * and the groups are not looked at.
  */
 size_t paged_decode_shared_prefix_workspace_size(int32_t num_seqs, int32_t num_q_heads,
                                                  int32_t num_kv_heads, int32_t head_dim,

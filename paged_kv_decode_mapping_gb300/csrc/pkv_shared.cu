@@ -352,18 +352,19 @@ SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int
   const double own = 0.5 * mlen / p.parts * d * 4;  // bytes of a tail CTA
   const double tail = std::max(tail_ctas * (4.5 + own / 34e3) / occ, tail_ctas * own / 6.5e6 * sms);
   const double tma = d == 64 ? 0.79 : 1.57;
-  double best = 0;
+  double best = 0, shared = 0;  // the choice's cost, and its time with the launch's 3 us once
   p.splits = 1;
   for (int64_t n = 1; n <= std::min<int64_t>(blocks, 1024); ++n) {
     const double ctas = (double)units * n;
     if (n > 1 && ctas > sms) break;
-    const double hbm = (double)groups * hkv * n * kTileKeys * d * 4 / 6.5e6;
+    const double hbm = (double)groups * hkv * n * kTileKeys * d * 4 / 6.5e6 * std::min(1., sms / ctas);
     const double tile = 8.5 + (double)((blocks + n - 1) / n) * std::max(tma, hbm);
     const double fits = ctas + tail_ctas / occ <= sms ? 0 : 5;  // or the tail begins after it
     const double t = std::max(tile, (tail + std::min<double>(ctas, sms) * tile) / sms) + fits;
     if (n == 1 || t < best) {
       best = t;
       p.splits = (int32_t)n;
+      shared = std::max(tile, 3 + (tail + ctas * (tile - 3)) / sms) + fits;
     }
   }
   p.split_keys = (int32_t)std::min<int64_t>(
@@ -386,10 +387,16 @@ SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int
   p.total = p.lse_part + up256(prow * sizeof(float));
   p.plain_len = (int32_t)std::min<int64_t>((int64_t)max_prefix + max_suffix, 0x7fffffff);
   p.total = std::max(p.total, paged_decode_workspace_size(num_seqs, hq, hkv, d, p.plain_len));
-  // Little is read twice: the plain decode, one launch, is the faster one.  Measured, shared
-  // against plain: 3 sequences over 512 tokens (2 MB saved) 8.3 against 7.5 us, 16 over 2048
-  // (63 MB) 10.9 against 12.7 us, 64 over 8192 (1 GB) 38 against 258 us.
-  p.plain = (double)(num_seqs - groups) * max_prefix * hkv * d * 4 < 40e6;
+  // The plain decode, one launch, is the faster one where little is read twice, and where
+  // there are so many short groups that their CTAs' starts cost more than the reads (the last
+  // term: tasks a merging warp has after its first, 11 us each).  Plain: 5.5 us and every key
+  // at 7.5 TB/s, shared pages coming from L2 in part.  Measured, shared against plain, us: 3
+  // sequences over 512 tokens 8.3, 7.5; 16 over 2048 10.9, 12.7; 64 over 8192 38, 258; groups
+  // of 4 over 1000 tokens (32 / 8 heads of 64), 16 of them 20, 30, 64 of them 71, 76, 256 of
+  // them 339, 276; 256 groups of 16 over 250 tokens 745, 366.
+  shared += std::max(0., (double)tasks / cap - 1) * 11;
+  const double plain = 5.5 + (double)num_seqs * hkv * (max_prefix + 0.5 * mlen) * d * 4 / 7.5e6;
+  p.plain = plain < 0.9 * shared;
   return p;
 }
 
