@@ -265,6 +265,19 @@ def test_copy_blocks_list_of_layers_and_one_layer(B):
 
 
 @pytest.mark.gpu
+def test_nothing_to_do(B):
+    k = torch.randn(8, 2, 16, 64, device="cuda").to(torch.bfloat16)
+    was, none = k.clone(), torch.zeros(0, 2, dtype=torch.int32, device="cuda")
+    B.paged_kv_copy_blocks(k, k, none)
+    B.paged_kv_copy_blocks(k, k, none, none[:, 0].contiguous())
+    B.paged_kv_compact(k, k, none)
+    B.paged_kv_compact(k, k, none, torch.zeros(0, 4, dtype=torch.int32, device="cuda"),
+                       torch.arange(8, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(k, was) and B.pkv_device_errors() == 0
+
+
+@pytest.mark.gpu
 def test_copy_blocks_skips_bad_pairs_and_clamps_rows(B):
     """Blocks outside the pool are skipped and flagged, bad row counts clamped and flagged,
     and src == dst does nothing; the good pairs of the same call are copied."""

@@ -238,6 +238,16 @@ def test_strides_streams_and_graphs(B):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("seqs", [0, 3])
+def test_nothing_to_do(B, seqs):
+    q, k = (torch.zeros(0, h, 64, dtype=torch.bfloat16, device="cuda") for h in (4, 2))
+    start = torch.zeros(seqs + 1, dtype=torch.int32, device="cuda")
+    B.prompt_attention(torch.empty_like(q), q, k, k, start, 5, 0.1)
+    torch.cuda.synchronize()
+    assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.gpu
 def test_bad_starts_are_flagged(B):
     """Sequences that are too long, run backwards or leave the tensors are cut and flagged;
     the others are computed."""

@@ -208,6 +208,20 @@ def test_contexts_shorter_than_the_prefix(B, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("groups", [0, 1])
+@pytest.mark.parametrize("n", [0, 2])
+def test_nothing_to_do(B, n, groups):
+    """No sequences; sequences without keys (zeros)."""
+    q = torch.ones(n, 4, 64, dtype=torch.bfloat16, device="cuda")
+    k = torch.ones(8, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    c = dict(q=q, k=k, v=k, tables=torch.zeros(n, 4, dtype=torch.int32, device="cuda"),
+             lens=torch.zeros(n, dtype=torch.int32, device="cuda"),
+             start=torch.zeros(groups + 1, dtype=torch.int32, device="cuda"),
+             prefix=torch.zeros(groups, dtype=torch.int32, device="cuda"), max_prefix=0, max_suffix=64)
+    assert bool((call(B, c, 0.1) == 0).all()) and B.pkv_device_errors() == 0
+
+
+@pytest.mark.gpu
 def test_modes_agree(B):
     """Shared, plain and by size, in turn on one workspace."""
     c = make([20, 4], [1000, 2500], list(range(24)), 32, 8, 64, 16, 1)
