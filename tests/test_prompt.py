@@ -80,6 +80,9 @@ CASES = [
     ([5, 260], 10, 2, 128, True),                 # group 5
     ([1100], 3, 1, 64, False),
     ([1] * 70 + [130] * 3, 4, 2, 64, False),      # more sequences than a warp has lanes
+    ([60, 7, 131], 128, 1, 64, True),             # a token fills a tile
+    ([40, 129], 100, 1, 128, False),              # tiles of one token and 28 empty rows
+    ([50, 3], 65, 1, 64, True),
 ]
 
 
