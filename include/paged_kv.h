@@ -304,10 +304,13 @@ int paged_decode_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k_c
  * the whole pages of its group's prefix; both are at most max_blocks_per_seq * block_size.
  * A longer one is cut there, a group that begins inside the one before it or leaves the
  * batch is moved or cut, and PKV_DEVERR_CONTEXT_LEN is raised.  Layouts, supported sizes,
- * alignment, and the rules for the workspace (zero-filled before its first use, left ready
- * by every call for the next one with as many sequences and kv heads, not shared by calls
- * that overlap; paged_decode_shared_prefix_workspace_size() bytes) are those of
- * paged_decode_attention.  All arguments are DEVICE memory.
+ * and alignment are those of paged_decode_attention.  All arguments are DEVICE memory.
+ *
+ * The workspace (paged_decode_shared_prefix_workspace_size() bytes) must be zero-filled
+ * before its first use, and every call that completes leaves it ready for the next one, of
+ * any sizes up to 65536 (sequence, kv head) pairs that it is large enough for: calls, or
+ * captured graphs, for many batch sizes may take turns on one.  Not two that overlap, and not
+ * paged_decode_attention's calls with these.
  *
  * Two launches: the prefixes as matrix products on the tensor cores, and beside them, as a
  * programmatic dependent, every sequence's own keys and the log-sum-exp merge.  Where that

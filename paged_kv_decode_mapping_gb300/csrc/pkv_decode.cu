@@ -1635,7 +1635,7 @@ int decode_fused(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k_cache,
                  const int32_t *context_lens, int32_t max_context_len, int32_t num_seqs,
                  int32_t num_q_heads, const pkv_cache_desc *cache, float scale, void *workspace,
                  size_t workspace_bytes, cudaStream_t s, bool programmatic, bool launch,
-                 const char *fn, bool q_wait = false) {
+                 const char *fn, bool q_wait = false, uint32_t *words = nullptr) {
   int rc = check_decode(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
                         max_context_len, num_seqs, num_q_heads, cache, fn);
   if (rc) return rc;
@@ -1654,12 +1654,12 @@ int decode_fused(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k_cache,
     return set_error(PKV_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
   if (!launch) return PKV_OK;
   char *ws = static_cast<char *>(workspace);
-  uint32_t *counters = reinterpret_cast<uint32_t *>(ws + f.counters);
+  uint32_t *sched = words ? words : reinterpret_cast<uint32_t *>(ws + f.sched);
+  uint32_t *counters = words ? words + 2 : reinterpret_cast<uint32_t *>(ws + f.counters);
   float *o_part = reinterpret_cast<float *>(ws + f.o_part);
   float *lse_part = reinterpret_cast<float *>(ws + f.lse_part);
   const int path = decode_path(num_seqs, cache->num_kv_heads, D, mlen, P, sms_or_default(0));
   if (path == PKV_PATH_PERSISTENT) {
-    uint32_t *sched = reinterpret_cast<uint32_t *>(ws + f.sched);
     return D == 64 ? launch_persistent<64>(q, k_cache, v_cache, block_tables, max_blocks_per_seq,
                                            context_lens, mlen, num_seqs, num_q_heads, *cache,
                                            scale, P, o_part, lse_part, out, counters, sched, s,
@@ -1693,6 +1693,17 @@ int check_decode_attention(const pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf1
   return decode_fused(const_cast<pkv_bf16 *>(out), q, k_cache, v_cache, block_tables,
                       max_blocks_per_seq, context_lens, max_context_len, num_seqs, num_q_heads,
                       cache, 1.f, aligned_stand_in, workspace_bytes, nullptr, false, false, fn);
+}
+
+int decode_attention_words(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k_cache,
+                           const pkv_bf16 *v_cache, const int32_t *block_tables,
+                           int32_t max_blocks_per_seq, const int32_t *context_lens,
+                           int32_t max_context_len, int32_t num_seqs, int32_t num_q_heads,
+                           const pkv_cache_desc *cache, float scale, uint32_t *words,
+                           void *workspace, size_t workspace_bytes, cudaStream_t s, const char *fn) {
+  return decode_fused(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                      max_context_len, num_seqs, num_q_heads, cache, scale, workspace,
+                      workspace_bytes, s, false, true, fn, false, words);
 }
 
 }  // namespace pkv

@@ -99,6 +99,14 @@ int query_map(const pkv_bf16 *x, int64_t tokens, int32_t heads, int32_t d, int64
 int check_decode(const void *q, const void *k_cache, const void *v_cache, const int32_t *bt,
                  int32_t max_blocks, const int32_t *lens, int32_t max_len, int32_t num_seqs,
                  int32_t hq, const pkv_cache_desc *c, const char *fn);
+// paged_decode_attention with the words that are zero between calls apart from the workspace's
+// partials: words [2 + num_seqs * num_kv_heads] (the persistent kernel's two, the counters).
+int decode_attention_words(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k_cache,
+                           const pkv_bf16 *v_cache, const int32_t *block_tables,
+                           int32_t max_blocks_per_seq, const int32_t *context_lens,
+                           int32_t max_context_len, int32_t num_seqs, int32_t num_q_heads,
+                           const pkv_cache_desc *cache, float scale, uint32_t *words,
+                           void *workspace, size_t workspace_bytes, cudaStream_t s, const char *fn);
 int ilog2(int x);  // smallest r with 2^r >= x
 // Every host check paged_decode_attention makes (shape, pointers, alignment, the
 // planned workspace against `workspace_bytes`), without enqueuing anything, for a caller

@@ -326,8 +326,13 @@ struct SharedPlan {
   int32_t split_keys, splits, partition_tokens, parts, n_rows, sorted, merge_ctas, merge_heads, plain, plain_len;
   int32_t stages;  // of the tail's ring
   int64_t tiles;  // row tiles over all groups, at most
-  size_t o_part, lse_part, total;
+  size_t partials, o_part, lse_part, total;
 };
+
+// The words that are zero between calls -- the plain decode's two and a counter per (sequence,
+// kv head) -- have the front of the workspace to themselves, as long for all calls of up to
+// this many: no call's partial rows lie where another's counters are, whatever their sizes.
+constexpr size_t kWords = 65536;
 
 SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int32_t num_groups,
                        int32_t max_prefix, int32_t max_suffix, int sms) {
@@ -382,11 +387,12 @@ SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int
   }
   p.merge_ctas = (int32_t)((std::min(tasks, cap) + warps - 1) / warps);
   const size_t prow = (size_t)num_seqs * hq * p.n_rows;
-  p.o_part = up256((size_t)num_seqs * hkv * 4 + 8);  // behind the plain decode's words too
+  p.partials = up256((std::max((size_t)num_seqs * hkv, kWords) + 2) * 4);
+  p.o_part = p.partials;
   p.lse_part = p.o_part + up256(prow * d * sizeof(float));
   p.total = p.lse_part + up256(prow * sizeof(float));
   p.plain_len = (int32_t)std::min<int64_t>((int64_t)max_prefix + max_suffix, 0x7fffffff);
-  p.total = std::max(p.total, paged_decode_workspace_size(num_seqs, hq, hkv, d, p.plain_len));
+  p.total = std::max(p.total, p.partials + paged_decode_workspace_size(num_seqs, hq, hkv, d, p.plain_len));
   // The plain decode, one launch, is the faster one where little is read twice, and where
   // there are so many short groups that their CTAs' starts cost more than the reads (the last
   // term: tasks a merging warp has after its first, 11 us each).  Plain: 5.5 us and every key
@@ -500,10 +506,15 @@ PKV_API int paged_decode_shared_prefix_attention(
   if (mode == PKV_SHARED_NEVER || (mode == PKV_SHARED_AUTO && p.plain)) {
     const int64_t cap = (int64_t)max_blocks_per_seq * cache->block_size;
     const int32_t len = (int32_t)std::min<int64_t>(p.plain_len, cap);
-    if (workspace_bytes >= paged_decode_workspace_size(num_seqs, num_q_heads, hkv, D, len))
-      return paged_decode_attention(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
-                                    context_lens, len, num_seqs, num_q_heads, cache, scale, workspace,
-                                    workspace_bytes, stream);
+    if (workspace_bytes >= p.partials + paged_decode_workspace_size(num_seqs, num_q_heads, hkv, D, len)) {
+      rc = decode_attention_words(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                                  len, num_seqs, num_q_heads, cache, scale,
+                                  static_cast<uint32_t *>(workspace),
+                                  static_cast<char *>(workspace) + p.partials,
+                                  workspace_bytes - p.partials, static_cast<cudaStream_t>(stream), fn);
+      if (!rc) clear_error();
+      return rc;
+    }
   }
   CUtensorMap tmk, tmv;
   {
@@ -520,7 +531,7 @@ PKV_API int paged_decode_shared_prefix_attention(
   a.o_part = reinterpret_cast<float *>(ws + p.o_part);
   a.lse_part = reinterpret_cast<float *>(ws + p.lse_part);
   a.out = out;
-  a.counters = reinterpret_cast<uint32_t *>(ws);
+  a.counters = reinterpret_cast<uint32_t *>(ws) + 2;
   a.num_blocks = cache->num_blocks;
   a.num_seqs = num_seqs;
   a.num_groups = num_groups;

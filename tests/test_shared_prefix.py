@@ -271,6 +271,34 @@ def test_two_calls_at_once(B):
 
 
 @pytest.mark.gpu
+def test_one_workspace_for_many_sizes(B):
+    """Calls of other batch sizes, heads and lengths, eager and as captured graphs, in turn on
+    one workspace, shared and plain."""
+    cs = [make([20, 4], [1000, 2500], list(range(24)), 32, 8, 64, 16, 1, poison=False),
+          make([3], [300], [5, 0, 400], 8, 2, 128, 16, 2, poison=False),
+          make([60, 30], [700, 900], [k % 7 * 90 for k in range(90)], 16, 8, 128, 32, 3, poison=False),
+          make([2, 2, 2], [64, 0, 200], [1500, 2, 3, 4, 900, 6], 6, 1, 64, 16, 4, poison=False)]
+    refs = [reference(c, 0.1) for c in cs]
+    ws = max((workspace(B, c) for c in cs), key=lambda w: w.numel())
+    outs, graphs = [torch.empty_like(c["q"]) for c in cs], []
+    for mode in (B.SHARED_ALWAYS, B.SHARED_NEVER):
+        B.pkv_set_shared_prefix(mode)
+        for i, c in enumerate(cs):
+            check(call(B, c, 0.1, ws), *refs[i], f"mode {mode}, {i}")
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                call(B, c, 0.1, ws, outs[i])
+            graphs.append((i, g))
+    rng = random.Random(7)
+    for _ in range(4):
+        for i, g in rng.sample(graphs, len(graphs)):
+            outs[i].fill_(5.0)
+            g.replay()
+            check(outs[i], *refs[i], f"graph {i}")
+    assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.gpu
 def test_equals_plain_decode(B):
     c = make([20, 4], [1000, 2500], list(range(24)), 32, 8, 64, 16, 1)
     a, b = call(B, c, 0.125), torch.empty_like(c["q"])
