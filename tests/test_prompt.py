@@ -150,6 +150,23 @@ def test_rows_past_4_gb(B, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_prompt(B, d):
+    """One prompt of 100003 tokens, compared at rows of its start, its middle and its end."""
+    n = 100003
+    q, k, v, start = make([n], 6, 2, d, True, seed=d)
+    out = torch.empty(n, 6, d, dtype=torch.bfloat16, device="cuda")
+    B.pkv_device_errors()
+    B.prompt_attention(out, q, k, v, start.cuda(), n, 2 * d ** -0.5)
+    assert B.pkv_device_errors() == 0
+    for i in (0, 1, 127, 128, 50000, 65535, 65536, 99999, n - 1):
+        for h in range(6):
+            kk, vv = k[:i + 1, h // 3].double(), v[:i + 1, h // 3].double()
+            p = torch.softmax(kk @ q[i, h].double() * (2 * d ** -0.5), 0)
+            check(out[i, h], p @ vv, p @ vv.abs(), f"row {i}")
+
+
+@pytest.mark.gpu
 def test_two_calls_at_once(B):
     """Two streams' calls beside each other, many times over."""
     sets = [make([700, 90, 1300], 12, 4, 128, True, seed=1), make([33] * 60, 8, 2, 64, False, seed=2)]
