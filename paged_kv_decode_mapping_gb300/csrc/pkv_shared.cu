@@ -343,35 +343,49 @@ SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int
   const int64_t units = p.tiles * hkv;
   const int64_t blocks = ((int64_t)max_prefix + kTileKeys - 1) / kTileKeys;
   const int32_t mlen = std::max(max_suffix, 1);
-  p.partition_tokens = paged_decode_plan(num_seqs, hq, hkv, d, mlen, sms);
-  p.parts = (mlen + p.partition_tokens - 1) / p.partition_tokens;
   // The prefix's CTAs take an SM each; the tail's run beside them on the others, and take
-  // theirs over.  So: as many splits as make the longer of a tile CTA's time and of the whole
-  // work over the SMs the shortest.  Measured, in us: a tile CTA 8.5 and, per block of 128
-  // keys, what the TMA unit needs for its boxes of 16 rows (63 cycles each and 64 bytes a
-  // cycle at 1.93 GHz) or the HBM for all CTAs' (6.5 TB/s); a tail CTA 4.5 and 34 KB a us, 2 or
-  // 3 to an SM, all of them at most the HBM's.  Own lengths are taken at half the longest.
-  const double tail_ctas = (double)num_seqs * hkv * p.parts;
-  p.stages = tail_stages(d, tail_ctas > (double)sms * tail_occupancy(d, tail_stages(d, false)));
-  const int occ = tail_occupancy(d, p.stages);
-  const double own = 0.5 * mlen / p.parts * d * 4;  // bytes of a tail CTA
-  const double tail = std::max(tail_ctas * (4.5 + own / 34e3) / occ, tail_ctas * own / 6.5e6 * sms);
+  // theirs over.  So: as many splits, and tail parts as short, as make the longest of a tile
+  // CTA's time, the longest part's and the whole work over the SMs the shortest.  Measured, in
+  // us, with the merge that follows: a tile CTA 8.1 and, per block of 128 keys, what the TMA
+  // unit needs for its boxes of 16 rows (63 cycles each and 64 bytes a cycle at 1.93 GHz) or
+  // the HBM for all CTAs' (6.5 TB/s); a part 8.7 and 31 KB a us at head_dim 64, 46 at 128, if
+  // it starts at once.  Of an SM, a part takes 4.5 and 34 KB a us, 2 or 3 at a time, all of
+  // them at most the HBM's.  Own lengths are taken at half the longest.  (Parts as long as the
+  // plain decode's, for 16 sequences of 1 to 512 own keys over 2048, 32 / 8 heads of 64: 11.6
+  // us; chosen so, 10.0.)
   const double tma = d == 64 ? 0.79 : 1.57;
   double best = 0, shared = 0;  // the choice's cost, and its time with the launch's 3 us once
-  p.splits = 1;
-  for (int64_t n = 1; n <= std::min<int64_t>(blocks, 1024); ++n) {
-    const double ctas = (double)units * n;
-    if (n > 1 && ctas > sms) break;
-    const double hbm = (double)groups * hkv * n * kTileKeys * d * 4 / 6.5e6 * std::min(1., sms / ctas);
-    const double tile = 8.5 + (double)((blocks + n - 1) / n) * std::max(tma, hbm);
-    const double fits = ctas + tail_ctas / occ <= sms ? 0 : 5;  // or the tail begins after it
-    const double t = std::max(tile, (tail + std::min<double>(ctas, sms) * tile) / sms) + fits;
-    if (n == 1 || t < best) {
-      best = t;
-      p.splits = (int32_t)n;
-      shared = std::max(tile, 3 + (tail + ctas * (tile - 3)) / sms) + fits;
+  int occ = 0;
+  const int32_t longest = paged_decode_plan(num_seqs, hq, hkv, d, mlen, sms);
+  for (int32_t P = longest, next = 256;; P = next, next *= 2) {
+    const int32_t parts = (mlen + P - 1) / P;
+    const double tail_ctas = (double)num_seqs * hkv * parts;
+    const int32_t stages = tail_stages(d, tail_ctas > (double)sms * tail_occupancy(d, tail_stages(d, false)));
+    const int fit = tail_occupancy(d, stages);
+    const double own = 0.5 * mlen / parts * d * 4;  // bytes of a tail CTA
+    const double tail = std::max(tail_ctas * (4.5 + own / 34e3) / fit, tail_ctas * own / 6.5e6 * sms);
+    const double part = 8.7 + (double)std::min(P, mlen) * d * 4 / (d == 64 ? 31e3 : 46e3);
+    for (int64_t n = 1; n <= std::min<int64_t>(blocks, 1024) || n == 1; ++n) {
+      const double ctas = (double)units * n;
+      if (n > 1 && ctas > sms) break;
+      const double hbm = (double)groups * hkv * n * kTileKeys * d * 4 / 6.5e6 * std::min(1., sms / std::max(ctas, 1.));
+      const double tile = 8.1 + (double)((blocks + n - 1) / n) * std::max(tma, hbm);
+      const double late = ctas + tail_ctas / fit <= sms ? 0 : 5;  // or the tail begins after it
+      // (of equals, the one with the prefix done first)
+      const double t = std::max({tile, part, (tail + std::min<double>(ctas, sms) * tile) / sms}) + late + 0.1 * tile;
+      if (best == 0 || t < (P == longest ? best : 0.97 * best)) {
+        best = t;
+        p.splits = (int32_t)n;
+        p.partition_tokens = P;
+        p.parts = parts;
+        p.stages = stages;
+        occ = fit;
+        shared = std::max({tile, part, 3 + (tail + ctas * (tile - 3)) / sms}) + late;
+      }
     }
+    if (next >= longest) break;
   }
+  const double tail_ctas = (double)num_seqs * hkv * p.parts;
   p.split_keys = (int32_t)std::min<int64_t>(
       std::max<int64_t>((blocks + p.splits - 1) / p.splits, 1) * kTileKeys, 1 << 29);
   p.sorted = num_seqs <= kSortSeqs && mlen >= 512 && units * p.splits + tail_ctas / occ > sms;
@@ -395,12 +409,12 @@ SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int
   p.total = std::max(p.total, p.partials + paged_decode_workspace_size(num_seqs, hq, hkv, d, p.plain_len));
   // The plain decode, one launch, is the faster one where little is read twice, and where
   // there are so many short groups that their CTAs' starts cost more than the reads (the last
-  // term: tasks a merging warp has after its first, 11 us each).  Plain: 5.5 us and every key
+  // term: tasks a merging warp has after its second, 14 us each).  Plain: 5.5 us and every key
   // at 7.5 TB/s, shared pages coming from L2 in part.  Measured, shared against plain, us: 3
-  // sequences over 512 tokens 8.3, 7.5; 16 over 2048 10.9, 12.7; 64 over 8192 38, 258; groups
+  // sequences over 512 tokens 8.3, 7.5; 16 over 2048 10.0, 12.7; 64 over 8192 38, 258; groups
   // of 4 over 1000 tokens (32 / 8 heads of 64), 16 of them 20, 30, 64 of them 71, 76, 256 of
   // them 339, 276; 256 groups of 16 over 250 tokens 745, 366.
-  shared += std::max(0., (double)tasks / cap - 1) * 11;
+  shared += std::max(0., (double)tasks / cap - 2) * 14;
   const double plain = 5.5 + (double)num_seqs * hkv * (max_prefix + 0.5 * mlen) * d * 4 / 7.5e6;
   p.plain = plain < 0.9 * shared;
   return p;
