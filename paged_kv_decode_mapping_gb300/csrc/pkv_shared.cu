@@ -326,7 +326,7 @@ struct SharedPlan {
   int32_t split_keys, splits, partition_tokens, parts, n_rows, sorted, merge_ctas, merge_heads, plain, plain_len;
   int32_t stages;  // of the tail's ring
   int64_t tiles;  // row tiles over all groups, at most
-  size_t partials, o_part, lse_part, total;
+  size_t partials, o_part, lse_part, total, plain_bytes;  // plain_bytes: of the plain decode
 };
 
 // The words that are zero between calls -- the plain decode's two and a counter per (sequence,
@@ -406,7 +406,8 @@ SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int
   p.lse_part = p.o_part + up256(prow * d * sizeof(float));
   p.total = p.lse_part + up256(prow * sizeof(float));
   p.plain_len = (int32_t)std::min<int64_t>((int64_t)max_prefix + max_suffix, 0x7fffffff);
-  p.total = std::max(p.total, p.partials + paged_decode_workspace_size(num_seqs, hq, hkv, d, p.plain_len));
+  p.plain_bytes = decode_workspace_size(num_seqs, hq, hkv, d, p.plain_len, sms);
+  p.total = std::max(p.total, p.partials + p.plain_bytes);
   // The plain decode, one launch, is the faster one where little is read twice, and where
   // there are so many short groups that their CTAs' starts cost more than the reads (the last
   // term: tasks a merging warp has after its second, 14 us each).  Plain: 5.5 us and every key
@@ -520,7 +521,9 @@ PKV_API int paged_decode_shared_prefix_attention(
   if (mode == PKV_SHARED_NEVER || (mode == PKV_SHARED_AUTO && p.plain)) {
     const int64_t cap = (int64_t)max_blocks_per_seq * cache->block_size;
     const int32_t len = (int32_t)std::min<int64_t>(p.plain_len, cap);
-    if (workspace_bytes >= p.partials + paged_decode_workspace_size(num_seqs, num_q_heads, hkv, D, len)) {
+    const size_t need =
+        len == p.plain_len ? p.plain_bytes : decode_workspace_size(num_seqs, num_q_heads, hkv, D, len, sms);
+    if (workspace_bytes >= p.partials + need) {
       rc = decode_attention_words(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
                                   len, num_seqs, num_q_heads, cache, scale,
                                   static_cast<uint32_t *>(workspace),
