@@ -485,7 +485,8 @@ def paged_decode_shared_prefix_attention(out: torch.Tensor, q: torch.Tensor, k_c
     if workspace is None:
         need = paged_decode_shared_prefix_workspace_size(B, Hq, Hkv, D, groups, max_prefix_len,
                                                          max_suffix_len)
-        workspace = torch.zeros(max(need, 1), dtype=torch.uint8, device=q.device)
+        with torch.cuda.stream(stream):  # zeroed, and given back, in that stream's order
+            workspace = torch.zeros(max(need, 1), dtype=torch.uint8, device=q.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous and on the current device")
     d = pkv_cache_desc(NB, BS, Hkv, D)

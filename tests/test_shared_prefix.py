@@ -271,6 +271,28 @@ def test_two_calls_at_once(B):
 
 
 @pytest.mark.gpu
+def test_workspace_of_its_own_on_a_given_stream(B):
+    """stream= without a workspace while the current stream is busy and freed memory is not
+    zero: the workspace is made in the given stream's order."""
+    c = make([20], [2000], [70] * 20, 16, 4, 64, 16, 9, poison=False)
+    o, amp = reference(c, 0.1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        dirty = torch.full((workspace(B, c).numel(),), 255, dtype=torch.uint8, device="cuda")
+        del dirty
+        out = torch.empty_like(c["q"])
+        torch.cuda.current_stream().synchronize()
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+        B.paged_decode_shared_prefix_attention(out, c["q"], c["k"], c["v"], c["tables"], c["lens"],
+                                               c["start"], c["prefix"], c["max_prefix"],
+                                               c["max_suffix"], 0.1, stream=side)
+        side.synchronize()
+        check(out, o, amp)
+    assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.gpu
 def test_one_workspace_for_many_sizes(B):
     """Calls of other batch sizes, heads and lengths, eager and as captured graphs, in turn on
     one workspace, shared and plain."""
