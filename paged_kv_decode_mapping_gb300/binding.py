@@ -456,8 +456,10 @@ def paged_decode_shared_prefix_attention(out: torch.Tensor, q: torch.Tensor, k_c
     """paged_decode_attention where the sequences group_start[g] .. group_start[g+1]-1 share
     the pages of their first prefix_lens[g] tokens, which are read once per group.
 
-    max_suffix_len bounds every context_len less the whole pages of its prefix; ``workspace``
-    is as in paged_decode_attention, of ``paged_decode_shared_prefix_workspace_size`` bytes.
+    max_suffix_len bounds every context_len less the whole pages of its prefix.  ``workspace``
+    (uint8, CUDA, ``paged_decode_shared_prefix_workspace_size`` bytes, zero-filled before its
+    first use) serves calls of any sizes in turn, but none of paged_decode_attention's; it may
+    be omitted as there.
     """
     dev = _home(q)
     if not (_fine(dev, torch.bfloat16, q, out, k_cache, v_cache) and
