@@ -178,7 +178,8 @@ int append(pkv_block_manager *m, const int64_t *seq_ids, int32_t n, int64_t *slo
       if ((size_t)lb >= s.blocks.capacity()) s.blocks.reserve(2 * (size_t)lb + 1);
     } else if (before == 0) {
       const int32_t b = s.blocks[(size_t)lb];
-      if (m->refs[(size_t)b] - leaving[b] > 1) {
+      // (a block of this sequence alone makes no entry: one for each took half the call's time)
+      if (m->refs[(size_t)b] > 1 && m->refs[(size_t)b] - leaving[b] > 1) {
         if (!pairs)
           return set_error(PKV_ERR_UNSUPPORTED,
                            "%s: sequence %lld shares its last block %d; append with "
