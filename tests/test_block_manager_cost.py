@@ -34,7 +34,7 @@ def best_append(B, block_size, rounds=40):
 
 def test_append_to_unshared_blocks(B):
     """A token into a partly filled block that one sequence holds is no dearer than one into a
-    new block, which takes that block besides (a hash entry for each such block made it 1.7
+    new block, which takes that block besides (a hash entry for each such block made it 1.8
     times as dear)."""
     ratios = []
     for _ in range(5):  # of the least times: other work on the host only adds to them
