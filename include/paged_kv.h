@@ -301,7 +301,8 @@ int paged_decode_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k_c
  * group are computed without a prefix.
  *
  * max_prefix_len >= every prefix_lens[g], and max_suffix_len >= every context_lens[b] less
- * the whole pages of its group's prefix; both are at most max_blocks_per_seq * block_size.
+ * the whole pages of its group's prefix; both are at most max_blocks_per_seq * block_size, and
+ * at most 2^29 (PKV_ERR_UNSUPPORTED; the workspace size is 0 there).
  * A longer one is cut there, a group that begins inside the one before it or leaves the
  * batch is moved or cut, and PKV_DEVERR_CONTEXT_LEN is raised.  Layouts, supported sizes,
  * and alignment are those of paged_decode_attention.  All arguments are DEVICE memory.

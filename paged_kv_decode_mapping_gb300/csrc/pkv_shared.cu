@@ -334,6 +334,10 @@ struct SharedPlan {
 // this many: no call's partial rows lie where another's counters are, whatever their sizes.
 constexpr size_t kWords = 65536;
 
+// The longest prefix and the longest own part: what a row stands for, and a place in a
+// sequence with one such step added, stay within 31 bits.
+constexpr int32_t kMaxSharedLen = 1 << 29;
+
 SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int32_t num_groups,
                        int32_t max_prefix, int32_t max_suffix, int sms) {
   SharedPlan p;
@@ -386,8 +390,7 @@ SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int
     if (next >= longest) break;
   }
   const double tail_ctas = (double)num_seqs * hkv * p.parts;
-  p.split_keys = (int32_t)std::min<int64_t>(
-      std::max<int64_t>((blocks + p.splits - 1) / p.splits, 1) * kTileKeys, 1 << 29);
+  p.split_keys = (int32_t)(std::max<int64_t>((blocks + p.splits - 1) / p.splits, 1) * kTileKeys);
   p.sorted = num_seqs <= kSortSeqs && mlen >= 512 && units * p.splits + tail_ctas / occ > sms;
   p.n_rows = p.splits + p.parts;
   // A warp per head, or per as many heads as keep the merging CTAs within half of those that
@@ -474,7 +477,8 @@ PKV_API size_t paged_decode_shared_prefix_workspace_size(int32_t num_seqs, int32
                                                          int32_t num_kv_heads, int32_t head_dim,
                                                          int32_t num_groups, int32_t max_prefix_len,
                                                          int32_t max_suffix_len) {
-  if (num_groups < 0 || max_prefix_len < 0 || max_suffix_len < 0 ||
+  if (num_groups < 0 || max_prefix_len < 0 || max_suffix_len < 0 || max_prefix_len > kMaxSharedLen ||
+      max_suffix_len > kMaxSharedLen ||
       paged_decode_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, std::max(max_suffix_len, 1), 1) <= 0)
     return 0;
   int sms = 0;
@@ -496,6 +500,8 @@ PKV_API int paged_decode_shared_prefix_attention(
   if (rc) return rc;
   if (num_groups < 0 || max_prefix_len < 0 || max_suffix_len < 0)
     return set_error(PKV_ERR_SHAPE, "%s: negative num_groups, max_prefix_len or max_suffix_len", fn);
+  if (max_prefix_len > kMaxSharedLen || max_suffix_len > kMaxSharedLen)
+    return set_error(PKV_ERR_UNSUPPORTED, "%s: max_prefix_len or max_suffix_len over 2^29", fn);
   if (num_seqs == 0) {
     clear_error();
     return PKV_OK;
