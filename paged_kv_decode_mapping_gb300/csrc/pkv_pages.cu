@@ -31,18 +31,20 @@ struct PageArgs {
   uint32_t block_size;
   uint32_t chunks;          // CTAs per page
   int32_t planes;           // 2 * layers: plane 2l is layer l's K, 2l + 1 its V
-  int32_t *tables;          // compaction: entries to rewrite (plane `planes`), or NULL
+  int32_t *tables;          // compaction: entries to rewrite (from plane `planes` on), or NULL
   int64_t entries;
   const int32_t *block_map;
 };
 
-// Grid: x = (pair, chunk of its page), chunk fastest; y = plane.  With `tables`, one more
-// plane rewrites the block-table entries, grid-stride.
+// Grid: x = (pair, chunk of its page), chunk fastest; y = plane.  With `tables`, the rows of CTAs
+// past the planes rewrite the block-table entries, grid-stride: as many rows as the entries
+// need (in one row, a single moved page of one chunk left the whole table to one CTA).
 __global__ void __launch_bounds__(kPageThreads) copy_pages_kernel(const __grid_constant__ PageArgs a) {
   const int tid = threadIdx.x, plane = blockIdx.y;
-  if (plane == a.planes) {
-    for (int64_t i = (int64_t)blockIdx.x * kPageThreads + tid; i < a.entries;
-         i += (int64_t)gridDim.x * kPageThreads) {
+  if (plane >= a.planes) {
+    const int64_t cta = (int64_t)(plane - a.planes) * gridDim.x + blockIdx.x;
+    const int64_t ctas = (int64_t)(gridDim.y - a.planes) * gridDim.x;
+    for (int64_t i = cta * kPageThreads + tid; i < a.entries; i += ctas * kPageThreads) {
       const int32_t x = a.tables[i];
       if (x < 0) continue;  // unused entry
       int32_t y = -1;
@@ -147,9 +149,10 @@ int launch_pages(pkv_bf16 *const *k_caches, pkv_bf16 *const *v_caches, int32_t n
     a.tables = remap ? tables : nullptr;
     a.entries = remap ? entries : 0;
     a.block_map = block_map;
+    const int64_t table_ctas = remap ? std::min<int64_t>((entries + kPageThreads - 1) / kPageThreads, 4096) : 0;
     int64_t x = num_layers > 0 ? num_pairs * a.chunks : 0;
-    if (x == 0) x = std::min<int64_t>((entries + kPageThreads - 1) / kPageThreads, 4096);
-    const unsigned y = (unsigned)(a.planes + (remap ? 1 : 0));
+    if (x == 0) x = table_ctas;
+    const unsigned y = (unsigned)(a.planes + (remap ? (table_ctas + x - 1) / x : 0));
     if (y > 0) {
       copy_pages_kernel<<<dim3((unsigned)x, y, 1), kPageThreads, 0, stream>>>(a);
       const cudaError_t e = cudaGetLastError();
