@@ -310,8 +310,9 @@ int paged_decode_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k_c
  * The workspace (paged_decode_shared_prefix_workspace_size() bytes) must be zero-filled
  * before its first use, and every call that completes leaves it ready for the next one, of
  * any sizes up to 65536 (sequence, kv head) pairs that it is large enough for: calls, or
- * captured graphs, for many batch sizes may take turns on one.  Not two that overlap, and not
- * paged_decode_attention's calls with these.
+ * captured graphs, for many batch sizes may take turns on one.  For one set of heads, the size
+ * for the most sequences, groups and tokens is enough for fewer of any of them.  Not two calls
+ * that overlap, and not paged_decode_attention's calls with these.
  *
  * Two launches: the prefixes as matrix products on the tensor cores, and beside them, as a
  * programmatic dependent, every sequence's own keys and the log-sum-exp merge.  Where that

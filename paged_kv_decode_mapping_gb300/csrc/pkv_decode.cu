@@ -1497,6 +1497,16 @@ size_t pkv::decode_workspace_size(int32_t num_seqs, int32_t hq, int32_t hkv, int
   return P <= 0 ? 0 : fused_layout(num_seqs, hq, hkv, d, mlen, P).total;
 }
 
+size_t pkv::decode_workspace_bound(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int32_t max_len,
+                                   int sms) {
+  const int64_t units = (int64_t)num_seqs * hkv, mlen = max_len > 0 ? max_len : 1;
+  const int64_t pm = num_seqs <= kMaxPersistSeqs ? 1536 : 1024;  // as in plan_partition
+  const int64_t parts = std::min(units * ((mlen + 511) / 512),
+                                 std::max<int64_t>((int64_t)sms * split_occupancy(d), units * ((mlen + pm - 1) / pm)));
+  const size_t rows = (size_t)(parts * (hq / hkv));
+  return align256((size_t)units * 4 + 8) + align256(rows * d * sizeof(float)) + align256(rows * sizeof(float));
+}
+
 PKV_API int32_t pkv_set_decode_consumer(int32_t consumer) {
   if (consumer != PKV_CONSUMER_TENSOR && consumer != PKV_CONSUMER_FMA)
     return set_error(PKV_ERR_UNSUPPORTED, "pkv_set_decode_consumer: unknown form %d", consumer);

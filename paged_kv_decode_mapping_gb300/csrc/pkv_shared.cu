@@ -329,6 +329,23 @@ struct SharedPlan {
   size_t partials, o_part, lse_part, total, plain_bytes;  // plain_bytes: of the plain decode
 };
 
+// Partial rows that no call of up to these sizes passes, whatever cut it takes: never fewer for
+// larger sizes, though a cut may well have fewer rows for them (64 sequences take 9 splits where
+// 42, one row tile, take 19), so that a workspace sized by the largest sizes serves all others.
+//  * the prefix's: n > 1 splits only where the tiles' CTAs all fit at once, so with t row tiles
+//    at most tile_seqs * t sequences, sms / (t * hkv) rows each;
+//  * the own keys': parts of at least 256 tokens, but for a single part.
+int64_t most_rows(int32_t num_seqs, int32_t hq, int32_t hkv, bool groups, int64_t blocks, int32_t mlen,
+                  int sms) {
+  const int64_t tile_seqs = kTileRows / (hq / hkv), units = (int64_t)num_seqs * hkv;
+  int64_t seq_rows = num_seqs;  // one split
+  const int64_t tiles = groups ? std::min<int64_t>((num_seqs + tile_seqs - 1) / tile_seqs, sms / hkv) : 0;
+  for (int64_t t = 1; t <= tiles; ++t)
+    seq_rows = std::max(seq_rows, std::min<int64_t>(t * tile_seqs, num_seqs) *
+                                      std::min<int64_t>({std::max<int64_t>(blocks, 1), 1024, sms / (t * hkv)}));
+  return seq_rows * hq + units * (hq / hkv) * (((int64_t)mlen + 255) / 256);
+}
+
 // The words that are zero between calls -- the plain decode's two and a counter per (sequence,
 // kv head) -- have the front of the workspace to themselves, as long for all calls of up to
 // this many: no call's partial rows lie where another's counters are, whatever their sizes.
@@ -345,7 +362,7 @@ SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int
   const int64_t tile_seqs = kTileRows / (hq / hkv);  // sequences of a tile
   p.tiles = groups > 0 ? (num_seqs - groups) / tile_seqs + groups : 0;  // at most, however they are cut
   const int64_t units = p.tiles * hkv;
-  const int64_t blocks = ((int64_t)max_prefix + kTileKeys - 1) / kTileKeys;
+  const int64_t blocks = groups > 0 ? ((int64_t)max_prefix + kTileKeys - 1) / kTileKeys : 0;
   const int32_t mlen = std::max(max_suffix, 1);
   // The prefix's CTAs take an SM each; the tail's run beside them on the others, and take
   // theirs over.  So: as many splits, and tail parts as short, as make the longest of a tile
@@ -407,10 +424,11 @@ SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int
   p.partials = up256((std::max((size_t)num_seqs * hkv, kWords) + 2) * 4);
   p.o_part = p.partials;
   p.lse_part = p.o_part + up256(prow * d * sizeof(float));
-  p.total = p.lse_part + up256(prow * sizeof(float));
   p.plain_len = (int32_t)std::min<int64_t>((int64_t)max_prefix + max_suffix, 0x7fffffff);
   p.plain_bytes = decode_workspace_size(num_seqs, hq, hkv, d, p.plain_len, sms);
-  p.total = std::max(p.total, p.partials + p.plain_bytes);
+  const size_t most = (size_t)most_rows(num_seqs, hq, hkv, groups > 0, blocks, mlen, sms);
+  p.total = p.partials + std::max(up256(most * d * sizeof(float)) + up256(most * sizeof(float)),
+                                  decode_workspace_bound(num_seqs, hq, hkv, d, p.plain_len, sms));
   // The plain decode, one launch, is the faster one where little is read twice, and where
   // there are so many short groups that their CTAs' starts cost more than the reads (the last
   // term: tasks a merging warp has after its second, 14 us each).  Plain: 5.5 us and every key
