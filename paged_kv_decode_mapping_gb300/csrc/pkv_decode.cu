@@ -1490,13 +1490,6 @@ PKV_API int32_t paged_decode_plan(int32_t num_seqs, int32_t num_q_heads, int32_t
   return plan_partition(num_seqs, num_kv_heads, head_dim, max_context_len, sms_or_default(num_sms));
 }
 
-size_t pkv::decode_workspace_size(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int32_t max_len,
-                                  int sms) {
-  const int32_t mlen = max_len > 0 ? max_len : 1;
-  const int32_t P = paged_decode_plan(num_seqs, hq, hkv, d, mlen, sms);
-  return P <= 0 ? 0 : fused_layout(num_seqs, hq, hkv, d, mlen, P).total;
-}
-
 size_t pkv::decode_workspace_bound(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int32_t max_len,
                                    int sms) {
   const int64_t units = (int64_t)num_seqs * hkv, mlen = max_len > 0 ? max_len : 1;
@@ -1581,7 +1574,10 @@ PKV_API size_t paged_decode_split_workspace_size(int32_t num_seqs, int32_t num_q
 PKV_API size_t paged_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads,
                                            int32_t num_kv_heads, int32_t head_dim,
                                            int32_t max_context_len) {
-  return decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, 0);
+  const int32_t mlen = max_context_len > 0 ? max_context_len : 1;
+  const int32_t P = paged_decode_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, mlen, 0);
+  if (P <= 0) return 0;
+  return fused_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, mlen, P).total;
 }
 
 PKV_API int paged_decode_split(float *o_part, float *lse_part, const pkv_bf16 *q,

@@ -99,11 +99,9 @@ int query_map(const pkv_bf16 *x, int64_t tokens, int32_t heads, int32_t d, int64
 int check_decode(const void *q, const void *k_cache, const void *v_cache, const int32_t *bt,
                  int32_t max_blocks, const int32_t *lens, int32_t max_len, int32_t num_seqs,
                  int32_t hq, const pkv_cache_desc *c, const char *fn);
-// paged_decode_workspace_size on a GPU of `sms` SMs (0: the current device's).
-size_t decode_workspace_size(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int32_t max_len, int sms);
-// No less than decode_workspace_size for any batch and length up to these (which may itself
-// shrink as a batch grows, for few sequences): a wave of partitions at most, or partitions of
-// plan_partition's size for many sequences.
+// No less than paged_decode_workspace_size for any batch and length up to these on a GPU of
+// `sms` SMs (that may itself shrink as a batch grows, for few sequences): a wave of partitions
+// at most, or partitions of plan_partition's size for many sequences.
 size_t decode_workspace_bound(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int32_t max_len, int sms);
 // paged_decode_attention with the words that are zero between calls apart from the workspace's
 // partials: words [2 + num_seqs * num_kv_heads] (the persistent kernel's two, the counters).

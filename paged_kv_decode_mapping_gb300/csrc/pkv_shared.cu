@@ -323,10 +323,11 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 // How a call is cut: split_keys prefix keys per tile CTA, partition_tokens tail tokens per
 // tail CTA, and the workspace.
 struct SharedPlan {
-  int32_t split_keys, splits, partition_tokens, parts, n_rows, sorted, merge_ctas, merge_heads, plain, plain_len;
+  int32_t split_keys, splits, partition_tokens, parts, n_rows, sorted, merge_ctas, merge_heads;
+  int32_t plain, plain_len;  // whether the plain decode takes the call by its sizes, and its length
   int32_t stages;  // of the tail's ring
   int64_t tiles;  // row tiles over all groups, at most
-  size_t partials, o_part, lse_part, total, plain_bytes;  // plain_bytes: of the plain decode
+  size_t partials, o_part, lse_part, total;
 };
 
 // Partial rows that no call of up to these sizes passes, whatever cut it takes: never fewer for
@@ -425,7 +426,6 @@ SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int
   p.o_part = p.partials;
   p.lse_part = p.o_part + up256(prow * d * sizeof(float));
   p.plain_len = (int32_t)std::min<int64_t>((int64_t)max_prefix + max_suffix, 0x7fffffff);
-  p.plain_bytes = decode_workspace_size(num_seqs, hq, hkv, d, p.plain_len, sms);
   const size_t most = (size_t)most_rows(num_seqs, hq, hkv, groups > 0, blocks, mlen, sms);
   p.total = p.partials + std::max(up256(most * d * sizeof(float)) + up256(most * sizeof(float)),
                                   decode_workspace_bound(num_seqs, hq, hkv, d, p.plain_len, sms));
@@ -543,19 +543,16 @@ PKV_API int paged_decode_shared_prefix_attention(
     return set_error(PKV_ERR_UNSUPPORTED, "%s: too many parts", fn);
   const int mode = g_mode.load(std::memory_order_relaxed);
   if (mode == PKV_SHARED_NEVER || (mode == PKV_SHARED_AUTO && p.plain)) {
+    // cut to the table: fewer tokens may take more parts, but none that the bound has no room for
     const int64_t cap = (int64_t)max_blocks_per_seq * cache->block_size;
     const int32_t len = (int32_t)std::min<int64_t>(p.plain_len, cap);
-    const size_t need =
-        len == p.plain_len ? p.plain_bytes : decode_workspace_size(num_seqs, num_q_heads, hkv, D, len, sms);
-    if (workspace_bytes >= p.partials + need) {
-      rc = decode_attention_words(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
-                                  len, num_seqs, num_q_heads, cache, scale,
-                                  static_cast<uint32_t *>(workspace),
-                                  static_cast<char *>(workspace) + p.partials,
-                                  workspace_bytes - p.partials, static_cast<cudaStream_t>(stream), fn);
-      if (!rc) clear_error();
-      return rc;
-    }
+    rc = decode_attention_words(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                                len, num_seqs, num_q_heads, cache, scale,
+                                static_cast<uint32_t *>(workspace),
+                                static_cast<char *>(workspace) + p.partials,
+                                workspace_bytes - p.partials, static_cast<cudaStream_t>(stream), fn);
+    if (!rc) clear_error();
+    return rc;
   }
   CUtensorMap tmk, tmv;
   {

@@ -86,3 +86,29 @@ def test_one_workspace_as_sequences_leave(B, mode):
     finally:
         B.pkv_set_shared_prefix(before)
     assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.gpu
+def test_never_is_the_plain_decode_past_the_table(B):
+    """Bounds whose sum passes the tables: the call is cut to what they hold, where the plain
+    decode takes 19 parts and not the 18 of the sum; it is the plain decode all the same."""
+    n, d, bs, blocks = 24, 64, 8, 1161
+    cap = blocks * bs  # 9288
+    g = torch.Generator(device="cuda").manual_seed(6)
+    k, v = (torch.randn(n * blocks, 1, bs, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(n, 1, d, generator=g, device="cuda").to(torch.bfloat16)
+    tables = torch.randperm(n * blocks, generator=g, device="cuda").to(torch.int32).view(n, blocks)
+    lens = torch.randint(1, cap + 1, (n,), generator=g, device="cuda").to(torch.int32)
+    lens[0] = cap
+    want, out = torch.empty_like(q), torch.empty_like(q)
+    B.paged_decode_attention(want, q, k, v, tables, lens, cap, 0.125)
+    ws = torch.zeros(B.paged_decode_shared_prefix_workspace_size(n, 1, 1, d, n, cap, 512),
+                     dtype=torch.uint8, device="cuda")
+    before = B.pkv_set_shared_prefix(B.SHARED_NEVER)
+    try:
+        B.paged_decode_shared_prefix_attention(
+            out, q, k, v, tables, lens, torch.arange(n + 1, dtype=torch.int32, device="cuda"),
+            torch.full((n,), cap, dtype=torch.int32, device="cuda"), cap, 512, 0.125, workspace=ws)
+    finally:
+        B.pkv_set_shared_prefix(before)
+    assert torch.equal(out, want) and B.pkv_device_errors() == 0
