@@ -239,7 +239,8 @@ int32_t pkv_decode_ctas_per_sm(int32_t head_dim, int32_t path);
  * paged_decode_workspace_size -- bytes of workspace paged_decode_attention needs for
  * these sizes on the current device: a completion counter per (sequence, kv head),
  * then the partition results of paged_decode_split's layout for P =
- * paged_decode_plan(...).  0 for empty sizes.
+ * paged_decode_plan(...).  0 for empty sizes.  The plan goes by the sizes, so that a
+ * smaller call may need more: a workspace for several takes the most that any of them needs.
  */
 size_t paged_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                    int32_t head_dim, int32_t max_context_len);
@@ -272,8 +273,10 @@ size_t paged_decode_split_workspace_size(int32_t num_seqs, int32_t num_q_heads, 
  * ticket; no CTA waits for another).
  * `workspace` must hold paged_decode_workspace_size() bytes and must be ZERO-FILLED
  * before its first use (it holds completion counters); every call that completes
- * leaves it ready for the next one.  Calls that share a workspace must not overlap
- * on the GPU.
+ * leaves it ready for the next one with the same num_seqs and num_kv_heads.  Before a
+ * call with others it must be zero-filled again (that call's counters lie where these
+ * calls' partition results may be), or each such pair has a workspace of its own.
+ * Calls that share a workspace must not overlap on the GPU.
  */
 int paged_decode_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k_cache,
                            const pkv_bf16 *v_cache, const int32_t *block_tables,

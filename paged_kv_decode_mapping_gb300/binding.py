@@ -406,8 +406,9 @@ def paged_decode_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Te
                            workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """out [B, Hq, D] bf16 = paged GQA decode attention (split + combine when the plan says so).
 
-    ``workspace`` (uint8, CUDA, zero-filled before its first use) may be omitted; then a
-    zeroed buffer of ``paged_decode_workspace_size`` bytes is taken from torch's allocator.
+    ``workspace`` (uint8, CUDA, zero-filled before its first use and before a call with
+    another number of sequences or kv heads) may be omitted; then a zeroed buffer of
+    ``paged_decode_workspace_size`` bytes is taken from torch's allocator.
     out, q, block_tables and context_lens may be pinned host tensors (read and written
     by the kernels over the host link).
     """
