@@ -24,6 +24,10 @@ __device__ __forceinline__ void acc_reset(WarpAcc<D> &a) {
   a.l0 = a.l1 = 0.f;
 }
 
+// What exponents are taken against where the largest score so far is m: m, or, where no score
+// was over -inf yet, 0, so that scores of -inf weigh 0 and a sum that is NaN tells of a NaN.
+__device__ __forceinline__ float softmax_ref(float m) { return m == -INFINITY ? 0.f : m; }
+
 // QK, online softmax and PV for this warp's 16 keys (nvalid of them in range) of the
 // stage whose K tile is at kb and V tile at vb.
 template <int D>
@@ -59,9 +63,10 @@ __device__ __forceinline__ void warp_tile(WarpAcc<D> &acc, const uint32_t (&qb)[
     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, x));
   }
   const float mn0 = fmaxf(acc.m0, mx0), mn1 = fmaxf(acc.m1, mx1);
-  const float al0 = dev::ex2(acc.m0 - mn0), al1 = dev::ex2(acc.m1 - mn1);
-  const float p0 = dev::ex2(s0 - mn0), p1 = dev::ex2(s1 - mn1);
-  const float p2 = dev::ex2(s2 - mn0), p3 = dev::ex2(s3 - mn1);
+  const float ref0 = softmax_ref(mn0), ref1 = softmax_ref(mn1);
+  const float al0 = dev::ex2(acc.m0 - ref0), al1 = dev::ex2(acc.m1 - ref1);
+  const float p0 = dev::ex2(s0 - ref0), p1 = dev::ex2(s1 - ref1);
+  const float p2 = dev::ex2(s2 - ref0), p3 = dev::ex2(s3 - ref1);
   acc.l0 = acc.l0 * al0 + (p0 + p2);
   acc.l1 = acc.l1 * al1 + (p1 + p3);
   acc.m0 = mn0;
@@ -139,7 +144,8 @@ __device__ __forceinline__ void warp_stash(WarpAcc<D> &acc, const MergeArea &r, 
 
 // The four warps' softmax states merged for head h, dim d: the normalised output;
 // *M2 gets the base-2 max and *den the sum, so lse2 = *M2 + log2(*den).  A warp that
-// saw no key has m = -inf and weighs nothing.
+// saw no key, or scores of -inf alone, has m = -inf and weighs nothing; if all are such, *den
+// is 0 and so is the output (unless a v that weighs 0 is not finite).
 template <int D>
 __device__ __forceinline__ float cta_merge(const MergeArea &r, int G, int h, int d, float *M2,
                                            float *den) {
@@ -149,13 +155,13 @@ __device__ __forceinline__ float cta_merge(const MergeArea &r, int G, int h, int
   float num = 0.f, dn = 0.f;
 #pragma unroll
   for (int w = 0; w < kConsumerWarps; ++w) {
-    const float wt = dev::ex2(r.m[w * kMaxGroup + h] - M);
+    const float wt = dev::ex2(r.m[w * kMaxGroup + h] - softmax_ref(M));
     num += wt * r.o[(w * G + h) * D + d];
     dn += wt * r.l[w * kMaxGroup + h];
   }
   *M2 = M;
   *den = dn;
-  return num / dn;
+  return dn == 0.f ? num : num / dn;
 }
 
 __device__ __forceinline__ uint16_t to_bf16(float x) {
@@ -201,21 +207,21 @@ __device__ __forceinline__ void merge_rows(uint16_t *dst, const float *o_rows,
     float mb = lk[0];
 #pragma unroll
     for (int u = 1; u < 8; ++u) mb = fmaxf(mb, lk[u]);
-    const float Mn = fmaxf(M, mb);
-    const float sc = dev::ex2(M - Mn);
+    const float Mn = fmaxf(M, mb), ref = softmax_ref(Mn);
+    const float sc = dev::ex2(M - ref);
     den *= sc;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) acc[v] *= sc;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const float wt = dev::ex2(lk[u] - Mn);
+      const float wt = dev::ex2(lk[u] - ref);
       den += wt;
 #pragma unroll
       for (int v = 0; v < VPL; ++v) acc[v] += wt * ov[u][v];
     }
     M = Mn;
   }
-  const float inv = 1.f / den;
+  const float inv = den == 0.f ? 0.f : 1.f / den;
   uint16_t *d = dst + lane * VPL;
   if constexpr (VPL == 2) {
     *reinterpret_cast<uint32_t *>(d) = dev::pack_bf16x2(acc[0] * inv, acc[1] * inv);

@@ -132,9 +132,9 @@ __device__ __forceinline__ void warp_tile_fma(WarpAccF<D> &acc, uint32_t qs, int
       float mx = sh;
 #pragma unroll
       for (int x = 1; x < 16; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-      const float mn = fmaxf(acc.m[h], mx);
-      const float al = dev::ex2(acc.m[h] - mn);
-      p[h] = dev::ex2(sh - mn);
+      const float mn = fmaxf(acc.m[h], mx), ref = softmax_ref(mn);
+      const float al = dev::ex2(acc.m[h] - ref);
+      p[h] = dev::ex2(sh - ref);
       acc.l[h] = acc.l[h] * al + (hf == 0 ? p[h] : 0.f);
       acc.m[h] = mn;
 #pragma unroll
@@ -211,7 +211,7 @@ __device__ __forceinline__ void warp_stash_fma(WarpAccF<D> &acc, const MergeArea
 // Cluster merge of one query head on the CTA that owns it: receive-area rows
 // u * hpo + j (u = 0 .. n-1; j = the head's index among the CTA's heads) hold partition
 // u's normalised output [D] and its base-2 lse (-inf for a partition without keys).
-// One warp; each lane owns D/32 dims.  All -inf (empty context): zeros.
+// One warp; each lane owns D/32 dims.  All -inf (empty context): zeros; NaN: NaN.
 template <int D>
 __device__ __forceinline__ void recv_merge_head(uint16_t *dst, const float *recv_o,
                                                 const float *recv_l, int j, int hpo, int n,
@@ -245,16 +245,15 @@ __device__ __forceinline__ void recv_merge_head(uint16_t *dst, const float *recv
   float den = 0.f, acc[VPL];
 #pragma unroll
   for (int v = 0; v < VPL; ++v) acc[v] = 0.f;
-  if (M != -INFINITY) {
+  const float ref = softmax_ref(M);
 #pragma unroll
-    for (int u = 0; u < kMaxClusterParts; ++u) {
-      const float wt = dev::ex2(lk[u] - M);  // 0 for an empty partition
-      den += wt;
+  for (int u = 0; u < kMaxClusterParts; ++u) {
+    const float wt = dev::ex2(lk[u] - ref);  // 0 for an empty partition, NaN for one with a NaN
+    den += wt;
 #pragma unroll
-      for (int v = 0; v < VPL; ++v) acc[v] += wt * ov[u][v];
-    }
+    for (int v = 0; v < VPL; ++v) acc[v] += wt * ov[u][v];
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const float inv = den == 0.f ? 0.f : 1.f / den;
   uint16_t *d = dst + lane * VPL;
   if constexpr (VPL == 2) {
     *reinterpret_cast<uint32_t *>(d) = dev::pack_bf16x2(acc[0] * inv, acc[1] * inv);
@@ -550,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, split_occupancy(D))
           float M2, den, M2b, denb;
           const float v0 = cta_merge<D>(r, a.group, h, d, &M2, &den);
           const float v1 = cta_merge<D>(r, a.group, h, d + 1, &M2b, &denb);
-          const bool live = den > 0.f;  // false (or NaN) when this range had no keys
+          const bool live = den != 0.f;  // 0: no key weighs anything; NaN goes on to the merge
           const int slot = rank * hpo + h / n;
           const uint32_t dst = dev::mapa(recv, (uint32_t)(h % n));
           const uint32_t dbar = dev::mapa(bar_merge, (uint32_t)(h % n));
@@ -1173,7 +1172,7 @@ __global__ void __launch_bounds__(128)
   for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
   if ((tid & 31) == 0) s_max[tid >> 5] = M;
   __syncthreads();
-  M = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+  M = softmax_ref(fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3])));
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float den = 0.f;
 #pragma unroll 4
@@ -1200,7 +1199,7 @@ __global__ void __launch_bounds__(128)
       for (int j = 0; j < 4; ++j) t[j] += s_red[q][4 * col + j];
       dsum += s_den[q];
     }
-    const float inv = 1.f / dsum;
+    const float inv = dsum == 0.f ? 0.f : 1.f / dsum;
     o2[col] = make_uint2(dev::pack_bf16x2(t[0] * inv, t[1] * inv),
                          dev::pack_bf16x2(t[2] * inv, t[3] * inv));
   }
