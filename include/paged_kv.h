@@ -299,9 +299,8 @@ int paged_decode_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k_c
  * sequence's row is the one that is read.  The result is that of paged_decode_attention(q,
  * ..., block_tables, context_lens), to fp32 rounding and the bf16 rounding of the prefix's
  * weights: each sequence attends to its own first context_lens[b] tokens, even where that
- * is less than the prefix, and context_lens[b] == 0 gives zeros (v of the shared pages
- * must be finite: a weight of zero does not keep a NaN out of such a row).  Sequences of no
- * group are computed without a prefix.
+ * is less than the prefix, and context_lens[b] == 0 gives zeros.  Sequences of no group are
+ * computed without a prefix.
  *
  * max_prefix_len >= every prefix_lens[g], and max_suffix_len >= every context_lens[b] less
  * the whole pages of its group's prefix; both are at most max_blocks_per_seq * block_size, and

@@ -136,7 +136,7 @@ constexpr int kTileRows = 128;  // query rows of a tile
 constexpr int kTileKeys = 128;  // keys per block
 struct SharedCut;
 struct PrefixLaunch {
-  const pkv_bf16 *q;
+  const pkv_bf16 *q, *k_cache, *v_cache;
   const int32_t *block_tables, *context_lens, *group_start, *prefix_lens;
   float *o_part, *lse_part;
   int32_t num_seqs, num_groups, num_q_heads;

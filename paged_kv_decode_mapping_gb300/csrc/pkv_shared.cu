@@ -592,6 +592,8 @@ PKV_API int paged_decode_shared_prefix_attention(
   if (prefix) {
     PrefixLaunch l;
     l.q = q;
+    l.k_cache = k_cache;
+    l.v_cache = v_cache;
     l.block_tables = block_tables;
     l.context_lens = context_lens;
     l.group_start = group_start;

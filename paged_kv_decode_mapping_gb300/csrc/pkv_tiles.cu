@@ -58,6 +58,7 @@ struct TileArgs {
   int32_t num_q_heads, num_kv_heads, group;
   int32_t tile_tokens;      // query tokens of a tile: 128 / group
   float scale_log2;
+  const uint16_t *q, *k, *v;  // for the rows that are computed once more (row_by_keys)
   // prefix
   const int32_t *block_tables, *context_lens, *prefix_lens;
   int64_t num_blocks;
@@ -393,6 +394,107 @@ __device__ __forceinline__ void chunk_exp(const uint32_t (&x)[32], int c0, int l
   }
 }
 
+// ---------------------------------------------------------------------------
+// A row that must not see a key gives it the weight 0, and in the product with V a NaN or an
+// infinity of that key's v comes through all the same (0 * inf).  A masked row whose result is
+// not finite is therefore computed once more, from its own keys alone, on the CUDA cores: by one
+// warp, 32 keys at a time, a key's score per lane, D / 32 dims of the result per lane.  (Looking
+// for such rows costs a call behind shared pages 0.1 to 0.3 us, 0.5 to 1%.)
+
+template <int D>
+struct RowSum {
+  float m = -INFINITY, l = 0.f, acc[D / 32] = {};  // max (base 2), sum, unnormalised result
+};
+
+// The lane's dims of a row of bf16 values.
+template <int D>
+__device__ __forceinline__ void lane_dims(const uint16_t *row, int lane, float (&x)[D / 32]) {
+  const uint32_t *const p = reinterpret_cast<const uint32_t *>(row) + lane * (D / 64);
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    const uint32_t w = __ldg(p + i);
+    x[2 * i] = dev::bf16lo_to_f32(w);
+    x[2 * i + 1] = dev::bf16hi_to_f32(w);
+  }
+}
+
+// Query row q over keys [n0, n1), key t's k and v at k_at(t) and v_at(t); stop(sum): no need to
+// go on.  Whole warps.
+template <int D, typename KAt, typename VAt, typename Stop>
+__device__ __forceinline__ RowSum<D> row_by_keys(const uint16_t *q, int n0, int n1, float scale_log2, int lane,
+                                                 KAt k_at, VAt v_at, Stop stop) {
+  RowSum<D> r;
+#pragma unroll 1
+  for (int t0 = n0; t0 < n1; t0 += 32) {
+    float x = -INFINITY;
+    if (t0 + lane < n1) {
+      const uint4 *const kr = reinterpret_cast<const uint4 *>(k_at(t0 + lane)), *const qr = reinterpret_cast<const uint4 *>(q);
+      x = 0.f;
+#pragma unroll 2
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 kk = __ldg(kr + i), qq = __ldg(qr + i);
+        const uint32_t kw[4] = {kk.x, kk.y, kk.z, kk.w}, qw[4] = {qq.x, qq.y, qq.z, qq.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x = fmaf(dev::bf16lo_to_f32(qw[e]), dev::bf16lo_to_f32(kw[e]), x);
+          x = fmaf(dev::bf16hi_to_f32(qw[e]), dev::bf16hi_to_f32(kw[e]), x);
+        }
+      }
+      x *= scale_log2;
+    }
+    float m = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = fmaxf(m, r.m);
+    const float ref = m == -INFINITY ? 0.f : m;  // no weight yet: all are 0
+    const float f = dev::ex2(r.m - ref), p = dev::ex2(x - ref);
+    float sum = p;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    r.m = m;
+    r.l = r.l * f + sum;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d) r.acc[d] *= f;
+    const int nk = min(32, n1 - t0);
+#pragma unroll 4
+    for (int u = 0; u < nk; ++u) {
+      const float w = __shfl_sync(0xffffffffu, p, u);
+      float v[D / 32];
+      lane_dims<D>(v_at(t0 + u), lane, v);
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) r.acc[d] = fmaf(w, v[d], r.acc[d]);
+    }
+    if (stop(r)) break;
+  }
+  return r;
+}
+
+// kPrefix: partial row `split` of query row `row` (b * Hq + h) once more, if it is not finite, from
+// keys [key0, see) of the pages of sequence `first`.  Whole warps.
+template <int D>
+__device__ __noinline__ void prefix_row(const TileArgs &a, int row, int split, int first, int g, int key0,
+                                        int see, int lane) {
+  constexpr int VPL = D / 32;
+  float *const dst = a.o_part + ((int64_t)row * a.cut.n_rows + split) * D + lane * VPL;
+  bool bad = false;
+#pragma unroll
+  for (int d = 0; d < VPL; ++d) bad |= !isfinite(dst[d]);
+  if (!__any_sync(0xffffffffu, bad)) return;
+  const int32_t *const table = a.block_tables + (int64_t)first * a.cut.max_blocks;
+  auto at = [&](int t) {
+    int64_t phys = __ldg(table + (t >> a.cut.log2_bs));
+    if (phys < 0 || phys >= a.num_blocks) phys = 0;  // (flagged where it was copied)
+    return ((phys * a.num_kv_heads + g) * a.cut.block_size + (t & (a.cut.block_size - 1))) * D;
+  };
+  const RowSum<D> r = row_by_keys<D>(
+      a.q + (int64_t)row * D, key0, see, a.scale_log2, lane, [&](int t) { return a.k + at(t); },
+      [&](int t) { return a.v + at(t); }, [](const RowSum<D> &) { return false; });
+#pragma unroll
+  for (int d = 0; d < VPL; ++d) dst[d] = r.l == 0.f ? 0.f : r.acc[d] / r.l;
+  if (lane == 0)
+    a.lse_part[(int64_t)row * a.cut.n_rows + split] = r.l == 0.f ? -INFINITY : (r.m + log2f(r.l)) * kLn2;
+}
+
 template <int D, int MODE>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
@@ -507,6 +609,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     return x.live != 0;
   };
   int issued = 0, qn0 = 0, qn1 = 0;  // producers: blocks loaded, Q tiles of either tile
+  [[maybe_unused]] int ends = 0;     // kPrefix's softmax warps: whether the row's context ends among the keys
 
   // Loads blocks [from, to) of the item's K or V into this warp's ring, each after
   // before(block); `issued` runs on.
@@ -568,6 +671,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       int see = it.t_end;
       if (kPaged && valid) see = min(max(__ldg(a.context_lens + token), 0), it.t_end);
       if (!kPaged) see = min(qi + 1, it.t_end);
+      if (kPaged) ends = valid && see > it.key0 && see < it.t_end;
       float m_ref = -INFINITY;
       float ls[4] = {0.f, 0.f, 0.f, 0.f};
       auto rescale_o = [&](float f) {  // O_t (and its row-sum column) and the row sum scale by f
@@ -972,7 +1076,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       a.lse_part[(int64_t)row * a.cut.n_rows + blockIdx.y] =
           any0 || any1 ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
-    __syncthreads();
+    const int any_ends = __syncthreads_or(ends);
 #pragma unroll 4
     for (int r = r_first; r < nrows; r += kStep) {
       const float2 w = s_join[r];
@@ -981,6 +1085,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       auto join = [&](float u, float v) { return (w.x == -1.f ? 0.f : w.x * u) + (w.y == -1.f ? 0.f : w.y * v); };
       reinterpret_cast<float4 *>(a.o_part + ((int64_t)s_row[r] * a.cut.n_rows + blockIdx.y) * D)[c16] =
           make_float4(join(x0.x, x1.x), join(x0.y, x1.y), join(x0.z, x1.z), join(x0.w, x1.w));
+    }
+    if (any_ends) {
+      __syncthreads();  // the rows are written
+      for (int r = warp; r < nrows; r += kTileThreads / 32) {
+        const int see = __ldg(a.context_lens + first.first + first.tok0 + r / G);
+        if (see > first.key0 && see < first.t_end)
+          prefix_row<D>(a, s_row[r], blockIdx.y, first.first, first.g, first.key0, see, lane);
+      }
     }
   }
   // a wait that gave up leaves copies possibly in flight: waited for (bounded)
@@ -1057,6 +1169,9 @@ int launch_prefix(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv_cach
   a.group = l.num_q_heads / c.num_kv_heads;
   a.tile_tokens = kTileRows / a.group;
   a.scale_log2 = l.scale * kLog2e;
+  a.q = l.q;
+  a.k = l.k_cache;
+  a.v = l.v_cache;
   a.block_tables = l.block_tables;
   a.context_lens = l.context_lens;
   a.prefix_lens = l.prefix_lens;

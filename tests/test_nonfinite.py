@@ -1,0 +1,103 @@
+"""NaN and infinities in k and v: they reach the rows that see their keys, and no others.
+
+Reference in 64 bits, over the keys each row sees.  Where it is finite the output is within
+2^-8 |o| + (2^-7 + 2^-12) sum p |v| of it (the output's rounding, the weights', and where it
+is of rounded weights their sum's; fp32 elsewhere); where it is not, the output is not either.
+"""
+
+import pytest
+import torch
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def B():
+    from paged_kv_decode_mapping_gb300 import build
+
+    build.build()
+    from paged_kv_decode_mapping_gb300 import binding
+
+    return binding
+
+
+def reference(q, k, v, scale, seen=None):
+    """(o, sum p |v|) of q [r, d] over k, v [n, d]; seen [r, n]: other keys are left out."""
+    q, k, v = q.double(), k.double(), v.double()
+    x = q @ k.T * scale
+    if seen is not None:
+        x = torch.where(seen, x, -INF)
+    p = torch.softmax(x, -1)
+    if seen is None:
+        return p @ v, p @ v.abs()
+    # dims that are finite everywhere as a product; the others key by key, seen ones only
+    vf = torch.where(v.isfinite(), v, 0.0)
+    o, amp = p @ vf, p @ vf.abs()
+    for t in (~v.isfinite()).any(1).nonzero()[:, 0].tolist():
+        for d in (~v[t].isfinite()).nonzero()[:, 0].tolist():
+            add = torch.where(seen[:, t], p[:, t] * v[t, d], 0.0)
+            o[:, d] += add
+            amp[:, d] += add.abs()
+    return o, amp
+
+
+def check(out, o, amp, what=""):
+    out, ok = out.double(), o.isfinite()
+    assert torch.equal(out.isfinite(), ok), \
+        f"{what}: {int((~out.isfinite() & ok).sum())} values hit, {int((out.isfinite() & ~ok).sum())} missed"
+    bound = 2.0**-8 * o.abs() + (2.0**-7 + 2.0**-12) * amp + 1e-30
+    worst = ((out - o).abs() / bound)[ok].max().item() if bool(ok.any()) else 0.0
+    assert worst <= 1, f"{what}: {worst} of the bound"
+
+
+def spoil(x, at, d, seed):
+    """Some dims of rows x[at] (pairs of row and head) become NaN or infinite."""
+    g = torch.Generator().manual_seed(seed)
+    for n, (t, h) in enumerate(at):
+        dims = torch.randperm(d, generator=g)[:1 + n % 5]
+        x[t, h, dims.to(x.device)] = [NAN, INF, -INF][n % 3]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", [1, 2])
+@pytest.mark.parametrize("hq,hkv,d,bs,prefix", [(24, 8, 128, 16, 2048), (8, 8, 64, 32, 1000), (8, 1, 64, 8, 700),
+                                                (12, 4, 128, 64, 9000)])
+def test_shared_pages(B, mode, hq, hkv, d, bs, prefix):
+    """Contexts that end all over the shared prefix, non-finite v at the ends of some and behind,
+    shared and plain."""
+    g = torch.Generator(device="cuda").manual_seed(d + bs)
+    ends = [prefix + 9, 0, 1, 63, 64, 65, prefix // 2, prefix // 2 + 1, prefix - prefix % bs, prefix - 1, 130, prefix + 40]
+    ends += [1 + 37 * i % prefix for i in range(30)]
+    n, sh = len(ends), prefix // bs
+    own = -(-(prefix + 40) // bs) - sh
+    k, v = (torch.randn((sh + n * own) * bs, hkv, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    grp = hq // hkv
+    spoil(v, [(t % (sh * bs), h) for t, h in ((prefix // 2, 0), (64, hkv - 1), (prefix - 2, hkv // 2), (128, 0),
+                                              (prefix // 3, hkv - 1), (bs, 0))], d, 5)
+    k[sh * bs - 1, 0, 3] = NAN
+    perm = torch.randperm(sh + n * own, generator=g, device="cuda")
+    pages = [x.view(-1, bs, hkv, d).transpose(1, 2).contiguous() for x in (k, v)]
+    pool = [torch.empty_like(x) for x in pages]
+    for p, x in zip(pool, pages):
+        p[perm] = x
+    rows = [list(range(sh)) + [sh + b * own + j for j in range(own)] for b in range(n)]
+    tables = perm[torch.tensor(rows, device="cuda")].to(torch.int32).contiguous()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.randn(n, hq, d, generator=g, device="cuda").to(torch.bfloat16)
+    out = torch.full_like(q, 3.0)
+    before = B.pkv_set_shared_prefix(mode)
+    try:
+        B.paged_decode_shared_prefix_attention(out, q, *pool, tables, torch.tensor(ends, **i32),
+                                               torch.tensor([0, n], **i32), torch.tensor([prefix], **i32), prefix,
+                                               own * bs, d**-0.5)
+    finally:
+        B.pkv_set_shared_prefix(before)
+    for b, end in enumerate(ends):
+        if end == 0:
+            assert bool((out[b] == 0).all())
+            continue
+        at = torch.cat([torch.arange(r * bs, r * bs + bs) for r in rows[b]])[:end].cuda()
+        for h in range(hkv):
+            o, amp = reference(q[b, h * grp:(h + 1) * grp], k[at, h], v[at, h], d**-0.5)
+            check(out[b, h * grp:(h + 1) * grp], o, amp, f"end {end}, kv head {h}")
+    assert B.pkv_device_errors() == 0
