@@ -21,24 +21,10 @@ def B():
     return binding
 
 
-def reference(q, k, v, scale, seen=None):
-    """(o, sum p |v|) of q [r, d] over k, v [n, d]; seen [r, n]: other keys are left out."""
-    q, k, v = q.double(), k.double(), v.double()
-    x = q @ k.T * scale
-    if seen is not None:
-        x = torch.where(seen, x, -INF)
-    p = torch.softmax(x, -1)
-    if seen is None:
-        return p @ v, p @ v.abs()
-    # dims that are finite everywhere as a product; the others key by key, seen ones only
-    vf = torch.where(v.isfinite(), v, 0.0)
-    o, amp = p @ vf, p @ vf.abs()
-    for t in (~v.isfinite()).any(1).nonzero()[:, 0].tolist():
-        for d in (~v[t].isfinite()).nonzero()[:, 0].tolist():
-            add = torch.where(seen[:, t], p[:, t] * v[t, d], 0.0)
-            o[:, d] += add
-            amp[:, d] += add.abs()
-    return o, amp
+def reference(q, k, v, scale):
+    """(o, sum p |v|) of q [r, d] over k, v [n, d]."""
+    p = torch.softmax(q.double() @ k.double().T * scale, -1)
+    return p @ v.double(), p @ v.double().abs()
 
 
 def check(out, o, amp, what=""):
