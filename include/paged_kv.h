@@ -430,7 +430,8 @@ int paged_prefill_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k_
  * max_query_len >= every length; a longer or misplaced sequence raises
  * PKV_DEVERR_CONTEXT_LEN and only its first max_query_len rows within the tensors are
  * computed.  Rows of no sequence are not written, and no sequence reads another's rows;
- * within a sequence v must be finite (a NaN or infinity may reach rows up to 127 before it).
+ * within a sequence v must be finite: a NaN or infinity may reach rows before it, fewer than
+ * 128 + 128 / (num_q_heads / num_kv_heads) tokens before.  (One in k reaches no row before it.)
  */
 int prompt_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v,
                      int64_t out_stride, int64_t q_stride, int64_t k_stride, int64_t v_stride,

@@ -87,3 +87,34 @@ def test_shared_pages(B, mode, hq, hkv, d, bs, prefix):
             o, amp = reference(q[b, h * grp:(h + 1) * grp], k[at, h], v[at, h], d**-0.5)
             check(out[b, h * grp:(h + 1) * grp], o, amp, f"end {end}, kv head {h}")
     assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hkv,grp", [(2, 1), (2, 3), (1, 5), (2, 8), (1, 128)])
+def test_prompts(B, d, hkv, grp):
+    """A NaN key makes the rows that see it NaN and changes no bit before it; a NaN in v, the
+    rows that see it, and none that many tokens before it, nor of another sequence."""
+    g = torch.Generator(device="cuda").manual_seed(d + grp)
+    lens, hq = [257, 700, 1, 90], hkv * grp
+    start = [sum(lens[:i]) for i in range(len(lens) + 1)]
+    q, k, v = (torch.randn(sum(lens), h, d, generator=g, device="cuda").to(torch.bfloat16) for h in (hq, hkv, hkv))
+
+    def run(k, v):
+        out = torch.full_like(q, 3.0)
+        B.prompt_attention(out, q, k, v, torch.tensor(start, dtype=torch.int32, device="cuda"), max(lens), d**-0.5)
+        return out
+
+    clean, rows = run(k, v), torch.arange(sum(lens), device="cuda")
+    for at in (start[1], start[1] + 127, start[1] + 255, start[1] + 256, start[1] + 300, start[1] + 511, start[2] - 1):
+        hit = (rows >= at) & (rows < start[2])
+        for which in (0, 1):
+            kv = [k.clone(), v.clone()]
+            kv[which][at, 0, 11] = NAN
+            out = run(*kv)
+            free = ~hit if which == 0 else ~hit & ~((rows < at) & (rows >= start[1]) & (rows > at - 128 - 128 // grp))
+            assert torch.equal(out[free], clean[free]), at
+            assert torch.equal(out[:, grp:], clean[:, grp:])  # the other kv heads
+            dims = slice(None) if which == 0 else slice(11, 12)
+            assert bool(out[hit][:, :grp, dims].isnan().all()), at
+    assert B.pkv_device_errors() == 0
