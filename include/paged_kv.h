@@ -300,7 +300,8 @@ int paged_decode_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k_c
  * ..., block_tables, context_lens), to fp32 rounding and the bf16 rounding of the prefix's
  * weights: each sequence attends to its own first context_lens[b] tokens, even where that
  * is less than the prefix, and context_lens[b] == 0 gives zeros.  Sequences of no group are
- * computed without a prefix.
+ * computed without a prefix.  (The weights' rounding, 2^-8 of each at most, is of the shared
+ * form; where the call is paged_decode_attention's launch, see below, they keep 16 bits.)
  *
  * max_prefix_len >= every prefix_lens[g], and max_suffix_len >= every context_lens[b] less
  * the whole pages of its group's prefix; both are at most max_blocks_per_seq * block_size, and

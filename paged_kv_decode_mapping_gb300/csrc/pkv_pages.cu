@@ -7,7 +7,8 @@
 // (2 bytes of traffic per byte copied), and the small ones by the launch itself.  16 KB of a
 // page per CTA, four 16-byte loads in flight per thread before the first store.  Measured: 256
 // pages of 28 layers (939 MB) 128 us, 7.3 TB/s; 2900 pages of 4 layers (381 MB) 58 us, 6.6
-// TB/s; 5 pages of 16 layers 2.6 us.
+// TB/s; 5 pages of 16 layers 2.6 us.  Pages of 8 KB and over; smaller ones, a CTA each with less
+// than a vector per thread and load, were not timed.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -38,7 +39,8 @@ struct PageArgs {
 
 // Grid: x = (pair, chunk of its page), chunk fastest; y = plane.  With `tables`, the rows of CTAs
 // past the planes rewrite the block-table entries, grid-stride: as many rows as the entries
-// need (in one row, a single moved page of one chunk left the whole table to one CTA).
+// need (in one row, a single moved page of one chunk left the whole table to one CTA: tables of
+// 256 x 512 took 115 us, now 1.8; of 64 x 8192 455, now 2.7).
 __global__ void __launch_bounds__(kPageThreads) copy_pages_kernel(const __grid_constant__ PageArgs a) {
   const int tid = threadIdx.x, plane = blockIdx.y;
   if (plane >= a.planes) {

@@ -10,7 +10,7 @@
 // dependent of the first, so that its CTAs run beside the prefix's, on the SMs these leave,
 // and only store their parts.  Its last CTAs merge, a warp for a few heads of a sequence: they
 // wait for the prefix's grid and for the sequence's own parts.  Measured: 64 sequences of 1 to
-// 1024 own keys over 8192 shared ones (24 / 8 heads of 128) 37.6 us, of which the prefix's
+// 1024 own keys over 8192 shared ones (24 / 8 heads of 128) 37.5 us, of which the prefix's
 // CTAs, 64 of them, run for 29; without sharing 258 us.  (Merged by whichever part came last,
 // by tickets, the last tile CTA of a group had 126 rows to merge alone, 7 us; merged by each
 // tail CTA after waiting for the prefix, the tail held its SMs until the prefix was done.)
@@ -46,8 +46,9 @@ struct TailArgs {
 
 // Stages of the ring and CTAs per SM.  At head_dim 128 three stages and two CTAs; with more
 // CTAs than those hold at once, two stages and three: their starts and ends, 5 us of 12, lie
-// under the others' streams (64 sequences of 1 to 1024 own keys over 8192: 42.6 against 37.6
-// us; 16 of 1 to 256, which all fit: 55.0 against 56.3 us).
+// under the others' streams (64 sequences of 1 to 1024 own keys over 8192: 42.5 against 37.5
+// us, and without the order by length below either 47.5; 16 of 1 to 256, which all fit: 55.0
+// against 56.3 us).
 constexpr int tail_stages(int d, bool many) { return d == 64 ? 4 : many ? 2 : 3; }
 constexpr int tail_occupancy(int d, int stages) { return d == 64 || stages == 2 ? 3 : 2; }
 constexpr size_t tail_smem(int d, int stages) {
@@ -67,8 +68,8 @@ constexpr int kSortSeqs = kThreads;  // one sequence per thread
 // keep out the ones they wait for, and every wait is bounded.
 //
 // With more CTAs than fit at once the longest sequences go first, so that none of them starts
-// when the others end (64 sequences of 1 to 1024 own keys over 8192 shared ones: 42.6 against
-// 37.7 us).
+// when the others end (64 sequences of 1 to 1024 own keys over 8192 shared ones: in the order of
+// the batch 42.4 against 37.5 us).
 template <int D, int STAGES>
 __global__ void __launch_bounds__(kThreads, tail_occupancy(D, STAGES))
     tail_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -372,7 +373,9 @@ SharedPlan shared_plan(int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d, int
   // unit needs for its boxes of 16 rows (63 cycles each and 64 bytes a cycle at 1.93 GHz) or
   // the HBM for all CTAs' (6.5 TB/s); a part 8.7 and 31 KB a us at head_dim 64, 46 at 128, if
   // it starts at once.  Of an SM, a part takes 4.5 and 34 KB a us, 2 or 3 at a time, all of
-  // them at most the HBM's.  Own lengths are taken at half the longest.  (Parts as long as the
+  // them at most the HBM's.  Own lengths are taken at half the longest.  (The sizes do not tell the
+  // block size: `tma` is for 16 rows.  By the same formula a block takes 2.6 us at 8 rows, head_dim
+  // 128, and 0.79 at 64, so that longer pages get more splits than they need.)  (Parts as long as the
   // plain decode's, for 16 sequences of 1 to 512 own keys over 2048, 32 / 8 heads of 64: 11.6
   // us; chosen so, 10.0.)
   const double tma = d == 64 ? 0.79 : 1.57;

@@ -34,9 +34,9 @@ namespace pkv {
 //    launch control): its rings, queries and scores of the next item fill while the rows of
 //    the last one are written, so that an item costs no launch, set-up and first-copy latency
 //    of its own (about 9 us, the time of six key blocks).
-//    Measured: 8192 tokens of 24 / 8 heads of 128 at 1560 TFLOP/s, the tensor pipe 67% busy
+//    Measured: 8192 tokens of 24 / 8 heads of 128 at 1565 TFLOP/s, the tensor pipe 67% busy
 //    (a block pair takes 3080 cycles, 2080 of them MMAs; the exponentials and their rounding
-//    are the rest); 8192 of 32 / 8 heads of 64 at 900, the tensor pipe 42% busy: half the MMAs
+//    are the rest); 8192 of 32 / 8 heads of 64 at 905, the tensor pipe 42% busy: half the MMAs
 //    for the same softmax.  Short prompts end in what an item costs beside its blocks (an
 //    epilogue of 2000 cycles, the last P.V, the first S: about 2.6 us).
 //  * kPrefix: both tiles hold the same rows (queries of a group of sequences) and take
@@ -288,7 +288,7 @@ __device__ __forceinline__ void load_packed_block(const CUtensorMap *tm, uint32_
 
 // dev::mbar_wait in as few instructions as it takes: the kernel waits in forty places, and
 // with 90 KB of code its warps spent a quarter of their time waiting for instructions
-// (128 prompts of 336 tokens, 217 us; with 57 KB 155 us).
+// (128 prompts of 336 tokens, 217 us; with 57 KB 157 us).
 __device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity) {
   uint64_t since = 0;
 #pragma unroll 1
@@ -616,7 +616,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto load_ring = [&](bool is_k, const TileItem &x, int from, int to, auto before) {
     const CUtensorMap *const tm = is_k ? &tmk : &tmv;
     const int ks = is_k ? KSK : KSV;
-    const uint64_t policy = dev::policy_evict_last();  // other CTAs read the same keys
+    // other CTAs read the same keys (kPrefix: only where the group has more than one tile of rows)
+    const uint64_t policy = dev::policy_evict_last();
     const int32_t *const trow = kPaged ? a.block_tables + (int64_t)x.first * a.cut.max_blocks : nullptr;
     const int lb_last = kPaged ? (x.t_end - 1) >> a.cut.log2_bs : 0;
     [[maybe_unused]] int win = kPaged ? x.key0 >> a.cut.log2_bs : 0;
