@@ -118,3 +118,53 @@ def test_prompts(B, d, hkv, grp):
             dims = slice(None) if which == 0 else slice(11, 12)
             assert bool(out[hit][:, :grp, dims].isnan().all()), at
     assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", [1, 2])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_of_minus_infinity(B, mode, d):
+    """Keys of score -inf weigh nothing: leading ones, whole blocks and splits, the own keys alone;
+    in prompts the rows that see such keys only have no value and are left out."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    hq, hkv, bs, prefix, own, n = 8, 2, 16, 1024, 48, 6
+    sh, cols = prefix // bs, (prefix + own) // bs
+    tables = torch.empty(n, cols, dtype=torch.int32, device="cuda")
+    tables[:, :sh] = torch.arange(sh, device="cuda")
+    tables[:, sh:] = sh + torch.arange(n * (cols - sh), device="cuda").view(n, -1)
+    k, v = (torch.randn(sh + n * (cols - sh), hkv, bs, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(n, hq, d, generator=g, device="cuda").to(torch.bfloat16)
+    q[:, :, 5] = q[:, :, 5].abs() + 0.25
+    i32 = dict(dtype=torch.int32, device="cuda")
+    lens = [prefix + 1 + 9 * b for b in range(n)]
+    for dead in ([(0, 1)], [(0, 700)], [(128, 256), (prefix, prefix + own)], [(0, prefix)], [(prefix - 300, prefix + own)]):
+        kk = k.clone()
+        for b in range(n):
+            for lo, hi in dead:
+                for t in range(lo, hi):
+                    kk[tables[b, t // bs].long(), :, t % bs, 5] = -INF
+        out = torch.full_like(q, 3.0)
+        before = B.pkv_set_shared_prefix(mode)
+        try:
+            B.paged_decode_shared_prefix_attention(out, q, kk, v, tables, torch.tensor(lens, **i32),
+                                                   torch.tensor([0, n], **i32), torch.tensor([prefix], **i32), prefix,
+                                                   own, d**-0.5)
+        finally:
+            B.pkv_set_shared_prefix(before)
+        for b in range(n):
+            for h in range(hkv):
+                x, y = (z[tables[b].long(), h].reshape(-1, d)[:lens[b]] for z in (kk, v))
+                o, amp = reference(q[b, 4 * h:4 * h + 4], x, y, d**-0.5)
+                check(out[b, 4 * h:4 * h + 4], o, amp, f"{dead}, sequence {b}, kv head {h}")
+    t = 600
+    q, k, v = (torch.randn(t, h, d, generator=g, device="cuda").to(torch.bfloat16) for h in (hq, hkv, hkv))
+    q[:, :, 5] = q[:, :, 5].abs() + 0.25
+    for lo, hi in ((0, 1), (0, 128), (0, 300), (200, 500), (130, 131)):
+        kk, out = k.clone(), torch.full_like(q, 3.0)
+        kk[lo:hi, :, 5] = -INF
+        B.prompt_attention(out, q, kk, v, torch.tensor([0, t], **i32), t, d**-0.5)
+        for h in range(hq):
+            for i in range(hi if lo == 0 else 0, t, 37):
+                o, amp = reference(q[i:i + 1, h], kk[:i + 1, h // 4], v[:i + 1, h // 4], d**-0.5)
+                check(out[i:i + 1, h], o, amp, f"prompt {lo}..{hi}, row {i}, head {h}")
+    assert B.pkv_device_errors() == 0
