@@ -251,7 +251,7 @@ def _plain_write(s):
         rows = torch.where(fresh, x[src].permute(0, 2, 1, 3).float(), 0.0)  # [P, Hkv, bs, D]
         need = rows.abs().amax((2, 3))
         old = torch.where(held.any(2)[..., 0], scale[phys], 0.0)  # a page that begins here has none
-        to = torch.maximum(old, torch.where(need > 0, (need / top).clamp(min=2.0 ** -126), 0.0))
+        to = torch.maximum(old, torch.where(need > 0, (need / torch.full_like(need, top)).clamp(min=2.0 ** -126), 0.0))
         unit = torch.where(to > 0, to, 1.0)[..., None, None]
         was = codes.view(torch.uint8)[phys].view(codes.dtype)
         again = _round(was.float() * old[..., None, None] / unit, codes.dtype)
