@@ -441,6 +441,147 @@ int prompt_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k, const 
                      int32_t head_dim, float scale, void *stream);
 
 /*
+ * The 8-bit cache -- a paged pool that holds K and V as 8-bit codes with one fp32 scale for each
+ * block and kv head ("mini-vLLM" README, paged KV-cache paragraph: the pool's blocks are the unit
+ * of everything).  Decode reads every byte of its context, so that half the bytes are half the
+ * time, and twice the tokens fit.
+ *   k_cache, v_cache : [num_blocks][num_kv_heads][block_size][head_dim] codes of `kind`
+ *   k_scale, v_scale : [num_blocks][num_kv_heads] fp32
+ * A code c of block n and kv head h stands for c * scale[n][h].  PKV_Q8_INT8: whole numbers of
+ * [-127, 127]; PKV_Q8_E4M3: 8-bit floats (4 exponent bits, 3 of the fraction, largest 448).
+ * int8 keeps each value to half of 1/127 of the block's largest; e4m3 to 2^-4 of itself, down
+ * to 2^-10 / 448 of the largest.  head_dim 64 or 128; block_size a power of two in [8, 256];
+ * num_blocks * num_kv_heads * block_size < 2^31; caches 16-byte, scales 4-byte aligned.
+ * Pages and scales need no initial values: a page begins with the write of its first row.
+ */
+enum { PKV_Q8_E4M3 = 0, PKV_Q8_INT8 = 1 };
+typedef struct pkv_q8_cache {
+  void *k_cache, *v_cache;
+  float *k_scale, *v_scale;
+  int32_t kind; /* PKV_Q8_* */
+} pkv_q8_cache;
+
+/*
+ * paged_kv_write_q8 -- each sequence's newest tokens, quantised into its pages.
+ *
+ * Sequence b holds L_b = context_lens[b] tokens, these included; its newest n_b =
+ * query_start[b+1] - query_start[b] (DEVICE int32 [num_seqs + 1]) are rows query_start[b] ..
+ * query_start[b+1]-1 of k and v, at positions L_b - n_b .. L_b - 1 of its block table (as in
+ * paged_prefill_attention).  query_start NULL: one token for each sequence with L_b > 0, row b.
+ * One token's kv heads are contiguous; the strides, in elements, lead from one token to the next
+ * (multiples of 8), so that k and v may be slices of one fused projection.  k, v 16-byte aligned.
+ *
+ * For every page that gets a row, and every kv head (k; v alike), with x its new rows:
+ *   old = the page's scale, or 0 where its row 0 is among them (the page begins here);
+ *   s   = max(old, |x|max / top), top = 127 or 448, the quotient at least 2^-126; 0 if old and
+ *         x are all 0;  NaN if a value of x is not finite, or old is NaN;
+ *   codes of x = round(x / s);   and where s > old, the rows of the page before the new ones are
+ *   rounded anew: round((c * old) / s)
+ * in fp32, each operation rounded once, codes to nearest with halves to even.  So a page with a
+ * value that is not finite reads as NaN until it begins again.  Rows behind the new ones, and
+ * pages without a new row, are left as they were.  No two sequences may write into one page in
+ * one call (shared pages are copied first, pkv_bm_append_slots_cow), nor may a page's row 0
+ * be written again while rows behind it are to be kept.
+ *
+ * max_query_len >= every n_b.  A sequence whose lengths do not fit (n_b over that or over L_b,
+ * L_b over the table's capacity, rows past num_tokens) is skipped with PKV_DEVERR_CONTEXT_LEN; a
+ * page outside the pool is skipped with PKV_DEVERR_BLOCK_ID.
+ */
+int paged_kv_write_q8(const pkv_bf16 *k, const pkv_bf16 *v, int64_t k_stride, int64_t v_stride,
+                      const int32_t *query_start, int64_t num_tokens, int32_t max_query_len,
+                      const int32_t *block_tables, int32_t max_blocks_per_seq,
+                      const int32_t *context_lens, int32_t num_seqs, const pkv_q8_cache *cache,
+                      const pkv_cache_desc *desc, void *stream);
+
+/*
+ * paged_kv_write_rope_q8 -- paged_kv_write_q8 of k rotated as by paged_kv_write_rope (rounded to
+ * bf16, then quantised).  With q != NULL ([num_tokens][num_q_heads][head_dim], strided alike) the
+ * rotated q goes to q_out, which may be q; rows of no sequence are not written.  positions
+ * (DEVICE int64 [num_tokens]) or, where NULL, each token's position in its sequence.  A position
+ * outside [0, max_position) raises PKV_DEVERR_POSITION: that token's k and q rows are skipped.
+ */
+int paged_kv_write_rope_q8(const pkv_bf16 *k, const pkv_bf16 *v, int64_t k_stride, int64_t v_stride,
+                           const pkv_bf16 *q, pkv_bf16 *q_out, int64_t q_stride,
+                           int64_t q_out_stride, int32_t num_q_heads, const int64_t *positions,
+                           const float *cos_sin, int64_t max_position, int32_t rotary_dim,
+                           int32_t neox_style, const int32_t *query_start, int64_t num_tokens,
+                           int32_t max_query_len, const int32_t *block_tables,
+                           int32_t max_blocks_per_seq, const int32_t *context_lens,
+                           int32_t num_seqs, const pkv_q8_cache *cache,
+                           const pkv_cache_desc *desc, void *stream);
+
+/*
+ * paged_kv_read_q8 -- the reading back: row i of k_out and v_out is bf16(c * scale) of the token
+ * that paged_kv_write_q8 takes from row i of k and v, same arguments.  With n_b = L_b that is a
+ * sequence's whole context.  Rows of no sequence are left as they were; so are a skipped
+ * sequence's (lengths that do not fit).  A page outside the pool is read as block 0.
+ */
+int paged_kv_read_q8(pkv_bf16 *k_out, pkv_bf16 *v_out, int64_t k_stride, int64_t v_stride,
+                     const int32_t *query_start, int64_t num_tokens, int32_t max_query_len,
+                     const int32_t *block_tables, int32_t max_blocks_per_seq,
+                     const int32_t *context_lens, int32_t num_seqs, const pkv_q8_cache *cache,
+                     const pkv_cache_desc *desc, void *stream);
+
+/*
+ * paged_decode_attention_q8 -- paged_decode_attention over an 8-bit cache:
+ *   K_t = k_cache[n][g][t % BS] * k_scale[n][g],  n = block_tables[b][t / BS];  V_t alike
+ * with exact codes and q, fp32 sums and softmax; the weights enter the product with V in fp16,
+ * the largest as 2^15, times their page's scale over the largest scale so far (each off by 2^-11
+ * of itself, or by 2^-40 of the largest |v| times weight where that is more).  Sizes, alignment
+ * and bad values as in paged_decode_attention.
+ *
+ * The workspace (paged_decode_q8_workspace_size() bytes) must be zero-filled before its first
+ * use, and every call that completes leaves it ready for the next one of any sizes that it is
+ * large enough for; its size goes by the heads alone.  Calls that share it must not overlap on
+ * the GPU.  One launch: as many CTAs as the GPU holds at once, each with an even share of all
+ * sequences' keys.
+ */
+size_t paged_decode_q8_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                      int32_t head_dim, int32_t max_context_len);
+int paged_decode_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, const pkv_q8_cache *cache,
+                              const int32_t *block_tables, int32_t max_blocks_per_seq,
+                              const int32_t *context_lens, int32_t max_context_len,
+                              int32_t num_seqs, int32_t num_q_heads, const pkv_cache_desc *desc,
+                              float scale, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * paged_decode_step_q8, paged_decode_step_rope_q8 -- one decode step: paged_kv_write_q8 (or
+ * paged_kv_write_rope_q8, q rotated into q_out, contiguous) of one token for each sequence, then
+ * paged_decode_attention_q8 over the updated cache (with q_out).  k, v, q: row b is sequence b's.
+ * Both are checked before either is enqueued; the attention is a programmatic dependent of the
+ * write.
+ */
+int paged_decode_step_q8(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k, const pkv_bf16 *v,
+                         int64_t k_stride, int64_t v_stride, const pkv_q8_cache *cache,
+                         const int32_t *block_tables, int32_t max_blocks_per_seq,
+                         const int32_t *context_lens, int32_t max_context_len, int32_t num_seqs,
+                         int32_t num_q_heads, const pkv_cache_desc *desc, float scale,
+                         void *workspace, size_t workspace_bytes, void *stream);
+int paged_decode_step_rope_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t q_stride, pkv_bf16 *q_out,
+                              const pkv_bf16 *k, const pkv_bf16 *v, int64_t k_stride,
+                              int64_t v_stride, const int64_t *positions, const float *cos_sin,
+                              int64_t max_position, int32_t rotary_dim, int32_t neox_style,
+                              const pkv_q8_cache *cache, const int32_t *block_tables,
+                              int32_t max_blocks_per_seq, const int32_t *context_lens,
+                              int32_t max_context_len, int32_t num_seqs, int32_t num_q_heads,
+                              const pkv_cache_desc *desc, float scale, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
+ * paged_prefill_attention_q8 -- paged_prefill_attention over an 8-bit cache: the contexts are
+ * read back as bf16 pages into the workspace (paged_prefill_q8_workspace_size() bytes, no initial
+ * values), and the prefill kernel runs over those.  Sizes and rules of paged_prefill_attention.
+ */
+size_t paged_prefill_q8_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t block_size, int32_t max_context_len);
+int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, const pkv_q8_cache *cache,
+                               const int32_t *block_tables, int32_t max_blocks_per_seq,
+                               const int32_t *context_lens, int32_t max_context_len,
+                               const int32_t *query_start, int32_t max_query_len, int32_t num_seqs,
+                               int32_t num_q_heads, const pkv_cache_desc *desc, float scale,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * paged_decode_split -- flash-decoding partition kernel (split-K over the keys;
  * the FlashAttention-2 online-softmax algebra that the first page references).
  *

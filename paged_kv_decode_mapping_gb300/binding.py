@@ -44,9 +44,15 @@ class pkv_cache_desc(ctypes.Structure):
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
+class pkv_q8_cache(ctypes.Structure):
+    _fields_ = [("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("kind", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _i32, _i64, _f32, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _D = ctypes.POINTER(pkv_cache_desc)
+_Q8 = ctypes.POINTER(pkv_q8_cache)
 
 _lib.paged_kv_write.argtypes = [_P, _P, _P, _i64, _P, _P, _D, _P]
 _lib.paged_kv_write.restype = ctypes.c_int
@@ -91,6 +97,28 @@ _lib.paged_prefill_attention.restype = ctypes.c_int
 _lib.prompt_attention.argtypes = [_P, _P, _P, _P, _i64, _i64, _i64, _i64, _P, _i64, _i32, _i32,
                                   _i32, _i32, _i32, _f32, _P]
 _lib.prompt_attention.restype = ctypes.c_int
+_lib.paged_kv_write_q8.argtypes = [_P, _P, _i64, _i64, _P, _i64, _i32, _P, _i32, _P, _i32, _Q8, _D, _P]
+_lib.paged_kv_write_q8.restype = ctypes.c_int
+_lib.paged_kv_write_rope_q8.argtypes = [_P, _P, _i64, _i64, _P, _P, _i64, _i64, _i32, _P, _P, _i64, _i32,
+                                        _i32, _P, _i64, _i32, _P, _i32, _P, _i32, _Q8, _D, _P]
+_lib.paged_kv_write_rope_q8.restype = ctypes.c_int
+_lib.paged_kv_read_q8.argtypes = [_P, _P, _i64, _i64, _P, _i64, _i32, _P, _i32, _P, _i32, _Q8, _D, _P]
+_lib.paged_kv_read_q8.restype = ctypes.c_int
+_lib.paged_decode_q8_workspace_size.argtypes = [_i32] * 5
+_lib.paged_decode_q8_workspace_size.restype = _sz
+_lib.paged_decode_attention_q8.argtypes = [_P, _P, _Q8, _P, _i32, _P, _i32, _i32, _i32, _D, _f32, _P, _sz, _P]
+_lib.paged_decode_attention_q8.restype = ctypes.c_int
+_lib.paged_decode_step_q8.argtypes = [_P, _P, _P, _P, _i64, _i64, _Q8, _P, _i32, _P, _i32, _i32, _i32, _D,
+                                      _f32, _P, _sz, _P]
+_lib.paged_decode_step_q8.restype = ctypes.c_int
+_lib.paged_decode_step_rope_q8.argtypes = [_P, _P, _i64, _P, _P, _P, _i64, _i64, _P, _P, _i64, _i32, _i32,
+                                           _Q8, _P, _i32, _P, _i32, _i32, _i32, _D, _f32, _P, _sz, _P]
+_lib.paged_decode_step_rope_q8.restype = ctypes.c_int
+_lib.paged_prefill_q8_workspace_size.argtypes = [_i32] * 5
+_lib.paged_prefill_q8_workspace_size.restype = _sz
+_lib.paged_prefill_attention_q8.argtypes = [_P, _P, _Q8, _P, _i32, _P, _i32, _P, _i32, _i32, _i32, _D, _f32,
+                                            _P, _sz, _P]
+_lib.paged_prefill_attention_q8.restype = ctypes.c_int
 _lib.paged_decode_split.argtypes = [_P, _P, _P, _P, _P, _P, _i32, _P, _i32, _i32, _i32, _D, _f32,
                                     _i32, _P]
 _lib.paged_decode_split.restype = ctypes.c_int
@@ -642,6 +670,265 @@ def _prompt_checks(out, q, k, v) -> None:
             raise ValueError(f"{name}: a token's heads must be contiguous")
     if out.shape != q.shape or k.shape != v.shape:
         raise ValueError("out must have q's shape, and v k's")
+
+
+# ---- the 8-bit cache: codes [NB, Hkv, BS, D] int8 or float8_e4m3fn, scales [NB, Hkv] float32
+
+Q8_E4M3, Q8_INT8 = 0, 1
+_Q8_KINDS = {torch.float8_e4m3fn: Q8_E4M3, torch.int8: Q8_INT8}
+
+
+def _q8_cache(dev: int, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start=None):
+    """(pkv_q8_cache, pkv_cache_desc) of checked tensors on device `dev`; names what is wrong."""
+    kind = _Q8_KINDS.get(k_cache.dtype)
+    if kind is None:
+        raise TypeError(f"k_cache: expected torch.int8 or torch.float8_e4m3fn, got {k_cache.dtype}")
+    if not (_fine(dev, k_cache.dtype, k_cache, v_cache) and _fine(dev, torch.float32, k_scale, v_scale) and
+            _fine(dev, torch.int32, block_tables, context_lens, query_start)):
+        _need(k_cache, "k_cache", k_cache.dtype, 4)
+        _need(v_cache, "v_cache", k_cache.dtype, 4)
+        _need(k_scale, "k_scale", torch.float32, 2)
+        _need(v_scale, "v_scale", torch.float32, 2)
+        _need(block_tables, "block_tables", torch.int32, 2)
+        _need(context_lens, "context_lens", torch.int32, 1)
+        if query_start is not None:
+            _need(query_start, "query_start", torch.int32, 1)
+        _one_device(k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, block_tables=block_tables,
+                    context_lens=context_lens, query_start=query_start)
+        raise ValueError("the cache and the rows are on different devices")
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must be [NB, Hkv, BS, D], alike")
+    if k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
+        raise ValueError("k_scale and v_scale must be [NB, Hkv]")
+    if context_lens.dim() != 1 or block_tables.dim() != 2 or block_tables.shape[0] != context_lens.shape[0]:
+        raise ValueError("block_tables must be [B, M] and context_lens [B]")
+    if query_start is not None and query_start.shape != (context_lens.shape[0] + 1,):
+        raise ValueError("query_start must be [B + 1] for context_lens [B]")
+    NB, Hkv, BS, D = shape
+    return (pkv_q8_cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), kind),
+            pkv_cache_desc(NB, BS, Hkv, D))
+
+
+def _packed(t: torch.Tensor, name: str, tokens: int, D: int, dev: int) -> int:
+    """The token stride of rows t [tokens, heads, D] bf16 whose heads are contiguous."""
+    shape = t.shape
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != D:
+        raise ValueError(f"{name}: expected [{tokens}, heads, {D}], got shape {tuple(shape)}")
+    step, head, one = t.stride()
+    if tokens > 0 and (one != 1 or (shape[1] > 1 and head != D)):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: must be a CUDA tensor")
+        raise ValueError(f"{name}: on {t.device}, not where the other tensors and the current device are")
+    return step if tokens > 1 else shape[1] * D
+
+
+def _q8_rows(k, v, k_cache, names=("k", "v")):
+    """(device, tokens, strides) of k and v [T, Hkv, D]."""
+    dev = _home(k)
+    if k.dim() != 3 or k_cache.dim() != 4 or v.shape != k.shape or k.shape[1:] != (k_cache.shape[1], k_cache.shape[3]):
+        raise ValueError(f"{names[0]} and {names[1]} must be [T, Hkv, D] for a cache [NB, Hkv, BS, D]")
+    T, D = k.shape[0], k.shape[2]
+    return dev, T, _packed(k, names[0], T, D, dev), _packed(v, names[1], T, D, dev)
+
+
+def paged_kv_write_q8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                      k_scale: torch.Tensor, v_scale: torch.Tensor, block_tables: torch.Tensor,
+                      context_lens: torch.Tensor, query_start: Optional[torch.Tensor] = None,
+                      max_query_len: int = 1, stream=None) -> None:
+    """Each sequence's newest tokens, rows query_start[b] .. query_start[b+1]-1 of k and v
+    [T, Hkv, D] (the tokens may be strided), quantised into its pages at positions
+    context_lens[b] - n .. context_lens[b] - 1.  Without query_start: one token per sequence."""
+    dev, T, sk, sv = _q8_rows(k, v, k_cache)
+    c, d = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
+    B, M = block_tables.shape
+    _check(_lib.paged_kv_write_q8(k.data_ptr(), v.data_ptr(), sk, sv, _ptr(query_start), T, int(max_query_len),
+                                  block_tables.data_ptr(), M, context_lens.data_ptr(), B, ctypes.byref(c),
+                                  ctypes.byref(d), _stream(stream, dev)), "paged_kv_write_q8")
+
+
+def paged_kv_write_rope_q8(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor,
+                           v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                           block_tables: torch.Tensor, context_lens: torch.Tensor,
+                           query_start: Optional[torch.Tensor] = None, max_query_len: int = 1,
+                           q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                           positions: Optional[torch.Tensor] = None, rotary_dim: Optional[int] = None,
+                           neox_style: bool = True, stream=None) -> None:
+    """paged_kv_write_q8 of the rotated k; the rotated q goes to q_out (default: q itself).
+    positions [T] int64 default to the tokens' positions in their sequences."""
+    dev, T, sk, sv = _q8_rows(k, v, k_cache)
+    c, d = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
+    sq = so = heads = 0
+    if q is not None:
+        q_out = q if q_out is None else q_out
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        sq, so = _packed(q, "q", T, k.shape[2], dev), _packed(q_out, "q_out", T, k.shape[2], dev)
+        heads = q.shape[1]
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    r = _rope_table(cos_sin, positions, k.shape[2] if rotary_dim is None else int(rotary_dim), T, dev)
+    B, M = block_tables.shape
+    _check(_lib.paged_kv_write_rope_q8(k.data_ptr(), v.data_ptr(), sk, sv, _ptr(q), _ptr(q_out), sq, so, heads,
+                                       _ptr(positions), cos_sin.data_ptr(), cos_sin.shape[0], r,
+                                       1 if neox_style else 0, _ptr(query_start), T, int(max_query_len),
+                                       block_tables.data_ptr(), M, context_lens.data_ptr(), B, ctypes.byref(c),
+                                       ctypes.byref(d), _stream(stream, dev)), "paged_kv_write_rope_q8")
+
+
+def _rope_table(cos_sin, positions, r: int, tokens: int, dev: int) -> int:
+    if not (_fine(dev, torch.float32, cos_sin) and _fine(dev, torch.int64, positions)):
+        _need(cos_sin, "cos_sin", torch.float32, 2)
+        if positions is not None:
+            _need(positions, "positions", torch.int64, 1)
+        raise ValueError("cos_sin and positions: on another device than the rows")
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != r:
+        raise ValueError("cos_sin must be [max_position, rotary_dim]")
+    if positions is not None and positions.shape != (tokens,):
+        raise ValueError("positions must have one entry per token")
+    return r
+
+
+def paged_kv_read_q8(k_out: torch.Tensor, v_out: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     k_scale: torch.Tensor, v_scale: torch.Tensor, block_tables: torch.Tensor,
+                     context_lens: torch.Tensor, query_start: Optional[torch.Tensor] = None,
+                     max_query_len: int = 1, stream=None) -> None:
+    """Each sequence's newest query_start[b+1] - query_start[b] tokens back as bf16 rows
+    query_start[b] .. of k_out and v_out [T, Hkv, D] (the tokens may be strided)."""
+    dev, T, sk, sv = _q8_rows(k_out, v_out, k_cache, ("k_out", "v_out"))
+    c, d = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
+    B, M = block_tables.shape
+    _check(_lib.paged_kv_read_q8(k_out.data_ptr(), v_out.data_ptr(), sk, sv, _ptr(query_start), T,
+                                 int(max_query_len), block_tables.data_ptr(), M, context_lens.data_ptr(), B,
+                                 ctypes.byref(c), ctypes.byref(d), _stream(stream, dev)), "paged_kv_read_q8")
+
+
+def paged_decode_q8_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                   max_context_len: int) -> int:
+    return int(_lib.paged_decode_q8_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len))
+
+
+def paged_prefill_q8_workspace_size(num_seqs: int, num_kv_heads: int, head_dim: int, block_size: int,
+                                    max_context_len: int) -> int:
+    return int(_lib.paged_prefill_q8_workspace_size(num_seqs, num_kv_heads, head_dim, block_size, max_context_len))
+
+
+def _q8_query(out, q, k_cache, rows: Optional[int], dev: int) -> None:
+    if not _fine(dev, torch.bfloat16, q, out):
+        _need(q, "q", torch.bfloat16, 3)
+        _need(out, "out", torch.bfloat16, 3)
+        _one_device(q, out=out)
+    if q.dim() != 3 or k_cache.dim() != 4 or q.shape[2] != k_cache.shape[3] or (rows is not None and q.shape[0] != rows):
+        raise ValueError("q must be [rows, Hq, D] for a cache [NB, Hkv, BS, D]")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+
+
+def _q8_workspace(workspace, need: int, zeroed: bool, like: torch.Tensor, dev: int, stream) -> torch.Tensor:
+    if workspace is None:
+        with torch.cuda.stream(stream):  # made, and given back, in that stream's order
+            make = torch.zeros if zeroed else torch.empty
+            return make(max(need, 1), dtype=torch.uint8, device=like.device)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous and on the current device")
+    return workspace
+
+
+def paged_decode_attention_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                              k_scale: torch.Tensor, v_scale: torch.Tensor, block_tables: torch.Tensor,
+                              context_lens: torch.Tensor, max_context_len: int, scale: float,
+                              workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """paged_decode_attention over an 8-bit cache.  ``workspace`` (uint8, CUDA,
+    ``paged_decode_q8_workspace_size`` bytes, zero-filled before its first use) serves calls of
+    any sizes in turn; it may be omitted as there."""
+    dev = _home(q)
+    _q8_query(out, q, k_cache, context_lens.shape[0], dev)
+    c, d = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    B, Hq, D = q.shape
+    workspace = _q8_workspace(workspace, 0 if workspace is not None else paged_decode_q8_workspace_size(
+        B, Hq, d.num_kv_heads, D, int(max_context_len)), True, q, dev, stream)
+    _check(_lib.paged_decode_attention_q8(
+        out.data_ptr(), q.data_ptr(), ctypes.byref(c), block_tables.data_ptr(), block_tables.shape[1],
+        context_lens.data_ptr(), int(max_context_len), B, Hq, ctypes.byref(d), float(scale), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream, dev)), "paged_decode_attention_q8")
+
+
+def paged_decode_step_q8(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                         k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                         v_scale: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                         max_context_len: int, scale: float, workspace: Optional[torch.Tensor] = None,
+                         stream=None) -> None:
+    """One decode step over an 8-bit cache: paged_kv_write_q8 of one token per sequence, then
+    paged_decode_attention_q8 of q [B, Hq, D] (k, v [B, Hkv, D], tokens may be strided)."""
+    dev, T, sk, sv = _q8_rows(k, v, k_cache)
+    _q8_query(out, q, k_cache, T, dev)
+    c, d = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    B, Hq, D = q.shape
+    if context_lens.shape != (B,):
+        raise ValueError("q, k and v need one row per sequence")
+    workspace = _q8_workspace(workspace, 0 if workspace is not None else paged_decode_q8_workspace_size(
+        B, Hq, d.num_kv_heads, D, int(max_context_len)), True, q, dev, stream)
+    _check(_lib.paged_decode_step_q8(
+        out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), sk, sv, ctypes.byref(c), block_tables.data_ptr(),
+        block_tables.shape[1], context_lens.data_ptr(), int(max_context_len), B, Hq, ctypes.byref(d), float(scale),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream, dev)),
+        "paged_decode_step_q8")
+
+
+def paged_decode_step_rope_q8(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                              cos_sin: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                              k_scale: torch.Tensor, v_scale: torch.Tensor, block_tables: torch.Tensor,
+                              context_lens: torch.Tensor, max_context_len: int, scale: float,
+                              q_out: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                              rotary_dim: Optional[int] = None, neox_style: bool = True,
+                              workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """paged_decode_step_q8 with RoPE: q [B, Hq, D] (tokens may be strided) is rotated into the
+    contiguous q_out (default: q itself), k on its way into the cache."""
+    dev, T, sk, sv = _q8_rows(k, v, k_cache)
+    q_out = q if q_out is None else q_out
+    _q8_query(out, q_out, k_cache, T, dev)
+    if q.shape != q_out.shape:
+        raise ValueError("q_out must have q's shape")
+    sq = _packed(q, "q", T, k.shape[2], dev)
+    c, d = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    B, Hq, D = q.shape
+    if context_lens.shape != (B,):
+        raise ValueError("q, k and v need one row per sequence")
+    r = _rope_table(cos_sin, positions, D if rotary_dim is None else int(rotary_dim), T, dev)
+    workspace = _q8_workspace(workspace, 0 if workspace is not None else paged_decode_q8_workspace_size(
+        B, Hq, d.num_kv_heads, D, int(max_context_len)), True, q, dev, stream)
+    _check(_lib.paged_decode_step_rope_q8(
+        out.data_ptr(), q.data_ptr(), sq, q_out.data_ptr(), k.data_ptr(), v.data_ptr(), sk, sv, _ptr(positions),
+        cos_sin.data_ptr(), cos_sin.shape[0], r, 1 if neox_style else 0, ctypes.byref(c), block_tables.data_ptr(),
+        block_tables.shape[1], context_lens.data_ptr(), int(max_context_len), B, Hq, ctypes.byref(d), float(scale),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream, dev)),
+        "paged_decode_step_rope_q8")
+
+
+def paged_prefill_attention_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                               k_scale: torch.Tensor, v_scale: torch.Tensor, block_tables: torch.Tensor,
+                               context_lens: torch.Tensor, max_context_len: int, query_start: torch.Tensor,
+                               max_query_len: int, scale: float, workspace: Optional[torch.Tensor] = None,
+                               stream=None) -> None:
+    """paged_prefill_attention over an 8-bit cache.  ``workspace``: uint8, CUDA,
+    ``paged_prefill_q8_workspace_size`` bytes with any contents; it may be omitted."""
+    dev = _home(q)
+    _q8_query(out, q, k_cache, None, dev)
+    if query_start is None:
+        raise ValueError("query_start must be [B + 1]")
+    c, d = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
+    B, M = block_tables.shape
+    workspace = _q8_workspace(workspace, 0 if workspace is not None else paged_prefill_q8_workspace_size(
+        B, d.num_kv_heads, d.head_dim, d.block_size, int(max_context_len)), False, q, dev, stream)
+    _check(_lib.paged_prefill_attention_q8(
+        out.data_ptr(), q.data_ptr(), ctypes.byref(c), block_tables.data_ptr(), M, context_lens.data_ptr(),
+        int(max_context_len), query_start.data_ptr(), int(max_query_len), B, q.shape[1], ctypes.byref(d),
+        float(scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream, dev)),
+        "paged_prefill_attention_q8")
 
 
 def paged_decode_attention_noalloc(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,

@@ -128,6 +128,39 @@ cudaError_t read_prefill_errors(uint32_t *flags, int clear);
 cudaError_t read_page_errors(uint32_t *flags, int clear);
 cudaError_t read_tile_errors(uint32_t *flags, int clear);
 cudaError_t read_shared_errors(uint32_t *flags, int clear);
+cudaError_t read_q8_errors(uint32_t *flags, int clear);
+cudaError_t read_decode_q8_errors(uint32_t *flags, int clear);
+
+// The 8-bit cache: the checks of its descriptor, and the quantising write split into its host
+// checks and its launch.
+int check_q8(const pkv_q8_cache *q, const pkv_cache_desc *c, int32_t num_seqs, const char *fn);
+struct WriteQ8 {
+  const pkv_bf16 *k, *v;
+  int64_t k_stride, v_stride;
+  const int32_t *query_start;  // NULL: one token for each sequence
+  int64_t num_tokens;
+  int32_t max_query_len;
+  const int32_t *block_tables;
+  int32_t max_blocks;
+  const int32_t *context_lens;
+  int32_t num_seqs;
+  const pkv_q8_cache *cache;
+  const pkv_cache_desc *desc;
+  bool rope;
+  const pkv_bf16 *q;
+  pkv_bf16 *q_out;
+  int64_t q_stride, q_out_stride;
+  int32_t num_q_heads;
+  const int64_t *positions;  // NULL: each token's position in its sequence
+  const float *cos_sin;
+  int64_t max_position;
+  int32_t rotary_dim, neox_style;
+};
+int check_write_q8(const WriteQ8 &w, const char *fn);
+int launch_write_q8(const WriteQ8 &w, cudaStream_t stream);
+// Encodes the TMA map of a pool of 8-bit codes, rows of d bytes: box {d, box_rows}, 64- or
+// 128-byte swizzle; the caller holds attn_mutex().
+int codes_map(const void *codes, const pkv_cache_desc &c, int32_t box_rows, CUtensorMap *out);
 
 // The shared-prefix half of paged_decode_shared_prefix_attention (pkv_tiles.cu): the
 // partial results of split s of every query row of the groups, in row s of o_part

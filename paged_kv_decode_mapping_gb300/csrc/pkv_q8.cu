@@ -1,0 +1,710 @@
+// pkv_q8.cu -- the 8-bit paged cache: the quantising write (with or without rotary embedding),
+// the reading back, chunked prefill over it, and its pages' copies.
+//
+// A page of one kv head is block_size rows of head_dim codes and one fp32 scale s; a code c
+// stands for c * s.  The write gives each page that it touches the scale its rows need,
+//   s = max(old s, max |x| / top),     top = 127 (int8) or 448 (e4m3),
+// and the codes round(x / s); where s grew, the rows that the page held before are rounded
+// anew, round((c * old s) / s).  The new rows of a page are known to one group of threads, since
+// the call names sequences and not slots, so that nothing is shared between groups: no atomics,
+// the same bits every time.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "attn_device.cuh"
+#include "q8_device.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kQ8Threads = 256;
+constexpr int kQ8Unroll = 8;  // 16-byte vectors of new rows a thread keeps in registers
+
+// What names the tokens of a call: sequence b's newest n of context_lens[b], its rows in the
+// packed tensors from row0 on.
+struct Span {
+  const int32_t *tables, *lens, *start;
+  int64_t num_blocks, num_tokens;
+  int32_t max_blocks, num_seqs, max_new, num_kv_heads, block_size, log2_bs;
+};
+struct Tokens {
+  int32_t begin, end;  // positions; begin == end where there are none, or they do not fit
+  int64_t row0;        // packed row of position `begin`
+};
+
+// The tokens of sequence b.  Without `start` one token for each sequence that has any, packed row
+// b.  Lengths that do not fit the tables, the packed rows or max_new: none, and *bad is set.
+__device__ __forceinline__ Tokens tokens_of(const Span &s, int b, bool *bad) {
+  const int L = __ldg(s.lens + b);
+  int64_t row0 = b, n = L > 0 ? 1 : 0;
+  if (s.start) {
+    row0 = __ldg(s.start + b);
+    n = (int64_t)__ldg(s.start + b + 1) - row0;
+  }
+  *bad = L < 0 || (int64_t)L > (int64_t)s.max_blocks * s.block_size || n < 0 || n > s.max_new || n > L ||
+         row0 < 0 || row0 + n > s.num_tokens;
+  Tokens t;
+  t.end = *bad ? 0 : L;
+  t.begin = *bad ? 0 : L - (int)n;
+  t.row0 = row0;
+  return t;
+}
+
+// ---------------------------------------------------------------------------
+// Rotary embedding of 8 coordinates: products and sums in fp32, each rounded once, then bf16.
+
+struct Rope {
+  const float *cos_sin;      // [max_position][r]: the cosine of pair i at i, its sine at r/2 + i
+  const int64_t *positions;  // of the packed rows; NULL: a token's position in its sequence
+  int64_t max_position;
+  int32_t r, neox;
+};
+
+__device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+
+// Vector c (coordinates 8c .. 8c+7) of the row at `row`, rotated; cs: the position's cosines and
+// sines.  Coordinates at or past r stay as they are.
+__device__ __forceinline__ uint4 rotated(const uint4 *row, int c, const float *cs, const Rope &p) {
+  const uint4 x = row[c];  // (not a read-only load: q may be rotated in place)
+  if (8 * c >= p.r) return x;
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t o[4];
+  if (p.neox) {  // pairs (e, e + r/2): the partners are vector c +- r/16
+    const int half = p.r / 16;
+    const bool lo = c < half;
+    const int e = lo ? c : c - half;
+    const uint4 y = row[lo ? c + half : c - half];
+    const uint32_t v[4] = {y.x, y.y, y.z, y.w};
+    float cc[8], ss[8];
+    load8(cs + 8 * e, cc);
+    load8(cs + p.r / 2 + 8 * e, ss);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float f[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float own = __fmul_rn(k ? dev::bf16hi_to_f32(w[j]) : dev::bf16lo_to_f32(w[j]), cc[2 * j + k]);
+        const float other = __fmul_rn(k ? dev::bf16hi_to_f32(v[j]) : dev::bf16lo_to_f32(v[j]), ss[2 * j + k]);
+        f[k] = lo ? __fsub_rn(own, other) : __fadd_rn(own, other);
+      }
+      o[j] = dev::pack_bf16x2(f[0], f[1]);
+    }
+  } else {  // pairs (2i, 2i + 1): word j holds pair 4c + j
+    const float4 c4 = __ldg(reinterpret_cast<const float4 *>(cs + 4 * c));
+    const float4 s4 = __ldg(reinterpret_cast<const float4 *>(cs + p.r / 2 + 4 * c));
+    const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = dev::bf16lo_to_f32(w[j]), b = dev::bf16hi_to_f32(w[j]);
+      o[j] = dev::pack_bf16x2(__fsub_rn(__fmul_rn(a, cc[j]), __fmul_rn(b, ss[j])),
+                              __fadd_rn(__fmul_rn(b, cc[j]), __fmul_rn(a, ss[j])));
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// ---------------------------------------------------------------------------
+// The write.  One group of 2^log2_group threads (a warp to the whole CTA) per (sequence, touched
+// page, K or V, kv head): it holds the page's new rows in registers between finding their largest
+// value and rounding them; what does not fit in 8 vectors a thread is read a second time.
+
+struct WriteArgs {
+  Span s;
+  const uint4 *k, *v;           // rows of head_dim, heads contiguous
+  int64_t k_stride, v_stride;   // vectors from one token to the next
+  uint8_t *k_cache, *v_cache;
+  float *k_scale, *v_scale;     // [num_blocks][num_kv_heads]
+  int32_t pages;                // touched pages of a sequence, at most
+  int32_t log2_group;
+  int64_t items;                // groups
+  int64_t item_ctas;            // CTAs of them; the ones behind rotate q
+  Rope rope;
+  const uint4 *q;
+  uint4 *q_out;
+  int64_t q_stride, q_out_stride;
+  int32_t num_q_heads, q_ctas;  // CTAs per sequence that rotate its q rows
+};
+
+__device__ __forceinline__ uint32_t absmax(uint32_t m, const uint4 &x) {
+  m = __vmaxu2(m, x.x & 0x7fff7fffu);
+  m = __vmaxu2(m, x.y & 0x7fff7fffu);
+  m = __vmaxu2(m, x.z & 0x7fff7fffu);
+  return __vmaxu2(m, x.w & 0x7fff7fffu);
+}
+
+// The q rows of one sequence: a thread owns a rotation's whole unit (both partner vectors), so
+// that q_out may be q.
+template <int D>
+__device__ __forceinline__ void rotate_q(const WriteArgs &a, int64_t cta) {
+  const int b = (int)(cta / a.q_ctas), part = (int)(cta - (int64_t)b * a.q_ctas);
+  bool bad;
+  const Tokens t = tokens_of(a.s, b, &bad);
+  const int half = a.rope.neox ? a.rope.r / 16 : 0;
+  const int units = D / 8 - half;  // of a row
+  const int64_t n = (int64_t)(t.end - t.begin) * a.num_q_heads * units;
+  for (int64_t i = (int64_t)part * kQ8Threads + threadIdx.x; i < n; i += (int64_t)a.q_ctas * kQ8Threads) {
+    const int64_t row = i / units;
+    int c = (int)(i - row * units);
+    if (c >= half) c += half;  // vectors half .. 2 half - 1 belong to their partners
+    const int64_t tok = row / a.num_q_heads;
+    const int h = (int)(row - tok * a.num_q_heads);
+    const int64_t at = t.row0 + tok;
+    const int64_t pos = a.rope.positions ? __ldg(a.rope.positions + at) : t.begin + tok;
+    if (pos < 0 || pos >= a.rope.max_position) continue;  // reported by the k rows
+    const float *cs = a.rope.cos_sin + pos * a.rope.r;
+    const uint4 *src = a.q + at * a.q_stride + h * (D / 8);
+    uint4 *dst = a.q_out + at * a.q_out_stride + h * (D / 8);
+    const uint4 y0 = rotated(src, c, cs, a.rope);
+    if (c < half) {
+      const uint4 y1 = rotated(src, c + half, cs, a.rope);
+      dst[c + half] = y1;
+    }
+    dst[c] = y0;
+  }
+}
+
+template <int D, int KIND, bool ROPE>
+__global__ void __launch_bounds__(kQ8Threads) write_q8_kernel(const __grid_constant__ WriteArgs a) {
+  constexpr int V = D / 8;  // vectors of a row: 8 bf16 in, 8 codes out
+  // A decode kernel behind this one may start its set-up (paged_decode_step_q8).
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (ROPE) {
+    if ((int64_t)blockIdx.x >= a.item_ctas) {
+      rotate_q<D>(a, blockIdx.x - a.item_ctas);
+      return;
+    }
+  }
+  __shared__ uint32_t s_max[kQ8Threads / 32];
+  const int tid = threadIdx.x, group = 1 << a.log2_group, gt = tid & (group - 1);
+  const int64_t item = (int64_t)blockIdx.x * (kQ8Threads >> a.log2_group) + (tid >> a.log2_group);
+  bool live = item < a.items;
+  uint32_t i = live ? (uint32_t)item : 0u;
+  const int h = (int)(i % (uint32_t)a.s.num_kv_heads);
+  i /= (uint32_t)a.s.num_kv_heads;
+  const bool is_v = i & 1u;
+  i >>= 1;
+  const int b = (int)(i / (uint32_t)a.pages), j = (int)(i - (uint32_t)b * a.pages);
+  bool bad;
+  const Tokens t = tokens_of(a.s, b, &bad);
+  if (live && bad && gt == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
+  const int page = (t.begin >> a.s.log2_bs) + j;
+  const int64_t lo = (int64_t)page << a.s.log2_bs;  // the page's first position
+  const int r0 = max(t.begin - (int)min(lo, (int64_t)t.end), 0);
+  const int r1 = (int)min((int64_t)t.end - lo, (int64_t)a.s.block_size);
+  live = live && r1 > r0;  // rows r0 .. r1-1 are new, rows before r0 are held
+  int64_t phys = live ? __ldg(a.s.tables + (int64_t)b * a.s.max_blocks + page) : 0;
+  if (phys < 0 || phys >= a.s.num_blocks) {
+    if (gt == 0) raise_error(PKV_DEVERR_BLOCK_ID);
+    live = false;
+    phys = 0;
+  }
+  const int64_t unit = phys * a.s.num_kv_heads + h;
+  float *const scale = (is_v ? a.v_scale : a.k_scale) + unit;
+  uint8_t *const rows = (is_v ? a.v_cache : a.k_cache) + unit * a.s.block_size * D;
+  const float old = live && r0 > 0 ? *scale : 0.f;  // a page that begins here has none
+
+  const int64_t row0 = t.row0 + (lo + r0 - t.begin), stride = is_v ? a.v_stride : a.k_stride;
+  const uint4 *const src = (is_v ? a.v : a.k) + row0 * stride + h * V;
+  const int count = live ? (r1 - r0) * V : 0;
+  auto fetch = [&](int e, bool *skip) -> uint4 {
+    const int r = e / V, c = e % V;
+    const uint4 *const row = src + r * stride;
+    *skip = false;
+    if constexpr (ROPE) {
+      if (!is_v) {
+        const int64_t pos = a.rope.positions ? __ldg(a.rope.positions + row0 + r) : lo + r0 + r;
+        if (pos < 0 || pos >= a.rope.max_position) {
+          raise_error(PKV_DEVERR_POSITION);
+          *skip = true;
+          return make_uint4(0, 0, 0, 0);
+        }
+        return rotated(row, c, a.rope.cos_sin + pos * a.rope.r, a.rope);
+      }
+    }
+    return __ldg(row + c);
+  };
+  uint4 x[kQ8Unroll];
+  bool skip[kQ8Unroll];
+  uint32_t m = 0;
+#pragma unroll
+  for (int u = 0; u < kQ8Unroll; ++u) {
+    const int e = gt + u * group;
+    skip[u] = true;
+    x[u] = make_uint4(0, 0, 0, 0);
+    if (e < count) x[u] = fetch(e, &skip[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < kQ8Unroll; ++u) m = absmax(m, x[u]);
+  for (int e = gt + kQ8Unroll * group; e < count; e += group) {
+    bool none;
+    m = absmax(m, fetch(e, &none));
+  }
+  m = max(m & 0xffffu, m >> 16);  // bf16 patterns order as whole numbers, infinity and NaN on top
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (group > 32) {  // uniform over the grid
+    if ((tid & 31) == 0) s_max[tid >> 5] = m;
+    __syncthreads();
+    for (int w = 0; w < group / 32; ++w) m = max(m, s_max[((tid >> a.log2_group) << (a.log2_group - 5)) + w]);
+  } else {
+    __syncwarp();  // every lane has read the old scale
+  }
+  if (!live) return;
+  constexpr float kTop = q8::top<KIND>();
+  float to = old;
+  if (m >= 0x7f80u || old != old) {
+    to = __int_as_float(0x7fc00000);  // what is not finite has no place under a shared scale
+  } else if (m > 0u) {
+    to = fmaxf(old, fmaxf(__fdiv_rn(__uint_as_float(m << 16), kTop), 1.17549435e-38f));
+  }
+  if (gt == 0 && !(to == old && r0 > 0)) *scale = to;
+  const float by = to > 0.f ? to : (to == 0.f ? 1.f : to);
+  auto store = [&](int e, const uint4 &v) {
+    const uint32_t lo4 = q8::encode4<KIND>(__fdiv_rn(dev::bf16lo_to_f32(v.x), by), __fdiv_rn(dev::bf16hi_to_f32(v.x), by),
+                                           __fdiv_rn(dev::bf16lo_to_f32(v.y), by), __fdiv_rn(dev::bf16hi_to_f32(v.y), by));
+    const uint32_t hi4 = q8::encode4<KIND>(__fdiv_rn(dev::bf16lo_to_f32(v.z), by), __fdiv_rn(dev::bf16hi_to_f32(v.z), by),
+                                           __fdiv_rn(dev::bf16lo_to_f32(v.w), by), __fdiv_rn(dev::bf16hi_to_f32(v.w), by));
+    *reinterpret_cast<uint2 *>(rows + (int64_t)r0 * D + (int64_t)e * 8) = make_uint2(lo4, hi4);
+  };
+#pragma unroll
+  for (int u = 0; u < kQ8Unroll; ++u)
+    if (!skip[u]) store(gt + u * group, x[u]);
+  for (int e = gt + kQ8Unroll * group; e < count; e += group) {
+    bool none;
+    const uint4 v = fetch(e, &none);
+    if (!none) store(e, v);
+  }
+  if (to > old && r0 > 0) {  // the rows held before, in units of the new scale
+    for (int e = gt; e < r0 * (D / 16); e += group) {
+      uint4 *const p = reinterpret_cast<uint4 *>(rows) + e;
+      const uint4 v = *p;
+      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t z = q8::prep<KIND>(w[k]);
+        const float2 f = q8::f16x2_to_f32(q8::pair<KIND, 0>(z)), g = q8::f16x2_to_f32(q8::pair<KIND, 1>(z));
+        w[k] = q8::encode4<KIND>(__fdiv_rn(__fmul_rn(f.x, old), to), __fdiv_rn(__fmul_rn(f.y, old), to),
+                                 __fdiv_rn(__fmul_rn(g.x, old), to), __fdiv_rn(__fmul_rn(g.y, old), to));
+      }
+      *p = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Reading back: bf16(code * scale).  One group of threads per (sequence, page, K or V, kv head).
+
+struct ReadArgs {
+  Span s;
+  const uint8_t *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  uint4 *k_out, *v_out;
+  int64_t k_stride, v_stride;  // packed rows: vectors from one token to the next
+  int32_t *out_tables;         // pages: the whole contexts as pages of a pool of their own, page j
+  int32_t out_blocks;          //   of sequence b at b * out_blocks + j, and its table; else NULL
+  int32_t pages, log2_group;
+  int64_t items;
+};
+
+template <int D, int KIND>
+__global__ void __launch_bounds__(kQ8Threads) read_q8_kernel(const __grid_constant__ ReadArgs a) {
+  constexpr int V = D / 16;  // vectors of a row: 16 codes in, 2 x 8 bf16 out
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, group = 1 << a.log2_group, gt = tid & (group - 1);
+  const int64_t item = (int64_t)blockIdx.x * (kQ8Threads >> a.log2_group) + (tid >> a.log2_group);
+  if (item >= a.items) return;
+  uint32_t i = (uint32_t)item;
+  const int h = (int)(i % (uint32_t)a.s.num_kv_heads);
+  i /= (uint32_t)a.s.num_kv_heads;
+  const bool is_v = i & 1u;
+  i >>= 1;
+  const int b = (int)(i / (uint32_t)a.pages), j = (int)(i - (uint32_t)b * a.pages);
+  Tokens t;
+  if (a.out_tables) {  // lengths past the tables are cut, as the attention does
+    int L = __ldg(a.s.lens + b);
+    const int cap = (int)min((int64_t)a.s.max_blocks * a.s.block_size, (int64_t)a.s.max_new);
+    if ((L < 0 || L > cap) && gt == 0 && j == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
+    t.begin = 0;
+    t.end = min(max(L, 0), cap);
+    t.row0 = 0;
+    if (!is_v && h == 0 && gt == 0) a.out_tables[(int64_t)b * a.out_blocks + j] = b * a.out_blocks + j;
+  } else {
+    bool bad;
+    t = tokens_of(a.s, b, &bad);
+    if (bad && gt == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
+  }
+  const int page = (t.begin >> a.s.log2_bs) + j;
+  const int64_t lo = (int64_t)page << a.s.log2_bs;
+  const int r0 = max(t.begin - (int)min(lo, (int64_t)t.end), 0);
+  const int r1 = (int)min((int64_t)t.end - lo, (int64_t)a.s.block_size);
+  if (r1 <= r0) return;
+  const int64_t phys = __ldg(a.s.tables + (int64_t)b * a.s.max_blocks + page);
+  int64_t from = phys;
+  if (phys < 0 || phys >= a.s.num_blocks) {
+    if (gt == 0) raise_error(PKV_DEVERR_BLOCK_ID);
+    from = 0;
+  }
+  const int64_t unit = from * a.s.num_kv_heads + h;
+  const float scale = __ldg((is_v ? a.v_scale : a.k_scale) + unit);
+  const uint4 *const src =
+      reinterpret_cast<const uint4 *>((is_v ? a.v_cache : a.k_cache) + unit * a.s.block_size * D) + r0 * V;
+  uint4 *dst = is_v ? a.v_out : a.k_out;
+  int64_t stride;
+  if (a.out_tables) {
+    dst += (((int64_t)b * a.out_blocks + j) * a.s.num_kv_heads + h) * a.s.block_size * (D / 8);
+    stride = D / 8;
+  } else {
+    stride = is_v ? a.v_stride : a.k_stride;
+    dst += (t.row0 + (lo + r0 - t.begin)) * stride + h * (D / 8);
+  }
+  const int count = (r1 - r0) * V;
+  for (int e0 = gt; e0 < count; e0 += 4 * group) {
+    uint4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (e0 + u * group < count) x[u] = __ldcs(src + e0 + u * group);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = e0 + u * group;
+      if (e >= count) break;
+      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      uint32_t o[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t z = q8::prep<KIND>(w[k]);
+        const float2 f = q8::f16x2_to_f32(q8::pair<KIND, 0>(z)), g = q8::f16x2_to_f32(q8::pair<KIND, 1>(z));
+        o[2 * k] = dev::pack_bf16x2(__fmul_rn(f.x, scale), __fmul_rn(f.y, scale));
+        o[2 * k + 1] = dev::pack_bf16x2(__fmul_rn(g.x, scale), __fmul_rn(g.y, scale));
+      }
+      uint4 *const p = dst + (e / V) * stride + 2 * (e % V);
+      p[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
+int log2_group_of(int64_t vectors, int per_thread) {  // of one item's threads: a warp to a CTA
+  int r = 5;
+  while (r < 8 && ((int64_t)per_thread << r) < vectors) ++r;
+  return r;
+}
+
+// Pages that `n` consecutive tokens touch, at most.
+int64_t touched(int64_t n, int bs) { return n <= 0 ? 0 : (n + bs - 2) / bs + 1; }
+
+Span span_of(const int32_t *tables, int32_t max_blocks, const int32_t *lens, const int32_t *start,
+             int32_t max_new, int32_t num_seqs, int64_t num_tokens, const pkv_cache_desc &c) {
+  Span s;
+  s.tables = tables;
+  s.lens = lens;
+  s.start = start;
+  s.num_blocks = c.num_blocks;
+  s.num_tokens = num_tokens;
+  s.max_blocks = max_blocks;
+  s.num_seqs = num_seqs;
+  s.max_new = max_new;
+  s.num_kv_heads = c.num_kv_heads;
+  s.block_size = c.block_size;
+  s.log2_bs = ilog2(c.block_size);
+  return s;
+}
+
+bool misaligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+// What the write and the reading back check alike: x, y are the packed tensors.
+int check_span(const void *x, const void *y, int64_t x_stride, int64_t y_stride, const int32_t *start,
+               int64_t num_tokens, int32_t max_new, const int32_t *tables, int32_t max_blocks,
+               const int32_t *lens, int32_t num_seqs, const pkv_q8_cache *q, const pkv_cache_desc *c,
+               const char *fn) {
+  int rc = check_q8(q, c, num_seqs, fn);
+  if (rc) return rc;
+  if (num_seqs < 0 || num_tokens < 0 || max_new < 0)
+    return set_error(PKV_ERR_SHAPE, "%s: negative count", fn);
+  if (max_blocks <= 0) return set_error(PKV_ERR_SHAPE, "%s: max_blocks_per_seq must be positive", fn);
+  if (!start && max_new > 1)
+    return set_error(PKV_ERR_SHAPE, "%s: more than one token a sequence needs query_start", fn);
+  if (!start && num_tokens < num_seqs)
+    return set_error(PKV_ERR_SHAPE, "%s: fewer rows than sequences, and no query_start", fn);
+  const int64_t row = (int64_t)c->num_kv_heads * c->head_dim;
+  if (num_tokens > 1 && (x_stride < row || y_stride < row))
+    return set_error(PKV_ERR_SHAPE, "%s: a token stride is under num_kv_heads * head_dim", fn);
+  if (num_seqs == 0 || num_tokens == 0 || max_new == 0) return PKV_OK;
+  if (x_stride % 8 || y_stride % 8)
+    return set_error(PKV_ERR_ALIGN, "%s: token strides must be multiples of 8 elements", fn);
+  if (!x || !y || !tables || !lens) return set_error(PKV_ERR_NULL, "%s: NULL tensor pointer", fn);
+  if (!aligned16(x) || !aligned16(y)) return set_error(PKV_ERR_ALIGN, "%s: k and v must be 16-byte aligned", fn);
+  if (misaligned4(tables) || misaligned4(lens) || misaligned4(start))
+    return set_error(PKV_ERR_ALIGN, "%s: int32 tensors must be 4-byte aligned", fn);
+  const int64_t pages = std::min<int64_t>(touched(max_new, c->block_size), max_blocks);
+  if (pages * num_seqs > 0x7fffffffLL / (2 * c->num_kv_heads))
+    return set_error(PKV_ERR_UNSUPPORTED, "%s: more than 2^31-1 pages of heads", fn);
+  return PKV_OK;
+}
+
+int launch_read(const Span &s, const pkv_q8_cache &q, const pkv_cache_desc &c, pkv_bf16 *k_out, pkv_bf16 *v_out,
+                int64_t k_stride, int64_t v_stride, int32_t *out_tables, int32_t out_blocks, int64_t pages,
+                cudaStream_t stream) {
+  ReadArgs a;
+  a.s = s;
+  a.k_cache = static_cast<const uint8_t *>(q.k_cache);
+  a.v_cache = static_cast<const uint8_t *>(q.v_cache);
+  a.k_scale = q.k_scale;
+  a.v_scale = q.v_scale;
+  a.k_out = reinterpret_cast<uint4 *>(k_out);
+  a.v_out = reinterpret_cast<uint4 *>(v_out);
+  a.k_stride = k_stride / 8;
+  a.v_stride = v_stride / 8;
+  a.out_tables = out_tables;
+  a.out_blocks = out_blocks;
+  a.pages = (int32_t)pages;
+  a.items = pages * s.num_seqs * 2 * c.num_kv_heads;
+  a.log2_group = log2_group_of((int64_t)std::min(s.block_size, s.max_new) * c.head_dim / 16, 4);
+  const int per = kQ8Threads >> a.log2_group;
+  const unsigned ctas = (unsigned)((a.items + per - 1) / per);
+  const bool i8 = q.kind == PKV_Q8_INT8;
+  auto *const kern = c.head_dim == 64 ? (i8 ? read_q8_kernel<64, PKV_Q8_INT8> : read_q8_kernel<64, PKV_Q8_E4M3>)
+                                      : (i8 ? read_q8_kernel<128, PKV_Q8_INT8> : read_q8_kernel<128, PKV_Q8_E4M3>);
+  kern<<<ctas, kQ8Threads, 0, stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_error(e, "read_q8_kernel launch");
+  return PKV_OK;
+}
+
+}  // namespace
+
+cudaError_t read_q8_errors(uint32_t *flags, int clear) { return read_tu_errors(flags, clear); }
+
+int check_q8(const pkv_q8_cache *q, const pkv_cache_desc *c, int32_t num_seqs, const char *fn) {
+  if (!q || !c) return set_error(PKV_ERR_NULL, "%s: cache descriptor is NULL", fn);
+  if (q->kind != PKV_Q8_E4M3 && q->kind != PKV_Q8_INT8)
+    return set_error(PKV_ERR_UNSUPPORTED, "%s: unknown kind of codes %d", fn, q->kind);
+  if (c->num_blocks <= 0 || c->num_kv_heads <= 0 || c->block_size <= 0 || c->head_dim <= 0)
+    return set_error(PKV_ERR_SHAPE, "%s: cache sizes must be positive", fn);
+  if (c->head_dim != 64 && c->head_dim != 128)
+    return set_error(PKV_ERR_UNSUPPORTED, "%s: head_dim %d (built: 64, 128)", fn, c->head_dim);
+  if (c->block_size < 8 || c->block_size > 256 || (c->block_size & (c->block_size - 1)))
+    return set_error(PKV_ERR_UNSUPPORTED, "%s: block_size %d (built: powers of two 8..256)", fn, c->block_size);
+  if (c->num_blocks > 0x7fffffffLL / ((int64_t)c->num_kv_heads * c->block_size))
+    return set_error(PKV_ERR_UNSUPPORTED, "%s: pool has more than 2^31-1 rows", fn);
+  if (num_seqs > 65535) return set_error(PKV_ERR_UNSUPPORTED, "%s: num_seqs > 65535", fn);
+  if (num_seqs <= 0) return PKV_OK;
+  if (!q->k_cache || !q->v_cache || !q->k_scale || !q->v_scale)
+    return set_error(PKV_ERR_NULL, "%s: NULL cache or scale pointer", fn);
+  if (!aligned16(q->k_cache) || !aligned16(q->v_cache) || misaligned4(q->k_scale) || misaligned4(q->v_scale))
+    return set_error(PKV_ERR_ALIGN, "%s: caches must be 16-byte, scales 4-byte aligned", fn);
+  return PKV_OK;
+}
+
+int check_write_q8(const WriteQ8 &w, const char *fn) {
+  int rc = check_span(w.k, w.v, w.k_stride, w.v_stride, w.query_start, w.num_tokens, w.max_query_len,
+                      w.block_tables, w.max_blocks, w.context_lens, w.num_seqs, w.cache, w.desc, fn);
+  if (rc || !w.rope) return rc;
+  if (w.rotary_dim <= 0 || w.rotary_dim % 16 != 0 || w.rotary_dim > w.desc->head_dim)
+    return set_error(PKV_ERR_UNSUPPORTED, "%s: rotary_dim %d must be a positive multiple of 16 <= head_dim", fn,
+                     w.rotary_dim);
+  if (w.max_position <= 0) return set_error(PKV_ERR_SHAPE, "%s: max_position <= 0", fn);
+  if (w.q && w.num_q_heads <= 0) return set_error(PKV_ERR_SHAPE, "%s: num_q_heads <= 0", fn);
+  if (w.q && w.num_tokens > 1 && (w.q_stride < (int64_t)w.num_q_heads * w.desc->head_dim ||
+                                  w.q_out_stride < (int64_t)w.num_q_heads * w.desc->head_dim))
+    return set_error(PKV_ERR_SHAPE, "%s: a token stride of q is under num_q_heads * head_dim", fn);
+  if (w.num_tokens == 0 || w.num_seqs == 0 || w.max_query_len == 0) return PKV_OK;
+  if (!w.cos_sin || (w.q && !w.q_out)) return set_error(PKV_ERR_NULL, "%s: NULL cos_sin/q_out", fn);
+  if (!aligned16(w.cos_sin) || !aligned16(w.q) || !aligned16(w.q_out) ||
+      (reinterpret_cast<uintptr_t>(w.positions) & 7u))
+    return set_error(PKV_ERR_ALIGN, "%s: cos_sin and q 16-byte, positions 8-byte aligned", fn);
+  if (w.q && (w.q_stride % 8 || w.q_out_stride % 8))
+    return set_error(PKV_ERR_ALIGN, "%s: token strides must be multiples of 8 elements", fn);
+  return PKV_OK;
+}
+
+int launch_write_q8(const WriteQ8 &w, cudaStream_t stream) {
+  if (w.num_tokens == 0 || w.num_seqs == 0 || w.max_query_len == 0) return PKV_OK;
+  const pkv_cache_desc &c = *w.desc;
+  WriteArgs a = {};
+  a.s = span_of(w.block_tables, w.max_blocks, w.context_lens, w.query_start, w.max_query_len, w.num_seqs,
+                w.num_tokens, c);
+  a.k = reinterpret_cast<const uint4 *>(w.k);
+  a.v = reinterpret_cast<const uint4 *>(w.v);
+  a.k_stride = w.k_stride / 8;
+  a.v_stride = w.v_stride / 8;
+  a.k_cache = static_cast<uint8_t *>(w.cache->k_cache);
+  a.v_cache = static_cast<uint8_t *>(w.cache->v_cache);
+  a.k_scale = w.cache->k_scale;
+  a.v_scale = w.cache->v_scale;
+  a.pages = (int32_t)std::min<int64_t>(touched(w.max_query_len, c.block_size), w.max_blocks);
+  a.items = (int64_t)a.pages * w.num_seqs * 2 * c.num_kv_heads;
+  a.log2_group = log2_group_of((int64_t)std::min(c.block_size, w.max_query_len) * c.head_dim / 8, kQ8Unroll);
+  const int per = kQ8Threads >> a.log2_group;
+  a.item_ctas = (a.items + per - 1) / per;
+  int64_t ctas = a.item_ctas;
+  if (w.rope) {
+    a.rope.cos_sin = w.cos_sin;
+    a.rope.positions = w.positions;
+    a.rope.max_position = w.max_position;
+    a.rope.r = w.rotary_dim;
+    a.rope.neox = w.neox_style ? 1 : 0;
+    if (w.q) {
+      a.q = reinterpret_cast<const uint4 *>(w.q);
+      a.q_out = reinterpret_cast<uint4 *>(w.q_out);
+      a.q_stride = w.q_stride / 8;
+      a.q_out_stride = w.q_out_stride / 8;
+      a.num_q_heads = w.num_q_heads;
+      const int64_t vecs = (int64_t)w.max_query_len * w.num_q_heads * (c.head_dim / 8);
+      a.q_ctas = (int32_t)std::min<int64_t>((vecs + 4 * kQ8Threads - 1) / (4 * kQ8Threads), 16384);
+      ctas += (int64_t)a.q_ctas * w.num_seqs;
+    }
+  }
+  if (ctas > 0x7fffffffLL) return set_error(PKV_ERR_UNSUPPORTED, "paged_kv_write_q8: too many tokens");
+  const bool i8 = w.cache->kind == PKV_Q8_INT8;
+  void (*kern)(const WriteArgs) = nullptr;
+  if (w.rope)
+    kern = c.head_dim == 64
+               ? (i8 ? write_q8_kernel<64, PKV_Q8_INT8, true> : write_q8_kernel<64, PKV_Q8_E4M3, true>)
+               : (i8 ? write_q8_kernel<128, PKV_Q8_INT8, true> : write_q8_kernel<128, PKV_Q8_E4M3, true>);
+  else
+    kern = c.head_dim == 64
+               ? (i8 ? write_q8_kernel<64, PKV_Q8_INT8, false> : write_q8_kernel<64, PKV_Q8_E4M3, false>)
+               : (i8 ? write_q8_kernel<128, PKV_Q8_INT8, false> : write_q8_kernel<128, PKV_Q8_E4M3, false>);
+  kern<<<(unsigned)ctas, kQ8Threads, 0, stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_error(e, "write_q8_kernel launch");
+  return PKV_OK;
+}
+
+}  // namespace pkv
+
+using namespace pkv;
+
+PKV_API int paged_kv_write_q8(const pkv_bf16 *k, const pkv_bf16 *v, int64_t k_stride, int64_t v_stride,
+                              const int32_t *query_start, int64_t num_tokens, int32_t max_query_len,
+                              const int32_t *block_tables, int32_t max_blocks_per_seq,
+                              const int32_t *context_lens, int32_t num_seqs, const pkv_q8_cache *cache,
+                              const pkv_cache_desc *desc, void *stream) {
+  WriteQ8 w = {};
+  w.k = k, w.v = v, w.k_stride = k_stride, w.v_stride = v_stride;
+  w.query_start = query_start, w.num_tokens = num_tokens, w.max_query_len = max_query_len;
+  w.block_tables = block_tables, w.max_blocks = max_blocks_per_seq, w.context_lens = context_lens;
+  w.num_seqs = num_seqs, w.cache = cache, w.desc = desc;
+  int rc = check_write_q8(w, "paged_kv_write_q8");
+  if (!rc) rc = launch_write_q8(w, static_cast<cudaStream_t>(stream));
+  if (!rc) clear_error();
+  return rc;
+}
+
+PKV_API int paged_kv_write_rope_q8(const pkv_bf16 *k, const pkv_bf16 *v, int64_t k_stride, int64_t v_stride,
+                                   const pkv_bf16 *q, pkv_bf16 *q_out, int64_t q_stride, int64_t q_out_stride,
+                                   int32_t num_q_heads, const int64_t *positions, const float *cos_sin,
+                                   int64_t max_position, int32_t rotary_dim, int32_t neox_style,
+                                   const int32_t *query_start, int64_t num_tokens, int32_t max_query_len,
+                                   const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t *context_lens, int32_t num_seqs, const pkv_q8_cache *cache,
+                                   const pkv_cache_desc *desc, void *stream) {
+  WriteQ8 w = {};
+  w.k = k, w.v = v, w.k_stride = k_stride, w.v_stride = v_stride;
+  w.query_start = query_start, w.num_tokens = num_tokens, w.max_query_len = max_query_len;
+  w.block_tables = block_tables, w.max_blocks = max_blocks_per_seq, w.context_lens = context_lens;
+  w.num_seqs = num_seqs, w.cache = cache, w.desc = desc;
+  w.rope = true;
+  w.q = q, w.q_out = q_out, w.q_stride = q_stride, w.q_out_stride = q_out_stride, w.num_q_heads = num_q_heads;
+  w.positions = positions, w.cos_sin = cos_sin, w.max_position = max_position;
+  w.rotary_dim = rotary_dim, w.neox_style = neox_style;
+  int rc = check_write_q8(w, "paged_kv_write_rope_q8");
+  if (!rc) rc = launch_write_q8(w, static_cast<cudaStream_t>(stream));
+  if (!rc) clear_error();
+  return rc;
+}
+
+PKV_API int paged_kv_read_q8(pkv_bf16 *k_out, pkv_bf16 *v_out, int64_t k_stride, int64_t v_stride,
+                             const int32_t *query_start, int64_t num_tokens, int32_t max_query_len,
+                             const int32_t *block_tables, int32_t max_blocks_per_seq,
+                             const int32_t *context_lens, int32_t num_seqs, const pkv_q8_cache *cache,
+                             const pkv_cache_desc *desc, void *stream) {
+  int rc = check_span(k_out, v_out, k_stride, v_stride, query_start, num_tokens, max_query_len, block_tables,
+                      max_blocks_per_seq, context_lens, num_seqs, cache, desc, "paged_kv_read_q8");
+  if (!rc && num_seqs > 0 && num_tokens > 0 && max_query_len > 0) {
+    const Span s = span_of(block_tables, max_blocks_per_seq, context_lens, query_start, max_query_len, num_seqs,
+                           num_tokens, *desc);
+    rc = launch_read(s, *cache, *desc, k_out, v_out, k_stride, v_stride, nullptr, 0,
+                     std::min<int64_t>(touched(max_query_len, desc->block_size), max_blocks_per_seq),
+                     static_cast<cudaStream_t>(stream));
+  }
+  if (!rc) clear_error();
+  return rc;
+}
+
+// ---------------------------------------------------------------------------
+// Chunked prefill: the contexts' pages are read back into a bf16 pool in the workspace, and the
+// prefill kernel runs over that.  The tensor-core tiles want K and V in 16 bits in shared memory
+// (the weights of a causal row need more than the 4 bits of an e4m3 operand); a chunk of a few
+// hundred queries spends far more on its products than on the pool's 5 bytes for each code.
+
+namespace {
+
+struct PrefillLayout {
+  int64_t blocks;  // pages of a sequence
+  size_t k, v, tables, total;
+};
+
+bool prefill_layout(int32_t num_seqs, int32_t hkv, int32_t d, int32_t bs, int32_t max_len, PrefillLayout *p) {
+  if (num_seqs <= 0 || hkv <= 0 || bs <= 0 || max_len <= 0 || (d != 64 && d != 128)) return false;
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  p->blocks = ((int64_t)max_len + bs - 1) / bs;
+  if (p->blocks * num_seqs > 0x7fffffffLL / ((int64_t)hkv * bs)) return false;
+  const size_t pool = up((size_t)p->blocks * num_seqs * hkv * bs * d * 2);
+  p->k = 0;
+  p->v = pool;
+  p->tables = 2 * pool;
+  p->total = 2 * pool + up((size_t)p->blocks * num_seqs * 4);
+  return true;
+}
+
+}  // namespace
+
+PKV_API size_t paged_prefill_q8_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim,
+                                               int32_t block_size, int32_t max_context_len) {
+  PrefillLayout p;
+  return prefill_layout(num_seqs, num_kv_heads, head_dim, block_size, max_context_len, &p) ? p.total : 0;
+}
+
+PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, const pkv_q8_cache *cache,
+                                       const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                       const int32_t *context_lens, int32_t max_context_len,
+                                       const int32_t *query_start, int32_t max_query_len, int32_t num_seqs,
+                                       int32_t num_q_heads, const pkv_cache_desc *desc, float scale,
+                                       void *workspace, size_t workspace_bytes, void *stream) {
+  const char *const fn = "paged_prefill_attention_q8";
+  int rc = check_q8(cache, desc, num_seqs, fn);
+  if (!rc)
+    rc = check_decode(q, cache->k_cache, cache->v_cache, block_tables, max_blocks_per_seq, context_lens,
+                      max_context_len, num_seqs, num_q_heads, desc, fn);
+  if (rc) return rc;
+  if (max_query_len < 0 || max_query_len > max_context_len)
+    return set_error(PKV_ERR_SHAPE, "%s: need 0 <= max_query_len <= max_context_len", fn);
+  if (num_seqs == 0 || max_query_len == 0) {
+    clear_error();
+    return PKV_OK;
+  }
+  if (!out || !query_start) return set_error(PKV_ERR_NULL, "%s: NULL out/query_start", fn);
+  if (!aligned16(out)) return set_error(PKV_ERR_ALIGN, "%s: out must be 16-byte aligned", fn);
+  PrefillLayout p;
+  if (!prefill_layout(num_seqs, desc->num_kv_heads, desc->head_dim, desc->block_size, max_context_len, &p) ||
+      p.blocks * num_seqs > 0x7fffffffLL / (2 * desc->num_kv_heads))
+    return set_error(PKV_ERR_UNSUPPORTED, "%s: the contexts' pages have more than 2^31-1 rows", fn);
+  if (!workspace || workspace_bytes < p.total)
+    return set_error(PKV_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, workspace_bytes, p.total);
+  if (!aligned16(workspace)) return set_error(PKV_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+  char *const ws = static_cast<char *>(workspace);
+  pkv_bf16 *const k = reinterpret_cast<pkv_bf16 *>(ws + p.k), *const v = reinterpret_cast<pkv_bf16 *>(ws + p.v);
+  int32_t *const tables = reinterpret_cast<int32_t *>(ws + p.tables);
+  const Span s = span_of(block_tables, max_blocks_per_seq, context_lens, nullptr, max_context_len, num_seqs, 0, *desc);
+  rc = launch_read(s, *cache, *desc, k, v, 0, 0, tables, (int32_t)p.blocks, p.blocks,
+                   static_cast<cudaStream_t>(stream));
+  if (rc) return rc;
+  pkv_cache_desc pool = *desc;
+  pool.num_blocks = p.blocks * num_seqs;
+  return paged_prefill_attention(out, q, k, v, tables, (int32_t)p.blocks, context_lens, max_context_len,
+                                 query_start, max_query_len, num_seqs, num_q_heads, &pool, scale, stream);
+}

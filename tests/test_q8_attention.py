@@ -1,0 +1,344 @@
+"""Attention over the 8-bit cache against fp64 on the same codes.
+
+Tolerance: the output's rounding to bf16 is at most 2^-8 of it; a weight's rounding to fp16 at most
+2^-11 of the weight, so 2^-11 of sum p |v|; the scores' fp32 sums (at most 128 exact products and
+a few roundings of 2^-24 each, on scores up to some tens) and the exponential move each weight by
+less than 2^-12.  Together 2^-8 |out| + 2^-10 sum p |v|.  A weight is held times 2^15 (the largest
+weight being 1) and its page's V scale over the largest, in fp16, whose steps below 2^-14 are 2^-24: off
+by 2^-25 there, so by 2^-40 of the largest |v| of the context's codes, for each key.
+"""
+
+import math
+
+import pytest
+import torch
+
+import q8_ref as R
+from test_q8_cache import DEV, Batch, same, starts
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from paged_kv_decode_mapping_gb300 import build
+
+    build.build()
+    from paged_kv_decode_mapping_gb300 import binding
+
+    binding.pkv_device_errors(clear=True)
+    return binding
+
+
+def poison(b):
+    """NaN in all that no sequence owns: other pages' scales, and (e4m3) rows past the contexts."""
+    owned = {p for t in b.tables for p in t if p >= 0}
+    for p in range(b.nb):
+        if p not in owned:
+            b.ks[p] = b.vs[p] = math.nan
+    fill = 0x7f if b.dtype is torch.float8_e4m3fn else 0x80
+    for s, n in enumerate(b.lens):
+        if n % b.bs:
+            for codes in (b.k, b.v):
+                R.bits(codes)[b.tables[s][n // b.bs], :, n % b.bs:] = fill
+
+
+def check(got, want, mag, what=""):
+    err = (got.double() - want).abs()
+    bound = 2.0 ** -8 * want.abs() + 2.0 ** -10 * mag
+    bad = ~(err <= bound)
+    assert not bool(bad.any()), f"{what}: {int(bad.sum())} of {bad.numel()} off, worst {err.max():.3e}"
+
+
+def decode_ref(b, q, scale):
+    out, mag = torch.zeros(q.shape, dtype=torch.float64, device=DEV), torch.zeros(q.shape, dtype=torch.float64, device=DEV)
+    for s, n in enumerate(b.lens):
+        k, v = (R.values(c, sc, b.tables[s], 0, n, torch.float64) for c, sc in ((b.k, b.ks), (b.v, b.vs)))
+        o, m = R.attention(q[s:s + 1], k, v, scale)
+        out[s:s + 1], mag[s:s + 1] = o, m
+        if n:  # 2^-10 of this is n 2^-40 of the largest |v| that the head's scales can hold
+            top = b.vs[b.tables[s][:-(-n // b.bs)]].nan_to_num().amax(0).double() * R.TOP[b.dtype]
+            mag[s] += n * 2.0 ** -30 * top.repeat_interleave(q.shape[1] // b.hkv)[:, None]
+    return out, mag
+
+
+def decode(B, b, q, scale, **kw):
+    out = torch.full_like(q, 77.0)
+    B.paged_decode_attention_q8(out, q, *b.cache(), b.bt, b.cl, max(max(b.lens), 1), scale, **kw)
+    return out
+
+
+DECODE = [
+    # lens, q heads, kv heads, head_dim, block size
+    ([1], 1, 1, 64, 8),
+    ([128], 32, 8, 64, 16),
+    ([127, 128, 129, 0, 1, 255, 256, 257], 6, 2, 128, 16),
+    ([15, 16, 17, 31, 32, 33, 8, 9], 8, 1, 64, 8),
+    ([0, 0, 0], 4, 2, 64, 16),
+    ([700, 1, 2048, 0, 333], 14, 2, 128, 32),
+    ([3000], 8, 8, 64, 64),
+    ([5000, 4100, 300], 24, 8, 128, 16),
+    ([1000, 513], 10, 2, 128, 256),
+    ([777, 130], 3, 1, 64, 128),
+    ([100] * 200, 4, 4, 64, 16),
+    (list(range(0, 600, 2)), 6, 2, 64, 16),
+]
+
+
+@pytest.mark.parametrize("dtype", R.KINDS)
+@pytest.mark.parametrize("lens,hq,hkv,d,bs", DECODE)
+def test_decode(B, dtype, lens, hq, hkv, d, bs):
+    b = Batch(lens, dtype, hkv, d, bs, seed=20)
+    poison(b)
+    q = b.randn(len(lens), hq, d)
+    out = decode(B, b, q, d ** -0.5)
+    check(out, *decode_ref(b, q, d ** -0.5))
+    assert B.pkv_device_errors() == 0
+    assert torch.equal(out, decode(B, b, q, d ** -0.5))  # the same bits every time
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,d,bs,n", [
+    (torch.int8, 1, 1, 64, 16, 120000), (torch.float8_e4m3fn, 8, 1, 128, 32, 100003),
+    (torch.int8, 4, 2, 128, 64, 40001),
+])
+def test_one_long_context(B, dtype, hq, hkv, d, bs, n):
+    """One context over every CTA of the GPU; a key that draws the query sits in each region."""
+    b = Batch([n], dtype, hkv, d, bs, seed=21)
+    poison(b)
+    q = b.randn(1, hq, d)
+    check(decode(B, b, q, d ** -0.5), *decode_ref(b, q, d ** -0.5))
+    # a query aimed at one key: the output is that key's value, wherever it lies
+    for t in (0, 1, 127, 128, n // 3, n // 2 + 5, n - 129, n - 2, n - 1):
+        k = R.values(b.k, b.ks, b.tables[0], t, t + 1)[0]  # [Hkv, D]
+        aim = (k * 6.0).repeat_interleave(hq // hkv, 0)[None].to(torch.bfloat16)
+        want, mag = decode_ref(b, aim, 1.0)
+        check(decode(B, b, aim, 1.0), want, mag, f"key {t}")
+        v = R.values(b.v, b.vs, b.tables[0], t, t + 1, torch.float64)[0].repeat_interleave(hq // hkv, 0)
+        assert float((want[0] - v).abs().max()) < 1e-3  # the aim is good: a lost key would show
+    assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", R.KINDS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_scales_far_apart(B, dtype, d):
+    """Pages whose V scales differ by up to 2^40, and K scales by 2^6."""
+    b = Batch([400, 400, 37], dtype, 2, d, 16, seed=22)
+    gen = torch.Generator().manual_seed(23)
+    b.vs *= torch.exp2(torch.randint(-20, 21, b.vs.shape, generator=gen).float()).to(DEV)
+    b.ks *= torch.exp2(torch.randint(-5, 2, b.ks.shape, generator=gen).float()).to(DEV)
+    b.vs[b.tables[1][3]] = 0.0
+    b.ks[b.tables[1][4]] = 0.0
+    q = b.randn(3, 8, d)
+    check(decode(B, b, q, d ** -0.5), *decode_ref(b, q, d ** -0.5))
+
+
+@pytest.mark.parametrize("dtype", R.KINDS)
+def test_queries_of_any_size(B, dtype):
+    """Rows of q between 2^-100 and 2^100 (the scale undoes them), with small values beside large."""
+    b = Batch([200] * 6, dtype, 1, 128, 16, seed=24)
+    q = b.randn(6, 2, 128)
+    base, mag = decode_ref(b, q, 128 ** -0.5)
+    for e in (-100, -30, 30, 100):
+        qq = (q.float() * 2.0 ** e).to(torch.bfloat16)
+        got = decode(B, b, qq, 128 ** -0.5 * 2.0 ** -e)
+        check(got, base, mag, f"2^{e}")
+    q[0] = 0
+    q[1, 0, :] = 0
+    q[1, 0, 7] = 2.0 ** -130  # not a normal number
+    check(decode(B, b, q, 128 ** -0.5), *decode_ref(b, q, 128 ** -0.5), "zeros")
+
+
+def test_long_tails_keep_their_weight(B):
+    """One key with a large score and 30000 equal ones far below it: their sum still counts."""
+    for dtype in R.KINDS:
+        b = Batch([30001], dtype, 1, 64, 16, seed=25)
+        R.bits(b.k).zero_()
+        b.k[b.tables[0][0], 0, 0, 0] = 100
+        b.ks.fill_(1.0)
+        b.vs.fill_(0.01)
+        R.bits(b.v)[:] = R.bits(torch.full((1,), 64.0, device=DEV).to(dtype))[0]
+        b.v[b.tables[0][0], 0, 0] = -64.0 if dtype is not torch.int8 else -64
+        q = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device=DEV)
+        q[0, 0, 0] = 1.0
+        for gap in (2.0, 8.0, 12.0, 14.0):  # in powers of e
+            want, mag = decode_ref(b, q, gap / 100)
+            check(decode(B, b, q, gap / 100), want, mag, f"gap {gap}")
+
+
+@pytest.mark.parametrize("dtype", R.KINDS)
+def test_not_finite(B, dtype):
+    """A page of scale NaN makes its (sequence, kv head) NaN and nothing else; a query's NaN its row."""
+    b = Batch([300, 40, 2000], dtype, 2, 64, 16, seed=26)
+    q = b.randn(3, 4, 64)
+    want, mag = decode_ref(b, q, 0.125)
+    b.vs[b.tables[0][18], 1] = math.nan
+    b.ks[b.tables[2][100], 0] = math.nan
+    q[1, 2, 9] = math.nan
+    out = decode(B, b, q, 0.125)
+    nan = torch.zeros(3, 4, dtype=torch.bool)
+    nan[0, 2:] = nan[2, :2] = nan[1, 2] = True
+    assert torch.equal(out.isnan().all(-1).cpu(), nan) and torch.equal(out.isnan().any(-1).cpu(), nan)
+    keep = ~nan.to(DEV)
+    check(out[keep], want[keep], mag[keep])
+    if dtype is torch.float8_e4m3fn:  # a NaN code within the context
+        b = Batch([300, 300], dtype, 2, 64, 16, seed=27)
+        R.bits(b.v)[b.tables[1][5], 0, 3, 11] = 0x7f
+        q = b.randn(2, 4, 64)
+        out = decode(B, b, q, 0.125)
+        nan = torch.zeros(2, 4, 64, dtype=torch.bool, device=DEV)
+        nan[1, :2, 11] = True
+        assert torch.equal(out.isnan(), nan)
+
+
+def test_bad_values_are_flagged(B):
+    b = Batch([100, 100, 100], torch.int8, 1, 64, 16, seed=28)
+    q = b.randn(3, 2, 64)
+    want, mag = decode_ref(b, q, 0.125)
+    b.cl[0] = -5
+    b.cl[2] = 1 << 30
+    out = torch.empty_like(q)
+    B.paged_decode_attention_q8(out, q, *b.cache(), b.bt, b.cl, 100, 0.125)
+    assert B.pkv_device_errors() == 4
+    assert bool((out[0] == 0).all())
+    check(out[1:], want[1:], mag[1:])  # the third's length is cut to max_context_len
+    b.cl[:] = 100
+    b.bt[1, 2] = b.nb + 7
+    b.bt[1, 3] = -2
+    B.paged_decode_attention_q8(out, q, *b.cache(), b.bt, b.cl, 100, 0.125)
+    assert B.pkv_device_errors() == 1
+    check(out[::2], want[::2], mag[::2])
+    assert bool(out.isfinite().all())
+
+
+def test_one_workspace_for_calls_of_any_sizes(B):
+    batches = [Batch([5000, 10], torch.int8, 2, 64, 16, seed=30), Batch([300] * 100, torch.float8_e4m3fn, 4, 128, 16, seed=31),
+               Batch([1], torch.int8, 1, 64, 8, seed=32), Batch([20000], torch.float8_e4m3fn, 1, 128, 32, seed=33)]
+    need = max(B.paged_decode_q8_workspace_size(len(b.lens), 2 * b.hkv, b.hkv, b.d, max(b.lens)) for b in batches)
+    ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        for b in batches:
+            q = b.randn(len(b.lens), 2 * b.hkv, b.d)
+            check(decode(B, b, q, 0.1, workspace=ws), *decode_ref(b, q, 0.1))
+    assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", R.KINDS)
+@pytest.mark.parametrize("d,hq,hkv,bs", [(64, 8, 2, 16), (128, 3, 3, 32)])
+def test_steps(B, dtype, d, hq, hkv, bs):
+    """Steps of a batch, as a model's layer runs them: the write, then attention over what it wrote."""
+    lens = [0, 15, 16, 200, 1300]
+    b = Batch([n + 20 for n in lens], dtype, hkv, d, bs, seed=40)
+    want_cache = b.copies()
+    ws = torch.zeros(B.paged_decode_q8_workspace_size(5, hq, hkv, d, 1400), dtype=torch.uint8, device=DEV)
+    for step in range(20):
+        b.lens = [n + step + 1 for n in lens]
+        b.cl = torch.tensor(b.lens, dtype=torch.int32, device=DEV)
+        x = b.randn(5, hq + 2 * hkv, d)
+        q, k, v = x[:, :hq].contiguous(), x[:, hq:hq + hkv], x[:, hq + hkv:]
+        out = torch.empty_like(q)
+        B.paged_decode_step_q8(out, q, k, v, *b.cache(), b.bt, b.cl, max(b.lens), d ** -0.5, workspace=ws)
+        for s, n in enumerate(b.lens):
+            R.write(want_cache[0], want_cache[2], k[s:s + 1], b.tables[s], n - 1)
+            R.write(want_cache[1], want_cache[3], v[s:s + 1], b.tables[s], n - 1)
+        for got, w, what in zip(b.cache(), want_cache, ("k codes", "v codes", "k scales", "v scales")):
+            same(got, w, f"{what}, step {step}")
+        check(out, *decode_ref(b, q, d ** -0.5), f"step {step}")
+    assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("neox", [True, False])
+def test_rotary_steps(B, neox):
+    dtype, d, hq, hkv, bs, r = torch.float8_e4m3fn, 128, 6, 2, 16, 64
+    lens = [30, 700, 0]
+    b = Batch([n + 6 for n in lens], dtype, hkv, d, bs, seed=41)
+    ang = torch.arange(800, dtype=torch.float64)[:, None] * 10000.0 ** (-2.0 * torch.arange(r // 2, dtype=torch.float64) / r)
+    table = torch.cat((ang.cos(), ang.sin()), 1).float().to(DEV)
+    want_cache = b.copies()
+    for step in range(6):
+        b.lens = [n + step + 1 for n in lens]
+        b.cl = torch.tensor(b.lens, dtype=torch.int32, device=DEV)
+        pos = torch.tensor([n - 1 for n in b.lens], device=DEV)
+        x = b.randn(3, hq + 2 * hkv, d)
+        q, k, v = x.split([hq, hkv, hkv], dim=1)
+        wq, wk = R.rotate(q, table, pos, r, neox), R.rotate(k, table, pos, r, neox)
+        out, q_out = (torch.empty(3, hq, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        B.paged_decode_step_rope_q8(out, q, k, v, table, *b.cache(), b.bt, b.cl, max(b.lens), d ** -0.5,
+                                    q_out=q_out, rotary_dim=r, neox_style=neox)
+        for s, n in enumerate(b.lens):
+            R.write(want_cache[0], want_cache[2], wk[s:s + 1], b.tables[s], n - 1)
+            R.write(want_cache[1], want_cache[3], v[s:s + 1], b.tables[s], n - 1)
+        for got, w in zip(b.cache(), want_cache):
+            same(got, w, "cache")
+        assert torch.equal(q_out, wq)
+        check(out, *decode_ref(b, wq, d ** -0.5))
+    assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", R.KINDS)
+@pytest.mark.parametrize("lens,new,hq,hkv,d,bs", [
+    ([100, 37, 0, 300], [5, 1, 0, 300], 4, 2, 64, 16), ([1000, 700], [130, 257], 6, 2, 128, 32),
+    ([50], [50], 8, 1, 128, 8), ([600, 256], [3, 256], 3, 3, 64, 256),
+])
+def test_prefill(B, dtype, lens, new, hq, hkv, d, bs):
+    b = Batch(lens, dtype, hkv, d, bs, seed=50)
+    poison(b)
+    t = sum(new)
+    q = b.randn(t, hq, d)
+    out = torch.full_like(q, 77.0)
+    ws = torch.full((B.paged_prefill_q8_workspace_size(len(lens), hkv, d, bs, max(lens)),), 0xff, dtype=torch.uint8,
+                    device=DEV)  # bf16 NaN all over
+    B.paged_prefill_attention_q8(out, q, *b.cache(), b.bt, b.cl, max(lens), starts(new), max(new), d ** -0.5,
+                                 workspace=ws)
+    at = 0
+    for s, (m, n) in enumerate(zip(lens, new)):
+        k, v = (R.values(c, sc, b.tables[s], 0, m).to(torch.bfloat16) for c, sc in ((b.k, b.ks), (b.v, b.vs)))
+        seen = torch.arange(m, device=DEV)[None, :] <= torch.arange(m - n, m, device=DEV)[:, None]
+        want, mag = R.attention(q[at:at + n], k, v, d ** -0.5, seen)
+        err = (out[at:at + n].double() - want).abs()
+        # the prefill kernel's weights are bf16: 2^-8 each
+        assert bool((err <= 2.0 ** -8 * want.abs() + 2.0 ** -7 * mag).all()), float(err.max())
+        at += n
+    assert B.pkv_device_errors() == 0
+
+
+def test_streams_and_graphs(B):
+    """A step captured once and replayed on other inputs; another stream with a workspace of its own."""
+    dtype, d, hq, hkv = torch.int8, 64, 8, 2
+    b = Batch([200, 900], dtype, hkv, d, 16, seed=60)
+    ws = torch.zeros(B.paged_decode_q8_workspace_size(2, hq, hkv, d, 900), dtype=torch.uint8, device=DEV)
+    q, k, v = b.randn(2, hq, d), b.randn(2, hkv, d), b.randn(2, hkv, d)
+    out = torch.empty_like(q)
+
+    def step():
+        B.paged_decode_step_q8(out, q, k, v, *b.cache(), b.bt, b.cl, 900, 0.125, workspace=ws)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    side = torch.cuda.Stream()
+    b2 = Batch([3000, 64], torch.float8_e4m3fn, hkv, 128, 16, seed=61)
+    q2 = b2.randn(2, hq, 128)
+    want2 = decode_ref(b2, q2, 0.1)
+    for i in range(5):
+        for t, s in ((q, 1.0), (k, 1.0 + i), (v, 2.0)):
+            t.copy_(b.randn(*t.shape) * s)
+        before = b.copies()
+        torch.cuda.synchronize()
+        g.replay()
+        out2 = torch.empty_like(q2)
+        with torch.cuda.stream(side):
+            pass
+        B.paged_decode_attention_q8(out2, q2, *b2.cache(), b2.bt, b2.cl, 3000, 0.1, stream=side)
+        torch.cuda.synchronize()
+        for s, n in enumerate(b.lens):
+            R.write(before[0], before[2], k[s:s + 1], b.tables[s], n - 1)
+            R.write(before[1], before[3], v[s:s + 1], b.tables[s], n - 1)
+        for got, w in zip(b.cache(), before):
+            same(got, w, "cache")
+        check(out, *decode_ref(b, q, 0.125), f"replay {i}")
+        check(out2, *want2, "side stream")
+    assert B.pkv_device_errors() == 0
