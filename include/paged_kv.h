@@ -525,9 +525,10 @@ int paged_kv_read_q8(pkv_bf16 *k_out, pkv_bf16 *v_out, int64_t k_stride, int64_t
 /*
  * paged_decode_attention_q8 -- paged_decode_attention over an 8-bit cache:
  *   K_t = k_cache[n][g][t % BS] * k_scale[n][g],  n = block_tables[b][t / BS];  V_t alike
- * with exact codes and q, fp32 sums and softmax; the weights enter the product with V in fp16,
- * the largest as 2^15, times their page's scale over the largest scale so far (each off by 2^-11
- * of itself, or by 2^-40 of the largest |v| times weight where that is more).  Sizes, alignment
+ * with exact codes, fp32 sums and softmax.  q and the weights enter the products in fp16, scaled:
+ * q, by a power of two for each row, is exact down to 2^-28 of the row's largest; a weight, times
+ * its page's V scale over the largest so far, is off by 2^-11 of itself, or by 2^-35 of the
+ * largest weight where that is more.  Sizes, alignment
  * and bad values as in paged_decode_attention.
  *
  * The workspace (paged_decode_q8_workspace_size() bytes) must be zero-filled before its first

@@ -13,9 +13,13 @@
 //  * No ldmatrix: the fragments' element order along dims (K) and along keys (V) is free, as long
 //    as both operands agree, so each lane loads 16 bytes in a row and widens them in registers:
 //    K rows' dims 2 bytes at a time, V rows by interleaving the bytes of two keys (prmt).
-//  * The batch's keys, in 128-key chunks, are one list (sequence, kv head, chunk), and every CTA
-//    of a single wave takes an even share of it.  A (sequence, kv head) that several CTAs share
-//    is merged by the last of them, in the order of the keys whoever that is.
+//  * The batch's keys, in 128-key chunks, are one list (sequence, kv head, chunk), cut into even
+//    shares whatever lies at the cuts.  A (sequence, kv head) that several shares cut is merged by
+//    the last of them to end, in the order of the keys whoever that is.
+//  * One CTA per SM, of several groups: a producer and four consumer warps with a ring, and a
+//    share, of their own.  The producers issue their chunks in step.  As CTAs of their own, three
+//    to an SM, groups drew even parts of an SM's rate only on average: of equal shares the last
+//    was done 60 us after the start where the mean was 46 (256 contexts of 16 to 8192 tokens).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -29,80 +33,95 @@ namespace pkv {
 namespace {
 
 constexpr int kQ8Keys = 128;           // keys of a stage: 32 for each consumer warp
-constexpr int kQ8MinChunks = 2;        // chunks a CTA takes at least (fewer CTAs run otherwise)
-constexpr int kQ8MaxCtas = 1024;       // CTAs of a launch, at most
-constexpr float kWeightLog2 = 15.f;    // the largest weight is 2^15 (fp16 ends at 65504)
+constexpr int kQ8MinChunks = 2;        // chunks of a share at least (fewer shares otherwise)
+constexpr int kQ8MaxShares = 1024;
 
-constexpr int q8_stages(int d) { return d == 64 ? 4 : 3; }
-constexpr int q8_occupancy(int d) { return d == 64 ? 3 : 2; }
+__host__ __device__ constexpr int q8_groups(int d) { return d == 64 ? 3 : 2; }
+constexpr int q8_stages(int d) { return d == 64 ? 4 : 3; }  // of a group's ring
+__host__ __device__ constexpr int q8_threads(int d) { return q8_groups(d) * (kConsumers + 32); }
 
 struct Q8Desc {                 // one stage's chunk
-  int32_t b, g, key0, len;      // its first key, and the context's length
-  int32_t first, last;          // of this CTA's share of the (sequence, kv head)
-  int32_t slot;                 // partial row its result goes to; -1: the whole context is here
-  int32_t cta0, parts;          // CTAs that share it: cta0 .. cta0 + parts - 1
+  int32_t nkeys;                // keys in range
+  int32_t flags;                // kBegins | kEnds: of this share's part of the (sequence, kv head)
+  int32_t b, g;
+  int32_t slot;                 // partial row the result goes to; -1: the whole context is here
+  int32_t share0, parts;        // shares that cut it: share0 .. share0 + parts - 1
+  int32_t pad;
 };
+constexpr int32_t kBegins = 1, kEnds = 2;
 
 template <int D>
 struct Q8Smem {  // offsets from the 1024-byte aligned base
   static constexpr int kStages = q8_stages(D);
-  static constexpr uint32_t kTile = kQ8Keys * D;
-  static constexpr uint32_t kStage = 2 * kTile;
+  static constexpr uint32_t kStage = 2 * kQ8Keys * D;
   static constexpr uint32_t kQ = kMaxGroup * D * 2;
+  // of each group, from group * kGroup
   static constexpr uint32_t q = kStages * kStage;
-  static constexpr uint32_t scales = q + kStages * kQ;             // ks[16], vs[16] of a stage
+  static constexpr uint32_t scales = q + kStages * kQ;             // (K's, V's) of a stage's boxes
   static constexpr uint32_t desc = scales + kStages * 128;
-  static constexpr uint32_t bars = (desc + kStages * (uint32_t)sizeof(Q8Desc) + 15) / 16 * 16;
-  static constexpr uint32_t misc = bars + kStages * 16;            // flag, last, issued, start b
-  static constexpr uint32_t sums = misc + 32;                      // the prefix scan's warps
-  static constexpr uint32_t total = sums + 64;
+  static constexpr uint32_t bars = desc + kStages * (uint32_t)sizeof(Q8Desc);  // full, empty
+  static constexpr uint32_t misc = bars + kStages * 16;            // flag, last, issued
+  static constexpr uint32_t kGroup = (misc + 16 + 1023) / 1024 * 1024;
+  // of the CTA
+  static constexpr uint32_t step = q8_groups(D) * kGroup;          // the producers' barrier
+  static constexpr uint32_t sums = step + 16;                      // the prefix scan: per warp,
+  static constexpr uint32_t incl = sums + q8_threads(D) / 32 * 8;  // per thread within its warp
+  static constexpr uint32_t total = incl + q8_threads(D) * 8;
 };
 constexpr size_t q8_smem(int d) { return 1024 + (d == 64 ? Q8Smem<64>::total : Q8Smem<128>::total); }
-static_assert(3 * (q8_smem(64) + 1024) <= 228 * 1024 && 2 * (q8_smem(128) + 1024) <= 228 * 1024,
-              "8-bit decode CTAs per SM");
-static_assert(kConsumerWarps * kMaxGroup * (128 + 2) * 4 <= (int)Q8Smem<128>::kStage &&
-                  kConsumerWarps * kMaxGroup * (64 + 2) * 4 <= (int)Q8Smem<64>::kStage,
-              "the warps' merge fits a stage");
+static_assert(q8_smem(64) <= 227 * 1024 && q8_smem(128) <= 227 * 1024, "the groups fit an SM");
+// A share's result in its last stage: per warp and head a row of D floats (4 apart, so that the
+// lanes' stores lie in different banks), then the references and the sums.
+__host__ __device__ constexpr int q8_row(int d) { return d + 4; }
+static_assert(kConsumerWarps * kMaxGroup * (q8_row(128) + 2) * 4 <= (int)Q8Smem<128>::kStage &&
+                  kConsumerWarps * kMaxGroup * (q8_row(64) + 2) * 4 <= (int)Q8Smem<64>::kStage,
+              "the warps' results fit a stage");
 
 struct Q8Args {
   const uint16_t *q;            // [B][Hq][D]
   uint16_t *out;
   const int32_t *tables, *lens;
   const float *k_scale, *v_scale;
-  float *o_part;                // [2 * CTAs][G][D]: a CTA's first share's row, then its last's
-  float *lse_part;              // [2 * CTAs][G], base 2
-  uint32_t *counters;           // [kQ8MaxCtas] by first sharing CTA; zero between calls
+  float *o_part;                // [2 * shares][G][D]: a share's first row, then its last's
+  float *lse_part;              // [2 * shares][G], base 2
+  uint32_t *counters;           // [kQ8MaxShares] by the first that cuts; zero between calls
   int64_t num_blocks;
   int32_t max_blocks, max_len, num_seqs, num_q_heads, num_kv_heads, group;
   int32_t block_size, log2_bs, box_rows, log2_box;
+  int32_t depth;                // 1: the first map leads to the other pool too
+  int32_t v_first;              // V's rows lie first in a box
   float scale_log2;
 };
 
-// Which key of a 16-key tile row r of the products' fragments is.  Lanes read K rows key_of(2j),
-// key_of(2j + 1) together, and V rows key_of(2t + i), t = 0 .. 3: with 64-byte rows this order puts
-// each such set into different banks; with 128-byte rows the swizzle does it alone.
+// A stage is filled by 128-byte-swizzled boxes, one pool's rows of a box and then the other's: rows
+// of 128 bytes hold one key (head_dim 128) or two (64).  Where the 16-byte chunk of dims 16 c ..
+// 16 c + 15 of key `key` of the first (v = 0) or second (v = 1) lies.
 template <int D>
-__device__ __forceinline__ int key_of(int r) {
-  return D == 128 ? r : (r & 8) | (int)((0x65742130u >> (4 * (r & 7))) & 7u);
+__device__ __forceinline__ uint32_t chunk_off(int key, int c, int v, int log2_box) {
+  const int in_box = key & ((1 << log2_box) - 1);
+  const uint32_t row = (uint32_t)(((2 * (key >> log2_box) + v) << log2_box) + in_box) * D & ~127u;
+  const uint32_t col = D == 128 ? (uint32_t)c : (uint32_t)(((key & 1) << 2) | c);
+  return row + ((col ^ ((row >> 7) & 7)) << 4);
 }
-// Byte offset of 16-byte chunk `c` of key row `key` in a tile filled by swizzled boxes.
-template <int D>
-__device__ __forceinline__ uint32_t chunk_off(int key, int c) {
-  return (uint32_t)(key * D + ((c ^ (D == 128 ? key & 7 : (key >> 1) & 3)) << 4));
-}
+// Which key of 16 row r of the score product is.  (Row r + 8 is not key r + 8, so that the 8 rows
+// that a transposing load reads together lie in 8 different bank groups.)
+__device__ __forceinline__ int key_of(int r) { return r < 8 ? r : 8 | ((r & 7) ^ 4); }
 
 __device__ __forceinline__ void lds(uint32_t (&w)[4], uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                : "r"(addr));
 }
-__device__ __forceinline__ void lds(uint32_t (&w)[2], uint32_t addr) {
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+// Two 16x16 byte matrices, transposed: matrix m's rows are the 16 bytes at lanes 16 m .. 16 m + 15's
+// addresses; r[2m + i] holds bytes gid + 8 i of its rows 4 tig .. 4 tig + 3.
+__device__ __forceinline__ void ldsm_b8_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
 }
-
 // D(16x8, f32) += A(16x16, fp16, row) * B(16x8, fp16, col)
-__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
@@ -114,21 +133,66 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// mbar_wait for waits that are mostly long: the thread may sleep up to 20 us at a time, so that
+// waiting warps take no issue slots from the working ones.  The same 2 s limit.
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = dev::globaltimer_ns();
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    if (done) return true;
+    if (dev::globaltimer_ns() - t0 > 2000000000ull) return false;
+  }
+}
 
-// A consumer warp's state.  Lane (gid, tig): O^T fragments, row gid of m-tile mt being dim
-// D/8 * gid + 2 mt and row gid + 8 the dim after it, for heads 2 tig and 2 tig + 1.
+// The largest of three (FMNMX3).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Weights are taken against a reference that moves only when a score is more than kSlack (in base
+// 2) over it, to that score: fp16 weights of 2^kTop at the reference have room for 2^kSlack more.
+// So most steps need no maximum over the warp.
+constexpr float kTop = 10.f, kSlack = 5.f;
+
+// K's codes as fp16 operands.  int8: the byte c + 128 alone is the fp16 number (c + 128) 2^-24; the
+// sum over dims of 128 q is taken off where the accumulator begins.  (So no subtraction for each
+// pair.  The sums' rounding is that of products with |code| up to 255.)  V's codes come without a
+// bias: theirs would grow with every key while the sum of v need not.
+template <int KIND>
+__device__ __forceinline__ void k_pairs(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  if constexpr (KIND == PKV_Q8_INT8) {  // bytes 0, 2 and 1, 3
+    lo = (w & 0x00ff00ffu) ^ 0x00800080u;
+    hi = ((w >> 8) & 0x00ff00ffu) ^ 0x00800080u;
+  } else {
+    lo = q8::pair<KIND, 0>(w);
+    hi = q8::pair<KIND, 1>(w);
+  }
+}
+
+// A consumer warp's state.  Lane (gid, tig): O^T fragments, rows gid and gid + 8 of m-tile mt being
+// dims 16 mt + gid and + 8, for heads 2 tig and 2 tig + 1.
 template <int D>
 struct Q8Acc {
   float o[D / 16][4];
-  float m0, m1, l0, l1;
+  float m0, m1, l0, l1;     // the heads' references; sums of weights, per lane
   float vref, vinv;         // the largest V scale so far, and 1 over it: o is in units of vref
-  uint32_t q[D / 16][2];    // fragments of q, fp16
+  uint32_t q[D / 16][2];    // fragments of q
   float f0, f1;             // scores' factors of the two heads, without K's scale
+  float b0, b1;             // what the two heads' raw scores begin with
 };
 
 // The (sequence, kv head)'s query rows at qs ([G][D] bf16, shared) as fragments: head gid, the
 // dims that this lane's K bytes hold (D/4 tig ..).
-template <int D>
+template <int D, int KIND>
 __device__ __forceinline__ void load_q(Q8Acc<D> &a, uint32_t qs, int group, int lane, float scale_log2) {
   const int gid = lane >> 2, tig = lane & 3;
   uint32_t w[D / 8];
@@ -143,89 +207,146 @@ __device__ __forceinline__ void load_q(Q8Acc<D> &a, uint32_t qs, int group, int 
       for (int k = 0; k < 4; ++k) w[4 * i + k] = v[k];
     }
   }
-  float mx = 0.f;
+  uint32_t mb = 0;
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i)
-    mx = fmaxf(mx, fmaxf(fabsf(dev::bf16lo_to_f32(w[i])), fabsf(dev::bf16hi_to_f32(w[i]))));
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-  // 2^(14 - exponent of mx), as far as that and its inverse are normal numbers
-  const int e = min(max(14 - ((int)(__float_as_uint(mx) >> 23) - 127), -126), 126);
+  for (int i = 0; i < D / 8; ++i) mb = __vmaxu2(mb, w[i] & 0x7fff7fffu);
+  mb = max(mb & 0xffffu, mb >> 16);
+  mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+  mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+  // 2^(14 - exponent of the largest), as far as that and its inverse are normal numbers
+  const int e = min(max(14 - ((int)(mb >> 7) - 127), -126), 126);
   const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-  const float down = __uint_as_float((uint32_t)(127 - e) << 23) * scale_log2;
+  float down = __uint_as_float((uint32_t)(127 - e) << 23) * scale_log2;
+  float sum = 0.f;
 #pragma unroll
-  for (int ks = 0; ks < D / 16; ++ks)
+  for (int i = 0; i < D / 8; ++i) {
+    const float lo = dev::bf16lo_to_f32(w[i]) * up, hi = dev::bf16hi_to_f32(w[i]) * up;
+    w[i] = pack_f16x2(lo, hi);
+    sum += lo + hi;
+  }
+  float begin = 0.f;
+  if constexpr (KIND == PKV_Q8_INT8) {
+    down *= 16777216.f;  // the codes' 2^-24
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    begin = -128.f * 5.9604645e-8f * sum;
+  }
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      a.q[ks][k] = pack_f16x2(dev::bf16lo_to_f32(w[2 * ks + k]) * up, dev::bf16hi_to_f32(w[2 * ks + k]) * up);
+  for (int i = 0; i < D / 16; ++i) {  // dims 4 i .. 4 i + 3 in the order of k_pairs' bytes
+    if constexpr (KIND == PKV_Q8_INT8) {
+      a.q[i][0] = __byte_perm(w[2 * i], w[2 * i + 1], 0x5410);
+      a.q[i][1] = __byte_perm(w[2 * i], w[2 * i + 1], 0x7632);
+    } else {
+      a.q[i][0] = w[2 * i];
+      a.q[i][1] = w[2 * i + 1];
+    }
+  }
   a.f0 = __shfl_sync(0xffffffffu, down, 8 * tig);  // lanes of heads 2 tig and 2 tig + 1
   a.f1 = __shfl_sync(0xffffffffu, down, 8 * tig + 4);
+  a.b0 = __shfl_sync(0xffffffffu, begin, 8 * tig);
+  a.b1 = __shfl_sync(0xffffffffu, begin, 8 * tig + 4);
 #pragma unroll
   for (int mt = 0; mt < D / 16; ++mt) a.o[mt][0] = a.o[mt][1] = a.o[mt][2] = a.o[mt][3] = 0.f;
   a.m0 = a.m1 = -INFINITY;
   a.l0 = a.l1 = a.vref = a.vinv = 0.f;
 }
 
-// Scores, softmax and weighted sum of the warp's 32 keys (the first nvalid of them in range) of a
-// stage: K tile at kb, V tile at vb, the boxes' scales at sc (ks[16], vs[16]).
-template <int D, int KIND>
-__device__ __forceinline__ void q8_tiles(Q8Acc<D> &a, uint32_t kb, uint32_t vb, const float *sc, int log2_box,
-                                         int warp, int lane, int nvalid) {
-  constexpr int KS = D / 16;
-  const int gid = lane >> 2, tig = lane & 3;
-  float s[2][4], vs[4];
-  float mx0 = -INFINITY, mx1 = -INFINITY, vmax = 0.f;
+// Where a lane reads in a stage, of its warp's 32 keys.
+struct Q8Lane {
+  uint32_t k[2][2];  // K: its first chunk of rows gid and gid + 8 of each 16 keys
+  uint32_t v;        // V: the first chunk of its row of the two transposed matrices
+};
+template <int D>
+__device__ __forceinline__ Q8Lane q8_lane(int warp, int lane, int log2_box, int v_first) {
+  const int gid = lane >> 2, tig = lane & 3, r = lane & 15;
+  Q8Lane x;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int nv = nvalid - 16 * t;  // uniform over the warp
-    vs[2 * t] = vs[2 * t + 1] = 0.f;
-    s[t][0] = s[t][1] = s[t][2] = s[t][3] = -INFINITY;
-    if (nv <= 0) continue;
-    float c[4] = {0.f, 0.f, 0.f, 0.f};
-    const int r0 = 32 * warp + 16 * t + key_of<D>(gid);
-    uint32_t w0[D / 16], w1[D / 16];
+    x.k[t][0] = chunk_off<D>(32 * warp + 16 * t + gid, (D / 64) * tig, v_first, log2_box);
+    x.k[t][1] = chunk_off<D>(32 * warp + 16 * t + key_of(gid + 8), (D / 64) * tig, v_first, log2_box);
+  }
+  // V's rows in the order of the weights' rows: 2 t, 2 t + 1, 2 t + 8, 2 t + 9 as bytes of a word
+  x.v = chunk_off<D>(32 * warp + 16 * (lane >> 4) + key_of(2 * (r >> 2) + (r & 1) + 8 * ((r >> 1) & 1)), 0, v_first ^ 1, log2_box);
+  return x;
+}
+
+// Raw scores of 16 keys, rows gid and gid + 8 (key_of(row)) x heads 2 tig, 2 tig + 1: the K chunks of
+// these rows are at k0 and k1.
+template <int D, int KIND>
+__device__ __forceinline__ void q8_scores(const Q8Acc<D> &a, float (&c)[4], uint32_t k0, uint32_t k1) {
+  c[0] = c[2] = a.b0;
+  c[1] = c[3] = a.b1;
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      uint32_t x[4], y[4];
-      lds(x, kb + chunk_off<D>(r0, (D / 64) * tig + i));
-      lds(y, kb + chunk_off<D>(r0 + 8, (D / 64) * tig + i));
+  for (int i = 0; i < D / 64; ++i) {  // (the next chunk is the other of a pair)
+    uint32_t x[4], y[4];
+    lds(x, k0 ^ (16u * i));
+    lds(y, k1 ^ (16u * i));
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        w0[4 * i + k] = q8::prep<KIND>(x[k]);
-        w1[4 * i + k] = q8::prep<KIND>(y[k]);
+    for (int k = 0; k < 4; ++k) {
+      uint32_t x0, x1, y0, y1;
+      k_pairs<KIND>(x[k], x0, x1);
+      k_pairs<KIND>(y[k], y0, y1);
+      mma_f16(c, x0, y0, x1, y1, a.q[4 * i + k][0], a.q[4 * i + k][1]);
+    }
+  }
+}
+
+// Scores, softmax and weighted sum of the warp's 32 keys (the first nvalid of them in range) of a
+// stage at sb, the boxes' scales (K's, V's) at sc.
+template <int D, int KIND>
+__device__ __forceinline__ void q8_tiles(Q8Acc<D> &a, uint32_t sb, const Q8Lane &at, const float2 *sc, int log2_box,
+                                         int warp, int lane, int nvalid) {
+  const int gid = lane >> 2, tig = lane & 3;
+  float s[2][4], vs[4], f0[4], f1[4];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) q8_scores<D, KIND>(a, s[t], sb + at.k[t][0], sb + at.k[t][1]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // 8 keys lie in one box; one box may hold more of these
+    if (i == 0 || (i == 2 && log2_box < 5) || log2_box < 4) {
+      const float2 f = sc[(32 * warp + 8 * i) >> log2_box];
+      vs[i] = f.y;
+      f0[i] = a.f0 * f.x;
+      f1[i] = a.f1 * f.x;
+    } else {
+      vs[i] = vs[i - 1];
+      f0[i] = f0[i - 1];
+      f1[i] = f1[i - 1];
+    }
+  }
+  if (nvalid < 32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (8 * i >= nvalid) vs[i] = 0.f;  // its box may not have been loaded
+      // scores of -inf; by a factor of 0 they would be NaN
+      if (16 * (i >> 1) + key_of(gid + 8 * (i & 1)) >= nvalid) {
+        s[i >> 1][2 * (i & 1)] = s[i >> 1][2 * (i & 1) + 1] = -INFINITY;
+        f0[i] = f1[i] = 1.f;
       }
     }
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-      mma_f16_16816(c, q8::pair<KIND, 0>(w0[ks]), q8::pair<KIND, 0>(w1[ks]), q8::pair<KIND, 1>(w0[ks]),
-                    q8::pair<KIND, 1>(w1[ks]), a.q[ks][0], a.q[ks][1]);
-    // a half of 8 keys lies in one box; a half past the range has no scale
-    const int b0 = (32 * warp + 16 * t) >> log2_box, b1 = (32 * warp + 16 * t + 8) >> log2_box;
-    const float ks0 = sc[b0], ks1 = nv > 8 ? sc[b1] : 0.f;
-    vs[2 * t] = sc[16 + b0];
-    vs[2 * t + 1] = nv > 8 ? sc[16 + b1] : 0.f;
-    if (key_of<D>(gid) < nv) {
-      s[t][0] = c[0] * (a.f0 * ks0);
-      s[t][1] = c[1] * (a.f1 * ks0);
-    }
-    if (key_of<D>(gid) + 8 < nv) {
-      s[t][2] = c[2] * (a.f0 * ks1);
-      s[t][3] = c[3] * (a.f1 * ks1);
-    }
-    mx0 = fmaxf(mx0, fmaxf(s[t][0], s[t][2]));
-    mx1 = fmaxf(mx1, fmaxf(s[t][1], s[t][3]));
-    vmax = fmaxf(vmax, fmaxf(vs[2 * t], vs[2 * t + 1]));
   }
+  float sh0 = kTop - softmax_ref(a.m0), sh1 = kTop - softmax_ref(a.m1);
+  float x[2][4];  // scores over the reference, plus kTop
 #pragma unroll
-  for (int x = 4; x < 32; x <<= 1) {
-    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, x));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, x));
+  for (int i = 0; i < 4; ++i) {
+    x[i >> 1][2 * (i & 1)] = fmaf(s[i >> 1][2 * (i & 1)], f0[i], sh0);
+    x[i >> 1][2 * (i & 1) + 1] = fmaf(s[i >> 1][2 * (i & 1) + 1], f1[i], sh1);
   }
-  const float mn0 = fmaxf(a.m0, mx0), mn1 = fmaxf(a.m1, mx1);
-  const float ref0 = softmax_ref(mn0), ref1 = softmax_ref(mn1);
-  // The running maxima and the largest V scale move rarely once a few keys are seen.
-  if (vmax > a.vref || __any_sync(0xffffffffu, mn0 > a.m0 || mn1 > a.m1)) {
-    float al0 = dev::ex2(a.m0 - ref0), al1 = dev::ex2(a.m1 - ref1);
+  float mx0 = max3(max3(x[0][0], x[0][2], x[1][0]), x[1][2], x[1][2]);
+  float mx1 = max3(max3(x[0][1], x[0][3], x[1][1]), x[1][3], x[1][3]);
+  const float vmax = max3(max3(vs[0], vs[1], vs[2]), vs[3], vs[3]);
+  // (A reference of -inf, no score over that so far, moves with the first one that is.)
+  const bool over = mx0 > kTop + kSlack || mx1 > kTop + kSlack || (a.m0 == -INFINITY && mx0 > -INFINITY) ||
+                    (a.m1 == -INFINITY && mx1 > -INFINITY);
+  if (vmax > a.vref || __any_sync(0xffffffffu, over)) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+    }
+    const float mn0 = fmaxf(a.m0, mx0 - sh0), mn1 = fmaxf(a.m1, mx1 - sh1);
+    float al0 = dev::ex2(a.m0 - softmax_ref(mn0)), al1 = dev::ex2(a.m1 - softmax_ref(mn1));
+    a.m0 = mn0;
+    a.m1 = mn1;
     a.l0 *= al0;
     a.l1 *= al1;
     if (vmax > a.vref) {
@@ -235,48 +356,53 @@ __device__ __forceinline__ void q8_tiles(Q8Acc<D> &a, uint32_t kb, uint32_t vb, 
       a.vref = vmax;
     }
 #pragma unroll
-    for (int mt = 0; mt < KS; ++mt) {
+    for (int mt = 0; mt < D / 16; ++mt) {
       a.o[mt][0] *= al0;
       a.o[mt][1] *= al1;
       a.o[mt][2] *= al0;
       a.o[mt][3] *= al1;
     }
-    a.m0 = mn0;
-    a.m1 = mn1;
+    sh0 = kTop - softmax_ref(mn0);
+    sh1 = kTop - softmax_ref(mn1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i >> 1][2 * (i & 1)] = fmaf(s[i >> 1][2 * (i & 1)], f0[i], sh0);
+      x[i >> 1][2 * (i & 1) + 1] = fmaf(s[i >> 1][2 * (i & 1) + 1], f1[i], sh1);
+    }
   }
+  uint32_t b[2][2];  // the weights as B operands of the two tiles
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int nv = nvalid - 16 * t;
-    if (nv <= 0) continue;
-    const float p0 = dev::ex2(s[t][0] - ref0 + kWeightLog2), p1 = dev::ex2(s[t][1] - ref1 + kWeightLog2);
-    const float p2 = dev::ex2(s[t][2] - ref0 + kWeightLog2), p3 = dev::ex2(s[t][3] - ref1 + kWeightLog2);
+    const float r0 = vs[2 * t] * a.vinv, r1 = vs[2 * t + 1] * a.vinv;
+    const float p0 = dev::ex2(x[t][0]), p1 = dev::ex2(x[t][1]), p2 = dev::ex2(x[t][2]), p3 = dev::ex2(x[t][3]);
     a.l0 += p0 + p2;
     a.l1 += p1 + p3;
-    const float r0 = vs[2 * t] * a.vinv, r1 = vs[2 * t + 1] * a.vinv;
-    const uint32_t b0 = dev::movmatrix_trans(pack_f16x2(p0 * r0, p1 * r0));
-    const uint32_t b1 = dev::movmatrix_trans(pack_f16x2(p2 * r1, p3 * r1));
-    // V bytes of 4 keys, D/8 dims from D/8 gid on; a row past the range may hold anything (e4m3
-    // has NaN codes): zeroed
-    uint32_t w[4][D / 32];
+    b[t][0] = dev::movmatrix_trans(pack_f16x2(p0 * r0, p1 * r0));
+    b[t][1] = dev::movmatrix_trans(pack_f16x2(p2 * r1, p3 * r1));
+  }
+  uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+  if (KIND == PKV_Q8_E4M3 && nvalid < 32) {  // rows past the range may hold NaN codes
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int key = key_of<D>(2 * tig + (k & 1) + 8 * (k >> 1));
-      const int row = 32 * warp + 16 * t + key;
-      if constexpr (D == 128)
-        lds(w[k], vb + chunk_off<D>(row, gid));
-      else
-        lds(w[k], vb + chunk_off<D>(row, gid >> 1) + 8u * (gid & 1));
-      const uint32_t keep = key < nv ? 0xffffffffu : 0u;
+    for (int t = 0; t < 2; ++t) {
+      keep[t] = 0u;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) w[k][i] = q8::prep<KIND>(KIND == PKV_Q8_E4M3 ? w[k][i] & keep : w[k][i]);
+      for (int k = 0; k < 4; ++k)
+        if (16 * t + key_of(2 * tig + (k & 1) + 8 * (k >> 1)) < nvalid) keep[t] |= 0xffu << (8 * k);
     }
+  }
 #pragma unroll
-    for (int mt = 0; mt < KS; ++mt) {
-      const uint32_t sel = mt & 1 ? 0x7362 : 0x5140;  // bytes (key, key', key, key') of dims 2mt, 2mt + 1
-      const uint32_t lo = __byte_perm(w[0][mt / 2], w[1][mt / 2], sel);
-      const uint32_t hi = __byte_perm(w[2][mt / 2], w[3][mt / 2], sel);
-      mma_f16_16816(a.o[mt], q8::pair<KIND, 0>(lo), q8::pair<KIND, 1>(lo), q8::pair<KIND, 0>(hi),
-                    q8::pair<KIND, 1>(hi), b0, b1);
+  for (int mt = 0; mt < D / 16; ++mt) {
+    uint32_t v[4];
+    ldsm_b8_trans(v, (sb + at.v) ^ (16u * mt));
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (KIND == PKV_Q8_E4M3) {
+        v[2 * t] &= keep[t];
+        v[2 * t + 1] &= keep[t];
+      }
+      const uint32_t y = q8::prep<KIND>(v[2 * t]), z = q8::prep<KIND>(v[2 * t + 1]);
+      mma_f16(a.o[mt], q8::pair<KIND, 0>(y), q8::pair<KIND, 0>(z), q8::pair<KIND, 1>(y), q8::pair<KIND, 1>(z),
+              b[t][0], b[t][1]);
     }
   }
 }
@@ -299,106 +425,148 @@ __device__ __forceinline__ void q8_stash(Q8Acc<D> &a, const MergeArea &r, int G,
     r.l[warp * kMaxGroup + h1] = l1;
   }
 #pragma unroll
-  for (int mt = 0; mt < D / 16; ++mt) {
-    const int d = (D / 8) * gid + 2 * mt;
-    if (h0 < G)
-      *reinterpret_cast<float2 *>(r.o + (warp * G + h0) * D + d) =
-          make_float2(a.o[mt][0] * a.vref, a.o[mt][2] * a.vref);
-    if (h1 < G)
-      *reinterpret_cast<float2 *>(r.o + (warp * G + h1) * D + d) =
-          make_float2(a.o[mt][1] * a.vref, a.o[mt][3] * a.vref);
-  }
+  for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int h = h0 + (k & 1);
+      if (h < G) r.o[(warp * G + h) * q8_row(D) + 16 * mt + gid + 8 * (k >> 1)] = a.o[mt][k] * a.vref;
+    }
 }
 
-// One head's partial results -- rows row_of(0 .. n-1): normalised output and base-2 log-sum --
-// merged into bf16.  One warp; as merge_rows, but for where the rows are.
+// Four dims of one head from the four warps' results: the normalised output and the base-2
+// log-sum (of weights 2^kTop at the reference, in every partial alike).
 template <int D>
-__device__ __forceinline__ void q8_merge_head(uint16_t *dst, const Q8Args &a, int cta0, int n, int h, int lane) {
-  constexpr int VPL = D / 32;
-  float M = -INFINITY, den = 0.f, acc[VPL];
+__device__ __forceinline__ float4 q8_joined(const MergeArea &r, int G, int h, int d, float *lse) {
+  float m[kConsumerWarps], M = -INFINITY;
 #pragma unroll
-  for (int v = 0; v < VPL; ++v) acc[v] = 0.f;
-  for (int k0 = 0; k0 < n; k0 += 8) {
-    float lk[8], ov[8][VPL];
+  for (int w = 0; w < kConsumerWarps; ++w) M = fmaxf(M, m[w] = r.m[w * kMaxGroup + h]);
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  float den = 0.f;
+#pragma unroll
+  for (int w = 0; w < kConsumerWarps; ++w) {
+    const float wt = dev::ex2(m[w] - softmax_ref(M));
+    const float4 o = *reinterpret_cast<const float4 *>(r.o + (w * G + h) * q8_row(D) + d);
+    x.x += wt * o.x;
+    x.y += wt * o.y;
+    x.z += wt * o.z;
+    x.w += wt * o.w;
+    den += wt * r.l[w * kMaxGroup + h];
+  }
+  *lse = M + log2f(den);
+  const float inv = den == 0.f ? 1.f : 1.f / den;
+  return make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+}
+
+__device__ __forceinline__ void store4(uint16_t *dst, const float4 &x) {
+  *reinterpret_cast<uint2 *>(dst) = make_uint2(dev::pack_bf16x2(x.x, x.y), dev::pack_bf16x2(x.z, x.w));
+}
+
+// Four dims of one head from the n shares that cut a context, in the order of the keys: those of
+// `sub`, sub + every, ... are this lane's, the others its neighbours'.
+template <int D>
+__device__ __forceinline__ void q8_merge(uint16_t *dst, const Q8Args &a, int share0, int n, int h, int d, int sub,
+                                         int every) {
+  float M = -INFINITY, den = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = sub; k0 < n; k0 += 8 * every) {
+    float lk[8];
+    float4 o[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const int k = k0 + u;
+      const int k = k0 + u * every;
       lk[u] = -INFINITY;
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) ov[u][v] = 0.f;
+      o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (k < n) {
-        const int64_t row = (int64_t)(k == 0 ? 2 * cta0 + 1 : 2 * (cta0 + k)) * a.group + h;
+        const int64_t row = (int64_t)(k == 0 ? 2 * share0 + 1 : 2 * (share0 + k)) * a.group + h;
         lk[u] = __ldcg(a.lse_part + row);
-        const float *src = a.o_part + row * D + lane * VPL;
-        if constexpr (VPL == 2) {
-          const float2 t2 = __ldcg(reinterpret_cast<const float2 *>(src));
-          ov[u][0] = t2.x;
-          ov[u][1] = t2.y;
-        } else {
-          const float4 t4 = __ldcg(reinterpret_cast<const float4 *>(src));
-          ov[u][0] = t4.x;
-          ov[u][1] = t4.y;
-          ov[u][2] = t4.z;
-          ov[u][3] = t4.w;
-        }
+        o[u] = __ldcg(reinterpret_cast<const float4 *>(a.o_part + row * D + d));
       }
     }
-    float mb = lk[0];
+    float Mn = M;
 #pragma unroll
-    for (int u = 1; u < 8; ++u) mb = fmaxf(mb, lk[u]);
-    const float Mn = fmaxf(M, mb), ref = softmax_ref(Mn);
-    const float sc = dev::ex2(M - ref);
+    for (int u = 0; u < 8; ++u) Mn = fmaxf(Mn, lk[u]);
+    const float ref = softmax_ref(Mn), sc = dev::ex2(M - ref);
     den *= sc;
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) acc[v] *= sc;
+    x.x *= sc;
+    x.y *= sc;
+    x.z *= sc;
+    x.w *= sc;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const float wt = dev::ex2(lk[u] - ref);
       den += wt;
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) acc[v] += wt * ov[u][v];
+      x.x += wt * o[u].x;
+      x.y += wt * o[u].y;
+      x.z += wt * o[u].z;
+      x.w += wt * o[u].w;
     }
     M = Mn;
   }
-  const float inv = den == 0.f ? 0.f : 1.f / den;
-  uint16_t *d = dst + lane * VPL;
-  if constexpr (VPL == 2)
-    *reinterpret_cast<uint32_t *>(d) = dev::pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  else
-    *reinterpret_cast<uint2 *>(d) = make_uint2(dev::pack_bf16x2(acc[0] * inv, acc[1] * inv),
-                                              dev::pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  for (int e = 1; e < every; e <<= 1) {  // `every` neighbouring lanes (a power of two)
+    const float M2 = __shfl_xor_sync(0xffffffffu, M, e), Mn = fmaxf(M, M2);
+    const float s1 = dev::ex2(M - softmax_ref(Mn)), s2 = dev::ex2(M2 - softmax_ref(Mn));
+    den = s1 * den + s2 * __shfl_xor_sync(0xffffffffu, den, e);
+    x.x = s1 * x.x + s2 * __shfl_xor_sync(0xffffffffu, x.x, e);
+    x.y = s1 * x.y + s2 * __shfl_xor_sync(0xffffffffu, x.y, e);
+    x.z = s1 * x.z + s2 * __shfl_xor_sync(0xffffffffu, x.z, e);
+    x.w = s1 * x.w + s2 * __shfl_xor_sync(0xffffffffu, x.w, e);
+    M = Mn;
+  }
+  const float inv = den == 0.f ? 1.f : 1.f / den;
+  if (sub == 0) store4(dst, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
 }
 
-// The end of a share, on the consumer warps after q8_stash (cf. finish_partition).
+// A barrier of one group's consumer warps.
+__device__ __forceinline__ void group_bar(int group) {
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kConsumers) : "memory");
+}
+
+// The end of a share's part of a context, whose four results lie in r (cf. finish_partition).
 template <int D>
-__device__ __forceinline__ void q8_finish(const Q8Args &a, const MergeArea &r, const Q8Desc &d, int tid, int warp,
-                                          int lane, volatile int *s_flag, volatile int *s_last) {
+__device__ __forceinline__ void q8_finish(const Q8Args &a, const MergeArea &r, const Q8Desc &d, int grp, int tid,
+                                          volatile int *s_flag, volatile int *s_last) {
+  constexpr int T = kConsumers;
+  const int items = a.group * (D / 4);  // four dims of a head
   const int64_t head0 = (int64_t)d.b * a.num_q_heads + d.g * a.group;
-  for (int i = tid; i < a.group * D; i += kConsumers) {
-    const int h = i / D, c = i - h * D;
-    float M2, den;
-    const float val = cta_merge<D>(r, a.group, h, c, &M2, &den);
+  for (int i = tid; i < items; i += T) {
+    const int h = i / (D / 4), c = 4 * (i - h * (D / 4));
+    float lse;
+    const float4 x = q8_joined<D>(r, a.group, h, c, &lse);
     if (d.slot < 0) {
-      a.out[head0 * D + i] = to_bf16(val);
+      store4(a.out + (head0 + h) * D + c, x);
     } else {
       const int64_t row = (int64_t)d.slot * a.group + h;
-      a.o_part[row * D + c] = val;
-      if (c == 0) a.lse_part[row] = M2 + log2f(den);
+      *reinterpret_cast<float4 *>(a.o_part + row * D + c) = x;
+      if (c == 0) a.lse_part[row] = lse;
     }
   }
   if (d.slot < 0) return;
-  consumer_bar();
+  group_bar(grp);
   if (tid == 0) {
     int last = 0;
-    if (!*s_flag) last = dev::atomic_add_acq_rel(a.counters + d.cta0, 1u) + 1 == (unsigned)d.parts;
+    if (!*s_flag) last = dev::atomic_add_acq_rel(a.counters + d.share0, 1u) + 1 == (unsigned)d.parts;
     *s_last = last;
   }
-  consumer_bar();
-  if (*s_last) {
-    for (int h = warp; h < a.group; h += kConsumerWarps)
-      q8_merge_head<D>(a.out + (head0 + h) * D, a, d.cta0, d.parts, h, lane);
-    if (tid == 0) a.counters[d.cta0] = 0u;  // ready for the next call
+  group_bar(grp);
+  if (!*s_last) return;  // (written again behind the next end's barriers)
+  int every = 1;  // lanes per item
+  while (every < 32 && 2 * every * items <= T && 8 * every < d.parts) every <<= 1;
+  for (int i0 = 0; i0 < items; i0 += T / every) {  // uniform over the warp: q8_merge shuffles
+    const int i = min(i0 + tid / every, items - 1);  // (the last item may be merged twice, alike)
+    const int h = i / (D / 4), c = 4 * (i - h * (D / 4));
+    q8_merge<D>(a.out + (head0 + h) * D + c, a, d.share0, d.parts, h, c, tid & (every - 1), every);
   }
+  if (tid == 0) a.counters[d.share0] = 0u;  // ready for the next call
+}
+
+// The two pools' boxes at row y, by one copy: the map's third dimension leads from one pool to the other.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int32_t y, uint32_t bar,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(0), "r"(bar), "l"(policy)
+      : "memory");
 }
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const float *src) {
@@ -410,45 +578,81 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 }
 
 template <int D, int KIND>
-__global__ void __launch_bounds__(kThreads, q8_occupancy(D))
-    decode_q8_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+__global__ void __launch_bounds__(q8_threads(D), 1)
+    decode_q8_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1,
                      const __grid_constant__ Q8Args a) {
   using SL = Q8Smem<D>;
-  constexpr int STAGES = SL::kStages;
+  constexpr int STAGES = SL::kStages, GROUPS = q8_groups(D), WARPS = q8_threads(D) / 32;
+  constexpr int kFirstProducer = GROUPS * kConsumerWarps;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = dev::smem_addr(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t *const base_ptr = smem_raw + (base - raw);
-  const uint32_t bar_full = base + SL::bars, bar_empty = bar_full + STAGES * 8;
+  const uint32_t cta_base = (raw + 1023u) & ~1023u;
+  uint8_t *const cta_ptr = smem_raw + (cta_base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool producer = warp >= kFirstProducer;
+  const int grp = producer ? warp - kFirstProducer : warp / kConsumerWarps;
+  const uint32_t base = cta_base + grp * SL::kGroup;
+  uint8_t *const base_ptr = cta_ptr + grp * SL::kGroup;
+  const uint32_t bar_full = base + SL::bars, bar_empty = bar_full + STAGES * 8, bar_step = cta_base + SL::step;
   volatile int *const s_flag = reinterpret_cast<volatile int *>(base_ptr + SL::misc);
   volatile int *const s_last = s_flag + 1;
   volatile int *const s_issued = s_flag + 2;
-  volatile int *const s_b = s_flag + 3;
-  volatile int64_t *const s_base = reinterpret_cast<volatile int64_t *>(base_ptr + SL::misc + 16);
-  volatile int64_t *const s_sums = reinterpret_cast<volatile int64_t *>(base_ptr + SL::sums);
   Q8Desc *const s_desc = reinterpret_cast<Q8Desc *>(base_ptr + SL::desc);
+  int64_t *const s_sums = reinterpret_cast<int64_t *>(cta_ptr + SL::sums);
+  int64_t *const s_incl = reinterpret_cast<int64_t *>(cta_ptr + SL::incl);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int Hkv = a.num_kv_heads;
   const int cap = (int)min((int64_t)a.max_blocks * a.block_size, (int64_t)a.max_len);
   auto length = [&](int b) { return min(max(__ldg(a.lens + b), 0), cap); };
   auto chunks_of = [](int L) { return (int)(((int64_t)L + kQ8Keys - 1) / kQ8Keys); };
+  auto shares_of = [&](int64_t w) {
+    return min((int64_t)gridDim.x * GROUPS, max((int64_t)1, (w + kQ8MinChunks - 1) / kQ8MinChunks));
+  };
+  // Shares 0 .. gridDim.x - 1 are the CTAs' first groups', so that a few lie on SMs of their own.
+  const int share = grp * (int)gridDim.x + (int)blockIdx.x;
+  // Entries of the block table, one a lane.
+  auto entries = [&](int seq, int at) {
+    return seq < a.num_seqs && at + lane < a.max_blocks ? __ldg(a.tables + (int64_t)seq * a.max_blocks + at + lane) : 0;
+  };
 
-  // ---- this CTA's share of the list: the prefix of the sequences' chunks, a run of sequences
-  // per thread
-  const int run = (a.num_seqs + kThreads - 1) / kThreads;
-  const int b_lo = min(tid * run, a.num_seqs), b_hi = min(b_lo + run, a.num_seqs);
-  int64_t mine = 0;
+  // The table window of where this share would begin if all contexts had max_len keys: for equal
+  // lengths its load is under way before the lengths are known.
+  int guess_b = -1, guess_win = 0, guess_tb = 0;
+  if (producer) {
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm0)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm1)) : "memory");
+    }
+    const int64_t n = chunks_of(cap), all = n * Hkv * a.num_seqs, shares = shares_of(all);
+    if (share < shares && all > 0) {
+      const int64_t at = all * share / shares;
+      guess_b = (int)(at / (n * Hkv));
+      guess_win = (int)(at % n) * kQ8Keys >> a.log2_bs;
+      guess_tb = entries(guess_b, guess_win);
+    }
+  }
+
+  // ---- the list: the prefix of the sequences' chunks, a run of sequences per thread
+  const int run = (a.num_seqs + WARPS * 32 - 1) / (WARPS * 32);
+  const int b_lo = min((int)threadIdx.x * run, a.num_seqs), b_hi = min(b_lo + run, a.num_seqs);
+  int64_t incl = 0;
   for (int b = b_lo; b < b_hi; ++b) {
     const int L0 = __ldg(a.lens + b), L = min(max(L0, 0), cap);
     if (L != L0 && blockIdx.x == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
-    mine += chunks_of(L);
+    incl += chunks_of(L);
     if (L == 0 && b % (int)gridDim.x == (int)blockIdx.x) {  // empty context: zero output
       uint2 *o = reinterpret_cast<uint2 *>(a.out + (int64_t)b * a.num_q_heads * D);
       for (int i = 0; i < a.num_q_heads * D / 4; ++i) o[i] = make_uint2(0u, 0u);
     }
   }
-  if (tid == 0) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_sums[warp] = incl;
+  s_incl[threadIdx.x] = incl;
+  if (producer && lane == 0) {
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) {
       dev::mbar_init(bar_full + 8 * s, 33);  // lane 0's bytes, and every producer lane's scales
@@ -458,51 +662,71 @@ __global__ void __launch_bounds__(kThreads, q8_occupancy(D))
     *s_issued = 0;
     dev::fence_mbar_init();
   }
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) s_sums[warp] = incl;
   __syncthreads();
-  int64_t before = incl - mine, total = 0;
+  int64_t total = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += s_sums[w];
-    total += s_sums[w];
-  }
-  const int64_t W = total * Hkv;
-  const int64_t N = min((int64_t)gridDim.x, max((int64_t)1, (W + kQ8MinChunks - 1) / kQ8MinChunks));
-  if ((int64_t)blockIdx.x >= N || W == 0) return;
-  const int64_t lo = W * blockIdx.x / N, hi = W * (blockIdx.x + 1) / N;
-  if (before * Hkv <= lo && lo < (before + mine) * Hkv) {  // one thread
-    int b = b_lo;
-    int64_t at = before;
-    for (;; ++b) {
-      const int n = chunks_of(length(b));
-      if (lo < (at + n) * Hkv) break;
-      at += n;
-    }
-    *s_b = b;
-    *s_base = at * Hkv;
+  for (int w = 0; w < WARPS; ++w) total += s_sums[w];
+  const int64_t W = total * Hkv, N = shares_of(W);
+  const int active = W == 0 ? 0 : (int)min((int64_t)GROUPS, max((N - 1 - (int64_t)blockIdx.x) / gridDim.x + 1, (int64_t)0));
+  if ((int64_t)blockIdx.x >= N || active == 0) return;  // the whole CTA
+  if (threadIdx.x == 0) {
+    dev::mbar_init(bar_step, active);
+    dev::fence_mbar_init();
   }
   __syncthreads();
+  if (grp >= active) return;  // (no barrier of the whole CTA follows)
+  const int64_t lo = W * share / N, hi = W * (share + 1) / N;
   const int n_chunks = (int)(hi - lo);
+  auto timeout = [&] {
+    if (lane == 0) {
+      raise_error(PKV_DEVERR_TIMEOUT);
+      *s_flag = 1;
+    }
+  };
 
-  if (warp == kConsumerWarps) {
-    // ------------------------------------------------------------- producer warp
+  if (producer) {
     const uint64_t policy = dev::policy_evict_first();
     const int rb = a.box_rows;
     const uint32_t box_bytes = (uint32_t)(rb * D);
     const uint32_t q_bytes = (uint32_t)a.group * D * 2u;
-    int b = *s_b;
-    int64_t seq0 = *s_base;  // where the sequence begins in the list
-    int L = length(b), nch = chunks_of(L);
+    // ---- place lo of the list: the thread whose run of sequences holds it, then the sequence
+    int b, at_lane, n;
+    int64_t at = 0;  // chunks before
+    {
+      int w = 0;
+      while (w + 1 < WARPS && (at + s_sums[w]) * Hkv <= lo) at += s_sums[w++];
+      const unsigned past = __ballot_sync(0xffffffffu, (at + s_incl[32 * w + lane]) * Hkv > lo);
+      const int r = past ? __ffs(past) - 1 : 31;
+      if (r > 0) at += s_incl[32 * w + r - 1];
+      for (b = (32 * w + r) * run;; b += 32) {
+        n = b + lane < a.num_seqs ? chunks_of(length(b + lane)) : 0;
+        int64_t inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, (at + inc) * Hkv > lo);
+        if (hit || b + 32 >= a.num_seqs) {
+          at_lane = hit ? __ffs(hit) - 1 : 0;
+          at += __shfl_sync(0xffffffffu, inc - n, at_lane);
+          break;
+        }
+        at += __shfl_sync(0xffffffffu, inc, 31);
+      }
+      b += at_lane;
+    }
+    int L = length(b), nch = max(__shfl_sync(0xffffffffu, n, at_lane), 1);
+    int64_t seq0 = at * Hkv;  // where the sequence begins in the list
     int g = (int)((lo - seq0) / nch), c = (int)((lo - seq0) - (int64_t)g * nch);
-    const int32_t *trow = a.tables + (int64_t)b * a.max_blocks;
-    int win = -1, tb = 0;  // lanes hold the table's entries [win, win + 32)
+    // Table entries are loaded ahead of their use: the current window of 32, the one after it, the
+    // sequence's first, and the next sequence's length and first window.
+    int win = (c * kQ8Keys) >> a.log2_bs;
+    int tb = b == guess_b && win == guess_win ? guess_tb : entries(b, win);
+    int tb_next = entries(b, win + 32), tb_first = win == 0 ? tb : entries(b, 0);
+    int len_seq = b + 1 < a.num_seqs ? length(b + 1) : 0, tb_seq = entries(b + 1, 0);
     Q8Desc dsc;
+    dsc.pad = 0;
     bool first = true;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the step's write is done
     int i = 0;
@@ -512,38 +736,45 @@ __global__ void __launch_bounds__(kThreads, q8_occupancy(D))
         const int64_t u0 = seq0 + (int64_t)g * nch, u1 = u0 + nch;
         dsc.b = b;
         dsc.g = g;
-        dsc.len = L;
         dsc.slot = -1;
-        dsc.cta0 = (int)blockIdx.x;
+        dsc.share0 = share;
         dsc.parts = 1;
-        if (u0 < lo || u1 > hi) {  // shared: place x is CTA floor(((x + 1) N - 1) / W)'s
-          dsc.cta0 = (int)(((u0 + 1) * N - 1) / W);
-          dsc.parts = (int)((u1 * N - 1) / W) - dsc.cta0 + 1;
-          dsc.slot = 2 * (int)blockIdx.x + (dsc.cta0 == (int)blockIdx.x ? 1 : 0);
+        if (u0 < lo || u1 > hi) {  // cut: place x is in share floor(((x + 1) N - 1) / W)
+          dsc.share0 = (int)(((u0 + 1) * N - 1) / W);
+          dsc.parts = (int)((u1 * N - 1) / W) - dsc.share0 + 1;
+          dsc.slot = 2 * share + (dsc.share0 == share ? 1 : 0);
         }
       }
+      // In step: all of the CTA's producers have issued the chunk before.  (Shares differ by one
+      // chunk at most, so that none waits for one that has no more.)
+      if (i > 0 && active > 1 && !__all_sync(0xffffffffu, wait_long(bar_step, (i - 1) & 1))) {
+        timeout();
+        break;
+      }
       if (i >= STAGES &&
-          !__all_sync(0xffffffffu, dev::mbar_wait(bar_empty + 8 * s, ((i / STAGES) - 1) & 1))) {
-        if (lane == 0) {
-          raise_error(PKV_DEVERR_TIMEOUT);
-          *s_flag = 1;
-        }
+          !__all_sync(0xffffffffu, wait_long(bar_empty + 8 * s, ((i / STAGES) - 1) & 1))) {
+        timeout();
         break;
       }
       const int k0 = c * kQ8Keys;
       const int nk = min(kQ8Keys, L - k0);
       const int nbox = (nk + rb - 1) >> a.log2_box;
-      const int lb_hi = (k0 + (nbox - 1) * rb) >> a.log2_bs;
-      if (win < 0 || (k0 >> a.log2_bs) < win || lb_hi >= win + 32) {
-        win = k0 >> a.log2_bs;
-        tb = win + lane <= ((L - 1) >> a.log2_bs) ? __ldg(trow + win + lane) : 0;
+      if ((k0 >> a.log2_bs) >= win + 32) {  // (a chunk's pages lie in one window)
+        win += 32;
+        tb = tb_next;
+        tb_next = entries(b, win + 32);
       }
       const int key = k0 + lane * rb;
-      const int64_t phys_raw = __shfl_sync(0xffffffffu, tb, min(max((key >> a.log2_bs) - win, 0), 31));
+      int64_t phys = __shfl_sync(0xffffffffu, tb, min((key >> a.log2_bs) - win, 31));
+      if (phys < 0 || phys >= a.num_blocks) {
+        if (lane < nbox) raise_error(PKV_DEVERR_BLOCK_ID);
+        phys = 0;
+      }
+      const int64_t unit = phys * Hkv + g;
+      const int32_t row = (int32_t)((unit * a.block_size + (key & (a.block_size - 1))) * D / 128);
       if (lane == 0) {
-        dsc.key0 = k0;
-        dsc.first = first ? 1 : 0;
-        dsc.last = c + 1 == nch || i + 1 == n_chunks ? 1 : 0;
+        dsc.nkeys = nk;
+        dsc.flags = (first ? kBegins : 0) | (c + 1 == nch || i + 1 == n_chunks ? kEnds : 0);
         s_desc[s] = dsc;
         dev::mbar_arrive_expect_tx(bar_full + 8 * s, 2u * nbox * box_bytes + (first ? q_bytes : 0u));
         if (first)
@@ -552,22 +783,20 @@ __global__ void __launch_bounds__(kThreads, q8_occupancy(D))
       }
       __syncwarp();
       if (lane < nbox) {
-        int64_t phys = phys_raw;
-        if (phys < 0 || phys >= a.num_blocks) {
-          raise_error(PKV_DEVERR_BLOCK_ID);
-          phys = 0;
+        const uint32_t dst = base + s * SL::kStage + lane * 2 * box_bytes;
+        if (a.depth) {
+          tma_load_3d(dst, &tm0, row, bar_full + 8 * s, policy);
+        } else {
+          dev::tma_load_2d(dst, &tm0, 0, row, bar_full + 8 * s, policy);
+          dev::tma_load_2d(dst + box_bytes, &tm1, 0, row, bar_full + 8 * s, policy);
         }
-        const int64_t unit = phys * Hkv + g;
-        const int32_t row = (int32_t)(unit * a.block_size + (key & (a.block_size - 1)));
-        const uint32_t dk = base + s * SL::kStage + lane * box_bytes;
-        dev::tma_load_2d(dk, &tmk, 0, row, bar_full + 8 * s, policy);
-        dev::tma_load_2d(dk + SL::kTile, &tmv, 0, row, bar_full + 8 * s, policy);
-        const uint32_t ds = base + SL::scales + s * 128 + lane * 4;
+        const uint32_t ds = base + SL::scales + s * 128 + lane * 8;
         cp_async4(ds, a.k_scale + unit);
-        cp_async4(ds + 64, a.v_scale + unit);
+        cp_async4(ds + 4, a.v_scale + unit);
       }
       cp_async_arrive(bar_full + 8 * s);
       __syncwarp();
+      if (lane == 0 && active > 1) dev::mbar_arrive(bar_step);
       first = false;
       if (++c == nch) {  // the next kv head, or the next sequence that has keys
         c = 0;
@@ -576,59 +805,66 @@ __global__ void __launch_bounds__(kThreads, q8_occupancy(D))
           g = 0;
           seq0 += (int64_t)nch * Hkv;
           do {  // i + 1 < n_chunks: there is one
-            L = length(++b);
+            ++b;
+            L = len_seq;
+            tb_first = tb_seq;
+            len_seq = b + 1 < a.num_seqs ? length(b + 1) : 0;
+            tb_seq = entries(b + 1, 0);
           } while (L == 0 && b + 1 < a.num_seqs);
           nch = chunks_of(L);
-          trow = a.tables + (int64_t)b * a.max_blocks;
-          win = -1;
         }
+        win = 0;
+        tb = tb_first;
+        tb_next = entries(b, 32);
       }
     }
     if (lane == 0) *s_issued = i;
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ----------------------------------------------------------- consumer warps
+    const int wg = warp - grp * kConsumerWarps, tid = (int)threadIdx.x - grp * kConsumers;
+    const Q8Lane at = q8_lane<D>(wg, lane, a.log2_box, a.v_first);
     Q8Acc<D> acc;
     for (int i = 0; i < n_chunks; ++i) {
       const int s = i % STAGES;
-      if (!__all_sync(0xffffffffu, dev::mbar_wait(bar_full + 8 * s, (i / STAGES) & 1))) {
-        if (lane == 0) {
-          raise_error(PKV_DEVERR_TIMEOUT);
-          *s_flag = 1;
-        }
+      if (!__all_sync(0xffffffffu, wait_long(bar_full + 8 * s, (i / STAGES) & 1))) {
+        timeout();
         break;
       }
-      const int key0 = s_desc[s].key0, len = s_desc[s].len;
-      if (s_desc[s].first) load_q<D>(acc, base + SL::q + s * SL::kQ, a.group, lane, a.scale_log2);
-      const uint32_t kb = base + s * SL::kStage;
-      const int nvalid = min(32, len - key0 - 32 * warp);
+      const int2 info = *reinterpret_cast<const int2 *>(s_desc + s);  // keys, flags
+      if (info.y & kBegins) load_q<D, KIND>(acc, base + SL::q + s * SL::kQ, a.group, lane, a.scale_log2);
+      const int nvalid = min(32, info.x - 32 * wg);
       if (nvalid > 0)
-        q8_tiles<D, KIND>(acc, kb, kb + SL::kTile, reinterpret_cast<const float *>(base_ptr + SL::scales + s * 128),
-                          a.log2_box, warp, lane, nvalid);
-      if (s_desc[s].last) {
+        q8_tiles<D, KIND>(acc, base + s * SL::kStage, at,
+                          reinterpret_cast<const float2 *>(base_ptr + SL::scales + s * 128), a.log2_box, wg, lane,
+                          nvalid);
+      if (info.y & kEnds) {
         const Q8Desc d = s_desc[s];
-        consumer_bar();  // every warp is done with this stage's tiles: reuse them to merge
+        group_bar(grp);  // every warp is done with this stage's tiles: the results go there
         MergeArea r;
         r.o = reinterpret_cast<float *>(base_ptr + s * SL::kStage);
-        r.m = r.o + kConsumerWarps * a.group * D;
+        r.m = r.o + kConsumerWarps * a.group * q8_row(D);
         r.l = r.m + kConsumerWarps * kMaxGroup;
-        q8_stash<D>(acc, r, a.group, warp, lane);
-        consumer_bar();
-        q8_finish<D>(a, r, d, tid, warp, lane, s_flag, s_last);
-        dev::fence_proxy_async_smem();  // what was written here, ahead of the next boxes
+        q8_stash<D>(acc, r, a.group, wg, lane);
+        group_bar(grp);
+        q8_finish<D>(a, r, d, grp, tid, s_flag, s_last);
+        dev::fence_proxy_async_smem();  // the results, ahead of the boxes that follow them
       }
       __syncwarp();
       if (lane == 0) dev::mbar_arrive(bar_empty + 8 * s);
     }
-  }
-
-  // ---- a timed-out wait leaves copies possibly in flight: wait for them (bounded)
-  __syncthreads();
-  if (tid == 0 && *s_flag) {
-    const int issued = *s_issued;
-    for (int s = 0; s < STAGES; ++s) {
-      const int last = s + ((issued - 1 - s) / STAGES) * STAGES;  // last chunk on stage s
-      if (last >= 0 && last < issued) (void)dev::mbar_wait(bar_full + 8 * s, (last / STAGES) & 1);
+    // ---- a timed-out wait leaves copies possibly in flight: wait for them (bounded), with what
+    // the producer had issued when the flag was seen
+    group_bar(grp);
+    if (tid == 0 && *s_flag) {
+      const uint64_t t0 = dev::globaltimer_ns();
+      while (*s_issued == 0 && dev::globaltimer_ns() - t0 < 4000000000ull) {
+      }
+      const int issued = *s_issued;
+      for (int s = 0; s < STAGES; ++s) {
+        const int last = s + ((issued - 1 - s) / STAGES) * STAGES;  // last chunk on stage s
+        if (last >= 0 && last < issued) (void)dev::mbar_wait(bar_full + 8 * s, (last / STAGES) & 1);
+      }
     }
   }
 }
@@ -639,12 +875,12 @@ struct Q8Layout {
   size_t o_part, lse_part, total;
 };
 
-// Counters first, at the same place for every call; then the partial rows of as many CTAs as the
-// GPU holds.
+// The words that are zero between calls first, at the same place for every call; then the partial
+// rows of as many shares as the GPU holds groups.
 Q8Layout q8_layout(int group, int d, int sms) {
-  const size_t rows = (size_t)2 * std::min(sms * q8_occupancy(d), kQ8MaxCtas) * group;
+  const size_t rows = (size_t)2 * std::min(sms * q8_groups(d), kQ8MaxShares) * group;
   Q8Layout l;
-  l.o_part = kQ8MaxCtas * sizeof(uint32_t);
+  l.o_part = kQ8MaxShares * sizeof(uint32_t);
   l.lse_part = l.o_part + rows * d * sizeof(float);
   l.total = (l.lse_part + rows * sizeof(float) + 255) & ~size_t(255);
   return l;
@@ -689,15 +925,22 @@ int check_decode_q8(const DecodeQ8 &x, const char *fn) {
 template <int D, int KIND>
 int launch_decode_q8(const DecodeQ8 &x, cudaStream_t stream, bool programmatic) {
   const pkv_cache_desc &c = *x.desc;
-  CUtensorMap tmk, tmv;
+  CUtensorMap tm0, tm1;
   int sms = 0;
   auto *const kern = decode_q8_kernel<D, KIND>;
   const int box = std::min(c.block_size, kQ8Keys);
+  // One map for both pools where they are whole rows apart (half the copies: 16 keys of head_dim 64
+  // took the producer longer to issue than HBM to bring).
+  const void *first = x.cache->k_cache, *second = x.cache->v_cache;
+  const bool v_first = reinterpret_cast<uintptr_t>(second) < reinterpret_cast<uintptr_t>(first);
+  if (v_first) std::swap(first, second);
+  const size_t apart = reinterpret_cast<uintptr_t>(second) - reinterpret_cast<uintptr_t>(first);
+  const bool depth = apart > 0 && apart % 128 == 0 && apart < (size_t(1) << 40);
   {
     std::lock_guard<std::mutex> lk(attn_mutex());
     int dev = 0, rc;
-    if ((rc = current_device(&dev)) || (rc = device_sms(&sms)) || (rc = codes_map(x.cache->k_cache, c, box, &tmk)) ||
-        (rc = codes_map(x.cache->v_cache, c, box, &tmv)))
+    if ((rc = current_device(&dev)) || (rc = device_sms(&sms)) ||
+        (rc = codes_map(first, depth ? apart : 0, c, box, &tm0)) || (rc = codes_map(second, 0, c, box, &tm1)))
       return rc;
     bool *const attr = &g_q8_attr[dev][D == 64 ? 0 : 1][KIND];
     if (!*attr) {
@@ -730,14 +973,16 @@ int launch_decode_q8(const DecodeQ8 &x, cudaStream_t stream, bool programmatic) 
   a.log2_bs = ilog2(c.block_size);
   a.box_rows = box;
   a.log2_box = ilog2(box);
+  a.depth = depth ? 1 : 0;
+  a.v_first = v_first ? 1 : 0;
   a.scale_log2 = x.scale * kLog2e;
-  // one wave; fewer CTAs where the batch cannot have that many shares of kQ8MinChunks
+  // one CTA per SM; fewer where the batch cannot have that many shares of kQ8MinChunks
   const int64_t most = ((int64_t)x.max_len + kQ8Keys - 1) / kQ8Keys * x.num_seqs * c.num_kv_heads;
-  const int64_t wave = std::min(sms * q8_occupancy(D), kQ8MaxCtas);
-  const int64_t grid = std::max<int64_t>(1, std::min(wave, (most + kQ8MinChunks - 1) / kQ8MinChunks));
+  const int64_t ctas = std::min(sms, kQ8MaxShares / q8_groups(D));
+  const int64_t grid = std::max<int64_t>(1, std::min(ctas, (most + kQ8MinChunks - 1) / kQ8MinChunks));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(q8_threads(D), 1, 1);
   cfg.dynamicSmemBytes = q8_smem(D);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -745,7 +990,7 @@ int launch_decode_q8(const DecodeQ8 &x, cudaStream_t stream, bool programmatic) 
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = programmatic ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmk, tmv, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tm0, tm1, a);
   if (e != cudaSuccess) return cuda_error(e, "decode_q8_kernel launch");
   return PKV_OK;
 }

@@ -160,18 +160,18 @@ int query_map(const pkv_bf16 *x, int64_t tokens, int32_t heads, int32_t d, int64
   return PKV_OK;
 }
 
-int codes_map(const void *codes, const pkv_cache_desc &c, int32_t box_rows, CUtensorMap *out) {
+int codes_map(const void *codes, size_t ahead, const pkv_cache_desc &c, int32_t box_rows, CUtensorMap *out) {
   const int rc = get_encoder();
   if (rc) return rc;
-  cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.num_blocks * c.num_kv_heads * c.block_size};
-  cuuint64_t strides[1] = {(cuuint64_t)c.head_dim};
-  cuuint32_t box[2] = {(cuuint32_t)c.head_dim, (cuuint32_t)box_rows};
-  cuuint32_t es[2] = {1, 1};
+  const cuuint64_t bytes = (cuuint64_t)c.num_blocks * c.num_kv_heads * c.block_size * c.head_dim;
+  cuuint64_t dims[3] = {128, bytes / 128, 2};
+  cuuint64_t strides[2] = {128, (cuuint64_t)ahead};
+  cuuint32_t box[3] = {128, (cuuint32_t)(box_rows * c.head_dim / 128), 2};
+  cuuint32_t es[3] = {1, 1, 1};
   const CUresult r =
-      g_encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(codes), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE,
-               c.head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+      g_encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, ahead ? 3 : 2, const_cast<void *>(codes), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return set_error(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return PKV_OK;
 }

@@ -158,9 +158,10 @@ struct WriteQ8 {
 };
 int check_write_q8(const WriteQ8 &w, const char *fn);
 int launch_write_q8(const WriteQ8 &w, cudaStream_t stream);
-// Encodes the TMA map of a pool of 8-bit codes, rows of d bytes: box {d, box_rows}, 64- or
-// 128-byte swizzle; the caller holds attn_mutex().
-int codes_map(const void *codes, const pkv_cache_desc &c, int32_t box_rows, CUtensorMap *out);
+// Encodes the TMA map of a pool of 8-bit codes as rows of 128 bytes (of two tokens at head_dim 64),
+// boxes of box_rows tokens, 128-byte swizzle; with ahead > 0 a box holds those rows and the ones
+// `ahead` bytes behind them (another pool's); the caller holds attn_mutex().
+int codes_map(const void *codes, size_t ahead, const pkv_cache_desc &c, int32_t box_rows, CUtensorMap *out);
 
 // The shared-prefix half of paged_decode_shared_prefix_attention (pkv_tiles.cu): the
 // partial results of split s of every query row of the groups, in row s of o_part

@@ -3,9 +3,10 @@
 Tolerance: the output's rounding to bf16 is at most 2^-8 of it; a weight's rounding to fp16 at most
 2^-11 of the weight, so 2^-11 of sum p |v|; the scores' fp32 sums (at most 128 exact products and
 a few roundings of 2^-24 each, on scores up to some tens) and the exponential move each weight by
-less than 2^-12.  Together 2^-8 |out| + 2^-10 sum p |v|.  A weight is held times 2^15 (the largest
-weight being 1) and its page's V scale over the largest, in fp16, whose steps below 2^-14 are 2^-24: off
-by 2^-25 there, so by 2^-40 of the largest |v| of the context's codes, for each key.
+less than 2^-12.  Together 2^-8 |out| + 2^-10 sum p |v|.  A small weight has an absolute step
+instead: weights are held in fp16, the largest of them (times its page's V scale over the largest) at
+2^10 or more, and fp16's steps below 2^-14 are 2^-24, so off by 2^-25 2^-10 = 2^-35 of the largest |v|
+of the context's codes, for each key.
 """
 
 import math
@@ -58,9 +59,9 @@ def decode_ref(b, q, scale):
         k, v = (R.values(c, sc, b.tables[s], 0, n, torch.float64) for c, sc in ((b.k, b.ks), (b.v, b.vs)))
         o, m = R.attention(q[s:s + 1], k, v, scale)
         out[s:s + 1], mag[s:s + 1] = o, m
-        if n:  # 2^-10 of this is n 2^-40 of the largest |v| that the head's scales can hold
+        if n:  # 2^-10 of this is n 2^-35 of the largest |v| that the head's scales can hold
             top = b.vs[b.tables[s][:-(-n // b.bs)]].nan_to_num().amax(0).double() * R.TOP[b.dtype]
-            mag[s] += n * 2.0 ** -30 * top.repeat_interleave(q.shape[1] // b.hkv)[:, None]
+            mag[s] += n * 2.0 ** -25 * top.repeat_interleave(q.shape[1] // b.hkv)[:, None]
     return out, mag
 
 
