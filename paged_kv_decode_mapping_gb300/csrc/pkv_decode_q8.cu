@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
   if (producer) {
     if (lane == 0) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm0)) : "memory");
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm1)) : "memory");
+      if (!a.depth) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm1)) : "memory");
     }
     const int64_t n = chunks_of(cap), all = n * Hkv * a.num_seqs, shares = shares_of(all);
     if (share < shares && all > 0) {
@@ -925,7 +925,7 @@ int check_decode_q8(const DecodeQ8 &x, const char *fn) {
 template <int D, int KIND>
 int launch_decode_q8(const DecodeQ8 &x, cudaStream_t stream, bool programmatic) {
   const pkv_cache_desc &c = *x.desc;
-  CUtensorMap tm0, tm1;
+  CUtensorMap tm0, tm1 = {};
   int sms = 0;
   auto *const kern = decode_q8_kernel<D, KIND>;
   const int box = std::min(c.block_size, kQ8Keys);
@@ -940,7 +940,8 @@ int launch_decode_q8(const DecodeQ8 &x, cudaStream_t stream, bool programmatic) 
     std::lock_guard<std::mutex> lk(attn_mutex());
     int dev = 0, rc;
     if ((rc = current_device(&dev)) || (rc = device_sms(&sms)) ||
-        (rc = codes_map(first, depth ? apart : 0, c, box, &tm0)) || (rc = codes_map(second, 0, c, box, &tm1)))
+        (rc = codes_map(first, depth ? apart : 0, c, box, &tm0)) ||
+        (!depth && (rc = codes_map(second, 0, c, box, &tm1))))
       return rc;
     bool *const attr = &g_q8_attr[dev][D == 64 ? 0 : 1][KIND];
     if (!*attr) {

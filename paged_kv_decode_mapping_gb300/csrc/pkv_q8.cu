@@ -19,7 +19,8 @@ namespace pkv {
 namespace {
 
 constexpr int kQ8Threads = 256;
-constexpr int kQ8Unroll = 8;  // 16-byte vectors of new rows a thread keeps in registers
+constexpr int kQ8Unroll = 8;    // 16-byte vectors of new rows a thread keeps in registers
+constexpr int kReadUnroll = 8;  // loads a thread has in flight, reading back
 
 // What names the tokens of a call: sequence b's newest n of context_lens[b], its rows in the
 // packed tensors from row0 on.
@@ -120,8 +121,7 @@ struct WriteArgs {
   float *k_scale, *v_scale;     // [num_blocks][num_kv_heads]
   int32_t pages;                // touched pages of a sequence, at most
   int32_t log2_group;
-  int64_t items;                // groups
-  int64_t item_ctas;            // CTAs of them; the ones behind rotate q
+  uint32_t item_ctas;           // CTAs of a sequence's K (or V) groups; the ones behind rotate q
   Rope rope;
   const uint4 *q;
   uint4 *q_out;
@@ -130,19 +130,17 @@ struct WriteArgs {
 };
 
 __device__ __forceinline__ uint32_t absmax(uint32_t m, const uint4 &x) {
-  m = __vmaxu2(m, x.x & 0x7fff7fffu);
-  m = __vmaxu2(m, x.y & 0x7fff7fffu);
-  m = __vmaxu2(m, x.z & 0x7fff7fffu);
-  return __vmaxu2(m, x.w & 0x7fff7fffu);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)  // magnitudes compared (the sign is left over), NaN on top
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[k]));
+  return m;
 }
 
 // The q rows of one sequence: a thread owns a rotation's whole unit (both partner vectors), so
 // that q_out may be q.
 template <int D>
-__device__ __forceinline__ void rotate_q(const WriteArgs &a, int64_t cta) {
-  const int b = (int)(cta / a.q_ctas), part = (int)(cta - (int64_t)b * a.q_ctas);
-  bool bad;
-  const Tokens t = tokens_of(a.s, b, &bad);
+__device__ __forceinline__ void rotate_q(const WriteArgs &a, const Tokens &t, uint32_t part) {
   const int half = a.rope.neox ? a.rope.r / 16 : 0;
   const int units = D / 8 - half;  // of a row
   const int64_t n = (int64_t)(t.end - t.begin) * a.num_q_heads * units;
@@ -168,29 +166,34 @@ __device__ __forceinline__ void rotate_q(const WriteArgs &a, int64_t cta) {
 }
 
 template <int D, int KIND, bool ROPE>
-__global__ void __launch_bounds__(kQ8Threads) write_q8_kernel(const __grid_constant__ WriteArgs a) {
+__global__ void __launch_bounds__(kQ8Threads, ROPE ? 2 : 4) write_q8_kernel(const __grid_constant__ WriteArgs a) {
   constexpr int V = D / 8;  // vectors of a row: 8 bf16 in, 8 codes out
   // A decode kernel behind this one may start its set-up (paged_decode_step_q8).
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int b = blockIdx.z;
+  const bool is_v = blockIdx.y;
+  bool bad;
+  const Tokens t = tokens_of(a.s, b, &bad);
   if constexpr (ROPE) {
-    if ((int64_t)blockIdx.x >= a.item_ctas) {
-      rotate_q<D>(a, blockIdx.x - a.item_ctas);
+    if (blockIdx.x >= a.item_ctas) {
+      if (!is_v) rotate_q<D>(a, t, blockIdx.x - a.item_ctas);
       return;
     }
   }
   __shared__ uint32_t s_max[kQ8Threads / 32];
   const int tid = threadIdx.x, group = 1 << a.log2_group, gt = tid & (group - 1);
-  const int64_t item = (int64_t)blockIdx.x * (kQ8Threads >> a.log2_group) + (tid >> a.log2_group);
-  bool live = item < a.items;
-  uint32_t i = live ? (uint32_t)item : 0u;
-  const int h = (int)(i % (uint32_t)a.s.num_kv_heads);
-  i /= (uint32_t)a.s.num_kv_heads;
-  const bool is_v = i & 1u;
-  i >>= 1;
-  const int b = (int)(i / (uint32_t)a.pages), j = (int)(i - (uint32_t)b * a.pages);
-  bool bad;
-  const Tokens t = tokens_of(a.s, b, &bad);
-  if (live && bad && gt == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
+  const uint32_t item = blockIdx.x * (kQ8Threads >> a.log2_group) + (tid >> a.log2_group);
+  const int j = (int)(item / (uint32_t)a.s.num_kv_heads), h = (int)(item - (uint32_t)j * a.s.num_kv_heads);
+  bool live = j < a.pages;
+  if (bad) {
+    if (live && gt == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
+    return;  // (the whole CTA, as below)
+  }
+  {  // the CTA's first group is the one of the earliest page
+    const int64_t earliest = (t.begin >> a.s.log2_bs) +
+                             (blockIdx.x * (kQ8Threads >> a.log2_group)) / (uint32_t)a.s.num_kv_heads;
+    if (t.begin == t.end || earliest << a.s.log2_bs >= t.end) return;
+  }
   const int page = (t.begin >> a.s.log2_bs) + j;
   const int64_t lo = (int64_t)page << a.s.log2_bs;  // the page's first position
   const int r0 = max(t.begin - (int)min(lo, (int64_t)t.end), 0);
@@ -207,15 +210,17 @@ __global__ void __launch_bounds__(kQ8Threads) write_q8_kernel(const __grid_const
   uint8_t *const rows = (is_v ? a.v_cache : a.k_cache) + unit * a.s.block_size * D;
   const float old = live && r0 > 0 ? *scale : 0.f;  // a page that begins here has none
 
+  // A thread's vectors are one column of every (group / V)-th row.
   const int64_t row0 = t.row0 + (lo + r0 - t.begin), stride = is_v ? a.v_stride : a.k_stride;
-  const uint4 *const src = (is_v ? a.v : a.k) + row0 * stride + h * V;
-  const int count = live ? (r1 - r0) * V : 0;
-  auto fetch = [&](int e, bool *skip) -> uint4 {
-    const int r = e / V, c = e % V;
-    const uint4 *const row = src + r * stride;
+  const int c = gt % V, rows_apart = group / V, first = gt / V, count = live ? r1 - r0 : 0;
+  const uint4 *const src = (is_v ? a.v : a.k) + (row0 + first) * stride + h * V;
+  const int64_t apart = rows_apart * stride;
+  auto fetch = [&](int u, bool *skip) -> uint4 {  // of row first + u * rows_apart
+    const uint4 *const row = src + u * apart;
     *skip = false;
     if constexpr (ROPE) {
       if (!is_v) {
+        const int r = first + u * rows_apart;
         const int64_t pos = a.rope.positions ? __ldg(a.rope.positions + row0 + r) : lo + r0 + r;
         if (pos < 0 || pos >= a.rope.max_position) {
           raise_error(PKV_DEVERR_POSITION);
@@ -228,21 +233,21 @@ __global__ void __launch_bounds__(kQ8Threads) write_q8_kernel(const __grid_const
     return __ldg(row + c);
   };
   uint4 x[kQ8Unroll];
-  bool skip[kQ8Unroll];
-  uint32_t m = 0;
+  uint32_t m = 0, skip = 0;
 #pragma unroll
   for (int u = 0; u < kQ8Unroll; ++u) {
-    const int e = gt + u * group;
-    skip[u] = true;
     x[u] = make_uint4(0, 0, 0, 0);
-    if (e < count) x[u] = fetch(e, &skip[u]);
+    bool none = true;
+    if (first + u * rows_apart < count) x[u] = fetch(u, &none);
+    if (ROPE && none) skip |= 1u << u;
   }
 #pragma unroll
   for (int u = 0; u < kQ8Unroll; ++u) m = absmax(m, x[u]);
-  for (int e = gt + kQ8Unroll * group; e < count; e += group) {
+  for (int u = kQ8Unroll; first + u * rows_apart < count; ++u) {
     bool none;
-    m = absmax(m, fetch(e, &none));
+    m = absmax(m, fetch(u, &none));
   }
+  m &= 0x7fff7fffu;
   m = max(m & 0xffffu, m >> 16);  // bf16 patterns order as whole numbers, infinity and NaN on top
   m = __reduce_max_sync(0xffffffffu, m);
   if (group > 32) {  // uniform over the grid
@@ -261,21 +266,15 @@ __global__ void __launch_bounds__(kQ8Threads) write_q8_kernel(const __grid_const
     to = fmaxf(old, fmaxf(__fdiv_rn(__uint_as_float(m << 16), kTop), 1.17549435e-38f));
   }
   if (gt == 0 && !(to == old && r0 > 0)) *scale = to;
-  const float by = to > 0.f ? to : (to == 0.f ? 1.f : to);
-  auto store = [&](int e, const uint4 &v) {
-    const uint32_t lo4 = q8::encode4<KIND>(__fdiv_rn(dev::bf16lo_to_f32(v.x), by), __fdiv_rn(dev::bf16hi_to_f32(v.x), by),
-                                           __fdiv_rn(dev::bf16lo_to_f32(v.y), by), __fdiv_rn(dev::bf16hi_to_f32(v.y), by));
-    const uint32_t hi4 = q8::encode4<KIND>(__fdiv_rn(dev::bf16lo_to_f32(v.z), by), __fdiv_rn(dev::bf16hi_to_f32(v.z), by),
-                                           __fdiv_rn(dev::bf16lo_to_f32(v.w), by), __fdiv_rn(dev::bf16hi_to_f32(v.w), by));
-    *reinterpret_cast<uint2 *>(rows + (int64_t)r0 * D + (int64_t)e * 8) = make_uint2(lo4, hi4);
-  };
+  const q8::Inverse by = q8::inverse_of(to == 0.f ? 1.f : to);
+  uint2 *const dst = reinterpret_cast<uint2 *>(rows + (int64_t)(r0 + first) * D) + c;
 #pragma unroll
   for (int u = 0; u < kQ8Unroll; ++u)
-    if (!skip[u]) store(gt + u * group, x[u]);
-  for (int e = gt + kQ8Unroll * group; e < count; e += group) {
+    if (ROPE ? !(skip >> u & 1u) : first + u * rows_apart < count) dst[u * rows_apart * V] = q8::encode8<KIND>(x[u], by);
+  for (int u = kQ8Unroll; first + u * rows_apart < count; ++u) {
     bool none;
-    const uint4 v = fetch(e, &none);
-    if (!none) store(e, v);
+    const uint4 v = fetch(u, &none);
+    if (!none) dst[u * rows_apart * V] = q8::encode8<KIND>(v, by);
   }
   if (to > old && r0 > 0) {  // the rows held before, in units of the new scale
     for (int e = gt; e < r0 * (D / 16); e += group) {
@@ -306,22 +305,18 @@ struct ReadArgs {
   int32_t *out_tables;         // pages: the whole contexts as pages of a pool of their own, page j
   int32_t out_blocks;          //   of sequence b at b * out_blocks + j, and its table; else NULL
   int32_t pages, log2_group;
-  int64_t items;
 };
 
 template <int D, int KIND>
 __global__ void __launch_bounds__(kQ8Threads) read_q8_kernel(const __grid_constant__ ReadArgs a) {
-  constexpr int V = D / 16;  // vectors of a row: 16 codes in, 2 x 8 bf16 out
+  constexpr int V = D / 8;  // vectors of a row: 8 codes in, 8 bf16 out
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, group = 1 << a.log2_group, gt = tid & (group - 1);
-  const int64_t item = (int64_t)blockIdx.x * (kQ8Threads >> a.log2_group) + (tid >> a.log2_group);
-  if (item >= a.items) return;
-  uint32_t i = (uint32_t)item;
-  const int h = (int)(i % (uint32_t)a.s.num_kv_heads);
-  i /= (uint32_t)a.s.num_kv_heads;
-  const bool is_v = i & 1u;
-  i >>= 1;
-  const int b = (int)(i / (uint32_t)a.pages), j = (int)(i - (uint32_t)b * a.pages);
+  const int b = blockIdx.z;
+  const bool is_v = blockIdx.y;
+  const uint32_t item = blockIdx.x * (kQ8Threads >> a.log2_group) + (tid >> a.log2_group);
+  const int j = (int)(item / (uint32_t)a.s.num_kv_heads), h = (int)(item - (uint32_t)j * a.s.num_kv_heads);
+  if (j >= a.pages) return;
   Tokens t;
   if (a.out_tables) {  // lengths past the tables are cut, as the attention does
     int L = __ldg(a.s.lens + b);
@@ -349,8 +344,9 @@ __global__ void __launch_bounds__(kQ8Threads) read_q8_kernel(const __grid_consta
   }
   const int64_t unit = from * a.s.num_kv_heads + h;
   const float scale = __ldg((is_v ? a.v_scale : a.k_scale) + unit);
-  const uint4 *const src =
-      reinterpret_cast<const uint4 *>((is_v ? a.v_cache : a.k_cache) + unit * a.s.block_size * D) + r0 * V;
+  const uint64_t scale2 = q8::f32x2(scale, scale);
+  const uint2 *src =
+      reinterpret_cast<const uint2 *>((is_v ? a.v_cache : a.k_cache) + unit * a.s.block_size * D) + r0 * V;
   uint4 *dst = is_v ? a.v_out : a.k_out;
   int64_t stride;
   if (a.out_tables) {
@@ -360,29 +356,35 @@ __global__ void __launch_bounds__(kQ8Threads) read_q8_kernel(const __grid_consta
     stride = is_v ? a.v_stride : a.k_stride;
     dst += (t.row0 + (lo + r0 - t.begin)) * stride + h * (D / 8);
   }
-  const int count = (r1 - r0) * V;
-  for (int e0 = gt; e0 < count; e0 += 4 * group) {
-    uint4 x[4];
+  // A thread's vectors are one column of every (group / V)-th row.
+  const int rows_apart = group / V, first = gt / V, count = r1 - r0;
+  src += first * V + gt % V;
+  dst += first * stride + gt % V;
+  const int src_step = rows_apart * V;
+  const int64_t dst_step = rows_apart * stride;
+  for (int r = first; r < count; r += kReadUnroll * rows_apart) {
+    uint2 x[kReadUnroll];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (e0 + u * group < count) x[u] = __ldcs(src + e0 + u * group);
+    for (int u = 0; u < kReadUnroll; ++u)
+      if (r + u * rows_apart < count) x[u] = __ldcs(src + u * src_step);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int e = e0 + u * group;
-      if (e >= count) break;
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      uint32_t o[8];
+    for (int u = 0; u < kReadUnroll; ++u) {
+      if (r + u * rows_apart >= count) break;
+      const uint32_t w[2] = {x[u].x, x[u].y};
+      uint32_t o[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 2; ++k) {
         const uint32_t z = q8::prep<KIND>(w[k]);
         const float2 f = q8::f16x2_to_f32(q8::pair<KIND, 0>(z)), g = q8::f16x2_to_f32(q8::pair<KIND, 1>(z));
-        o[2 * k] = dev::pack_bf16x2(__fmul_rn(f.x, scale), __fmul_rn(f.y, scale));
-        o[2 * k + 1] = dev::pack_bf16x2(__fmul_rn(g.x, scale), __fmul_rn(g.y, scale));
+        const float2 p = q8::split(q8::mul2(q8::f32x2(f.x, f.y), scale2));
+        const float2 q = q8::split(q8::mul2(q8::f32x2(g.x, g.y), scale2));
+        o[2 * k] = dev::pack_bf16x2(p.x, p.y);
+        o[2 * k + 1] = dev::pack_bf16x2(q.x, q.y);
       }
-      uint4 *const p = dst + (e / V) * stride + 2 * (e % V);
-      p[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      *dst = make_uint4(o[0], o[1], o[2], o[3]);
+      dst += dst_step;
     }
+    src += kReadUnroll * src_step;
   }
 }
 
@@ -460,10 +462,9 @@ int launch_read(const Span &s, const pkv_q8_cache &q, const pkv_cache_desc &c, p
   a.out_tables = out_tables;
   a.out_blocks = out_blocks;
   a.pages = (int32_t)pages;
-  a.items = pages * s.num_seqs * 2 * c.num_kv_heads;
-  a.log2_group = log2_group_of((int64_t)std::min(s.block_size, s.max_new) * c.head_dim / 16, 4);
+  a.log2_group = log2_group_of((int64_t)std::min(s.block_size, s.max_new) * c.head_dim / 8, kReadUnroll);
   const int per = kQ8Threads >> a.log2_group;
-  const unsigned ctas = (unsigned)((a.items + per - 1) / per);
+  const dim3 ctas((unsigned)((pages * c.num_kv_heads + per - 1) / per), 2, (unsigned)s.num_seqs);
   const bool i8 = q.kind == PKV_Q8_INT8;
   auto *const kern = c.head_dim == 64 ? (i8 ? read_q8_kernel<64, PKV_Q8_INT8> : read_q8_kernel<64, PKV_Q8_E4M3>)
                                       : (i8 ? read_q8_kernel<128, PKV_Q8_INT8> : read_q8_kernel<128, PKV_Q8_E4M3>);
@@ -535,11 +536,10 @@ int launch_write_q8(const WriteQ8 &w, cudaStream_t stream) {
   a.k_scale = w.cache->k_scale;
   a.v_scale = w.cache->v_scale;
   a.pages = (int32_t)std::min<int64_t>(touched(w.max_query_len, c.block_size), w.max_blocks);
-  a.items = (int64_t)a.pages * w.num_seqs * 2 * c.num_kv_heads;
   a.log2_group = log2_group_of((int64_t)std::min(c.block_size, w.max_query_len) * c.head_dim / 8, kQ8Unroll);
   const int per = kQ8Threads >> a.log2_group;
-  a.item_ctas = (a.items + per - 1) / per;
-  int64_t ctas = a.item_ctas;
+  a.item_ctas = (uint32_t)(((int64_t)a.pages * c.num_kv_heads + per - 1) / per);
+  uint32_t ctas = a.item_ctas;
   if (w.rope) {
     a.rope.cos_sin = w.cos_sin;
     a.rope.positions = w.positions;
@@ -554,10 +554,9 @@ int launch_write_q8(const WriteQ8 &w, cudaStream_t stream) {
       a.num_q_heads = w.num_q_heads;
       const int64_t vecs = (int64_t)w.max_query_len * w.num_q_heads * (c.head_dim / 8);
       a.q_ctas = (int32_t)std::min<int64_t>((vecs + 4 * kQ8Threads - 1) / (4 * kQ8Threads), 16384);
-      ctas += (int64_t)a.q_ctas * w.num_seqs;
+      ctas += (uint32_t)a.q_ctas;
     }
   }
-  if (ctas > 0x7fffffffLL) return set_error(PKV_ERR_UNSUPPORTED, "paged_kv_write_q8: too many tokens");
   const bool i8 = w.cache->kind == PKV_Q8_INT8;
   void (*kern)(const WriteArgs) = nullptr;
   if (w.rope)
@@ -568,7 +567,7 @@ int launch_write_q8(const WriteQ8 &w, cudaStream_t stream) {
     kern = c.head_dim == 64
                ? (i8 ? write_q8_kernel<64, PKV_Q8_INT8, false> : write_q8_kernel<64, PKV_Q8_E4M3, false>)
                : (i8 ? write_q8_kernel<128, PKV_Q8_INT8, false> : write_q8_kernel<128, PKV_Q8_E4M3, false>);
-  kern<<<(unsigned)ctas, kQ8Threads, 0, stream>>>(a);
+  kern<<<dim3(ctas, 2, (unsigned)w.num_seqs), kQ8Threads, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_error(e, "write_q8_kernel launch");
   return PKV_OK;

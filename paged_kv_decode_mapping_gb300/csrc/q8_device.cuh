@@ -56,5 +56,73 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
   }
 }
 
+// Two products rounded once each (a packed instruction), and with an addend.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split(uint64_t x) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(x));
+  return f;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// The codes of x / s for bf16 x, as fp32 division gives them, mostly without one.  x times either
+// bound of 1 / s brackets the quotient (below 2^-21 of it apart either way, its own rounding
+// included); where both round to one code, that is its code, since rounding is monotone.  Only
+// quotients next to a border between two codes are divided.  (Eight divisions a vector were most
+// of the write's 57 million instructions: 34000 tokens of 8 heads of 128 took 69 us.)
+struct Inverse {
+  float s;
+  uint64_t lo, hi;  // twice each
+};
+__device__ __forceinline__ Inverse inverse_of(float s) {
+  const float inv = __fdiv_rn(1.f, s);
+  // (an infinite one, of a scale that is no normal number, leaves every quotient to the division)
+  const float lo = isinf(inv) ? 0.f : inv * (1.f - 4.76837158e-7f), hi = inv * (1.f + 4.76837158e-7f);
+  return {s, f32x2(lo, lo), f32x2(hi, hi)};
+}
+template <int KIND>
+__device__ __forceinline__ uint2 encode8(const uint4 &v, const Inverse &s) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[4], differ[4];  // two codes each
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint64_t x = f32x2(dev::bf16lo_to_f32(w[k]), dev::bf16hi_to_f32(w[k]));
+    if constexpr (KIND == PKV_Q8_INT8) {
+      // 2^23 + 2^22 + x / s, whose last bits are the rounded whole number (of at most 127)
+      const uint64_t magic = f32x2(12582912.f, 12582912.f);
+      const float2 a = split(fma2(x, s.lo, magic)), b = split(fma2(x, s.hi, magic));
+      differ[k] = (__float_as_uint(a.x) ^ __float_as_uint(b.x)) | (__float_as_uint(a.y) ^ __float_as_uint(b.y));
+      c[k] = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);  // low bytes
+    } else {
+      const float2 a = split(mul2(x, s.lo)), b = split(mul2(x, s.hi));
+      uint16_t p, q;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(a.y), "f"(a.x));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(b.y), "f"(b.x));
+      c[k] = p;
+      differ[k] = (uint32_t)(p ^ q);
+    }
+  }
+  if (differ[0] | differ[1] | differ[2] | differ[3]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (differ[k])
+        c[k] = encode4<KIND>(__fdiv_rn(dev::bf16lo_to_f32(w[k]), s.s), __fdiv_rn(dev::bf16hi_to_f32(w[k]), s.s), 0.f, 0.f);
+  }
+  return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+}
+
 }  // namespace q8
 }  // namespace pkv
