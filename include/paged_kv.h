@@ -569,18 +569,25 @@ int paged_decode_step_rope_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t q_stride
                               size_t workspace_bytes, void *stream);
 
 /*
- * paged_prefill_attention_q8 -- paged_prefill_attention over an 8-bit cache: the contexts are
- * read back as bf16 pages into the workspace (paged_prefill_q8_workspace_size() bytes, no initial
- * values), and the prefill kernel runs over those.  Sizes and rules of paged_prefill_attention.
+ * paged_prefill_attention_q8 -- paged_prefill_attention over an 8-bit cache: q and out are
+ * [num_queries][num_q_heads][head_dim], sequence b's newest tokens at rows query_start[b] ..
+ * query_start[b+1]-1.  The contexts are read back as fp16 rows into the workspace
+ * (paged_prefill_q8_workspace_size() bytes, no initial values; not for two calls that overlap),
+ * scores and weights are fp16 products with fp32 sums as in paged_decode_attention_q8.
+ * max_query_len and max_context_len bound every length; longer ones, and sequences of more queries
+ * than tokens, raise PKV_DEVERR_CONTEXT_LEN (they are cut; a query before the first token gives
+ * zeros).  Rows of no sequence are not written.  A page of scale NaN (see paged_kv_write_q8) may make
+ * queries NaN from fewer than 128 + 128 / (num_q_heads / num_kv_heads) tokens before it on.
  */
 size_t paged_prefill_q8_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim,
-                                       int32_t block_size, int32_t max_context_len);
-int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, const pkv_q8_cache *cache,
-                               const int32_t *block_tables, int32_t max_blocks_per_seq,
-                               const int32_t *context_lens, int32_t max_context_len,
-                               const int32_t *query_start, int32_t max_query_len, int32_t num_seqs,
-                               int32_t num_q_heads, const pkv_cache_desc *desc, float scale,
-                               void *workspace, size_t workspace_bytes, void *stream);
+                                       int32_t max_context_len);
+int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t num_queries,
+                               const pkv_q8_cache *cache, const int32_t *block_tables,
+                               int32_t max_blocks_per_seq, const int32_t *context_lens,
+                               int32_t max_context_len, const int32_t *query_start,
+                               int32_t max_query_len, int32_t num_seqs, int32_t num_q_heads,
+                               const pkv_cache_desc *desc, float scale, void *workspace,
+                               size_t workspace_bytes, void *stream);
 
 /*
  * paged_decode_split -- flash-decoding partition kernel (split-K over the keys;

@@ -114,9 +114,9 @@ _lib.paged_decode_step_q8.restype = ctypes.c_int
 _lib.paged_decode_step_rope_q8.argtypes = [_P, _P, _i64, _P, _P, _P, _i64, _i64, _P, _P, _i64, _i32, _i32,
                                            _Q8, _P, _i32, _P, _i32, _i32, _i32, _D, _f32, _P, _sz, _P]
 _lib.paged_decode_step_rope_q8.restype = ctypes.c_int
-_lib.paged_prefill_q8_workspace_size.argtypes = [_i32] * 5
+_lib.paged_prefill_q8_workspace_size.argtypes = [_i32] * 4
 _lib.paged_prefill_q8_workspace_size.restype = _sz
-_lib.paged_prefill_attention_q8.argtypes = [_P, _P, _Q8, _P, _i32, _P, _i32, _P, _i32, _i32, _i32, _D, _f32,
+_lib.paged_prefill_attention_q8.argtypes = [_P, _P, _i64, _Q8, _P, _i32, _P, _i32, _P, _i32, _i32, _i32, _D, _f32,
                                             _P, _sz, _P]
 _lib.paged_prefill_attention_q8.restype = ctypes.c_int
 _lib.paged_decode_split.argtypes = [_P, _P, _P, _P, _P, _P, _i32, _P, _i32, _i32, _i32, _D, _f32,
@@ -834,7 +834,8 @@ def paged_decode_q8_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads
 
 def paged_prefill_q8_workspace_size(num_seqs: int, num_kv_heads: int, head_dim: int, block_size: int,
                                     max_context_len: int) -> int:
-    return int(_lib.paged_prefill_q8_workspace_size(num_seqs, num_kv_heads, head_dim, block_size, max_context_len))
+    """(By tokens: the block size makes no difference.)"""
+    return int(_lib.paged_prefill_q8_workspace_size(num_seqs, num_kv_heads, head_dim, max_context_len))
 
 
 def _q8_query(out, q, k_cache, rows: Optional[int], dev: int) -> None:
@@ -947,7 +948,7 @@ def paged_prefill_attention_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torc
     workspace = _q8_workspace(workspace, 0 if workspace is not None else paged_prefill_q8_workspace_size(
         B, d.num_kv_heads, d.head_dim, d.block_size, int(max_context_len)), False, q, dev, stream)
     _check(_lib.paged_prefill_attention_q8(
-        out.data_ptr(), q.data_ptr(), ctypes.byref(c), block_tables.data_ptr(), M, context_lens.data_ptr(),
+        out.data_ptr(), q.data_ptr(), q.shape[0], ctypes.byref(c), block_tables.data_ptr(), M, context_lens.data_ptr(),
         int(max_context_len), query_start.data_ptr(), int(max_query_len), B, q.shape[1], ctypes.byref(d),
         float(scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream, dev)),
         "paged_prefill_attention_q8")

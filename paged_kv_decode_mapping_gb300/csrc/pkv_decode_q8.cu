@@ -128,11 +128,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // mbar_wait for waits that are mostly long: the thread may sleep up to 20 us at a time, so that
 // waiting warps take no issue slots from the working ones.  The same 2 s limit.
 __device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity) {
@@ -221,7 +216,7 @@ __device__ __forceinline__ void load_q(Q8Acc<D> &a, uint32_t qs, int group, int 
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) {
     const float lo = dev::bf16lo_to_f32(w[i]) * up, hi = dev::bf16hi_to_f32(w[i]) * up;
-    w[i] = pack_f16x2(lo, hi);
+    w[i] = q8::pack_f16x2(lo, hi);
     sum += lo + hi;
   }
   float begin = 0.f;
@@ -377,8 +372,8 @@ __device__ __forceinline__ void q8_tiles(Q8Acc<D> &a, uint32_t sb, const Q8Lane 
     const float p0 = dev::ex2(x[t][0]), p1 = dev::ex2(x[t][1]), p2 = dev::ex2(x[t][2]), p3 = dev::ex2(x[t][3]);
     a.l0 += p0 + p2;
     a.l1 += p1 + p3;
-    b[t][0] = dev::movmatrix_trans(pack_f16x2(p0 * r0, p1 * r0));
-    b[t][1] = dev::movmatrix_trans(pack_f16x2(p2 * r1, p3 * r1));
+    b[t][0] = dev::movmatrix_trans(q8::pack_f16x2(p0 * r0, p1 * r0));
+    b[t][1] = dev::movmatrix_trans(q8::pack_f16x2(p2 * r1, p3 * r1));
   }
   uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
   if (KIND == PKV_Q8_E4M3 && nvalid < 32) {  // rows past the range may hold NaN codes

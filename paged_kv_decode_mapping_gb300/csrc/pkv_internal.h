@@ -182,6 +182,21 @@ struct PrefixLaunch {
 int launch_prefix(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv_cache_desc &c,
                   const PrefixLaunch &l, cudaStream_t stream);
 
+// Causal attention of each sequence's newest tokens over fp16 rows of its own (pkv_tiles.cu): row
+// seq * kv_rows + t of k and v, [rows][num_kv_heads][head_dim], holds token t's keys and values in
+// units of k_unit and v_unit [num_seqs][num_kv_heads].  Arguments already checked.
+struct ChunkLaunch {
+  pkv_bf16 *out;
+  const pkv_bf16 *q;
+  const uint16_t *k, *v;
+  const float *k_unit, *v_unit;
+  const int32_t *query_start, *context_lens;
+  int64_t num_queries;
+  int32_t max_query_len, max_context, kv_rows, num_seqs, num_q_heads, num_kv_heads, head_dim;
+  float scale;
+};
+int launch_chunk(const ChunkLaunch &l, cudaStream_t stream);
+
 }  // namespace pkv
 
 // ----------------------------------------------------------------------------

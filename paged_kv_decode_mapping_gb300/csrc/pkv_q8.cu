@@ -295,6 +295,9 @@ __global__ void __launch_bounds__(kQ8Threads, ROPE ? 2 : 4) write_q8_kernel(cons
 
 // ---------------------------------------------------------------------------
 // Reading back: bf16(code * scale).  One group of threads per (sequence, page, K or V, kv head).
+// For the prefill, whole contexts as fp16 rows, row seq * out_rows + t being token t's: code *
+// (scale / unit) for the largest scale of the (sequence, kv head) as unit, so that codes keep 11
+// bits (bf16 rows, of 8, doubled the error of the output).
 
 struct ReadArgs {
   Span s;
@@ -302,12 +305,52 @@ struct ReadArgs {
   const float *k_scale, *v_scale;
   uint4 *k_out, *v_out;
   int64_t k_stride, v_stride;  // packed rows: vectors from one token to the next
-  int32_t *out_tables;         // pages: the whole contexts as pages of a pool of their own, page j
-  int32_t out_blocks;          //   of sequence b at b * out_blocks + j, and its table; else NULL
+  int32_t out_rows;            // whole contexts in fp16; 0: bf16 rows of the newest tokens
+  const float *k_unit, *v_unit;
   int32_t pages, log2_group;
 };
 
-template <int D, int KIND>
+// The units: the largest scale of each (sequence, kv head)'s pages.  One CTA per sequence; thread
+// (page % rows, kv head), joined through shared memory.
+struct UnitArgs {
+  Span s;
+  const float *k_scale, *v_scale;
+  float *k_unit, *v_unit;
+};
+__global__ void __launch_bounds__(kQ8Threads) units_q8_kernel(const __grid_constant__ UnitArgs a) {
+  __shared__ float s_k[kQ8Threads], s_v[kQ8Threads];
+  const int b = blockIdx.x, H = a.s.num_kv_heads, tid = threadIdx.x;
+  const int cap = (int)min((int64_t)a.s.max_blocks * a.s.block_size, (int64_t)a.s.max_new);
+  const int L = min(max(__ldg(a.s.lens + b), 0), cap), pages = (L + a.s.block_size - 1) >> a.s.log2_bs;
+  const int32_t *const row = a.s.tables + (int64_t)b * a.s.max_blocks;
+  for (int h0 = 0; h0 < H; h0 += kQ8Threads) {  // (heads past 256 in further rounds)
+    const int wide = min(H - h0, kQ8Threads), rows = kQ8Threads / wide;
+    const int h = tid % wide, r = tid / wide;
+    float k = 0.f, v = 0.f;
+    if (r < rows)
+#pragma unroll 4
+      for (int p = r; p < pages; p += rows) {
+        int64_t phys = __ldg(row + p);
+        if (phys < 0 || phys >= a.s.num_blocks) phys = 0;  // (flagged by the reading)
+        k = fmaxf(k, __ldg(a.k_scale + phys * H + h0 + h));
+        v = fmaxf(v, __ldg(a.v_scale + phys * H + h0 + h));
+      }
+    s_k[tid] = k;
+    s_v[tid] = v;
+    __syncthreads();
+    if (tid < wide) {
+      for (int x = 1; x < rows; ++x) {
+        k = fmaxf(k, s_k[x * wide + tid]);
+        v = fmaxf(v, s_v[x * wide + tid]);
+      }
+      a.k_unit[(int64_t)b * H + h0 + tid] = k;
+      a.v_unit[(int64_t)b * H + h0 + tid] = v;
+    }
+    __syncthreads();
+  }
+}
+
+template <int D, int KIND, bool WHOLE>
 __global__ void __launch_bounds__(kQ8Threads) read_q8_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int V = D / 8;  // vectors of a row: 8 codes in, 8 bf16 out
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -318,14 +361,11 @@ __global__ void __launch_bounds__(kQ8Threads) read_q8_kernel(const __grid_consta
   const int j = (int)(item / (uint32_t)a.s.num_kv_heads), h = (int)(item - (uint32_t)j * a.s.num_kv_heads);
   if (j >= a.pages) return;
   Tokens t;
-  if (a.out_tables) {  // lengths past the tables are cut, as the attention does
-    int L = __ldg(a.s.lens + b);
+  if constexpr (WHOLE) {  // lengths past the tables are cut, as the attention does
     const int cap = (int)min((int64_t)a.s.max_blocks * a.s.block_size, (int64_t)a.s.max_new);
-    if ((L < 0 || L > cap) && gt == 0 && j == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
     t.begin = 0;
-    t.end = min(max(L, 0), cap);
-    t.row0 = 0;
-    if (!is_v && h == 0 && gt == 0) a.out_tables[(int64_t)b * a.out_blocks + j] = b * a.out_blocks + j;
+    t.end = min(max(__ldg(a.s.lens + b), 0), cap);
+    t.row0 = (int64_t)b * a.out_rows;
   } else {
     bool bad;
     t = tokens_of(a.s, b, &bad);
@@ -343,19 +383,16 @@ __global__ void __launch_bounds__(kQ8Threads) read_q8_kernel(const __grid_consta
     from = 0;
   }
   const int64_t unit = from * a.s.num_kv_heads + h;
-  const float scale = __ldg((is_v ? a.v_scale : a.k_scale) + unit);
+  float scale = __ldg((is_v ? a.v_scale : a.k_scale) + unit);
+  if constexpr (WHOLE) {
+    const float of = __ldg((is_v ? a.v_unit : a.k_unit) + (int64_t)b * a.s.num_kv_heads + h);
+    scale = of > 0.f ? __fdiv_rn(scale, of) : scale * 0.f;  // (a NaN stays)
+  }
   const uint64_t scale2 = q8::f32x2(scale, scale);
   const uint2 *src =
       reinterpret_cast<const uint2 *>((is_v ? a.v_cache : a.k_cache) + unit * a.s.block_size * D) + r0 * V;
-  uint4 *dst = is_v ? a.v_out : a.k_out;
-  int64_t stride;
-  if (a.out_tables) {
-    dst += (((int64_t)b * a.out_blocks + j) * a.s.num_kv_heads + h) * a.s.block_size * (D / 8);
-    stride = D / 8;
-  } else {
-    stride = is_v ? a.v_stride : a.k_stride;
-    dst += (t.row0 + (lo + r0 - t.begin)) * stride + h * (D / 8);
-  }
+  const int64_t stride = is_v ? a.v_stride : a.k_stride;
+  uint4 *dst = (is_v ? a.v_out : a.k_out) + (t.row0 + (lo + r0 - t.begin)) * stride + h * V;
   // A thread's vectors are one column of every (group / V)-th row.
   const int rows_apart = group / V, first = gt / V, count = r1 - r0;
   src += first * V + gt % V;
@@ -378,8 +415,8 @@ __global__ void __launch_bounds__(kQ8Threads) read_q8_kernel(const __grid_consta
         const float2 f = q8::f16x2_to_f32(q8::pair<KIND, 0>(z)), g = q8::f16x2_to_f32(q8::pair<KIND, 1>(z));
         const float2 p = q8::split(q8::mul2(q8::f32x2(f.x, f.y), scale2));
         const float2 q = q8::split(q8::mul2(q8::f32x2(g.x, g.y), scale2));
-        o[2 * k] = dev::pack_bf16x2(p.x, p.y);
-        o[2 * k + 1] = dev::pack_bf16x2(q.x, q.y);
+        o[2 * k] = WHOLE ? q8::pack_f16x2(p.x, p.y) : dev::pack_bf16x2(p.x, p.y);
+        o[2 * k + 1] = WHOLE ? q8::pack_f16x2(q.x, q.y) : dev::pack_bf16x2(q.x, q.y);
       }
       *dst = make_uint4(o[0], o[1], o[2], o[3]);
       dst += dst_step;
@@ -446,28 +483,37 @@ int check_span(const void *x, const void *y, int64_t x_stride, int64_t y_stride,
   return PKV_OK;
 }
 
-int launch_read(const Span &s, const pkv_q8_cache &q, const pkv_cache_desc &c, pkv_bf16 *k_out, pkv_bf16 *v_out,
-                int64_t k_stride, int64_t v_stride, int32_t *out_tables, int32_t out_blocks, int64_t pages,
-                cudaStream_t stream) {
+// out_rows > 0: whole contexts in fp16, units at k_unit and v_unit.
+int launch_read(const Span &s, const pkv_q8_cache &q, const pkv_cache_desc &c, void *k_out, void *v_out,
+                int64_t k_stride, int64_t v_stride, int32_t out_rows, const float *k_unit, const float *v_unit,
+                int64_t pages, cudaStream_t stream) {
   ReadArgs a;
   a.s = s;
   a.k_cache = static_cast<const uint8_t *>(q.k_cache);
   a.v_cache = static_cast<const uint8_t *>(q.v_cache);
   a.k_scale = q.k_scale;
   a.v_scale = q.v_scale;
-  a.k_out = reinterpret_cast<uint4 *>(k_out);
-  a.v_out = reinterpret_cast<uint4 *>(v_out);
+  a.k_out = static_cast<uint4 *>(k_out);
+  a.v_out = static_cast<uint4 *>(v_out);
   a.k_stride = k_stride / 8;
   a.v_stride = v_stride / 8;
-  a.out_tables = out_tables;
-  a.out_blocks = out_blocks;
+  a.out_rows = out_rows;
+  a.k_unit = k_unit;
+  a.v_unit = v_unit;
   a.pages = (int32_t)pages;
   a.log2_group = log2_group_of((int64_t)std::min(s.block_size, s.max_new) * c.head_dim / 8, kReadUnroll);
   const int per = kQ8Threads >> a.log2_group;
   const dim3 ctas((unsigned)((pages * c.num_kv_heads + per - 1) / per), 2, (unsigned)s.num_seqs);
   const bool i8 = q.kind == PKV_Q8_INT8;
-  auto *const kern = c.head_dim == 64 ? (i8 ? read_q8_kernel<64, PKV_Q8_INT8> : read_q8_kernel<64, PKV_Q8_E4M3>)
-                                      : (i8 ? read_q8_kernel<128, PKV_Q8_INT8> : read_q8_kernel<128, PKV_Q8_E4M3>);
+  void (*kern)(const ReadArgs);
+  if (out_rows)
+    kern = c.head_dim == 64
+               ? (i8 ? read_q8_kernel<64, PKV_Q8_INT8, true> : read_q8_kernel<64, PKV_Q8_E4M3, true>)
+               : (i8 ? read_q8_kernel<128, PKV_Q8_INT8, true> : read_q8_kernel<128, PKV_Q8_E4M3, true>);
+  else
+    kern = c.head_dim == 64
+               ? (i8 ? read_q8_kernel<64, PKV_Q8_INT8, false> : read_q8_kernel<64, PKV_Q8_E4M3, false>)
+               : (i8 ? read_q8_kernel<128, PKV_Q8_INT8, false> : read_q8_kernel<128, PKV_Q8_E4M3, false>);
   kern<<<ctas, kQ8Threads, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_error(e, "read_q8_kernel launch");
@@ -626,7 +672,7 @@ PKV_API int paged_kv_read_q8(pkv_bf16 *k_out, pkv_bf16 *v_out, int64_t k_stride,
   if (!rc && num_seqs > 0 && num_tokens > 0 && max_query_len > 0) {
     const Span s = span_of(block_tables, max_blocks_per_seq, context_lens, query_start, max_query_len, num_seqs,
                            num_tokens, *desc);
-    rc = launch_read(s, *cache, *desc, k_out, v_out, k_stride, v_stride, nullptr, 0,
+    rc = launch_read(s, *cache, *desc, k_out, v_out, k_stride, v_stride, 0, nullptr, nullptr,
                      std::min<int64_t>(touched(max_query_len, desc->block_size), max_blocks_per_seq),
                      static_cast<cudaStream_t>(stream));
   }
@@ -635,75 +681,103 @@ PKV_API int paged_kv_read_q8(pkv_bf16 *k_out, pkv_bf16 *v_out, int64_t k_stride,
 }
 
 // ---------------------------------------------------------------------------
-// Chunked prefill: the contexts' pages are read back into a bf16 pool in the workspace, and the
-// prefill kernel runs over that.  The tensor-core tiles want K and V in 16 bits in shared memory
-// (the weights of a causal row need more than the 4 bits of an e4m3 operand); a chunk of a few
-// hundred queries spends far more on its products than on the pool's 5 bytes for each code.
+// Chunked prefill: the contexts are read back into fp16 rows in the workspace, and the tensor-core
+// tiles of the packed prompts run over those.  (Widening the codes where the tiles stage them would
+// be done once for every 256 query rows that see them, on the warps that the softmax waits for; the
+// reading back costs 5 bytes of traffic a code once.)
 
 namespace {
 
 struct PrefillLayout {
-  int64_t blocks;  // pages of a sequence
-  size_t k, v, tables, total;
+  int32_t rows;  // packed rows of a sequence
+  size_t k, v, k_unit, v_unit, total;
 };
 
-bool prefill_layout(int32_t num_seqs, int32_t hkv, int32_t d, int32_t bs, int32_t max_len, PrefillLayout *p) {
-  if (num_seqs <= 0 || hkv <= 0 || bs <= 0 || max_len <= 0 || (d != 64 && d != 128)) return false;
+bool prefill_layout(int32_t num_seqs, int32_t hkv, int32_t d, int32_t max_len, PrefillLayout *p) {
+  if (num_seqs <= 0 || hkv <= 0 || max_len <= 0 || (d != 64 && d != 128)) return false;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-  p->blocks = ((int64_t)max_len + bs - 1) / bs;
-  if (p->blocks * num_seqs > 0x7fffffffLL / ((int64_t)hkv * bs)) return false;
-  const size_t pool = up((size_t)p->blocks * num_seqs * hkv * bs * d * 2);
+  if ((int64_t)max_len * num_seqs > 0x7fffff00LL / hkv) return false;
+  p->rows = max_len;
+  const size_t rows = up((size_t)max_len * num_seqs * hkv * d * 2), units = up((size_t)num_seqs * hkv * 4);
   p->k = 0;
-  p->v = pool;
-  p->tables = 2 * pool;
-  p->total = 2 * pool + up((size_t)p->blocks * num_seqs * 4);
+  p->v = rows;
+  p->k_unit = 2 * rows;
+  p->v_unit = p->k_unit + units;
+  p->total = p->v_unit + units;
   return true;
 }
 
 }  // namespace
 
 PKV_API size_t paged_prefill_q8_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim,
-                                               int32_t block_size, int32_t max_context_len) {
+                                               int32_t max_context_len) {
   PrefillLayout p;
-  return prefill_layout(num_seqs, num_kv_heads, head_dim, block_size, max_context_len, &p) ? p.total : 0;
+  return prefill_layout(num_seqs, num_kv_heads, head_dim, max_context_len, &p) ? p.total : 0;
 }
 
-PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, const pkv_q8_cache *cache,
-                                       const int32_t *block_tables, int32_t max_blocks_per_seq,
-                                       const int32_t *context_lens, int32_t max_context_len,
-                                       const int32_t *query_start, int32_t max_query_len, int32_t num_seqs,
-                                       int32_t num_q_heads, const pkv_cache_desc *desc, float scale,
+PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t num_queries,
+                                       const pkv_q8_cache *cache, const int32_t *block_tables,
+                                       int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                       int32_t max_context_len, const int32_t *query_start, int32_t max_query_len,
+                                       int32_t num_seqs, int32_t num_q_heads, const pkv_cache_desc *desc, float scale,
                                        void *workspace, size_t workspace_bytes, void *stream) {
   const char *const fn = "paged_prefill_attention_q8";
   int rc = check_q8(cache, desc, num_seqs, fn);
   if (!rc)
     rc = check_decode(q, cache->k_cache, cache->v_cache, block_tables, max_blocks_per_seq, context_lens,
-                      max_context_len, num_seqs, num_q_heads, desc, fn);
+                      max_context_len, num_queries > 0 ? num_seqs : 0, num_q_heads, desc, fn);
   if (rc) return rc;
-  if (max_query_len < 0 || max_query_len > max_context_len)
-    return set_error(PKV_ERR_SHAPE, "%s: need 0 <= max_query_len <= max_context_len", fn);
-  if (num_seqs == 0 || max_query_len == 0) {
+  if (num_queries < 0 || max_query_len < 0 || max_query_len > max_context_len)
+    return set_error(PKV_ERR_SHAPE, "%s: need num_queries >= 0, 0 <= max_query_len <= max_context_len", fn);
+  if (num_seqs == 0 || max_query_len == 0 || num_queries == 0) {
     clear_error();
     return PKV_OK;
   }
   if (!out || !query_start) return set_error(PKV_ERR_NULL, "%s: NULL out/query_start", fn);
   if (!aligned16(out)) return set_error(PKV_ERR_ALIGN, "%s: out must be 16-byte aligned", fn);
+  if (misaligned4(query_start) || misaligned4(block_tables) || misaligned4(context_lens))
+    return set_error(PKV_ERR_ALIGN, "%s: int32 tensors must be 4-byte aligned", fn);
   PrefillLayout p;
-  if (!prefill_layout(num_seqs, desc->num_kv_heads, desc->head_dim, desc->block_size, max_context_len, &p) ||
-      p.blocks * num_seqs > 0x7fffffffLL / (2 * desc->num_kv_heads))
-    return set_error(PKV_ERR_UNSUPPORTED, "%s: the contexts' pages have more than 2^31-1 rows", fn);
+  if (!prefill_layout(num_seqs, desc->num_kv_heads, desc->head_dim, max_context_len, &p))
+    return set_error(PKV_ERR_UNSUPPORTED, "%s: the contexts have more than 2^31 rows of heads", fn);
   if (!workspace || workspace_bytes < p.total)
     return set_error(PKV_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, workspace_bytes, p.total);
   if (!aligned16(workspace)) return set_error(PKV_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   char *const ws = static_cast<char *>(workspace);
-  pkv_bf16 *const k = reinterpret_cast<pkv_bf16 *>(ws + p.k), *const v = reinterpret_cast<pkv_bf16 *>(ws + p.v);
-  int32_t *const tables = reinterpret_cast<int32_t *>(ws + p.tables);
-  const Span s = span_of(block_tables, max_blocks_per_seq, context_lens, nullptr, max_context_len, num_seqs, 0, *desc);
-  rc = launch_read(s, *cache, *desc, k, v, 0, 0, tables, (int32_t)p.blocks, p.blocks,
-                   static_cast<cudaStream_t>(stream));
+  const Span span = span_of(block_tables, max_blocks_per_seq, context_lens, nullptr, max_context_len, num_seqs, 0, *desc);
+  UnitArgs u;
+  u.s = span;
+  u.k_scale = cache->k_scale;
+  u.v_scale = cache->v_scale;
+  u.k_unit = reinterpret_cast<float *>(ws + p.k_unit);
+  u.v_unit = reinterpret_cast<float *>(ws + p.v_unit);
+  units_q8_kernel<<<(unsigned)num_seqs, kQ8Threads, 0, s>>>(u);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_error(e, "units_q8_kernel launch");
+  const int64_t stride = (int64_t)desc->num_kv_heads * desc->head_dim;
+  rc = launch_read(span, *cache, *desc, ws + p.k, ws + p.v, stride, stride, p.rows, u.k_unit, u.v_unit,
+                   ((int64_t)max_context_len + desc->block_size - 1) / desc->block_size, s);
   if (rc) return rc;
-  pkv_cache_desc pool = *desc;
-  pool.num_blocks = p.blocks * num_seqs;
-  return paged_prefill_attention(out, q, k, v, tables, (int32_t)p.blocks, context_lens, max_context_len,
-                                 query_start, max_query_len, num_seqs, num_q_heads, &pool, scale, stream);
+  ChunkLaunch l;
+  l.out = out;
+  l.q = q;
+  l.k = reinterpret_cast<const uint16_t *>(ws + p.k);
+  l.v = reinterpret_cast<const uint16_t *>(ws + p.v);
+  l.k_unit = u.k_unit;
+  l.v_unit = u.v_unit;
+  l.query_start = query_start;
+  l.context_lens = context_lens;
+  l.num_queries = num_queries;
+  l.max_query_len = max_query_len;
+  l.max_context = (int32_t)std::min<int64_t>((int64_t)max_blocks_per_seq * desc->block_size, max_context_len);
+  l.kv_rows = p.rows;
+  l.num_seqs = num_seqs;
+  l.num_q_heads = num_q_heads;
+  l.num_kv_heads = desc->num_kv_heads;
+  l.head_dim = desc->head_dim;
+  l.scale = scale;
+  rc = launch_chunk(l, s);
+  if (!rc) clear_error();
+  return rc;
 }

@@ -48,7 +48,13 @@ namespace pkv {
 //    them against 1 us to write them all.)  Bound by the copies: a box of 16 rows and 64 dims
 //    takes the TMA unit 63 cycles and its bytes, 1.57 us per block of 128 keys at block_size
 //    16 and head_dim 128, at which 152 CTAs draw 6.3 TB/s (16 sequences over 65536 tokens).
-enum { kPrompt = 0, kPrefix = 1 };
+//  * kNewest: kPrompt for the newest tokens of sequences whose keys lie in packed rows of their own,
+//    kv_rows to a sequence, in fp16 (the rows that an 8-bit cache is read back to): a query sees
+//    `past` more keys than its place.  All operands are fp16: the queries are widened where their
+//    tile was loaded, each row times a power of two; K's and V's rows are in units of a factor of
+//    their (sequence, kv head); weights are taken with 2^7 at the reference.
+enum { kPrompt = 0, kPrefix = 1, kNewest = 2 };
+constexpr float kNewestTop = 7.f;  // weights reach 2^(kNewestTop + kTcRescale): fp16 ends at 65504
 
 struct TileArgs {
   uint16_t *out;            // prompt
@@ -66,6 +72,9 @@ struct TileArgs {
   int32_t split_keys;       // keys per split (a multiple of kTcKeys)
   float *o_part, *lse_part; // [B][Hq][n_rows][D], [B][Hq][n_rows]; row s: the s-th split
   SharedCut cut;
+  // newest tokens (and context_lens)
+  int32_t kv_rows, max_context;    // packed rows of a sequence; the longest context
+  const float *k_unit, *v_unit;    // [num][num_kv_heads]
 };
 
 // 8 softmax warps, the K and the V producer (two warps a ring measured neutral), an MMA warp per
@@ -83,7 +92,7 @@ struct TileItem {
   int32_t key0, t_end;      // keys [key0, t_end) are staged, in blocks of kTcKeys
   int32_t nb0, nb1;         // blocks of each tile
   int32_t prefix;           // kPrefix: the whole pages of the group's prefix
-  int32_t pad[2];
+  int32_t past, seq;        // kNewest: keys before the sequence's first query; its number
 };
 
 template <int D, int MODE>
@@ -92,11 +101,11 @@ struct TileSmem {
   // tile j & 1's): a waiter may trust a barrier's parity only if it saw the phase before,
   // and a tile's MMA thread sees the phases of its own blocks.
   static constexpr int KSK = D == 64 ? 4 : 2;
-  static constexpr int KSV = D == 64 ? 4 : (MODE == kPrompt ? 2 : 4);
-  static_assert(MODE == kPrompt || (KSK % 2 == 0 && KSV % 2 == 0), "one tile per stage");
+  static constexpr int KSV = D == 64 ? 4 : (MODE != kPrefix ? 2 : 4);
+  static_assert(MODE != kPrefix || (KSK % 2 == 0 && KSV % 2 == 0), "one tile per stage");
   static constexpr uint32_t kSub = kTcKeys * 128;     // 128 rows x 128 B (64 dims)
   static constexpr uint32_t kTile = kSub * (D / 64);
-  static constexpr int kQ = MODE == kPrompt ? 2 : 1;  // Q tiles
+  static constexpr int kQ = MODE != kPrefix ? 2 : 1;  // Q tiles
   static constexpr uint32_t k = 0;
   static constexpr uint32_t v = k + KSK * kTile;
   static constexpr uint32_t q = v + KSV * kTile;
@@ -107,18 +116,18 @@ struct TileSmem {
   // kPrompt: 32 dims of each softmax warp's 32 output rows, row r's 16-byte chunk c at
   // c ^ (r / 2 & 3)
   static constexpr uint32_t stage = ones + (kOnes ? kSub : 0);
-  static constexpr uint32_t item = stage + (MODE == kPrompt ? 2 * kTcRows * 64 : 0);  // two items
+  static constexpr uint32_t item = stage + (MODE != kPrefix ? 2 * kTcRows * 64 : 0);  // two items
   static constexpr uint32_t clc = item + 2 * sizeof(TileItem); // a launch-control answer, 16 B
   // kPrefix, once the rings are done with: the tiles' rows [2][128][D] fp32, row r's 16-byte
   // chunk c at c ^ (r & 7), where the rings begin; (max in base 2, sum) per row at their end
   static constexpr uint32_t rows = 0;
   static constexpr uint32_t ml = q - 2 * kTcRows * 8;
   static constexpr uint32_t bars = clc + 16;
-  static_assert(MODE == kPrompt || rows + 2u * kTcRows * D * 4 <= ml, "the rows fit the rings");
+  static_assert(MODE != kPrefix || rows + 2u * kTcRows * D * 4 <= ml, "the rows fit the rings");
   // the rings, then s_full, pv_done per tile, p_half per tile and half, q_full, q_free, o_free
-  // per tile, item_full, item_empty per slot, clc_full, mma_done, tiles_done
+  // per tile, item_full, item_empty per slot, clc_full, mma_done, tiles_done; kNewest: q_wide per tile
   static constexpr int kRings = 2 * KSK + 2 * KSV;
-  static constexpr int kBars = kRings + 21;
+  static constexpr int kBars = kRings + (MODE == kNewest ? 23 : 21);
   static constexpr uint32_t tslot = bars + kBars * 8;
   static constexpr uint32_t flag = tslot + 8;
   static constexpr uint32_t turns = flag + 8;  // P.V batches issued, per tile
@@ -167,7 +176,7 @@ struct TileCursor {
 // where the last one ended (from the beginning, 512 sequences of 84 tokens took 15 us an item).
 __device__ __forceinline__ bool locate_tile(const TileArgs &a, TileCursor &at, int64_t idx, int tokens,
                                             int lane, int &first, int &n, int &tile, int &ntiles,
-                                            int &prefix) {
+                                            int &prefix, int &seq) {
   if (idx < at.before) at = TileCursor();
   while (true) {
     const int64_t total = at.before + __shfl_sync(0xffffffffu, at.upto, 31);
@@ -187,6 +196,7 @@ __device__ __forceinline__ bool locate_tile(const TileArgs &a, TileCursor &at, i
   }
   const int l = __ffs(__ballot_sync(0xffffffffu, at.before + at.upto > idx)) - 1;
   prefix = __shfl_sync(0xffffffffu, at.prefix, l);
+  seq = at.c + l;
   first = __shfl_sync(0xffffffffu, at.s, l);
   n = __shfl_sync(0xffffffffu, at.len, l);
   ntiles = __shfl_sync(0xffffffffu, at.mine, l);
@@ -200,11 +210,22 @@ __device__ __forceinline__ bool make_item(const TileArgs &a, TileCursor &at, uns
                                           int lane, TileItem &it) {
   it.live = 1;
   it.g = (int)(cta_x % (unsigned)a.num_kv_heads);
-  const int tokens = a.tile_tokens * (MODE == kPrompt ? 2 : 1);
+  const int tokens = a.tile_tokens * (MODE != kPrefix ? 2 : 1);
   int tile, ntiles, prefix;
-  if (!locate_tile(a, at, cta_x / (unsigned)a.num_kv_heads, tokens, lane, it.first, it.n, tile, ntiles, prefix))
+  if (!locate_tile(a, at, cta_x / (unsigned)a.num_kv_heads, tokens, lane, it.first, it.n, tile, ntiles, prefix,
+                   it.seq))
     return false;
-  if constexpr (MODE == kPrompt) {
+  if constexpr (MODE == kNewest) {
+    const int L = __ldg(a.context_lens + it.seq), len = min(max(L, 0), a.max_context);
+    if ((len != L || len < it.n) && lane == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
+    it.past = len - it.n;  // (below 0: the first queries see no key, and give zeros)
+    it.tok0 = (ntiles - 1 - tile) * tokens;
+    const int e0 = min(it.tok0 + a.tile_tokens, it.n), e1 = min(it.tok0 + tokens, it.n);
+    it.key0 = 0;
+    it.t_end = max(it.past + e1, 1);
+    it.nb0 = (max(it.past + e0, 1) + kTcKeys - 1) / kTcKeys;
+    it.nb1 = e1 > e0 ? (it.t_end + kTcKeys - 1) / kTcKeys : 0;
+  } else if constexpr (MODE == kPrompt) {
     it.tok0 = (ntiles - 1 - tile) * tokens;  // a sequence's last tiles see the most keys: first
     const int e0 = min(it.tok0 + a.tile_tokens, it.n), e1 = min(it.tok0 + tokens, it.n);
     it.key0 = 0;
@@ -373,11 +394,11 @@ __device__ __forceinline__ void add_f32x2(float &a0, float &a1, float b0, float 
       : "f"(b0), "f"(b1));
 }
 
-// P = exp2(S * scale - m) of the 32 columns x (columns c0 .. of the row) as bf16 pairs, and
+// P = exp2(S * scale - m) of the 32 columns x (columns c0 .. of the row) as bf16 (fp16) pairs, and
 // their sum added to ls: of the weights as they are before the rounding, two to an add (the
 // rounded ones, one to an add, measured 6% slower).  Rounding moves a weight by at most 2^-8
 // of itself, and so the output by at most 2^-8 of sum p |v|.
-template <bool kMask, bool kSum>
+template <bool kMask, bool kSum, bool kHalf>
 __device__ __forceinline__ void chunk_exp(const uint32_t (&x)[32], int c0, int lim, float scale_log2,
                                           float m, uint32_t *pk, float (&ls)[4]) {
 #pragma unroll
@@ -389,7 +410,10 @@ __device__ __forceinline__ void chunk_exp(const uint32_t (&x)[32], int c0, int l
       a1 = c0 + 2 * e + 1 <= lim ? a1 : -INFINITY;
     }
     const float p0 = dev::ex2(a0), p1 = dev::ex2(a1);
-    pk[e] = dev::pack_bf16x2(p0, p1);
+    if constexpr (kHalf)
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[e]) : "f"(p1), "f"(p0));
+    else
+      pk[e] = dev::pack_bf16x2(p0, p1);
     if constexpr (kSum) add_f32x2(ls[2 * (e & 1)], ls[2 * (e & 1) + 1], p0, p1);
   }
 }
@@ -495,6 +519,37 @@ __device__ __noinline__ void prefix_row(const TileArgs &a, int row, int split, i
     a.lse_part[(int64_t)row * a.cut.n_rows + split] = r.l == 0.f ? -INFINITY : (r.m + log2f(r.l)) * kLn2;
 }
 
+// Row r of a query tile [D/64][128][128 B] from bf16 to fp16 in place, times 2^e (returned): for
+// its largest value to be in [2^14, 2^15), as far as 2^e and its inverse are normal numbers.
+template <int D, uint32_t SUB>
+__device__ __forceinline__ int widen_row(uint8_t *tile, int r) {
+  uint32_t m = 0;
+#pragma unroll 1
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 x = *reinterpret_cast<const uint4 *>(tile + (c >> 3) * SUB + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x.x));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x.y));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x.z));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x.w));
+  }
+  m &= 0x7fff7fffu;
+  m = max(m & 0xffffu, m >> 16);
+  const int e = min(max(14 - ((int)(m >> 7) - 127), -126), 126);
+  const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll 1
+  for (int c = 0; c < D / 8; ++c) {
+    uint4 *const p = reinterpret_cast<uint4 *>(tile + (c >> 3) * SUB + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    const uint4 x = *p;
+    auto half2 = [&](uint32_t w) {
+      uint32_t h;
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(dev::bf16hi_to_f32(w) * up), "f"(dev::bf16lo_to_f32(w) * up));
+      return h;
+    };
+    *p = make_uint4(half2(x.x), half2(x.y), half2(x.z), half2(x.w));
+  }
+  return e;
+}
+
 template <int D, int MODE>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
@@ -502,7 +557,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   using SL = TileSmem<D, MODE>;
   constexpr int KSK = SL::KSK, KSV = SL::KSV, kRings = SL::kRings;
   constexpr bool kPaged = MODE == kPrefix;     // keys from pages; partial outputs; one item
-  constexpr bool kShareKeys = MODE == kPrompt; // both tiles take every block
+  constexpr bool kShareKeys = MODE != kPrefix; // both tiles take every block
+  constexpr bool kHalf = MODE == kNewest;       // fp16 operands, scaled (else bf16)
   constexpr bool kOnes = SL::kOnes;
   constexpr int kON = D + (kOnes ? 16 : 0);    // O columns per tile (then the row sums)
   constexpr int kProducer = 8, kProducerV = 9, kMma = 10;  // kMma + t: tile t's MMA warp
@@ -526,6 +582,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t clc_full = bars + 8u * (kRings + 18);
   const uint32_t mma_done = bars + 8u * (kRings + 19);
   const uint32_t tiles_done = bars + 8u * (kRings + 20);
+  [[maybe_unused]] auto q_wide = [&](int t) { return bars + 8u * (kRings + 21 + t); };
   volatile int *const s_turn = reinterpret_cast<volatile int *>(bp + SL::turns);
   volatile uint32_t *const s_tmem = reinterpret_cast<volatile uint32_t *>(bp + SL::tslot);
   volatile int *const s_flag = reinterpret_cast<volatile int *>(bp + SL::flag);
@@ -556,6 +613,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                              : r == 16 || r == 17 ? (uint32_t)kItemReaders
                              : r == 19 ? 2u                   // mma_done: both MMA threads
                              : r == 20 ? 8u                   // tiles_done: every softmax warp
+                             : r == 21 || r == 22 ? 4u        // q_wide: one per softmax warp
                                        : 1u;
       dev::mbar_init(bars + 8u * i, count);
       dev::fence_mbar_init();
@@ -564,11 +622,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       *s_flag = 0;
       s_turn[0] = s_turn[1] = 0;
     }
-    if (kOnes && tid < 256) {  // bf16 1.0 everywhere; read by the tensor core (async proxy)
+    if (kOnes && tid < 256) {  // 1.0 everywhere; read by the tensor core (async proxy)
+      constexpr uint32_t kOne = kHalf ? 0x3C003C00u : 0x3F803F80u;
 #pragma unroll 1
       for (int i = tid; i < (int)(SL::kSub / 16); i += 256)
         *reinterpret_cast<uint4 *>(bp + SL::ones + i * 16) =
-            make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+            make_uint4(kOne, kOne, kOne, kOne);
     }
     // rows of the Q tiles past the last whole token are never loaded: zeros
     if (tid < 256) {
@@ -634,7 +693,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                       min(kTcKeys, x.t_end - x.key0 - j * kTcKeys), win, tb, trow,
                                       lb_last, a, x.g, lane, policy);
       else if (lane == 0)
-        load_packed_block(tm, dst, full, SL::kTile, x.first + j * kTcKeys, x.g, policy);
+        load_packed_block(tm, dst, full, SL::kTile, (MODE == kNewest ? x.seq * a.kv_rows : x.first) + j * kTcKeys, x.g, policy);
     }
     return true;
   };
@@ -660,7 +719,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
     const uint32_t sb = tmem + lane_base + 128u * t;
     const uint32_t ob = tmem + lane_base + 256u + (uint32_t)(kON * t);
-    const float scale_log2 = fabsf(a.scale_log2);
+    float scale_log2 = fabsf(a.scale_log2);
     int blocks = 0, sc = 0, on = 0;  // as in the MMA threads
     bool ok = true;
     for (int items = 0; ok && next_item(items, it); ++items) {
@@ -671,8 +730,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // keys < see are this row's
       int see = it.t_end;
       if (kPaged && valid) see = min(max(__ldg(a.context_lens + token), 0), it.t_end);
-      if (!kPaged) see = min(qi + 1, it.t_end);
+      if (!kPaged) see = min((MODE == kNewest ? it.past : 0) + qi + 1, it.t_end);
       if (kPaged) ends = valid && see > it.key0 && see < it.t_end;
+      [[maybe_unused]] float v_unit = 1.f;
+      if constexpr (MODE == kNewest) {
+        // The row's queries as fp16, times a power of two for the largest to be in [2^14, 2^15).
+        const int64_t unit = (int64_t)it.seq * a.num_kv_heads + it.g;
+        const float k_unit = __ldg(a.k_unit + unit);
+        v_unit = __ldg(a.v_unit + unit);
+        if (nb > 0) {
+          if (!(ok = warp_wait(q_full(t), on & 1))) {
+            if (lane == 0) fail(false);
+            break;
+          }
+          const int e = widen_row<D, SL::kSub>(bp + SL::q + t * SL::kTile, r);
+          scale_log2 = fabsf(a.scale_log2) * k_unit * __uint_as_float((uint32_t)(127 - e) << 23);
+          dev::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) dev::mbar_arrive(q_wide(t));
+        }
+      }
       float m_ref = -INFINITY;
       float ls[4] = {0.f, 0.f, 0.f, 0.f};
       auto rescale_o = [&](float f) {  // O_t (and its row-sum column) and the row sum scale by f
@@ -718,7 +795,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           m_ref = bm;
         }
         // a row that has seen no key yet takes its weights, all masked to 0, against 0
-        const float m = m_ref == -INFINITY ? 0.f : m_ref;
+        const float m = (m_ref == -INFINITY ? 0.f : m_ref) - (kHalf ? kNewestTop : 0.f);
         auto publish_half = [&](int hf) {
           dev::tmem_wait_st();
           dev::tc_fence_before();
@@ -727,13 +804,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         };
         if (masked) {
           // V rows past the prefix are stale, past the sequence another's
-          const int nk = (kPaged ? it.t_end : it.n) - k0;
+          const int nk = (kPaged ? it.t_end : MODE == kNewest ? max(it.past + it.n, 0) : it.n) - k0;
           if (nk < kTcKeys) {
             const int j = blocks + blk(t, i), s = j % KSV;
             if (!(ok = warp_wait(v_full(s), (j / KSV) & 1))) break;
             const uint32_t vt = SL::v + s * SL::kTile;
 #pragma unroll 1
-            for (int idx = r; idx < (kTcKeys - nk) * (D / 8); idx += kTcRows) {
+            for (int idx = r; idx < (kTcKeys - nk) * (D / 8); idx += kTcRows) {  // (nk >= 0: see the item)
               const int row = nk + idx / (D / 8), c = idx % (D / 8);
               *reinterpret_cast<uint4 *>(bp + vt + (c >> 3) * SL::kSub + row * 128 +
                                          (((c & 7) ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
@@ -748,12 +825,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               tmem_wait_ld_regs(xa);
             }
             if (l.lo >= c0 + 31) {
-              chunk_exp<false, !kOnes>(xa, 0, 0, scale_log2, m, pk, ls);
+              chunk_exp<false, !kOnes, kHalf>(xa, 0, 0, scale_log2, m, pk, ls);
             } else if (l.hi < c0) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) pk[e] = 0u;
             } else {
-              chunk_exp<true, !kOnes>(xa, 0, l.lim - c0, scale_log2, m, pk, ls);
+              chunk_exp<true, !kOnes, kHalf>(xa, 0, l.lim - c0, scale_log2, m, pk, ls);
             }
             tmem_st16(sb + c0 / 2, pk);  // over columns this thread has read
             if (c0 & 32) publish_half(c0 >> 6);
@@ -763,10 +840,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int hf = 0; hf < 2; ++hf) {
             uint32_t xb[32], pk[32];
             dev::tmem_ld32(sb + 64 * hf + 32, xb);
-            chunk_exp<false, !kOnes>(xa, 0, 0, scale_log2, m, pk, ls);
+            chunk_exp<false, !kOnes, kHalf>(xa, 0, 0, scale_log2, m, pk, ls);
             tmem_wait_ld_regs(xb);
             if (hf == 0) dev::tmem_ld32(sb + 64, xa);
-            chunk_exp<false, !kOnes>(xb, 0, 0, scale_log2, m, pk + 16, ls);
+            chunk_exp<false, !kOnes, kHalf>(xb, 0, 0, scale_log2, m, pk + 16, ls);
             if (hf == 0) tmem_wait_ld_regs(xa);
             dev::tmem_st32(sb + 32 * hf, pk);  // over columns this thread has read
             publish_half(hf);
@@ -787,7 +864,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!kPaged && nb > 0) {
         // through shared memory, so that 4 lanes write 64 bytes of a row (a row per lane, 16
         // bytes at a time, was a line per lane: 512 sequences of 84 tokens 167 against 124 us)
-        const float inv = 1.f / lsum;
+        const float inv = MODE == kNewest ? (lsum == 0.f ? 0.f : v_unit / lsum) : 1.f / lsum;
         const uint64_t dst = valid ? reinterpret_cast<uint64_t>(
                                          a.out + token * a.out_stride + (int64_t)(it.g * G + h) * D)
                                    : 0;  // the lane's row
@@ -947,10 +1024,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // scores came at the same moment and both softmaxes ran against each other while the
       // tensor core idled (4011 against 3080 cycles per block pair at head_dim 128).
       const int t = warp - kMma;
+      constexpr uint32_t kTypes = kHalf ? 1u << 7 | 1u << 10 : 0u;  // A and B: fp16 is 0, bf16 1
       // a negative scale negates the queries instead, so that the softmax sees none
       const uint32_t id_s =
-          dev::idesc_bf16_f32(kTcRows, kTcKeys, 0) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
-      constexpr uint32_t id_o = dev::idesc_bf16_f32(kTcRows, kON, 1);
+          (dev::idesc_bf16_f32(kTcRows, kTcKeys, 0) & ~kTypes) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
+      constexpr uint32_t id_o = dev::idesc_bf16_f32(kTcRows, kON, 1) & ~kTypes;
       const uint64_t dq = dev::smem_desc(base + SL::q + (kShareKeys ? t * SL::kTile : 0u), 16, 1024);
       const uint64_t dk0 = dev::smem_desc(base + SL::k, 16, 1024);
       // V stage s as the MN-major B operand: the next 64 columns are V's other half
@@ -990,7 +1068,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (kShareKeys && i + 1 == nb) dev::umma_commit(q_free(t));
           };
           if (nb > 0) {
-            ok = tile_wait(q_full(kShareKeys ? t : 0), on & 1) && wait_k(0);
+            ok = tile_wait(kHalf ? q_wide(t) : q_full(kShareKeys ? t : 0), on & 1) && wait_k(0);
             if (ok) {
               dev::tc_fence_after();
               issue_s(0);
@@ -1117,7 +1195,7 @@ cudaError_t read_tile_errors(uint32_t *flags, int clear) { return read_tu_errors
 
 namespace {
 
-bool g_tile_attr[kMaxDevices][2][2];  // dynamic smem attribute set: [D 64/128][mode]
+bool g_tile_attr[kMaxDevices][2][3];  // dynamic smem attribute set: [D 64/128][mode]
 
 template <int D, int MODE>
 int prepare_tile_kernel() {
@@ -1136,12 +1214,12 @@ int prepare_tile_kernel() {
   return PKV_OK;
 }
 
-template <int D>
+template <int D, int MODE>
 int launch_prompt(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
                   const TileArgs &a, unsigned grid, cudaStream_t stream) {
-  const int rc = prepare_tile_kernel<D, kPrompt>();
+  const int rc = prepare_tile_kernel<D, MODE>();
   if (rc) return rc;
-  tile_kernel<D, kPrompt><<<grid, kTileThreads, tile_smem<D, kPrompt>(), stream>>>(tmq, tmk, tmv, a);
+  tile_kernel<D, MODE><<<grid, kTileThreads, tile_smem<D, MODE>(), stream>>>(tmq, tmk, tmv, a);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? PKV_OK : cuda_error(e, "tile_kernel launch");
 }
@@ -1194,6 +1272,41 @@ int launch_prefix(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv_cach
   const dim3 grid((unsigned)(l.tiles * c.num_kv_heads), (unsigned)l.splits);
   return c.head_dim == 64 ? launch_prefix_tiles<64>(tmq, tmk, tmv, a, grid, stream)
                           : launch_prefix_tiles<128>(tmq, tmk, tmv, a, grid, stream);
+}
+
+int launch_chunk(const ChunkLaunch &l, cudaStream_t stream) {
+  TileArgs a = {};
+  a.out = l.out;
+  a.out_stride = (int64_t)l.num_q_heads * l.head_dim;
+  a.start = l.query_start;
+  a.num = l.num_seqs;
+  a.total = (int32_t)l.num_queries;
+  a.max_len = l.max_query_len;
+  a.num_q_heads = l.num_q_heads;
+  a.num_kv_heads = l.num_kv_heads;
+  a.group = l.num_q_heads / l.num_kv_heads;
+  a.tile_tokens = kTileRows / a.group;
+  a.scale_log2 = l.scale * kLog2e;
+  a.context_lens = l.context_lens;
+  a.kv_rows = l.kv_rows;
+  a.max_context = l.max_context;
+  a.k_unit = l.k_unit;
+  a.v_unit = l.v_unit;
+  const int64_t tiles = l.num_queries / (2 * a.tile_tokens) + std::min<int64_t>(l.num_seqs, l.num_queries);
+  if (l.num_queries > 0x7fffff00LL || tiles > 0x7fffffffLL / l.num_kv_heads)
+    return set_error(PKV_ERR_UNSUPPORTED, "paged_prefill_attention_q8: too many query rows");
+  const int64_t rows = (int64_t)l.num_seqs * l.kv_rows, kw = (int64_t)l.num_kv_heads * l.head_dim;
+  CUtensorMap tmq, tmk, tmv;
+  {
+    std::lock_guard<std::mutex> lk(attn_mutex());
+    int rc = query_map(l.q, l.num_queries, l.num_q_heads, l.head_dim, a.out_stride, a.group, a.tile_tokens, &tmq);
+    if (!rc) rc = packed_map(l.k, rows, l.num_kv_heads, l.head_dim, kw, kTcKeys, &tmk);
+    if (!rc) rc = packed_map(l.v, rows, l.num_kv_heads, l.head_dim, kw, kTcKeys, &tmv);
+    if (rc) return rc;
+  }
+  const unsigned grid = (unsigned)(tiles * l.num_kv_heads);
+  return l.head_dim == 64 ? launch_prompt<64, kNewest>(tmq, tmk, tmv, a, grid, stream)
+                          : launch_prompt<128, kNewest>(tmq, tmk, tmv, a, grid, stream);
 }
 
 }  // namespace pkv
@@ -1261,8 +1374,8 @@ PKV_API int prompt_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k
   if (rc) return rc;
   const unsigned grid = (unsigned)(tiles * num_kv_heads);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  rc = head_dim == 64 ? launch_prompt<64>(tmq, tmk, tmv, a, grid, s)
-                      : launch_prompt<128>(tmq, tmk, tmv, a, grid, s);
+  rc = head_dim == 64 ? launch_prompt<64, kPrompt>(tmq, tmk, tmv, a, grid, s)
+                      : launch_prompt<128, kPrompt>(tmq, tmk, tmv, a, grid, s);
   if (!rc) clear_error();
   return rc;
 }

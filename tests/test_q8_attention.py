@@ -277,10 +277,24 @@ def test_rotary_steps(B, neox):
     assert B.pkv_device_errors() == 0
 
 
+def check_prefill(got, q, k, want, mag, scale):
+    """K, V and the weights are fp16 here, each off by 2^-11 of itself at most (values below 2^-14 of
+    the largest scale's unit by 2^-25 of it): the weights' and V's are 2^-10 sum p |v| together, K's
+    move a score by 2^-11 sum |q k| scale, and so a normalised weight by twice that of itself."""
+    if not k.shape[0]:
+        return
+    g = q.shape[1] // k.shape[1]
+    top = max(float((q[:, h].double().abs() @ k[:, h // g].abs().T).max()) for h in range(q.shape[1])) * abs(scale)
+    err = (got.double() - want).abs()
+    assert bool((err <= 2.0 ** -8 * want.abs() + (2.0 ** -10 + 2.0 ** -10 * top) * mag + 2.0 ** -24 * mag.max()).all()), float(err.max())
+
+
 @pytest.mark.parametrize("dtype", R.KINDS)
 @pytest.mark.parametrize("lens,new,hq,hkv,d,bs", [
     ([100, 37, 0, 300], [5, 1, 0, 300], 4, 2, 64, 16), ([1000, 700], [130, 257], 6, 2, 128, 32),
     ([50], [50], 8, 1, 128, 8), ([600, 256], [3, 256], 3, 3, 64, 256),
+    ([1], [1], 1, 1, 64, 8), ([129, 128, 127, 257], [1, 128, 2, 129], 5, 1, 128, 16),
+    ([3000], [700], 4, 4, 64, 64), ([2000] * 20, [64] * 20, 8, 2, 128, 16),
 ])
 def test_prefill(B, dtype, lens, new, hq, hkv, d, bs):
     b = Batch(lens, dtype, hkv, d, bs, seed=50)
@@ -294,14 +308,53 @@ def test_prefill(B, dtype, lens, new, hq, hkv, d, bs):
                                  workspace=ws)
     at = 0
     for s, (m, n) in enumerate(zip(lens, new)):
-        k, v = (R.values(c, sc, b.tables[s], 0, m).to(torch.bfloat16) for c, sc in ((b.k, b.ks), (b.v, b.vs)))
+        k, v = (R.values(c, sc, b.tables[s], 0, m, torch.float64) for c, sc in ((b.k, b.ks), (b.v, b.vs)))
         seen = torch.arange(m, device=DEV)[None, :] <= torch.arange(m - n, m, device=DEV)[:, None]
         want, mag = R.attention(q[at:at + n], k, v, d ** -0.5, seen)
-        err = (out[at:at + n].double() - want).abs()
-        # the prefill kernel's weights are bf16: 2^-8 each
-        assert bool((err <= 2.0 ** -8 * want.abs() + 2.0 ** -7 * mag).all()), float(err.max())
+        check_prefill(out[at:at + n], q[at:at + n], k, want, mag, d ** -0.5)
         at += n
     assert B.pkv_device_errors() == 0
+
+
+def test_prefill_of_hard_values(B):
+    """Queries of any size, a scale below 0, pages of scales far apart and of zeros."""
+    for dtype in R.KINDS:
+        b = Batch([300, 200], dtype, 2, 64, 16, seed=51)
+        gen = torch.Generator().manual_seed(52)
+        b.vs *= torch.exp2(torch.randint(-6, 7, b.vs.shape, generator=gen).float()).to(DEV)
+        b.ks *= torch.exp2(torch.randint(-3, 2, b.ks.shape, generator=gen).float()).to(DEV)
+        b.ks[b.tables[0][2]] = b.vs[b.tables[0][3]] = 0.0
+        b.ks[b.tables[1]] = 0.0  # all of a context's keys are zeros
+        poison(b)
+        base = b.randn(9, 4, 64)
+        for e, scale in ((0, 0.125), (0, -0.125), (60, 0.125 * 2.0 ** -60), (-90, 0.125 * 2.0 ** 90)):
+            q = (base.float() * 2.0 ** e).to(torch.bfloat16)
+            out = torch.empty_like(q)
+            B.paged_prefill_attention_q8(out, q, *b.cache(), b.bt, b.cl, 300, starts([4, 5]), 5, scale)
+            for s, (lo, hi) in enumerate(((0, 4), (4, 9))):
+                m, n = b.lens[s], hi - lo
+                k, v = (R.values(c, sc, b.tables[s], 0, m, torch.float64) for c, sc in ((b.k, b.ks), (b.v, b.vs)))
+                seen = torch.arange(m, device=DEV)[None, :] <= torch.arange(m - n, m, device=DEV)[:, None]
+                want, mag = R.attention(q[lo:hi], k, v, scale, seen)
+                check_prefill(out[lo:hi], q[lo:hi], k, want, mag, scale)
+    assert B.pkv_device_errors() == 0
+
+
+def test_prefill_lengths_that_do_not_fit(B):
+    b = Batch([100, 100, 100], torch.int8, 1, 64, 16, seed=53)
+    q = b.randn(12, 2, 64)
+    b.cl[0] = 2          # of 4 queries, two lie before the first token
+    b.cl[2] = 1 << 30    # cut to max_context_len
+    out = torch.full((14, 2, 64), 9.0, dtype=torch.bfloat16, device=DEV)
+    B.paged_prefill_attention_q8(out[:12], q, *b.cache(), b.bt, b.cl, 100, starts([4, 4, 4]), 4, 0.125)
+    assert B.pkv_device_errors() == 4
+    assert bool((out[:2] == 0).all()) and bool((out[12:] == 9).all())
+    for s, (lo, m) in enumerate(((2, 2), (4, 100), (8, 100))):
+        n = (4, 8, 12)[s] - lo
+        k, v = (R.values(c, sc, b.tables[s], 0, m, torch.float64) for c, sc in ((b.k, b.ks), (b.v, b.vs)))
+        seen = torch.arange(m, device=DEV)[None, :] <= torch.arange(m - n, m, device=DEV)[:, None]
+        want, mag = R.attention(q[lo:lo + n], k, v, 0.125, seen)
+        check_prefill(out[lo:lo + n], q[lo:lo + n], k, want, mag, 0.125)
 
 
 def test_streams_and_graphs(B):

@@ -105,16 +105,17 @@ def test_steps(B):
 
 def test_prefill(B):
     ws = B.paged_prefill_q8_workspace_size(2, 2, 64, 16, 100)
-    assert ws >= 2 * 2 * 7 * 2 * 16 * 64 * 2 and B.paged_prefill_q8_workspace_size(2, 2, 80, 16, 100) == 0
+    assert ws >= 2 * 2 * 100 * 2 * 64 * 2 and B.paged_prefill_q8_workspace_size(2, 2, 80, 16, 100) == 0
     assert B.paged_prefill_q8_workspace_size(65535, 8, 64, 16, 1 << 20) == 0  # over 2^31 rows
 
-    def call(out=FAKE, most=100, start=FAKE, new=4, w=FAKE, size=ws, c=q8(B)):
-        return B.lib().paged_prefill_attention_q8(out, FAKE, ctypes.byref(c), FAKE, 8, FAKE, most, start, new, 2, 8,
+    def call(out=FAKE, most=100, start=FAKE, new=4, w=FAKE, size=ws, c=q8(B), queries=8):
+        return B.lib().paged_prefill_attention_q8(out, FAKE, queries, ctypes.byref(c), FAKE, 8, FAKE, most, start, new, 2, 8,
                                                   ctypes.byref(desc(B)), 0.1, w, size, None)
 
     assert call(out=None) == -1 and call(start=None) == -1 and call(new=101) == -2 and call(w=None) == -4
     assert call(size=ws - 1) == -4 and call(w=ODD) == -5 and call(out=ODD) == -5 and call(c=q8(B, kind=3)) == -3
-    assert call(new=0) == 0
+    assert call(queries=-1) == -2
+    assert call(new=0) == 0 and call(queries=0) == 0
 
 
 def test_the_binding_names_what_is_wrong(B):
