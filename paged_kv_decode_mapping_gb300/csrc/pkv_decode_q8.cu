@@ -13,13 +13,15 @@
 //  * No ldmatrix: the fragments' element order along dims (K) and along keys (V) is free, as long
 //    as both operands agree, so each lane loads 16 bytes in a row and widens them in registers:
 //    K rows' dims 2 bytes at a time, V rows by interleaving the bytes of two keys (prmt).
-//  * The batch's keys, in 128-key chunks, are one list (sequence, kv head, chunk), cut into even
-//    shares whatever lies at the cuts.  A (sequence, kv head) that several shares cut is merged by
-//    the last of them to end, in the order of the keys whoever that is.
+//  * The batch's keys, in 128-key chunks, are one list (sequence, kv head, chunk), cut into shares
+//    of even cost whatever lies at the cuts.  A chunk costs as much as the end of a (sequence, kv
+//    head): by chunks alone, the shares of many short contexts were the last (256 contexts of 16 to
+//    8192 tokens 51.0 against 40.3 us; 2 : 1 43.1, 2 : 3 41.2).  A (sequence, kv head) that several
+//    shares cut is merged by the last of them to end, in the order of the keys whoever that is.
 //  * One CTA per SM, of several groups: a producer and four consumer warps with a ring, and a
-//    share, of their own.  The producers issue their chunks in step.  As CTAs of their own, three
-//    to an SM, groups drew even parts of an SM's rate only on average: of equal shares the last
-//    was done 60 us after the start where the mean was 46 (256 contexts of 16 to 8192 tokens).
+//    share, of their own.  As CTAs of their own, three to an SM, groups drew even parts of an SM's
+//    rate only on average: of equal shares the last was done 60 us after the start where the mean
+//    was 46 (256 contexts of 16 to 8192 tokens).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -33,7 +35,11 @@ namespace pkv {
 namespace {
 
 constexpr int kQ8Keys = 128;           // keys of a stage: 32 for each consumer warp
-constexpr int kQ8MinChunks = 2;        // chunks of a share at least (fewer shares otherwise)
+constexpr int kChunkCost = 1, kEndCost = 1;  // of a chunk, and of a (sequence, kv head)'s end
+// A share's cost at least (fewer shares otherwise).  As much as lies between two chunks' beginnings,
+// so that no share is empty.
+constexpr int kMinCost = 2;
+static_assert(kMinCost >= kChunkCost + kEndCost, "no empty shares");
 constexpr int kQ8MaxShares = 1024;
 
 __host__ __device__ constexpr int q8_groups(int d) { return d == 64 ? 3 : 2; }
@@ -42,13 +48,14 @@ __host__ __device__ constexpr int q8_threads(int d) { return q8_groups(d) * (kCo
 
 struct Q8Desc {                 // one stage's chunk
   int32_t nkeys;                // keys in range
-  int32_t flags;                // kBegins | kEnds: of this share's part of the (sequence, kv head)
+  int32_t flags;                // kBegins, kEnds: of this share's part of the (sequence, kv head);
+                                // kLastOne: of its chunks
   int32_t b, g;
   int32_t slot;                 // partial row the result goes to; -1: the whole context is here
   int32_t share0, parts;        // shares that cut it: share0 .. share0 + parts - 1
   int32_t pad;
 };
-constexpr int32_t kBegins = 1, kEnds = 2;
+constexpr int32_t kBegins = 1, kEnds = 2, kLastOne = 4;
 
 template <int D>
 struct Q8Smem {  // offsets from the 1024-byte aligned base
@@ -63,8 +70,7 @@ struct Q8Smem {  // offsets from the 1024-byte aligned base
   static constexpr uint32_t misc = bars + kStages * 16;            // flag, last, issued
   static constexpr uint32_t kGroup = (misc + 16 + 1023) / 1024 * 1024;
   // of the CTA
-  static constexpr uint32_t step = q8_groups(D) * kGroup;          // the producers' barrier
-  static constexpr uint32_t sums = step + 16;                      // the prefix scan: per warp,
+  static constexpr uint32_t sums = q8_groups(D) * kGroup;          // the prefix scan: per warp,
   static constexpr uint32_t incl = sums + q8_threads(D) / 32 * 8;  // per thread within its warp
   static constexpr uint32_t total = incl + q8_threads(D) * 8;
 };
@@ -81,10 +87,12 @@ struct Q8Args {
   const uint16_t *q;            // [B][Hq][D]
   uint16_t *out;
   const int32_t *tables, *lens;
+  const int32_t *seqs;          // NULL, or whose tables row b of q reads (-1: none, and no output)
   const float *k_scale, *v_scale;
   float *o_part;                // [2 * shares][G][D]: a share's first row, then its last's
   float *lse_part;              // [2 * shares][G], base 2
-  uint32_t *counters;           // [kQ8MaxShares] by the first that cuts; zero between calls
+  uint32_t *counters;           // [2][kQ8MaxShares] by the first that cuts: a context, a run of its
+                                // shares; zero between calls
   int64_t num_blocks;
   int32_t max_blocks, max_len, num_seqs, num_q_heads, num_kv_heads, group;
   int32_t block_size, log2_bs, box_rows, log2_box;
@@ -157,6 +165,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // 2) over it, to that score: fp16 weights of 2^kTop at the reference have room for 2^kSlack more.
 // So most steps need no maximum over the warp.
 constexpr float kTop = 10.f, kSlack = 5.f;
+
+// V's codes as fp16 operands.  int8: behind 0x64 the byte c + 128 is the fp16 1024 + c + 128.
+template <int KIND>
+__device__ __forceinline__ void v_pairs(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  if constexpr (KIND == PKV_Q8_INT8) {  // bytes 0, 2 and 1, 3
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"((w & 0x00ff00ffu) ^ 0x64806480u), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(((w >> 8) & 0x00ff00ffu) ^ 0x64806480u), "r"(0x64806480u));
+  } else {
+    lo = q8::pair<KIND, 0>(w);
+    hi = q8::pair<KIND, 1>(w);
+  }
+}
 
 // K's codes as fp16 operands.  int8: the byte c + 128 alone is the fp16 number (c + 128) 2^-24; the
 // sum over dims of 128 q is taken off where the accumulator begins.  (So no subtraction for each
@@ -251,7 +271,7 @@ struct Q8Lane {
   uint32_t k[2][2];  // K: its first chunk of rows gid and gid + 8 of each 16 keys
   uint32_t v;        // V: the first chunk of its row of the two transposed matrices
 };
-template <int D>
+template <int D, int KIND>
 __device__ __forceinline__ Q8Lane q8_lane(int warp, int lane, int log2_box, int v_first) {
   const int gid = lane >> 2, tig = lane & 3, r = lane & 15;
   Q8Lane x;
@@ -260,8 +280,10 @@ __device__ __forceinline__ Q8Lane q8_lane(int warp, int lane, int log2_box, int 
     x.k[t][0] = chunk_off<D>(32 * warp + 16 * t + gid, (D / 64) * tig, v_first, log2_box);
     x.k[t][1] = chunk_off<D>(32 * warp + 16 * t + key_of(gid + 8), (D / 64) * tig, v_first, log2_box);
   }
-  // V's rows in the order of the weights' rows: 2 t, 2 t + 1, 2 t + 8, 2 t + 9 as bytes of a word
-  x.v = chunk_off<D>(32 * warp + 16 * (lane >> 4) + key_of(2 * (r >> 2) + (r & 1) + 8 * ((r >> 1) & 1)), 0, v_first ^ 1, log2_box);
+  // V's rows in the order of the weights' rows: 2 t, 2 t + 1, 2 t + 8, 2 t + 9 as the bytes of a word
+  // that v_pairs takes together
+  const int r1 = KIND == PKV_Q8_INT8 ? (r >> 1) & 1 : r & 1, r8 = KIND == PKV_Q8_INT8 ? r & 1 : (r >> 1) & 1;
+  x.v = chunk_off<D>(32 * warp + 16 * (lane >> 4) + key_of(2 * (r >> 2) + r1 + 8 * r8), 0, v_first ^ 1, log2_box);
   return x;
 }
 
@@ -395,9 +417,10 @@ __device__ __forceinline__ void q8_tiles(Q8Acc<D> &a, uint32_t sb, const Q8Lane 
         v[2 * t] &= keep[t];
         v[2 * t + 1] &= keep[t];
       }
-      const uint32_t y = q8::prep<KIND>(v[2 * t]), z = q8::prep<KIND>(v[2 * t + 1]);
-      mma_f16(a.o[mt], q8::pair<KIND, 0>(y), q8::pair<KIND, 0>(z), q8::pair<KIND, 1>(y), q8::pair<KIND, 1>(z),
-              b[t][0], b[t][1]);
+      uint32_t y0, y1, z0, z1;
+      v_pairs<KIND>(v[2 * t], y0, y1);
+      v_pairs<KIND>(v[2 * t + 1], z0, z1);
+      mma_f16(a.o[mt], y0, z0, y1, z1, b[t][0], b[t][1]);
     }
   }
 }
@@ -456,11 +479,23 @@ __device__ __forceinline__ void store4(uint16_t *dst, const float4 &x) {
   *reinterpret_cast<uint2 *>(dst) = make_uint2(dev::pack_bf16x2(x.x, x.y), dev::pack_bf16x2(x.z, x.w));
 }
 
-// Four dims of one head from the n shares that cut a context, in the order of the keys: those of
-// `sub`, sub + every, ... are this lane's, the others its neighbours'.
+// The shares of a context cut into more than kOneJoin are joined kRunParts at a time, by the last of
+// each such run, and then the runs, by the last of those: all at once, the last share of 128 (one context of 32768
+// tokens, one kv head of 8 x 128) read 16 rows after one another for 26 us; 17 shares in two steps
+// took 1.5 us more.
+constexpr int kOneJoin = 32, kRunParts = 16;
+
+// Where part p of a context cut from share0 on has its row.
+__device__ __forceinline__ int64_t q8_row_of(const Q8Args &a, int share0, int p, int h) {
+  return (int64_t)(p == 0 ? 2 * share0 + 1 : 2 * (share0 + p)) * a.group + h;
+}
+
+// Four dims of head h from the rows of parts p0, p0 + step, .. (n of them), in that order: those of
+// `sub`, sub + every, ... are this lane's, the others its neighbours'.  The normalised result and its
+// base-2 log-sum.
 template <int D>
-__device__ __forceinline__ void q8_merge(uint16_t *dst, const Q8Args &a, int share0, int n, int h, int d, int sub,
-                                         int every) {
+__device__ __forceinline__ float4 q8_merge(const Q8Args &a, int share0, int p0, int step, int n, int h, int d,
+                                           int sub, int every, float *lse) {
   float M = -INFINITY, den = 0.f;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k0 = sub; k0 < n; k0 += 8 * every) {
@@ -472,7 +507,7 @@ __device__ __forceinline__ void q8_merge(uint16_t *dst, const Q8Args &a, int sha
       lk[u] = -INFINITY;
       o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (k < n) {
-        const int64_t row = (int64_t)(k == 0 ? 2 * share0 + 1 : 2 * (share0 + k)) * a.group + h;
+        const int64_t row = q8_row_of(a, share0, p0 + k * step, h);
         lk[u] = __ldcg(a.lse_part + row);
         o[u] = __ldcg(reinterpret_cast<const float4 *>(a.o_part + row * D + d));
       }
@@ -507,8 +542,9 @@ __device__ __forceinline__ void q8_merge(uint16_t *dst, const Q8Args &a, int sha
     x.w = s1 * x.w + s2 * __shfl_xor_sync(0xffffffffu, x.w, e);
     M = Mn;
   }
+  *lse = M + log2f(den);
   const float inv = den == 0.f ? 1.f : 1.f / den;
-  if (sub == 0) store4(dst, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+  return make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
 }
 
 // A barrier of one group's consumer warps.
@@ -536,22 +572,49 @@ __device__ __forceinline__ void q8_finish(const Q8Args &a, const MergeArea &r, c
     }
   }
   if (d.slot < 0) return;
-  group_bar(grp);
-  if (tid == 0) {
-    int last = 0;
-    if (!*s_flag) last = dev::atomic_add_acq_rel(a.counters + d.share0, 1u) + 1 == (unsigned)d.parts;
-    *s_last = last;
+  // Whether this is the last of n ends that count on `counter` (then it is 0 again).
+  auto last_of = [&](uint32_t *counter, int n) {
+    group_bar(grp);
+    if (tid == 0) {
+      int last = 0;
+      if (!*s_flag) last = dev::atomic_add_acq_rel(counter, 1u) + 1 == (unsigned)n;
+      if (last) *counter = 0u;
+      *s_last = last;
+    }
+    group_bar(grp);
+    return *s_last != 0;  // (written again behind the next end's barriers)
+  };
+  // Joins the rows of parts p0, p0 + step, ..; into the output, or into the first one's place.
+  auto join = [&](int p0, int step, int n, bool out) {
+    int every = 1;  // lanes per item
+    while (every < 32 && 2 * every * items <= T && 8 * every < n) every <<= 1;
+    for (int i0 = 0; i0 < items; i0 += T / every) {  // uniform over the warp: q8_merge shuffles
+      const int i = min(i0 + tid / every, items - 1);  // (the last item may be joined twice, alike)
+      const int h = i / (D / 4), c = 4 * (i - h * (D / 4)), sub = tid & (every - 1);
+      float lse;
+      const float4 x = q8_merge<D>(a, d.share0, p0, step, n, h, c, sub, every, &lse);
+      if (out) {
+        if (sub == 0) store4(a.out + (head0 + h) * D + c, x);
+      } else {  // every other row of the run has been read when the barrier lets this one be
+        group_bar(grp);
+        const int64_t row = q8_row_of(a, d.share0, p0, h);
+        if (sub == 0 && i0 + tid / every < items) {
+          *reinterpret_cast<float4 *>(a.o_part + row * D + c) = x;
+          if (c == 0) a.lse_part[row] = lse;
+        }
+        group_bar(grp);
+      }
+    }
+  };
+  if (d.parts > kOneJoin) {
+    const int runs = (d.parts + kRunParts - 1) / kRunParts;
+    const int p0 = ((d.slot >> 1) - d.share0) / kRunParts * kRunParts, n = min(kRunParts, d.parts - p0);
+    if (!last_of(a.counters + kQ8MaxShares + d.share0 + p0, n)) return;
+    join(p0, 1, n, false);
+    if (last_of(a.counters + d.share0, runs)) join(0, kRunParts, runs, true);
+  } else if (last_of(a.counters + d.share0, d.parts)) {
+    join(0, 1, d.parts, true);
   }
-  group_bar(grp);
-  if (!*s_last) return;  // (written again behind the next end's barriers)
-  int every = 1;  // lanes per item
-  while (every < 32 && 2 * every * items <= T && 8 * every < d.parts) every <<= 1;
-  for (int i0 = 0; i0 < items; i0 += T / every) {  // uniform over the warp: q8_merge shuffles
-    const int i = min(i0 + tid / every, items - 1);  // (the last item may be merged twice, alike)
-    const int h = i / (D / 4), c = 4 * (i - h * (D / 4));
-    q8_merge<D>(a.out + (head0 + h) * D + c, a, d.share0, d.parts, h, c, tid & (every - 1), every);
-  }
-  if (tid == 0) a.counters[d.share0] = 0u;  // ready for the next call
 }
 
 // The two pools' boxes at row y, by one copy: the map's third dimension leads from one pool to the other.
@@ -562,6 +625,12 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
       ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(0), "r"(bar), "l"(policy)
       : "memory");
+}
+
+// n / d for n >= 0, d > 0, by 32 bits where that is enough (a 64-bit division takes 0.2 us).
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+  if (((n | d) >> 32) == 0) return (uint32_t)n / (uint32_t)d;
+  return n / d;
 }
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const float *src) {
@@ -588,7 +657,7 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
   const int grp = producer ? warp - kFirstProducer : warp / kConsumerWarps;
   const uint32_t base = cta_base + grp * SL::kGroup;
   uint8_t *const base_ptr = cta_ptr + grp * SL::kGroup;
-  const uint32_t bar_full = base + SL::bars, bar_empty = bar_full + STAGES * 8, bar_step = cta_base + SL::step;
+  const uint32_t bar_full = base + SL::bars, bar_empty = bar_full + STAGES * 8;
   volatile int *const s_flag = reinterpret_cast<volatile int *>(base_ptr + SL::misc);
   volatile int *const s_last = s_flag + 1;
   volatile int *const s_issued = s_flag + 2;
@@ -600,14 +669,15 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
   const int cap = (int)min((int64_t)a.max_blocks * a.block_size, (int64_t)a.max_len);
   auto length = [&](int b) { return min(max(__ldg(a.lens + b), 0), cap); };
   auto chunks_of = [](int L) { return (int)(((int64_t)L + kQ8Keys - 1) / kQ8Keys); };
-  auto shares_of = [&](int64_t w) {
-    return min((int64_t)gridDim.x * GROUPS, max((int64_t)1, (w + kQ8MinChunks - 1) / kQ8MinChunks));
-  };
+  auto cost_of = [&](int L) { return L > 0 ? kChunkCost * (int64_t)chunks_of(L) + kEndCost : 0; };  // of a kv head
+  auto shares_of = [&](int64_t w) { return min((int64_t)gridDim.x * GROUPS, max((int64_t)1, quotient(w, kMinCost))); };
   // Shares 0 .. gridDim.x - 1 are the CTAs' first groups', so that a few lie on SMs of their own.
   const int share = grp * (int)gridDim.x + (int)blockIdx.x;
   // Entries of the block table, one a lane.
-  auto entries = [&](int seq, int at) {
-    return seq < a.num_seqs && at + lane < a.max_blocks ? __ldg(a.tables + (int64_t)seq * a.max_blocks + at + lane) : 0;
+  auto entries = [&](int b, int at) {
+    if (b >= a.num_seqs) return 0;
+    const int seq = a.seqs ? max(__ldg(a.seqs + b), 0) : b;
+    return at + lane < a.max_blocks ? __ldg(a.tables + (int64_t)seq * a.max_blocks + at + lane) : 0;
   };
 
   // The table window of where this share would begin if all contexts had max_len keys: for equal
@@ -618,11 +688,11 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm0)) : "memory");
       if (!a.depth) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm1)) : "memory");
     }
-    const int64_t n = chunks_of(cap), all = n * Hkv * a.num_seqs, shares = shares_of(all);
+    const int64_t n = cost_of(cap), all = n * Hkv * a.num_seqs, shares = shares_of(all);
     if (share < shares && all > 0) {
-      const int64_t at = all * share / shares;
-      guess_b = (int)(at / (n * Hkv));
-      guess_win = (int)(at % n) * kQ8Keys >> a.log2_bs;
+      const int64_t at = quotient(all * share, shares), unit = quotient(at, n);
+      guess_b = (int)quotient(unit, Hkv);
+      guess_win = (int)((at - unit * n + kChunkCost - 1) / kChunkCost) * kQ8Keys >> a.log2_bs;
       guess_tb = entries(guess_b, guess_win);
     }
   }
@@ -634,8 +704,8 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
   for (int b = b_lo; b < b_hi; ++b) {
     const int L0 = __ldg(a.lens + b), L = min(max(L0, 0), cap);
     if (L != L0 && blockIdx.x == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
-    incl += chunks_of(L);
-    if (L == 0 && b % (int)gridDim.x == (int)blockIdx.x) {  // empty context: zero output
+    incl += cost_of(L);
+    if (L == 0 && b % (int)gridDim.x == (int)blockIdx.x && !(a.seqs && __ldg(a.seqs + b) < 0)) {  // empty: zeros
       uint2 *o = reinterpret_cast<uint2 *>(a.out + (int64_t)b * a.num_q_heads * D);
       for (int i = 0; i < a.num_q_heads * D / 4; ++i) o[i] = make_uint2(0u, 0u);
     }
@@ -662,16 +732,8 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) total += s_sums[w];
   const int64_t W = total * Hkv, N = shares_of(W);
-  const int active = W == 0 ? 0 : (int)min((int64_t)GROUPS, max((N - 1 - (int64_t)blockIdx.x) / gridDim.x + 1, (int64_t)0));
-  if ((int64_t)blockIdx.x >= N || active == 0) return;  // the whole CTA
-  if (threadIdx.x == 0) {
-    dev::mbar_init(bar_step, active);
-    dev::fence_mbar_init();
-  }
-  __syncthreads();
-  if (grp >= active) return;  // (no barrier of the whole CTA follows)
-  const int64_t lo = W * share / N, hi = W * (share + 1) / N;
-  const int n_chunks = (int)(hi - lo);
+  if (W == 0 || share >= N) return;  // (no barrier of the whole CTA follows)
+  const int64_t lo = quotient(W * share, N), hi = quotient(W * (share + 1), N);
   auto timeout = [&] {
     if (lane == 0) {
       raise_error(PKV_DEVERR_TIMEOUT);
@@ -684,9 +746,10 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
     const int rb = a.box_rows;
     const uint32_t box_bytes = (uint32_t)(rb * D);
     const uint32_t q_bytes = (uint32_t)a.group * D * 2u;
-    // ---- place lo of the list: the thread whose run of sequences holds it, then the sequence
-    int b, at_lane, n;
-    int64_t at = 0;  // chunks before
+    // ---- the first chunk at or behind place lo: the thread whose run of sequences holds the place,
+    // then the sequence, the kv head and the chunk
+    int b, at_lane;
+    int64_t at = 0, n;  // cost before; of the lane's sequence
     {
       int w = 0;
       while (w + 1 < WARPS && (at + s_sums[w]) * Hkv <= lo) at += s_sums[w++];
@@ -694,7 +757,7 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
       const int r = past ? __ffs(past) - 1 : 31;
       if (r > 0) at += s_incl[32 * w + r - 1];
       for (b = (32 * w + r) * run;; b += 32) {
-        n = b + lane < a.num_seqs ? chunks_of(length(b + lane)) : 0;
+        n = b + lane < a.num_seqs ? cost_of(length(b + lane)) : 0;
         int64_t inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -711,46 +774,64 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
       }
       b += at_lane;
     }
-    int L = length(b), nch = max(__shfl_sync(0xffffffffu, n, at_lane), 1);
-    int64_t seq0 = at * Hkv;  // where the sequence begins in the list
-    int g = (int)((lo - seq0) / nch), c = (int)((lo - seq0) - (int64_t)g * nch);
+    int64_t cost = max(__shfl_sync(0xffffffffu, n, at_lane), (int64_t)1);  // of a kv head of sequence b
+    int nch = (int)max((cost - kEndCost) / kChunkCost, (int64_t)1), L = length(b);
+    int g = (int)quotient(lo - at * Hkv, cost);
+    int64_t u0 = at * Hkv + g * cost;  // where the kv head begins in the list
+    int c = (int)((lo - u0 + kChunkCost - 1) / kChunkCost);
     // Table entries are loaded ahead of their use: the current window of 32, the one after it, the
     // sequence's first, and the next sequence's length and first window.
     int win = (c * kQ8Keys) >> a.log2_bs;
     int tb = b == guess_b && win == guess_win ? guess_tb : entries(b, win);
     int tb_next = entries(b, win + 32), tb_first = win == 0 ? tb : entries(b, 0);
     int len_seq = b + 1 < a.num_seqs ? length(b + 1) : 0, tb_seq = entries(b + 1, 0);
+    // The next kv head, or the next sequence that has keys (there is one: its place is below hi).
+    auto next_head = [&] {
+      c = 0;
+      u0 += cost;
+      if (++g == Hkv) {
+        g = 0;
+        do {
+          ++b;
+          L = len_seq;
+          tb_first = tb_seq;
+          len_seq = b + 1 < a.num_seqs ? length(b + 1) : 0;
+          tb_seq = entries(b + 1, 0);
+        } while (L == 0 && b + 1 < a.num_seqs);
+        nch = chunks_of(L);
+        cost = cost_of(L);
+      }
+      win = 0;
+      tb = tb_first;
+      tb_next = entries(b, 32);
+    };
+    if (c >= nch) next_head();  // lo lies at a kv head's end
     Q8Desc dsc;
     dsc.pad = 0;
-    bool first = true;
+    bool first = true, last = false;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the step's write is done
     int i = 0;
-    for (; i < n_chunks; ++i) {
+    for (; !last; ++i) {
       const int s = i % STAGES;
       if (first) {
-        const int64_t u0 = seq0 + (int64_t)g * nch, u1 = u0 + nch;
+        const int64_t end = u0 + kChunkCost * (int64_t)(nch - 1);  // its last chunk's place
         dsc.b = b;
         dsc.g = g;
         dsc.slot = -1;
         dsc.share0 = share;
         dsc.parts = 1;
-        if (u0 < lo || u1 > hi) {  // cut: place x is in share floor(((x + 1) N - 1) / W)
-          dsc.share0 = (int)(((u0 + 1) * N - 1) / W);
-          dsc.parts = (int)((u1 * N - 1) / W) - dsc.share0 + 1;
+        if (u0 < lo || end >= hi) {  // cut: place x is in share floor(((x + 1) N - 1) / W)
+          dsc.share0 = (int)quotient((u0 + 1) * N - 1, W);
+          dsc.parts = (int)quotient((end + 1) * N - 1, W) - dsc.share0 + 1;
           dsc.slot = 2 * share + (dsc.share0 == share ? 1 : 0);
         }
-      }
-      // In step: all of the CTA's producers have issued the chunk before.  (Shares differ by one
-      // chunk at most, so that none waits for one that has no more.)
-      if (i > 0 && active > 1 && !__all_sync(0xffffffffu, wait_long(bar_step, (i - 1) & 1))) {
-        timeout();
-        break;
       }
       if (i >= STAGES &&
           !__all_sync(0xffffffffu, wait_long(bar_empty + 8 * s, ((i / STAGES) - 1) & 1))) {
         timeout();
         break;
       }
+      last = (c + 1 < nch ? u0 + kChunkCost * (int64_t)(c + 1) : u0 + cost) >= hi;
       const int k0 = c * kQ8Keys;
       const int nk = min(kQ8Keys, L - k0);
       const int nbox = (nk + rb - 1) >> a.log2_box;
@@ -769,7 +850,7 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
       const int32_t row = (int32_t)((unit * a.block_size + (key & (a.block_size - 1))) * D / 128);
       if (lane == 0) {
         dsc.nkeys = nk;
-        dsc.flags = (first ? kBegins : 0) | (c + 1 == nch || i + 1 == n_chunks ? kEnds : 0);
+        dsc.flags = (first ? kBegins : 0) | (c + 1 == nch || last ? kEnds : 0) | (last ? kLastOne : 0);
         s_desc[s] = dsc;
         dev::mbar_arrive_expect_tx(bar_full + 8 * s, 2u * nbox * box_bytes + (first ? q_bytes : 0u));
         if (first)
@@ -791,26 +872,10 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
       }
       cp_async_arrive(bar_full + 8 * s);
       __syncwarp();
-      if (lane == 0 && active > 1) dev::mbar_arrive(bar_step);
       first = false;
-      if (++c == nch) {  // the next kv head, or the next sequence that has keys
-        c = 0;
+      if (++c == nch && !last) {
         first = true;
-        if (++g == Hkv && i + 1 < n_chunks) {
-          g = 0;
-          seq0 += (int64_t)nch * Hkv;
-          do {  // i + 1 < n_chunks: there is one
-            ++b;
-            L = len_seq;
-            tb_first = tb_seq;
-            len_seq = b + 1 < a.num_seqs ? length(b + 1) : 0;
-            tb_seq = entries(b + 1, 0);
-          } while (L == 0 && b + 1 < a.num_seqs);
-          nch = chunks_of(L);
-        }
-        win = 0;
-        tb = tb_first;
-        tb_next = entries(b, 32);
+        next_head();
       }
     }
     if (lane == 0) *s_issued = i;
@@ -818,9 +883,9 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
   } else {
     // ----------------------------------------------------------- consumer warps
     const int wg = warp - grp * kConsumerWarps, tid = (int)threadIdx.x - grp * kConsumers;
-    const Q8Lane at = q8_lane<D>(wg, lane, a.log2_box, a.v_first);
+    const Q8Lane at = q8_lane<D, KIND>(wg, lane, a.log2_box, a.v_first);
     Q8Acc<D> acc;
-    for (int i = 0; i < n_chunks; ++i) {
+    for (int i = 0;; ++i) {
       const int s = i % STAGES;
       if (!__all_sync(0xffffffffu, wait_long(bar_full + 8 * s, (i / STAGES) & 1))) {
         timeout();
@@ -845,6 +910,7 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
         q8_finish<D>(a, r, d, grp, tid, s_flag, s_last);
         dev::fence_proxy_async_smem();  // the results, ahead of the boxes that follow them
       }
+      if (info.y & kLastOne) break;
       __syncwarp();
       if (lane == 0) dev::mbar_arrive(bar_empty + 8 * s);
     }
@@ -875,13 +941,14 @@ struct Q8Layout {
 Q8Layout q8_layout(int group, int d, int sms) {
   const size_t rows = (size_t)2 * std::min(sms * q8_groups(d), kQ8MaxShares) * group;
   Q8Layout l;
-  l.o_part = kQ8MaxShares * sizeof(uint32_t);
+  l.o_part = 2 * kQ8MaxShares * sizeof(uint32_t);
   l.lse_part = l.o_part + rows * d * sizeof(float);
   l.total = (l.lse_part + rows * sizeof(float) + 255) & ~size_t(255);
   return l;
 }
 
 struct DecodeQ8 {
+  const int32_t *seqs;
   pkv_bf16 *out;
   const pkv_bf16 *q;
   const pkv_q8_cache *cache;
@@ -953,6 +1020,7 @@ int launch_decode_q8(const DecodeQ8 &x, cudaStream_t stream, bool programmatic) 
   a.out = x.out;
   a.tables = x.tables;
   a.lens = x.lens;
+  a.seqs = x.seqs;
   a.k_scale = x.cache->k_scale;
   a.v_scale = x.cache->v_scale;
   a.counters = reinterpret_cast<uint32_t *>(ws);
@@ -972,10 +1040,11 @@ int launch_decode_q8(const DecodeQ8 &x, cudaStream_t stream, bool programmatic) 
   a.depth = depth ? 1 : 0;
   a.v_first = v_first ? 1 : 0;
   a.scale_log2 = x.scale * kLog2e;
-  // one CTA per SM; fewer where the batch cannot have that many shares of kQ8MinChunks
-  const int64_t most = ((int64_t)x.max_len + kQ8Keys - 1) / kQ8Keys * x.num_seqs * c.num_kv_heads;
+  // one CTA per SM; fewer where the batch cannot have that many shares
+  const int64_t most =
+      (((int64_t)x.max_len + kQ8Keys - 1) / kQ8Keys * kChunkCost + kEndCost) * x.num_seqs * c.num_kv_heads;
   const int64_t ctas = std::min(sms, kQ8MaxShares / q8_groups(D));
-  const int64_t grid = std::max<int64_t>(1, std::min(ctas, (most + kQ8MinChunks - 1) / kQ8MinChunks));
+  const int64_t grid = std::max<int64_t>(1, std::min(ctas, most / kMinCost));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
   cfg.blockDim = dim3(q8_threads(D), 1, 1);
@@ -1001,6 +1070,37 @@ int launch_decode_q8(const DecodeQ8 &x, cudaStream_t s, bool programmatic) {
             : launch_decode_q8<128, PKV_Q8_E4M3>(x, s, programmatic);
 }
 
+// The rows of a few queries per sequence as sequences of their own: query i of n sees the context's
+// first L - n + i + 1 keys.  Also zeroes the decode's counters (this workspace keeps none).
+struct RowsArgs {
+  const int32_t *start, *lens;
+  int32_t *row_lens, *row_seqs;
+  uint32_t *counters;
+  int32_t num_seqs, num_queries, max_new, cap;
+};
+__global__ void __launch_bounds__(256) query_rows_kernel(const RowsArgs a) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i < 2 * kQ8MaxShares) a.counters[i] = 0u;
+  if (i < a.num_seqs) {
+    const int L = __ldg(a.lens + i), s = __ldg(a.start + i), e = __ldg(a.start + i + 1);
+    if (L < 0 || L > a.cap || s < 0 || e < s || e > a.num_queries || e - s > a.max_new || e - s > max(L, 0))
+      raise_error(PKV_DEVERR_CONTEXT_LEN);
+  }
+  if (i >= a.num_queries) return;
+  int b = 0, end = a.num_seqs;  // the last sequence that starts at or before row i
+  while (end - b > 1) {
+    const int mid = (b + end) / 2;
+    if (__ldg(a.start + mid) <= i)
+      b = mid;
+    else
+      end = mid;
+  }
+  const int s = __ldg(a.start + b), n = min(__ldg(a.start + b + 1) - s, a.max_new), at = i - s;
+  const bool in = at >= 0 && at < n;
+  a.row_seqs[i] = in ? b : -1;
+  a.row_lens[i] = in ? max(min(max(__ldg(a.lens + b), 0), a.cap) - n + at + 1, 0) : 0;
+}
+
 // Both halves of a step checked, then both enqueued.
 int step_q8(const WriteQ8 &w, const DecodeQ8 &x, cudaStream_t s, const char *fn) {
   int rc = check_write_q8(w, fn);
@@ -1012,6 +1112,32 @@ int step_q8(const WriteQ8 &w, const DecodeQ8 &x, cudaStream_t s, const char *fn)
 }
 
 }  // namespace
+
+size_t rows_q8_workspace(int32_t num_queries, int32_t d, int sms) {
+  return q8_layout(kMaxGroup, d, sms).total + (size_t)num_queries * 8;
+}
+
+int launch_rows_q8(const ChunkLaunch &l, const pkv_q8_cache &cache, const pkv_cache_desc &c,
+                   const int32_t *block_tables, int32_t max_blocks, void *workspace, int sms, cudaStream_t stream) {
+  const size_t decode = q8_layout(kMaxGroup, c.head_dim, sms).total;
+  RowsArgs r;
+  r.start = l.query_start;
+  r.lens = l.context_lens;
+  r.row_lens = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + decode);
+  r.row_seqs = r.row_lens + l.num_queries;
+  r.counters = static_cast<uint32_t *>(workspace);
+  r.num_seqs = l.num_seqs;
+  r.num_queries = (int32_t)l.num_queries;
+  r.max_new = l.max_query_len;
+  r.cap = l.max_context;
+  const int threads = std::max({2 * kQ8MaxShares, r.num_seqs, r.num_queries});
+  query_rows_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(r);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_error(e, "query_rows_kernel launch");
+  const DecodeQ8 x = {r.row_seqs, l.out, l.q, &cache, block_tables, max_blocks, r.row_lens, l.max_context,
+                      r.num_queries, l.num_q_heads, &c, l.scale, workspace, decode};
+  return launch_decode_q8(x, stream, false);
+}
 
 cudaError_t read_decode_q8_errors(uint32_t *flags, int clear) { return read_tu_errors(flags, clear); }
 
@@ -1034,7 +1160,7 @@ PKV_API int paged_decode_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, const pk
                                       const int32_t *context_lens, int32_t max_context_len, int32_t num_seqs,
                                       int32_t num_q_heads, const pkv_cache_desc *desc, float scale, void *workspace,
                                       size_t workspace_bytes, void *stream) {
-  const DecodeQ8 x = {out, q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
+  const DecodeQ8 x = {nullptr, out, q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
                       num_seqs, num_q_heads, desc, scale, workspace, workspace_bytes};
   int rc = check_decode_q8(x, "paged_decode_attention_q8");
   if (!rc) rc = launch_decode_q8(x, static_cast<cudaStream_t>(stream), false);
@@ -1052,7 +1178,7 @@ PKV_API int paged_decode_step_q8(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf1
   w.k = k, w.v = v, w.k_stride = k_stride, w.v_stride = v_stride, w.num_tokens = num_seqs, w.max_query_len = 1;
   w.block_tables = block_tables, w.max_blocks = max_blocks_per_seq, w.context_lens = context_lens;
   w.num_seqs = num_seqs, w.cache = cache, w.desc = desc;
-  const DecodeQ8 x = {out, q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
+  const DecodeQ8 x = {nullptr, out, q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
                       num_seqs, num_q_heads, desc, scale, workspace, workspace_bytes};
   return step_q8(w, x, static_cast<cudaStream_t>(stream), "paged_decode_step_q8");
 }
@@ -1077,7 +1203,7 @@ PKV_API int paged_decode_step_rope_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t 
   w.num_q_heads = num_q_heads;
   w.positions = positions, w.cos_sin = cos_sin, w.max_position = max_position;
   w.rotary_dim = rotary_dim, w.neox_style = neox_style;
-  const DecodeQ8 x = {out, q_out, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
+  const DecodeQ8 x = {nullptr, out, q_out, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
                       num_seqs, num_q_heads, desc, scale, workspace, workspace_bytes};
   return step_q8(w, x, static_cast<cudaStream_t>(stream), fn);
 }

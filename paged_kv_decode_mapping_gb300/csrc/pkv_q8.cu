@@ -317,14 +317,15 @@ struct UnitArgs {
   const float *k_scale, *v_scale;
   float *k_unit, *v_unit;
 };
-__global__ void __launch_bounds__(kQ8Threads) units_q8_kernel(const __grid_constant__ UnitArgs a) {
-  __shared__ float s_k[kQ8Threads], s_v[kQ8Threads];
+constexpr int kUnitThreads = 1024;
+__global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_constant__ UnitArgs a) {
+  __shared__ float s_k[kUnitThreads], s_v[kUnitThreads];
   const int b = blockIdx.x, H = a.s.num_kv_heads, tid = threadIdx.x;
   const int cap = (int)min((int64_t)a.s.max_blocks * a.s.block_size, (int64_t)a.s.max_new);
   const int L = min(max(__ldg(a.s.lens + b), 0), cap), pages = (L + a.s.block_size - 1) >> a.s.log2_bs;
   const int32_t *const row = a.s.tables + (int64_t)b * a.s.max_blocks;
-  for (int h0 = 0; h0 < H; h0 += kQ8Threads) {  // (heads past 256 in further rounds)
-    const int wide = min(H - h0, kQ8Threads), rows = kQ8Threads / wide;
+  for (int h0 = 0; h0 < H; h0 += kUnitThreads) {  // (heads past 1024 in further rounds)
+    const int wide = min(H - h0, kUnitThreads), rows = kUnitThreads / wide;
     const int h = tid % wide, r = tid / wide;
     float k = 0.f, v = 0.f;
     if (r < rows)
@@ -681,7 +682,9 @@ PKV_API int paged_kv_read_q8(pkv_bf16 *k_out, pkv_bf16 *v_out, int64_t k_stride,
 }
 
 // ---------------------------------------------------------------------------
-// Chunked prefill: the contexts are read back into fp16 rows in the workspace, and the tensor-core
+// Chunked prefill.  A few queries per sequence (draft tokens to check) are rows of the decode kernel,
+// each a sequence of its own that reads the codes as they are; more of them take the tensor-core
+// tiles of the packed prompts: the contexts are read back into fp16 rows in the workspace, and the tensor-core
 // tiles of the packed prompts run over those.  (Widening the codes where the tiles stage them would
 // be done once for every 256 query rows that see them, on the warps that the softmax waits for; the
 // reading back costs 5 bytes of traffic a code once.)
@@ -692,8 +695,25 @@ struct PrefillLayout {
   int32_t rows;  // packed rows of a sequence
   size_t k, v, k_unit, v_unit, total;
 };
+constexpr int kMaxRowQueries = 32, kMaxRows = 65535;  // of a sequence, of a call, as the decode's rows
 
-bool prefill_layout(int32_t num_seqs, int32_t hkv, int32_t d, int32_t max_len, PrefillLayout *p) {
+// Whether the decode's rows are the shorter way, by the longest context: they read it once for each
+// query, spread over the GPU; the tiles read it once (and once more back), but the CTAs of one
+// (sequence, kv head) take its blocks of 128 keys one after another.  Block times as measured: 1.3 us
+// of a group's chunk; 1.5 us of a tile's block, 4 TB/s and two launches for the reading back.  (8
+// sequences of 5 queries over 100 to 2000 tokens: XXX us by rows, YYY by tiles.)
+bool rows_pay(int64_t num_queries, int32_t max_query_len, int32_t num_seqs, int32_t hq, const pkv_cache_desc &c,
+              int32_t max_len, int sms) {
+  if (max_query_len > kMaxRowQueries || num_queries > kMaxRows) return false;
+  const double blocks = (max_len + 127) / 128, hkv = c.num_kv_heads;
+  const double groups = c.head_dim == 64 ? 3 : 2, tokens = 2 * (128 / (hq / c.num_kv_heads));
+  const double rows = num_queries * hkv * blocks / (sms * groups) * 1.3 + 2;
+  const double ctas = (num_queries / tokens + num_seqs) * hkv;
+  const double tiles = (ctas > sms ? ctas / sms : 1) * blocks * 1.5 + 8 + num_seqs * hkv * c.head_dim * max_len * 6. / 4e6;
+  return rows < tiles;
+}
+
+bool prefill_layout(int32_t num_seqs, int32_t hkv, int32_t d, int32_t max_len, int sms, PrefillLayout *p) {
   if (num_seqs <= 0 || hkv <= 0 || max_len <= 0 || (d != 64 && d != 128)) return false;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   if ((int64_t)max_len * num_seqs > 0x7fffff00LL / hkv) return false;
@@ -703,8 +723,16 @@ bool prefill_layout(int32_t num_seqs, int32_t hkv, int32_t d, int32_t max_len, P
   p->v = rows;
   p->k_unit = 2 * rows;
   p->v_unit = p->k_unit + units;
-  p->total = p->v_unit + units;
+  p->total = std::max(p->v_unit + units,  // either way
+                      up(rows_q8_workspace(std::min((int64_t)num_seqs * kMaxRowQueries, (int64_t)kMaxRows), d, sms)));
   return true;
+}
+
+// The current device's SMs; without a device (the checks that need none still stand) `otherwise`.
+int sms_or(int otherwise) {
+  std::lock_guard<std::mutex> lk(attn_mutex());
+  int sms = 0;
+  return device_sms(&sms) == PKV_OK && sms > 0 ? sms : otherwise;
 }
 
 }  // namespace
@@ -712,7 +740,7 @@ bool prefill_layout(int32_t num_seqs, int32_t hkv, int32_t d, int32_t max_len, P
 PKV_API size_t paged_prefill_q8_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim,
                                                int32_t max_context_len) {
   PrefillLayout p;
-  return prefill_layout(num_seqs, num_kv_heads, head_dim, max_context_len, &p) ? p.total : 0;
+  return prefill_layout(num_seqs, num_kv_heads, head_dim, max_context_len, sms_or(152), &p) ? p.total : 0;
 }
 
 PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t num_queries,
@@ -738,34 +766,17 @@ PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t
   if (misaligned4(query_start) || misaligned4(block_tables) || misaligned4(context_lens))
     return set_error(PKV_ERR_ALIGN, "%s: int32 tensors must be 4-byte aligned", fn);
   PrefillLayout p;
-  if (!prefill_layout(num_seqs, desc->num_kv_heads, desc->head_dim, max_context_len, &p))
+  const int sms = sms_or(152);
+  if (!prefill_layout(num_seqs, desc->num_kv_heads, desc->head_dim, max_context_len, sms, &p))
     return set_error(PKV_ERR_UNSUPPORTED, "%s: the contexts have more than 2^31 rows of heads", fn);
   if (!workspace || workspace_bytes < p.total)
     return set_error(PKV_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, workspace_bytes, p.total);
   if (!aligned16(workspace)) return set_error(PKV_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char *const ws = static_cast<char *>(workspace);
-  const Span span = span_of(block_tables, max_blocks_per_seq, context_lens, nullptr, max_context_len, num_seqs, 0, *desc);
-  UnitArgs u;
-  u.s = span;
-  u.k_scale = cache->k_scale;
-  u.v_scale = cache->v_scale;
-  u.k_unit = reinterpret_cast<float *>(ws + p.k_unit);
-  u.v_unit = reinterpret_cast<float *>(ws + p.v_unit);
-  units_q8_kernel<<<(unsigned)num_seqs, kQ8Threads, 0, s>>>(u);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_error(e, "units_q8_kernel launch");
-  const int64_t stride = (int64_t)desc->num_kv_heads * desc->head_dim;
-  rc = launch_read(span, *cache, *desc, ws + p.k, ws + p.v, stride, stride, p.rows, u.k_unit, u.v_unit,
-                   ((int64_t)max_context_len + desc->block_size - 1) / desc->block_size, s);
-  if (rc) return rc;
-  ChunkLaunch l;
+  ChunkLaunch l = {};
   l.out = out;
   l.q = q;
-  l.k = reinterpret_cast<const uint16_t *>(ws + p.k);
-  l.v = reinterpret_cast<const uint16_t *>(ws + p.v);
-  l.k_unit = u.k_unit;
-  l.v_unit = u.v_unit;
   l.query_start = query_start;
   l.context_lens = context_lens;
   l.num_queries = num_queries;
@@ -777,6 +788,29 @@ PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t
   l.num_kv_heads = desc->num_kv_heads;
   l.head_dim = desc->head_dim;
   l.scale = scale;
+  if (rows_pay(num_queries, max_query_len, num_seqs, num_q_heads, *desc, max_context_len, sms)) {
+    rc = launch_rows_q8(l, *cache, *desc, block_tables, max_blocks_per_seq, workspace, sms, s);
+    if (!rc) clear_error();
+    return rc;
+  }
+  const Span span = span_of(block_tables, max_blocks_per_seq, context_lens, nullptr, max_context_len, num_seqs, 0, *desc);
+  UnitArgs u;
+  u.s = span;
+  u.k_scale = cache->k_scale;
+  u.v_scale = cache->v_scale;
+  u.k_unit = reinterpret_cast<float *>(ws + p.k_unit);
+  u.v_unit = reinterpret_cast<float *>(ws + p.v_unit);
+  units_q8_kernel<<<(unsigned)num_seqs, kUnitThreads, 0, s>>>(u);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_error(e, "units_q8_kernel launch");
+  const int64_t stride = (int64_t)desc->num_kv_heads * desc->head_dim;
+  rc = launch_read(span, *cache, *desc, ws + p.k, ws + p.v, stride, stride, p.rows, u.k_unit, u.v_unit,
+                   ((int64_t)max_context_len + desc->block_size - 1) / desc->block_size, s);
+  if (rc) return rc;
+  l.k = reinterpret_cast<const uint16_t *>(ws + p.k);
+  l.v = reinterpret_cast<const uint16_t *>(ws + p.v);
+  l.k_unit = u.k_unit;
+  l.v_unit = u.v_unit;
   rc = launch_chunk(l, s);
   if (!rc) clear_error();
   return rc;

@@ -295,6 +295,7 @@ def check_prefill(got, q, k, want, mag, scale):
     ([50], [50], 8, 1, 128, 8), ([600, 256], [3, 256], 3, 3, 64, 256),
     ([1], [1], 1, 1, 64, 8), ([129, 128, 127, 257], [1, 128, 2, 129], 5, 1, 128, 16),
     ([3000], [700], 4, 4, 64, 64), ([2000] * 20, [64] * 20, 8, 2, 128, 16),
+    ([700, 30, 5000, 6], [5, 5, 5, 5], 8, 2, 64, 16), ([9000], [32], 3, 1, 128, 32), ([300] * 50, [1, 2, 3, 4, 5] * 10, 4, 4, 128, 8),
 ])
 def test_prefill(B, dtype, lens, new, hq, hkv, d, bs):
     b = Batch(lens, dtype, hkv, d, bs, seed=50)
@@ -316,7 +317,8 @@ def test_prefill(B, dtype, lens, new, hq, hkv, d, bs):
     assert B.pkv_device_errors() == 0
 
 
-def test_prefill_of_hard_values(B):
+@pytest.mark.parametrize("new", [[4, 5], [150, 170]])  # as rows of the decode, and on the tiles
+def test_prefill_of_hard_values(B, new):
     """Queries of any size, a scale below 0, pages of scales far apart and of zeros."""
     for dtype in R.KINDS:
         b = Batch([300, 200], dtype, 2, 64, 16, seed=51)
@@ -326,12 +328,12 @@ def test_prefill_of_hard_values(B):
         b.ks[b.tables[0][2]] = b.vs[b.tables[0][3]] = 0.0
         b.ks[b.tables[1]] = 0.0  # all of a context's keys are zeros
         poison(b)
-        base = b.randn(9, 4, 64)
+        base = b.randn(sum(new), 4, 64)
         for e, scale in ((0, 0.125), (0, -0.125), (60, 0.125 * 2.0 ** -60), (-90, 0.125 * 2.0 ** 90)):
             q = (base.float() * 2.0 ** e).to(torch.bfloat16)
             out = torch.empty_like(q)
-            B.paged_prefill_attention_q8(out, q, *b.cache(), b.bt, b.cl, 300, starts([4, 5]), 5, scale)
-            for s, (lo, hi) in enumerate(((0, 4), (4, 9))):
+            B.paged_prefill_attention_q8(out, q, *b.cache(), b.bt, b.cl, 300, starts(new), max(new), scale)
+            for s, (lo, hi) in enumerate(((0, new[0]), (new[0], sum(new)))):
                 m, n = b.lens[s], hi - lo
                 k, v = (R.values(c, sc, b.tables[s], 0, m, torch.float64) for c, sc in ((b.k, b.ks), (b.v, b.vs)))
                 seen = torch.arange(m, device=DEV)[None, :] <= torch.arange(m - n, m, device=DEV)[:, None]
@@ -340,21 +342,40 @@ def test_prefill_of_hard_values(B):
     assert B.pkv_device_errors() == 0
 
 
-def test_prefill_lengths_that_do_not_fit(B):
+@pytest.mark.parametrize("n", [4, 40])
+def test_prefill_lengths_that_do_not_fit(B, n):
     b = Batch([100, 100, 100], torch.int8, 1, 64, 16, seed=53)
-    q = b.randn(12, 2, 64)
-    b.cl[0] = 2          # of 4 queries, two lie before the first token
+    q = b.randn(3 * n, 2, 64)
+    b.cl[0] = 2          # of n queries, all but two lie before the first token
     b.cl[2] = 1 << 30    # cut to max_context_len
-    out = torch.full((14, 2, 64), 9.0, dtype=torch.bfloat16, device=DEV)
-    B.paged_prefill_attention_q8(out[:12], q, *b.cache(), b.bt, b.cl, 100, starts([4, 4, 4]), 4, 0.125)
+    out = torch.full((3 * n + 2, 2, 64), 9.0, dtype=torch.bfloat16, device=DEV)
+    B.paged_prefill_attention_q8(out[:3 * n], q, *b.cache(), b.bt, b.cl, 100, starts([n, n, n]), n, 0.125)
     assert B.pkv_device_errors() == 4
-    assert bool((out[:2] == 0).all()) and bool((out[12:] == 9).all())
-    for s, (lo, m) in enumerate(((2, 2), (4, 100), (8, 100))):
-        n = (4, 8, 12)[s] - lo
+    assert bool((out[:n - 2] == 0).all()) and bool((out[3 * n:] == 9).all())
+    for s, (lo, m) in enumerate(((n - 2, 2), (n, 100), (2 * n, 100))):
         k, v = (R.values(c, sc, b.tables[s], 0, m, torch.float64) for c, sc in ((b.k, b.ks), (b.v, b.vs)))
-        seen = torch.arange(m, device=DEV)[None, :] <= torch.arange(m - n, m, device=DEV)[:, None]
-        want, mag = R.attention(q[lo:lo + n], k, v, 0.125, seen)
-        check_prefill(out[lo:lo + n], q[lo:lo + n], k, want, mag, 0.125)
+        x = (s + 1) * n - lo
+        seen = torch.arange(m, device=DEV)[None, :] <= torch.arange(m - x, m, device=DEV)[:, None]
+        want, mag = R.attention(q[lo:lo + x], k, v, 0.125, seen)
+        check_prefill(out[lo:lo + x], q[lo:lo + x], k, want, mag, 0.125)
+
+
+def test_prefill_leaves_rows_of_no_sequence(B):
+    """Rows between and behind the sequences', empty contexts among them, both ways."""
+    for n in (3, 60):
+        b = Batch([200, 0, 90], torch.float8_e4m3fn, 2, 128, 16, seed=54)
+        q = b.randn(2 * n + 7, 4, 128)
+        out = torch.full_like(q, 5.0)
+        st = torch.tensor([2, 2 + n, 2 + n, 2 + 2 * n], dtype=torch.int32, device=DEV)
+        B.paged_prefill_attention_q8(out, q, *b.cache(), b.bt, b.cl, 200, st, n, 0.1)
+        assert bool((out[:2] == 5).all()) and bool((out[2 + 2 * n:] == 5).all())
+        for s, (lo, m) in enumerate(((2, 200), (0, 0), (2 + n, 90))):
+            if m:
+                k, v = (R.values(c, sc, b.tables[s], 0, m, torch.float64) for c, sc in ((b.k, b.ks), (b.v, b.vs)))
+                seen = torch.arange(m, device=DEV)[None, :] <= torch.arange(m - n, m, device=DEV)[:, None]
+                want, mag = R.attention(q[lo:lo + n], k, v, 0.1, seen)
+                check_prefill(out[lo:lo + n], q[lo:lo + n], k, want, mag, 0.1)
+        assert B.pkv_device_errors() == 0
 
 
 def test_streams_and_graphs(B):
