@@ -590,6 +590,21 @@ int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t num_que
                                size_t workspace_bytes, void *stream);
 
 /*
+ * paged_kv_copy_blocks_q8, paged_kv_compact_q8 -- paged_kv_copy_blocks and paged_kv_compact for
+ * 8-bit caches, one pkv_q8_cache per layer (HOST array): a page's rows with its scales.  A pair of
+ * whose rows some are copied takes the source's scales (so the destination's other rows lose their
+ * meaning: a fork's new page has none); one of no rows is left.  Either may be applied with
+ * num_tokens; tables and map as there (NULL, 0: pages alone).  Two launches per 64 layers.
+ */
+int paged_kv_copy_blocks_q8(const pkv_q8_cache *caches, int32_t num_layers,
+                            const int32_t *block_pairs, const int32_t *num_tokens,
+                            int64_t num_pairs, const pkv_cache_desc *desc, void *stream);
+int paged_kv_compact_q8(const pkv_q8_cache *caches, int32_t num_layers, const int32_t *block_moves,
+                        const int32_t *num_tokens, int64_t num_moves, int32_t *block_tables,
+                        int64_t num_seqs, int32_t max_blocks_per_seq, const int32_t *block_map,
+                        const pkv_cache_desc *desc, void *stream);
+
+/*
  * paged_decode_split -- flash-decoding partition kernel (split-K over the keys;
  * the FlashAttention-2 online-softmax algebra that the first page references).
  *

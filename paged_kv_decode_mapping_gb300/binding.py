@@ -119,6 +119,10 @@ _lib.paged_prefill_q8_workspace_size.restype = _sz
 _lib.paged_prefill_attention_q8.argtypes = [_P, _P, _i64, _Q8, _P, _i32, _P, _i32, _P, _i32, _i32, _i32, _D, _f32,
                                             _P, _sz, _P]
 _lib.paged_prefill_attention_q8.restype = ctypes.c_int
+_lib.paged_kv_copy_blocks_q8.argtypes = [_P, _i32, _P, _P, _i64, _D, _P]
+_lib.paged_kv_copy_blocks_q8.restype = ctypes.c_int
+_lib.paged_kv_compact_q8.argtypes = [_P, _i32, _P, _P, _i64, _P, _i64, _i32, _P, _D, _P]
+_lib.paged_kv_compact_q8.restype = ctypes.c_int
 _lib.paged_decode_split.argtypes = [_P, _P, _P, _P, _P, _P, _i32, _P, _i32, _i32, _i32, _D, _f32,
                                     _i32, _P]
 _lib.paged_decode_split.restype = ctypes.c_int
@@ -952,6 +956,83 @@ def paged_prefill_attention_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torc
         int(max_context_len), query_start.data_ptr(), int(max_query_len), B, q.shape[1], ctypes.byref(d),
         float(scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream, dev)),
         "paged_prefill_attention_q8")
+
+
+def _q8_layers(dev: int, k_caches, v_caches, k_scales, v_scales, where: str):
+    """(array of pkv_q8_cache, layers, descriptor, the first k cache) of one layer's tensors, of
+    tensors with the layers in front, or of sequences of the layers' tensors."""
+    if isinstance(k_caches, torch.Tensor):
+        tensors = (k_caches, v_caches, k_scales, v_scales)
+        if not all(isinstance(t, torch.Tensor) for t in tensors):
+            raise TypeError(f"{where}: the caches and scales must be given alike")
+        if k_caches.dim() == 5:
+            for t, name, n in zip(tensors, ("k_caches", "v_caches", "k_scales", "v_scales"), (5, 5, 3, 3)):
+                if t.dim() != n or t.shape[0] != k_caches.shape[0]:
+                    raise ValueError(f"{where}: {name} must have the layers in front, as k_caches has")
+            layers = list(zip(*(t.unbind(0) for t in tensors)))
+        else:
+            layers = [tensors]
+    else:
+        layers = list(zip(list(k_caches), list(v_caches), list(k_scales), list(v_scales), strict=True))
+    if not layers:
+        raise ValueError(f"{where}: no layers")
+    first = layers[0][0]
+    none = torch.empty((0, 0), dtype=torch.int32, device=first.device), torch.empty(0, dtype=torch.int32,
+                                                                                   device=first.device)
+    out = (pkv_q8_cache * len(layers))()
+    for i, tensors in enumerate(layers):
+        if tensors[0].shape != first.shape or tensors[0].dtype != first.dtype:
+            raise ValueError(f"{where}: the layers' caches must be alike")
+        out[i], d = _q8_cache(dev, *tensors, *none)
+    return out, len(layers), d, first
+
+
+def paged_kv_copy_blocks_q8(k_caches, v_caches, k_scales, v_scales, block_pairs: torch.Tensor,
+                            num_tokens: Optional[torch.Tensor] = None, stream=None) -> None:
+    """paged_kv_copy_blocks for 8-bit caches: rows and scales.  One layer's tensors [NB, Hkv, BS, D]
+    and [NB, Hkv], all layers' with the layers in front, or lists of the layers'."""
+    dev = _home(block_pairs)
+    caches, n, d, first = _q8_layers(dev, k_caches, v_caches, k_scales, v_scales, "paged_kv_copy_blocks_q8")
+    if not _fine(dev, torch.int32, block_pairs, num_tokens):
+        _need(block_pairs, "block_pairs", torch.int32, 2)
+        if num_tokens is not None:
+            _need(num_tokens, "num_tokens", torch.int32, 1)
+        _one_device(first, block_pairs=block_pairs, num_tokens=num_tokens)
+    shape = block_pairs.shape
+    if len(shape) != 2 or shape[1] != 2:
+        raise ValueError("block_pairs must be [n, 2]")
+    if num_tokens is not None and num_tokens.shape != shape[:1]:
+        raise ValueError("num_tokens must have one entry per pair")
+    _check(_lib.paged_kv_copy_blocks_q8(ctypes.addressof(caches), n, block_pairs.data_ptr(), _ptr(num_tokens),
+                                        shape[0], ctypes.byref(d), _stream(stream, dev)), "paged_kv_copy_blocks_q8")
+
+
+def paged_kv_compact_q8(k_caches, v_caches, k_scales, v_scales, block_moves: torch.Tensor,
+                        block_tables: Optional[torch.Tensor] = None, block_map: Optional[torch.Tensor] = None,
+                        stream=None) -> None:
+    """paged_kv_compact for 8-bit caches (as in paged_kv_copy_blocks_q8)."""
+    dev = _home(block_moves)
+    caches, n, d, first = _q8_layers(dev, k_caches, v_caches, k_scales, v_scales, "paged_kv_compact_q8")
+    if not _fine(dev, torch.int32, block_moves, block_tables, block_map):
+        _need(block_moves, "block_moves", torch.int32, 2)
+        if block_tables is not None:
+            _need(block_tables, "block_tables", torch.int32, 2)
+        if block_map is not None:
+            _need(block_map, "block_map", torch.int32, 1)
+        _one_device(first, block_moves=block_moves, block_tables=block_tables, block_map=block_map)
+    shape = block_moves.shape
+    if len(shape) != 2 or shape[1] != 2:
+        raise ValueError("block_moves must be [n, 2]")
+    rows = cols = 0
+    if block_tables is not None:
+        if block_tables.dim() != 2:
+            raise ValueError("block_tables must be [B, M]")
+        if block_map is None or block_map.shape != (d.num_blocks,):
+            raise ValueError("block_tables need a block_map with one entry per block")
+        rows, cols = block_tables.shape
+    _check(_lib.paged_kv_compact_q8(ctypes.addressof(caches), n, block_moves.data_ptr(), None, shape[0],
+                                    _ptr(block_tables), rows, cols, _ptr(block_map), ctypes.byref(d),
+                                    _stream(stream, dev)), "paged_kv_compact_q8")
 
 
 def paged_decode_attention_noalloc(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,

@@ -92,6 +92,29 @@ __global__ void __launch_bounds__(kPageThreads) copy_pages_kernel(const __grid_c
     if (take[u]) __stcs(dst + i0 + u * kPageThreads, x[u]);
 }
 
+// The 8-bit cache's scales of the copied pages: plane 2l is layer l's K, 2l + 1 its V.  A pair of which
+// no row is copied leaves its destination's scales too.
+struct ScaleArgs {
+  float *k[kPageLayers], *v[kPageLayers];
+  const int2 *pairs;
+  const int32_t *rows;
+  int64_t num_blocks, num_pairs;
+  uint32_t heads;
+};
+__global__ void __launch_bounds__(kPageThreads) copy_scales_kernel(const __grid_constant__ ScaleArgs a) {
+  const int plane = blockIdx.y;
+  const int64_t i = (int64_t)blockIdx.x * kPageThreads + threadIdx.x;
+  const int64_t pair = i / a.heads;
+  if (pair >= a.num_pairs) return;
+  const int2 p = __ldg(a.pairs + pair);
+  // (flagged by the rows' copy)
+  if (p.x < 0 || p.x >= a.num_blocks || p.y < 0 || p.y >= a.num_blocks || p.x == p.y) return;
+  if (a.rows && __ldg(a.rows + pair) <= 0) return;
+  float *const pool = (plane & 1) ? a.v[plane >> 1] : a.k[plane >> 1];
+  const uint32_t h = (uint32_t)(i - pair * a.heads);
+  pool[(int64_t)p.y * a.heads + h] = pool[(int64_t)p.x * a.heads + h];
+}
+
 cudaError_t read_page_errors(uint32_t *flags, int clear) { return read_tu_errors(flags, clear); }
 
 namespace {
@@ -165,6 +188,54 @@ int launch_pages(pkv_bf16 *const *k_caches, pkv_bf16 *const *v_caches, int32_t n
   return PKV_OK;
 }
 
+// The layers' 8-bit caches checked; the rows as ones of head_dim / 2 16-bit elements.
+int check_q8_pages(const pkv_q8_cache *caches, int32_t num_layers, const pkv_cache_desc *c, const char *fn) {
+  if (!c || (num_layers > 0 && !caches)) return set_error(PKV_ERR_NULL, "%s: NULL caches or descriptor", fn);
+  if (num_layers < 0) return set_error(PKV_ERR_SHAPE, "%s: negative count", fn);
+  for (int32_t l = 0; l < num_layers; ++l) {
+    const int rc = check_q8(caches + l, c, 1, fn);
+    if (rc) return rc;
+  }
+  return PKV_OK;
+}
+
+int copy_q8_pages(const pkv_q8_cache *caches, int32_t num_layers, const int32_t *pairs, const int32_t *rows,
+                  int64_t num_pairs, int32_t *tables, int64_t entries, const int32_t *block_map,
+                  const pkv_cache_desc &c, cudaStream_t stream) {
+  pkv_cache_desc half = c;
+  half.head_dim = c.head_dim / 2;
+  int32_t l0 = 0;
+  do {
+    const int32_t n = std::min(num_layers - l0, (int32_t)kPageLayers);
+    pkv_bf16 *k[kPageLayers], *v[kPageLayers];
+    ScaleArgs a = {};
+    for (int32_t l = 0; l < n; ++l) {
+      const pkv_q8_cache &q = caches[l0 + l];
+      k[l] = static_cast<pkv_bf16 *>(q.k_cache);
+      v[l] = static_cast<pkv_bf16 *>(q.v_cache);
+      a.k[l] = q.k_scale;
+      a.v[l] = q.v_scale;
+    }
+    const bool remap = l0 == 0;
+    const int rc = launch_pages(k, v, n, pairs, rows, num_pairs, remap ? tables : nullptr, remap ? entries : 0,
+                                block_map, half, stream);
+    if (rc) return rc;
+    if (n > 0 && num_pairs > 0) {
+      a.pairs = reinterpret_cast<const int2 *>(pairs);
+      a.rows = rows;
+      a.num_blocks = c.num_blocks;
+      a.num_pairs = num_pairs;
+      a.heads = (uint32_t)c.num_kv_heads;
+      const int64_t ctas = (num_pairs * c.num_kv_heads + kPageThreads - 1) / kPageThreads;
+      copy_scales_kernel<<<dim3((unsigned)ctas, (unsigned)(2 * n)), kPageThreads, 0, stream>>>(a);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return cuda_error(e, "copy_scales_kernel launch");
+    }
+    l0 += n;
+  } while (l0 < num_layers);
+  return PKV_OK;
+}
+
 }  // namespace
 }  // namespace pkv
 
@@ -204,6 +275,38 @@ PKV_API int paged_kv_compact(pkv_bf16 *const *k_caches, pkv_bf16 *const *v_cache
   if ((num_moves > 0 && num_layers > 0) || entries > 0)
     rc = launch_pages(k_caches, v_caches, num_layers, block_moves, nullptr, num_moves, block_tables,
                       entries, block_map, *cache, static_cast<cudaStream_t>(stream));
+  if (!rc) clear_error();
+  return rc;
+}
+
+PKV_API int paged_kv_copy_blocks_q8(const pkv_q8_cache *caches, int32_t num_layers, const int32_t *block_pairs,
+                                    const int32_t *num_tokens, int64_t num_pairs, const pkv_cache_desc *desc,
+                                    void *stream) {
+  return paged_kv_compact_q8(caches, num_layers, block_pairs, num_tokens, num_pairs, nullptr, 0, 0, nullptr, desc,
+                             stream);
+}
+
+PKV_API int paged_kv_compact_q8(const pkv_q8_cache *caches, int32_t num_layers, const int32_t *block_moves,
+                                const int32_t *num_tokens, int64_t num_moves, int32_t *block_tables,
+                                int64_t num_seqs, int32_t max_blocks_per_seq, const int32_t *block_map,
+                                const pkv_cache_desc *desc, void *stream) {
+  const char *const fn = "paged_kv_copy_blocks_q8/compact_q8";
+  int rc = check_q8_pages(caches, num_layers, desc, fn);
+  if (rc) return rc;
+  if (num_moves < 0 || num_seqs < 0 || max_blocks_per_seq < 0) return set_error(PKV_ERR_SHAPE, "%s: negative count", fn);
+  if (num_moves > 0 && !block_moves) return set_error(PKV_ERR_NULL, "%s: NULL block pairs", fn);
+  if ((reinterpret_cast<uintptr_t>(block_moves) & 7u) || (reinterpret_cast<uintptr_t>(num_tokens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(block_tables) & 3u) || (reinterpret_cast<uintptr_t>(block_map) & 3u))
+    return set_error(PKV_ERR_ALIGN, "%s: block pairs must be 8-byte, other int32 arrays 4-byte aligned", fn);
+  if (num_moves > 0x3fffffffLL / desc->num_kv_heads / desc->block_size)
+    return set_error(PKV_ERR_UNSUPPORTED, "%s: too many pairs", fn);
+  const int64_t entries = num_seqs > 0x7fffffffLL ? -1 : num_seqs * max_blocks_per_seq;
+  if (entries < 0) return set_error(PKV_ERR_UNSUPPORTED, "%s: num_seqs > 2^31-1", fn);
+  if (entries > 0 && (!block_tables || !block_map))
+    return set_error(PKV_ERR_NULL, "%s: NULL block_tables/block_map", fn);
+  if ((num_moves > 0 && num_layers > 0) || entries > 0)
+    rc = copy_q8_pages(caches, num_layers, block_moves, num_tokens, num_moves, block_tables, entries, block_map, *desc,
+                       static_cast<cudaStream_t>(stream));
   if (!rc) clear_error();
   return rc;
 }

@@ -699,15 +699,16 @@ constexpr int kMaxRowQueries = 32, kMaxRows = 65535;  // of a sequence, of a cal
 
 // Whether the decode's rows are the shorter way, by the longest context: they read it once for each
 // query, spread over the GPU; the tiles read it once (and once more back), but the CTAs of one
-// (sequence, kv head) take its blocks of 128 keys one after another.  Block times as measured: 1.3 us
-// of a group's chunk; 1.5 us of a tile's block, 4 TB/s and two launches for the reading back.  (8
-// sequences of 5 queries over 100 to 2000 tokens: XXX us by rows, YYY by tiles.)
+// (sequence, kv head) take its blocks of 128 keys one after another.  Times as measured: 1.5 or 1.75
+// us of a group's chunk; 1.5 us of a tile's block, 4 TB/s and two launches for the reading back.
+// With 8 kv heads of 4 x 64: 8 sequences of 2 queries over 4000 tokens 21 us by rows, 69 by tiles, of
+// 8 queries 54 and 69, of 32 182 and 70; 64 of 8 over 500 60 and 57; one of 32 over 20000 107 and 218.
 bool rows_pay(int64_t num_queries, int32_t max_query_len, int32_t num_seqs, int32_t hq, const pkv_cache_desc &c,
               int32_t max_len, int sms) {
   if (max_query_len > kMaxRowQueries || num_queries > kMaxRows) return false;
   const double blocks = (max_len + 127) / 128, hkv = c.num_kv_heads;
   const double groups = c.head_dim == 64 ? 3 : 2, tokens = 2 * (128 / (hq / c.num_kv_heads));
-  const double rows = num_queries * hkv * blocks / (sms * groups) * 1.3 + 2;
+  const double rows = num_queries * hkv * blocks / (sms * groups) * (c.head_dim == 64 ? 1.5 : 1.75) + 2;
   const double ctas = (num_queries / tokens + num_seqs) * hkv;
   const double tiles = (ctas > sms ? ctas / sms : 1) * blocks * 1.5 + 8 + num_seqs * hkv * c.head_dim * max_len * 6. / 4e6;
   return rows < tiles;

@@ -316,3 +316,78 @@ def test_pages_past_4_gb(B):
     B.paged_decode_attention_q8(out, q, k, v, ks, vs, bt, cl, 300, 0.125)
     want, mag = R.attention(q, R.values(k, ks, table[0], 0, 300), R.values(v, vs, table[0], 0, 300), 0.125)
     assert bool(((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * mag).all())
+
+
+@pytest.mark.parametrize("dtype", R.KINDS)
+@pytest.mark.parametrize("layers,form", [(1, "one"), (3, "stacked"), (70, "list")])
+def test_pages_are_copied_with_their_scales(B, dtype, layers, form):
+    gen = torch.Generator().manual_seed(14)
+    pools = [R.pools(20, 2, 16, 64, dtype, gen, DEV) for _ in range(layers)]
+    want = [[t.clone() for t in p] for p in pools]
+    pairs = [(3, 10), (3, 11), (4, 12), (5, 5), (6, 13), (7, 14)]
+    rows = [16, 5, 0, 3, 1, 16]
+    for p in want:
+        for (s, t), n in zip(pairs, rows):
+            if s != t and n:
+                for codes, scale in ((p[0], p[2]), (p[1], p[3])):
+                    R.bits(codes)[t, :, :n] = R.bits(codes)[s, :, :n]
+                    scale[t] = scale[s]
+    given = [list(x) for x in zip(*pools)]
+    if form == "one":
+        args = [x[0] for x in given]
+    elif form == "stacked":
+        args = [torch.stack([R.bits(t) for t in x]).view(x[0].dtype) for x in given]
+    else:
+        args = given
+    bp = torch.tensor(pairs, dtype=torch.int32, device=DEV)
+    B.paged_kv_copy_blocks_q8(*args, bp, torch.tensor(rows, dtype=torch.int32, device=DEV))
+    for l in range(layers):
+        for i in range(4):
+            same(args[i] if form == "one" else args[i][l], want[l][i], f"layer {l}")
+    assert B.pkv_device_errors() == 0
+    # a compaction: two pages into free ones, the tables after them
+    table = torch.tensor([[3, 19, -1], [18, 4, 5]], dtype=torch.int32, device=DEV)
+    bmap = torch.arange(20, dtype=torch.int32, device=DEV)
+    bmap[19], bmap[18] = 0, 1
+    B.paged_kv_compact_q8(*args, torch.tensor([[19, 0], [18, 1]], dtype=torch.int32, device=DEV), table, bmap)
+    assert table.tolist() == [[3, 0, -1], [1, 4, 5]]
+    for l in range(layers):
+        for i in range(4):
+            x = args[i] if form == "one" else args[i][l]
+            want[l][i][0], want[l][i][1] = R.bits(want[l][i])[19].view(x.dtype), R.bits(want[l][i])[18].view(x.dtype)
+            same(x, want[l][i], f"layer {l}")
+    assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", R.KINDS)
+def test_forks_write_into_copies(B, dtype):
+    """The block manager's forks over an 8-bit cache: a prompt written, forked, each fork's next tokens
+    into its own copy of the last page; every sequence reads what writing it alone would give."""
+    n, hkv, d, bs, nb, steps = 37, 2, 64, 16, 40, 3
+    gen = torch.Generator().manual_seed(15)
+    k, v, ks, vs = R.pools(nb, hkv, bs, d, dtype, gen, DEV)
+    prompt = torch.randn(2, n, hkv, d, generator=gen).to(torch.bfloat16).to(DEV)
+    bm = B.BlockManager(nb, bs)
+    bm.add_sequence(0, n)
+    bt, cl = bm.block_tables([0], 5)
+    B.paged_kv_write_q8(prompt[0], prompt[1], k, v, ks, vs, bt.to(DEV), cl.to(DEV), starts([n]), n)
+    for child in (1, 2, 3):
+        bm.fork(0, child)
+    new = torch.randn(2, steps, 4, hkv, d, generator=gen).to(torch.bfloat16).to(DEV) * 2
+    for s in range(steps):
+        _, pairs, rows = bm.append_slots_cow(range(4))
+        if pairs.shape[0]:
+            B.paged_kv_copy_blocks_q8(k, v, ks, vs, pairs.to(DEV), rows.to(DEV))
+        bt, cl = bm.block_tables(list(range(4)), 5)
+        B.paged_kv_write_q8(new[0, s], new[1, s], k, v, ks, vs, bt.to(DEV), cl.to(DEV))
+    tables = bt.tolist()
+    for seq in range(4):
+        alone = [t.clone().zero_() if t.dtype is torch.float32 else torch.zeros_like(R.bits(t)).view(t.dtype)
+                 for t in (k, v, ks, vs)]
+        for i, (codes, scale, mine, my_scale) in enumerate(((alone[0], alone[2], k, ks), (alone[1], alone[3], v, vs))):
+            R.write(codes, scale, prompt[i], tables[seq], 0)
+            for s in range(steps):
+                R.write(codes, scale, new[i, s, seq][None], tables[seq], n + s)
+            got = R.values(mine, my_scale, tables[seq], 0, n + steps)
+            assert torch.equal(got, R.values(codes, scale, tables[seq], 0, n + steps)), f"sequence {seq}"
+    assert B.pkv_device_errors() == 0

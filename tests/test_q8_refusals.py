@@ -132,3 +132,19 @@ def test_the_binding_names_what_is_wrong(B):
         B.paged_decode_attention_q8(bf, bf, codes, codes, scale, scale, bt, cl, 16, 0.1)
     with pytest.raises(TypeError, match="int8"):
         B._q8_cache(-2, bf, bf, scale, scale, bt, cl)
+
+
+def test_copies(B):
+    one = (B.pkv_q8_cache * 2)(q8(B), q8(B, kind=1))
+
+    def call(caches=one, layers=2, pairs=FAKE, n=3, d=desc(B), tables=FAKE, seqs=2, bmap=FAKE, rows=FAKE):
+        return B.lib().paged_kv_compact_q8(ctypes.addressof(caches) if caches is not None else None, layers, pairs, rows, n,
+                                           tables, seqs, 4, bmap, ctypes.byref(d) if d else None, None)
+
+    assert call(caches=None) == -1 and call(d=None) == -1 and call(layers=-1) == -2 and call(n=-1) == -2 and call(seqs=-1) == -2
+    assert call(pairs=None) == -1 and call(tables=None) == -1 and call(bmap=None) == -1
+    assert call(pairs=ODD) == -5 and call(rows=ctypes.c_void_p((1 << 20) + 2)) == -5
+    assert call(d=desc(B, d=96)) == -3 and call(n=1 << 40) == -3
+    assert call(caches=(B.pkv_q8_cache * 2)(q8(B), q8(B, ks=None))) == -1
+    assert call(n=0, seqs=0) == 0 and call(layers=0, seqs=0) == 0
+    assert B.lib().paged_kv_copy_blocks_q8(ctypes.addressof(one), 2, FAKE, None, 0, ctypes.byref(desc(B)), None) == 0
