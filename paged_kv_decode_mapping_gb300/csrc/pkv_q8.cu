@@ -354,7 +354,6 @@ __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_con
 template <int D, int KIND, bool WHOLE>
 __global__ void __launch_bounds__(kQ8Threads) read_q8_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int V = D / 8;  // vectors of a row: 8 codes in, 8 bf16 out
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, group = 1 << a.log2_group, gt = tid & (group - 1);
   const int b = blockIdx.z;
   const bool is_v = blockIdx.y;
@@ -696,6 +695,7 @@ struct PrefillLayout {
   size_t k, v, k_unit, v_unit, total;
 };
 constexpr int kMaxRowQueries = 32, kMaxRows = 65535;  // of a sequence, of a call, as the decode's rows
+int64_t row_capacity(int32_t num_seqs) { return std::min((int64_t)num_seqs * kMaxRowQueries, (int64_t)kMaxRows); }
 
 // Whether the decode's rows are the shorter way, by the longest context: they read it once for each
 // query, spread over the GPU; the tiles read it once (and once more back), but the CTAs of one
@@ -705,7 +705,8 @@ constexpr int kMaxRowQueries = 32, kMaxRows = 65535;  // of a sequence, of a cal
 // 8 queries 54 and 69, of 32 182 and 70; 64 of 8 over 500 60 and 57; one of 32 over 20000 107 and 218.
 bool rows_pay(int64_t num_queries, int32_t max_query_len, int32_t num_seqs, int32_t hq, const pkv_cache_desc &c,
               int32_t max_len, int sms) {
-  if (max_query_len > kMaxRowQueries || num_queries > kMaxRows) return false;
+  // (packed rows that no sequence has count too: the workspace holds row_capacity of them)
+  if (max_query_len > kMaxRowQueries || num_queries > row_capacity(num_seqs)) return false;
   const double blocks = (max_len + 127) / 128, hkv = c.num_kv_heads;
   const double groups = c.head_dim == 64 ? 3 : 2, tokens = 2 * (128 / (hq / c.num_kv_heads));
   const double rows = num_queries * hkv * blocks / (sms * groups) * (c.head_dim == 64 ? 1.5 : 1.75) + 2;
@@ -725,7 +726,7 @@ bool prefill_layout(int32_t num_seqs, int32_t hkv, int32_t d, int32_t max_len, i
   p->k_unit = 2 * rows;
   p->v_unit = p->k_unit + units;
   p->total = std::max(p->v_unit + units,  // either way
-                      up(rows_q8_workspace(std::min((int64_t)num_seqs * kMaxRowQueries, (int64_t)kMaxRows), d, sms)));
+                      up(rows_q8_workspace((int32_t)row_capacity(num_seqs), d, sms)));
   return true;
 }
 
