@@ -121,6 +121,25 @@ def test_one_long_context(B, dtype, hq, hkv, d, bs, n):
     assert B.pkv_device_errors() == 0
 
 
+@pytest.mark.parametrize("dtype,d,share,cut", [
+    (torch.int8, 64, 10, 329), (torch.float8_e4m3fn, 64, 10, 489), (torch.int8, 128, 10, 325),
+])
+def test_a_share_of_two_long_contexts(B, dtype, d, share, cut):
+    """The first context (of 33 or 49 shares) ends in the share that the second begins in."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    groups = 3 if d == 64 else 2
+    lens = [(cut - 1) * 128, (share * groups * sms - cut - 1) * 128]
+    b = Batch(lens, dtype, 1, d, 128, seed=30)
+    q = b.randn(2, 1, d)
+    ws = torch.zeros(B.paged_decode_q8_workspace_size(2, 1, 1, d, max(lens)), dtype=torch.uint8, device=DEV)
+    outs = [decode(B, b, q, 2 * d ** -0.5, workspace=ws) for _ in range(40)]
+    check(outs[0], *decode_ref(b, q, 2 * d ** -0.5))
+    for o in outs[1:]:
+        same(o, outs[0], "the same bits every time")
+    assert not ws[:8192].any()
+    assert B.pkv_device_errors() == 0
+
+
 @pytest.mark.parametrize("dtype", R.KINDS)
 @pytest.mark.parametrize("d", [64, 128])
 def test_scales_far_apart(B, dtype, d):
@@ -376,6 +395,28 @@ def test_prefill_leaves_rows_of_no_sequence(B):
                 want, mag = R.attention(q[lo:lo + n], k, v, 0.1, seen)
                 check_prefill(out[lo:lo + n], q[lo:lo + n], k, want, mag, 0.1)
         assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("seqs,rows", [(1, 3000), (3, 97)])
+def test_prefill_of_a_padded_batch(B, seqs, rows):
+    """More packed rows than the sequences could have: the others stay, and so does what lies behind the
+    workspace."""
+    lens, hq, hkv, d = [40, 9, 300][:seqs], 2, 1, 64
+    b = Batch(lens, torch.int8, hkv, d, 16, seed=31)
+    q = b.randn(rows, hq, d)
+    start = starts([4] * seqs)
+    size = B.paged_prefill_q8_workspace_size(seqs, hkv, d, 16, max(lens))
+    ws = torch.full((size + (1 << 16),), 7, dtype=torch.uint8, device=DEV)
+    out = torch.full_like(q, 77.0)
+    B.paged_prefill_attention_q8(out, q, *b.cache(), b.bt, b.cl, max(lens), start, 4, d ** -0.5, workspace=ws[:size])
+    assert (out[4 * seqs:] == 77).all() and (ws[size:] == 7).all()
+    for s, n in enumerate(lens):
+        k, v = (R.values(c, sc, b.tables[s], 0, n, torch.float64) for c, sc in ((b.k, b.ks), (b.v, b.vs)))
+        for i in range(4):
+            at = n - 3 + i
+            want, mag = R.attention(q[4 * s + i:4 * s + i + 1], k[:at], v[:at], d ** -0.5)
+            check(out[4 * s + i:4 * s + i + 1], want, mag, f"sequence {s}, query {i}")
+    assert B.pkv_device_errors() == 0
 
 
 def test_streams_and_graphs(B):
