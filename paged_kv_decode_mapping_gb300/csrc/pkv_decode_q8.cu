@@ -25,7 +25,7 @@
 //    was 46 (256 contexts of 16 to 8192 tokens).
 // What bounds it: int8, the consumers' issue slots (a code pair takes 1.5 instructions to widen); e4m3
 // of 128, HBM; short batches, the start: 2.5 us until the first box is asked for and 2 for it to come.
-// Measured (one GPU of 152 SMs; a plain copy runs at 6.8 TB/s): 64 contexts of 100 to 8192 keys, 8 kv
+// Measured (one GPU of 152 SMs; a plain copy runs at 6.8 TB/s): 64 contexts of 128 to 4096 keys, 8 kv
 // heads of 128 e4m3 48.6 us, 5.8 TB/s; 256 of 16 to 8192, 4 of 64 int8 41.4 us, 4.7 TB/s; 4 of 32768, 8
 // of 128 int8 47.2 us, 5.7 TB/s; 16 of 2048, 8 of 64 e4m3 14.0 us; one of 128, 8 of 64 5.5 us.
 #include <cuda.h>
@@ -635,12 +635,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
-// n / d for n >= 0, d > 0, by 32 bits where that is enough (a 64-bit division takes 0.2 us).
-__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
-  if (((n | d) >> 32) == 0) return (uint32_t)n / (uint32_t)d;
-  return n / d;
-}
-
 __device__ __forceinline__ void cp_async4(uint32_t dst, const float *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -678,7 +672,7 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
   auto length = [&](int b) { return min(max(__ldg(a.lens + b), 0), cap); };
   auto chunks_of = [](int L) { return (int)(((int64_t)L + kQ8Keys - 1) / kQ8Keys); };
   auto cost_of = [&](int L) { return L > 0 ? kChunkCost * (int64_t)chunks_of(L) + kEndCost : 0; };  // of a kv head
-  auto shares_of = [&](int64_t w) { return min((int64_t)gridDim.x * GROUPS, max((int64_t)1, quotient(w, kMinCost))); };
+  auto shares_of = [&](int64_t w) { return min((int64_t)gridDim.x * GROUPS, max((int64_t)1, q8::quotient(w, kMinCost))); };
   // Shares 0 .. gridDim.x - 1 are the CTAs' first groups', so that a few lie on SMs of their own.
   const int share = grp * (int)gridDim.x + (int)blockIdx.x;
   // Entries of the block table, one a lane.
@@ -698,8 +692,8 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
     }
     const int64_t n = cost_of(cap), all = n * Hkv * a.num_seqs, shares = shares_of(all);
     if (share < shares && all > 0) {
-      const int64_t at = quotient(all * share, shares), unit = quotient(at, n);
-      guess_b = (int)quotient(unit, Hkv);
+      const int64_t at = q8::quotient(all * share, shares), unit = q8::quotient(at, n);
+      guess_b = (int)q8::quotient(unit, Hkv);
       guess_win = (int)((at - unit * n + kChunkCost - 1) / kChunkCost) * kQ8Keys >> a.log2_bs;
       guess_tb = entries(guess_b, guess_win);
     }
@@ -741,7 +735,7 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
   for (int w = 0; w < WARPS; ++w) total += s_sums[w];
   const int64_t W = total * Hkv, N = shares_of(W);
   if (W == 0 || share >= N) return;  // (no barrier of the whole CTA follows)
-  const int64_t lo = quotient(W * share, N), hi = quotient(W * (share + 1), N);
+  const int64_t lo = q8::quotient(W * share, N), hi = q8::quotient(W * (share + 1), N);
   auto timeout = [&] {
     if (lane == 0) {
       raise_error(PKV_DEVERR_TIMEOUT);
@@ -784,7 +778,7 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
     }
     int64_t cost = max(__shfl_sync(0xffffffffu, n, at_lane), (int64_t)1);  // of a kv head of sequence b
     int nch = (int)max((cost - kEndCost) / kChunkCost, (int64_t)1), L = length(b);
-    int g = (int)quotient(lo - at * Hkv, cost);
+    int g = (int)q8::quotient(lo - at * Hkv, cost);
     int64_t u0 = at * Hkv + g * cost;  // where the kv head begins in the list
     int c = (int)((lo - u0 + kChunkCost - 1) / kChunkCost);
     // Table entries are loaded ahead of their use: the current window of 32, the one after it, the
@@ -829,8 +823,8 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
         dsc.share0 = share;
         dsc.parts = 1;
         if (u0 < lo || end >= hi) {  // cut: place x is in share floor(((x + 1) N - 1) / W)
-          dsc.share0 = (int)quotient((u0 + 1) * N - 1, W);
-          dsc.parts = (int)quotient((end + 1) * N - 1, W) - dsc.share0 + 1;
+          dsc.share0 = (int)q8::quotient((u0 + 1) * N - 1, W);
+          dsc.parts = (int)q8::quotient((end + 1) * N - 1, W) - dsc.share0 + 1;
           dsc.slot = 2 * share + (dsc.share0 == share ? 1 : 0);
         }
       }

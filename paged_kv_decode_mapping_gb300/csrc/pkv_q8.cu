@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_device.cuh"
 #include "q8_device.cuh"
@@ -18,9 +19,9 @@
 namespace pkv {
 namespace {
 
-constexpr int kQ8Threads = 256;
-constexpr int kQ8Unroll = 8;    // 16-byte vectors of new rows a thread keeps in registers
-constexpr int kReadUnroll = 8;  // loads a thread has in flight, reading back
+constexpr int kQ8Threads = 128;   // of a CTA; of a write's twice as many where its pages are large
+constexpr int64_t kReadWide = 1 << 20;
+constexpr int kRotateHeads = 4;  // q heads a thread rotates with one position's cosines and sines
 
 // What names the tokens of a call: sequence b's newest n of context_lens[b], its rows in the
 // packed tensors from row0 on.
@@ -67,51 +68,67 @@ __device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
   f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
 }
 
-// Vector c (coordinates 8c .. 8c+7) of the row at `row`, rotated; cs: the position's cosines and
-// sines.  Coordinates at or past r stay as they are.
-__device__ __forceinline__ uint4 rotated(const uint4 *row, int c, const float *cs, const Rope &p) {
-  const uint4 x = row[c];  // (not a read-only load: q may be rotated in place)
-  if (8 * c >= p.r) return x;
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t o[4];
-  if (p.neox) {  // pairs (e, e + r/2): the partners are vector c +- r/16
-    const int half = p.r / 16;
-    const bool lo = c < half;
-    const int e = lo ? c : c - half;
-    const uint4 y = row[lo ? c + half : c - half];
-    const uint32_t v[4] = {y.x, y.y, y.z, y.w};
-    float cc[8], ss[8];
-    load8(cs + 8 * e, cc);
-    load8(cs + p.r / 2 + 8 * e, ss);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float f[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float own = __fmul_rn(k ? dev::bf16hi_to_f32(w[j]) : dev::bf16lo_to_f32(w[j]), cc[2 * j + k]);
-        const float other = __fmul_rn(k ? dev::bf16hi_to_f32(v[j]) : dev::bf16lo_to_f32(v[j]), ss[2 * j + k]);
-        f[k] = lo ? __fsub_rn(own, other) : __fadd_rn(own, other);
-      }
-      o[j] = dev::pack_bf16x2(f[0], f[1]);
-    }
-  } else {  // pairs (2i, 2i + 1): word j holds pair 4c + j
+// The cosines and sines of vector c (coordinates 8c .. 8c+7, below r), of the position's row cs.
+struct Angles {
+  float c[8], s[8];  // neox: of the vector's pairs (e, e + r/2); else of its 4 pairs (2i, 2i + 1)
+};
+__device__ __forceinline__ Angles angles_of(const float *cs, int c, const Rope &p) {
+  Angles a;
+  if (p.neox) {
+    const int e = c < p.r / 16 ? c : c - p.r / 16;
+    load8(cs + 8 * e, a.c);
+    load8(cs + p.r / 2 + 8 * e, a.s);
+  } else {
     const float4 c4 = __ldg(reinterpret_cast<const float4 *>(cs + 4 * c));
     const float4 s4 = __ldg(reinterpret_cast<const float4 *>(cs + p.r / 2 + 4 * c));
-    const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
+    a.c[0] = c4.x, a.c[1] = c4.y, a.c[2] = c4.z, a.c[3] = c4.w;
+    a.s[0] = s4.x, a.s[1] = s4.y, a.s[2] = s4.z, a.s[3] = s4.w;
+  }
+  return a;
+}
+// neox: x rotated, y being the partners' vector; lo: x holds the pairs' first coordinates.
+__device__ __forceinline__ uint4 rotate_neox(const uint4 &x, const uint4 &y, const Angles &a, bool lo) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+  uint32_t o[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a = dev::bf16lo_to_f32(w[j]), b = dev::bf16hi_to_f32(w[j]);
-      o[j] = dev::pack_bf16x2(__fsub_rn(__fmul_rn(a, cc[j]), __fmul_rn(b, ss[j])),
-                              __fadd_rn(__fmul_rn(b, cc[j]), __fmul_rn(a, ss[j])));
+  for (int j = 0; j < 4; ++j) {
+    float f[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float own = __fmul_rn(k ? dev::bf16hi_to_f32(w[j]) : dev::bf16lo_to_f32(w[j]), a.c[2 * j + k]);
+      const float other = __fmul_rn(k ? dev::bf16hi_to_f32(v[j]) : dev::bf16lo_to_f32(v[j]), a.s[2 * j + k]);
+      f[k] = lo ? __fsub_rn(own, other) : __fadd_rn(own, other);
     }
+    o[j] = dev::pack_bf16x2(f[0], f[1]);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ uint4 rotate_pairs(const uint4 &x, const Angles &a) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float e = dev::bf16lo_to_f32(w[j]), f = dev::bf16hi_to_f32(w[j]);
+    o[j] = dev::pack_bf16x2(__fsub_rn(__fmul_rn(e, a.c[j]), __fmul_rn(f, a.s[j])),
+                            __fadd_rn(__fmul_rn(f, a.c[j]), __fmul_rn(e, a.s[j])));
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// Vector c of the row at `row`, rotated; cs: the position's cosines and sines.  Coordinates at or
+// past r stay as they are.
+__device__ __forceinline__ uint4 rotated(const uint4 *row, int c, const float *cs, const Rope &p) {
+  const uint4 x = __ldg(row + c);
+  if (8 * c >= p.r) return x;
+  const Angles a = angles_of(cs, c, p);
+  if (!p.neox) return rotate_pairs(x, a);
+  const int half = p.r / 16;
+  return rotate_neox(x, __ldg(row + (c < half ? c + half : c - half)), a, c < half);
 }
 
 // ---------------------------------------------------------------------------
 // The write.  One group of 2^log2_group threads (a warp to the whole CTA) per (sequence, touched
 // page, K or V, kv head): it holds the page's new rows in registers between finding their largest
-// value and rounding them; what does not fit in 8 vectors a thread is read a second time.
+// value and rounding them, U 16-byte vectors a thread; what does not fit is read a second time.
 
 struct WriteArgs {
   Span s;
@@ -126,7 +143,7 @@ struct WriteArgs {
   const uint4 *q;
   uint4 *q_out;
   int64_t q_stride, q_out_stride;
-  int32_t num_q_heads, q_ctas;  // CTAs per sequence that rotate its q rows
+  int32_t num_q_heads, q_ctas;  // CTAs (of both halves) per sequence that rotate its q rows
 };
 
 __device__ __forceinline__ uint32_t absmax(uint32_t m, const uint4 &x) {
@@ -138,35 +155,48 @@ __device__ __forceinline__ uint32_t absmax(uint32_t m, const uint4 &x) {
 }
 
 // The q rows of one sequence: a thread owns a rotation's whole unit (both partner vectors), so
-// that q_out may be q.
+// that q_out may be q, of kRotateHeads heads.
 template <int D>
 __device__ __forceinline__ void rotate_q(const WriteArgs &a, const Tokens &t, uint32_t part) {
   const int half = a.rope.neox ? a.rope.r / 16 : 0;
   const int units = D / 8 - half;  // of a row
-  const int64_t n = (int64_t)(t.end - t.begin) * a.num_q_heads * units;
-  for (int64_t i = (int64_t)part * kQ8Threads + threadIdx.x; i < n; i += (int64_t)a.q_ctas * kQ8Threads) {
-    const int64_t row = i / units;
-    int c = (int)(i - row * units);
+  const int runs = (a.num_q_heads + kRotateHeads - 1) / kRotateHeads;
+  const int64_t n = (int64_t)(t.end - t.begin) * runs * units;
+  for (int64_t i = (int64_t)part * blockDim.x + threadIdx.x; i < n; i += (int64_t)a.q_ctas * blockDim.x) {
+    const int64_t run = q8::quotient(i, units), tok = q8::quotient(run, runs);
+    int c = (int)(i - run * units);
     if (c >= half) c += half;  // vectors half .. 2 half - 1 belong to their partners
-    const int64_t tok = row / a.num_q_heads;
-    const int h = (int)(row - tok * a.num_q_heads);
+    const int h0 = (int)(run - tok * runs) * kRotateHeads, heads = min(a.num_q_heads - h0, kRotateHeads);
     const int64_t at = t.row0 + tok;
     const int64_t pos = a.rope.positions ? __ldg(a.rope.positions + at) : t.begin + tok;
     if (pos < 0 || pos >= a.rope.max_position) continue;  // reported by the k rows
-    const float *cs = a.rope.cos_sin + pos * a.rope.r;
-    const uint4 *src = a.q + at * a.q_stride + h * (D / 8);
-    uint4 *dst = a.q_out + at * a.q_out_stride + h * (D / 8);
-    const uint4 y0 = rotated(src, c, cs, a.rope);
-    if (c < half) {
-      const uint4 y1 = rotated(src, c + half, cs, a.rope);
-      dst[c + half] = y1;
-    }
-    dst[c] = y0;
+    const uint4 *const src = a.q + at * a.q_stride + h0 * (D / 8) + c;
+    uint4 *const dst = a.q_out + at * a.q_out_stride + h0 * (D / 8) + c;
+    const bool turns = 8 * c < a.rope.r, two = c < half;
+    Angles ang = {};
+    if (turns) ang = angles_of(a.rope.cos_sin + pos * a.rope.r, c, a.rope);
+    uint4 x[kRotateHeads], y[kRotateHeads];
+#pragma unroll
+    for (int h = 0; h < kRotateHeads; ++h)
+      if (h < heads) {
+        x[h] = src[h * (D / 8)];  // (not a read-only load: q may be rotated in place)
+        if (two) y[h] = src[h * (D / 8) + half];
+      }
+#pragma unroll
+    for (int h = 0; h < kRotateHeads; ++h)
+      if (h < heads) {
+        if (two) {
+          dst[h * (D / 8)] = rotate_neox(x[h], y[h], ang, true);
+          dst[h * (D / 8) + half] = rotate_neox(y[h], x[h], ang, false);
+        } else {
+          dst[h * (D / 8)] = turns ? rotate_pairs(x[h], ang) : x[h];
+        }
+      }
   }
 }
 
-template <int D, int KIND, bool ROPE>
-__global__ void __launch_bounds__(kQ8Threads, ROPE ? 2 : 4) write_q8_kernel(const __grid_constant__ WriteArgs a) {
+template <int D, int KIND, bool ROPE, int U>
+__global__ void __launch_bounds__(2 * kQ8Threads, ROPE ? 2 : 4) write_q8_kernel(const __grid_constant__ WriteArgs a) {
   constexpr int V = D / 8;  // vectors of a row: 8 bf16 in, 8 codes out
   // A decode kernel behind this one may start its set-up (paged_decode_step_q8).
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -176,13 +206,13 @@ __global__ void __launch_bounds__(kQ8Threads, ROPE ? 2 : 4) write_q8_kernel(cons
   const Tokens t = tokens_of(a.s, b, &bad);
   if constexpr (ROPE) {
     if (blockIdx.x >= a.item_ctas) {
-      if (!is_v) rotate_q<D>(a, t, blockIdx.x - a.item_ctas);
+      rotate_q<D>(a, t, 2 * (blockIdx.x - a.item_ctas) + blockIdx.y);
       return;
     }
   }
-  __shared__ uint32_t s_max[kQ8Threads / 32];
+  __shared__ uint32_t s_max[2 * kQ8Threads / 32];
   const int tid = threadIdx.x, group = 1 << a.log2_group, gt = tid & (group - 1);
-  const uint32_t item = blockIdx.x * (kQ8Threads >> a.log2_group) + (tid >> a.log2_group);
+  const uint32_t item = blockIdx.x * (blockDim.x >> a.log2_group) + (tid >> a.log2_group);
   const int j = (int)(item / (uint32_t)a.s.num_kv_heads), h = (int)(item - (uint32_t)j * a.s.num_kv_heads);
   bool live = j < a.pages;
   if (bad) {
@@ -191,7 +221,7 @@ __global__ void __launch_bounds__(kQ8Threads, ROPE ? 2 : 4) write_q8_kernel(cons
   }
   {  // the CTA's first group is the one of the earliest page
     const int64_t earliest = (t.begin >> a.s.log2_bs) +
-                             (blockIdx.x * (kQ8Threads >> a.log2_group)) / (uint32_t)a.s.num_kv_heads;
+                             (blockIdx.x * (blockDim.x >> a.log2_group)) / (uint32_t)a.s.num_kv_heads;
     if (t.begin == t.end || earliest << a.s.log2_bs >= t.end) return;
   }
   const int page = (t.begin >> a.s.log2_bs) + j;
@@ -232,18 +262,18 @@ __global__ void __launch_bounds__(kQ8Threads, ROPE ? 2 : 4) write_q8_kernel(cons
     }
     return __ldg(row + c);
   };
-  uint4 x[kQ8Unroll];
+  uint4 x[U];
   uint32_t m = 0, skip = 0;
 #pragma unroll
-  for (int u = 0; u < kQ8Unroll; ++u) {
+  for (int u = 0; u < U; ++u) {
     x[u] = make_uint4(0, 0, 0, 0);
     bool none = true;
     if (first + u * rows_apart < count) x[u] = fetch(u, &none);
     if (ROPE && none) skip |= 1u << u;
   }
 #pragma unroll
-  for (int u = 0; u < kQ8Unroll; ++u) m = absmax(m, x[u]);
-  for (int u = kQ8Unroll; first + u * rows_apart < count; ++u) {
+  for (int u = 0; u < U; ++u) m = absmax(m, x[u]);
+  for (int u = U; first + u * rows_apart < count; ++u) {
     bool none;
     m = absmax(m, fetch(u, &none));
   }
@@ -269,9 +299,9 @@ __global__ void __launch_bounds__(kQ8Threads, ROPE ? 2 : 4) write_q8_kernel(cons
   const q8::Inverse by = q8::inverse_of(to == 0.f ? 1.f : to);
   uint2 *const dst = reinterpret_cast<uint2 *>(rows + (int64_t)(r0 + first) * D) + c;
 #pragma unroll
-  for (int u = 0; u < kQ8Unroll; ++u)
+  for (int u = 0; u < U; ++u)
     if (ROPE ? !(skip >> u & 1u) : first + u * rows_apart < count) dst[u * rows_apart * V] = q8::encode8<KIND>(x[u], by);
-  for (int u = kQ8Unroll; first + u * rows_apart < count; ++u) {
+  for (int u = U; first + u * rows_apart < count; ++u) {
     bool none;
     const uint4 v = fetch(u, &none);
     if (!none) dst[u * rows_apart * V] = q8::encode8<KIND>(v, by);
@@ -307,7 +337,9 @@ struct ReadArgs {
   int64_t k_stride, v_stride;  // packed rows: vectors from one token to the next
   int32_t out_rows;            // whole contexts in fp16; 0: bf16 rows of the newest tokens
   const float *k_unit, *v_unit;
-  int32_t pages, log2_group;
+  int32_t pages;
+  int32_t log2_heads, runs;    // kv heads of an item: a power of two; items of a page
+  int32_t log2_group;
 };
 
 // The units: the largest scale of each (sequence, kv head)'s pages.  One CTA per sequence; thread
@@ -320,6 +352,7 @@ struct UnitArgs {
 constexpr int kUnitThreads = 1024;
 __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_constant__ UnitArgs a) {
   __shared__ float s_k[kUnitThreads], s_v[kUnitThreads];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int b = blockIdx.x, H = a.s.num_kv_heads, tid = threadIdx.x;
   const int cap = (int)min((int64_t)a.s.max_blocks * a.s.block_size, (int64_t)a.s.max_new);
   const int L = min(max(__ldg(a.s.lens + b), 0), cap), pages = (L + a.s.block_size - 1) >> a.s.log2_bs;
@@ -351,15 +384,19 @@ __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_con
   }
 }
 
-template <int D, int KIND, bool WHOLE>
-__global__ void __launch_bounds__(kQ8Threads) read_q8_kernel(const __grid_constant__ ReadArgs a) {
+template <int D, int KIND, bool WHOLE, int U>
+__global__ void __launch_bounds__(kQ8Threads, 5) read_q8_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int V = D / 8;  // vectors of a row: 8 codes in, 8 bf16 out
-  const int tid = threadIdx.x, group = 1 << a.log2_group, gt = tid & (group - 1);
+  if constexpr (WHOLE) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the units
+  }
+  const int tid = threadIdx.x, lane = tid & 31, group = 1 << a.log2_group, gt = tid & (group - 1);
   const int b = blockIdx.z;
   const bool is_v = blockIdx.y;
   const uint32_t item = blockIdx.x * (kQ8Threads >> a.log2_group) + (tid >> a.log2_group);
-  const int j = (int)(item / (uint32_t)a.s.num_kv_heads), h = (int)(item - (uint32_t)j * a.s.num_kv_heads);
-  if (j >= a.pages) return;
+  const int j = (int)(item / (uint32_t)a.runs), h0 = (int)(item - (uint32_t)j * a.runs) << a.log2_heads;
+  if (j >= a.pages) return;  // (whole warps, here and below)
   Tokens t;
   if constexpr (WHOLE) {  // lengths past the tables are cut, as the attention does
     const int cap = (int)min((int64_t)a.s.max_blocks * a.s.block_size, (int64_t)a.s.max_new);
@@ -382,53 +419,92 @@ __global__ void __launch_bounds__(kQ8Threads) read_q8_kernel(const __grid_consta
     if (gt == 0) raise_error(PKV_DEVERR_BLOCK_ID);
     from = 0;
   }
-  const int64_t unit = from * a.s.num_kv_heads + h;
-  float scale = __ldg((is_v ? a.v_scale : a.k_scale) + unit);
-  if constexpr (WHOLE) {
-    const float of = __ldg((is_v ? a.v_unit : a.k_unit) + (int64_t)b * a.s.num_kv_heads + h);
-    scale = of > 0.f ? __fdiv_rn(scale, of) : scale * 0.f;  // (a NaN stays)
+  const int heads = min(1 << a.log2_heads, a.s.num_kv_heads - h0);
+  const int64_t unit = from * a.s.num_kv_heads + h0;
+  float scale = 0.f;  // lane l: head h0 + l's
+  if (lane < heads) {
+    scale = __ldg((is_v ? a.v_scale : a.k_scale) + unit + lane);
+    if constexpr (WHOLE) {
+      const float of = (is_v ? a.v_unit : a.k_unit)[(int64_t)b * a.s.num_kv_heads + h0 + lane];
+      scale = of > 0.f ? __fdiv_rn(scale, of) : scale * 0.f;  // (a NaN stays)
+    }
   }
-  const uint64_t scale2 = q8::f32x2(scale, scale);
-  const uint2 *src =
-      reinterpret_cast<const uint2 *>((is_v ? a.v_cache : a.k_cache) + unit * a.s.block_size * D) + r0 * V;
+  const uint2 *const src = reinterpret_cast<const uint2 *>((is_v ? a.v_cache : a.k_cache) + unit * a.s.block_size * D) + gt % V;
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
-  uint4 *dst = (is_v ? a.v_out : a.k_out) + (t.row0 + (lo + r0 - t.begin)) * stride + h * V;
-  // A thread's vectors are one column of every (group / V)-th row.
-  const int rows_apart = group / V, first = gt / V, count = r1 - r0;
-  src += first * V + gt % V;
-  dst += first * stride + gt % V;
-  const int src_step = rows_apart * V;
-  const int64_t dst_step = rows_apart * stride;
-  for (int r = first; r < count; r += kReadUnroll * rows_apart) {
-    uint2 x[kReadUnroll];
+  uint4 *const dst = (is_v ? a.v_out : a.k_out) + (t.row0 + lo - t.begin) * stride + h0 * V + gt % V;
+  // The heads' pages are one run of rows; a thread's vectors are one column of every (group / V)-th.
+  const int rows_apart = group / V, rows = heads << a.s.log2_bs;
+  auto run = [&](auto whole, int r) {  // whole: every row of them is wanted
+    constexpr bool kAll = decltype(whole)::value;
+    uint2 x[U];
 #pragma unroll
-    for (int u = 0; u < kReadUnroll; ++u)
-      if (r + u * rows_apart < count) x[u] = __ldcs(src + u * src_step);
+    for (int u = 0; u < U; ++u) {
+      const int at = r + u * rows_apart, in = at & (a.s.block_size - 1);
+      if (kAll || (at < rows && in >= r0 && in < r1)) x[u] = __ldcs(src + at * V);
+    }
 #pragma unroll
-    for (int u = 0; u < kReadUnroll; ++u) {
-      if (r + u * rows_apart >= count) break;
+    for (int u = 0; u < U; ++u) {
+      const int at = r + u * rows_apart, in = at & (a.s.block_size - 1), h = at >> a.s.log2_bs;
+      const float s = __shfl_sync(0xffffffffu, scale, h & 31);  // (a warp's rows are of one head)
+      if (!kAll && (at >= rows || in < r0 || in >= r1)) continue;
+      const uint64_t s2 = q8::f32x2(s, s);
       const uint32_t w[2] = {x[u].x, x[u].y};
       uint32_t o[4];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint32_t z = q8::prep<KIND>(w[k]);
         const float2 f = q8::f16x2_to_f32(q8::pair<KIND, 0>(z)), g = q8::f16x2_to_f32(q8::pair<KIND, 1>(z));
-        const float2 p = q8::split(q8::mul2(q8::f32x2(f.x, f.y), scale2));
-        const float2 q = q8::split(q8::mul2(q8::f32x2(g.x, g.y), scale2));
+        const float2 p = q8::split(q8::mul2(q8::f32x2(f.x, f.y), s2));
+        const float2 q = q8::split(q8::mul2(q8::f32x2(g.x, g.y), s2));
         o[2 * k] = WHOLE ? q8::pack_f16x2(p.x, p.y) : dev::pack_bf16x2(p.x, p.y);
         o[2 * k + 1] = WHOLE ? q8::pack_f16x2(q.x, q.y) : dev::pack_bf16x2(q.x, q.y);
       }
-      *dst = make_uint4(o[0], o[1], o[2], o[3]);
-      dst += dst_step;
+      uint4 *const to = dst + in * stride + h * V;
+      if (WHOLE)  // (the tiles read it next)
+        *to = make_uint4(o[0], o[1], o[2], o[3]);
+      else
+        __stcs(to, make_uint4(o[0], o[1], o[2], o[3]));
     }
-    src += kReadUnroll * src_step;
+  };
+  for (int r = gt / V; r < rows; r += U * rows_apart) {
+    if (r1 - r0 == a.s.block_size && r - gt / V + U * rows_apart <= rows)
+      run(std::true_type{}, r);
+    else
+      run(std::false_type{}, r);
   }
 }
 
-int log2_group_of(int64_t vectors, int per_thread) {  // of one item's threads: a warp to a CTA
+int log2_group_of(int64_t vectors, int per_thread, int threads) {  // of one item's threads: a warp to a CTA
   int r = 5;
-  while (r < 8 && ((int64_t)per_thread << r) < vectors) ++r;
+  while (r < ilog2(threads) && ((int64_t)per_thread << r) < vectors) ++r;
   return r;
+}
+
+// pick(head_dim, kind), with both as constants.
+template <typename F>
+auto of_kinds(int32_t d, int32_t kind, F pick) {
+  using std::integral_constant;
+  constexpr integral_constant<int, 64> d64{};
+  constexpr integral_constant<int, 128> d128{};
+  constexpr integral_constant<int, PKV_Q8_INT8> i8{};
+  constexpr integral_constant<int, PKV_Q8_E4M3> e4{};
+  if (d == 64) return kind == PKV_Q8_INT8 ? pick(d64, i8) : pick(d64, e4);
+  return kind == PKV_Q8_INT8 ? pick(d128, i8) : pick(d128, e4);
+}
+
+// early: the kernel may start before the one ahead of it in the stream has ended (it waits for that itself).
+template <typename A>
+void launch_dependent(void (*kern)(const A), dim3 ctas, int threads, const A &a, bool early, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = ctas;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = early ? 1 : 0;
+  (void)cudaLaunchKernelEx(&cfg, kern, a);  // (the caller asks for the error)
 }
 
 // Pages that `n` consecutive tokens touch, at most.
@@ -487,7 +563,7 @@ int check_span(const void *x, const void *y, int64_t x_stride, int64_t y_stride,
 int launch_read(const Span &s, const pkv_q8_cache &q, const pkv_cache_desc &c, void *k_out, void *v_out,
                 int64_t k_stride, int64_t v_stride, int32_t out_rows, const float *k_unit, const float *v_unit,
                 int64_t pages, cudaStream_t stream) {
-  ReadArgs a;
+  ReadArgs a = {};
   a.s = s;
   a.k_cache = static_cast<const uint8_t *>(q.k_cache);
   a.v_cache = static_cast<const uint8_t *>(q.v_cache);
@@ -501,20 +577,23 @@ int launch_read(const Span &s, const pkv_q8_cache &q, const pkv_cache_desc &c, v
   a.k_unit = k_unit;
   a.v_unit = v_unit;
   a.pages = (int32_t)pages;
-  a.log2_group = log2_group_of((int64_t)std::min(s.block_size, s.max_new) * c.head_dim / 8, kReadUnroll);
+  // 16 vectors a thread, of several heads where a page of one has fewer; 4 where the call is too short for
+  // that to fill the GPU (FIGR).
+  const int64_t page_vecs = (int64_t)s.block_size * c.head_dim / 8;
+  const bool wide = pages * s.num_seqs * 2 * c.num_kv_heads * page_vecs >= kReadWide;
+  const int per_thread = wide ? 16 : 4;
+  while ((page_vecs << (a.log2_heads + 1)) <= 32 * per_thread && (1 << a.log2_heads) < c.num_kv_heads) ++a.log2_heads;
+  a.runs = (c.num_kv_heads + (1 << a.log2_heads) - 1) >> a.log2_heads;
+  a.log2_group = log2_group_of(page_vecs << a.log2_heads, per_thread, kQ8Threads);
   const int per = kQ8Threads >> a.log2_group;
-  const dim3 ctas((unsigned)((pages * c.num_kv_heads + per - 1) / per), 2, (unsigned)s.num_seqs);
-  const bool i8 = q.kind == PKV_Q8_INT8;
-  void (*kern)(const ReadArgs);
-  if (out_rows)
-    kern = c.head_dim == 64
-               ? (i8 ? read_q8_kernel<64, PKV_Q8_INT8, true> : read_q8_kernel<64, PKV_Q8_E4M3, true>)
-               : (i8 ? read_q8_kernel<128, PKV_Q8_INT8, true> : read_q8_kernel<128, PKV_Q8_E4M3, true>);
-  else
-    kern = c.head_dim == 64
-               ? (i8 ? read_q8_kernel<64, PKV_Q8_INT8, false> : read_q8_kernel<64, PKV_Q8_E4M3, false>)
-               : (i8 ? read_q8_kernel<128, PKV_Q8_INT8, false> : read_q8_kernel<128, PKV_Q8_E4M3, false>);
-  kern<<<ctas, kQ8Threads, 0, stream>>>(a);
+  const dim3 ctas((unsigned)((pages * a.runs + per - 1) / per), 2, (unsigned)s.num_seqs);
+  auto pick = [&](auto d, auto kind) -> void (*)(const ReadArgs) {
+    if (out_rows)
+      return wide ? read_q8_kernel<d(), kind(), true, 16> : read_q8_kernel<d(), kind(), true, 4>;
+    return wide ? read_q8_kernel<d(), kind(), false, 16> : read_q8_kernel<d(), kind(), false, 4>;
+  };
+  void (*const kern)(const ReadArgs) = of_kinds(c.head_dim, q.kind, pick);
+  launch_dependent(kern, ctas, kQ8Threads, a, out_rows > 0, stream);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_error(e, "read_q8_kernel launch");
   return PKV_OK;
@@ -582,8 +661,11 @@ int launch_write_q8(const WriteQ8 &w, cudaStream_t stream) {
   a.k_scale = w.cache->k_scale;
   a.v_scale = w.cache->v_scale;
   a.pages = (int32_t)std::min<int64_t>(touched(w.max_query_len, c.block_size), w.max_blocks);
-  a.log2_group = log2_group_of((int64_t)std::min(c.block_size, w.max_query_len) * c.head_dim / 8, kQ8Unroll);
-  const int per = kQ8Threads >> a.log2_group;
+  const int64_t vecs = (int64_t)std::min(c.block_size, w.max_query_len) * c.head_dim / 8;  // of an item
+  const int per_thread = vecs <= 32 ? 1 : vecs <= 128 ? 4 : 8;
+  const int threads = vecs > 8 * kQ8Threads ? 2 * kQ8Threads : kQ8Threads;
+  a.log2_group = log2_group_of(vecs, per_thread, threads);
+  const int per = threads >> a.log2_group;
   a.item_ctas = (uint32_t)(((int64_t)a.pages * c.num_kv_heads + per - 1) / per);
   uint32_t ctas = a.item_ctas;
   if (w.rope) {
@@ -598,22 +680,24 @@ int launch_write_q8(const WriteQ8 &w, cudaStream_t stream) {
       a.q_stride = w.q_stride / 8;
       a.q_out_stride = w.q_out_stride / 8;
       a.num_q_heads = w.num_q_heads;
-      const int64_t vecs = (int64_t)w.max_query_len * w.num_q_heads * (c.head_dim / 8);
-      a.q_ctas = (int32_t)std::min<int64_t>((vecs + 4 * kQ8Threads - 1) / (4 * kQ8Threads), 16384);
-      ctas += (uint32_t)a.q_ctas;
+      // (at most: with kRotateHeads heads a thread, both halves of the grid's y)
+      const int64_t units = (int64_t)w.max_query_len * ((w.num_q_heads + kRotateHeads - 1) / kRotateHeads) *
+                            (c.head_dim / 8 - (w.neox_style ? w.rotary_dim / 16 : 0));
+      a.q_ctas = 2 * (int32_t)std::min<int64_t>((units + 2 * threads - 1) / (2 * threads), 16384);
+      ctas += (uint32_t)a.q_ctas / 2;
     }
   }
-  const bool i8 = w.cache->kind == PKV_Q8_INT8;
-  void (*kern)(const WriteArgs) = nullptr;
-  if (w.rope)
-    kern = c.head_dim == 64
-               ? (i8 ? write_q8_kernel<64, PKV_Q8_INT8, true> : write_q8_kernel<64, PKV_Q8_E4M3, true>)
-               : (i8 ? write_q8_kernel<128, PKV_Q8_INT8, true> : write_q8_kernel<128, PKV_Q8_E4M3, true>);
-  else
-    kern = c.head_dim == 64
-               ? (i8 ? write_q8_kernel<64, PKV_Q8_INT8, false> : write_q8_kernel<64, PKV_Q8_E4M3, false>)
-               : (i8 ? write_q8_kernel<128, PKV_Q8_INT8, false> : write_q8_kernel<128, PKV_Q8_E4M3, false>);
-  kern<<<dim3(ctas, 2, (unsigned)w.num_seqs), kQ8Threads, 0, stream>>>(a);
+  auto pick = [&](auto d, auto kind) -> void (*)(const WriteArgs) {
+    if (w.rope)
+      return per_thread == 1   ? write_q8_kernel<d(), kind(), true, 1>
+             : per_thread == 4 ? write_q8_kernel<d(), kind(), true, 4>
+                               : write_q8_kernel<d(), kind(), true, 8>;
+    return per_thread == 1   ? write_q8_kernel<d(), kind(), false, 1>
+           : per_thread == 4 ? write_q8_kernel<d(), kind(), false, 4>
+                             : write_q8_kernel<d(), kind(), false, 8>;
+  };
+  void (*const kern)(const WriteArgs) = of_kinds(c.head_dim, w.cache->kind, pick);
+  kern<<<dim3(ctas, 2, (unsigned)w.num_seqs), threads, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_error(e, "write_q8_kernel launch");
   return PKV_OK;

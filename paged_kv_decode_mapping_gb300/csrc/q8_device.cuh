@@ -9,6 +9,12 @@
 namespace pkv {
 namespace q8 {
 
+// n / d for n >= 0, d > 0, by 32 bits where that is enough (a 64-bit division takes 0.2 us).
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+  if (((n | d) >> 32) == 0) return (uint32_t)n / (uint32_t)d;
+  return n / d;
+}
+
 template <int KIND>
 __host__ __device__ constexpr float top() { return KIND == PKV_Q8_INT8 ? 127.f : 448.f; }
 
