@@ -20,7 +20,7 @@ namespace pkv {
 namespace {
 
 constexpr int kQ8Threads = 128;   // of a CTA; of a write's twice as many where its pages are large
-constexpr int64_t kReadWide = 1 << 20;
+constexpr int64_t kReadWide = 1 << 18;  // vectors of a call
 constexpr int kRotateHeads = 4;  // q heads a thread rotates with one position's cosines and sines
 
 // What names the tokens of a call: sequence b's newest n of context_lens[b], its rows in the
@@ -114,21 +114,13 @@ __device__ __forceinline__ uint4 rotate_pairs(const uint4 &x, const Angles &a) {
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
-// Vector c of the row at `row`, rotated; cs: the position's cosines and sines.  Coordinates at or
-// past r stay as they are.
-__device__ __forceinline__ uint4 rotated(const uint4 *row, int c, const float *cs, const Rope &p) {
-  const uint4 x = __ldg(row + c);
-  if (8 * c >= p.r) return x;
-  const Angles a = angles_of(cs, c, p);
-  if (!p.neox) return rotate_pairs(x, a);
-  const int half = p.r / 16;
-  return rotate_neox(x, __ldg(row + (c < half ? c + half : c - half)), a, c < half);
-}
-
 // ---------------------------------------------------------------------------
 // The write.  One group of 2^log2_group threads (a warp to the whole CTA) per (sequence, touched
 // page, K or V, kv head): it holds the page's new rows in registers between finding their largest
 // value and rounding them, U 16-byte vectors a thread; what does not fit is read a second time.
+// Bound by its instructions (two thirds of the issue slots; widening, two products and two
+// conversions for each pair of codes) and by HBM: 34000 tokens of 8 heads of 128 take 56 us, 3.7
+// TB/s; with k rotated 83, with 24 heads of q besides 144.  256 tokens of a step: 6 us.
 
 struct WriteArgs {
   Span s;
@@ -154,49 +146,60 @@ __device__ __forceinline__ uint32_t absmax(uint32_t m, const uint4 &x) {
   return m;
 }
 
-// The q rows of one sequence: a thread owns a rotation's whole unit (both partner vectors), so
-// that q_out may be q, of kRotateHeads heads.
+// The q rows of one sequence: a thread owns two vectors (of a rotation, both partners, so that q_out
+// may be q) of kRotateHeads heads.
 template <int D>
 __device__ __forceinline__ void rotate_q(const WriteArgs &a, const Tokens &t, uint32_t part) {
+  constexpr int V = D / 8;
   const int half = a.rope.neox ? a.rope.r / 16 : 0;
-  const int units = D / 8 - half;  // of a row
   const int runs = (a.num_q_heads + kRotateHeads - 1) / kRotateHeads;
-  const int64_t n = (int64_t)(t.end - t.begin) * runs * units;
+  const int64_t n = (int64_t)(t.end - t.begin) * runs * (V / 2);
   for (int64_t i = (int64_t)part * blockDim.x + threadIdx.x; i < n; i += (int64_t)a.q_ctas * blockDim.x) {
-    const int64_t run = q8::quotient(i, units), tok = q8::quotient(run, runs);
-    int c = (int)(i - run * units);
-    if (c >= half) c += half;  // vectors half .. 2 half - 1 belong to their partners
+    const int c = (int)(i % (V / 2)), ca = c < half ? c : 2 * c, cb = c < half ? c + half : 2 * c + 1;
+    const int64_t run = i / (V / 2), tok = q8::quotient(run, runs);
     const int h0 = (int)(run - tok * runs) * kRotateHeads, heads = min(a.num_q_heads - h0, kRotateHeads);
     const int64_t at = t.row0 + tok;
     const int64_t pos = a.rope.positions ? __ldg(a.rope.positions + at) : t.begin + tok;
     if (pos < 0 || pos >= a.rope.max_position) continue;  // reported by the k rows
-    const uint4 *const src = a.q + at * a.q_stride + h0 * (D / 8) + c;
-    uint4 *const dst = a.q_out + at * a.q_out_stride + h0 * (D / 8) + c;
-    const bool turns = 8 * c < a.rope.r, two = c < half;
-    Angles ang = {};
-    if (turns) ang = angles_of(a.rope.cos_sin + pos * a.rope.r, c, a.rope);
+    const uint4 *const src = a.q + at * a.q_stride + h0 * V;
+    uint4 *const dst = a.q_out + at * a.q_out_stride + h0 * V;
     uint4 x[kRotateHeads], y[kRotateHeads];
 #pragma unroll
     for (int h = 0; h < kRotateHeads; ++h)
       if (h < heads) {
-        x[h] = src[h * (D / 8)];  // (not a read-only load: q may be rotated in place)
-        if (two) y[h] = src[h * (D / 8) + half];
+        x[h] = src[h * V + ca];  // (not a read-only load: q may be rotated in place)
+        y[h] = src[h * V + cb];
       }
+    if (8 * ca < a.rope.r) {
+      const float *const cs = a.rope.cos_sin + pos * a.rope.r;
+      const Angles g = angles_of(cs, ca, a.rope);
+      if (half) {
+#pragma unroll
+        for (int h = 0; h < kRotateHeads; ++h) {
+          const uint4 z = x[h];
+          x[h] = rotate_neox(z, y[h], g, true);
+          y[h] = rotate_neox(y[h], z, g, false);
+        }
+      } else {
+        const Angles g2 = angles_of(cs, cb, a.rope);
+#pragma unroll
+        for (int h = 0; h < kRotateHeads; ++h) {
+          x[h] = rotate_pairs(x[h], g);
+          y[h] = rotate_pairs(y[h], g2);
+        }
+      }
+    }
 #pragma unroll
     for (int h = 0; h < kRotateHeads; ++h)
       if (h < heads) {
-        if (two) {
-          dst[h * (D / 8)] = rotate_neox(x[h], y[h], ang, true);
-          dst[h * (D / 8) + half] = rotate_neox(y[h], x[h], ang, false);
-        } else {
-          dst[h * (D / 8)] = turns ? rotate_pairs(x[h], ang) : x[h];
-        }
+        dst[h * V + ca] = x[h];
+        dst[h * V + cb] = y[h];
       }
   }
 }
 
 template <int D, int KIND, bool ROPE, int U>
-__global__ void __launch_bounds__(2 * kQ8Threads, ROPE ? 2 : 4) write_q8_kernel(const __grid_constant__ WriteArgs a) {
+__global__ void __launch_bounds__(2 * kQ8Threads, ROPE ? 3 : 4) write_q8_kernel(const __grid_constant__ WriteArgs a) {
   constexpr int V = D / 8;  // vectors of a row: 8 bf16 in, 8 codes out
   // A decode kernel behind this one may start its set-up (paged_decode_step_q8).
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -240,42 +243,65 @@ __global__ void __launch_bounds__(2 * kQ8Threads, ROPE ? 2 : 4) write_q8_kernel(
   uint8_t *const rows = (is_v ? a.v_cache : a.k_cache) + unit * a.s.block_size * D;
   const float old = live && r0 > 0 ? *scale : 0.f;  // a page that begins here has none
 
-  // A thread's vectors are one column of every (group / V)-th row.
+  // A thread's vectors are P columns of every (group / (V / P))-th row: where k is rotated, the two of
+  // a rotation.
+  constexpr int P = ROPE ? 2 : 1, S = U / P;
+  const int c = gt % (V / P), half = ROPE && !is_v && a.rope.neox ? a.rope.r / 16 : 0;
+  const int col[2] = {c < half ? c : P * c, c < half ? c + half : P * c + 1};
+  const bool turns = ROPE && !is_v && 8 * col[0] < a.rope.r;
   const int64_t row0 = t.row0 + (lo + r0 - t.begin), stride = is_v ? a.v_stride : a.k_stride;
-  const int c = gt % V, rows_apart = group / V, first = gt / V, count = live ? r1 - r0 : 0;
+  const int rows_apart = group / (V / P), first = gt / (V / P), count = live ? r1 - r0 : 0;
   const uint4 *const src = (is_v ? a.v : a.k) + (row0 + first) * stride + h * V;
   const int64_t apart = rows_apart * stride;
-  auto fetch = [&](int u, bool *skip) -> uint4 {  // of row first + u * rows_apart
-    const uint4 *const row = src + u * apart;
-    *skip = false;
-    if constexpr (ROPE) {
-      if (!is_v) {
-        const int r = first + u * rows_apart;
-        const int64_t pos = a.rope.positions ? __ldg(a.rope.positions + row0 + r) : lo + r0 + r;
-        if (pos < 0 || pos >= a.rope.max_position) {
-          raise_error(PKV_DEVERR_POSITION);
-          *skip = true;
-          return make_uint4(0, 0, 0, 0);
-        }
-        return rotated(row, c, a.rope.cos_sin + pos * a.rope.r, a.rope);
-      }
+  // The columns of row first + u * rows_apart.
+  auto load = [&](int u, uint4 *x) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) x[p] = __ldg(src + u * apart + col[p]);
+  };
+  // The same, rotated; false, and zeros, where the row's position has no angles.
+  auto turn = [&](int u, uint4 *x) {
+    if (!ROPE || is_v) return true;
+    const int r = first + u * rows_apart;
+    const int64_t pos = a.rope.positions ? __ldg(a.rope.positions + row0 + r) : lo + r0 + r;
+    if (pos < 0 || pos >= a.rope.max_position) {
+      raise_error(PKV_DEVERR_POSITION);
+      x[0] = x[P - 1] = make_uint4(0, 0, 0, 0);
+      return false;
     }
-    return __ldg(row + c);
+    if (!turns) return true;
+    const float *const cs = a.rope.cos_sin + pos * a.rope.r;
+    const Angles g = angles_of(cs, col[0], a.rope);
+    if (half) {
+      const uint4 y = x[0];
+      x[0] = rotate_neox(y, x[P - 1], g, true);
+      x[P - 1] = rotate_neox(x[P - 1], y, g, false);
+    } else {
+      x[0] = rotate_pairs(x[0], g);
+      x[P - 1] = rotate_pairs(x[P - 1], angles_of(cs, col[1], a.rope));
+    }
+    return true;
   };
   uint4 x[U];
   uint32_t m = 0, skip = 0;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    x[u] = make_uint4(0, 0, 0, 0);
-    bool none = true;
-    if (first + u * rows_apart < count) x[u] = fetch(u, &none);
-    if (ROPE && none) skip |= 1u << u;
+  for (int u = 0; u < S; ++u) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) x[P * u + p] = make_uint4(0, 0, 0, 0);
+    if (first + u * rows_apart < count) load(u, x + P * u);
+  }
+  if constexpr (ROPE) {
+#pragma unroll
+    for (int u = 0; u < S; ++u)
+      if (first + u * rows_apart < count && !turn(u, x + P * u)) skip |= 1u << u;
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) m = absmax(m, x[u]);
-  for (int u = U; first + u * rows_apart < count; ++u) {
-    bool none;
-    m = absmax(m, fetch(u, &none));
+  for (int u = S; first + u * rows_apart < count; ++u) {
+    uint4 y[P];
+    load(u, y);
+    turn(u, y);
+#pragma unroll
+    for (int p = 0; p < P; ++p) m = absmax(m, y[p]);
   }
   m &= 0x7fff7fffu;
   m = max(m & 0xffffu, m >> 16);  // bf16 patterns order as whole numbers, infinity and NaN on top
@@ -297,14 +323,18 @@ __global__ void __launch_bounds__(2 * kQ8Threads, ROPE ? 2 : 4) write_q8_kernel(
   }
   if (gt == 0 && !(to == old && r0 > 0)) *scale = to;
   const q8::Inverse by = q8::inverse_of(to == 0.f ? 1.f : to);
-  uint2 *const dst = reinterpret_cast<uint2 *>(rows + (int64_t)(r0 + first) * D) + c;
+  uint2 *const dst = reinterpret_cast<uint2 *>(rows + (int64_t)(r0 + first) * D);
+  auto store = [&](int u, const uint4 *x) {
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (ROPE ? !(skip >> u & 1u) : first + u * rows_apart < count) dst[u * rows_apart * V] = q8::encode8<KIND>(x[u], by);
-  for (int u = U; first + u * rows_apart < count; ++u) {
-    bool none;
-    const uint4 v = fetch(u, &none);
-    if (!none) dst[u * rows_apart * V] = q8::encode8<KIND>(v, by);
+    for (int p = 0; p < P; ++p) dst[u * rows_apart * V + col[p]] = q8::encode8<KIND, ROPE>(x[p], by);
+  };
+#pragma unroll
+  for (int u = 0; u < S; ++u)
+    if (first + u * rows_apart < count && !(skip >> u & 1u)) store(u, x + P * u);
+  for (int u = S; first + u * rows_apart < count; ++u) {
+    uint4 y[P];
+    load(u, y);
+    if (turn(u, y)) store(u, y);
   }
   if (to > old && r0 > 0) {  // the rows held before, in units of the new scale
     for (int e = gt; e < r0 * (D / 16); e += group) {
@@ -324,7 +354,9 @@ __global__ void __launch_bounds__(2 * kQ8Threads, ROPE ? 2 : 4) write_q8_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// Reading back: bf16(code * scale).  One group of threads per (sequence, page, K or V, kv head).
+// Reading back: bf16(code * scale).  One group of threads per (sequence, page, K or V, run of kv
+// heads), up to 16 loads of a thread in flight.  Bound by HBM, which takes two bytes for each one
+// read: 16 contexts of 1 to 8192 tokens, 8 heads of 128, 31.5 us, 5.0 TB/s (27.6 with 256-token pages).
 // For the prefill, whole contexts as fp16 rows, row seq * out_rows + t being token t's: code *
 // (scale / unit) for the largest scale of the (sequence, kv head) as unit, so that codes keep 11
 // bits (bf16 rows, of 8, doubled the error of the output).
@@ -343,20 +375,50 @@ struct ReadArgs {
 };
 
 // The units: the largest scale of each (sequence, kv head)'s pages.  One CTA per sequence; thread
-// (page % rows, kv head), joined through shared memory.
+// (page % rows, kv head), joined through shared memory.  And the sequence's place in the order of the
+// tiles, longest contexts first (the tiles of 4 chunks over 1600 to 5800 tokens took 174 us in the
+// batch's order, whose last was not the shortest), with its query rows: moved behind those of every
+// sequence before it, cut and flagged where they do not fit (as in disjoint_group).
 struct UnitArgs {
   Span s;
   const float *k_scale, *v_scale;
   float *k_unit, *v_unit;
+  const int32_t *start;
+  int4 *order;
+  int32_t num_queries, max_query_len;
 };
 constexpr int kUnitThreads = 1024;
 __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_constant__ UnitArgs a) {
+  static_assert(kUnitThreads == 32 * 32, "a warp joins the warps' results");
   __shared__ float s_k[kUnitThreads], s_v[kUnitThreads];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ int s_before[32], s_rank[32];
   const int b = blockIdx.x, H = a.s.num_kv_heads, tid = threadIdx.x;
   const int cap = (int)min((int64_t)a.s.max_blocks * a.s.block_size, (int64_t)a.s.max_new);
   const int L = min(max(__ldg(a.s.lens + b), 0), cap), pages = (L + a.s.block_size - 1) >> a.s.log2_bs;
   const int32_t *const row = a.s.tables + (int64_t)b * a.s.max_blocks;
+  int before = 0, rank = 0;  // the furthest end of the sequences before b; how many are taken before b
+  for (int i = tid; i < a.s.num_seqs; i += kUnitThreads) {
+    if (i < b) before = max(before, min(max(__ldg(a.start + i + 1), 0), a.num_queries));
+    const int Li = min(max(__ldg(a.s.lens + i), 0), cap);
+    rank += Li > L || (Li == L && i < b);
+  }
+  before = __reduce_max_sync(0xffffffffu, before);
+  rank = __reduce_add_sync(0xffffffffu, rank);
+  if ((tid & 31) == 0) {
+    s_before[tid >> 5] = before;
+    s_rank[tid >> 5] = rank;
+  }
+  __syncthreads();
+  if (tid < 32) {
+    before = __reduce_max_sync(0xffffffffu, s_before[tid]);
+    rank = __reduce_add_sync(0xffffffffu, s_rank[tid]);
+    if (tid == 0) {
+      const int s0 = __ldg(a.start + b), e0 = __ldg(a.start + b + 1), e = min(max(e0, 0), a.num_queries);
+      const int s = min(max(max(s0, 0), before), a.num_queries), n = min(max(e - s, 0), a.max_query_len);
+      if (s != s0 || s + n != e0) raise_error(PKV_DEVERR_CONTEXT_LEN);
+      a.order[rank] = make_int4(b, s, n, 0);
+    }
+  }
   for (int h0 = 0; h0 < H; h0 += kUnitThreads) {  // (heads past 1024 in further rounds)
     const int wide = min(H - h0, kUnitThreads), rows = kUnitThreads / wide;
     const int h = tid % wide, r = tid / wide;
@@ -385,16 +447,12 @@ __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_con
 }
 
 template <int D, int KIND, bool WHOLE, int U>
-__global__ void __launch_bounds__(kQ8Threads, 5) read_q8_kernel(const __grid_constant__ ReadArgs a) {
+__global__ void __launch_bounds__(kQ8Threads, U == 16 ? 5 : 8) read_q8_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int V = D / 8;  // vectors of a row: 8 codes in, 8 bf16 out
-  if constexpr (WHOLE) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the units
-  }
   const int tid = threadIdx.x, lane = tid & 31, group = 1 << a.log2_group, gt = tid & (group - 1);
   const int b = blockIdx.z;
   const bool is_v = blockIdx.y;
-  const uint32_t item = blockIdx.x * (kQ8Threads >> a.log2_group) + (tid >> a.log2_group);
+  const uint32_t item = blockIdx.x * (blockDim.x >> a.log2_group) + (tid >> a.log2_group);
   const int j = (int)(item / (uint32_t)a.runs), h0 = (int)(item - (uint32_t)j * a.runs) << a.log2_heads;
   if (j >= a.pages) return;  // (whole warps, here and below)
   Tokens t;
@@ -425,7 +483,7 @@ __global__ void __launch_bounds__(kQ8Threads, 5) read_q8_kernel(const __grid_con
   if (lane < heads) {
     scale = __ldg((is_v ? a.v_scale : a.k_scale) + unit + lane);
     if constexpr (WHOLE) {
-      const float of = (is_v ? a.v_unit : a.k_unit)[(int64_t)b * a.s.num_kv_heads + h0 + lane];
+      const float of = __ldg((is_v ? a.v_unit : a.k_unit) + (int64_t)b * a.s.num_kv_heads + h0 + lane);
       scale = of > 0.f ? __fdiv_rn(scale, of) : scale * 0.f;  // (a NaN stays)
     }
   }
@@ -490,21 +548,6 @@ auto of_kinds(int32_t d, int32_t kind, F pick) {
   constexpr integral_constant<int, PKV_Q8_E4M3> e4{};
   if (d == 64) return kind == PKV_Q8_INT8 ? pick(d64, i8) : pick(d64, e4);
   return kind == PKV_Q8_INT8 ? pick(d128, i8) : pick(d128, e4);
-}
-
-// early: the kernel may start before the one ahead of it in the stream has ended (it waits for that itself).
-template <typename A>
-void launch_dependent(void (*kern)(const A), dim3 ctas, int threads, const A &a, bool early, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = ctas;
-  cfg.blockDim = dim3((unsigned)threads, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = early ? 1 : 0;
-  (void)cudaLaunchKernelEx(&cfg, kern, a);  // (the caller asks for the error)
 }
 
 // Pages that `n` consecutive tokens touch, at most.
@@ -578,22 +621,28 @@ int launch_read(const Span &s, const pkv_q8_cache &q, const pkv_cache_desc &c, v
   a.v_unit = v_unit;
   a.pages = (int32_t)pages;
   // 16 vectors a thread, of several heads where a page of one has fewer; 4 where the call is too short for
-  // that to fill the GPU (FIGR).
+  // that to fill the GPU (8 heads of 128, pages of 16: one context of 100 tokens 3.3 us by 16 and 2.6 by
+  // 4, 16 of 300 5.4 and 6.4, 16 of 8192 at most 34 and 47).  With registers for 8 or 4 where all heads
+  // together have fewer.
   const int64_t page_vecs = (int64_t)s.block_size * c.head_dim / 8;
-  const bool wide = pages * s.num_seqs * 2 * c.num_kv_heads * page_vecs >= kReadWide;
-  const int per_thread = wide ? 16 : 4;
+  int per_thread = pages * s.num_seqs * 2 * c.num_kv_heads * page_vecs >= kReadWide ? 16 : 4;
   while ((page_vecs << (a.log2_heads + 1)) <= 32 * per_thread && (1 << a.log2_heads) < c.num_kv_heads) ++a.log2_heads;
+  while (per_thread > 4 && (page_vecs << a.log2_heads) <= 16 * per_thread) per_thread /= 2;
   a.runs = (c.num_kv_heads + (1 << a.log2_heads) - 1) >> a.log2_heads;
   a.log2_group = log2_group_of(page_vecs << a.log2_heads, per_thread, kQ8Threads);
   const int per = kQ8Threads >> a.log2_group;
   const dim3 ctas((unsigned)((pages * a.runs + per - 1) / per), 2, (unsigned)s.num_seqs);
   auto pick = [&](auto d, auto kind) -> void (*)(const ReadArgs) {
     if (out_rows)
-      return wide ? read_q8_kernel<d(), kind(), true, 16> : read_q8_kernel<d(), kind(), true, 4>;
-    return wide ? read_q8_kernel<d(), kind(), false, 16> : read_q8_kernel<d(), kind(), false, 4>;
+      return per_thread == 16  ? read_q8_kernel<d(), kind(), true, 16>
+             : per_thread == 8 ? read_q8_kernel<d(), kind(), true, 8>
+                               : read_q8_kernel<d(), kind(), true, 4>;
+    return per_thread == 16  ? read_q8_kernel<d(), kind(), false, 16>
+           : per_thread == 8 ? read_q8_kernel<d(), kind(), false, 8>
+                             : read_q8_kernel<d(), kind(), false, 4>;
   };
   void (*const kern)(const ReadArgs) = of_kinds(c.head_dim, q.kind, pick);
-  launch_dependent(kern, ctas, kQ8Threads, a, out_rows > 0, stream);
+  kern<<<ctas, kQ8Threads, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_error(e, "read_q8_kernel launch");
   return PKV_OK;
@@ -680,16 +729,15 @@ int launch_write_q8(const WriteQ8 &w, cudaStream_t stream) {
       a.q_stride = w.q_stride / 8;
       a.q_out_stride = w.q_out_stride / 8;
       a.num_q_heads = w.num_q_heads;
-      // (at most: with kRotateHeads heads a thread, both halves of the grid's y)
-      const int64_t units = (int64_t)w.max_query_len * ((w.num_q_heads + kRotateHeads - 1) / kRotateHeads) *
-                            (c.head_dim / 8 - (w.neox_style ? w.rotary_dim / 16 : 0));
+      const int64_t units =
+          (int64_t)w.max_query_len * ((w.num_q_heads + kRotateHeads - 1) / kRotateHeads) * (c.head_dim / 16);
       a.q_ctas = 2 * (int32_t)std::min<int64_t>((units + 2 * threads - 1) / (2 * threads), 16384);
       ctas += (uint32_t)a.q_ctas / 2;
     }
   }
   auto pick = [&](auto d, auto kind) -> void (*)(const WriteArgs) {
     if (w.rope)
-      return per_thread == 1   ? write_q8_kernel<d(), kind(), true, 1>
+      return per_thread == 1   ? write_q8_kernel<d(), kind(), true, 2>
              : per_thread == 4 ? write_q8_kernel<d(), kind(), true, 4>
                                : write_q8_kernel<d(), kind(), true, 8>;
     return per_thread == 1   ? write_q8_kernel<d(), kind(), false, 1>
@@ -776,7 +824,7 @@ namespace {
 
 struct PrefillLayout {
   int32_t rows;  // packed rows of a sequence
-  size_t k, v, k_unit, v_unit, total;
+  size_t k, v, k_unit, v_unit, order, total;
 };
 constexpr int kMaxRowQueries = 32, kMaxRows = 65535;  // of a sequence, of a call, as the decode's rows
 int64_t row_capacity(int32_t num_seqs) { return std::min((int64_t)num_seqs * kMaxRowQueries, (int64_t)kMaxRows); }
@@ -809,7 +857,8 @@ bool prefill_layout(int32_t num_seqs, int32_t hkv, int32_t d, int32_t max_len, i
   p->v = rows;
   p->k_unit = 2 * rows;
   p->v_unit = p->k_unit + units;
-  p->total = std::max(p->v_unit + units,  // either way
+  p->order = p->v_unit + units;
+  p->total = std::max(p->order + up((size_t)num_seqs * sizeof(int4)),  // either way
                       up(rows_q8_workspace((int32_t)row_capacity(num_seqs), d, sms)));
   return true;
 }
@@ -848,6 +897,7 @@ PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t
     return PKV_OK;
   }
   if (!out || !query_start) return set_error(PKV_ERR_NULL, "%s: NULL out/query_start", fn);
+  if (num_queries > 0x7fffff00LL) return set_error(PKV_ERR_UNSUPPORTED, "%s: num_queries over 2^31", fn);
   if (!aligned16(out)) return set_error(PKV_ERR_ALIGN, "%s: out must be 16-byte aligned", fn);
   if (misaligned4(query_start) || misaligned4(block_tables) || misaligned4(context_lens))
     return set_error(PKV_ERR_ALIGN, "%s: int32 tensors must be 4-byte aligned", fn);
@@ -886,6 +936,10 @@ PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t
   u.v_scale = cache->v_scale;
   u.k_unit = reinterpret_cast<float *>(ws + p.k_unit);
   u.v_unit = reinterpret_cast<float *>(ws + p.v_unit);
+  u.start = query_start;
+  u.order = reinterpret_cast<int4 *>(ws + p.order);
+  u.num_queries = (int32_t)num_queries;
+  u.max_query_len = max_query_len;
   units_q8_kernel<<<(unsigned)num_seqs, kUnitThreads, 0, s>>>(u);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_error(e, "units_q8_kernel launch");
@@ -897,6 +951,7 @@ PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t
   l.v = reinterpret_cast<const uint16_t *>(ws + p.v);
   l.k_unit = u.k_unit;
   l.v_unit = u.v_unit;
+  l.order = u.order;
   rc = launch_chunk(l, s);
   if (!rc) clear_error();
   return rc;

@@ -75,6 +75,7 @@ struct TileArgs {
   // newest tokens (and context_lens)
   int32_t kv_rows, max_context;    // packed rows of a sequence; the longest context
   const float *k_unit, *v_unit;    // [num][num_kv_heads]
+  const int4 *order;               // [num] longest context first: a sequence, its first query row, its rows
 };
 
 // 8 softmax warps, the K and the V producer (two warps a ring measured neutral), an MMA warp per
@@ -168,12 +169,14 @@ struct TileCursor {
   int c = -32, carry = 0, next_carry = 0;  // the furthest end before these, and with them
   int64_t before = 0;                      // pieces before these
   int s = 0, len = 0, mine = 0, upto = 0, prefix = 0;
+  int seq = 0;                             // kNewest
 };
 
 // The sequence (or group) whose pieces of `tokens` query tokens hold piece number idx, its
 // first query token, its length, the piece's place in it, its pieces and its prefix.  Whole
 // warps; misplaced and over-long sequences are moved, cut and flagged.  The search goes on from
 // where the last one ended (from the beginning, 512 sequences of 84 tokens took 15 us an item).
+template <int MODE>
 __device__ __forceinline__ bool locate_tile(const TileArgs &a, TileCursor &at, int64_t idx, int tokens,
                                             int lane, int &first, int &n, int &tile, int &ntiles,
                                             int &prefix, int &seq) {
@@ -186,7 +189,14 @@ __device__ __forceinline__ bool locate_tile(const TileArgs &a, TileCursor &at, i
     at.before = total;
     at.carry = at.next_carry;
     at.prefix = a.prefix_lens && at.c + lane < a.num ? __ldg(a.prefix_lens + at.c + lane) : 0;
-    disjoint_group(a.start, a.num, a.total, a.max_len, at.c, lane, at.next_carry, at.s, at.len);
+    if constexpr (MODE == kNewest) {
+      const int4 o = at.c + lane < a.num ? __ldg(a.order + at.c + lane) : make_int4(0, 0, 0, 0);
+      at.seq = o.x;
+      at.s = o.y;
+      at.len = o.z;
+    } else {
+      disjoint_group(a.start, a.num, a.total, a.max_len, at.c, lane, at.next_carry, at.s, at.len);
+    }
     at.mine = at.upto = (at.len + tokens - 1) / tokens;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
@@ -196,7 +206,7 @@ __device__ __forceinline__ bool locate_tile(const TileArgs &a, TileCursor &at, i
   }
   const int l = __ffs(__ballot_sync(0xffffffffu, at.before + at.upto > idx)) - 1;
   prefix = __shfl_sync(0xffffffffu, at.prefix, l);
-  seq = at.c + l;
+  seq = MODE == kNewest ? __shfl_sync(0xffffffffu, at.seq, l) : at.c + l;
   first = __shfl_sync(0xffffffffu, at.s, l);
   n = __shfl_sync(0xffffffffu, at.len, l);
   ntiles = __shfl_sync(0xffffffffu, at.mine, l);
@@ -212,7 +222,7 @@ __device__ __forceinline__ bool make_item(const TileArgs &a, TileCursor &at, uns
   it.g = (int)(cta_x % (unsigned)a.num_kv_heads);
   const int tokens = a.tile_tokens * (MODE != kPrefix ? 2 : 1);
   int tile, ntiles, prefix;
-  if (!locate_tile(a, at, cta_x / (unsigned)a.num_kv_heads, tokens, lane, it.first, it.n, tile, ntiles, prefix,
+  if (!locate_tile<MODE>(a, at, cta_x / (unsigned)a.num_kv_heads, tokens, lane, it.first, it.n, tile, ntiles, prefix,
                    it.seq))
     return false;
   if constexpr (MODE == kNewest) {
@@ -1292,6 +1302,7 @@ int launch_chunk(const ChunkLaunch &l, cudaStream_t stream) {
   a.max_context = l.max_context;
   a.k_unit = l.k_unit;
   a.v_unit = l.v_unit;
+  a.order = l.order;
   const int64_t tiles = l.num_queries / (2 * a.tile_tokens) + std::min<int64_t>(l.num_seqs, l.num_queries);
   if (l.num_queries > 0x7fffff00LL || tiles > 0x7fffffffLL / l.num_kv_heads)
     return set_error(PKV_ERR_UNSUPPORTED, "paged_prefill_attention_q8: too many query rows");

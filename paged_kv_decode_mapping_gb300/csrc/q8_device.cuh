@@ -105,7 +105,20 @@ __device__ __forceinline__ Inverse inverse_of(float s) {
   const float lo = isinf(inv) ? 0.f : inv * (1.f - 4.76837158e-7f), hi = inv * (1.f + 4.76837158e-7f);
   return {s, f32x2(lo, lo), f32x2(hi, hi)};
 }
+// CALL: by a function of its own (a kernel with a rotation besides fits the instruction cache so: 91 us
+// instead of 97; one without is slower by the call: 61 and 63).
 template <int KIND>
+__device__ __noinline__ uint2 divided8(uint4 v, float s) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float q[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    q[2 * k] = __fdiv_rn(dev::bf16lo_to_f32(w[k]), s);
+    q[2 * k + 1] = __fdiv_rn(dev::bf16hi_to_f32(w[k]), s);
+  }
+  return make_uint2(encode4<KIND>(q[0], q[1], q[2], q[3]), encode4<KIND>(q[4], q[5], q[6], q[7]));
+}
+template <int KIND, bool CALL>
 __device__ __forceinline__ uint2 encode8(const uint4 &v, const Inverse &s) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t c[4], differ[4];  // two codes each
@@ -128,6 +141,7 @@ __device__ __forceinline__ uint2 encode8(const uint4 &v, const Inverse &s) {
     }
   }
   if (differ[0] | differ[1] | differ[2] | differ[3]) {
+    if constexpr (CALL) return divided8<KIND>(v, s.s);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (differ[k])
