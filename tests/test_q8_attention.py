@@ -458,3 +458,174 @@ def test_streams_and_graphs(B):
         check(out, *decode_ref(b, q, 0.125), f"replay {i}")
         check(out2, *want2, "side stream")
     assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("k_at,v_at", [(0, 1 << 20), (1 << 20, 0), (0, (1 << 20) + 16), ((1 << 20) + 48, 0), (0, 0)])
+@pytest.mark.parametrize("dtype,d", [(torch.int8, 64), (torch.float8_e4m3fn, 128)])
+def test_pools_anywhere_in_memory(B, dtype, d, k_at, v_at):
+    """V's pool behind K's, before it, not a whole number of 128-byte rows away, and K's itself."""
+    b = Batch([130, 1, 300], dtype, 2, d, 16, seed=62)
+    room = torch.zeros((1 << 20) + 64 + b.k.numel(), dtype=torch.uint8, device=DEV)
+    assert b.k.numel() <= 1 << 20
+    old = (b.k, b.v)
+    b.k, b.v = (room[at:at + x.numel()].view(x.dtype).view(x.shape) for x, at in zip(old, (k_at, v_at)))
+    R.bits(b.k).copy_(R.bits(old[0]))
+    if k_at != v_at:
+        R.bits(b.v).copy_(R.bits(old[1]))
+    q = b.randn(3, 6, d)
+    check(decode(B, b, q, 0.1), *decode_ref(b, q, 0.1))
+    assert B.pkv_device_errors() == 0
+
+
+def test_many_sequences(B):
+    """More sequences than the GPU has threads in a CTA's scan, some empty, some long."""
+    gen = torch.Generator().manual_seed(63)
+    lens = [0 if x < 0.2 else (200 if x > 0.98 else int(1 + 40 * x)) for x in torch.rand(7000, generator=gen).tolist()]
+    b = Batch(lens, torch.int8, 1, 64, 8, seed=64)
+    q = b.randn(7000, 2, 64)
+    out = decode(B, b, q, 0.125)
+    # (two heads of one kv head, so all sequences of one length at once)
+    for n in sorted(set(lens)):
+        at = [s for s, m in enumerate(lens) if m == n]
+        if n == 0:
+            assert not out[at].any()
+            continue
+        rows = torch.tensor([b.tables[s][:-(-n // 8)] for s in at], device=DEV)
+        k, v = ((x[rows].double() * s[rows][..., None, None].double()).permute(0, 2, 1, 3, 4).reshape(len(at), -1, 64)[:, :n]
+                for x, s in ((b.k, b.ks), (b.v, b.vs)))
+        p = torch.softmax(q[at].double() @ k.transpose(1, 2) * 0.125, -1)
+        check(out[at], p @ v, p @ v.abs(), f"length {n}")
+    assert B.pkv_device_errors() == 0
+
+
+def test_two_graphs_share_a_workspace(B):
+    """A decode of a batch and a chunk of another, captured, replayed in turns on one workspace each kind."""
+    b1, b2 = Batch([4000, 77], torch.int8, 2, 64, 16, seed=65), Batch([900] * 30, torch.float8_e4m3fn, 2, 64, 16, seed=66)
+    q1, q2 = b1.randn(2, 4, 64), b2.randn(30, 4, 64)
+    ws = torch.zeros(B.paged_decode_q8_workspace_size(30, 4, 2, 64, 4000), dtype=torch.uint8, device=DEV)
+    chunk = torch.empty(max(B.paged_prefill_q8_workspace_size(2, 2, 64, 16, 4000),
+                            B.paged_prefill_q8_workspace_size(30, 2, 64, 16, 900)), dtype=torch.uint8, device=DEV)
+    o1, o2, c1, c2 = (torch.empty_like(x) for x in (q1, q2, q1, q2))
+    s1, s2 = starts([1, 1]), starts([1] * 30)
+
+    def one():
+        decode_into(o1, q1, b1)
+        B.paged_prefill_attention_q8(c1, q1, *b1.cache(), b1.bt, b1.cl, 4000, s1, 1, 0.125, workspace=chunk)
+
+    def two():
+        decode_into(o2, q2, b2)
+        B.paged_prefill_attention_q8(c2, q2, *b2.cache(), b2.bt, b2.cl, 900, s2, 1, 0.125, workspace=chunk)
+
+    def decode_into(out, q, b):
+        B.paged_decode_attention_q8(out, q, *b.cache(), b.bt, b.cl, max(b.lens), 0.125, workspace=ws)
+
+    graphs = []
+    for f in (one, two):
+        f()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            f()
+    w1, w2 = decode_ref(b1, q1, 0.125), decode_ref(b2, q2, 0.125)
+    for i in (0, 1, 1, 0, 1):
+        for t in (o1, o2, c1, c2):
+            t.fill_(77)
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        for out in ((o1, c1), (o2, c2))[i]:
+            check(out, *(w1, w2)[i], f"graph {i}")
+    assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", R.KINDS)
+@pytest.mark.parametrize("d,bs", [(64, 16), (128, 32)])
+def test_prompts_chunks_drafts_forks_and_steps(B, dtype, d, bs):
+    """A serving loop over the 8-bit cache with the block manager: prompts, their next chunks, drafts
+    checked and partly taken back, forks, rotated steps, compaction, the contexts handed on as bf16."""
+    hq, hkv, nb, scale, r = 6, 2, 60, d ** -0.5, 32
+    gen = torch.Generator().manual_seed(67)
+    k, v, ks, vs = R.pools(nb, hkv, bs, d, dtype, gen, DEV)
+    cache = (k, v, ks, vs)
+    model = [t.clone() for t in cache]  # what R.write makes of the same calls
+    ang = torch.arange(400, dtype=torch.float64)[:, None] * 10000.0 ** (-2.0 * torch.arange(r // 2, dtype=torch.float64) / r)
+    table = torch.cat((ang.cos(), ang.sin()), 1).float().to(DEV)
+    bm = B.BlockManager(nb, bs)
+    lens = {}
+
+    def run(seqs, counts, attend):
+        """The next counts[i] tokens of seqs[i]: appended, rotated and written, attended to."""
+        rows = []
+        for s, n in zip(seqs, counts):
+            if s not in lens:
+                bm.add_sequence(s, n)
+                lens[s] = n
+            else:
+                for _ in range(n):
+                    _, pairs, copied = bm.append_slots_cow([s])
+                    if pairs.shape[0]:
+                        B.paged_kv_copy_blocks_q8(*cache, pairs.to(DEV), copied.to(DEV))
+                        for (a, z), m in zip(pairs.tolist(), copied.tolist()):
+                            for i in range(4):
+                                x = R.bits(model[i])
+                                if i < 2:
+                                    x[z, :, :m] = x[a, :, :m]
+                                else:
+                                    x[z] = x[a]
+                lens[s] += n
+            rows.append(range(lens[s] - n, lens[s]))
+        bt, cl = (t.to(DEV) for t in bm.block_tables(list(seqs), 16))
+        x = torch.randn(sum(counts), hq + 2 * hkv, d, generator=gen).to(torch.bfloat16).to(DEV)
+        q, kn, vn = x.split([hq, hkv, hkv], dim=1)
+        pos = torch.tensor([p for x in rows for p in x], device=DEV)
+        wq, wk = R.rotate(q, table, pos, r, True), R.rotate(kn, table, pos, r, True)
+        at = 0
+        for s, n in zip(seqs, counts):
+            tab = bt[list(seqs).index(s)].tolist()
+            R.write(model[0], model[2], wk[at:at + n], tab, lens[s] - n)
+            R.write(model[1], model[3], vn[at:at + n], tab, lens[s] - n)
+            at += n
+        out, q_out = (torch.empty(sum(counts), hq, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        longest = max(lens[s] for s in seqs)
+        if attend == "step":
+            B.paged_decode_step_rope_q8(out, q, kn, vn, table, *cache, bt, cl, longest, scale, q_out=q_out, rotary_dim=r)
+        else:
+            B.paged_kv_write_rope_q8(kn, vn, table, *cache, bt, cl, starts(counts), max(counts), q=q, q_out=q_out, rotary_dim=r)
+            B.paged_prefill_attention_q8(out, q_out, *cache, bt, cl, longest, starts(counts), max(counts), scale)
+        assert torch.equal(q_out, wq)
+        at = 0
+        for i, (s, n) in enumerate(zip(seqs, counts)):
+            kk, vv = (R.values(c, sc, bt[i].tolist(), 0, lens[s], torch.float64) for c, sc in ((k, ks), (v, vs)))
+            for got, c, sc in ((kk, model[0], model[2]), (vv, model[1], model[3])):
+                assert torch.equal(got, R.values(c, sc, bt[i].tolist(), 0, lens[s], torch.float64)), f"sequence {s}"
+            seen = torch.arange(lens[s], device=DEV)[None, :] <= torch.arange(lens[s] - n, lens[s], device=DEV)[:, None]
+            want, mag = R.attention(wq[at:at + n], kk, vv, scale, seen)
+            check_prefill(out[at:at + n], wq[at:at + n], kk, want, mag, scale)
+            at += n
+        return bt, cl
+
+    run((0, 1, 2), (70, 33, 100), "chunk")     # prompts
+    run((0, 2), (130, 1), "chunk")             # a prompt's next chunk beside a sequence's one token
+    run((0, 1, 2), (5, 5, 5), "chunk")         # drafts, of which two are right
+    for s in (0, 1, 2):
+        bm.truncate(s, lens[s] - 3)
+        lens[s] -= 3
+    for child in (3, 4):
+        bm.fork(0, child)
+        lens[child] = lens[0]
+    for _ in range(3):
+        bt, cl = run((0, 1, 2, 3, 4), (1,) * 5, "step")
+    before = [R.values(c, sc, bt[i].tolist(), 0, lens[s], torch.float32) for i, s in enumerate(range(5)) for c, sc in ((k, ks), (v, vs))]
+    bm.free_sequence(1)
+    moves, bmap = bm.compact()
+    B.paged_kv_compact_q8(*cache, moves.to(DEV), bt, bmap.to(DEV))
+    left = [0, 2, 3, 4]
+    bt2, cl2 = (t.to(DEV) for t in bm.block_tables(left, 16))
+    total = sum(lens[s] for s in left)
+    k_out, v_out = (torch.empty(total, hkv, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    B.paged_kv_read_q8(k_out, v_out, *cache, bt2, cl2, starts([lens[s] for s in left]), max(lens.values()))
+    at = 0
+    for s in left:
+        for got, want in ((k_out, before[2 * s]), (v_out, before[2 * s + 1])):
+            assert torch.equal(got[at:at + lens[s]], want.to(torch.bfloat16)), f"sequence {s}"
+        at += lens[s]
+    assert B.pkv_device_errors() == 0
