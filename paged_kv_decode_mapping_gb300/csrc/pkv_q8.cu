@@ -434,11 +434,16 @@ __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_con
     s_k[tid] = k;
     s_v[tid] = v;
     __syncthreads();
-    if (tid < wide) {
-      for (int x = 1; x < rows; ++x) {
-        k = fmaxf(k, s_k[x * wide + tid]);
-        v = fmaxf(v, s_v[x * wide + tid]);
+    int half = 1;
+    while (2 * half < rows) half *= 2;
+    for (; half > 0 && rows > 1; half /= 2) {
+      if (r < half && r + half < rows) {
+        s_k[tid] = k = fmaxf(k, s_k[tid + half * wide]);
+        s_v[tid] = v = fmaxf(v, s_v[tid + half * wide]);
       }
+      __syncthreads();
+    }
+    if (tid < wide) {
       a.k_unit[(int64_t)b * H + h0 + tid] = k;
       a.v_unit[(int64_t)b * H + h0 + tid] = v;
     }
