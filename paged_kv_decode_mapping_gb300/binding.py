@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import struct
 import os
 from typing import Optional
 
@@ -52,7 +53,11 @@ class pkv_q8_cache(ctypes.Structure):
 _P = ctypes.c_void_p
 _i32, _i64, _f32, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _D = ctypes.POINTER(pkv_cache_desc)
-_Q8 = ctypes.POINTER(pkv_q8_cache)
+# pkv_q8_cache and pkv_cache_desc as packed bytes, for the 8-bit cache's calls (0.3 us less than a
+# ctypes.Structure each)
+_Q8, _Q8D = ctypes.c_void_p, ctypes.c_void_p
+_pack_q8, _pack_desc = struct.Struct("PPPPi4x").pack, struct.Struct("qiii4x").pack
+assert struct.calcsize("PPPPi4x") == ctypes.sizeof(pkv_q8_cache) and struct.calcsize("qiii4x") == ctypes.sizeof(pkv_cache_desc)
 
 _lib.paged_kv_write.argtypes = [_P, _P, _P, _i64, _P, _P, _D, _P]
 _lib.paged_kv_write.restype = ctypes.c_int
@@ -97,31 +102,31 @@ _lib.paged_prefill_attention.restype = ctypes.c_int
 _lib.prompt_attention.argtypes = [_P, _P, _P, _P, _i64, _i64, _i64, _i64, _P, _i64, _i32, _i32,
                                   _i32, _i32, _i32, _f32, _P]
 _lib.prompt_attention.restype = ctypes.c_int
-_lib.paged_kv_write_q8.argtypes = [_P, _P, _i64, _i64, _P, _i64, _i32, _P, _i32, _P, _i32, _Q8, _D, _P]
+_lib.paged_kv_write_q8.argtypes = [_P, _P, _i64, _i64, _P, _i64, _i32, _P, _i32, _P, _i32, _Q8, _Q8D, _P]
 _lib.paged_kv_write_q8.restype = ctypes.c_int
 _lib.paged_kv_write_rope_q8.argtypes = [_P, _P, _i64, _i64, _P, _P, _i64, _i64, _i32, _P, _P, _i64, _i32,
-                                        _i32, _P, _i64, _i32, _P, _i32, _P, _i32, _Q8, _D, _P]
+                                        _i32, _P, _i64, _i32, _P, _i32, _P, _i32, _Q8, _Q8D, _P]
 _lib.paged_kv_write_rope_q8.restype = ctypes.c_int
-_lib.paged_kv_read_q8.argtypes = [_P, _P, _i64, _i64, _P, _i64, _i32, _P, _i32, _P, _i32, _Q8, _D, _P]
+_lib.paged_kv_read_q8.argtypes = [_P, _P, _i64, _i64, _P, _i64, _i32, _P, _i32, _P, _i32, _Q8, _Q8D, _P]
 _lib.paged_kv_read_q8.restype = ctypes.c_int
 _lib.paged_decode_q8_workspace_size.argtypes = [_i32] * 5
 _lib.paged_decode_q8_workspace_size.restype = _sz
-_lib.paged_decode_attention_q8.argtypes = [_P, _P, _Q8, _P, _i32, _P, _i32, _i32, _i32, _D, _f32, _P, _sz, _P]
+_lib.paged_decode_attention_q8.argtypes = [_P, _P, _Q8, _P, _i32, _P, _i32, _i32, _i32, _Q8D, _f32, _P, _sz, _P]
 _lib.paged_decode_attention_q8.restype = ctypes.c_int
-_lib.paged_decode_step_q8.argtypes = [_P, _P, _P, _P, _i64, _i64, _Q8, _P, _i32, _P, _i32, _i32, _i32, _D,
+_lib.paged_decode_step_q8.argtypes = [_P, _P, _P, _P, _i64, _i64, _Q8, _P, _i32, _P, _i32, _i32, _i32, _Q8D,
                                       _f32, _P, _sz, _P]
 _lib.paged_decode_step_q8.restype = ctypes.c_int
 _lib.paged_decode_step_rope_q8.argtypes = [_P, _P, _i64, _P, _P, _P, _i64, _i64, _P, _P, _i64, _i32, _i32,
-                                           _Q8, _P, _i32, _P, _i32, _i32, _i32, _D, _f32, _P, _sz, _P]
+                                           _Q8, _P, _i32, _P, _i32, _i32, _i32, _Q8D, _f32, _P, _sz, _P]
 _lib.paged_decode_step_rope_q8.restype = ctypes.c_int
 _lib.paged_prefill_q8_workspace_size.argtypes = [_i32] * 4
 _lib.paged_prefill_q8_workspace_size.restype = _sz
-_lib.paged_prefill_attention_q8.argtypes = [_P, _P, _i64, _Q8, _P, _i32, _P, _i32, _P, _i32, _i32, _i32, _D, _f32,
+_lib.paged_prefill_attention_q8.argtypes = [_P, _P, _i64, _Q8, _P, _i32, _P, _i32, _P, _i32, _i32, _i32, _Q8D, _f32,
                                             _P, _sz, _P]
 _lib.paged_prefill_attention_q8.restype = ctypes.c_int
-_lib.paged_kv_copy_blocks_q8.argtypes = [_P, _i32, _P, _P, _i64, _D, _P]
+_lib.paged_kv_copy_blocks_q8.argtypes = [_P, _i32, _P, _P, _i64, _Q8D, _P]
 _lib.paged_kv_copy_blocks_q8.restype = ctypes.c_int
-_lib.paged_kv_compact_q8.argtypes = [_P, _i32, _P, _P, _i64, _P, _i64, _i32, _P, _D, _P]
+_lib.paged_kv_compact_q8.argtypes = [_P, _i32, _P, _P, _i64, _P, _i64, _i32, _P, _Q8D, _P]
 _lib.paged_kv_compact_q8.restype = ctypes.c_int
 _lib.paged_decode_split.argtypes = [_P, _P, _P, _P, _P, _P, _i32, _P, _i32, _i32, _i32, _D, _f32,
                                     _i32, _P]
@@ -683,8 +688,8 @@ _BF16, _F32, _I32, _I8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torc
 
 
 def _q8_cache(dev: int, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start=None):
-    """(pkv_q8_cache, pkv_cache_desc) of tensors on device `dev`, checked in one expression (a call's
-    checks were 9 of its 12 us when each tensor had its own); _q8_wrong names what fails."""
+    """(pkv_q8_cache, pkv_cache_desc, Hkv, B, M) of tensors on device `dev`, checked in one expression (a
+    call's checks were 9 of its 12 us when each tensor had its own); _q8_wrong names what fails."""
     kt = k_cache.dtype
     if not (kt is v_cache.dtype and (kt is _I8 or kt is _E4M3) and k_scale.dtype is _F32 and
             v_scale.dtype is _F32 and block_tables.dtype is _I32 and context_lens.dtype is _I32 and
@@ -707,8 +712,8 @@ def _q8_cache(dev: int, k_cache, v_cache, k_scale, v_scale, block_tables, contex
         raise ValueError("block_tables must be [B, M] and context_lens [B]")
     if query_start is not None and query_start.shape != (B + 1,):
         raise ValueError("query_start must be [B + 1] for context_lens [B]")
-    return (pkv_q8_cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                         Q8_INT8 if kt is _I8 else Q8_E4M3), pkv_cache_desc(NB, BS, Hkv, D))
+    return (_pack_q8(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                     Q8_INT8 if kt is _I8 else Q8_E4M3), _pack_desc(NB, BS, Hkv, D), Hkv, B, bt[1])
 
 
 def _q8_wrong(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start) -> None:
@@ -768,11 +773,10 @@ def paged_kv_write_q8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v
     [T, Hkv, D] (the tokens may be strided), quantised into its pages at positions
     context_lens[b] - n .. context_lens[b] - 1.  Without query_start: one token per sequence."""
     dev, T, sk, sv = _q8_rows(k, v, k_cache)
-    c, d = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
-    B, M = block_tables.shape
+    c, d, H, B, M = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
     _check(_lib.paged_kv_write_q8(k.data_ptr(), v.data_ptr(), sk, sv, _ptr(query_start), T, int(max_query_len),
-                                  block_tables.data_ptr(), M, context_lens.data_ptr(), B, ctypes.byref(c),
-                                  ctypes.byref(d), _stream(stream, dev)), "paged_kv_write_q8")
+                                  block_tables.data_ptr(), M, context_lens.data_ptr(), B, c,
+                                  d, _stream(stream, dev)), "paged_kv_write_q8")
 
 
 def paged_kv_write_rope_q8(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor,
@@ -785,7 +789,7 @@ def paged_kv_write_rope_q8(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tens
     """paged_kv_write_q8 of the rotated k; the rotated q goes to q_out (default: q itself).
     positions [T] int64 default to the tokens' positions in their sequences."""
     dev, T, sk, sv = _q8_rows(k, v, k_cache)
-    c, d = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
+    c, d, H, B, M = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
     sq = so = heads = 0
     if q is not None:
         q_out = q if q_out is None else q_out
@@ -796,12 +800,11 @@ def paged_kv_write_rope_q8(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tens
     elif q_out is not None:
         raise ValueError("q_out without q")
     r = _rope_table(cos_sin, positions, k.shape[2] if rotary_dim is None else int(rotary_dim), T, dev)
-    B, M = block_tables.shape
     _check(_lib.paged_kv_write_rope_q8(k.data_ptr(), v.data_ptr(), sk, sv, _ptr(q), _ptr(q_out), sq, so, heads,
                                        _ptr(positions), cos_sin.data_ptr(), cos_sin.shape[0], r,
                                        1 if neox_style else 0, _ptr(query_start), T, int(max_query_len),
-                                       block_tables.data_ptr(), M, context_lens.data_ptr(), B, ctypes.byref(c),
-                                       ctypes.byref(d), _stream(stream, dev)), "paged_kv_write_rope_q8")
+                                       block_tables.data_ptr(), M, context_lens.data_ptr(), B, c,
+                                       d, _stream(stream, dev)), "paged_kv_write_rope_q8")
 
 
 def _rope_table(cos_sin, positions, r: int, tokens: int, dev: int) -> int:
@@ -824,11 +827,10 @@ def paged_kv_read_q8(k_out: torch.Tensor, v_out: torch.Tensor, k_cache: torch.Te
     """Each sequence's newest query_start[b+1] - query_start[b] tokens back as bf16 rows
     query_start[b] .. of k_out and v_out [T, Hkv, D] (the tokens may be strided)."""
     dev, T, sk, sv = _q8_rows(k_out, v_out, k_cache, ("k_out", "v_out"))
-    c, d = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
-    B, M = block_tables.shape
+    c, d, H, B, M = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
     _check(_lib.paged_kv_read_q8(k_out.data_ptr(), v_out.data_ptr(), sk, sv, _ptr(query_start), T,
                                  int(max_query_len), block_tables.data_ptr(), M, context_lens.data_ptr(), B,
-                                 ctypes.byref(c), ctypes.byref(d), _stream(stream, dev)), "paged_kv_read_q8")
+                                 c, d, _stream(stream, dev)), "paged_kv_read_q8")
 
 
 def paged_decode_q8_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -874,14 +876,14 @@ def paged_decode_attention_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torch
     any sizes in turn; it may be omitted as there."""
     dev = _home(q)
     _q8_query(out, q, k_cache, context_lens.shape[0], dev)
-    c, d = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
-    B, Hq, D = q.shape
+    c, d, H, B, M = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    _, Hq, D = q.shape
     workspace = _q8_workspace(workspace, 0 if workspace is not None else paged_decode_q8_workspace_size(
-        B, Hq, d.num_kv_heads, D, int(max_context_len)), True, q, dev, stream)
+        B, Hq, H, D, int(max_context_len)), True, q, dev, stream)
     _check(_lib.paged_decode_attention_q8(
-        out.data_ptr(), q.data_ptr(), ctypes.byref(c), block_tables.data_ptr(), block_tables.shape[1],
-        context_lens.data_ptr(), int(max_context_len), B, Hq, ctypes.byref(d), float(scale), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream, dev)), "paged_decode_attention_q8")
+        out.data_ptr(), q.data_ptr(), c, block_tables.data_ptr(), M,
+        context_lens.data_ptr(), int(max_context_len), B, Hq, d, float(scale), workspace.data_ptr(),
+        workspace.nbytes, _stream(stream, dev)), "paged_decode_attention_q8")
 
 
 def paged_decode_step_q8(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -893,16 +895,16 @@ def paged_decode_step_q8(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
     paged_decode_attention_q8 of q [B, Hq, D] (k, v [B, Hkv, D], tokens may be strided)."""
     dev, T, sk, sv = _q8_rows(k, v, k_cache)
     _q8_query(out, q, k_cache, T, dev)
-    c, d = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
-    B, Hq, D = q.shape
-    if context_lens.shape != (B,):
+    c, d, H, B, M = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    _, Hq, D = q.shape
+    if B != T:
         raise ValueError("q, k and v need one row per sequence")
     workspace = _q8_workspace(workspace, 0 if workspace is not None else paged_decode_q8_workspace_size(
-        B, Hq, d.num_kv_heads, D, int(max_context_len)), True, q, dev, stream)
+        B, Hq, H, D, int(max_context_len)), True, q, dev, stream)
     _check(_lib.paged_decode_step_q8(
-        out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), sk, sv, ctypes.byref(c), block_tables.data_ptr(),
-        block_tables.shape[1], context_lens.data_ptr(), int(max_context_len), B, Hq, ctypes.byref(d), float(scale),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream, dev)),
+        out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), sk, sv, c, block_tables.data_ptr(),
+        M, context_lens.data_ptr(), int(max_context_len), B, Hq, d, float(scale),
+        workspace.data_ptr(), workspace.nbytes, _stream(stream, dev)),
         "paged_decode_step_q8")
 
 
@@ -921,18 +923,18 @@ def paged_decode_step_rope_q8(out: torch.Tensor, q: torch.Tensor, k: torch.Tenso
     if q.shape != q_out.shape:
         raise ValueError("q_out must have q's shape")
     sq = _packed(q, "q", T, k.shape[2], dev)
-    c, d = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
-    B, Hq, D = q.shape
-    if context_lens.shape != (B,):
+    c, d, H, B, M = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    _, Hq, D = q.shape
+    if B != T:
         raise ValueError("q, k and v need one row per sequence")
     r = _rope_table(cos_sin, positions, D if rotary_dim is None else int(rotary_dim), T, dev)
     workspace = _q8_workspace(workspace, 0 if workspace is not None else paged_decode_q8_workspace_size(
-        B, Hq, d.num_kv_heads, D, int(max_context_len)), True, q, dev, stream)
+        B, Hq, H, D, int(max_context_len)), True, q, dev, stream)
     _check(_lib.paged_decode_step_rope_q8(
         out.data_ptr(), q.data_ptr(), sq, q_out.data_ptr(), k.data_ptr(), v.data_ptr(), sk, sv, _ptr(positions),
-        cos_sin.data_ptr(), cos_sin.shape[0], r, 1 if neox_style else 0, ctypes.byref(c), block_tables.data_ptr(),
-        block_tables.shape[1], context_lens.data_ptr(), int(max_context_len), B, Hq, ctypes.byref(d), float(scale),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream, dev)),
+        cos_sin.data_ptr(), cos_sin.shape[0], r, 1 if neox_style else 0, c, block_tables.data_ptr(),
+        M, context_lens.data_ptr(), int(max_context_len), B, Hq, d, float(scale),
+        workspace.data_ptr(), workspace.nbytes, _stream(stream, dev)),
         "paged_decode_step_rope_q8")
 
 
@@ -947,14 +949,13 @@ def paged_prefill_attention_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torc
     _q8_query(out, q, k_cache, None, dev)
     if query_start is None:
         raise ValueError("query_start must be [B + 1]")
-    c, d = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
-    B, M = block_tables.shape
+    c, d, H, B, M = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
     workspace = _q8_workspace(workspace, 0 if workspace is not None else paged_prefill_q8_workspace_size(
-        B, d.num_kv_heads, d.head_dim, d.block_size, int(max_context_len)), False, q, dev, stream)
+        B, H, q.shape[2], k_cache.shape[2], int(max_context_len)), False, q, dev, stream)
     _check(_lib.paged_prefill_attention_q8(
-        out.data_ptr(), q.data_ptr(), q.shape[0], ctypes.byref(c), block_tables.data_ptr(), M, context_lens.data_ptr(),
-        int(max_context_len), query_start.data_ptr(), int(max_query_len), B, q.shape[1], ctypes.byref(d),
-        float(scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream, dev)),
+        out.data_ptr(), q.data_ptr(), q.shape[0], c, block_tables.data_ptr(), M, context_lens.data_ptr(),
+        int(max_context_len), query_start.data_ptr(), int(max_query_len), B, q.shape[1], d,
+        float(scale), workspace.data_ptr(), workspace.nbytes, _stream(stream, dev)),
         "paged_prefill_attention_q8")
 
 
@@ -983,7 +984,8 @@ def _q8_layers(dev: int, k_caches, v_caches, k_scales, v_scales, where: str):
     for i, tensors in enumerate(layers):
         if tensors[0].shape != first.shape or tensors[0].dtype != first.dtype:
             raise ValueError(f"{where}: the layers' caches must be alike")
-        out[i], d = _q8_cache(dev, *tensors, *none)
+        c, d, *_ = _q8_cache(dev, *tensors, *none)
+        out[i] = pkv_q8_cache.from_buffer_copy(c)
     return out, len(layers), d, first
 
 
@@ -1004,7 +1006,7 @@ def paged_kv_copy_blocks_q8(k_caches, v_caches, k_scales, v_scales, block_pairs:
     if num_tokens is not None and num_tokens.shape != shape[:1]:
         raise ValueError("num_tokens must have one entry per pair")
     _check(_lib.paged_kv_copy_blocks_q8(ctypes.addressof(caches), n, block_pairs.data_ptr(), _ptr(num_tokens),
-                                        shape[0], ctypes.byref(d), _stream(stream, dev)), "paged_kv_copy_blocks_q8")
+                                        shape[0], d, _stream(stream, dev)), "paged_kv_copy_blocks_q8")
 
 
 def paged_kv_compact_q8(k_caches, v_caches, k_scales, v_scales, block_moves: torch.Tensor,
@@ -1027,11 +1029,11 @@ def paged_kv_compact_q8(k_caches, v_caches, k_scales, v_scales, block_moves: tor
     if block_tables is not None:
         if block_tables.dim() != 2:
             raise ValueError("block_tables must be [B, M]")
-        if block_map is None or block_map.shape != (d.num_blocks,):
+        if block_map is None or block_map.shape != first.shape[:1]:
             raise ValueError("block_tables need a block_map with one entry per block")
         rows, cols = block_tables.shape
     _check(_lib.paged_kv_compact_q8(ctypes.addressof(caches), n, block_moves.data_ptr(), None, shape[0],
-                                    _ptr(block_tables), rows, cols, _ptr(block_map), ctypes.byref(d),
+                                    _ptr(block_tables), rows, cols, _ptr(block_map), d,
                                     _stream(stream, dev)), "paged_kv_compact_q8")
 
 
