@@ -105,6 +105,7 @@ struct Q8Args {
   int32_t depth;                // 1: the first map leads to the other pool too
   int32_t v_first;              // V's rows lie first in a box
   float scale_log2;
+  int32_t step;  // behind a step's write: only the new tokens' pages, and q, are to be waited for
 };
 
 // A stage is filled by 128-byte-swizzled boxes, one pool's rows of a box and then the other's: rows
@@ -667,6 +668,7 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
   int64_t *const s_sums = reinterpret_cast<int64_t *>(cta_ptr + SL::sums);
   int64_t *const s_incl = reinterpret_cast<int64_t *>(cta_ptr + SL::incl);
 
+  if (!a.step) q8::await_stream();
   const int Hkv = a.num_kv_heads;
   const int cap = (int)min((int64_t)a.max_blocks * a.block_size, (int64_t)a.max_len);
   auto length = [&](int b) { return min(max(__ldg(a.lens + b), 0), cap); };
@@ -734,7 +736,10 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) total += s_sums[w];
   const int64_t W = total * Hkv, N = shares_of(W);
-  if (W == 0 || share >= N) return;  // (no barrier of the whole CTA follows)
+  if (W == 0 || share >= N) {  // (no barrier of the whole CTA follows)
+    if (a.step) q8::await_stream();  // the grid's end is the write's end, whoever has work
+    return;
+  }
   const int64_t lo = q8::quotient(W * share, N), hi = q8::quotient(W * (share + 1), N);
   auto timeout = [&] {
     if (lane == 0) {
@@ -811,7 +816,7 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
     Q8Desc dsc;
     dsc.pad = 0;
     bool first = true, last = false;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the step's write is done
+    q8::await_stream();  // the step's write is done
     int i = 0;
     for (; !last; ++i) {
       const int s = i % STAGES;
@@ -987,7 +992,7 @@ int check_decode_q8(const DecodeQ8 &x, const char *fn) {
 }
 
 template <int D, int KIND>
-int launch_decode_q8(const DecodeQ8 &x, cudaStream_t stream, bool programmatic) {
+int launch_decode_q8(const DecodeQ8 &x, cudaStream_t stream, bool step) {
   const pkv_cache_desc &c = *x.desc;
   CUtensorMap tm0, tm1 = {};
   int sms = 0;
@@ -1041,35 +1046,27 @@ int launch_decode_q8(const DecodeQ8 &x, cudaStream_t stream, bool programmatic) 
   a.log2_box = ilog2(box);
   a.depth = depth ? 1 : 0;
   a.v_first = v_first ? 1 : 0;
+  a.step = step ? 1 : 0;
   a.scale_log2 = x.scale * kLog2e;
   // one CTA per SM; fewer where the batch cannot have that many shares
   const int64_t most =
       (((int64_t)x.max_len + kQ8Keys - 1) / kQ8Keys * kChunkCost + kEndCost) * x.num_seqs * c.num_kv_heads;
   const int64_t ctas = std::min(sms, kQ8MaxShares / q8_groups(D));
   const int64_t grid = std::max<int64_t>(1, std::min(ctas, most / kMinCost));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, 1, 1);
-  cfg.blockDim = dim3(q8_threads(D), 1, 1);
-  cfg.dynamicSmemBytes = q8_smem(D);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = programmatic ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tm0, tm1, a);
+  const cudaError_t e =
+      q8::launch_early(kern, dim3((unsigned)grid), q8_threads(D), q8_smem(D), stream, tm0, tm1, a);
   if (e != cudaSuccess) return cuda_error(e, "decode_q8_kernel launch");
   return PKV_OK;
 }
 
-int launch_decode_q8(const DecodeQ8 &x, cudaStream_t s, bool programmatic) {
+int launch_decode_q8(const DecodeQ8 &x, cudaStream_t s, bool step) {
   if (x.num_seqs == 0) return PKV_OK;
   const bool i8 = x.cache->kind == PKV_Q8_INT8;
   if (x.desc->head_dim == 64)
-    return i8 ? launch_decode_q8<64, PKV_Q8_INT8>(x, s, programmatic)
-              : launch_decode_q8<64, PKV_Q8_E4M3>(x, s, programmatic);
-  return i8 ? launch_decode_q8<128, PKV_Q8_INT8>(x, s, programmatic)
-            : launch_decode_q8<128, PKV_Q8_E4M3>(x, s, programmatic);
+    return i8 ? launch_decode_q8<64, PKV_Q8_INT8>(x, s, step)
+              : launch_decode_q8<64, PKV_Q8_E4M3>(x, s, step);
+  return i8 ? launch_decode_q8<128, PKV_Q8_INT8>(x, s, step)
+            : launch_decode_q8<128, PKV_Q8_E4M3>(x, s, step);
 }
 
 // The rows of a few queries per sequence as sequences of their own: query i of n sees the context's
@@ -1081,6 +1078,8 @@ struct RowsArgs {
   int32_t num_seqs, num_queries, max_new, cap;
 };
 __global__ void __launch_bounds__(256) query_rows_kernel(const RowsArgs a) {
+  q8::await_stream();
+  q8::let_next_begin();
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i < 2 * kQ8MaxShares) a.counters[i] = 0u;
   if (i < a.num_seqs) {
@@ -1133,8 +1132,8 @@ int launch_rows_q8(const ChunkLaunch &l, const pkv_q8_cache &cache, const pkv_ca
   r.max_new = l.max_query_len;
   r.cap = l.max_context;
   const int threads = std::max({2 * kQ8MaxShares, r.num_seqs, r.num_queries});
-  query_rows_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(r);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      q8::launch_early(query_rows_kernel, dim3((unsigned)((threads + 255) / 256)), 256, 0, stream, r);
   if (e != cudaSuccess) return cuda_error(e, "query_rows_kernel launch");
   const DecodeQ8 x = {r.row_seqs, l.out, l.q, &cache, block_tables, max_blocks, r.row_lens, l.max_context,
                       r.num_queries, l.num_q_heads, &c, l.scale, workspace, decode};

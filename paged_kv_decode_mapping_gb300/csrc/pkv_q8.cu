@@ -201,8 +201,8 @@ __device__ __forceinline__ void rotate_q(const WriteArgs &a, const Tokens &t, ui
 template <int D, int KIND, bool ROPE, int U>
 __global__ void __launch_bounds__(2 * kQ8Threads, ROPE ? 3 : 4) write_q8_kernel(const __grid_constant__ WriteArgs a) {
   constexpr int V = D / 8;  // vectors of a row: 8 bf16 in, 8 codes out
-  // A decode kernel behind this one may start its set-up (paged_decode_step_q8).
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  q8::await_stream();
+  q8::let_next_begin();  // a step's decode: its set-up
   const int b = blockIdx.z;
   const bool is_v = blockIdx.y;
   bool bad;
@@ -390,6 +390,7 @@ struct UnitArgs {
 constexpr int kUnitThreads = 1024;
 __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_constant__ UnitArgs a) {
   static_assert(kUnitThreads == 32 * 32, "a warp joins the warps' results");
+  q8::await_stream();
   __shared__ float s_k[kUnitThreads], s_v[kUnitThreads];
   __shared__ int s_before[32], s_rank[32];
   const int b = blockIdx.x, H = a.s.num_kv_heads, tid = threadIdx.x;
@@ -454,6 +455,7 @@ __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_con
 template <int D, int KIND, bool WHOLE, int U>
 __global__ void __launch_bounds__(kQ8Threads, U == 16 ? 5 : 8) read_q8_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int V = D / 8;  // vectors of a row: 8 codes in, 8 bf16 out
+  q8::await_stream();
   const int tid = threadIdx.x, lane = tid & 31, group = 1 << a.log2_group, gt = tid & (group - 1);
   const int b = blockIdx.z;
   const bool is_v = blockIdx.y;
@@ -647,8 +649,7 @@ int launch_read(const Span &s, const pkv_q8_cache &q, const pkv_cache_desc &c, v
                              : read_q8_kernel<d(), kind(), false, 4>;
   };
   void (*const kern)(const ReadArgs) = of_kinds(c.head_dim, q.kind, pick);
-  kern<<<ctas, kQ8Threads, 0, stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = q8::launch_early(kern, ctas, kQ8Threads, 0, stream, a);
   if (e != cudaSuccess) return cuda_error(e, "read_q8_kernel launch");
   return PKV_OK;
 }
@@ -750,8 +751,7 @@ int launch_write_q8(const WriteQ8 &w, cudaStream_t stream) {
                              : write_q8_kernel<d(), kind(), false, 8>;
   };
   void (*const kern)(const WriteArgs) = of_kinds(c.head_dim, w.cache->kind, pick);
-  kern<<<dim3(ctas, 2, (unsigned)w.num_seqs), threads, 0, stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = q8::launch_early(kern, dim3(ctas, 2, (unsigned)w.num_seqs), threads, 0, stream, a);
   if (e != cudaSuccess) return cuda_error(e, "write_q8_kernel launch");
   return PKV_OK;
 }
@@ -945,8 +945,7 @@ PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t
   u.order = reinterpret_cast<int4 *>(ws + p.order);
   u.num_queries = (int32_t)num_queries;
   u.max_query_len = max_query_len;
-  units_q8_kernel<<<(unsigned)num_seqs, kUnitThreads, 0, s>>>(u);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = q8::launch_early(units_q8_kernel, dim3((unsigned)num_seqs), kUnitThreads, 0, s, u);
   if (e != cudaSuccess) return cuda_error(e, "units_q8_kernel launch");
   const int64_t stride = (int64_t)desc->num_kv_heads * desc->head_dim;
   rc = launch_read(span, *cache, *desc, ws + p.k, ws + p.v, stride, stride, p.rows, u.k_unit, u.v_unit,

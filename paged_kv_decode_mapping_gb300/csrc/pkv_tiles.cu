@@ -10,6 +10,7 @@
 #include <type_traits>
 
 #include "attn_tc.cuh"
+#include "q8_device.cuh"
 #include "shared_device.cuh"
 
 namespace pkv {
@@ -602,6 +603,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int G = a.group, tile_rows = a.tile_tokens * G;
   // the decode kernel that merges may start its own part while this one runs
   if constexpr (kPaged) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (MODE == kNewest) q8::await_stream();
   auto blk = [&](int t, int i) { return kShareKeys ? i : 2 * i + t; };
 
   // kPrompt: the K producer looks for the first item while the others set up.
@@ -1229,8 +1231,13 @@ int launch_prompt(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensor
                   const TileArgs &a, unsigned grid, cudaStream_t stream) {
   const int rc = prepare_tile_kernel<D, MODE>();
   if (rc) return rc;
-  tile_kernel<D, MODE><<<grid, kTileThreads, tile_smem<D, MODE>(), stream>>>(tmq, tmk, tmv, a);
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if constexpr (MODE == kNewest) {
+    e = q8::launch_early(tile_kernel<D, MODE>, dim3(grid), kTileThreads, tile_smem<D, MODE>(), stream, tmq, tmk, tmv, a);
+  } else {
+    tile_kernel<D, MODE><<<grid, kTileThreads, tile_smem<D, MODE>(), stream>>>(tmq, tmk, tmv, a);
+    e = cudaGetLastError();
+  }
   return e == cudaSuccess ? PKV_OK : cuda_error(e, "tile_kernel launch");
 }
 

@@ -9,6 +9,31 @@
 namespace pkv {
 namespace q8 {
 
+// The 8-bit cache's kernels are launched while the one ahead of them in the stream may still run,
+// and begin by waiting for its end: their launch and its end overlap (calls one after another, 16
+// contexts of 2048 keys: a decode every 13.1 us instead of 14.8; 256 contexts 41.1 instead of 43.3).
+__device__ __forceinline__ void await_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// From here on the kernel behind this one may be launched; await_stream() first, unless what that one
+// reads before its own await_stream() is older than both.
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e != cudaSuccess) (void)cudaGetLastError();  // (handed on, not left behind)
+  return e;
+}
+
 // n / d for n >= 0, d > 0, by 32 bits where that is enough (a 64-bit division takes 0.2 us).
 __device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
   if (((n | d) >> 32) == 0) return (uint32_t)n / (uint32_t)d;

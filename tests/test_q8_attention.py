@@ -537,6 +537,73 @@ def test_two_graphs_share_a_workspace(B):
     assert B.pkv_device_errors() == 0
 
 
+def test_behind_other_work(B):
+    """Calls right behind what makes their inputs: kernels, copies and fills of the same stream, another
+    stream's end; one after another and as a graph with a fork and a join."""
+    b = Batch([500, 33, 900], torch.int8, 2, 64, 16, seed=68)
+    side, main = torch.cuda.Stream(), torch.cuda.Stream()
+    new = [b.randn(3, 6 + 4, 64) for _ in range(4)]
+    big = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+    x, src = torch.zeros_like(new[0]), torch.zeros_like(new[0])
+    cl, bt, chunk = torch.zeros_like(b.cl), torch.zeros_like(b.bt), starts([1, 1, 1])
+    q, k, v = x.split([6, 2, 2], dim=1)
+    qc = torch.empty(3, 6, 64, dtype=torch.bfloat16, device=DEV)
+    kr, vr = (torch.empty(3, 2, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    ws = torch.zeros(B.paged_decode_q8_workspace_size(3, 6, 2, 64, 900), dtype=torch.uint8, device=DEV)
+    cws = torch.empty(B.paged_prefill_q8_workspace_size(3, 2, 64, 16, 900), dtype=torch.uint8, device=DEV)
+    outs = [torch.empty_like(qc) for _ in range(3)]
+    cache = b.cache()
+
+    def work():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            big.fill_(1)
+            cl.copy_(b.cl)              # (late, behind the fill)
+            bt.copy_(b.bt)
+        x.copy_(src)
+        qc.copy_(q)
+        here.wait_stream(side)
+        B.paged_decode_step_q8(outs[0], qc, k, v, *cache, bt, cl, 900, 0.125, workspace=ws)
+        big.zero_()
+        outs[1].fill_(3)
+        B.paged_decode_attention_q8(outs[1], qc, *cache, bt, cl, 900, 0.125, workspace=ws)
+        B.paged_prefill_attention_q8(outs[2], qc, *cache, bt, cl, 900, chunk, 1, 0.125, workspace=cws)
+        big.zero_()
+        B.paged_kv_read_q8(kr, vr, *cache, bt, cl, chunk, 1)
+        qc.zero_()
+        x.zero_()
+        cl.zero_()
+        bt.fill_(-1)
+
+    def checked(i, run):
+        want = b.copies()
+        src.copy_(new[i])
+        for s, n in enumerate(b.lens):
+            R.write(want[0], want[2], new[i][s:s + 1, 6:8], b.tables[s], n - 1)
+            R.write(want[1], want[3], new[i][s:s + 1, 8:], b.tables[s], n - 1)
+        torch.cuda.synchronize()
+        run()
+        torch.cuda.synchronize()
+        for got, w in zip(cache, want):
+            same(got, w, "cache")
+        for o in outs:
+            check(o, *decode_ref(b, new[i][:, :6], 0.125), f"run {i}")
+        for s, n in enumerate(b.lens):
+            for got, c, sc in ((kr, b.k, b.ks), (vr, b.v, b.vs)):
+                assert torch.equal(got[s], R.values(c, sc, b.tables[s], n - 1, n)[0].to(torch.bfloat16))
+
+    with torch.cuda.stream(main):
+        checked(0, work)
+        checked(1, work)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        work()
+    checked(2, graph.replay)
+    checked(3, graph.replay)
+    assert B.pkv_device_errors() == 0
+
+
 @pytest.mark.parametrize("dtype", R.KINDS)
 @pytest.mark.parametrize("d,bs", [(64, 16), (128, 32)])
 def test_prompts_chunks_drafts_forks_and_steps(B, dtype, d, bs):
