@@ -453,6 +453,7 @@ int prompt_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k, const 
  * to 2^-10 / 448 of the largest.  head_dim 64 or 128; block_size a power of two in [8, 256];
  * num_blocks * num_kv_heads * block_size < 2^31; caches 16-byte, scales 4-byte aligned.
  * Pages and scales need no initial values: a page begins with the write of its first row.
+ * Scales that a caller makes are 0, NaN, or of 2^-126 or more.
  */
 enum { PKV_Q8_E4M3 = 0, PKV_Q8_INT8 = 1 };
 typedef struct pkv_q8_cache {
@@ -573,11 +574,12 @@ int paged_decode_step_rope_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t q_stride
  * [num_queries][num_q_heads][head_dim], sequence b's newest tokens at rows query_start[b] ..
  * query_start[b+1]-1.  The contexts are read back as fp16 rows into the workspace
  * (paged_prefill_q8_workspace_size() bytes, no initial values; not for two calls that overlap),
- * scores and weights are fp16 products with fp32 sums as in paged_decode_attention_q8.
+ * scores and weights are fp16 products with fp32 sums as in paged_decode_attention_q8; or, where
+ * that is estimated to be less (up to 32 queries of a sequence), each query is a row of its kernel.
  * max_query_len and max_context_len bound every length; longer ones, and sequences of more queries
  * than tokens, raise PKV_DEVERR_CONTEXT_LEN (they are cut; a query before the first token gives
- * zeros).  Rows of no sequence are not written.  A page of scale NaN (see paged_kv_write_q8) may make
- * queries NaN from fewer than 128 + 128 / (num_q_heads / num_kv_heads) tokens before it on.
+ * zeros).  Rows of no sequence are not written.  A page of scale NaN (see paged_kv_write_q8) makes
+ * those queries NaN that see it.
  */
 size_t paged_prefill_q8_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim,
                                        int32_t max_context_len);

@@ -793,10 +793,14 @@ def paged_kv_write_rope_q8(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tens
     sq = so = heads = 0
     if q is not None:
         q_out = q if q_out is None else q_out
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-        sq, so = _packed(q, "q", T, k.shape[2], dev), _packed(q_out, "q_out", T, k.shape[2], dev)
-        heads = q.shape[1]
+        shape, D = q.shape, k.shape[2]
+        if len(shape) != 3 or q_out.shape != shape:
+            raise ValueError("q must be [T, Hq, D], and q_out alike")
+        (sq, h, one), (so, h_out, one_out) = q.stride(), q_out.stride()
+        if not (q.dtype is _BF16 and q_out.dtype is _BF16 and q.get_device() == dev == q_out.get_device() and
+                shape[0] == T > 1 and shape[2] == D and one == 1 == one_out and h == D == h_out):
+            sq, so = _packed(q, "q", T, D, dev), _packed(q_out, "q_out", T, D, dev)
+        heads = shape[1]
     elif q_out is not None:
         raise ValueError("q_out without q")
     r = _rope_table(cos_sin, positions, k.shape[2] if rotary_dim is None else int(rotary_dim), T, dev)
@@ -808,12 +812,14 @@ def paged_kv_write_rope_q8(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tens
 
 
 def _rope_table(cos_sin, positions, r: int, tokens: int, dev: int) -> int:
-    if not (_fine(dev, torch.float32, cos_sin) and _fine(dev, torch.int64, positions)):
+    if not (cos_sin.dtype is _F32 and cos_sin.get_device() == dev and cos_sin.is_contiguous() and
+            (positions is None or _fine(dev, torch.int64, positions))):
         _need(cos_sin, "cos_sin", torch.float32, 2)
         if positions is not None:
             _need(positions, "positions", torch.int64, 1)
         raise ValueError("cos_sin and positions: on another device than the rows")
-    if cos_sin.dim() != 2 or cos_sin.shape[1] != r:
+    shape = cos_sin.shape
+    if len(shape) != 2 or shape[1] != r:
         raise ValueError("cos_sin must be [max_position, rotary_dim]")
     if positions is not None and positions.shape != (tokens,):
         raise ValueError("positions must have one entry per token")

@@ -190,6 +190,7 @@ struct ChunkLaunch {
   const pkv_bf16 *q;
   const uint16_t *k, *v;
   const float *k_unit, *v_unit;
+  const int32_t *nan_from;  // [num_seqs][num_kv_heads] rows that see this key are NaN (its row is 0)
   const int4 *order;  // [num_seqs] as the tiles take them: a sequence, its first query row, its rows
   const int32_t *query_start, *context_lens;
   int64_t num_queries;

@@ -383,6 +383,7 @@ struct UnitArgs {
   Span s;
   const float *k_scale, *v_scale;
   float *k_unit, *v_unit;
+  int32_t *nan_from;  // the first key of a page whose scale is NaN
   const int32_t *start;
   int4 *order;
   int32_t num_queries, max_query_len;
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_con
   static_assert(kUnitThreads == 32 * 32, "a warp joins the warps' results");
   q8::await_stream();
   __shared__ float s_k[kUnitThreads], s_v[kUnitThreads];
-  __shared__ int s_before[32], s_rank[32];
+  __shared__ int s_before[32], s_rank[32], s_nan[kUnitThreads];
   const int b = blockIdx.x, H = a.s.num_kv_heads, tid = threadIdx.x;
   const int cap = (int)min((int64_t)a.s.max_blocks * a.s.block_size, (int64_t)a.s.max_new);
   const int L = min(max(__ldg(a.s.lens + b), 0), cap), pages = (L + a.s.block_size - 1) >> a.s.log2_bs;
@@ -424,16 +425,20 @@ __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_con
     const int wide = min(H - h0, kUnitThreads), rows = kUnitThreads / wide;
     const int h = tid % wide, r = tid / wide;
     float k = 0.f, v = 0.f;
+    int bad = pages;  // the first page of scale NaN
     if (r < rows)
 #pragma unroll 4
       for (int p = r; p < pages; p += rows) {
         int64_t phys = __ldg(row + p);
         if (phys < 0 || phys >= a.s.num_blocks) phys = 0;  // (flagged by the reading)
-        k = fmaxf(k, __ldg(a.k_scale + phys * H + h0 + h));
-        v = fmaxf(v, __ldg(a.v_scale + phys * H + h0 + h));
+        const float ks = __ldg(a.k_scale + phys * H + h0 + h), vs = __ldg(a.v_scale + phys * H + h0 + h);
+        if (ks != ks || vs != vs) bad = min(bad, p);
+        k = fmaxf(k, ks);
+        v = fmaxf(v, vs);
       }
     s_k[tid] = k;
     s_v[tid] = v;
+    s_nan[tid] = bad;
     __syncthreads();
     int half = 1;
     while (2 * half < rows) half *= 2;
@@ -441,12 +446,14 @@ __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_con
       if (r < half && r + half < rows) {
         s_k[tid] = k = fmaxf(k, s_k[tid + half * wide]);
         s_v[tid] = v = fmaxf(v, s_v[tid + half * wide]);
+        s_nan[tid] = bad = min(bad, s_nan[tid + half * wide]);
       }
       __syncthreads();
     }
     if (tid < wide) {
       a.k_unit[(int64_t)b * H + h0 + tid] = k;
       a.v_unit[(int64_t)b * H + h0 + tid] = v;
+      a.nan_from[(int64_t)b * H + h0 + tid] = (int32_t)min((int64_t)bad << a.s.log2_bs, (int64_t)0x7fffffff);
     }
     __syncthreads();
   }
@@ -491,7 +498,7 @@ __global__ void __launch_bounds__(kQ8Threads, U == 16 ? 5 : 8) read_q8_kernel(co
     scale = __ldg((is_v ? a.v_scale : a.k_scale) + unit + lane);
     if constexpr (WHOLE) {
       const float of = __ldg((is_v ? a.v_unit : a.k_unit) + (int64_t)b * a.s.num_kv_heads + h0 + lane);
-      scale = of > 0.f ? __fdiv_rn(scale, of) : scale * 0.f;  // (a NaN stays)
+      scale = of > 0.f ? __fdiv_rn(scale, of) : scale * 0.f;
     }
   }
   const uint2 *const src = reinterpret_cast<const uint2 *>((is_v ? a.v_cache : a.k_cache) + unit * a.s.block_size * D) + gt % V;
@@ -512,8 +519,10 @@ __global__ void __launch_bounds__(kQ8Threads, U == 16 ? 5 : 8) read_q8_kernel(co
       const int at = r + u * rows_apart, in = at & (a.s.block_size - 1), h = at >> a.s.log2_bs;
       const float s = __shfl_sync(0xffffffffu, scale, h & 31);  // (a warp's rows are of one head)
       if (!kAll && (at >= rows || in < r0 || in >= r1)) continue;
-      const uint64_t s2 = q8::f32x2(s, s);
-      const uint32_t w[2] = {x[u].x, x[u].y};
+      // (zeros for a page of scale NaN: a NaN among the keys would reach rows that do not see it)
+      const bool none = WHOLE && s != s;
+      const uint64_t s2 = none ? 0u : q8::f32x2(s, s);
+      const uint32_t w[2] = {none ? 0u : x[u].x, none ? 0u : x[u].y};
       uint32_t o[4];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -829,7 +838,7 @@ namespace {
 
 struct PrefillLayout {
   int32_t rows;  // packed rows of a sequence
-  size_t k, v, k_unit, v_unit, order, total;
+  size_t k, v, k_unit, v_unit, nan_from, order, total;
 };
 constexpr int kMaxRowQueries = 32, kMaxRows = 65535;  // of a sequence, of a call, as the decode's rows
 int64_t row_capacity(int32_t num_seqs) { return std::min((int64_t)num_seqs * kMaxRowQueries, (int64_t)kMaxRows); }
@@ -862,7 +871,8 @@ bool prefill_layout(int32_t num_seqs, int32_t hkv, int32_t d, int32_t max_len, i
   p->v = rows;
   p->k_unit = 2 * rows;
   p->v_unit = p->k_unit + units;
-  p->order = p->v_unit + units;
+  p->nan_from = p->v_unit + units;
+  p->order = p->nan_from + units;
   p->total = std::max(p->order + up((size_t)num_seqs * sizeof(int4)),  // either way
                       up(rows_q8_workspace((int32_t)row_capacity(num_seqs), d, sms)));
   return true;
@@ -941,6 +951,7 @@ PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t
   u.v_scale = cache->v_scale;
   u.k_unit = reinterpret_cast<float *>(ws + p.k_unit);
   u.v_unit = reinterpret_cast<float *>(ws + p.v_unit);
+  u.nan_from = reinterpret_cast<int32_t *>(ws + p.nan_from);
   u.start = query_start;
   u.order = reinterpret_cast<int4 *>(ws + p.order);
   u.num_queries = (int32_t)num_queries;
@@ -955,6 +966,7 @@ PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t
   l.v = reinterpret_cast<const uint16_t *>(ws + p.v);
   l.k_unit = u.k_unit;
   l.v_unit = u.v_unit;
+  l.nan_from = u.nan_from;
   l.order = u.order;
   rc = launch_chunk(l, s);
   if (!rc) clear_error();

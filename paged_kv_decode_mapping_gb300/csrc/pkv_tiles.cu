@@ -76,6 +76,7 @@ struct TileArgs {
   // newest tokens (and context_lens)
   int32_t kv_rows, max_context;    // packed rows of a sequence; the longest context
   const float *k_unit, *v_unit;    // [num][num_kv_heads]
+  const int32_t *nan_from;         // [num][num_kv_heads] rows that see this key are NaN
   const int4 *order;               // [num] longest context first: a sequence, its first query row, its rows
 };
 
@@ -750,6 +751,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int64_t unit = (int64_t)it.seq * a.num_kv_heads + it.g;
         const float k_unit = __ldg(a.k_unit + unit);
         v_unit = __ldg(a.v_unit + unit);
+        if (see > __ldg(a.nan_from + unit)) v_unit = __int_as_float(0x7fc00000);
         if (nb > 0) {
           if (!(ok = warp_wait(q_full(t), on & 1))) {
             if (lane == 0) fail(false);
@@ -1309,6 +1311,7 @@ int launch_chunk(const ChunkLaunch &l, cudaStream_t stream) {
   a.max_context = l.max_context;
   a.k_unit = l.k_unit;
   a.v_unit = l.v_unit;
+  a.nan_from = l.nan_from;
   a.order = l.order;
   const int64_t tiles = l.num_queries / (2 * a.tile_tokens) + std::min<int64_t>(l.num_seqs, l.num_queries);
   if (l.num_queries > 0x7fffff00LL || tiles > 0x7fffffffLL / l.num_kv_heads)

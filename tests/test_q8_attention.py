@@ -361,6 +361,40 @@ def test_prefill_of_hard_values(B, new):
     assert B.pkv_device_errors() == 0
 
 
+@pytest.mark.parametrize("dtype", R.KINDS)
+@pytest.mark.parametrize("new", [20, 220])  # as rows of the decode, and on the tiles
+def test_prefill_not_finite(B, dtype, new):
+    """A page of scale NaN makes the queries NaN that see it and no others; a query's NaN its row."""
+    lens, bs = [300, 250, 900], 16
+    b = Batch(lens, dtype, 2, 64, bs, seed=53)
+    q = b.randn(3 * new, 4, 64)
+    start = starts([new] * 3)
+    marks = [(0, b.vs, 1, lens[0] - 9), (1, b.ks, 0, lens[1] - 17), (2, b.vs, 0, 40)]  # sequence, scales, kv head, key
+    nan = torch.zeros(3 * new, 4, dtype=torch.bool)
+    for s, scales, g, key in marks:
+        page = key // bs
+        scales[b.tables[s][page], g] = math.nan
+        if dtype is torch.float8_e4m3fn:  # as the write leaves it
+            R.bits(b.v if scales is b.vs else b.k)[b.tables[s][page], g, 3:] = 0x7f
+        first = max(page * bs - (lens[s] - new), 0)  # the query at the page's first token sees it
+        nan[s * new + first:(s + 1) * new, 2 * g:2 * g + 2] = True
+    q[2 * new + 5, 3, 9] = math.nan
+    nan[2 * new + 5, 3] = True
+    out = torch.full_like(q, 77.0)
+    B.paged_prefill_attention_q8(out, q, *b.cache(), b.bt, b.cl, max(lens), start, new, 0.125)
+    assert torch.equal(out.isnan().all(-1).cpu(), nan) and torch.equal(out.isnan().any(-1).cpu(), nan)
+    for s, n in enumerate(lens):
+        k, v = (R.values(c, sc, b.tables[s], 0, n, torch.float64).nan_to_num(0.0) for c, sc in ((b.k, b.ks), (b.v, b.vs)))
+        rows = slice(s * new, (s + 1) * new)
+        seen = torch.arange(n, device=DEV)[None, :] <= torch.arange(n - new, n, device=DEV)[:, None]
+        want, mag = R.attention(q[rows].nan_to_num(0.0), k, v, 0.125, seen)
+        keep = ~nan[rows].to(DEV)
+        top = max(float((q[rows, h].double().nan_to_num(0.0).abs() @ k[:, h // 2].abs().T).max()) for h in range(4)) * 0.125
+        err = (out[rows].double() - want).abs()[keep]  # as check_prefill
+        assert bool((err <= (2.0 ** -8 * want.abs() + (2.0 ** -10 + 2.0 ** -10 * top) * mag)[keep] + 2.0 ** -24 * mag.max()).all())
+    assert B.pkv_device_errors() == 0
+
+
 @pytest.mark.parametrize("n", [4, 40])
 def test_prefill_lengths_that_do_not_fit(B, n):
     b = Batch([100, 100, 100], torch.int8, 1, 64, 16, seed=53)
