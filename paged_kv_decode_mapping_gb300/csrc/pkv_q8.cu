@@ -19,7 +19,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kQ8Threads = 128;   // of a CTA; of a write's twice as many where its pages are large
+constexpr int kQ8Threads = 128;   // of a CTA; a write's may have two or four times as many
 constexpr int64_t kReadWide = 1 << 18;  // vectors of a call
 constexpr int kRotateHeads = 4;  // q heads a thread rotates with one position's cosines and sines
 
@@ -119,8 +119,8 @@ __device__ __forceinline__ uint4 rotate_pairs(const uint4 &x, const Angles &a) {
 // page, K or V, kv head): it holds the page's new rows in registers between finding their largest
 // value and rounding them, U 16-byte vectors a thread; what does not fit is read a second time.
 // Bound by its instructions (two thirds of the issue slots; widening, two products and two
-// conversions for each pair of codes) and by HBM: 34000 tokens of 8 heads of 128 take 56 us, 3.7
-// TB/s; with k rotated 83, with 24 heads of q besides 144.  256 tokens of a step: 6 us.
+// conversions for each pair of codes) and by HBM: 34000 tokens of 8 heads of 128 take 49 us, 4.4
+// TB/s; with k rotated 84, with 24 heads of q besides 147.  256 tokens of a step: 6 us.
 
 struct WriteArgs {
   Span s;
@@ -199,7 +199,7 @@ __device__ __forceinline__ void rotate_q(const WriteArgs &a, const Tokens &t, ui
 }
 
 template <int D, int KIND, bool ROPE, int U>
-__global__ void __launch_bounds__(2 * kQ8Threads, ROPE ? 3 : 4) write_q8_kernel(const __grid_constant__ WriteArgs a) {
+__global__ void __launch_bounds__(ROPE ? 2 * kQ8Threads : 4 * kQ8Threads, ROPE ? 3 : 2) write_q8_kernel(const __grid_constant__ WriteArgs a) {
   constexpr int V = D / 8;  // vectors of a row: 8 bf16 in, 8 codes out
   q8::await_stream();
   q8::let_next_begin();  // a step's decode: its set-up
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(2 * kQ8Threads, ROPE ? 3 : 4) write_q8_kernel(
       return;
     }
   }
-  __shared__ uint32_t s_max[2 * kQ8Threads / 32];
+  __shared__ uint32_t s_max[4 * kQ8Threads / 32];
   const int tid = threadIdx.x, group = 1 << a.log2_group, gt = tid & (group - 1);
   const uint32_t item = blockIdx.x * (blockDim.x >> a.log2_group) + (tid >> a.log2_group);
   const int j = (int)(item / (uint32_t)a.s.num_kv_heads), h = (int)(item - (uint32_t)j * a.s.num_kv_heads);
@@ -296,12 +296,14 @@ __global__ void __launch_bounds__(2 * kQ8Threads, ROPE ? 3 : 4) write_q8_kernel(
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) m = absmax(m, x[u]);
-  for (int u = S; first + u * rows_apart < count; ++u) {
-    uint4 y[P];
-    load(u, y);
-    turn(u, y);
+  if constexpr (ROPE) {  // (without a rotation there are threads enough: write_threads)
+    for (int u = S; first + u * rows_apart < count; ++u) {
+      uint4 y[P];
+      load(u, y);
+      turn(u, y);
 #pragma unroll
-    for (int p = 0; p < P; ++p) m = absmax(m, y[p]);
+      for (int p = 0; p < P; ++p) m = absmax(m, y[p]);
+    }
   }
   m &= 0x7fff7fffu;
   m = max(m & 0xffffu, m >> 16);  // bf16 patterns order as whole numbers, infinity and NaN on top
@@ -324,17 +326,28 @@ __global__ void __launch_bounds__(2 * kQ8Threads, ROPE ? 3 : 4) write_q8_kernel(
   if (gt == 0 && !(to == old && r0 > 0)) *scale = to;
   const q8::Inverse by = q8::inverse_of(to == 0.f ? 1.f : to);
   uint2 *const dst = reinterpret_cast<uint2 *>(rows + (int64_t)(r0 + first) * D);
-  auto store = [&](int u, const uint4 *x) {
+  // The rare rows next to a border between codes are noted and divided at the end, from their loads on
+  // (with the divisions behind every vector the code left the instruction cache: 56 us, now 49).
+  auto store = [&](int u, const uint4 *x, bool exact) {
+    bool all = true;
 #pragma unroll
-    for (int p = 0; p < P; ++p) dst[u * rows_apart * V + col[p]] = q8::encode8<KIND, ROPE>(x[p], by);
+    for (int p = 0; p < P; ++p) {
+      bool sure = true;
+      dst[u * rows_apart * V + col[p]] = exact ? q8::divided8<KIND>(x[p], by.s) : q8::encode8<KIND>(x[p], by, &sure);
+      all = all && sure;
+    }
+    return all;
   };
+  uint32_t again = 0;
 #pragma unroll
   for (int u = 0; u < S; ++u)
-    if (first + u * rows_apart < count && !(skip >> u & 1u)) store(u, x + P * u);
-  for (int u = S; first + u * rows_apart < count; ++u) {
+    if (first + u * rows_apart < count && !(skip >> u & 1u) && !store(u, x + P * u, false)) again |= 1u << u;
+#pragma unroll 1
+  for (int u = again ? __ffs(again) - 1 : S; ROPE ? first + u * rows_apart < count : u < S; ++u) {
+    if (u < S && !(again >> u & 1u)) continue;
     uint4 y[P];
     load(u, y);
-    if (turn(u, y)) store(u, y);
+    if (turn(u, y) && (u < S || !store(u, y, false))) store(u, y, true);
   }
   if (to > old && r0 > 0) {  // the rows held before, in units of the new scale
     for (int e = gt; e < r0 * (D / 16); e += group) {
@@ -710,6 +723,12 @@ int check_write_q8(const WriteQ8 &w, const char *fn) {
   return PKV_OK;
 }
 
+// Threads of a write's CTA: as many as hold an item's vectors, 8 each; with a rotation (80 registers, not 64)
+// up to 256, whose rows past those are read twice.
+static int write_threads(int64_t vecs, bool rope) {
+  return vecs <= 8 * kQ8Threads ? kQ8Threads : vecs <= 16 * kQ8Threads || rope ? 2 * kQ8Threads : 4 * kQ8Threads;
+}
+
 int launch_write_q8(const WriteQ8 &w, cudaStream_t stream) {
   if (w.num_tokens == 0 || w.num_seqs == 0 || w.max_query_len == 0) return PKV_OK;
   const pkv_cache_desc &c = *w.desc;
@@ -727,7 +746,7 @@ int launch_write_q8(const WriteQ8 &w, cudaStream_t stream) {
   a.pages = (int32_t)std::min<int64_t>(touched(w.max_query_len, c.block_size), w.max_blocks);
   const int64_t vecs = (int64_t)std::min(c.block_size, w.max_query_len) * c.head_dim / 8;  // of an item
   const int per_thread = vecs <= 32 ? 1 : vecs <= 128 ? 4 : 8;
-  const int threads = vecs > 8 * kQ8Threads ? 2 * kQ8Threads : kQ8Threads;
+  const int threads = write_threads(vecs, w.rope);
   a.log2_group = log2_group_of(vecs, per_thread, threads);
   const int per = threads >> a.log2_group;
   a.item_ctas = (uint32_t)(((int64_t)a.pages * c.num_kv_heads + per - 1) / per);

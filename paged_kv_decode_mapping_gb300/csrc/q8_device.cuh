@@ -86,10 +86,12 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
     auto one = [](float x) { return (uint32_t)(__float2int_rn(fminf(fmaxf(x, -127.f), 127.f)) & 0xff); };
     return one(a) | one(b) << 8 | one(c) << 16 | one(d) << 24;
   } else {
-    uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-    return (uint32_t)lo | (uint32_t)hi << 16;
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
   }
 }
 
@@ -130,10 +132,8 @@ __device__ __forceinline__ Inverse inverse_of(float s) {
   const float lo = isinf(inv) ? 0.f : inv * (1.f - 4.76837158e-7f), hi = inv * (1.f + 4.76837158e-7f);
   return {s, f32x2(lo, lo), f32x2(hi, hi)};
 }
-// CALL: by a function of its own (a kernel with a rotation besides fits the instruction cache so: 91 us
-// instead of 97; one without is slower by the call: 61 and 63).
 template <int KIND>
-__device__ __noinline__ uint2 divided8(uint4 v, float s) {
+__device__ __forceinline__ uint2 divided8(const uint4 &v, float s) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   float q[8];
 #pragma unroll
@@ -143,36 +143,35 @@ __device__ __noinline__ uint2 divided8(uint4 v, float s) {
   }
   return make_uint2(encode4<KIND>(q[0], q[1], q[2], q[3]), encode4<KIND>(q[4], q[5], q[6], q[7]));
 }
-template <int KIND, bool CALL>
-__device__ __forceinline__ uint2 encode8(const uint4 &v, const Inverse &s) {
+// *sure: whether both bounds give these codes; else divided8 is wanted.
+template <int KIND>
+__device__ __forceinline__ uint2 encode8(const uint4 &v, const Inverse &s, bool *sure) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t c[4], differ[4];  // two codes each
+  uint32_t c[2], differ = 0u;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint64_t x = f32x2(dev::bf16lo_to_f32(w[k]), dev::bf16hi_to_f32(w[k]));
+  for (int k = 0; k < 2; ++k) {
+    const uint64_t x = f32x2(dev::bf16lo_to_f32(w[2 * k]), dev::bf16hi_to_f32(w[2 * k]));
+    const uint64_t y = f32x2(dev::bf16lo_to_f32(w[2 * k + 1]), dev::bf16hi_to_f32(w[2 * k + 1]));
     if constexpr (KIND == PKV_Q8_INT8) {
       // 2^23 + 2^22 + x / s, whose last bits are the rounded whole number (of at most 127)
       const uint64_t magic = f32x2(12582912.f, 12582912.f);
       const float2 a = split(fma2(x, s.lo, magic)), b = split(fma2(x, s.hi, magic));
-      differ[k] = (__float_as_uint(a.x) ^ __float_as_uint(b.x)) | (__float_as_uint(a.y) ^ __float_as_uint(b.y));
-      c[k] = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);  // low bytes
+      const float2 d = split(fma2(y, s.lo, magic)), e = split(fma2(y, s.hi, magic));
+      differ |= __float_as_uint(a.x) ^ __float_as_uint(b.x);
+      differ |= __float_as_uint(a.y) ^ __float_as_uint(b.y);
+      differ |= __float_as_uint(d.x) ^ __float_as_uint(e.x);
+      differ |= __float_as_uint(d.y) ^ __float_as_uint(e.y);
+      c[k] = __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),  // low bytes
+                         __byte_perm(__float_as_uint(d.x), __float_as_uint(d.y), 0x0040), 0x5410);
     } else {
       const float2 a = split(mul2(x, s.lo)), b = split(mul2(x, s.hi));
-      uint16_t p, q;
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(a.y), "f"(a.x));
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(b.y), "f"(b.x));
-      c[k] = p;
-      differ[k] = (uint32_t)(p ^ q);
+      const float2 d = split(mul2(y, s.lo)), e = split(mul2(y, s.hi));
+      c[k] = encode4<KIND>(a.x, a.y, d.x, d.y);
+      differ |= c[k] ^ encode4<KIND>(b.x, b.y, e.x, e.y);
     }
   }
-  if (differ[0] | differ[1] | differ[2] | differ[3]) {
-    if constexpr (CALL) return divided8<KIND>(v, s.s);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (differ[k])
-        c[k] = encode4<KIND>(__fdiv_rn(dev::bf16lo_to_f32(w[k]), s.s), __fdiv_rn(dev::bf16hi_to_f32(w[k]), s.s), 0.f, 0.f);
-  }
-  return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+  *sure = differ == 0u;
+  return make_uint2(c[0], c[1]);
 }
 
 }  // namespace q8
