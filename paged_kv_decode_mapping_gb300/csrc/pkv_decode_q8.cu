@@ -47,27 +47,35 @@ constexpr int kChunkCost = 1, kEndCost = 1;  // of a chunk, and of a (sequence, 
 constexpr int kMinCost = 2;
 static_assert(kMinCost >= kChunkCost + kEndCost, "no empty shares");
 constexpr int kQ8MaxShares = 1024;
+// Rows of a product's second operand.  A chunk of several queries a sequence takes two such tiles, so
+// that codes are widened once for up to 16 rows.
+constexpr int kRowTile = 8;
+static_assert(kRowTile >= kMaxGroup, "a query's heads fit a tile");
 
-__host__ __device__ constexpr int q8_groups(int d) { return d == 64 ? 3 : 2; }
+// Groups of a CTA: with two tiles of rows two at most, for 168 registers a thread.
+__host__ __device__ constexpr int q8_groups(int d, int nt) { return d == 64 && nt == 1 ? 3 : 2; }
 constexpr int q8_stages(int d) { return d == 64 ? 4 : 3; }  // of a group's ring
-__host__ __device__ constexpr int q8_threads(int d) { return q8_groups(d) * (kConsumers + 32); }
+__host__ __device__ constexpr int q8_threads(int d, int nt) { return q8_groups(d, nt) * (kConsumers + 32); }
 
-struct Q8Desc {                 // one stage's chunk
+struct alignas(16) Q8Desc {     // one stage's chunk
   int32_t nkeys;                // keys in range
   int32_t flags;                // kBegins, kEnds: of this share's part of the (sequence, kv head);
-                                // kLastOne: of its chunks
-  int32_t b, g;
+                                // kLastOne: of its chunks; above, its rows: (query, head of the group)
+  int32_t row0;                 // its first row of q
+  int32_t g;
+  int32_t seen;                 // keys of the chunk that the first query sees; the i-th sees i more
   int32_t slot;                 // partial row the result goes to; -1: the whole context is here
   int32_t share0, parts;        // shares that cut it: share0 .. share0 + parts - 1
-  int32_t pad;
+  __device__ int rows() const { return flags >> 8; }
 };
+static_assert(sizeof(Q8Desc) == 32, "stored and read 16 bytes at a time; the barriers lie behind");
 constexpr int32_t kBegins = 1, kEnds = 2, kLastOne = 4;
 
-template <int D>
+template <int D, int NT>
 struct Q8Smem {  // offsets from the 1024-byte aligned base
   static constexpr int kStages = q8_stages(D);
   static constexpr uint32_t kStage = 2 * kQ8Keys * D;
-  static constexpr uint32_t kQ = kMaxGroup * D * 2;
+  static constexpr uint32_t kQ = NT * kRowTile * D * 2;
   // of each group, from group * kGroup
   static constexpr uint32_t q = kStages * kStage;
   static constexpr uint32_t scales = q + kStages * kQ;             // (K's, V's) of a stage's boxes
@@ -76,31 +84,35 @@ struct Q8Smem {  // offsets from the 1024-byte aligned base
   static constexpr uint32_t misc = bars + kStages * 16;            // flag, last, issued
   static constexpr uint32_t kGroup = (misc + 16 + 1023) / 1024 * 1024;
   // of the CTA
-  static constexpr uint32_t sums = q8_groups(D) * kGroup;          // the prefix scan: per warp,
-  static constexpr uint32_t incl = sums + q8_threads(D) / 32 * 8;  // per thread within its warp
-  static constexpr uint32_t total = incl + q8_threads(D) * 8;
+  static constexpr uint32_t sums = q8_groups(D, NT) * kGroup;          // the prefix scan: per warp,
+  static constexpr uint32_t incl = sums + q8_threads(D, NT) / 32 * 8;  // per thread within its warp
+  static constexpr uint32_t total = incl + q8_threads(D, NT) * 8;
 };
-constexpr size_t q8_smem(int d) { return 1024 + (d == 64 ? Q8Smem<64>::total : Q8Smem<128>::total); }
-static_assert(q8_smem(64) <= 227 * 1024 && q8_smem(128) <= 227 * 1024, "the groups fit an SM");
+template <int D, int NT>
+constexpr size_t q8_smem() { return 1024 + Q8Smem<D, NT>::total; }
+static_assert(q8_smem<64, 2>() <= 227 * 1024 && q8_smem<128, 2>() <= 227 * 1024, "the groups fit an SM");
 // A share's result in its last stage: per warp and head a row of D floats (4 apart, so that the
 // lanes' stores lie in different banks), then the references and the sums.
 __host__ __device__ constexpr int q8_row(int d) { return d + 4; }
-static_assert(kConsumerWarps * kMaxGroup * (q8_row(128) + 2) * 4 <= (int)Q8Smem<128>::kStage &&
-                  kConsumerWarps * kMaxGroup * (q8_row(64) + 2) * 4 <= (int)Q8Smem<64>::kStage,
-              "the warps' results fit a stage");
+static_assert(kConsumerWarps * kRowTile * (q8_row(128) + 2) * 4 <= (int)Q8Smem<128, 1>::kStage &&
+                  kConsumerWarps * kRowTile * (q8_row(64) + 2) * 4 <= (int)Q8Smem<64, 1>::kStage,
+              "the warps' results of a tile of rows fit a stage");
 
 struct Q8Args {
   const uint16_t *q;            // [B][Hq][D]
   uint16_t *out;
   const int32_t *tables, *lens;
-  const int32_t *seqs;          // NULL, or whose tables row b of q reads (-1: none, and no output)
+  // NULL: row b of q is sequence b's one query.  Else what is listed as sequence b: its sequence (-1:
+  // none), its first row of q, its queries, the keys that the first of them sees; lens is the last's.
+  const int4 *queries;
   const float *k_scale, *v_scale;
-  float *o_part;                // [2 * shares][G][D]: a share's first row, then its last's
-  float *lse_part;              // [2 * shares][G], base 2
+  float *o_part;                // [2 * shares][rows][D]: a share's first part, then its last's
+  float *lse_part;              // [2 * shares][rows], base 2
   uint32_t *counters;           // [2][kQ8MaxShares] by the first that cuts: a context, a run of its
                                 // shares; zero between calls
   int64_t num_blocks;
   int32_t max_blocks, max_len, num_seqs, num_q_heads, num_kv_heads, group;
+  int32_t rows;                 // of a listed sequence and kv head, at most: group * its queries
   int32_t block_size, log2_bs, box_rows, log2_box;
   int32_t depth;                // 1: the first map leads to the other pool too
   int32_t v_first;              // V's rows lie first in a box
@@ -200,27 +212,31 @@ __device__ __forceinline__ void k_pairs(uint32_t w, uint32_t &lo, uint32_t &hi) 
   }
 }
 
-// A consumer warp's state.  Lane (gid, tig): O^T fragments, rows gid and gid + 8 of m-tile mt being
-// dims 16 mt + gid and + 8, for heads 2 tig and 2 tig + 1.
+// A consumer warp's state for a tile of rows.  Lane (gid, tig): O^T fragments, rows gid and gid + 8 of
+// m-tile mt being dims 16 mt + gid and + 8, for the tile's rows 2 tig and 2 tig + 1.
 template <int D>
 struct Q8Acc {
   float o[D / 16][4];
-  float m0, m1, l0, l1;     // the heads' references; sums of weights, per lane
-  float vref, vinv;         // the largest V scale so far, and 1 over it: o is in units of vref
+  float m0, m1, l0, l1;     // the rows' references; sums of weights, per lane
   uint32_t q[D / 16][2];    // fragments of q
-  float f0, f1;             // scores' factors of the two heads, without K's scale
-  float b0, b1;             // what the two heads' raw scores begin with
+  float f0, f1;             // scores' factors of the two rows, without K's scale
+  float b0, b1;             // what the two rows' raw scores begin with
+  int i0, i1;               // the rows' queries
+};
+// For all tiles: the largest V scale so far, and 1 over it: o is in units of vref.
+struct Q8Ref {
+  float vref, vinv;
 };
 
-// The (sequence, kv head)'s query rows at qs ([G][D] bf16, shared) as fragments: head gid, the
-// dims that this lane's K bytes hold (D/4 tig ..).
+// A tile's query rows at qs ([rows][D] bf16, shared) as fragments: row gid, the dims that this lane's K
+// bytes hold (D/4 tig ..).
 template <int D, int KIND>
-__device__ __forceinline__ void load_q(Q8Acc<D> &a, uint32_t qs, int group, int lane, float scale_log2) {
+__device__ __forceinline__ void load_q(Q8Acc<D> &a, uint32_t qs, int rows, int lane, float scale_log2) {
   const int gid = lane >> 2, tig = lane & 3;
   uint32_t w[D / 8];
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) w[i] = 0u;
-  if (gid < group) {
+  if (gid < rows) {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       uint32_t v[4];
@@ -263,14 +279,14 @@ __device__ __forceinline__ void load_q(Q8Acc<D> &a, uint32_t qs, int group, int 
       a.q[i][1] = w[2 * i + 1];
     }
   }
-  a.f0 = __shfl_sync(0xffffffffu, down, 8 * tig);  // lanes of heads 2 tig and 2 tig + 1
+  a.f0 = __shfl_sync(0xffffffffu, down, 8 * tig);  // lanes of rows 2 tig and 2 tig + 1
   a.f1 = __shfl_sync(0xffffffffu, down, 8 * tig + 4);
   a.b0 = __shfl_sync(0xffffffffu, begin, 8 * tig);
   a.b1 = __shfl_sync(0xffffffffu, begin, 8 * tig + 4);
 #pragma unroll
   for (int mt = 0; mt < D / 16; ++mt) a.o[mt][0] = a.o[mt][1] = a.o[mt][2] = a.o[mt][3] = 0.f;
   a.m0 = a.m1 = -INFINITY;
-  a.l0 = a.l1 = a.vref = a.vinv = 0.f;
+  a.l0 = a.l1 = 0.f;
 }
 
 // Where a lane reads in a stage, of its warp's 32 keys.
@@ -294,12 +310,15 @@ __device__ __forceinline__ Q8Lane q8_lane(int warp, int lane, int log2_box, int 
   return x;
 }
 
-// Raw scores of 16 keys, rows gid and gid + 8 (key_of(row)) x heads 2 tig, 2 tig + 1: the K chunks of
-// these rows are at k0 and k1.
-template <int D, int KIND>
-__device__ __forceinline__ void q8_scores(const Q8Acc<D> &a, float (&c)[4], uint32_t k0, uint32_t k1) {
-  c[0] = c[2] = a.b0;
-  c[1] = c[3] = a.b1;
+// Raw scores of 16 keys, rows gid and gid + 8 (key_of(row)) x each tile's rows 2 tig, 2 tig + 1: the K
+// chunks of these keys are at k0 and k1.
+template <int D, int KIND, int NT>
+__device__ __forceinline__ void q8_scores(const Q8Acc<D> (&a)[NT], float (&s)[NT][2][4], int t, uint32_t k0, uint32_t k1) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    s[n][t][0] = s[n][t][2] = a[n].b0;
+    s[n][t][1] = s[n][t][3] = a[n].b1;
+  }
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) {  // (the next chunk is the other of a pair)
     uint32_t x[4], y[4];
@@ -310,99 +329,137 @@ __device__ __forceinline__ void q8_scores(const Q8Acc<D> &a, float (&c)[4], uint
       uint32_t x0, x1, y0, y1;
       k_pairs<KIND>(x[k], x0, x1);
       k_pairs<KIND>(y[k], y0, y1);
-      mma_f16(c, x0, y0, x1, y1, a.q[4 * i + k][0], a.q[4 * i + k][1]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_f16(s[n][t], x0, y0, x1, y1, a[n].q[4 * i + k][0], a[n].q[4 * i + k][1]);
     }
   }
 }
 
-// Scores, softmax and weighted sum of the warp's 32 keys (the first nvalid of them in range) of a
-// stage at sb, the boxes' scales (K's, V's) at sc.
-template <int D, int KIND>
-__device__ __forceinline__ void q8_tiles(Q8Acc<D> &a, uint32_t sb, const Q8Lane &at, const float2 *sc, int log2_box,
-                                         int warp, int lane, int nvalid) {
+// Scores, softmax and weighted sum of the warp's 32 keys (the first nvalid of them in range; of these,
+// with MASK, query i sees the first seen + i) of a stage at sb, the boxes' scales (K's, V's) at sc.
+template <int D, int KIND, int NT, bool MASK>
+__device__ __forceinline__ void q8_tiles(Q8Acc<D> (&a)[NT], Q8Ref &ref, uint32_t sb, const Q8Lane &at, const float2 *sc,
+                                         int log2_box, int warp, int lane, int nvalid, int seen) {
   const int gid = lane >> 2, tig = lane & 3;
-  float s[2][4], vs[4], f0[4], f1[4];
+  float s[NT][2][4], vs[4], ks[4], f0[4], f1[4];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) q8_scores<D, KIND>(a, s[t], sb + at.k[t][0], sb + at.k[t][1]);
+  for (int t = 0; t < 2; ++t) q8_scores<D, KIND, NT>(a, s, t, sb + at.k[t][0], sb + at.k[t][1]);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {  // 8 keys lie in one box; one box may hold more of these
     if (i == 0 || (i == 2 && log2_box < 5) || log2_box < 4) {
       const float2 f = sc[(32 * warp + 8 * i) >> log2_box];
       vs[i] = f.y;
-      f0[i] = a.f0 * f.x;
-      f1[i] = a.f1 * f.x;
+      ks[i] = f.x;
+      if (NT == 1) {
+        f0[i] = a[0].f0 * f.x;
+        f1[i] = a[0].f1 * f.x;
+      }
     } else {
       vs[i] = vs[i - 1];
-      f0[i] = f0[i - 1];
-      f1[i] = f1[i - 1];
+      ks[i] = ks[i - 1];
+      if (NT == 1) {
+        f0[i] = f0[i - 1];
+        f1[i] = f1[i - 1];
+      }
     }
   }
+  auto key = [&](int i) { return 16 * (i >> 1) + key_of(gid + 8 * (i & 1)); };  // of the lane, in each 8 keys
   if (nvalid < 32) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (8 * i >= nvalid) vs[i] = 0.f;  // its box may not have been loaded
-      // scores of -inf; by a factor of 0 they would be NaN
-      if (16 * (i >> 1) + key_of(gid + 8 * (i & 1)) >= nvalid) {
-        s[i >> 1][2 * (i & 1)] = s[i >> 1][2 * (i & 1) + 1] = -INFINITY;
-        f0[i] = f1[i] = 1.f;
+      if (!MASK && key(i) >= nvalid) {  // scores of -inf; by a factor of 0 or NaN they would be NaN
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[n][i >> 1][2 * (i & 1)] = s[n][i >> 1][2 * (i & 1) + 1] = -INFINITY;
+        ks[i] = f0[i] = f1[i] = 1.f;
       }
     }
   }
-  float sh0 = kTop - softmax_ref(a.m0), sh1 = kTop - softmax_ref(a.m1);
-  float x[2][4];  // scores over the reference, plus kTop
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[i >> 1][2 * (i & 1)] = fmaf(s[i >> 1][2 * (i & 1)], f0[i], sh0);
-    x[i >> 1][2 * (i & 1) + 1] = fmaf(s[i >> 1][2 * (i & 1) + 1], f1[i], sh1);
-  }
-  float mx0 = max3(max3(x[0][0], x[0][2], x[1][0]), x[1][2], x[1][2]);
-  float mx1 = max3(max3(x[0][1], x[0][3], x[1][1]), x[1][3], x[1][3]);
   const float vmax = max3(max3(vs[0], vs[1], vs[2]), vs[3], vs[3]);
-  // (A reference of -inf, no score over that so far, moves with the first one that is.)
-  const bool over = mx0 > kTop + kSlack || mx1 > kTop + kSlack || (a.m0 == -INFINITY && mx0 > -INFINITY) ||
-                    (a.m1 == -INFINITY && mx1 > -INFINITY);
-  if (vmax > a.vref || __any_sync(0xffffffffu, over)) {
+  const bool grows = vmax > ref.vref;
+  float vscale = 1.f;  // what O is to be scaled by for a larger V scale
+  auto grow = [&] {
+    ref.vinv = 1.f / vmax;
+    vscale = ref.vref * ref.vinv;
+    ref.vref = vmax;
+  };
+  if (NT > 1 && grows) grow();
+  uint32_t b[NT][2][2];  // the weights as B operands of the two tiles of keys
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+  for (int n = 0; n < NT; ++n) {
+    Q8Acc<D> &c = a[n];
+    float sh0 = kTop - softmax_ref(c.m0), sh1 = kTop - softmax_ref(c.m1);
+    float x[2][4];  // scores over the reference, plus kTop
+    auto unseen = [&](int i, int query) { return key(i) >= min(nvalid, seen + query); };
+    if (NT > 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f0[i] = c.f0 * ks[i];
+        f1[i] = c.f1 * ks[i];
+      }
     }
-    const float mn0 = fmaxf(a.m0, mx0 - sh0), mn1 = fmaxf(a.m1, mx1 - sh1);
-    float al0 = dev::ex2(a.m0 - softmax_ref(mn0)), al1 = dev::ex2(a.m1 - softmax_ref(mn1));
-    a.m0 = mn0;
-    a.m1 = mn1;
-    a.l0 *= al0;
-    a.l1 *= al1;
-    if (vmax > a.vref) {
-      a.vinv = 1.f / vmax;
-      al0 *= a.vref * a.vinv;
-      al1 *= a.vref * a.vinv;
-      a.vref = vmax;
+    auto shifted = [&] {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i >> 1][2 * (i & 1)] = fmaf(s[n][i >> 1][2 * (i & 1)], f0[i], sh0);
+        x[i >> 1][2 * (i & 1) + 1] = fmaf(s[n][i >> 1][2 * (i & 1) + 1], f1[i], sh1);
+      }
+      if (MASK) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (unseen(i, c.i0)) x[i >> 1][2 * (i & 1)] = -INFINITY;
+          if (unseen(i, c.i1)) x[i >> 1][2 * (i & 1) + 1] = -INFINITY;
+        }
+      }
+    };
+    shifted();
+    float mx0 = max3(max3(x[0][0], x[0][2], x[1][0]), x[1][2], x[1][2]);
+    float mx1 = max3(max3(x[0][1], x[0][3], x[1][1]), x[1][3], x[1][3]);
+    // (A reference of -inf, no score over that so far, moves with the first one that is.)
+    const bool over = mx0 > kTop + kSlack || mx1 > kTop + kSlack || (c.m0 == -INFINITY && mx0 > -INFINITY) ||
+                      (c.m1 == -INFINITY && mx1 > -INFINITY);
+    if (grows || __any_sync(0xffffffffu, over)) {
+      if (NT == 1 && grows) grow();
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+      }
+      const float mn0 = fmaxf(c.m0, mx0 - sh0), mn1 = fmaxf(c.m1, mx1 - sh1);
+      float al0 = dev::ex2(c.m0 - softmax_ref(mn0)), al1 = dev::ex2(c.m1 - softmax_ref(mn1));
+      c.m0 = mn0;
+      c.m1 = mn1;
+      c.l0 *= al0;
+      c.l1 *= al1;
+      al0 *= vscale;
+      al1 *= vscale;
+#pragma unroll
+      for (int mt = 0; mt < D / 16; ++mt) {
+        c.o[mt][0] *= al0;
+        c.o[mt][1] *= al1;
+        c.o[mt][2] *= al0;
+        c.o[mt][3] *= al1;
+      }
+      sh0 = kTop - softmax_ref(mn0);
+      sh1 = kTop - softmax_ref(mn1);
+      shifted();
     }
 #pragma unroll
-    for (int mt = 0; mt < D / 16; ++mt) {
-      a.o[mt][0] *= al0;
-      a.o[mt][1] *= al1;
-      a.o[mt][2] *= al0;
-      a.o[mt][3] *= al1;
+    for (int t = 0; t < 2; ++t) {
+      const float r0 = vs[2 * t] * ref.vinv, r1 = vs[2 * t + 1] * ref.vinv;
+      const float p0 = dev::ex2(x[t][0]), p1 = dev::ex2(x[t][1]), p2 = dev::ex2(x[t][2]), p3 = dev::ex2(x[t][3]);
+      c.l0 += p0 + p2;
+      c.l1 += p1 + p3;
+      float w0 = p0 * r0, w1 = p1 * r0, w2 = p2 * r1, w3 = p3 * r1;
+      if (MASK) {  // (a V scale of NaN is for those who see it)
+        if (unseen(2 * t, c.i0)) w0 = 0.f;
+        if (unseen(2 * t, c.i1)) w1 = 0.f;
+        if (unseen(2 * t + 1, c.i0)) w2 = 0.f;
+        if (unseen(2 * t + 1, c.i1)) w3 = 0.f;
+      }
+      b[n][t][0] = dev::movmatrix_trans(q8::pack_f16x2(w0, w1));
+      b[n][t][1] = dev::movmatrix_trans(q8::pack_f16x2(w2, w3));
     }
-    sh0 = kTop - softmax_ref(mn0);
-    sh1 = kTop - softmax_ref(mn1);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i >> 1][2 * (i & 1)] = fmaf(s[i >> 1][2 * (i & 1)], f0[i], sh0);
-      x[i >> 1][2 * (i & 1) + 1] = fmaf(s[i >> 1][2 * (i & 1) + 1], f1[i], sh1);
-    }
-  }
-  uint32_t b[2][2];  // the weights as B operands of the two tiles
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const float r0 = vs[2 * t] * a.vinv, r1 = vs[2 * t + 1] * a.vinv;
-    const float p0 = dev::ex2(x[t][0]), p1 = dev::ex2(x[t][1]), p2 = dev::ex2(x[t][2]), p3 = dev::ex2(x[t][3]);
-    a.l0 += p0 + p2;
-    a.l1 += p1 + p3;
-    b[t][0] = dev::movmatrix_trans(q8::pack_f16x2(p0 * r0, p1 * r0));
-    b[t][1] = dev::movmatrix_trans(q8::pack_f16x2(p2 * r1, p3 * r1));
   }
   uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
   if (KIND == PKV_Q8_E4M3 && nvalid < 32) {  // rows past the range may hold NaN codes
@@ -412,6 +469,13 @@ __device__ __forceinline__ void q8_tiles(Q8Acc<D> &a, uint32_t sb, const Q8Lane 
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (16 * t + key_of(2 * tig + (k & 1) + 8 * (k >> 1)) < nvalid) keep[t] |= 0xffu << (8 * k);
+    }
+  }
+  if (KIND == PKV_Q8_E4M3 && MASK) {  // so may pages whose scale is NaN (the weights are NaN where they count)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (vs[2 * t] != vs[2 * t]) keep[t] &= 0xffff0000u;
+      if (vs[2 * t + 1] != vs[2 * t + 1]) keep[t] &= 0x0000ffffu;
     }
   }
 #pragma unroll
@@ -427,14 +491,15 @@ __device__ __forceinline__ void q8_tiles(Q8Acc<D> &a, uint32_t sb, const Q8Lane 
       uint32_t y0, y1, z0, z1;
       v_pairs<KIND>(v[2 * t], y0, y1);
       v_pairs<KIND>(v[2 * t + 1], z0, z1);
-      mma_f16(a.o[mt], y0, z0, y1, z1, b[t][0], b[t][1]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_f16(a[n].o[mt], y0, z0, y1, z1, b[n][t][0], b[n][t][1]);
     }
   }
 }
 
-// Reduces l over the warp and writes the warp's (m, l, O) for heads < G.
+// Reduces l over the warp and writes the warp's (m, l, O) of a tile's first n rows.
 template <int D>
-__device__ __forceinline__ void q8_stash(Q8Acc<D> &a, const MergeArea &r, int G, int warp, int lane) {
+__device__ __forceinline__ void q8_stash(const Q8Acc<D> &a, float vref, const MergeArea &r, int n, int warp, int lane) {
   const int gid = lane >> 2, tig = lane & 3;
   float l0 = a.l0, l1 = a.l1;
 #pragma unroll
@@ -444,38 +509,38 @@ __device__ __forceinline__ void q8_stash(Q8Acc<D> &a, const MergeArea &r, int G,
   }
   const int h0 = 2 * tig, h1 = h0 + 1;
   if (gid == 0) {
-    r.m[warp * kMaxGroup + h0] = a.m0;
-    r.m[warp * kMaxGroup + h1] = a.m1;
-    r.l[warp * kMaxGroup + h0] = l0;
-    r.l[warp * kMaxGroup + h1] = l1;
+    r.m[warp * kRowTile + h0] = a.m0;
+    r.m[warp * kRowTile + h1] = a.m1;
+    r.l[warp * kRowTile + h0] = l0;
+    r.l[warp * kRowTile + h1] = l1;
   }
 #pragma unroll
   for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int h = h0 + (k & 1);
-      if (h < G) r.o[(warp * G + h) * q8_row(D) + 16 * mt + gid + 8 * (k >> 1)] = a.o[mt][k] * a.vref;
+      if (h < n) r.o[(warp * n + h) * q8_row(D) + 16 * mt + gid + 8 * (k >> 1)] = a.o[mt][k] * vref;
     }
 }
 
-// Four dims of one head from the four warps' results: the normalised output and the base-2
+// Four dims of one row from the four warps' results: the normalised output and the base-2
 // log-sum (of weights 2^kTop at the reference, in every partial alike).
 template <int D>
-__device__ __forceinline__ float4 q8_joined(const MergeArea &r, int G, int h, int d, float *lse) {
+__device__ __forceinline__ float4 q8_joined(const MergeArea &r, int n, int h, int d, float *lse) {
   float m[kConsumerWarps], M = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < kConsumerWarps; ++w) M = fmaxf(M, m[w] = r.m[w * kMaxGroup + h]);
+  for (int w = 0; w < kConsumerWarps; ++w) M = fmaxf(M, m[w] = r.m[w * kRowTile + h]);
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
   float den = 0.f;
 #pragma unroll
   for (int w = 0; w < kConsumerWarps; ++w) {
     const float wt = dev::ex2(m[w] - softmax_ref(M));
-    const float4 o = *reinterpret_cast<const float4 *>(r.o + (w * G + h) * q8_row(D) + d);
+    const float4 o = *reinterpret_cast<const float4 *>(r.o + (w * n + h) * q8_row(D) + d);
     x.x += wt * o.x;
     x.y += wt * o.y;
     x.z += wt * o.z;
     x.w += wt * o.w;
-    den += wt * r.l[w * kMaxGroup + h];
+    den += wt * r.l[w * kRowTile + h];
   }
   *lse = M + log2f(den);
   const float inv = den == 0.f ? 1.f : 1.f / den;
@@ -494,10 +559,10 @@ constexpr int kOneJoin = 32, kRunParts = 16;
 
 // Where part p of a context cut from share0 on has its row.
 __device__ __forceinline__ int64_t q8_row_of(const Q8Args &a, int share0, int p, int h) {
-  return (int64_t)(p == 0 ? 2 * share0 + 1 : 2 * (share0 + p)) * a.group + h;
+  return (int64_t)(p == 0 ? 2 * share0 + 1 : 2 * (share0 + p)) * a.rows + h;
 }
 
-// Four dims of head h from the rows of parts p0, p0 + step, .. (n of them), in that order: those of
+// Four dims of row h from the rows of parts p0, p0 + step, .. (n of them), in that order: those of
 // `sub`, sub + every, ... are this lane's, the others its neighbours'.  The normalised result and its
 // base-2 log-sum.
 template <int D>
@@ -559,23 +624,39 @@ __device__ __forceinline__ void group_bar(int group) {
   asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kConsumers) : "memory");
 }
 
-// The end of a share's part of a context, whose four results lie in r (cf. finish_partition).
-template <int D>
-__device__ __forceinline__ void q8_finish(const Q8Args &a, const MergeArea &r, const Q8Desc &d, int grp, int tid,
-                                          volatile int *s_flag, volatile int *s_last) {
+// The end of a share's part of a context: the warps' results, a tile of rows after the other through
+// the stage at `area`, into the output or a partial row (cf. finish_partition), and joins.
+template <int D, int NT, bool LISTED>
+__device__ __forceinline__ void q8_finish(const Q8Args &a, const Q8Acc<D> (&acc)[NT], float vref, float *area,
+                                          const Q8Desc &d, int grp, int tid, volatile int *s_flag, volatile int *s_last) {
   constexpr int T = kConsumers;
-  const int items = a.group * (D / 4);  // four dims of a head
-  const int64_t head0 = (int64_t)d.b * a.num_q_heads + d.g * a.group;
-  for (int i = tid; i < items; i += T) {
-    const int h = i / (D / 4), c = 4 * (i - h * (D / 4));
-    float lse;
-    const float4 x = q8_joined<D>(r, a.group, h, c, &lse);
-    if (d.slot < 0) {
-      store4(a.out + (head0 + h) * D + c, x);
-    } else {
-      const int64_t row = (int64_t)d.slot * a.group + h;
-      *reinterpret_cast<float4 *>(a.o_part + row * D + c) = x;
-      if (c == 0) a.lse_part[row] = lse;
+  const int all = LISTED ? d.rows() : a.group, items = all * (D / 4);  // four dims of a row
+  auto out_of = [&](int row) {
+    const int i = LISTED ? row / a.group : 0;
+    return a.out + ((int64_t)(d.row0 + i) * a.num_q_heads + d.g * a.group + (row - i * a.group)) * D;
+  };
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int rows = NT > 1 ? min(all - n * kRowTile, kRowTile) : all;
+    if (rows <= 0) break;
+    group_bar(grp);  // every warp is done with the stage's keys, or with the last tile's results
+    MergeArea r;
+    r.o = area;
+    r.m = r.o + kConsumerWarps * rows * q8_row(D);
+    r.l = r.m + kConsumerWarps * kRowTile;
+    q8_stash<D>(acc[n], vref, r, rows, tid >> 5, tid & 31);
+    group_bar(grp);
+    for (int i = tid; i < rows * (D / 4); i += T) {
+      const int h = i / (D / 4), c = 4 * (i - h * (D / 4)), at = n * kRowTile + h;
+      float lse;
+      const float4 x = q8_joined<D>(r, rows, h, c, &lse);
+      if (d.slot < 0) {
+        store4(out_of(at) + c, x);
+      } else {
+        const int64_t row = (int64_t)d.slot * a.rows + at;
+        *reinterpret_cast<float4 *>(a.o_part + row * D + c) = x;
+        if (c == 0) a.lse_part[row] = lse;
+      }
     }
   }
   if (d.slot < 0) return;
@@ -601,7 +682,7 @@ __device__ __forceinline__ void q8_finish(const Q8Args &a, const MergeArea &r, c
       float lse;
       const float4 x = q8_merge<D>(a, d.share0, p0, step, n, h, c, sub, every, &lse);
       if (out) {
-        if (sub == 0) store4(a.out + (head0 + h) * D + c, x);
+        if (sub == 0) store4(out_of(h) + c, x);
       } else {  // every other row of the run has been read when the barrier lets this one be
         group_bar(grp);
         const int64_t row = q8_row_of(a, d.share0, p0, h);
@@ -644,12 +725,13 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-template <int D, int KIND>
-__global__ void __launch_bounds__(q8_threads(D), 1)
+// NT: tiles of rows.  LISTED: a.queries says whose the rows are, else row b of q is sequence b's one query.
+template <int D, int KIND, int NT, bool LISTED>
+__global__ void __launch_bounds__(q8_threads(D, NT), 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1,
                      const __grid_constant__ Q8Args a) {
-  using SL = Q8Smem<D>;
-  constexpr int STAGES = SL::kStages, GROUPS = q8_groups(D), WARPS = q8_threads(D) / 32;
+  using SL = Q8Smem<D, NT>;
+  constexpr int STAGES = SL::kStages, GROUPS = q8_groups(D, NT), WARPS = q8_threads(D, NT) / 32;
   constexpr int kFirstProducer = GROUPS * kConsumerWarps;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = dev::smem_addr(smem_raw);
@@ -680,7 +762,7 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
   // Entries of the block table, one a lane.
   auto entries = [&](int b, int at) {
     if (b >= a.num_seqs) return 0;
-    const int seq = a.seqs ? max(__ldg(a.seqs + b), 0) : b;
+    const int seq = LISTED ? max(__ldg(&a.queries[b].x), 0) : b;
     return at + lane < a.max_blocks ? __ldg(a.tables + (int64_t)seq * a.max_blocks + at + lane) : 0;
   };
 
@@ -709,9 +791,11 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
     const int L0 = __ldg(a.lens + b), L = min(max(L0, 0), cap);
     if (L != L0 && blockIdx.x == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
     incl += cost_of(L);
-    if (L == 0 && b % (int)gridDim.x == (int)blockIdx.x && !(a.seqs && __ldg(a.seqs + b) < 0)) {  // empty: zeros
-      uint2 *o = reinterpret_cast<uint2 *>(a.out + (int64_t)b * a.num_q_heads * D);
-      for (int i = 0; i < a.num_q_heads * D / 4; ++i) o[i] = make_uint2(0u, 0u);
+    if (L == 0 && b % (int)gridDim.x == (int)blockIdx.x) {  // empty: zeros
+      int4 l = make_int4(b, b, 1, 0);
+      if (LISTED) l = __ldg(a.queries + b);
+      uint2 *o = reinterpret_cast<uint2 *>(a.out + (int64_t)l.y * a.num_q_heads * D);
+      for (int i = 0; i < l.z * a.num_q_heads * D / 4; ++i) o[i] = make_uint2(0u, 0u);
     }
   }
 #pragma unroll
@@ -752,7 +836,7 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
     const uint64_t policy = dev::policy_evict_first();
     const int rb = a.box_rows;
     const uint32_t box_bytes = (uint32_t)(rb * D);
-    const uint32_t q_bytes = (uint32_t)a.group * D * 2u;
+    const uint32_t q_bytes = (uint32_t)a.group * D * 2u;  // of a query
     // ---- the first chunk at or behind place lo: the thread whose run of sequences holds the place,
     // then the sequence, the kv head and the chunk
     int b, at_lane;
@@ -813,8 +897,8 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
       tb_next = entries(b, 32);
     };
     if (c >= nch) next_head();  // lo lies at a kv head's end
-    Q8Desc dsc;
-    dsc.pad = 0;
+    Q8Desc dsc = {};
+    int4 listed = make_int4(0, 0, 1, 0);  // what sequence b is
     bool first = true, last = false;
     q8::await_stream();  // the step's write is done
     int i = 0;
@@ -822,7 +906,11 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
       const int s = i % STAGES;
       if (first) {
         const int64_t end = u0 + kChunkCost * (int64_t)(nch - 1);  // its last chunk's place
-        dsc.b = b;
+        if (LISTED)
+          listed = __ldg(a.queries + b);
+        else
+          listed.y = b;
+        dsc.row0 = listed.y;
         dsc.g = g;
         dsc.slot = -1;
         dsc.share0 = share;
@@ -857,12 +945,15 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
       const int32_t row = (int32_t)((unit * a.block_size + (key & (a.block_size - 1))) * D / 128);
       if (lane == 0) {
         dsc.nkeys = nk;
+        if (LISTED) dsc.seen = listed.w - k0;
         dsc.flags = (first ? kBegins : 0) | (c + 1 == nch || last ? kEnds : 0) | (last ? kLastOne : 0);
+        if (LISTED) dsc.flags |= a.group * listed.z << 8;
         s_desc[s] = dsc;
-        dev::mbar_arrive_expect_tx(bar_full + 8 * s, 2u * nbox * box_bytes + (first ? q_bytes : 0u));
+        dev::mbar_arrive_expect_tx(bar_full + 8 * s, 2u * nbox * box_bytes + (first ? (LISTED ? listed.z : 1) * q_bytes : 0u));
         if (first)
-          dev::bulk_load(base + SL::q + s * SL::kQ, a.q + ((int64_t)b * a.num_q_heads + g * a.group) * D, q_bytes,
-                         bar_full + 8 * s);
+          for (int i = 0; i < (LISTED ? listed.z : 1); ++i)
+            dev::bulk_load(base + SL::q + s * SL::kQ + i * q_bytes,
+                           a.q + ((int64_t)(listed.y + i) * a.num_q_heads + g * a.group) * D, q_bytes, bar_full + 8 * s);
       }
       __syncwarp();
       if (lane < nbox) {
@@ -891,7 +982,8 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
     // ----------------------------------------------------------- consumer warps
     const int wg = warp - grp * kConsumerWarps, tid = (int)threadIdx.x - grp * kConsumers;
     const Q8Lane at = q8_lane<D, KIND>(wg, lane, a.log2_box, a.v_first);
-    Q8Acc<D> acc;
+    Q8Acc<D> acc[NT];
+    Q8Ref ref = {};
     for (int i = 0;; ++i) {
       const int s = i % STAGES;
       if (!__all_sync(0xffffffffu, wait_long(bar_full + 8 * s, (i / STAGES) & 1))) {
@@ -899,22 +991,31 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
         break;
       }
       const int2 info = *reinterpret_cast<const int2 *>(s_desc + s);  // keys, flags
-      if (info.y & kBegins) load_q<D, KIND>(acc, base + SL::q + s * SL::kQ, a.group, lane, a.scale_log2);
-      const int nvalid = min(32, info.x - 32 * wg);
-      if (nvalid > 0)
-        q8_tiles<D, KIND>(acc, base + s * SL::kStage, at,
-                          reinterpret_cast<const float2 *>(base_ptr + SL::scales + s * 128), a.log2_box, wg, lane,
-                          nvalid);
+      if (info.y & kBegins) {
+        ref.vref = ref.vinv = 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int row = n * kRowTile;
+          load_q<D, KIND>(acc[n], base + SL::q + s * SL::kQ + row * D * 2, (LISTED ? info.y >> 8 : a.group) - row, lane,
+                          a.scale_log2);
+          if (LISTED) {
+            acc[n].i0 = (row + 2 * (lane & 3)) / a.group;
+            acc[n].i1 = (row + 2 * (lane & 3) + 1) / a.group;
+          }
+        }
+      }
+      const int nvalid = min(32, info.x - 32 * wg), seen = LISTED ? s_desc[s].seen - 32 * wg : nvalid;
+      const float2 *const sc = reinterpret_cast<const float2 *>(base_ptr + SL::scales + s * 128);
+      if (nvalid > 0) {
+        if (!LISTED || seen >= nvalid)
+          q8_tiles<D, KIND, NT, false>(acc, ref, base + s * SL::kStage, at, sc, a.log2_box, wg, lane, nvalid, seen);
+        else
+          q8_tiles<D, KIND, NT, LISTED>(acc, ref, base + s * SL::kStage, at, sc, a.log2_box, wg, lane, nvalid, seen);
+      }
       if (info.y & kEnds) {
         const Q8Desc d = s_desc[s];
-        group_bar(grp);  // every warp is done with this stage's tiles: the results go there
-        MergeArea r;
-        r.o = reinterpret_cast<float *>(base_ptr + s * SL::kStage);
-        r.m = r.o + kConsumerWarps * a.group * q8_row(D);
-        r.l = r.m + kConsumerWarps * kMaxGroup;
-        q8_stash<D>(acc, r, a.group, wg, lane);
-        group_bar(grp);
-        q8_finish<D>(a, r, d, grp, tid, s_flag, s_last);
+        q8_finish<D, NT, LISTED>(a, acc, ref.vref, reinterpret_cast<float *>(base_ptr + s * SL::kStage), d, grp, tid, s_flag,
+                         s_last);
         dev::fence_proxy_async_smem();  // the results, ahead of the boxes that follow them
       }
       if (info.y & kLastOne) break;
@@ -937,7 +1038,7 @@ __global__ void __launch_bounds__(q8_threads(D), 1)
   }
 }
 
-bool g_q8_attr[kMaxDevices][2][2];  // kernel attributes set [head_dim][kind]
+bool g_q8_attr[kMaxDevices][2][2][3];  // kernel attributes set [head_dim][kind][NT - 1 + listed]
 
 struct Q8Layout {
   size_t o_part, lse_part, total;
@@ -945,8 +1046,8 @@ struct Q8Layout {
 
 // The words that are zero between calls first, at the same place for every call; then the partial
 // rows of as many shares as the GPU holds groups.
-Q8Layout q8_layout(int group, int d, int sms) {
-  const size_t rows = (size_t)2 * std::min(sms * q8_groups(d), kQ8MaxShares) * group;
+Q8Layout q8_layout(int part_rows, int d, int sms) {
+  const size_t rows = (size_t)2 * std::min(sms * q8_groups(d, 1), kQ8MaxShares) * part_rows;
   Q8Layout l;
   l.o_part = 2 * kQ8MaxShares * sizeof(uint32_t);
   l.lse_part = l.o_part + rows * d * sizeof(float);
@@ -955,7 +1056,8 @@ Q8Layout q8_layout(int group, int d, int sms) {
 }
 
 struct DecodeQ8 {
-  const int32_t *seqs;
+  const int4 *queries;
+  int32_t most_queries;  // of a listed sequence
   pkv_bf16 *out;
   const pkv_bf16 *q;
   const pkv_q8_cache *cache;
@@ -991,12 +1093,12 @@ int check_decode_q8(const DecodeQ8 &x, const char *fn) {
   return PKV_OK;
 }
 
-template <int D, int KIND>
+template <int D, int KIND, int NT, bool LISTED>
 int launch_decode_q8(const DecodeQ8 &x, cudaStream_t stream, bool step) {
   const pkv_cache_desc &c = *x.desc;
   CUtensorMap tm0, tm1 = {};
   int sms = 0;
-  auto *const kern = decode_q8_kernel<D, KIND>;
+  auto *const kern = decode_q8_kernel<D, KIND, NT, LISTED>;
   const int box = std::min(c.block_size, kQ8Keys);
   // One map for both pools where they are whole rows apart (half the copies: 16 keys of head_dim 64
   // took the producer longer to issue than HBM to bring).
@@ -1012,22 +1114,23 @@ int launch_decode_q8(const DecodeQ8 &x, cudaStream_t stream, bool step) {
         (rc = codes_map(first, depth ? apart : 0, c, box, &tm0)) ||
         (!depth && (rc = codes_map(second, 0, c, box, &tm1))))
       return rc;
-    bool *const attr = &g_q8_attr[dev][D == 64 ? 0 : 1][KIND];
+    bool *const attr = &g_q8_attr[dev][D == 64 ? 0 : 1][KIND][NT - 1 + LISTED];
     if (!*attr) {
-      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)q8_smem(D));
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)q8_smem<D, NT>());
       if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
       if (e != cudaSuccess) return cuda_error(e, "cudaFuncSetAttribute");
       *attr = true;
     }
   }
-  const Q8Layout l = q8_layout(x.hq / c.num_kv_heads, D, sms);
+  const int part_rows = x.hq / c.num_kv_heads * (LISTED ? x.most_queries : 1);
+  const Q8Layout l = q8_layout(part_rows, D, sms);
   char *const ws = static_cast<char *>(x.workspace);
   Q8Args a;
   a.q = x.q;
   a.out = x.out;
   a.tables = x.tables;
   a.lens = x.lens;
-  a.seqs = x.seqs;
+  a.queries = x.queries;
   a.k_scale = x.cache->k_scale;
   a.v_scale = x.cache->v_scale;
   a.counters = reinterpret_cast<uint32_t *>(ws);
@@ -1040,6 +1143,7 @@ int launch_decode_q8(const DecodeQ8 &x, cudaStream_t stream, bool step) {
   a.num_q_heads = x.hq;
   a.num_kv_heads = c.num_kv_heads;
   a.group = x.hq / c.num_kv_heads;
+  a.rows = part_rows;
   a.block_size = c.block_size;
   a.log2_bs = ilog2(c.block_size);
   a.box_rows = box;
@@ -1051,55 +1155,51 @@ int launch_decode_q8(const DecodeQ8 &x, cudaStream_t stream, bool step) {
   // one CTA per SM; fewer where the batch cannot have that many shares
   const int64_t most =
       (((int64_t)x.max_len + kQ8Keys - 1) / kQ8Keys * kChunkCost + kEndCost) * x.num_seqs * c.num_kv_heads;
-  const int64_t ctas = std::min(sms, kQ8MaxShares / q8_groups(D));
+  const int64_t ctas = std::min(sms, kQ8MaxShares / q8_groups(D, NT));
   const int64_t grid = std::max<int64_t>(1, std::min(ctas, most / kMinCost));
   const cudaError_t e =
-      q8::launch_early(kern, dim3((unsigned)grid), q8_threads(D), q8_smem(D), stream, tm0, tm1, a);
+      q8::launch_early(kern, dim3((unsigned)grid), q8_threads(D, NT), q8_smem<D, NT>(), stream, tm0, tm1, a);
   if (e != cudaSuccess) return cuda_error(e, "decode_q8_kernel launch");
   return PKV_OK;
 }
 
-int launch_decode_q8(const DecodeQ8 &x, cudaStream_t s, bool step) {
-  if (x.num_seqs == 0) return PKV_OK;
+template <int NT, bool LISTED>
+int launch_kinds_q8(const DecodeQ8 &x, cudaStream_t s, bool step) {
   const bool i8 = x.cache->kind == PKV_Q8_INT8;
   if (x.desc->head_dim == 64)
-    return i8 ? launch_decode_q8<64, PKV_Q8_INT8>(x, s, step)
-              : launch_decode_q8<64, PKV_Q8_E4M3>(x, s, step);
-  return i8 ? launch_decode_q8<128, PKV_Q8_INT8>(x, s, step)
-            : launch_decode_q8<128, PKV_Q8_E4M3>(x, s, step);
+    return i8 ? launch_decode_q8<64, PKV_Q8_INT8, NT, LISTED>(x, s, step)
+              : launch_decode_q8<64, PKV_Q8_E4M3, NT, LISTED>(x, s, step);
+  return i8 ? launch_decode_q8<128, PKV_Q8_INT8, NT, LISTED>(x, s, step)
+            : launch_decode_q8<128, PKV_Q8_E4M3, NT, LISTED>(x, s, step);
 }
 
-// The rows of a few queries per sequence as sequences of their own: query i of n sees the context's
-// first L - n + i + 1 keys.  Also zeroes the decode's counters (this workspace keeps none).
-struct RowsArgs {
+int launch_decode_q8(const DecodeQ8 &x, cudaStream_t s, bool step) {
+  return x.num_seqs == 0 ? PKV_OK : launch_kinds_q8<1, false>(x, s, step);
+}
+
+// A few queries per sequence as a list for decode_q8_kernel, `each` queries to an entry, `per` entries to a
+// sequence: query i of n sees the context's first L - n + i + 1 keys.  Also zeroes the decode's
+// counters (this workspace keeps none).
+struct ListArgs {
   const int32_t *start, *lens;
-  int32_t *row_lens, *row_seqs;
+  int4 *queries;
+  int32_t *seen;  // keys that an entry's last query sees
   uint32_t *counters;
-  int32_t num_seqs, num_queries, max_new, cap;
+  int32_t num_seqs, num_queries, max_new, cap, each, per;
 };
-__global__ void __launch_bounds__(256) query_rows_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(256) list_queries_kernel(const ListArgs a) {
   q8::await_stream();
   q8::let_next_begin();
-  const int i = blockIdx.x * 256 + threadIdx.x;
+  const int i = blockIdx.x * 256 + threadIdx.x, b = i / a.per, first = (i - b * a.per) * a.each;
   if (i < 2 * kQ8MaxShares) a.counters[i] = 0u;
-  if (i < a.num_seqs) {
-    const int L = __ldg(a.lens + i), s = __ldg(a.start + i), e = __ldg(a.start + i + 1);
-    if (L < 0 || L > a.cap || s < 0 || e < s || e > a.num_queries || e - s > a.max_new || e - s > max(L, 0))
-      raise_error(PKV_DEVERR_CONTEXT_LEN);
-  }
-  if (i >= a.num_queries) return;
-  int b = 0, end = a.num_seqs;  // the last sequence that starts at or before row i
-  while (end - b > 1) {
-    const int mid = (b + end) / 2;
-    if (__ldg(a.start + mid) <= i)
-      b = mid;
-    else
-      end = mid;
-  }
-  const int s = __ldg(a.start + b), n = min(__ldg(a.start + b + 1) - s, a.max_new), at = i - s;
-  const bool in = at >= 0 && at < n;
-  a.row_seqs[i] = in ? b : -1;
-  a.row_lens[i] = in ? max(min(max(__ldg(a.lens + b), 0), a.cap) - n + at + 1, 0) : 0;
+  if (b >= a.num_seqs) return;
+  const int L = __ldg(a.lens + b), s0 = __ldg(a.start + b), e0 = __ldg(a.start + b + 1);
+  const int len = min(max(L, 0), a.cap), s = min(max(s0, 0), a.num_queries);
+  const int n = min(max(min(e0, a.num_queries) - s, 0), a.max_new);
+  if (first == 0 && (len != L || s != s0 || s + n != e0 || n > len)) raise_error(PKV_DEVERR_CONTEXT_LEN);
+  const int count = min(n - first, a.each), sees = len - n + first + 1;
+  a.queries[i] = count > 0 ? make_int4(b, s + first, count, sees) : make_int4(-1, 0, 0, 0);
+  a.seen[i] = count > 0 ? max(sees + count - 1, 0) : 0;
 }
 
 // Both halves of a step checked, then both enqueued.
@@ -1114,30 +1214,37 @@ int step_q8(const WriteQ8 &w, const DecodeQ8 &x, cudaStream_t s, const char *fn)
 
 }  // namespace
 
-size_t rows_q8_workspace(int32_t num_queries, int32_t d, int sms) {
-  return q8_layout(kMaxGroup, d, sms).total + (size_t)num_queries * 8;
+int32_t list_each(int32_t group) { return 2 * kRowTile / group; }
+
+size_t list_q8_workspace(int64_t entries, int32_t d, int sms) {
+  return q8_layout(2 * kRowTile, d, sms).total + (size_t)entries * (sizeof(int4) + sizeof(int32_t));
 }
 
-int launch_rows_q8(const ChunkLaunch &l, const pkv_q8_cache &cache, const pkv_cache_desc &c,
+int launch_list_q8(const ChunkLaunch &l, const pkv_q8_cache &cache, const pkv_cache_desc &c,
                    const int32_t *block_tables, int32_t max_blocks, void *workspace, int sms, cudaStream_t stream) {
-  const size_t decode = q8_layout(kMaxGroup, c.head_dim, sms).total;
-  RowsArgs r;
+  const size_t decode = q8_layout(2 * kRowTile, c.head_dim, sms).total;
+  ListArgs r;
   r.start = l.query_start;
   r.lens = l.context_lens;
-  r.row_lens = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + decode);
-  r.row_seqs = r.row_lens + l.num_queries;
+  const int32_t group = l.num_q_heads / l.num_kv_heads;
+  r.each = std::min(list_each(group), l.max_query_len);
+  r.per = (l.max_query_len + r.each - 1) / r.each;
+  const int32_t entries = l.num_seqs * r.per;
+  r.queries = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + decode);
+  r.seen = reinterpret_cast<int32_t *>(r.queries + entries);
   r.counters = static_cast<uint32_t *>(workspace);
   r.num_seqs = l.num_seqs;
   r.num_queries = (int32_t)l.num_queries;
   r.max_new = l.max_query_len;
   r.cap = l.max_context;
-  const int threads = std::max({2 * kQ8MaxShares, r.num_seqs, r.num_queries});
+  const int threads = std::max(2 * kQ8MaxShares, (int)entries);
   const cudaError_t e =
-      q8::launch_early(query_rows_kernel, dim3((unsigned)((threads + 255) / 256)), 256, 0, stream, r);
-  if (e != cudaSuccess) return cuda_error(e, "query_rows_kernel launch");
-  const DecodeQ8 x = {r.row_seqs, l.out, l.q, &cache, block_tables, max_blocks, r.row_lens, l.max_context,
-                      r.num_queries, l.num_q_heads, &c, l.scale, workspace, decode};
-  return launch_decode_q8(x, stream, false);
+      q8::launch_early(list_queries_kernel, dim3((unsigned)((threads + 255) / 256)), 256, 0, stream, r);
+  if (e != cudaSuccess) return cuda_error(e, "list_queries_kernel launch");
+  const DecodeQ8 x = {r.queries, r.each, l.out, l.q, &cache, block_tables, max_blocks, r.seen, l.max_context,
+                      entries, l.num_q_heads, &c, l.scale, workspace, decode};
+  // two tiles of rows only where one does not hold an entry: the second costs half as much again
+  return r.each * group > kRowTile ? launch_kinds_q8<2, true>(x, stream, false) : launch_kinds_q8<1, true>(x, stream, false);
 }
 
 cudaError_t read_decode_q8_errors(uint32_t *flags, int clear) { return read_tu_errors(flags, clear); }
@@ -1161,7 +1268,7 @@ PKV_API int paged_decode_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, const pk
                                       const int32_t *context_lens, int32_t max_context_len, int32_t num_seqs,
                                       int32_t num_q_heads, const pkv_cache_desc *desc, float scale, void *workspace,
                                       size_t workspace_bytes, void *stream) {
-  const DecodeQ8 x = {nullptr, out, q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
+  const DecodeQ8 x = {nullptr, 1, out, q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
                       num_seqs, num_q_heads, desc, scale, workspace, workspace_bytes};
   int rc = check_decode_q8(x, "paged_decode_attention_q8");
   if (!rc) rc = launch_decode_q8(x, static_cast<cudaStream_t>(stream), false);
@@ -1179,7 +1286,7 @@ PKV_API int paged_decode_step_q8(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf1
   w.k = k, w.v = v, w.k_stride = k_stride, w.v_stride = v_stride, w.num_tokens = num_seqs, w.max_query_len = 1;
   w.block_tables = block_tables, w.max_blocks = max_blocks_per_seq, w.context_lens = context_lens;
   w.num_seqs = num_seqs, w.cache = cache, w.desc = desc;
-  const DecodeQ8 x = {nullptr, out, q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
+  const DecodeQ8 x = {nullptr, 1, out, q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
                       num_seqs, num_q_heads, desc, scale, workspace, workspace_bytes};
   return step_q8(w, x, static_cast<cudaStream_t>(stream), "paged_decode_step_q8");
 }
@@ -1204,7 +1311,7 @@ PKV_API int paged_decode_step_rope_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t 
   w.num_q_heads = num_q_heads;
   w.positions = positions, w.cos_sin = cos_sin, w.max_position = max_position;
   w.rotary_dim = rotary_dim, w.neox_style = neox_style;
-  const DecodeQ8 x = {nullptr, out, q_out, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
+  const DecodeQ8 x = {nullptr, 1, out, q_out, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
                       num_seqs, num_q_heads, desc, scale, workspace, workspace_bytes};
   return step_q8(w, x, static_cast<cudaStream_t>(stream), fn);
 }

@@ -198,11 +198,13 @@ struct ChunkLaunch {
   float scale;
 };
 int launch_chunk(const ChunkLaunch &l, cudaStream_t stream);
-// The same for a few queries per sequence (pkv_decode_q8.cu), straight from the 8-bit cache: every
-// query a sequence of the decode kernel.  k, v and the units are not read; the workspace needs no
+// The same for a few queries per sequence (pkv_decode_q8.cu), straight from the 8-bit cache: a list of
+// up to list_each(group) queries an entry, as the decode kernel's sequences.  k, v and the units are not
+// read; the workspace (for num_seqs * ceil(max_query_len / list_each) entries, which fit int32) needs no
 // initial values.
-size_t rows_q8_workspace(int32_t num_queries, int32_t d, int sms);
-int launch_rows_q8(const ChunkLaunch &l, const pkv_q8_cache &cache, const pkv_cache_desc &c,
+int32_t list_each(int32_t group);
+size_t list_q8_workspace(int64_t entries, int32_t d, int sms);
+int launch_list_q8(const ChunkLaunch &l, const pkv_q8_cache &cache, const pkv_cache_desc &c,
                    const int32_t *block_tables, int32_t max_blocks, void *workspace, int sms, cudaStream_t stream);
 
 }  // namespace pkv

@@ -846,8 +846,8 @@ PKV_API int paged_kv_read_q8(pkv_bf16 *k_out, pkv_bf16 *v_out, int64_t k_stride,
 }
 
 // ---------------------------------------------------------------------------
-// Chunked prefill.  A few queries per sequence (draft tokens to check) are rows of the decode kernel,
-// each a sequence of its own that reads the codes as they are; more of them take the tensor-core
+// Chunked prefill.  A few queries per sequence (draft tokens to check) are rows of the decode kernel, up
+// to 16 of a kv head for each pass over the codes as they are; more of them take the tensor-core
 // tiles of the packed prompts: the contexts are read back into fp16 rows in the workspace, and the tensor-core
 // tiles of the packed prompts run over those.  (Widening the codes where the tiles stage them would
 // be done once for every 256 query rows that see them, on the warps that the softmax waits for; the
@@ -859,25 +859,21 @@ struct PrefillLayout {
   int32_t rows;  // packed rows of a sequence
   size_t k, v, k_unit, v_unit, nan_from, order, total;
 };
-constexpr int kMaxRowQueries = 32, kMaxRows = 65535;  // of a sequence, of a call, as the decode's rows
-int64_t row_capacity(int32_t num_seqs) { return std::min((int64_t)num_seqs * kMaxRowQueries, (int64_t)kMaxRows); }
+constexpr int kMaxListed = 32, kMaxEntries = 65535;  // queries of a sequence, entries of a call's list
+constexpr int kMaxPer = 16;  // entries of a sequence: of 2 queries at least (a kv head has up to 8 rows a query)
 
-// Whether the decode's rows are the shorter way, by the longest context: they read it once for each
-// query, spread over the GPU; the tiles read it once (and once more back), but the CTAs of one
-// (sequence, kv head) take its blocks of 128 keys one after another.  Times as measured: 1.5 or 1.75
-// us of a group's chunk; 1.5 us of a tile's block, 4 TB/s and two launches for the reading back.
-// With 8 kv heads of 4 x 64: 8 sequences of 2 queries over 4000 tokens 21 us by rows, 69 by tiles, of
-// 8 queries 54 and 69, of 32 182 and 70; 64 of 8 over 500 60 and 57; one of 32 over 20000 107 and 218.
-bool rows_pay(int64_t num_queries, int32_t max_query_len, int32_t num_seqs, int32_t hq, const pkv_cache_desc &c,
-              int32_t max_len, int sms) {
-  // (packed rows that no sequence has count too: the workspace holds row_capacity of them)
-  if (max_query_len > kMaxRowQueries || num_queries > row_capacity(num_seqs)) return false;
-  const double blocks = (max_len + 127) / 128, hkv = c.num_kv_heads;
-  const double groups = c.head_dim == 64 ? 3 : 2, tokens = 2 * (128 / (hq / c.num_kv_heads));
-  const double rows = num_queries * hkv * blocks / (sms * groups) * (c.head_dim == 64 ? 1.5 : 1.75) + 2;
-  const double ctas = (num_queries / tokens + num_seqs) * hkv;
+// Whether a list for the decode kernel is the shorter way, by the longest context: it reads that once for
+// each entry, spread over the GPU; the tiles read it once (and once more back), but the CTAs of one
+// (sequence, kv head) take its blocks of 128 keys one after another.  Times as measured: LISTT
+bool list_pays(int64_t num_queries, int32_t max_query_len, int32_t num_seqs, int32_t hq, const pkv_cache_desc &c,
+               int32_t max_len, int sms) {
+  const int32_t group = hq / c.num_kv_heads, each = list_each(group), per = (max_query_len + each - 1) / each;
+  if (max_query_len > kMaxListed || (int64_t)num_seqs * per > kMaxEntries) return false;
+  const double blocks = (max_len + 127) / 128, hkv = c.num_kv_heads, groups = c.head_dim == 64 ? 3 : 2;
+  const double list = (double)num_seqs * per * hkv * blocks / (sms * groups) * (c.head_dim == 64 ? 2. : 2.) + 2;
+  const double ctas = (num_queries / (2. * (128 / group)) + num_seqs) * hkv;
   const double tiles = (ctas > sms ? ctas / sms : 1) * blocks * 1.5 + 8 + num_seqs * hkv * c.head_dim * max_len * 6. / 4e6;
-  return rows < tiles;
+  return list < tiles;
 }
 
 bool prefill_layout(int32_t num_seqs, int32_t hkv, int32_t d, int32_t max_len, int sms, PrefillLayout *p) {
@@ -893,7 +889,7 @@ bool prefill_layout(int32_t num_seqs, int32_t hkv, int32_t d, int32_t max_len, i
   p->nan_from = p->v_unit + units;
   p->order = p->nan_from + units;
   p->total = std::max(p->order + up((size_t)num_seqs * sizeof(int4)),  // either way
-                      up(rows_q8_workspace((int32_t)row_capacity(num_seqs), d, sms)));
+                      up(list_q8_workspace(std::min((int64_t)num_seqs * kMaxPer, (int64_t)kMaxEntries), d, sms)));
   return true;
 }
 
@@ -958,8 +954,8 @@ PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t
   l.num_kv_heads = desc->num_kv_heads;
   l.head_dim = desc->head_dim;
   l.scale = scale;
-  if (rows_pay(num_queries, max_query_len, num_seqs, num_q_heads, *desc, max_context_len, sms)) {
-    rc = launch_rows_q8(l, *cache, *desc, block_tables, max_blocks_per_seq, workspace, sms, s);
+  if (list_pays(num_queries, max_query_len, num_seqs, num_q_heads, *desc, max_context_len, sms)) {
+    rc = launch_list_q8(l, *cache, *desc, block_tables, max_blocks_per_seq, workspace, sms, s);
     if (!rc) clear_error();
     return rc;
   }
