@@ -575,7 +575,8 @@ int paged_decode_step_rope_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t q_stride
  * query_start[b+1]-1.  The contexts are read back as fp16 rows into the workspace
  * (paged_prefill_q8_workspace_size() bytes, no initial values; not for two calls that overlap),
  * scores and weights are fp16 products with fp32 sums as in paged_decode_attention_q8; or, where
- * that is estimated to be less (up to 32 queries of a sequence), each query is a row of its kernel.
+ * that is estimated to be less (up to 32 queries of a sequence), a few queries at a time are rows of its
+ * kernel.
  * max_query_len and max_context_len bound every length; longer ones, and sequences of more queries
  * than tokens, raise PKV_DEVERR_CONTEXT_LEN (they are cut; a query before the first token gives
  * zeros).  Rows of no sequence are not written.  A page of scale NaN (see paged_kv_write_q8) makes

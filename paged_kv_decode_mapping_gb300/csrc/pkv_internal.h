@@ -199,10 +199,15 @@ struct ChunkLaunch {
 };
 int launch_chunk(const ChunkLaunch &l, cudaStream_t stream);
 // The same for a few queries per sequence (pkv_decode_q8.cu), straight from the 8-bit cache: a list of
-// up to list_each(group) queries an entry, as the decode kernel's sequences.  k, v and the units are not
-// read; the workspace (for num_seqs * ceil(max_query_len / list_each) entries, which fit int32) needs no
-// initial values.
-int32_t list_each(int32_t group);
+// entries of a few queries, as the decode kernel's sequences.  k, v and the units are not read; the
+// workspace (for num_seqs * per entries) needs no initial values.
+struct ListPlan {
+  int32_t each, per;  // queries of an entry, entries of a sequence (kMaxListPer at most)
+  int32_t tiles;      // of 8 rows, of an entry
+  double block;       // us of an entry's 128 keys, over the groups of an SM
+};
+constexpr int kMaxListPer = 16;
+ListPlan list_plan(int32_t group, int32_t head_dim, int32_t max_query_len);  // max_query_len 1 .. 32
 size_t list_q8_workspace(int64_t entries, int32_t d, int sms);
 int launch_list_q8(const ChunkLaunch &l, const pkv_q8_cache &cache, const pkv_cache_desc &c,
                    const int32_t *block_tables, int32_t max_blocks, void *workspace, int sms, cudaStream_t stream);

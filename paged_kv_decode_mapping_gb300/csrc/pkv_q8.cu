@@ -860,19 +860,23 @@ struct PrefillLayout {
   size_t k, v, k_unit, v_unit, nan_from, order, total;
 };
 constexpr int kMaxListed = 32, kMaxEntries = 65535;  // queries of a sequence, entries of a call's list
-constexpr int kMaxPer = 16;  // entries of a sequence: of 2 queries at least (a kv head has up to 8 rows a query)
 
 // Whether a list for the decode kernel is the shorter way, by the longest context: it reads that once for
 // each entry, spread over the GPU; the tiles read it once (and once more back), but the CTAs of one
-// (sequence, kv head) take its blocks of 128 keys one after another.  Times as measured: LISTT
+// (sequence, kv head) take its blocks of 128 keys one after another.  Times as measured: list_plan's, 10 us
+// besides; 1.3 us of a tile's block, 6 TB/s for the reading back, 12 us besides.  With 8 kv heads of
+// 4 x 64: 8 sequences of 2 queries over 4000 tokens 16 us by a list, 67 by tiles, of 8 queries 28 and
+// 67, of 32 75 and 68; 64 of 8 143 and 291, of 16 276 and 291, of 32 539 and 292.
 bool list_pays(int64_t num_queries, int32_t max_query_len, int32_t num_seqs, int32_t hq, const pkv_cache_desc &c,
                int32_t max_len, int sms) {
-  const int32_t group = hq / c.num_kv_heads, each = list_each(group), per = (max_query_len + each - 1) / each;
-  if (max_query_len > kMaxListed || (int64_t)num_seqs * per > kMaxEntries) return false;
-  const double blocks = (max_len + 127) / 128, hkv = c.num_kv_heads, groups = c.head_dim == 64 ? 3 : 2;
-  const double list = (double)num_seqs * per * hkv * blocks / (sms * groups) * (c.head_dim == 64 ? 2. : 2.) + 2;
+  if (max_query_len > kMaxListed) return false;
+  const int32_t group = hq / c.num_kv_heads;
+  const ListPlan plan = list_plan(group, c.head_dim, max_query_len);
+  if ((int64_t)num_seqs * plan.per > kMaxEntries) return false;
+  const double blocks = (max_len + 127) / 128, hkv = c.num_kv_heads;
+  const double list = (double)num_seqs * plan.per * hkv * (blocks + 1) / sms * plan.block + 10;  // (an end as a block)
   const double ctas = (num_queries / (2. * (128 / group)) + num_seqs) * hkv;
-  const double tiles = (ctas > sms ? ctas / sms : 1) * blocks * 1.5 + 8 + num_seqs * hkv * c.head_dim * max_len * 6. / 4e6;
+  const double tiles = (ctas > sms ? ctas / sms : 1) * blocks * 1.3 + 12 + num_seqs * hkv * c.head_dim * max_len * 6. / 6e6;
   return list < tiles;
 }
 
@@ -889,7 +893,7 @@ bool prefill_layout(int32_t num_seqs, int32_t hkv, int32_t d, int32_t max_len, i
   p->nan_from = p->v_unit + units;
   p->order = p->nan_from + units;
   p->total = std::max(p->order + up((size_t)num_seqs * sizeof(int4)),  // either way
-                      up(list_q8_workspace(std::min((int64_t)num_seqs * kMaxPer, (int64_t)kMaxEntries), d, sms)));
+                      up(list_q8_workspace(std::min((int64_t)num_seqs * kMaxListPer, (int64_t)kMaxEntries), d, sms)));
   return true;
 }
 

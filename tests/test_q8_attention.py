@@ -336,6 +336,19 @@ def test_prefill(B, dtype, lens, new, hq, hkv, d, bs):
     assert B.pkv_device_errors() == 0
 
 
+@pytest.mark.parametrize("dtype", R.KINDS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (2, 2), (6, 2), (4, 1), (10, 2), (7, 1), (8, 1)])
+@pytest.mark.parametrize("lens,new", [
+    ([2, 9, 131, 0, 257, 5000, 128, 40], [2, 9, 7, 0, 8, 6, 1, 3]),       # a page's and a chunk's border between queries
+    ([130, 300, 16, 9000], [17, 32, 16, 31]),
+    ([260] * 40, [3, 4] * 20),
+])
+def test_few_queries(B, dtype, d, hq, hkv, lens, new):
+    """Entries of 1 to 16 rows, whole and in part filled, whose queries end in different chunks."""
+    test_prefill(B, dtype, lens, new, hq, hkv, d, 16)
+
+
 @pytest.mark.parametrize("new", [[4, 5], [150, 170]])  # as rows of the decode, and on the tiles
 def test_prefill_of_hard_values(B, new):
     """Queries of any size, a scale below 0, pages of scales far apart and of zeros."""
