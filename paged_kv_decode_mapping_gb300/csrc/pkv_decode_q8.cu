@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(q8_threads(D, NT), 1)
   if (!a.step) q8::await_stream();
   const int Hkv = a.num_kv_heads;
   const int cap = (int)min((int64_t)a.max_blocks * a.block_size, (int64_t)a.max_len);
-  auto length = [&](int b) { return min(max(__ldg(a.lens + b), 0), cap); };
+  auto length = [&](int b) { return min(max(q8::ld(a.lens + b), 0), cap); };
   auto chunks_of = [](int L) { return (int)(((int64_t)L + kQ8Keys - 1) / kQ8Keys); };
   auto cost_of = [&](int L) { return L > 0 ? kChunkCost * (int64_t)chunks_of(L) + kEndCost : 0; };  // of a kv head
   auto shares_of = [&](int64_t w) { return min((int64_t)gridDim.x * GROUPS, max((int64_t)1, q8::quotient(w, kMinCost))); };
@@ -762,8 +762,8 @@ __global__ void __launch_bounds__(q8_threads(D, NT), 1)
   // Entries of the block table, one a lane.
   auto entries = [&](int b, int at) {
     if (b >= a.num_seqs) return 0;
-    const int seq = LISTED ? max(__ldg(&a.queries[b].x), 0) : b;
-    return at + lane < a.max_blocks ? __ldg(a.tables + (int64_t)seq * a.max_blocks + at + lane) : 0;
+    const int seq = LISTED ? max(q8::ld(&a.queries[b].x), 0) : b;
+    return at + lane < a.max_blocks ? q8::ld(a.tables + (int64_t)seq * a.max_blocks + at + lane) : 0;
   };
 
   // The table window of where this share would begin if all contexts had max_len keys: for equal
@@ -788,12 +788,12 @@ __global__ void __launch_bounds__(q8_threads(D, NT), 1)
   const int b_lo = min((int)threadIdx.x * run, a.num_seqs), b_hi = min(b_lo + run, a.num_seqs);
   int64_t incl = 0;
   for (int b = b_lo; b < b_hi; ++b) {
-    const int L0 = __ldg(a.lens + b), L = min(max(L0, 0), cap);
+    const int L0 = q8::ld(a.lens + b), L = min(max(L0, 0), cap);
     if (L != L0 && blockIdx.x == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
     incl += cost_of(L);
     if (L == 0 && b % (int)gridDim.x == (int)blockIdx.x) {  // empty: zeros
       int4 l = make_int4(b, b, 1, 0);
-      if (LISTED) l = __ldg(a.queries + b);
+      if (LISTED) l = q8::ld(a.queries + b);
       uint2 *o = reinterpret_cast<uint2 *>(a.out + (int64_t)l.y * a.num_q_heads * D);
       for (int i = 0; i < l.z * a.num_q_heads * D / 4; ++i) o[i] = make_uint2(0u, 0u);
     }
@@ -907,7 +907,7 @@ __global__ void __launch_bounds__(q8_threads(D, NT), 1)
       if (first) {
         const int64_t end = u0 + kChunkCost * (int64_t)(nch - 1);  // its last chunk's place
         if (LISTED)
-          listed = __ldg(a.queries + b);
+          listed = q8::ld(a.queries + b);
         else
           listed.y = b;
         dsc.row0 = listed.y;
@@ -1193,7 +1193,7 @@ __global__ void __launch_bounds__(256) list_queries_kernel(const ListArgs a) {
   const int i = blockIdx.x * 256 + threadIdx.x, b = i / a.per, first = (i - b * a.per) * a.each;
   if (i < 2 * kQ8MaxShares) a.counters[i] = 0u;
   if (b >= a.num_seqs) return;
-  const int L = __ldg(a.lens + b), s0 = __ldg(a.start + b), e0 = __ldg(a.start + b + 1);
+  const int L = q8::ld(a.lens + b), s0 = q8::ld(a.start + b), e0 = q8::ld(a.start + b + 1);
   const int len = min(max(L, 0), a.cap), s = min(max(s0, 0), a.num_queries);
   const int n = min(max(min(e0, a.num_queries) - s, 0), a.max_new);
   if (first == 0 && (len != L || s != s0 || s + n != e0 || n > len)) raise_error(PKV_DEVERR_CONTEXT_LEN);

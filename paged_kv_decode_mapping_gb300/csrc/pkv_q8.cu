@@ -38,11 +38,11 @@ struct Tokens {
 // The tokens of sequence b.  Without `start` one token for each sequence that has any, packed row
 // b.  Lengths that do not fit the tables, the packed rows or max_new: none, and *bad is set.
 __device__ __forceinline__ Tokens tokens_of(const Span &s, int b, bool *bad) {
-  const int L = __ldg(s.lens + b);
+  const int L = q8::ld(s.lens + b);
   int64_t row0 = b, n = L > 0 ? 1 : 0;
   if (s.start) {
-    row0 = __ldg(s.start + b);
-    n = (int64_t)__ldg(s.start + b + 1) - row0;
+    row0 = q8::ld(s.start + b);
+    n = (int64_t)q8::ld(s.start + b + 1) - row0;
   }
   *bad = L < 0 || (int64_t)L > (int64_t)s.max_blocks * s.block_size || n < 0 || n > s.max_new || n > L ||
          row0 < 0 || row0 + n > s.num_tokens;
@@ -64,7 +64,7 @@ struct Rope {
 };
 
 __device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  const float4 a = q8::ld(reinterpret_cast<const float4 *>(p)), b = q8::ld(reinterpret_cast<const float4 *>(p) + 1);
   f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
 }
 
@@ -79,8 +79,8 @@ __device__ __forceinline__ Angles angles_of(const float *cs, int c, const Rope &
     load8(cs + 8 * e, a.c);
     load8(cs + p.r / 2 + 8 * e, a.s);
   } else {
-    const float4 c4 = __ldg(reinterpret_cast<const float4 *>(cs + 4 * c));
-    const float4 s4 = __ldg(reinterpret_cast<const float4 *>(cs + p.r / 2 + 4 * c));
+    const float4 c4 = q8::ld(reinterpret_cast<const float4 *>(cs + 4 * c));
+    const float4 s4 = q8::ld(reinterpret_cast<const float4 *>(cs + p.r / 2 + 4 * c));
     a.c[0] = c4.x, a.c[1] = c4.y, a.c[2] = c4.z, a.c[3] = c4.w;
     a.s[0] = s4.x, a.s[1] = s4.y, a.s[2] = s4.z, a.s[3] = s4.w;
   }
@@ -159,7 +159,7 @@ __device__ __forceinline__ void rotate_q(const WriteArgs &a, const Tokens &t, ui
     const int64_t run = i / (V / 2), tok = q8::quotient(run, runs);
     const int h0 = (int)(run - tok * runs) * kRotateHeads, heads = min(a.num_q_heads - h0, kRotateHeads);
     const int64_t at = t.row0 + tok;
-    const int64_t pos = a.rope.positions ? __ldg(a.rope.positions + at) : t.begin + tok;
+    const int64_t pos = a.rope.positions ? q8::ld(a.rope.positions + at) : t.begin + tok;
     if (pos < 0 || pos >= a.rope.max_position) continue;  // reported by the k rows
     const uint4 *const src = a.q + at * a.q_stride + h0 * V;
     uint4 *const dst = a.q_out + at * a.q_out_stride + h0 * V;
@@ -167,7 +167,7 @@ __device__ __forceinline__ void rotate_q(const WriteArgs &a, const Tokens &t, ui
 #pragma unroll
     for (int h = 0; h < kRotateHeads; ++h)
       if (h < heads) {
-        x[h] = src[h * V + ca];  // (not a read-only load: q may be rotated in place)
+        x[h] = src[h * V + ca];
         y[h] = src[h * V + cb];
       }
     if (8 * ca < a.rope.r) {
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(ROPE ? 2 * kQ8Threads : 4 * kQ8Threads, ROPE ?
   const int r0 = max(t.begin - (int)min(lo, (int64_t)t.end), 0);
   const int r1 = (int)min((int64_t)t.end - lo, (int64_t)a.s.block_size);
   live = live && r1 > r0;  // rows r0 .. r1-1 are new, rows before r0 are held
-  int64_t phys = live ? __ldg(a.s.tables + (int64_t)b * a.s.max_blocks + page) : 0;
+  int64_t phys = live ? q8::ld(a.s.tables + (int64_t)b * a.s.max_blocks + page) : 0;
   if (phys < 0 || phys >= a.s.num_blocks) {
     if (gt == 0) raise_error(PKV_DEVERR_BLOCK_ID);
     live = false;
@@ -256,13 +256,13 @@ __global__ void __launch_bounds__(ROPE ? 2 * kQ8Threads : 4 * kQ8Threads, ROPE ?
   // The columns of row first + u * rows_apart.
   auto load = [&](int u, uint4 *x) {
 #pragma unroll
-    for (int p = 0; p < P; ++p) x[p] = __ldg(src + u * apart + col[p]);
+    for (int p = 0; p < P; ++p) x[p] = q8::ld(src + u * apart + col[p]);
   };
   // The same, rotated; false, and zeros, where the row's position has no angles.
   auto turn = [&](int u, uint4 *x) {
     if (!ROPE || is_v) return true;
     const int r = first + u * rows_apart;
-    const int64_t pos = a.rope.positions ? __ldg(a.rope.positions + row0 + r) : lo + r0 + r;
+    const int64_t pos = a.rope.positions ? q8::ld(a.rope.positions + row0 + r) : lo + r0 + r;
     if (pos < 0 || pos >= a.rope.max_position) {
       raise_error(PKV_DEVERR_POSITION);
       x[0] = x[P - 1] = make_uint4(0, 0, 0, 0);
@@ -409,12 +409,12 @@ __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_con
   __shared__ int s_before[32], s_rank[32], s_nan[kUnitThreads];
   const int b = blockIdx.x, H = a.s.num_kv_heads, tid = threadIdx.x;
   const int cap = (int)min((int64_t)a.s.max_blocks * a.s.block_size, (int64_t)a.s.max_new);
-  const int L = min(max(__ldg(a.s.lens + b), 0), cap), pages = (L + a.s.block_size - 1) >> a.s.log2_bs;
+  const int L = min(max(q8::ld(a.s.lens + b), 0), cap), pages = (L + a.s.block_size - 1) >> a.s.log2_bs;
   const int32_t *const row = a.s.tables + (int64_t)b * a.s.max_blocks;
   int before = 0, rank = 0;  // the furthest end of the sequences before b; how many are taken before b
   for (int i = tid; i < a.s.num_seqs; i += kUnitThreads) {
-    if (i < b) before = max(before, min(max(__ldg(a.start + i + 1), 0), a.num_queries));
-    const int Li = min(max(__ldg(a.s.lens + i), 0), cap);
+    if (i < b) before = max(before, min(max(q8::ld(a.start + i + 1), 0), a.num_queries));
+    const int Li = min(max(q8::ld(a.s.lens + i), 0), cap);
     rank += Li > L || (Li == L && i < b);
   }
   before = __reduce_max_sync(0xffffffffu, before);
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_con
     before = __reduce_max_sync(0xffffffffu, s_before[tid]);
     rank = __reduce_add_sync(0xffffffffu, s_rank[tid]);
     if (tid == 0) {
-      const int s0 = __ldg(a.start + b), e0 = __ldg(a.start + b + 1), e = min(max(e0, 0), a.num_queries);
+      const int s0 = q8::ld(a.start + b), e0 = q8::ld(a.start + b + 1), e = min(max(e0, 0), a.num_queries);
       const int s = min(max(max(s0, 0), before), a.num_queries), n = min(max(e - s, 0), a.max_query_len);
       if (s != s0 || s + n != e0) raise_error(PKV_DEVERR_CONTEXT_LEN);
       a.order[rank] = make_int4(b, s, n, 0);
@@ -442,9 +442,9 @@ __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_con
     if (r < rows)
 #pragma unroll 4
       for (int p = r; p < pages; p += rows) {
-        int64_t phys = __ldg(row + p);
+        int64_t phys = q8::ld(row + p);
         if (phys < 0 || phys >= a.s.num_blocks) phys = 0;  // (flagged by the reading)
-        const float ks = __ldg(a.k_scale + phys * H + h0 + h), vs = __ldg(a.v_scale + phys * H + h0 + h);
+        const float ks = q8::ld(a.k_scale + phys * H + h0 + h), vs = q8::ld(a.v_scale + phys * H + h0 + h);
         if (ks != ks || vs != vs) bad = min(bad, p);
         k = fmaxf(k, ks);
         v = fmaxf(v, vs);
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kQ8Threads, U == 16 ? 5 : 8) read_q8_kernel(co
   if constexpr (WHOLE) {  // lengths past the tables are cut, as the attention does
     const int cap = (int)min((int64_t)a.s.max_blocks * a.s.block_size, (int64_t)a.s.max_new);
     t.begin = 0;
-    t.end = min(max(__ldg(a.s.lens + b), 0), cap);
+    t.end = min(max(q8::ld(a.s.lens + b), 0), cap);
     t.row0 = (int64_t)b * a.out_rows;
   } else {
     bool bad;
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kQ8Threads, U == 16 ? 5 : 8) read_q8_kernel(co
   const int r0 = max(t.begin - (int)min(lo, (int64_t)t.end), 0);
   const int r1 = (int)min((int64_t)t.end - lo, (int64_t)a.s.block_size);
   if (r1 <= r0) return;
-  const int64_t phys = __ldg(a.s.tables + (int64_t)b * a.s.max_blocks + page);
+  const int64_t phys = q8::ld(a.s.tables + (int64_t)b * a.s.max_blocks + page);
   int64_t from = phys;
   if (phys < 0 || phys >= a.s.num_blocks) {
     if (gt == 0) raise_error(PKV_DEVERR_BLOCK_ID);
@@ -508,9 +508,9 @@ __global__ void __launch_bounds__(kQ8Threads, U == 16 ? 5 : 8) read_q8_kernel(co
   const int64_t unit = from * a.s.num_kv_heads + h0;
   float scale = 0.f;  // lane l: head h0 + l's
   if (lane < heads) {
-    scale = __ldg((is_v ? a.v_scale : a.k_scale) + unit + lane);
+    scale = q8::ld((is_v ? a.v_scale : a.k_scale) + unit + lane);
     if constexpr (WHOLE) {
-      const float of = __ldg((is_v ? a.v_unit : a.k_unit) + (int64_t)b * a.s.num_kv_heads + h0 + lane);
+      const float of = q8::ld((is_v ? a.v_unit : a.k_unit) + (int64_t)b * a.s.num_kv_heads + h0 + lane);
       scale = of > 0.f ? __fdiv_rn(scale, of) : scale * 0.f;
     }
   }

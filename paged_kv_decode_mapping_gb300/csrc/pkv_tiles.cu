@@ -192,7 +192,7 @@ __device__ __forceinline__ bool locate_tile(const TileArgs &a, TileCursor &at, i
     at.carry = at.next_carry;
     at.prefix = a.prefix_lens && at.c + lane < a.num ? __ldg(a.prefix_lens + at.c + lane) : 0;
     if constexpr (MODE == kNewest) {
-      const int4 o = at.c + lane < a.num ? __ldg(a.order + at.c + lane) : make_int4(0, 0, 0, 0);
+      const int4 o = at.c + lane < a.num ? q8::ld(a.order + at.c + lane) : make_int4(0, 0, 0, 0);
       at.seq = o.x;
       at.s = o.y;
       at.len = o.z;
@@ -228,7 +228,7 @@ __device__ __forceinline__ bool make_item(const TileArgs &a, TileCursor &at, uns
                    it.seq))
     return false;
   if constexpr (MODE == kNewest) {
-    const int L = __ldg(a.context_lens + it.seq), len = min(max(L, 0), a.max_context);
+    const int L = q8::ld(a.context_lens + it.seq), len = min(max(L, 0), a.max_context);
     if ((len != L || len < it.n) && lane == 0) raise_error(PKV_DEVERR_CONTEXT_LEN);
     it.past = len - it.n;  // (below 0: the first queries see no key, and give zeros)
     it.tok0 = (ntiles - 1 - tile) * tokens;
@@ -749,9 +749,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if constexpr (MODE == kNewest) {
         // The row's queries as fp16, times a power of two for the largest to be in [2^14, 2^15).
         const int64_t unit = (int64_t)it.seq * a.num_kv_heads + it.g;
-        const float k_unit = __ldg(a.k_unit + unit);
-        v_unit = __ldg(a.v_unit + unit);
-        if (see > __ldg(a.nan_from + unit)) v_unit = __int_as_float(0x7fc00000);
+        const float k_unit = q8::ld(a.k_unit + unit);
+        v_unit = q8::ld(a.v_unit + unit);
+        if (see > q8::ld(a.nan_from + unit)) v_unit = __int_as_float(0x7fc00000);
         if (nb > 0) {
           if (!(ok = warp_wait(q_full(t), on & 1))) {
             if (lane == 0) fail(false);

@@ -13,6 +13,10 @@ namespace q8 {
 // and begin by waiting for its end: their launch and its end overlap (calls one after another, 16
 // contexts of 2048 keys: a decode every 13.1 us instead of 14.8; 256 contexts 41.1 instead of 43.3).
 __device__ __forceinline__ void await_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// So what earlier kernels write may change in this one's lifetime, before the wait: plain loads, not the
+// ones for memory that is read-only (which may be moved up).
+template <typename T>
+__device__ __forceinline__ T ld(const T *p) { return *p; }
 // From here on the kernel behind this one may be launched; await_stream() first, unless what that one
 // reads before its own await_stream() is older than both.
 __device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
