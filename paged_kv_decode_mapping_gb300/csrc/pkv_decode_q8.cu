@@ -7,7 +7,7 @@
 //  * Codes are exact in fp16, so the products are mma.sync m16n8k16 fp16 tiles (16 keys x 8 heads)
 //    with fp32 accumulators.  (Of fp8 operands mma.sync is far slower here, and tcgen05's least
 //    tile is 64 or 128 rows where a kv head has at most 8.)  q, scaled by a power of two for its
-//    largest value to be in [2^14, 2^15), is fp16 without loss down to 2^-29 of that value; the
+//    largest value to be in [2^14, 2^15), is fp16 without loss down to 2^-28 of that value; the
 //    weights, times the page's V scale over the largest so far, are fp16 with the largest between
 //    2^10 and 2^15.  Scales of K apply to the scores.  (bf16 weights, without those two scalings,
 //    want a second product for their low halves.)
