@@ -148,3 +148,19 @@ def test_copies(B):
     assert call(caches=(B.pkv_q8_cache * 2)(q8(B), q8(B, ks=None))) == -1
     assert call(n=0, seqs=0) == 0 and call(layers=0, seqs=0) == 0
     assert B.lib().paged_kv_copy_blocks_q8(ctypes.addressof(one), 2, FAKE, None, 0, ctypes.byref(desc(B)), None) == 0
+
+
+def test_the_binding_names_what_is_wrong_with_copies(B):
+    codes, scale, pairs = torch.zeros(4, 2, 16, 64, dtype=torch.int8), torch.zeros(4, 2), torch.zeros(1, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        B.paged_kv_copy_blocks_q8(codes, codes, scale, scale, pairs)
+    with pytest.raises(ValueError, match="shorter"):
+        B.paged_kv_copy_blocks_q8([codes, codes], [codes], [scale] * 2, [scale] * 2, pairs)
+    with pytest.raises(ValueError, match="no layers"):
+        B.paged_kv_compact_q8([], [], [], [], pairs)
+    with pytest.raises(ValueError, match="in front"):
+        B.paged_kv_copy_blocks_q8(codes[None], codes, scale, scale, pairs)
+    with pytest.raises(TypeError, match="alike"):
+        B.paged_kv_copy_blocks_q8(codes, [codes], [scale], [scale], pairs)
+    with pytest.raises(TypeError, match="int8"):
+        B.paged_kv_compact_q8(codes.float(), codes, scale, scale, pairs)
