@@ -117,7 +117,8 @@ __device__ __forceinline__ uint4 rotate_pairs(const uint4 &x, const Angles &a) {
 // ---------------------------------------------------------------------------
 // The write.  One group of 2^log2_group threads (a warp to the whole CTA) per (sequence, touched
 // page, K or V, kv head): it holds the page's new rows in registers between finding their largest
-// value and rounding them, U 16-byte vectors a thread; what does not fit is read a second time.
+// value and rounding them, U 16-byte vectors a thread (where k is rotated, rows that do not fit are read
+// a second time).
 // Bound by its instructions (two thirds of the issue slots; widening, two products and two
 // conversions for each pair of codes) and by HBM: 34000 tokens of 8 heads of 128 take 49 us, 4.4
 // TB/s; with k rotated 84, with 24 heads of q besides 147.  256 tokens of a step: 6 us.
@@ -199,7 +200,8 @@ __device__ __forceinline__ void rotate_q(const WriteArgs &a, const Tokens &t, ui
 }
 
 template <int D, int KIND, bool ROPE, int U>
-__global__ void __launch_bounds__(ROPE ? 2 * kQ8Threads : 4 * kQ8Threads, ROPE ? 3 : 2) write_q8_kernel(const __grid_constant__ WriteArgs a) {
+__global__ void __launch_bounds__(ROPE ? 2 * kQ8Threads : 4 * kQ8Threads, ROPE ? 3 : 2)
+    write_q8_kernel(const __grid_constant__ WriteArgs a) {
   constexpr int V = D / 8;  // vectors of a row: 8 bf16 in, 8 codes out
   q8::await_stream();
   q8::let_next_begin();  // a step's decode: its set-up
