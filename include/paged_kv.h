@@ -608,6 +608,24 @@ int paged_kv_compact_q8(const pkv_q8_cache *caches, int32_t num_layers, const in
                         const pkv_cache_desc *desc, void *stream);
 
 /*
+ * pkv_call_q8 -- one of the 8-bit cache's calls above with its arguments as 64-bit words, for
+ * callers to whom each argument of a foreign call costs time (integers and addresses as they are,
+ * `scale` as a double; a count that does not fit its type is refused as a negative one is):
+ *   k_cache, v_cache, k_scale, v_scale, kind, num_blocks, block_size, num_kv_heads, head_dim,
+ *   block_tables, max_blocks_per_seq, context_lens, num_seqs, stream, and then
+ *   WRITE, READ:  k, v, k_stride, v_stride, query_start, num_tokens, max_query_len
+ *   WRITE_ROPE:   these, q, q_out, q_stride, q_out_stride, num_q_heads, positions, cos_sin,
+ *                 max_position, rotary_dim, neox_style
+ *   DECODE:       out, q, max_context_len, num_q_heads, scale, workspace, workspace_bytes
+ *   PREFILL:      these, num_queries, query_start, max_query_len
+ *   STEP:         DECODE's, k, v, k_stride, v_stride
+ *   STEP_ROPE:    STEP's, q_stride, q_out, positions, cos_sin, max_position, rotary_dim, neox_style
+ */
+enum { PKV_CALL_WRITE_Q8 = 0, PKV_CALL_READ_Q8 = 1, PKV_CALL_WRITE_ROPE_Q8 = 2, PKV_CALL_DECODE_Q8 = 3,
+       PKV_CALL_PREFILL_Q8 = 4, PKV_CALL_STEP_Q8 = 5, PKV_CALL_STEP_ROPE_Q8 = 6 };
+int pkv_call_q8(int32_t call, const int64_t *words);
+
+/*
  * paged_decode_split -- flash-decoding partition kernel (split-K over the keys;
  * the FlashAttention-2 online-softmax algebra that the first page references).
  *

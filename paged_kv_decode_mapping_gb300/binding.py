@@ -53,11 +53,7 @@ class pkv_q8_cache(ctypes.Structure):
 _P = ctypes.c_void_p
 _i32, _i64, _f32, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _D = ctypes.POINTER(pkv_cache_desc)
-# pkv_q8_cache and pkv_cache_desc as packed bytes, for the 8-bit cache's calls (0.3 us less than a
-# ctypes.Structure each)
-_Q8, _Q8D = ctypes.c_void_p, ctypes.c_void_p
-_pack_q8, _pack_desc = struct.Struct("PPPPi4x").pack, struct.Struct("qiii4x").pack
-assert struct.calcsize("PPPPi4x") == ctypes.sizeof(pkv_q8_cache) and struct.calcsize("qiii4x") == ctypes.sizeof(pkv_cache_desc)
+_Q8 = ctypes.POINTER(pkv_q8_cache)
 
 _lib.paged_kv_write.argtypes = [_P, _P, _P, _i64, _P, _P, _D, _P]
 _lib.paged_kv_write.restype = ctypes.c_int
@@ -102,31 +98,33 @@ _lib.paged_prefill_attention.restype = ctypes.c_int
 _lib.prompt_attention.argtypes = [_P, _P, _P, _P, _i64, _i64, _i64, _i64, _P, _i64, _i32, _i32,
                                   _i32, _i32, _i32, _f32, _P]
 _lib.prompt_attention.restype = ctypes.c_int
-_lib.paged_kv_write_q8.argtypes = [_P, _P, _i64, _i64, _P, _i64, _i32, _P, _i32, _P, _i32, _Q8, _Q8D, _P]
+_lib.paged_kv_write_q8.argtypes = [_P, _P, _i64, _i64, _P, _i64, _i32, _P, _i32, _P, _i32, _Q8, _D, _P]
 _lib.paged_kv_write_q8.restype = ctypes.c_int
 _lib.paged_kv_write_rope_q8.argtypes = [_P, _P, _i64, _i64, _P, _P, _i64, _i64, _i32, _P, _P, _i64, _i32,
-                                        _i32, _P, _i64, _i32, _P, _i32, _P, _i32, _Q8, _Q8D, _P]
+                                        _i32, _P, _i64, _i32, _P, _i32, _P, _i32, _Q8, _D, _P]
 _lib.paged_kv_write_rope_q8.restype = ctypes.c_int
-_lib.paged_kv_read_q8.argtypes = [_P, _P, _i64, _i64, _P, _i64, _i32, _P, _i32, _P, _i32, _Q8, _Q8D, _P]
+_lib.paged_kv_read_q8.argtypes = [_P, _P, _i64, _i64, _P, _i64, _i32, _P, _i32, _P, _i32, _Q8, _D, _P]
 _lib.paged_kv_read_q8.restype = ctypes.c_int
 _lib.paged_decode_q8_workspace_size.argtypes = [_i32] * 5
 _lib.paged_decode_q8_workspace_size.restype = _sz
-_lib.paged_decode_attention_q8.argtypes = [_P, _P, _Q8, _P, _i32, _P, _i32, _i32, _i32, _Q8D, _f32, _P, _sz, _P]
+_lib.paged_decode_attention_q8.argtypes = [_P, _P, _Q8, _P, _i32, _P, _i32, _i32, _i32, _D, _f32, _P, _sz, _P]
 _lib.paged_decode_attention_q8.restype = ctypes.c_int
-_lib.paged_decode_step_q8.argtypes = [_P, _P, _P, _P, _i64, _i64, _Q8, _P, _i32, _P, _i32, _i32, _i32, _Q8D,
+_lib.paged_decode_step_q8.argtypes = [_P, _P, _P, _P, _i64, _i64, _Q8, _P, _i32, _P, _i32, _i32, _i32, _D,
                                       _f32, _P, _sz, _P]
 _lib.paged_decode_step_q8.restype = ctypes.c_int
 _lib.paged_decode_step_rope_q8.argtypes = [_P, _P, _i64, _P, _P, _P, _i64, _i64, _P, _P, _i64, _i32, _i32,
-                                           _Q8, _P, _i32, _P, _i32, _i32, _i32, _Q8D, _f32, _P, _sz, _P]
+                                           _Q8, _P, _i32, _P, _i32, _i32, _i32, _D, _f32, _P, _sz, _P]
 _lib.paged_decode_step_rope_q8.restype = ctypes.c_int
 _lib.paged_prefill_q8_workspace_size.argtypes = [_i32] * 4
 _lib.paged_prefill_q8_workspace_size.restype = _sz
-_lib.paged_prefill_attention_q8.argtypes = [_P, _P, _i64, _Q8, _P, _i32, _P, _i32, _P, _i32, _i32, _i32, _Q8D, _f32,
+_lib.paged_prefill_attention_q8.argtypes = [_P, _P, _i64, _Q8, _P, _i32, _P, _i32, _P, _i32, _i32, _i32, _D, _f32,
                                             _P, _sz, _P]
 _lib.paged_prefill_attention_q8.restype = ctypes.c_int
-_lib.paged_kv_copy_blocks_q8.argtypes = [_P, _i32, _P, _P, _i64, _Q8D, _P]
+_lib.pkv_call_q8.argtypes = [_i32, _P]
+_lib.pkv_call_q8.restype = ctypes.c_int
+_lib.paged_kv_copy_blocks_q8.argtypes = [_P, _i32, _P, _P, _i64, _D, _P]
 _lib.paged_kv_copy_blocks_q8.restype = ctypes.c_int
-_lib.paged_kv_compact_q8.argtypes = [_P, _i32, _P, _P, _i64, _P, _i64, _i32, _P, _Q8D, _P]
+_lib.paged_kv_compact_q8.argtypes = [_P, _i32, _P, _P, _i64, _P, _i64, _i32, _P, _D, _P]
 _lib.paged_kv_compact_q8.restype = ctypes.c_int
 _lib.paged_decode_split.argtypes = [_P, _P, _P, _P, _P, _P, _i32, _P, _i32, _i32, _i32, _D, _f32,
                                     _i32, _P]
@@ -183,6 +181,10 @@ def _stream(stream: Optional[torch.cuda.Stream], dev: Optional[int] = None) -> i
         return stream.cuda_stream
     # torch.cuda.current_stream().cuda_stream without the Stream object (0.2 against 2.8 us)
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
+
+
+def _word(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -684,12 +686,18 @@ def _prompt_checks(out, q, k, v) -> None:
 # ---- the 8-bit cache: codes [NB, Hkv, BS, D] int8 or float8_e4m3fn, scales [NB, Hkv] float32
 
 Q8_E4M3, Q8_INT8 = 0, 1
+# pkv_call_q8's words (14 arguments of a call cost ctypes 1.1 us, packed 0.4)
+_CALL_WRITE, _CALL_READ, _CALL_WRITE_ROPE, _CALL_DECODE, _CALL_PREFILL, _CALL_STEP, _CALL_STEP_ROPE = range(7)
+_call_q8 = _lib.pkv_call_q8
+_pack_rows, _pack_rope = struct.Struct("14q7q").pack, struct.Struct("14q7q10q").pack
+_pack_decode, _pack_prefill = struct.Struct("14q4qd2q").pack, struct.Struct("14q4qd2q3q").pack
+_pack_step, _pack_step_rope = struct.Struct("14q4qd2q4q").pack, struct.Struct("14q4qd2q4q7q").pack
 _BF16, _F32, _I32, _I8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.float8_e4m3fn
 
 
 def _q8_cache(dev: int, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start=None):
-    """(pkv_q8_cache, pkv_cache_desc, Hkv, B, M) of tensors on device `dev`, checked in one expression (a
-    call's checks were 9 of its 12 us when each tensor had its own); _q8_wrong names what fails."""
+    """The words of pkv_call_q8 up to num_seqs, of tensors on device `dev`, checked in one expression (a call's
+    checks were 9 of its 12 us when each tensor had its own); _q8_wrong names what fails."""
     kt = k_cache.dtype
     if not (kt is v_cache.dtype and (kt is _I8 or kt is _E4M3) and k_scale.dtype is _F32 and
             v_scale.dtype is _F32 and block_tables.dtype is _I32 and context_lens.dtype is _I32 and
@@ -712,8 +720,8 @@ def _q8_cache(dev: int, k_cache, v_cache, k_scale, v_scale, block_tables, contex
         raise ValueError("block_tables must be [B, M] and context_lens [B]")
     if query_start is not None and query_start.shape != (B + 1,):
         raise ValueError("query_start must be [B + 1] for context_lens [B]")
-    return (_pack_q8(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                     Q8_INT8 if kt is _I8 else Q8_E4M3), _pack_desc(NB, BS, Hkv, D), Hkv, B, bt[1])
+    return (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            Q8_INT8 if kt is _I8 else Q8_E4M3, NB, BS, Hkv, D, block_tables.data_ptr(), bt[1], context_lens.data_ptr(), B)
 
 
 def _q8_wrong(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start) -> None:
@@ -773,10 +781,10 @@ def paged_kv_write_q8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v
     [T, Hkv, D] (the tokens may be strided), quantised into its pages at positions
     context_lens[b] - n .. context_lens[b] - 1.  Without query_start: one token per sequence."""
     dev, T, sk, sv = _q8_rows(k, v, k_cache)
-    c, d, H, B, M = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
-    _check(_lib.paged_kv_write_q8(k.data_ptr(), v.data_ptr(), sk, sv, _ptr(query_start), T, int(max_query_len),
-                                  block_tables.data_ptr(), M, context_lens.data_ptr(), B, c,
-                                  d, _stream(stream, dev)), "paged_kv_write_q8")
+    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
+    _check(_call_q8(_CALL_WRITE, _pack_rows(
+        *cache, _stream(stream, dev), k.data_ptr(), v.data_ptr(), sk, sv, _word(query_start), T, max_query_len)),
+        "paged_kv_write_q8")
 
 
 def paged_kv_write_rope_q8(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor,
@@ -789,7 +797,7 @@ def paged_kv_write_rope_q8(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tens
     """paged_kv_write_q8 of the rotated k; the rotated q goes to q_out (default: q itself).
     positions [T] int64 default to the tokens' positions in their sequences."""
     dev, T, sk, sv = _q8_rows(k, v, k_cache)
-    c, d, H, B, M = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
+    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
     sq = so = heads = 0
     if q is not None:
         q_out = q if q_out is None else q_out
@@ -804,11 +812,10 @@ def paged_kv_write_rope_q8(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tens
     elif q_out is not None:
         raise ValueError("q_out without q")
     r = _rope_table(cos_sin, positions, k.shape[2] if rotary_dim is None else int(rotary_dim), T, dev)
-    _check(_lib.paged_kv_write_rope_q8(k.data_ptr(), v.data_ptr(), sk, sv, _ptr(q), _ptr(q_out), sq, so, heads,
-                                       _ptr(positions), cos_sin.data_ptr(), cos_sin.shape[0], r,
-                                       1 if neox_style else 0, _ptr(query_start), T, int(max_query_len),
-                                       block_tables.data_ptr(), M, context_lens.data_ptr(), B, c,
-                                       d, _stream(stream, dev)), "paged_kv_write_rope_q8")
+    _check(_call_q8(_CALL_WRITE_ROPE, _pack_rope(
+        *cache, _stream(stream, dev), k.data_ptr(), v.data_ptr(), sk, sv, _word(query_start), T, max_query_len,
+        _word(q), _word(q_out), sq, so, heads, _word(positions), cos_sin.data_ptr(), cos_sin.shape[0], r,
+        1 if neox_style else 0)), "paged_kv_write_rope_q8")
 
 
 def _rope_table(cos_sin, positions, r: int, tokens: int, dev: int) -> int:
@@ -833,10 +840,10 @@ def paged_kv_read_q8(k_out: torch.Tensor, v_out: torch.Tensor, k_cache: torch.Te
     """Each sequence's newest query_start[b+1] - query_start[b] tokens back as bf16 rows
     query_start[b] .. of k_out and v_out [T, Hkv, D] (the tokens may be strided)."""
     dev, T, sk, sv = _q8_rows(k_out, v_out, k_cache, ("k_out", "v_out"))
-    c, d, H, B, M = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
-    _check(_lib.paged_kv_read_q8(k_out.data_ptr(), v_out.data_ptr(), sk, sv, _ptr(query_start), T,
-                                 int(max_query_len), block_tables.data_ptr(), M, context_lens.data_ptr(), B,
-                                 c, d, _stream(stream, dev)), "paged_kv_read_q8")
+    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
+    _check(_call_q8(_CALL_READ, _pack_rows(
+        *cache, _stream(stream, dev), k_out.data_ptr(), v_out.data_ptr(), sk, sv, _word(query_start), T, max_query_len)),
+        "paged_kv_read_q8")
 
 
 def paged_decode_q8_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -882,14 +889,13 @@ def paged_decode_attention_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torch
     any sizes in turn; it may be omitted as there."""
     dev = _home(q)
     _q8_query(out, q, k_cache, context_lens.shape[0], dev)
-    c, d, H, B, M = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
     _, Hq, D = q.shape
     workspace = _q8_workspace(workspace, 0 if workspace is not None else paged_decode_q8_workspace_size(
-        B, Hq, H, D, int(max_context_len)), True, q, dev, stream)
-    _check(_lib.paged_decode_attention_q8(
-        out.data_ptr(), q.data_ptr(), c, block_tables.data_ptr(), M,
-        context_lens.data_ptr(), int(max_context_len), B, Hq, d, float(scale), workspace.data_ptr(),
-        workspace.nbytes, _stream(stream, dev)), "paged_decode_attention_q8")
+        cache[12], Hq, cache[7], D, int(max_context_len)), True, q, dev, stream)
+    _check(_call_q8(_CALL_DECODE, _pack_decode(
+        *cache, _stream(stream, dev), out.data_ptr(), q.data_ptr(), max_context_len, Hq, scale, workspace.data_ptr(),
+        workspace.nbytes)), "paged_decode_attention_q8")
 
 
 def paged_decode_step_q8(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -901,17 +907,15 @@ def paged_decode_step_q8(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
     paged_decode_attention_q8 of q [B, Hq, D] (k, v [B, Hkv, D], tokens may be strided)."""
     dev, T, sk, sv = _q8_rows(k, v, k_cache)
     _q8_query(out, q, k_cache, T, dev)
-    c, d, H, B, M = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
     _, Hq, D = q.shape
-    if B != T:
+    if cache[12] != T:
         raise ValueError("q, k and v need one row per sequence")
     workspace = _q8_workspace(workspace, 0 if workspace is not None else paged_decode_q8_workspace_size(
-        B, Hq, H, D, int(max_context_len)), True, q, dev, stream)
-    _check(_lib.paged_decode_step_q8(
-        out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), sk, sv, c, block_tables.data_ptr(),
-        M, context_lens.data_ptr(), int(max_context_len), B, Hq, d, float(scale),
-        workspace.data_ptr(), workspace.nbytes, _stream(stream, dev)),
-        "paged_decode_step_q8")
+        cache[12], Hq, cache[7], D, int(max_context_len)), True, q, dev, stream)
+    _check(_call_q8(_CALL_STEP, _pack_step(
+        *cache, _stream(stream, dev), out.data_ptr(), q.data_ptr(), max_context_len, Hq, scale, workspace.data_ptr(),
+        workspace.nbytes, k.data_ptr(), v.data_ptr(), sk, sv)), "paged_decode_step_q8")
 
 
 def paged_decode_step_rope_q8(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -929,19 +933,17 @@ def paged_decode_step_rope_q8(out: torch.Tensor, q: torch.Tensor, k: torch.Tenso
     if q.shape != q_out.shape:
         raise ValueError("q_out must have q's shape")
     sq = _packed(q, "q", T, k.shape[2], dev)
-    c, d, H, B, M = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
     _, Hq, D = q.shape
-    if B != T:
+    if cache[12] != T:
         raise ValueError("q, k and v need one row per sequence")
     r = _rope_table(cos_sin, positions, D if rotary_dim is None else int(rotary_dim), T, dev)
     workspace = _q8_workspace(workspace, 0 if workspace is not None else paged_decode_q8_workspace_size(
-        B, Hq, H, D, int(max_context_len)), True, q, dev, stream)
-    _check(_lib.paged_decode_step_rope_q8(
-        out.data_ptr(), q.data_ptr(), sq, q_out.data_ptr(), k.data_ptr(), v.data_ptr(), sk, sv, _ptr(positions),
-        cos_sin.data_ptr(), cos_sin.shape[0], r, 1 if neox_style else 0, c, block_tables.data_ptr(),
-        M, context_lens.data_ptr(), int(max_context_len), B, Hq, d, float(scale),
-        workspace.data_ptr(), workspace.nbytes, _stream(stream, dev)),
-        "paged_decode_step_rope_q8")
+        cache[12], Hq, cache[7], D, int(max_context_len)), True, q, dev, stream)
+    _check(_call_q8(_CALL_STEP_ROPE, _pack_step_rope(
+        *cache, _stream(stream, dev), out.data_ptr(), q.data_ptr(), max_context_len, Hq, scale, workspace.data_ptr(),
+        workspace.nbytes, k.data_ptr(), v.data_ptr(), sk, sv, sq, q_out.data_ptr(), _word(positions), cos_sin.data_ptr(),
+        cos_sin.shape[0], r, 1 if neox_style else 0)), "paged_decode_step_rope_q8")
 
 
 def paged_prefill_attention_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -955,13 +957,12 @@ def paged_prefill_attention_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torc
     _q8_query(out, q, k_cache, None, dev)
     if query_start is None:
         raise ValueError("query_start must be [B + 1]")
-    c, d, H, B, M = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
+    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
     workspace = _q8_workspace(workspace, 0 if workspace is not None else paged_prefill_q8_workspace_size(
-        B, H, q.shape[2], k_cache.shape[2], int(max_context_len)), False, q, dev, stream)
-    _check(_lib.paged_prefill_attention_q8(
-        out.data_ptr(), q.data_ptr(), q.shape[0], c, block_tables.data_ptr(), M, context_lens.data_ptr(),
-        int(max_context_len), query_start.data_ptr(), int(max_query_len), B, q.shape[1], d,
-        float(scale), workspace.data_ptr(), workspace.nbytes, _stream(stream, dev)),
+        cache[12], cache[7], cache[8], cache[6], int(max_context_len)), False, q, dev, stream)
+    _check(_call_q8(_CALL_PREFILL, _pack_prefill(
+        *cache, _stream(stream, dev), out.data_ptr(), q.data_ptr(), max_context_len, q.shape[1], scale,
+        workspace.data_ptr(), workspace.nbytes, q.shape[0], query_start.data_ptr(), max_query_len)),
         "paged_prefill_attention_q8")
 
 
@@ -990,9 +991,10 @@ def _q8_layers(dev: int, k_caches, v_caches, k_scales, v_scales, where: str):
     for i, tensors in enumerate(layers):
         if tensors[0].shape != first.shape or tensors[0].dtype != first.dtype:
             raise ValueError(f"{where}: the layers' caches must be alike")
-        c, d, *_ = _q8_cache(dev, *tensors, *none)
-        out[i] = pkv_q8_cache.from_buffer_copy(c)
-    return out, len(layers), d, first
+        words = _q8_cache(dev, *tensors, *none)
+        out[i] = pkv_q8_cache(*words[:5])
+    NB, BS, Hkv, D = words[5:9]
+    return out, len(layers), pkv_cache_desc(NB, BS, Hkv, D), first
 
 
 def paged_kv_copy_blocks_q8(k_caches, v_caches, k_scales, v_scales, block_pairs: torch.Tensor,
@@ -1012,7 +1014,7 @@ def paged_kv_copy_blocks_q8(k_caches, v_caches, k_scales, v_scales, block_pairs:
     if num_tokens is not None and num_tokens.shape != shape[:1]:
         raise ValueError("num_tokens must have one entry per pair")
     _check(_lib.paged_kv_copy_blocks_q8(ctypes.addressof(caches), n, block_pairs.data_ptr(), _ptr(num_tokens),
-                                        shape[0], d, _stream(stream, dev)), "paged_kv_copy_blocks_q8")
+                                        shape[0], ctypes.byref(d), _stream(stream, dev)), "paged_kv_copy_blocks_q8")
 
 
 def paged_kv_compact_q8(k_caches, v_caches, k_scales, v_scales, block_moves: torch.Tensor,
@@ -1039,7 +1041,7 @@ def paged_kv_compact_q8(k_caches, v_caches, k_scales, v_scales, block_moves: tor
             raise ValueError("block_tables need a block_map with one entry per block")
         rows, cols = block_tables.shape
     _check(_lib.paged_kv_compact_q8(ctypes.addressof(caches), n, block_moves.data_ptr(), None, shape[0],
-                                    _ptr(block_tables), rows, cols, _ptr(block_map), d,
+                                    _ptr(block_tables), rows, cols, _ptr(block_map), ctypes.byref(d),
                                     _stream(stream, dev)), "paged_kv_compact_q8")
 
 
