@@ -695,7 +695,7 @@ _pack_step, _pack_step_rope = struct.Struct("14q4qd2q4q").pack, struct.Struct("1
 _BF16, _F32, _I32, _I8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.float8_e4m3fn
 
 
-def _q8_cache(dev: int, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start=None):
+def _q8_cache(dev: int, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start=None, shape=None):
     """The words of pkv_call_q8 up to num_seqs, of tensors on device `dev`, checked in one expression (a call's
     checks were 9 of its 12 us when each tensor had its own); _q8_wrong names what fails."""
     kt = k_cache.dtype
@@ -708,7 +708,9 @@ def _q8_cache(dev: int, k_cache, v_cache, k_scale, v_scale, block_tables, contex
             (query_start is None or (query_start.dtype is _I32 and query_start.get_device() == dev and
                                      query_start.is_contiguous()))):
         _q8_wrong(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
-    shape, (B,) = k_cache.shape, context_lens.shape
+    if shape is None:
+        shape = k_cache.shape
+    B, = context_lens.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [NB, Hkv, BS, D], alike")
     NB, Hkv, BS, D = shape
@@ -758,9 +760,9 @@ def _packed(t: torch.Tensor, name: str, tokens: int, D: int, dev: int) -> int:
     return step if tokens > 1 else shape[1] * D
 
 
-def _q8_rows(k, v, k_cache, names=("k", "v")):
-    """(device, tokens, strides) of k and v [T, Hkv, D]."""
-    shape, cache = k.shape, k_cache.shape
+def _q8_rows(k, v, cache, names=("k", "v")):
+    """(device, tokens, strides) of k and v [T, Hkv, D] for a cache of shape `cache`."""
+    shape = k.shape
     if (len(shape) != 3 or len(cache) != 4 or v.shape != shape or shape[1] != cache[1] or
             shape[2] != cache[3]):
         raise ValueError(f"{names[0]} and {names[1]} must be [T, Hkv, D] for a cache [NB, Hkv, BS, D]")
@@ -780,8 +782,9 @@ def paged_kv_write_q8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v
     """Each sequence's newest tokens, rows query_start[b] .. query_start[b+1]-1 of k and v
     [T, Hkv, D] (the tokens may be strided), quantised into its pages at positions
     context_lens[b] - n .. context_lens[b] - 1.  Without query_start: one token per sequence."""
-    dev, T, sk, sv = _q8_rows(k, v, k_cache)
-    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
+    shape = k_cache.shape
+    dev, T, sk, sv = _q8_rows(k, v, shape)
+    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start, shape)
     _check(_call_q8(_CALL_WRITE, _pack_rows(
         *cache, _stream(stream, dev), k.data_ptr(), v.data_ptr(), sk, sv, _word(query_start), T, max_query_len)),
         "paged_kv_write_q8")
@@ -796,19 +799,20 @@ def paged_kv_write_rope_q8(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tens
                            neox_style: bool = True, stream=None) -> None:
     """paged_kv_write_q8 of the rotated k; the rotated q goes to q_out (default: q itself).
     positions [T] int64 default to the tokens' positions in their sequences."""
-    dev, T, sk, sv = _q8_rows(k, v, k_cache)
-    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
+    shape = k_cache.shape
+    dev, T, sk, sv = _q8_rows(k, v, shape)
+    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start, shape)
     sq = so = heads = 0
     if q is not None:
         q_out = q if q_out is None else q_out
-        shape, D = q.shape, k.shape[2]
-        if len(shape) != 3 or q_out.shape != shape:
+        rows, D = q.shape, shape[3]
+        if len(rows) != 3 or q_out.shape != rows:
             raise ValueError("q must be [T, Hq, D], and q_out alike")
         (sq, h, one), (so, h_out, one_out) = q.stride(), q_out.stride()
         if not (q.dtype is _BF16 and q_out.dtype is _BF16 and q.get_device() == dev == q_out.get_device() and
-                shape[0] == T > 1 and shape[2] == D and one == 1 == one_out and h == D == h_out):
+                rows[0] == T > 1 and rows[2] == D and one == 1 == one_out and h == D == h_out):
             sq, so = _packed(q, "q", T, D, dev), _packed(q_out, "q_out", T, D, dev)
-        heads = shape[1]
+        heads = rows[1]
     elif q_out is not None:
         raise ValueError("q_out without q")
     r = _rope_table(cos_sin, positions, k.shape[2] if rotary_dim is None else int(rotary_dim), T, dev)
@@ -839,8 +843,9 @@ def paged_kv_read_q8(k_out: torch.Tensor, v_out: torch.Tensor, k_cache: torch.Te
                      max_query_len: int = 1, stream=None) -> None:
     """Each sequence's newest query_start[b+1] - query_start[b] tokens back as bf16 rows
     query_start[b] .. of k_out and v_out [T, Hkv, D] (the tokens may be strided)."""
-    dev, T, sk, sv = _q8_rows(k_out, v_out, k_cache, ("k_out", "v_out"))
-    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
+    shape = k_cache.shape
+    dev, T, sk, sv = _q8_rows(k_out, v_out, shape, ("k_out", "v_out"))
+    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start, shape)
     _check(_call_q8(_CALL_READ, _pack_rows(
         *cache, _stream(stream, dev), k_out.data_ptr(), v_out.data_ptr(), sk, sv, _word(query_start), T, max_query_len)),
         "paged_kv_read_q8")
@@ -857,13 +862,13 @@ def paged_prefill_q8_workspace_size(num_seqs: int, num_kv_heads: int, head_dim: 
     return int(_lib.paged_prefill_q8_workspace_size(num_seqs, num_kv_heads, head_dim, max_context_len))
 
 
-def _q8_query(out, q, k_cache, rows: Optional[int], dev: int) -> None:
+def _q8_query(out, q, cache, rows: Optional[int], dev: int) -> None:
     if not (q.dtype is _BF16 and out.dtype is _BF16 and q.get_device() == dev == out.get_device() and
             q.is_contiguous() and out.is_contiguous()):
         _need(q, "q", torch.bfloat16, 3)
         _need(out, "out", torch.bfloat16, 3)
         _one_device(q, out=out)
-    shape, cache = q.shape, k_cache.shape
+    shape = q.shape
     if len(shape) != 3 or len(cache) != 4 or shape[2] != cache[3] or (rows is not None and shape[0] != rows):
         raise ValueError("q must be [rows, Hq, D] for a cache [NB, Hkv, BS, D]")
     if out.shape != shape:
@@ -888,8 +893,9 @@ def paged_decode_attention_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torch
     ``paged_decode_q8_workspace_size`` bytes, zero-filled before its first use) serves calls of
     any sizes in turn; it may be omitted as there."""
     dev = _home(q)
-    _q8_query(out, q, k_cache, context_lens.shape[0], dev)
-    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    shape = k_cache.shape
+    _q8_query(out, q, shape, context_lens.shape[0], dev)
+    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, None, shape)
     _, Hq, D = q.shape
     workspace = _q8_workspace(workspace, 0 if workspace is not None else paged_decode_q8_workspace_size(
         cache[12], Hq, cache[7], D, int(max_context_len)), True, q, dev, stream)
@@ -905,9 +911,10 @@ def paged_decode_step_q8(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
                          stream=None) -> None:
     """One decode step over an 8-bit cache: paged_kv_write_q8 of one token per sequence, then
     paged_decode_attention_q8 of q [B, Hq, D] (k, v [B, Hkv, D], tokens may be strided)."""
-    dev, T, sk, sv = _q8_rows(k, v, k_cache)
-    _q8_query(out, q, k_cache, T, dev)
-    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    shape = k_cache.shape
+    dev, T, sk, sv = _q8_rows(k, v, shape)
+    _q8_query(out, q, shape, T, dev)
+    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, None, shape)
     _, Hq, D = q.shape
     if cache[12] != T:
         raise ValueError("q, k and v need one row per sequence")
@@ -927,13 +934,14 @@ def paged_decode_step_rope_q8(out: torch.Tensor, q: torch.Tensor, k: torch.Tenso
                               workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """paged_decode_step_q8 with RoPE: q [B, Hq, D] (tokens may be strided) is rotated into the
     contiguous q_out (default: q itself), k on its way into the cache."""
-    dev, T, sk, sv = _q8_rows(k, v, k_cache)
+    shape = k_cache.shape
+    dev, T, sk, sv = _q8_rows(k, v, shape)
     q_out = q if q_out is None else q_out
-    _q8_query(out, q_out, k_cache, T, dev)
+    _q8_query(out, q_out, shape, T, dev)
     if q.shape != q_out.shape:
         raise ValueError("q_out must have q's shape")
     sq = _packed(q, "q", T, k.shape[2], dev)
-    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, None, shape)
     _, Hq, D = q.shape
     if cache[12] != T:
         raise ValueError("q, k and v need one row per sequence")
@@ -954,10 +962,11 @@ def paged_prefill_attention_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torc
     """paged_prefill_attention over an 8-bit cache.  ``workspace``: uint8, CUDA,
     ``paged_prefill_q8_workspace_size`` bytes with any contents; it may be omitted."""
     dev = _home(q)
-    _q8_query(out, q, k_cache, None, dev)
+    shape = k_cache.shape
+    _q8_query(out, q, shape, None, dev)
     if query_start is None:
         raise ValueError("query_start must be [B + 1]")
-    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start)
+    cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start, shape)
     workspace = _q8_workspace(workspace, 0 if workspace is not None else paged_prefill_q8_workspace_size(
         cache[12], cache[7], cache[8], cache[6], int(max_context_len)), False, q, dev, stream)
     _check(_call_q8(_CALL_PREFILL, _pack_prefill(
