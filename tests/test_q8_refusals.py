@@ -1,6 +1,7 @@
 """The 8-bit cache's entry points refuse bad arguments on the host, before any launch."""
 
 import ctypes
+import struct
 
 import pytest
 import torch
@@ -164,3 +165,27 @@ def test_the_binding_names_what_is_wrong_with_copies(B):
         B.paged_kv_copy_blocks_q8(codes, [codes], [scale], [scale], pairs)
     with pytest.raises(TypeError, match="int8"):
         B.paged_kv_compact_q8(codes.float(), codes, scale, scale, pairs)
+
+
+def test_packed_calls(B):
+    """pkv_call_q8 refuses what its calls refuse, and counts that do not fit their types."""
+    lead = dict(k=1 << 20, v=1 << 20, ks=1 << 20, vs=1 << 20, kind=1, nb=64, bs=16, hkv=2, d=64, bt=1 << 20, m=8, cl=1 << 20,
+                b=2, stream=0)
+
+    def call(what, fmt, *rest, **changed):
+        words = struct.pack("14q" + fmt, *dict(lead, **changed).values(), *rest)
+        return B.lib().pkv_call_q8(what, words)
+
+    rows = (1 << 20, 1 << 20, 128, 128, 1 << 20, 8, 4)
+    decode = (1 << 20, 1 << 20, 100, 8, 0.125, 0, 0)
+    assert B.lib().pkv_call_q8(0, None) == -1 and call(7, "7q", *rows) == -3 and call(-1, "7q", *rows) == -3
+    for what in (0, 1):
+        assert call(what, "7q", *rows, k=0) == -1 and call(what, "7q", *rows, d=96) == -3 and call(what, "7q", *rows, kind=5) == -3
+        assert call(what, "7q", *rows, k=(1 << 20) + 4) == -5 and call(what, "7q", *rows, m=0) == -2
+        assert call(what, "7q", *rows[:6], 1 << 40) == -2 and call(what, "7q", *rows, b=1 << 33) == -2
+        assert call(what, "7q", *rows[:5], 0, 4) == 0
+    assert call(3, "4qd2q", *decode) == -4 and call(3, "4qd2q", *decode, b=0) == 0
+    assert call(3, "4qd2q", *decode[:3], 9, *decode[4:]) == -2
+    assert call(4, "4qd2q3q", *decode, 8, 1 << 20, 4) == -4 and call(4, "4qd2q3q", *decode, 0, 1 << 20, 4) == 0
+    assert call(5, "4qd2q4q", *decode, 1 << 20, 1 << 20, 128, 128) == -4
+    assert call(6, "4qd2q4q7q", *decode, 1 << 20, 1 << 20, 128, 128, 512, 1 << 20, 0, 1 << 20, 100, 8, 1) == -3
