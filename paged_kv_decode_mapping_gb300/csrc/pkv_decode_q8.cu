@@ -368,10 +368,11 @@ __device__ __forceinline__ void q8_tiles(Q8Acc<D> (&a)[NT], Q8Ref &ref, uint32_t
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (8 * i >= nvalid) vs[i] = 0.f;  // its box may not have been loaded
-      if (!MASK && key(i) >= nvalid) {  // scores of -inf; by a factor of 0 or NaN they would be NaN
-#pragma unroll
-        for (int n = 0; n < NT; ++n) s[n][i >> 1][2 * (i & 1)] = s[n][i >> 1][2 * (i & 1) + 1] = -INFINITY;
-        ks[i] = f0[i] = f1[i] = 1.f;
+      // Scores of -inf, by a factor of their own: by 0, NaN or one below 0 they would be something else.
+      // (With two tiles, whose rows' factors come later, the scaled scores are masked.)
+      if (!MASK && NT == 1 && key(i) >= nvalid) {
+        s[0][i >> 1][2 * (i & 1)] = s[0][i >> 1][2 * (i & 1) + 1] = -INFINITY;
+        f0[i] = f1[i] = 1.f;
       }
     }
   }
@@ -404,7 +405,7 @@ __device__ __forceinline__ void q8_tiles(Q8Acc<D> (&a)[NT], Q8Ref &ref, uint32_t
         x[i >> 1][2 * (i & 1)] = fmaf(s[n][i >> 1][2 * (i & 1)], f0[i], sh0);
         x[i >> 1][2 * (i & 1) + 1] = fmaf(s[n][i >> 1][2 * (i & 1) + 1], f1[i], sh1);
       }
-      if (MASK) {
+      if (MASK || (NT > 1 && nvalid < 32)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (unseen(i, c.i0)) x[i >> 1][2 * (i & 1)] = -INFINITY;
