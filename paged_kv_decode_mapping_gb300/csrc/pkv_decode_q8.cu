@@ -92,10 +92,10 @@ template <int D, int NT>
 constexpr size_t q8_smem() { return 1024 + Q8Smem<D, NT>::total; }
 static_assert(q8_smem<64, 2>() <= 227 * 1024 && q8_smem<128, 2>() <= 227 * 1024, "the groups fit an SM");
 // A share's result in its last stage: per warp and head a row of D floats (4 apart, so that the
-// lanes' stores lie in different banks), then the references and the sums.
+// lanes' stores lie in different banks), then the references, the sums and the warps' units of V.
 __host__ __device__ constexpr int q8_row(int d) { return d + 4; }
-static_assert(kConsumerWarps * kRowTile * (q8_row(128) + 2) * 4 <= (int)Q8Smem<128, 1>::kStage &&
-                  kConsumerWarps * kRowTile * (q8_row(64) + 2) * 4 <= (int)Q8Smem<64, 1>::kStage,
+static_assert(kConsumerWarps * (kRowTile * (q8_row(128) + 2) + 1) * 4 <= (int)Q8Smem<128, 1>::kStage &&
+                  kConsumerWarps * (kRowTile * (q8_row(64) + 2) + 1) * 4 <= (int)Q8Smem<64, 1>::kStage,
               "the warps' results of a tile of rows fit a stage");
 
 struct Q8Args {
@@ -498,7 +498,8 @@ __device__ __forceinline__ void q8_tiles(Q8Acc<D> (&a)[NT], Q8Ref &ref, uint32_t
   }
 }
 
-// Reduces l over the warp and writes the warp's (m, l, O) of a tile's first n rows.
+// Reduces l over the warp and writes the warp's (m, l, O) of a tile's first n rows, O in units of vref
+// (times it, sums of weights of 2^kTop and more would leave fp32 where V is near the end of bf16).
 template <int D>
 __device__ __forceinline__ void q8_stash(const Q8Acc<D> &a, float vref, const MergeArea &r, int n, int warp, int lane) {
   const int gid = lane >> 2, tig = lane & 3;
@@ -515,12 +516,13 @@ __device__ __forceinline__ void q8_stash(const Q8Acc<D> &a, float vref, const Me
     r.l[warp * kRowTile + h0] = l0;
     r.l[warp * kRowTile + h1] = l1;
   }
+  if (lane == 0) r.l[kConsumerWarps * kRowTile + warp] = vref;
 #pragma unroll
   for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int h = h0 + (k & 1);
-      if (h < n) r.o[(warp * n + h) * q8_row(D) + 16 * mt + gid + 8 * (k >> 1)] = a.o[mt][k] * vref;
+      if (h < n) r.o[(warp * n + h) * q8_row(D) + 16 * mt + gid + 8 * (k >> 1)] = a.o[mt][k];
     }
 }
 
@@ -528,24 +530,29 @@ __device__ __forceinline__ void q8_stash(const Q8Acc<D> &a, float vref, const Me
 // log-sum (of weights 2^kTop at the reference, in every partial alike).
 template <int D>
 __device__ __forceinline__ float4 q8_joined(const MergeArea &r, int n, int h, int d, float *lse) {
-  float m[kConsumerWarps], M = -INFINITY;
+  float m[kConsumerWarps], M = -INFINITY, unit = 0.f;
 #pragma unroll
-  for (int w = 0; w < kConsumerWarps; ++w) M = fmaxf(M, m[w] = r.m[w * kRowTile + h]);
+  for (int w = 0; w < kConsumerWarps; ++w) {
+    M = fmaxf(M, m[w] = r.m[w * kRowTile + h]);
+    unit = fmaxf(unit, r.l[kConsumerWarps * kRowTile + w]);
+  }
+  const float per_unit = unit > 0.f ? 1.f / unit : 0.f;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
   float den = 0.f;
 #pragma unroll
   for (int w = 0; w < kConsumerWarps; ++w) {
     const float wt = dev::ex2(m[w] - softmax_ref(M));
     const float4 o = *reinterpret_cast<const float4 *>(r.o + (w * n + h) * q8_row(D) + d);
-    x.x += wt * o.x;
-    x.y += wt * o.y;
-    x.z += wt * o.z;
-    x.w += wt * o.w;
+    const float wo = wt * (r.l[kConsumerWarps * kRowTile + w] * per_unit);
+    x.x += wo * o.x;
+    x.y += wo * o.y;
+    x.z += wo * o.z;
+    x.w += wo * o.w;
     den += wt * r.l[w * kRowTile + h];
   }
   *lse = M + log2f(den);
   const float inv = den == 0.f ? 1.f : 1.f / den;
-  return make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+  return make_float4(x.x * inv * unit, x.y * inv * unit, x.z * inv * unit, x.w * inv * unit);
 }
 
 __device__ __forceinline__ void store4(uint16_t *dst, const float4 &x) {
@@ -557,6 +564,7 @@ __device__ __forceinline__ void store4(uint16_t *dst, const float4 &x) {
 // tokens, one kv head of 8 x 128) read 16 rows after one another for 26 us; 17 shares in two steps
 // took 1.5 us more.
 constexpr int kOneJoin = 32, kRunParts = 16;
+constexpr float kShareUnit = 1.f / kQ8MaxShares;
 
 // Where part p of a context cut from share0 on has its row.
 __device__ __forceinline__ int64_t q8_row_of(const Q8Args &a, int share0, int p, int h) {
@@ -565,7 +573,7 @@ __device__ __forceinline__ int64_t q8_row_of(const Q8Args &a, int share0, int p,
 
 // Four dims of row h from the rows of parts p0, p0 + step, .. (n of them), in that order: those of
 // `sub`, sub + every, ... are this lane's, the others its neighbours'.  The normalised result and its
-// base-2 log-sum.
+// base-2 log-sum.  Rows are summed 2^-10 times: of up to 2^10 shares, each as large as bf16 goes.
 template <int D>
 __device__ __forceinline__ float4 q8_merge(const Q8Args &a, int share0, int p0, int step, int n, int h, int d,
                                            int sub, int every, float *lse) {
@@ -596,12 +604,12 @@ __device__ __forceinline__ float4 q8_merge(const Q8Args &a, int share0, int p0, 
     x.w *= sc;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const float wt = dev::ex2(lk[u] - ref);
+      const float wt = dev::ex2(lk[u] - ref), wo = wt * kShareUnit;
       den += wt;
-      x.x += wt * o[u].x;
-      x.y += wt * o[u].y;
-      x.z += wt * o[u].z;
-      x.w += wt * o[u].w;
+      x.x += wo * o[u].x;
+      x.y += wo * o[u].y;
+      x.z += wo * o[u].z;
+      x.w += wo * o[u].w;
     }
     M = Mn;
   }
@@ -617,7 +625,8 @@ __device__ __forceinline__ float4 q8_merge(const Q8Args &a, int share0, int p0, 
   }
   *lse = M + log2f(den);
   const float inv = den == 0.f ? 1.f : 1.f / den;
-  return make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+  constexpr float up = 1.f / kShareUnit;
+  return make_float4(x.x * inv * up, x.y * inv * up, x.z * inv * up, x.w * inv * up);
 }
 
 // A barrier of one group's consumer warps.

@@ -1,7 +1,10 @@
 """The 8-bit cache's attention at the ends of its ranges.
 
-Tolerances as in test_q8_attention.py: 2^-8 |out| + 2^-10 sum p |v|, and n 2^-35 of the largest |v|.
+Tolerances as in test_q8_attention.py: 2^-8 |out| + 2^-10 sum p |v|, and n 2^-35 of the largest |v|;
+where a chunk may go either way, or its queries are aimed at single keys, chunk_ref's.
 """
+
+import math
 
 import pytest
 import torch
@@ -67,4 +70,76 @@ def test_few_queries_of_any_scale(B, dtype, d, lens, new, hq, hkv):
         check(decode(B, b, q[:len(lens)], scale), *decode_ref(b, q[:len(lens)], scale), f"decode, scale {scale}")
     q = torch.zeros_like(q)
     check(prefill(B, b, q, new, 1e-30), *prefill_ref(b, q, new, 1e-30), "queries of zeros")
+    assert B.pkv_device_errors() == 0
+
+
+def chunk_ref(b, q, new, scale, codes=False):
+    """Output and bound of chunks.  Scores off by up to e_t move the output by at most sum p (exp(e) - 1)
+    |v - out| / sum p exp(-e).
+
+    Through fp16 rows, K's and V's codes and the weights are each off by 2^-11 of themselves at most, K and V
+    by 2^-25 of their unit (the head's largest scale) where that is more, a weight by 2^-25 of 2^-7 of the
+    largest; the scores' fp32 sums are an eighth of K's rounding.  Over the codes as they are, scores are D / 16
+    fp32 sums and a few roundings, each of 2^-23 of sum |q| |k|, |k| being up to 255 scales in int8 (codes are
+    taken as c + 128), and weights off by 2^-11 of themselves or by 2^-35 of the largest."""
+    out, bound = (torch.zeros(q.shape, dtype=torch.float64, device=DEV) for _ in range(2))
+    at, g = 0, q.shape[1] // b.hkv
+    for s, (m, n) in enumerate(zip(b.lens, new)):
+        if m and n:
+            pages = b.tables[s][:-(-m // b.bs)]
+            ku, vu = (x[pages].nan_to_num().amax(0).double() for x in (b.ks, b.vs))
+            k, v = (R.values(c, sc, b.tables[s], 0, m, torch.float64) for c, sc in ((b.k, b.ks), (b.v, b.vs)))
+            for lo in range(0, n, 64):
+                rows = slice(at + lo, at + min(n, lo + 64))
+                own = torch.arange(m - n + lo, m - n + min(n, lo + 64), device=DEV)
+                unseen = torch.arange(m, device=DEV)[None, :] > own[:, None]
+                for h in range(q.shape[1]):
+                    x, kk, vv = q[rows, h].double(), k[:, h // g], v[:, h // g]
+                    p = torch.softmax((x @ kk.T * scale).masked_fill(unseen, -math.inf), -1)
+                    o, mag, large = p @ vv, p @ vv.abs(), x.abs().sum(1, keepdim=True)
+                    if codes:
+                        of = large * 255 * ku[h // g] if b.dtype is torch.int8 else x.abs() @ kk.abs().T
+                        e, weights, least = (b.d // 16 + 4) * 2.0 ** -23 * of, 5 * 2.0 ** -13, m * 2.0 ** -35 * R.TOP[b.dtype]
+                    else:
+                        e = 9 * 2.0 ** -14 * (x.abs() @ kk.abs().T) + 2.0 ** -25 * ku[h // g] * large
+                        weights, least = 5 * 2.0 ** -12, m * 2.0 ** -32 * R.TOP[b.dtype] + 2.0 ** -25
+                    e = (e * abs(scale)).expand_as(p)
+                    apart = (vv[None] - o[:, None]).abs_()
+                    moved = torch.bmm((p * torch.expm1(e))[:, None], apart)[:, 0] / (p * torch.exp(-e)).sum(1, keepdim=True)
+                    out[rows, h] = o
+                    bound[rows, h] = 2.0 ** -8 * o.abs() + weights * mag + moved + least * vu[h // g]
+        at += n
+    return out, bound
+
+
+def check_chunk(got, want, bound, what=""):
+    bad = ~((got.double() - want).abs() <= bound)
+    assert not bool(bad.any()), f"{what}: {int(bad.sum())} of {bad.numel()} off, worst {float((got.double() - want).abs().max()):.3e}"
+
+
+# The same values times a power of two.
+RANGE = [([1], 2, 1), ([300, 129, 0, 17], 4, 2), ([20000, 31], 8, 1), ([100] * 40, 3, 3)]
+
+
+@pytest.mark.parametrize("dtype", R.KINDS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,hq,hkv", RANGE)
+def test_values_near_the_ends_of_the_range(B, dtype, d, lens, hq, hkv):
+    """V up to 1.7e38 and down to where the output is hardly a normal number, and pages of all the largest
+    value that bf16 has: decode, drafts, chunks."""
+    b = Batch(lens, dtype, hkv, d, 16, seed=81)
+    q, scale = b.randn(len(lens), hq, d), 2 * d ** -0.5
+    few, many = [min(n, 3) for n in lens], [min(n, 70) for n in lens]
+    q3, q70 = b.randn(sum(few), hq, d), b.randn(sum(many), hq, d)
+    plain = b.vs.clone()
+    for e in (125, 118, -110):
+        b.vs.copy_(plain * 2.0 ** e)
+        check(decode(B, b, q, scale), *decode_ref(b, q, scale), f"decode, 2^{e}")
+        check(prefill(B, b, q3, few, scale), *prefill_ref(b, q3, few, scale), f"drafts, 2^{e}")
+        check_chunk(prefill(B, b, q70, many, scale), *chunk_ref(b, q70, many, scale), f"chunk, 2^{e}")
+    largest = torch.finfo(torch.bfloat16).max
+    R.bits(b.v)[:] = R.bits(torch.full((1,), R.TOP[dtype], device=DEV).to(dtype))[0]
+    b.vs.fill_(largest / R.TOP[dtype])
+    for out in (decode(B, b, q, scale)[b.cl > 0], prefill(B, b, q3, few, scale), prefill(B, b, q70, many, scale)):
+        assert bool((out.double() >= largest * (1 - 2.0 ** -7)).all()) and bool(out.isfinite().all())
     assert B.pkv_device_errors() == 0
