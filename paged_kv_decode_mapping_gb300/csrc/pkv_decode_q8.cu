@@ -92,10 +92,10 @@ template <int D, int NT>
 constexpr size_t q8_smem() { return 1024 + Q8Smem<D, NT>::total; }
 static_assert(q8_smem<64, 2>() <= 227 * 1024 && q8_smem<128, 2>() <= 227 * 1024, "the groups fit an SM");
 // A share's result in its last stage: per warp and head a row of D floats (4 apart, so that the
-// lanes' stores lie in different banks), then the references, the sums and the warps' units of V.
+// lanes' stores lie in different banks), then the references and the sums.
 __host__ __device__ constexpr int q8_row(int d) { return d + 4; }
-static_assert(kConsumerWarps * (kRowTile * (q8_row(128) + 2) + 1) * 4 <= (int)Q8Smem<128, 1>::kStage &&
-                  kConsumerWarps * (kRowTile * (q8_row(64) + 2) + 1) * 4 <= (int)Q8Smem<64, 1>::kStage,
+static_assert(kConsumerWarps * kRowTile * (q8_row(128) + 2) * 4 <= (int)Q8Smem<128, 1>::kStage &&
+                  kConsumerWarps * kRowTile * (q8_row(64) + 2) * 4 <= (int)Q8Smem<64, 1>::kStage,
               "the warps' results of a tile of rows fit a stage");
 
 struct Q8Args {
@@ -498,8 +498,10 @@ __device__ __forceinline__ void q8_tiles(Q8Acc<D> (&a)[NT], Q8Ref &ref, uint32_t
   }
 }
 
-// Reduces l over the warp and writes the warp's (m, l, O) of a tile's first n rows, O in units of vref
-// (times it, sums of weights of 2^kTop and more would leave fp32 where V is near the end of bf16).
+// Reduces l over the warp and writes the warp's (m, l, O) of a tile's first n rows.  Where V is large, l and O
+// are written 2^kDown times, the references kDown higher: of weights up to 2^(kTop + kSlack), sums of up to
+// 2^(kDown - kTop - kSlack) keys are then no larger than V itself.  (Where it is small, O might become too small.)
+constexpr float kDown = 40.f;
 template <int D>
 __device__ __forceinline__ void q8_stash(const Q8Acc<D> &a, float vref, const MergeArea &r, int n, int warp, int lane) {
   const int gid = lane >> 2, tig = lane & 3;
@@ -510,19 +512,19 @@ __device__ __forceinline__ void q8_stash(const Q8Acc<D> &a, float vref, const Me
     l1 += __shfl_xor_sync(0xffffffffu, l1, x);
   }
   const int h0 = 2 * tig, h1 = h0 + 1;
+  const float higher = vref > 1.f ? kDown : 0.f, down = vref > 1.f ? dev::ex2(-kDown) : 1.f, unit = vref * down;
   if (gid == 0) {
-    r.m[warp * kRowTile + h0] = a.m0;
-    r.m[warp * kRowTile + h1] = a.m1;
-    r.l[warp * kRowTile + h0] = l0;
-    r.l[warp * kRowTile + h1] = l1;
+    r.m[warp * kRowTile + h0] = a.m0 + higher;
+    r.m[warp * kRowTile + h1] = a.m1 + higher;
+    r.l[warp * kRowTile + h0] = l0 * down;
+    r.l[warp * kRowTile + h1] = l1 * down;
   }
-  if (lane == 0) r.l[kConsumerWarps * kRowTile + warp] = vref;
 #pragma unroll
   for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int h = h0 + (k & 1);
-      if (h < n) r.o[(warp * n + h) * q8_row(D) + 16 * mt + gid + 8 * (k >> 1)] = a.o[mt][k];
+      if (h < n) r.o[(warp * n + h) * q8_row(D) + 16 * mt + gid + 8 * (k >> 1)] = a.o[mt][k] * unit;
     }
 }
 
@@ -530,31 +532,27 @@ __device__ __forceinline__ void q8_stash(const Q8Acc<D> &a, float vref, const Me
 // log-sum (of weights 2^kTop at the reference, in every partial alike).
 template <int D>
 __device__ __forceinline__ float4 q8_joined(const MergeArea &r, int n, int h, int d, float *lse) {
-  float m[kConsumerWarps], M = -INFINITY, unit = 0.f;
+  float m[kConsumerWarps], M = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < kConsumerWarps; ++w) {
-    M = fmaxf(M, m[w] = r.m[w * kRowTile + h]);
-    unit = fmaxf(unit, r.l[kConsumerWarps * kRowTile + w]);
-  }
-  const float per_unit = unit > 0.f ? 1.f / unit : 0.f;
+  for (int w = 0; w < kConsumerWarps; ++w) M = fmaxf(M, m[w] = r.m[w * kRowTile + h]);
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
   float den = 0.f;
 #pragma unroll
   for (int w = 0; w < kConsumerWarps; ++w) {
     const float wt = dev::ex2(m[w] - softmax_ref(M));
     const float4 o = *reinterpret_cast<const float4 *>(r.o + (w * n + h) * q8_row(D) + d);
-    const float wo = wt * (r.l[kConsumerWarps * kRowTile + w] * per_unit);
-    x.x += wo * o.x;
-    x.y += wo * o.y;
-    x.z += wo * o.z;
-    x.w += wo * o.w;
+    x.x += wt * o.x;
+    x.y += wt * o.y;
+    x.z += wt * o.z;
+    x.w += wt * o.w;
     den += wt * r.l[w * kRowTile + h];
   }
   *lse = M + log2f(den);
   const float inv = den == 0.f ? 1.f : 1.f / den;
-  return make_float4(x.x * inv * unit, x.y * inv * unit, x.z * inv * unit, x.w * inv * unit);
+  return make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
 }
 
+__device__ __forceinline__ float4 times(const float4 &x, float f) { return make_float4(x.x * f, x.y * f, x.z * f, x.w * f); }
 __device__ __forceinline__ void store4(uint16_t *dst, const float4 &x) {
   *reinterpret_cast<uint2 *>(dst) = make_uint2(dev::pack_bf16x2(x.x, x.y), dev::pack_bf16x2(x.z, x.w));
 }
@@ -564,6 +562,7 @@ __device__ __forceinline__ void store4(uint16_t *dst, const float4 &x) {
 // tokens, one kv head of 8 x 128) read 16 rows after one another for 26 us; 17 shares in two steps
 // took 1.5 us more.
 constexpr int kOneJoin = 32, kRunParts = 16;
+// Shares' rows are kept this many times their values: of so many, each as large as bf16 goes, the sum stays one.
 constexpr float kShareUnit = 1.f / kQ8MaxShares;
 
 // Where part p of a context cut from share0 on has its row.
@@ -573,7 +572,7 @@ __device__ __forceinline__ int64_t q8_row_of(const Q8Args &a, int share0, int p,
 
 // Four dims of row h from the rows of parts p0, p0 + step, .. (n of them), in that order: those of
 // `sub`, sub + every, ... are this lane's, the others its neighbours'.  The normalised result and its
-// base-2 log-sum.  Rows are summed 2^-10 times: of up to 2^10 shares, each as large as bf16 goes.
+// base-2 log-sum.
 template <int D>
 __device__ __forceinline__ float4 q8_merge(const Q8Args &a, int share0, int p0, int step, int n, int h, int d,
                                            int sub, int every, float *lse) {
@@ -604,12 +603,12 @@ __device__ __forceinline__ float4 q8_merge(const Q8Args &a, int share0, int p0, 
     x.w *= sc;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const float wt = dev::ex2(lk[u] - ref), wo = wt * kShareUnit;
+      const float wt = dev::ex2(lk[u] - ref);
       den += wt;
-      x.x += wo * o[u].x;
-      x.y += wo * o[u].y;
-      x.z += wo * o[u].z;
-      x.w += wo * o[u].w;
+      x.x += wt * o[u].x;
+      x.y += wt * o[u].y;
+      x.z += wt * o[u].z;
+      x.w += wt * o[u].w;
     }
     M = Mn;
   }
@@ -625,8 +624,7 @@ __device__ __forceinline__ float4 q8_merge(const Q8Args &a, int share0, int p0, 
   }
   *lse = M + log2f(den);
   const float inv = den == 0.f ? 1.f : 1.f / den;
-  constexpr float up = 1.f / kShareUnit;
-  return make_float4(x.x * inv * up, x.y * inv * up, x.z * inv * up, x.w * inv * up);
+  return make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
 }
 
 // A barrier of one group's consumer warps.
@@ -664,7 +662,7 @@ __device__ __forceinline__ void q8_finish(const Q8Args &a, const Q8Acc<D> (&acc)
         store4(out_of(at) + c, x);
       } else {
         const int64_t row = (int64_t)d.slot * a.rows + at;
-        *reinterpret_cast<float4 *>(a.o_part + row * D + c) = x;
+        *reinterpret_cast<float4 *>(a.o_part + row * D + c) = times(x, kShareUnit);
         if (c == 0) a.lse_part[row] = lse;
       }
     }
@@ -692,7 +690,7 @@ __device__ __forceinline__ void q8_finish(const Q8Args &a, const Q8Acc<D> (&acc)
       float lse;
       const float4 x = q8_merge<D>(a, d.share0, p0, step, n, h, c, sub, every, &lse);
       if (out) {
-        if (sub == 0) store4(out_of(h) + c, x);
+        if (sub == 0) store4(out_of(h) + c, times(x, 1.f / kShareUnit));
       } else {  // every other row of the run has been read when the barrier lets this one be
         group_bar(grp);
         const int64_t row = q8_row_of(a, d.share0, p0, h);
