@@ -336,7 +336,8 @@ __device__ __forceinline__ void q8_scores(const Q8Acc<D> (&a)[NT], float (&s)[NT
 }
 
 // Scores, softmax and weighted sum of the warp's 32 keys (the first nvalid of them in range; of these,
-// with MASK, query i sees the first seen + i) of a stage at sb, the boxes' scales (K's, V's) at sc.
+// with MASK, query i sees the first seen + i) of a stage at sb, the boxes' scales (K's, V's) at sc.  Two tiles
+// take keys that are not all in range with MASK: their rows' factors come after the scores.
 template <int D, int KIND, int NT, bool MASK>
 __device__ __forceinline__ void q8_tiles(Q8Acc<D> (&a)[NT], Q8Ref &ref, uint32_t sb, const Q8Lane &at, const float2 *sc,
                                          int log2_box, int warp, int lane, int nvalid, int seen) {
@@ -364,13 +365,12 @@ __device__ __forceinline__ void q8_tiles(Q8Acc<D> (&a)[NT], Q8Ref &ref, uint32_t
     }
   }
   auto key = [&](int i) { return 16 * (i >> 1) + key_of(gid + 8 * (i & 1)); };  // of the lane, in each 8 keys
-  if (nvalid < 32) {
+  if ((NT == 1 || MASK) && nvalid < 32) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (8 * i >= nvalid) vs[i] = 0.f;  // its box may not have been loaded
       // Scores of -inf, by a factor of their own: by 0, NaN or one below 0 they would be something else.
-      // (With two tiles, whose rows' factors come later, the scaled scores are masked.)
-      if (!MASK && NT == 1 && key(i) >= nvalid) {
+      if (!MASK && key(i) >= nvalid) {
         s[0][i >> 1][2 * (i & 1)] = s[0][i >> 1][2 * (i & 1) + 1] = -INFINITY;
         f0[i] = f1[i] = 1.f;
       }
@@ -405,7 +405,7 @@ __device__ __forceinline__ void q8_tiles(Q8Acc<D> (&a)[NT], Q8Ref &ref, uint32_t
         x[i >> 1][2 * (i & 1)] = fmaf(s[n][i >> 1][2 * (i & 1)], f0[i], sh0);
         x[i >> 1][2 * (i & 1) + 1] = fmaf(s[n][i >> 1][2 * (i & 1) + 1], f1[i], sh1);
       }
-      if (MASK || (NT > 1 && nvalid < 32)) {
+      if (MASK) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (unseen(i, c.i0)) x[i >> 1][2 * (i & 1)] = -INFINITY;
@@ -463,7 +463,7 @@ __device__ __forceinline__ void q8_tiles(Q8Acc<D> (&a)[NT], Q8Ref &ref, uint32_t
     }
   }
   uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-  if (KIND == PKV_Q8_E4M3 && nvalid < 32) {  // rows past the range may hold NaN codes
+  if (KIND == PKV_Q8_E4M3 && (NT == 1 || MASK) && nvalid < 32) {  // rows past the range may hold NaN codes
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       keep[t] = 0u;
@@ -1015,7 +1015,7 @@ __global__ void __launch_bounds__(q8_threads(D, NT), 1)
       const int nvalid = min(32, info.x - 32 * wg), seen = LISTED ? s_desc[s].seen - 32 * wg : nvalid;
       const float2 *const sc = reinterpret_cast<const float2 *>(base_ptr + SL::scales + s * 128);
       if (nvalid > 0) {
-        if (!LISTED || seen >= nvalid)
+        if (!LISTED || (seen >= nvalid && (NT == 1 || nvalid == 32)))
           q8_tiles<D, KIND, NT, false>(acc, ref, base + s * SL::kStage, at, sc, a.log2_box, wg, lane, nvalid, seen);
         else
           q8_tiles<D, KIND, NT, LISTED>(acc, ref, base + s * SL::kStage, at, sc, a.log2_box, wg, lane, nvalid, seen);
