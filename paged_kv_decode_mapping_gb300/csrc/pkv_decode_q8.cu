@@ -219,10 +219,19 @@ struct Q8Acc {
   float o[D / 16][4];
   float m0, m1, l0, l1;     // the rows' references; sums of weights, per lane
   uint32_t q[D / 16][2];    // fragments of q
-  float f0, f1;             // scores' factors of the two rows, without K's scale
+  float f0, f1;             // scores' factors of the two rows, without K's scale (and the codes' unit)
   float b0, b1;             // what the two rows' raw scores begin with
   int i0, i1;               // the rows' queries
 };
+// What raw scores of the two rows under a scale of K are to be multiplied by.  int8's codes are in units of 2^-24,
+// which comes last: with the rows' factor it would leave fp32 from q of 2^117 on, at a scale of 1.
+template <int D, int KIND>
+__device__ __forceinline__ void score_factors(const Q8Acc<D> &a, float k_scale, float &f0, float &f1) {
+  uint64_t f = q8::mul2(q8::f32x2(a.f0, a.f1), q8::f32x2(k_scale, k_scale));
+  if constexpr (KIND == PKV_Q8_INT8) f = q8::mul2(f, q8::f32x2(16777216.f, 16777216.f));
+  f0 = q8::split(f).x;
+  f1 = q8::split(f).y;
+}
 // For all tiles: the largest V scale so far, and 1 over it: o is in units of vref.
 struct Q8Ref {
   float vref, vinv;
@@ -254,7 +263,7 @@ __device__ __forceinline__ void load_q(Q8Acc<D> &a, uint32_t qs, int rows, int l
   // 2^(14 - exponent of the largest), as far as that and its inverse are normal numbers
   const int e = min(max(14 - ((int)(mb >> 7) - 127), -126), 126);
   const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-  float down = __uint_as_float((uint32_t)(127 - e) << 23) * scale_log2;
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23) * scale_log2;
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) {
@@ -264,7 +273,6 @@ __device__ __forceinline__ void load_q(Q8Acc<D> &a, uint32_t qs, int rows, int l
   }
   float begin = 0.f;
   if constexpr (KIND == PKV_Q8_INT8) {
-    down *= 16777216.f;  // the codes' 2^-24
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
     begin = -128.f * 5.9604645e-8f * sum;
@@ -352,8 +360,7 @@ __device__ __forceinline__ void q8_tiles(Q8Acc<D> (&a)[NT], Q8Ref &ref, uint32_t
       vs[i] = f.y;
       ks[i] = f.x;
       if (NT == 1) {
-        f0[i] = a[0].f0 * f.x;
-        f1[i] = a[0].f1 * f.x;
+        score_factors<D, KIND>(a[0], f.x, f0[i], f1[i]);
       }
     } else {
       vs[i] = vs[i - 1];
@@ -394,10 +401,7 @@ __device__ __forceinline__ void q8_tiles(Q8Acc<D> (&a)[NT], Q8Ref &ref, uint32_t
     auto unseen = [&](int i, int query) { return key(i) >= min(nvalid, seen + query); };
     if (NT > 1) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f0[i] = c.f0 * ks[i];
-        f1[i] = c.f1 * ks[i];
-      }
+      for (int i = 0; i < 4; ++i) score_factors<D, KIND>(c, ks[i], f0[i], f1[i]);
     }
     auto shifted = [&] {
 #pragma unroll

@@ -143,3 +143,31 @@ def test_values_near_the_ends_of_the_range(B, dtype, d, lens, hq, hkv):
     for out in (decode(B, b, q, scale)[b.cl > 0], prefill(B, b, q3, few, scale), prefill(B, b, q70, many, scale)):
         assert bool((out.double() >= largest * (1 - 2.0 ** -7)).all()) and bool(out.isfinite().all())
     assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", R.KINDS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_queries_near_the_end_of_the_range(B, dtype, d):
+    """q up to 2^127 over keys as small, and the other way round: the scores are ordinary."""
+    b = Batch([300, 1, 77], dtype, 2, d, 16, seed=82)
+    q, new = b.randn(3, 16, d), [5, 1, 5]
+    q5, plain = b.randn(11, 16, d), b.ks.clone()
+    for e in (118, 110, -110, -118):
+        k = 2.0 ** -e if e > 0 else 2.0 ** (-e - 3)
+        b.ks.copy_(plain * k)
+        qq, qq5 = ((x.float() * 2.0 ** e).to(torch.bfloat16) for x in (q, q5))
+        scale = 0.1 if e > 0 else 0.8
+        check(decode(B, b, qq, scale), *decode_ref(b, qq, scale), f"decode, 2^{e}")
+        check(prefill(B, b, qq5, new, scale), *prefill_ref(b, qq5, new, scale), f"drafts, 2^{e}")
+    # the largest exponents: q from 2^124 on, keys of 2^-124, one chosen by its sign
+    b.ks.fill_(2.0 ** -125)
+    R.bits(b.k)[:] = R.bits(torch.full((1,), 2.0, device=DEV).to(dtype))[0]
+    for s, n in enumerate(b.lens):
+        page, row = b.tables[s][(n // 2) // 16], (n // 2) % 16
+        b.k[page, :, row] = b.k[page, :, row].float().neg().to(dtype)
+    for sign in (1.0, -1.0):
+        q1 = torch.zeros(3, 16, d, dtype=torch.bfloat16, device=DEV)
+        q1[:, :, 3] = sign * 2.0 ** 127  # scores of 8 either way
+        check(decode(B, b, q1, 1.0), *decode_ref(b, q1, 1.0), "decode, one value")
+        check(prefill(B, b, q1, [1, 1, 1], 1.0), *prefill_ref(b, q1, [1, 1, 1], 1.0), "drafts, one value")
+    assert B.pkv_device_errors() == 0
