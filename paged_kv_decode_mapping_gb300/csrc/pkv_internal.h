@@ -133,6 +133,7 @@ cudaError_t read_decode_q8_errors(uint32_t *flags, int clear);
 
 // The 8-bit cache: the checks of its descriptor, and the quantising write split into its host
 // checks and its launch.
+int check_q8_sizes(const pkv_cache_desc *c, const char *fn);
 int check_q8(const pkv_q8_cache *q, const pkv_cache_desc *c, int32_t num_seqs, const char *fn);
 struct WriteQ8 {
   const pkv_bf16 *k, *v;

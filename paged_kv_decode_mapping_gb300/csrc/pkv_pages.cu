@@ -192,11 +192,9 @@ int launch_pages(pkv_bf16 *const *k_caches, pkv_bf16 *const *v_caches, int32_t n
 int check_q8_pages(const pkv_q8_cache *caches, int32_t num_layers, const pkv_cache_desc *c, const char *fn) {
   if (!c || (num_layers > 0 && !caches)) return set_error(PKV_ERR_NULL, "%s: NULL caches or descriptor", fn);
   if (num_layers < 0) return set_error(PKV_ERR_SHAPE, "%s: negative count", fn);
-  for (int32_t l = 0; l < num_layers; ++l) {
-    const int rc = check_q8(caches + l, c, 1, fn);
-    if (rc) return rc;
-  }
-  return PKV_OK;
+  int rc = check_q8_sizes(c, fn);  // (of no layers too: tables alone)
+  for (int32_t l = 0; !rc && l < num_layers; ++l) rc = check_q8(caches + l, c, 1, fn);
+  return rc;
 }
 
 int copy_q8_pages(const pkv_q8_cache *caches, int32_t num_layers, const int32_t *pairs, const int32_t *rows,

@@ -682,10 +682,7 @@ int launch_read(const Span &s, const pkv_q8_cache &q, const pkv_cache_desc &c, v
 
 cudaError_t read_q8_errors(uint32_t *flags, int clear) { return read_tu_errors(flags, clear); }
 
-int check_q8(const pkv_q8_cache *q, const pkv_cache_desc *c, int32_t num_seqs, const char *fn) {
-  if (!q || !c) return set_error(PKV_ERR_NULL, "%s: cache descriptor is NULL", fn);
-  if (q->kind != PKV_Q8_E4M3 && q->kind != PKV_Q8_INT8)
-    return set_error(PKV_ERR_UNSUPPORTED, "%s: unknown kind of codes %d", fn, q->kind);
+int check_q8_sizes(const pkv_cache_desc *c, const char *fn) {
   if (c->num_blocks <= 0 || c->num_kv_heads <= 0 || c->block_size <= 0 || c->head_dim <= 0)
     return set_error(PKV_ERR_SHAPE, "%s: cache sizes must be positive", fn);
   if (c->head_dim != 64 && c->head_dim != 128)
@@ -694,6 +691,15 @@ int check_q8(const pkv_q8_cache *q, const pkv_cache_desc *c, int32_t num_seqs, c
     return set_error(PKV_ERR_UNSUPPORTED, "%s: block_size %d (built: powers of two 8..256)", fn, c->block_size);
   if (c->num_blocks > 0x7fffffffLL / ((int64_t)c->num_kv_heads * c->block_size))
     return set_error(PKV_ERR_UNSUPPORTED, "%s: pool has more than 2^31-1 rows", fn);
+  return PKV_OK;
+}
+
+int check_q8(const pkv_q8_cache *q, const pkv_cache_desc *c, int32_t num_seqs, const char *fn) {
+  if (!q || !c) return set_error(PKV_ERR_NULL, "%s: cache descriptor is NULL", fn);
+  if (q->kind != PKV_Q8_E4M3 && q->kind != PKV_Q8_INT8)
+    return set_error(PKV_ERR_UNSUPPORTED, "%s: unknown kind of codes %d", fn, q->kind);
+  const int rc = check_q8_sizes(c, fn);
+  if (rc) return rc;
   if (num_seqs > 65535) return set_error(PKV_ERR_UNSUPPORTED, "%s: num_seqs > 65535", fn);
   if (num_seqs <= 0) return PKV_OK;
   if (!q->k_cache || !q->v_cache || !q->k_scale || !q->v_scale)
