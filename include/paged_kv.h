@@ -572,11 +572,15 @@ int paged_decode_step_rope_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t q_stride
 /*
  * paged_prefill_attention_q8 -- paged_prefill_attention over an 8-bit cache: q and out are
  * [num_queries][num_q_heads][head_dim], sequence b's newest tokens at rows query_start[b] ..
- * query_start[b+1]-1.  The contexts are read back as fp16 rows into the workspace
- * (paged_prefill_q8_workspace_size() bytes, no initial values; not for two calls that overlap),
- * scores and weights are fp16 products with fp32 sums as in paged_decode_attention_q8; or, where
- * that is estimated to be less (up to 32 queries of a sequence), a few queries at a time are rows of its
- * kernel.
+ * query_start[b+1]-1.  The contexts are read back as fp16 rows into the workspace (no initial values;
+ * not for two calls that overlap), scores and weights are fp16 products with fp32 sums as in
+ * paged_decode_attention_q8; or, where that is estimated to be less (up to 32 queries of a sequence) or
+ * num_seqs * max_context_len * num_kv_heads rows would be 2^31 or more, a few queries at a time are rows of
+ * its kernel.
+ * paged_prefill_q8_workspace_size() bytes are enough either way: 4 bytes for each of num_seqs *
+ * max_context_len * num_kv_heads * head_dim coordinates, or a few MB where that is less; 0: too many rows.
+ * paged_prefill_q8_workspace_size_for() are what a call of just these sizes needs: the few MB where it makes no
+ * rows; 0: it would be refused (or has nothing to do).
  * max_query_len and max_context_len bound every length; longer ones, and sequences of more queries
  * than tokens, raise PKV_DEVERR_CONTEXT_LEN (they are cut; a query before the first token gives
  * zeros).  Rows of no sequence are not written.  A page of scale NaN (see paged_kv_write_q8) makes
@@ -584,6 +588,9 @@ int paged_decode_step_rope_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t q_stride
  */
 size_t paged_prefill_q8_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim,
                                        int32_t max_context_len);
+size_t paged_prefill_q8_workspace_size_for(int64_t num_queries, int32_t max_query_len, int32_t num_seqs,
+                                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                           int32_t max_context_len);
 int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t num_queries,
                                const pkv_q8_cache *cache, const int32_t *block_tables,
                                int32_t max_blocks_per_seq, const int32_t *context_lens,

@@ -117,6 +117,8 @@ _lib.paged_decode_step_rope_q8.argtypes = [_P, _P, _i64, _P, _P, _P, _i64, _i64,
 _lib.paged_decode_step_rope_q8.restype = ctypes.c_int
 _lib.paged_prefill_q8_workspace_size.argtypes = [_i32] * 4
 _lib.paged_prefill_q8_workspace_size.restype = _sz
+_lib.paged_prefill_q8_workspace_size_for.argtypes = [_i64] + [_i32] * 6
+_lib.paged_prefill_q8_workspace_size_for.restype = _sz
 _lib.paged_prefill_attention_q8.argtypes = [_P, _P, _i64, _Q8, _P, _i32, _P, _i32, _P, _i32, _i32, _i32, _D, _f32,
                                             _P, _sz, _P]
 _lib.paged_prefill_attention_q8.restype = ctypes.c_int
@@ -858,8 +860,16 @@ def paged_decode_q8_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads
 
 def paged_prefill_q8_workspace_size(num_seqs: int, num_kv_heads: int, head_dim: int, block_size: int,
                                     max_context_len: int) -> int:
-    """(By tokens: the block size makes no difference.)"""
+    """For any call of these sizes: fp16 rows of num_seqs contexts of max_context_len.  (By tokens: the block
+    size makes no difference.)"""
     return int(_lib.paged_prefill_q8_workspace_size(num_seqs, num_kv_heads, head_dim, max_context_len))
+
+
+def paged_prefill_q8_workspace_size_for(num_queries: int, max_query_len: int, num_seqs: int, num_q_heads: int,
+                                        num_kv_heads: int, head_dim: int, max_context_len: int) -> int:
+    """For a call of just these sizes: where its few queries need no rows, by their number alone."""
+    return int(_lib.paged_prefill_q8_workspace_size_for(num_queries, max_query_len, num_seqs, num_q_heads, num_kv_heads,
+                                                        head_dim, max_context_len))
 
 
 def _q8_query(out, q, cache, rows: Optional[int], dev: int) -> None:
@@ -960,15 +970,15 @@ def paged_prefill_attention_q8(out: torch.Tensor, q: torch.Tensor, k_cache: torc
                                max_query_len: int, scale: float, workspace: Optional[torch.Tensor] = None,
                                stream=None) -> None:
     """paged_prefill_attention over an 8-bit cache.  ``workspace``: uint8, CUDA,
-    ``paged_prefill_q8_workspace_size`` bytes with any contents; it may be omitted."""
+    ``paged_prefill_q8_workspace_size`` (or ``_size_for``) bytes with any contents; it may be omitted."""
     dev = _home(q)
     shape = k_cache.shape
     _q8_query(out, q, shape, None, dev)
     if query_start is None:
         raise ValueError("query_start must be [B + 1]")
     cache = _q8_cache(dev, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start, shape)
-    workspace = _q8_workspace(workspace, 0 if workspace is not None else paged_prefill_q8_workspace_size(
-        cache[12], cache[7], cache[8], cache[6], int(max_context_len)), False, q, dev, stream)
+    workspace = _q8_workspace(workspace, 0 if workspace is not None else paged_prefill_q8_workspace_size_for(
+        q.shape[0], int(max_query_len), cache[12], q.shape[1], cache[7], cache[8], int(max_context_len)), False, q, dev, stream)
     _check(_call_q8(_CALL_PREFILL, _pack_prefill(
         *cache, _stream(stream, dev), out.data_ptr(), q.data_ptr(), max_context_len, q.shape[1], scale,
         workspace.data_ptr(), workspace.nbytes, q.shape[0], query_start.data_ptr(), max_query_len)),

@@ -869,28 +869,32 @@ struct PrefillLayout {
 };
 constexpr int kMaxListed = 32, kMaxEntries = 65535;  // queries of a sequence, entries of a call's list
 
-// Whether a list for the decode kernel is the shorter way, by the longest context: it reads that once for
-// each entry, spread over the GPU; the tiles read it once (and once more back), but the CTAs of one
-// (sequence, kv head) take its blocks of 128 keys one after another.  Times as measured: list_plan's, 10 us
-// besides; 1.3 us of a tile's block, 6 TB/s for the reading back, 12 us besides.  With 8 kv heads of
-// 4 x 64: 8 sequences of 2 queries over 4000 tokens 16 us by a list, 67 by tiles, of 8 queries 28 and
-// 67, of 32 75 and 68; 64 of 8 143 and 291, of 16 276 and 291, of 32 539 and 292.
-bool list_pays(int64_t num_queries, int32_t max_query_len, int32_t num_seqs, int32_t hq, const pkv_cache_desc &c,
+// Whether the queries fit a list for the decode kernel.
+bool list_fits(int32_t max_query_len, int32_t num_seqs, int32_t group, int32_t d) {
+  return max_query_len <= kMaxListed && (int64_t)num_seqs * list_plan(group, d, max_query_len).per <= kMaxEntries;
+}
+
+// Whether such a list is the shorter way, by the longest context: it reads that once for each entry, spread
+// over the GPU; the tiles read it once (and once more back), but the CTAs of one (sequence, kv head) take
+// its blocks of 128 keys one after another.  Times as measured: list_plan's, 10 us besides; 1.3 us of a
+// tile's block, 6 TB/s for the reading back, 12 us besides.  With 8 kv heads of 4 x 64: 8 sequences of 2
+// queries over 4000 tokens 16 us by a list, 67 by tiles, of 8 queries 28 and 67, of 32 75 and 68; 64 of 8
+// 143 and 291, of 16 276 and 291, of 32 539 and 292.
+bool list_pays(int64_t num_queries, int32_t max_query_len, int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d,
                int32_t max_len, int sms) {
-  if (max_query_len > kMaxListed) return false;
-  const int32_t group = hq / c.num_kv_heads;
-  const ListPlan plan = list_plan(group, c.head_dim, max_query_len);
-  if ((int64_t)num_seqs * plan.per > kMaxEntries) return false;
-  const double blocks = (max_len + 127) / 128, hkv = c.num_kv_heads;
-  const double list = (double)num_seqs * plan.per * hkv * (blocks + 1) / sms * plan.block + 10;  // (an end as a block)
-  const double ctas = (num_queries / (2. * (128 / group)) + num_seqs) * hkv;
-  const double tiles = (ctas > sms ? ctas / sms : 1) * blocks * 1.3 + 12 + num_seqs * hkv * c.head_dim * max_len * 6. / 6e6;
+  const int32_t group = hq / hkv;
+  const ListPlan plan = list_plan(group, d, max_query_len);
+  const double blocks = (max_len - 1) / 128 + 1, heads = hkv;
+  const double list = (double)num_seqs * plan.per * heads * (blocks + 1) / sms * plan.block + 10;  // (an end as a block)
+  const double ctas = (num_queries / (2. * (128 / group)) + num_seqs) * heads;
+  const double tiles = (ctas > sms ? ctas / sms : 1) * blocks * 1.3 + 12 + num_seqs * heads * d * max_len * 6. / 6e6;
   return list < tiles;
 }
 
-bool prefill_layout(int32_t num_seqs, int32_t hkv, int32_t d, int32_t max_len, int sms, PrefillLayout *p) {
-  if (num_seqs <= 0 || hkv <= 0 || max_len <= 0 || (d != 64 && d != 128)) return false;
-  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+size_t up(size_t x) { return (x + 255) & ~size_t(255); }
+
+// The tiles' workspace; false: more rows than they count.
+bool prefill_layout(int32_t num_seqs, int32_t hkv, int32_t d, int32_t max_len, PrefillLayout *p) {
   if ((int64_t)max_len * num_seqs > 0x7fffff00LL / hkv) return false;
   p->rows = max_len;
   const size_t rows = up((size_t)max_len * num_seqs * hkv * d * 2), units = up((size_t)num_seqs * hkv * 4);
@@ -900,9 +904,28 @@ bool prefill_layout(int32_t num_seqs, int32_t hkv, int32_t d, int32_t max_len, i
   p->v_unit = p->k_unit + units;
   p->nan_from = p->v_unit + units;
   p->order = p->nan_from + units;
-  p->total = std::max(p->order + up((size_t)num_seqs * sizeof(int4)),  // either way
-                      up(list_q8_workspace(std::min((int64_t)num_seqs * kMaxListPer, (int64_t)kMaxEntries), d, sms)));
+  p->total = p->order + up((size_t)num_seqs * sizeof(int4));
   return true;
+}
+// The list's, however many queries a sequence has.
+size_t list_bytes(int32_t num_seqs, int32_t d, int sms) {
+  return up(list_q8_workspace(std::min((int64_t)num_seqs * kMaxListPer, (int64_t)kMaxEntries), d, sms));
+}
+
+// The way that a call takes, and its workspace: 0 bytes where no way can be.
+struct PrefillWay {
+  bool list;
+  size_t bytes;
+  PrefillLayout tiles;
+};
+PrefillWay prefill_way(int64_t num_queries, int32_t max_query_len, int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d,
+                       int32_t max_len, int sms) {
+  PrefillWay w = {};
+  const bool rows = prefill_layout(num_seqs, hkv, d, max_len, &w.tiles);
+  w.list = list_fits(max_query_len, num_seqs, hq / hkv, d) &&
+           (!rows || list_pays(num_queries, max_query_len, num_seqs, hq, hkv, d, max_len, sms));
+  w.bytes = w.list ? list_bytes(num_seqs, d, sms) : rows ? w.tiles.total : 0;
+  return w;
 }
 
 // The current device's SMs; without a device (the checks that need none still stand) `otherwise`.
@@ -917,7 +940,21 @@ int sms_or(int otherwise) {
 PKV_API size_t paged_prefill_q8_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim,
                                                int32_t max_context_len) {
   PrefillLayout p;
-  return prefill_layout(num_seqs, num_kv_heads, head_dim, max_context_len, sms_or(152), &p) ? p.total : 0;
+  if (num_seqs <= 0 || num_kv_heads <= 0 || max_context_len <= 0 || (head_dim != 64 && head_dim != 128) ||
+      !prefill_layout(num_seqs, num_kv_heads, head_dim, max_context_len, &p))
+    return 0;
+  return std::max(p.total, list_bytes(num_seqs, head_dim, sms_or(152)));
+}
+
+PKV_API size_t paged_prefill_q8_workspace_size_for(int64_t num_queries, int32_t max_query_len, int32_t num_seqs,
+                                                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                                   int32_t max_context_len) {
+  if (num_queries <= 0 || max_query_len <= 0 || num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+      num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > kMaxGroup || (head_dim != 64 && head_dim != 128) ||
+      max_context_len < max_query_len)
+    return 0;
+  return prefill_way(num_queries, max_query_len, num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len,
+                     sms_or(152)).bytes;
 }
 
 PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t num_queries,
@@ -943,12 +980,14 @@ PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t
   if (!aligned16(out)) return set_error(PKV_ERR_ALIGN, "%s: out must be 16-byte aligned", fn);
   if (misaligned4(query_start) || misaligned4(block_tables) || misaligned4(context_lens))
     return set_error(PKV_ERR_ALIGN, "%s: int32 tensors must be 4-byte aligned", fn);
-  PrefillLayout p;
   const int sms = sms_or(152);
-  if (!prefill_layout(num_seqs, desc->num_kv_heads, desc->head_dim, max_context_len, sms, &p))
+  const PrefillWay way = prefill_way(num_queries, max_query_len, num_seqs, num_q_heads, desc->num_kv_heads, desc->head_dim,
+                                     max_context_len, sms);
+  const PrefillLayout &p = way.tiles;
+  if (way.bytes == 0)
     return set_error(PKV_ERR_UNSUPPORTED, "%s: the contexts have more than 2^31 rows of heads", fn);
-  if (!workspace || workspace_bytes < p.total)
-    return set_error(PKV_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, workspace_bytes, p.total);
+  if (!workspace || workspace_bytes < way.bytes)
+    return set_error(PKV_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, workspace_bytes, way.bytes);
   if (!aligned16(workspace)) return set_error(PKV_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char *const ws = static_cast<char *>(workspace);
@@ -966,7 +1005,7 @@ PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t
   l.num_kv_heads = desc->num_kv_heads;
   l.head_dim = desc->head_dim;
   l.scale = scale;
-  if (list_pays(num_queries, max_query_len, num_seqs, num_q_heads, *desc, max_context_len, sms)) {
+  if (way.list) {
     rc = launch_list_q8(l, *cache, *desc, block_tables, max_blocks_per_seq, workspace, sms, s);
     if (!rc) clear_error();
     return rc;

@@ -171,3 +171,25 @@ def test_queries_near_the_end_of_the_range(B, dtype, d):
         check(decode(B, b, q1, 1.0), *decode_ref(b, q1, 1.0), "decode, one value")
         check(prefill(B, b, q1, [1, 1, 1], 1.0), *prefill_ref(b, q1, [1, 1, 1], 1.0), "drafts, one value")
     assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", R.KINDS)
+def test_drafts_over_room_for_long_contexts(B, dtype):
+    """Tables and max_context_len for far longer contexts than the sequences have so far: a workspace that has no
+    room for those, exactly as large as the call says, and none."""
+    lens, new, hq, hkv, d, longest = [300, 17, 0, 129] * 16, [5, 3, 0, 1] * 16, 8, 8, 64, 1 << 22
+    b = Batch(lens, dtype, hkv, d, 256, seed=85)
+    wide = torch.full((len(lens), longest // 256), -1, dtype=torch.int32, device=DEV)
+    wide[:, :b.bt.shape[1]] = b.bt
+    q = b.randn(sum(new), hq, d)
+    assert B.paged_prefill_q8_workspace_size(len(lens), hkv, d, 256, longest) == 0  # (2^31 rows of heads)
+    size = B.paged_prefill_q8_workspace_size_for(sum(new), 5, len(lens), hq, hkv, d, longest)
+    assert 0 < size < 32 << 20
+    ws = torch.full((size + 4096,), 7, dtype=torch.uint8, device=DEV)
+    want, mag = prefill_ref(b, q, new, 0.125)
+    for kw in ({"workspace": ws[:size]}, {}):
+        out = torch.full_like(q, 77.0)
+        B.paged_prefill_attention_q8(out, q, *b.cache(), wide, b.cl, longest, starts(new), 5, 0.125, **kw)
+        check(out, want, mag, str(list(kw)))
+    assert bool((ws[size:] == 7).all())
+    assert B.pkv_device_errors() == 0
