@@ -53,6 +53,10 @@ __device__ __forceinline__ Tokens tokens_of(const Span &s, int b, bool *bad) {
   return t;
 }
 
+// Whether a chunk may have queries of sequence b.  (Of one that has none no page is looked at: its tables may
+// be old.)
+__device__ __forceinline__ bool has_queries(const Span &s, int b) { return q8::ld(s.start + b + 1) > q8::ld(s.start + b); }
+
 // ---------------------------------------------------------------------------
 // Rotary embedding of 8 coordinates: products and sums in fp32, each rounded once, then bf16.
 
@@ -372,9 +376,9 @@ __global__ void __launch_bounds__(ROPE ? 2 * kQ8Threads : 4 * kQ8Threads, ROPE ?
 // Reading back: bf16(code * scale).  One group of threads per (sequence, page, K or V, run of kv
 // heads), up to 16 loads of a thread in flight.  Bound by HBM, which takes two bytes for each one
 // read: 16 contexts of 1 to 8192 tokens, 8 heads of 128, 31.5 us, 5.0 TB/s (27.6 with 256-token pages).
-// For the prefill, whole contexts as fp16 rows, row seq * out_rows + t being token t's: code *
-// (scale / unit) for the largest scale of the (sequence, kv head) as unit, so that codes keep 11
-// bits (bf16 rows, of 8, doubled the error of the output).
+// For the prefill, whole contexts of the sequences with queries as fp16 rows, row seq * out_rows + t
+// being token t's: code * (scale / unit) for the largest scale of the (sequence, kv head) as unit, so
+// that codes keep 11 bits (bf16 rows, of 8, doubled the error of the output).
 
 struct ReadArgs {
   Span s;
@@ -399,7 +403,6 @@ struct UnitArgs {
   const float *k_scale, *v_scale;
   float *k_unit, *v_unit;
   int32_t *nan_from;  // the first key of a page whose scale is NaN
-  const int32_t *start;
   int4 *order;
   int32_t num_queries, max_query_len;
 };
@@ -411,11 +414,12 @@ __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_con
   __shared__ int s_before[32], s_rank[32], s_nan[kUnitThreads];
   const int b = blockIdx.x, H = a.s.num_kv_heads, tid = threadIdx.x;
   const int cap = (int)min((int64_t)a.s.max_blocks * a.s.block_size, (int64_t)a.s.max_new);
-  const int L = min(max(q8::ld(a.s.lens + b), 0), cap), pages = (L + a.s.block_size - 1) >> a.s.log2_bs;
+  const int L = min(max(q8::ld(a.s.lens + b), 0), cap);
+  const int pages = has_queries(a.s, b) ? (int)(((int64_t)L + a.s.block_size - 1) >> a.s.log2_bs) : 0;
   const int32_t *const row = a.s.tables + (int64_t)b * a.s.max_blocks;
   int before = 0, rank = 0;  // the furthest end of the sequences before b; how many are taken before b
   for (int i = tid; i < a.s.num_seqs; i += kUnitThreads) {
-    if (i < b) before = max(before, min(max(q8::ld(a.start + i + 1), 0), a.num_queries));
+    if (i < b) before = max(before, min(max(q8::ld(a.s.start + i + 1), 0), a.num_queries));
     const int Li = min(max(q8::ld(a.s.lens + i), 0), cap);
     rank += Li > L || (Li == L && i < b);
   }
@@ -430,7 +434,7 @@ __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_con
     before = __reduce_max_sync(0xffffffffu, s_before[tid]);
     rank = __reduce_add_sync(0xffffffffu, s_rank[tid]);
     if (tid == 0) {
-      const int s0 = q8::ld(a.start + b), e0 = q8::ld(a.start + b + 1), e = min(max(e0, 0), a.num_queries);
+      const int s0 = q8::ld(a.s.start + b), e0 = q8::ld(a.s.start + b + 1), e = min(max(e0, 0), a.num_queries);
       const int s = min(max(max(s0, 0), before), a.num_queries), n = min(max(e - s, 0), a.max_query_len);
       if (s != s0 || s + n != e0) raise_error(PKV_DEVERR_CONTEXT_LEN);
       a.order[rank] = make_int4(b, s, n, 0);
@@ -486,6 +490,7 @@ __global__ void __launch_bounds__(kQ8Threads, U == 16 ? 5 : 8) read_q8_kernel(co
   if (j >= a.pages) return;  // (whole warps, here and below)
   Tokens t;
   if constexpr (WHOLE) {  // lengths past the tables are cut, as the attention does
+    if (!has_queries(a.s, b)) return;
     const int cap = (int)min((int64_t)a.s.max_blocks * a.s.block_size, (int64_t)a.s.max_new);
     t.begin = 0;
     t.end = min(max(q8::ld(a.s.lens + b), 0), cap);
@@ -1010,7 +1015,7 @@ PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t
     if (!rc) clear_error();
     return rc;
   }
-  const Span span = span_of(block_tables, max_blocks_per_seq, context_lens, nullptr, max_context_len, num_seqs, 0, *desc);
+  const Span span = span_of(block_tables, max_blocks_per_seq, context_lens, query_start, max_context_len, num_seqs, 0, *desc);
   UnitArgs u;
   u.s = span;
   u.k_scale = cache->k_scale;
@@ -1018,7 +1023,6 @@ PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t
   u.k_unit = reinterpret_cast<float *>(ws + p.k_unit);
   u.v_unit = reinterpret_cast<float *>(ws + p.v_unit);
   u.nan_from = reinterpret_cast<int32_t *>(ws + p.nan_from);
-  u.start = query_start;
   u.order = reinterpret_cast<int4 *>(ws + p.order);
   u.num_queries = (int32_t)num_queries;
   u.max_query_len = max_query_len;

@@ -193,3 +193,26 @@ def test_drafts_over_room_for_long_contexts(B, dtype):
         check(out, want, mag, str(list(kw)))
     assert bool((ws[size:] == 7).all())
     assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", R.KINDS)
+@pytest.mark.parametrize("new", [[90, 0, 130, 0], [0, 70, 0, 0]])
+def test_sequences_without_queries_are_not_looked_at(B, dtype, new):
+    """A chunk's call over a batch some of whose sequences have no queries, and tables that mean nothing:
+    no flag, and nothing read back for them."""
+    b = Batch([300, 250, 200, 40], dtype, 2, 64, 16, seed=86)
+    q = b.randn(sum(new), 4, 64)
+    want, bound = chunk_ref(b, q, new, 0.125)
+    bt, cl = b.bt.clone(), b.cl.clone()
+    for s, n in enumerate(new):
+        if n == 0:
+            bt[s], cl[s] = b.nb + 1000, 288 if s < 3 else 0
+    size = B.paged_prefill_q8_workspace_size_for(sum(new), max(new), 4, 4, 2, 64, 300)
+    ws = torch.full((size,), 7, dtype=torch.uint8, device=DEV)
+    out = torch.full_like(q, 77.0)
+    B.paged_prefill_attention_q8(out, q, *b.cache(), bt, cl, 300, starts(new), max(new), 0.125, workspace=ws)
+    check_chunk(out, want, bound)
+    assert B.pkv_device_errors() == 0
+    rows = ws[:4 * 300 * 2 * 64 * 2].view(4, -1)  # K's, of each sequence
+    for s, n in enumerate(new):
+        assert bool((rows[s] == 7).all()) == (n == 0), f"sequence {s}"
