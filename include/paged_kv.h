@@ -449,8 +449,11 @@ int prompt_attention(pkv_bf16 *out, const pkv_bf16 *q, const pkv_bf16 *k, const 
  *   k_scale, v_scale : [num_blocks][num_kv_heads] fp32
  * A code c of block n and kv head h stands for c * scale[n][h].  PKV_Q8_INT8: whole numbers of
  * [-127, 127]; PKV_Q8_E4M3: 8-bit floats (4 exponent bits, 3 of the fraction, largest 448).
- * int8 keeps each value to half of 1/127 of the block's largest; e4m3 to 2^-4 of itself, down
- * to 2^-10 / 448 of the largest.  head_dim 64 or 128; block_size a power of two in [8, 256];
+ * A block written at once keeps each value to half of 1/127 of the block's largest (int8), or to
+ * 2^-4 of itself, or 2^-10 / 448 of the largest where that is more (e4m3).  Each time that its scale
+ * grows, the rows that it held are rounded anew, and may be off by as much again: after g growths by
+ * (g + 1) / 2 of 1/127 of the largest; by (1 + 2^-4)^(g+1) - 1 of themselves, or g + 1 times the
+ * other.  head_dim 64 or 128; block_size a power of two in [8, 256];
  * num_blocks * num_kv_heads * block_size < 2^31; caches 16-byte, scales 4-byte aligned.
  * Pages and scales need no initial values: a page begins with the write of its first row.
  * Scales that a caller makes are 0, NaN, or of 2^-126 or more.
