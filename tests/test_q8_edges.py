@@ -216,3 +216,41 @@ def test_sequences_without_queries_are_not_looked_at(B, dtype, new):
     rows = ws[:4 * 300 * 2 * 64 * 2].view(4, -1)  # K's, of each sequence
     for s, n in enumerate(new):
         assert bool((rows[s] == 7).all()) == (n == 0), f"sequence {s}"
+
+
+AIMS = [
+    # context lengths, new tokens, q heads, kv heads, block size: drafts, then chunks
+    ([700, 30, 5000, 131], [5, 5, 5, 3], 8, 2, 16), ([9000, 257], [31, 8], 3, 1, 32), ([2, 129, 300], [2, 1, 8], 16, 2, 8),
+    ([700, 130, 3000], [150, 130, 300], 6, 2, 16), ([1000, 256, 1], [129, 256, 1], 8, 1, 256),
+]
+
+
+@pytest.mark.parametrize("dtype", R.KINDS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,new,hq,hkv,bs", AIMS)
+def test_chunks_aimed_at_single_keys(B, dtype, d, lens, new, hq, hkv, bs):
+    """Every query aimed at one key, whose value is then the output: its own, the one before, those at the
+    borders of pages and of blocks of 128, any; and at the next one and the last, which it must not see."""
+    b = Batch(lens, dtype, hkv, d, bs, seed=83)
+    gen = torch.Generator().manual_seed(84)
+    own = torch.cat([torch.arange(m - n, m) for m, n in zip(lens, new)])
+    seq = torch.cat([torch.full((n,), s) for s, n in enumerate(new)])
+    last = torch.tensor(lens)[seq] - 1
+    k = [R.values(b.k, b.ks, b.tables[s], 0, m) for s, m in enumerate(lens)]
+    v = [R.values(b.v, b.vs, b.tables[s], 0, m, torch.float64) for s, m in enumerate(lens)]
+    aims = [("own", own), ("before", own - 1), ("next", own + 1), ("last", last)]
+    aims += [(f"key {t}", torch.full_like(own, t)) for t in (0, bs - 1, bs, 127, 128)]
+    aims += [("back 128", own - 128), ("back to a block", own // 128 * 128)]
+    aims += [("any", (torch.rand(len(own), generator=gen) * (own + 1)).long()) for _ in range(4)]
+    for what, at in aims:
+        at = torch.minimum(at.clamp(min=0), last)
+        aim = torch.stack([k[s][t] for s, t in zip(seq.tolist(), at.tolist())])
+        aimed = torch.stack([v[s][t] for s, t in zip(seq.tolist(), at.tolist())])
+        q = (aim * 6.0).repeat_interleave(hq // hkv, 1).to(torch.bfloat16)
+        out = prefill(B, b, q, new, 1.0)
+        want, bound = chunk_ref(b, q, new, 1.0, codes=max(new) <= 32)  # few queries are rows of the decode kernel
+        check_chunk(out, want, bound, what)
+        off = (want - aimed.repeat_interleave(hq // hkv, 1)).abs().amax((1, 2))
+        seen = (at <= own).to(DEV)
+        assert bool((off[seen] < 0.05).all()) and bool((off[~seen] > 0.5).all())  # a lost or an extra key would show
+    assert B.pkv_device_errors() == 0
