@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kQ8Threads = 128;   // of a CTA; a write's may have two or four times as many
 constexpr int64_t kReadWide = 1 << 18;  // vectors of a call
+constexpr int kHeldVecs = 4;  // of 16 held codes, a thread's loads in flight while they are rounded anew
 constexpr int kRotateHeads = 4;  // q heads a thread rotates with one position's cosines and sines
 
 // What names the tokens of a call: sequence b's newest n of context_lens[b], its rows in the
@@ -220,6 +221,7 @@ __global__ void __launch_bounds__(ROPE ? 2 * kQ8Threads : 4 * kQ8Threads, ROPE ?
     }
   }
   __shared__ uint32_t s_max[4 * kQ8Threads / 32];
+  __shared__ alignas(8) uint8_t s_again[4 * kQ8Threads / 32][256];
   const int tid = threadIdx.x, group = 1 << a.log2_group, gt = tid & (group - 1);
   const uint32_t item = blockIdx.x * (blockDim.x >> a.log2_group) + (tid >> a.log2_group);
   const int j = (int)(item / (uint32_t)a.s.num_kv_heads), h = (int)(item - (uint32_t)j * a.s.num_kv_heads);
@@ -356,18 +358,34 @@ __global__ void __launch_bounds__(ROPE ? 2 * kQ8Threads : 4 * kQ8Threads, ROPE ?
     if (turn(u, y) && (u < S || !store(u, y, false))) store(u, y, true);
   }
   if (to > old && r0 > 0) {  // the rows held before, in units of the new scale
-    for (int e = gt; e < r0 * (D / 16); e += group) {
-      uint4 *const p = reinterpret_cast<uint4 *>(rows) + e;
-      const uint4 v = *p;
-      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    // A code's new one goes by the code alone: each warp divides for the 256 there are.  (Divided element by
+    // element, 256 sequences of one token whose pages of 16 all grew took 24 us, of 256 rows 200.)
+    uint8_t *const map = s_again[tid >> 5];
+    uint2 w = make_uint2(0x03020100u + 0x08080808u * (tid & 31), 0x07060504u + 0x08080808u * (tid & 31));
+    auto anew = [&](uint32_t c) {
+      const uint32_t z = q8::prep<KIND>(c);
+      const float2 f = q8::f16x2_to_f32(q8::pair<KIND, 0>(z)), g = q8::f16x2_to_f32(q8::pair<KIND, 1>(z));
+      return q8::encode4<KIND>(__fdiv_rn(__fmul_rn(f.x, old), to), __fdiv_rn(__fmul_rn(f.y, old), to),
+                               __fdiv_rn(__fmul_rn(g.x, old), to), __fdiv_rn(__fmul_rn(g.y, old), to));
+    };
+    w.x = anew(w.x);
+    w.y = anew(w.y);
+    reinterpret_cast<uint2 *>(map)[tid & 31] = w;
+    __syncwarp();
+    auto mapped = [&](uint32_t c) {
+      return map[c & 255] | map[c >> 8 & 255] << 8 | map[c >> 16 & 255] << 16 | (uint32_t)map[c >> 24] << 24;
+    };
+    const int vecs = r0 * (D / 16);
+    for (int e = gt; e < vecs; e += kHeldVecs * group) {
+      uint4 v[kHeldVecs];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t z = q8::prep<KIND>(w[k]);
-        const float2 f = q8::f16x2_to_f32(q8::pair<KIND, 0>(z)), g = q8::f16x2_to_f32(q8::pair<KIND, 1>(z));
-        w[k] = q8::encode4<KIND>(__fdiv_rn(__fmul_rn(f.x, old), to), __fdiv_rn(__fmul_rn(f.y, old), to),
-                                 __fdiv_rn(__fmul_rn(g.x, old), to), __fdiv_rn(__fmul_rn(g.y, old), to));
-      }
-      *p = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int u = 0; u < kHeldVecs; ++u)
+        if (e + u * group < vecs) v[u] = reinterpret_cast<const uint4 *>(rows)[e + u * group];
+#pragma unroll
+      for (int u = 0; u < kHeldVecs; ++u)
+        if (e + u * group < vecs)
+          reinterpret_cast<uint4 *>(rows)[e + u * group] =
+              make_uint4(mapped(v[u].x), mapped(v[u].y), mapped(v[u].z), mapped(v[u].w));
     }
   }
 }
