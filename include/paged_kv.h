@@ -487,7 +487,8 @@ typedef struct pkv_q8_cache {
  * one call (shared pages are copied first, pkv_bm_append_slots_cow), nor may a page's row 0
  * be written again while rows behind it are to be kept.
  *
- * max_query_len >= every n_b.  A sequence whose lengths do not fit (n_b over that or over L_b,
+ * max_query_len >= every n_b (and the grid goes by it: see paged_prefill_attention_q8 on batches of chunks
+ * and single tokens).  A sequence whose lengths do not fit (n_b over that or over L_b,
  * L_b over the table's capacity, rows past num_tokens) is skipped with PKV_DEVERR_CONTEXT_LEN; a
  * page outside the pool is skipped with PKV_DEVERR_BLOCK_ID.
  */
@@ -533,7 +534,8 @@ int paged_kv_read_q8(pkv_bf16 *k_out, pkv_bf16 *v_out, int64_t k_stride, int64_t
  * q, by a power of two for each row, is exact down to 2^-28 of the row's largest; a weight, times
  * its page's V scale over the largest so far, is off by 2^-11 of itself, or by 2^-35 of the
  * largest weight where that is more.  Sizes, alignment
- * and bad values as in paged_decode_attention.
+ * and bad values as in paged_decode_attention; a row of q with an infinity gives NaN (or zeros, where it
+ * would make every score -inf).
  *
  * The workspace (paged_decode_q8_workspace_size() bytes) must be zero-filled before its first
  * use, and every call that completes leaves it ready for the next one of any sizes that it is
@@ -580,6 +582,12 @@ int paged_decode_step_rope_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t q_stride
  * paged_decode_attention_q8; or, where that is estimated to be less (up to 32 queries of a sequence) or
  * num_seqs * max_context_len * num_kv_heads rows would be 2^31 or more, a few queries at a time are rows of
  * its kernel.
+ * Through rows K's and V's values are rounded once more, to fp16 in units of the largest scale of
+ * the (sequence, kv head): off by 2^-11 of themselves, or by 2^-25 of that unit where that is more; a weight
+ * by 2^-11 of itself, or by 2^-32 of the largest.
+ * One way is taken for the whole call, by its longest chunk: beside one of more than 32 queries single tokens
+ * have their contexts read back too, and max_query_len is what the write's and the read's grids go by.  Chunks
+ * and single tokens are better called apart (paged_decode_attention_q8 for these).
  * paged_prefill_q8_workspace_size() bytes are enough either way: 4 bytes for each of num_seqs *
  * max_context_len * num_kv_heads * head_dim coordinates, or a few MB where that is less; 0: too many rows.
  * paged_prefill_q8_workspace_size_for() are what a call of just these sizes needs: the few MB where it makes no

@@ -117,7 +117,7 @@ struct Q8Args {
   int32_t depth;                // 1: the first map leads to the other pool too
   int32_t v_first;              // V's rows lie first in a box
   float scale_log2;
-  int32_t step;  // behind a step's write: only the new tokens' pages, and q, are to be waited for
+  int32_t step;  // behind a step's write, which may still run: tables and lengths are read ahead of its end
 };
 
 // A stage is filled by 128-byte-swizzled boxes, one pool's rows of a box and then the other's: rows

@@ -125,8 +125,9 @@ __device__ __forceinline__ uint4 rotate_pairs(const uint4 &x, const Angles &a) {
 // value and rounding them, U 16-byte vectors a thread (where k is rotated, rows that do not fit are read
 // a second time).
 // Bound by its instructions (two thirds of the issue slots; widening, two products and two
-// conversions for each pair of codes) and by HBM: 34000 tokens of 8 heads of 128 take 49 us, 4.4
-// TB/s; with k rotated 84, with 24 heads of q besides 147.  256 tokens of a step: 6 us.
+// conversions for each pair of codes) and by HBM: 35000 tokens of 8 heads of 128 take 47 us, 4.6
+// TB/s; with k rotated 84, with 24 heads of q besides 147.  256 tokens of a step: 3.6 us, and 4 more where
+// pages of 16 all grow (30 to 35 more with pages of 256).
 
 struct WriteArgs {
   Span s;
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(ROPE ? 2 * kQ8Threads : 4 * kQ8Threads, ROPE ?
   const q8::Inverse by = q8::inverse_of(to == 0.f ? 1.f : to);
   uint2 *const dst = reinterpret_cast<uint2 *>(rows + (int64_t)(r0 + first) * D);
   // The rare rows next to a border between codes are noted and divided at the end, from their loads on
-  // (with the divisions behind every vector the code left the instruction cache: 56 us, now 49).
+  // (with the divisions behind every vector the code left the instruction cache: 56 us, 49 without).
   auto store = [&](int u, const uint4 *x, bool exact) {
     bool all = true;
 #pragma unroll
