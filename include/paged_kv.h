@@ -579,19 +579,20 @@ int paged_decode_step_rope_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t q_stride
  * [num_queries][num_q_heads][head_dim], sequence b's newest tokens at rows query_start[b] ..
  * query_start[b+1]-1.  The contexts are read back as fp16 rows into the workspace (no initial values;
  * not for two calls that overlap), scores and weights are fp16 products with fp32 sums as in
- * paged_decode_attention_q8; or, where that is estimated to be less (up to 32 queries of a sequence) or
- * num_seqs * max_context_len * num_kv_heads rows would be 2^31 or more, a few queries at a time are rows of
- * its kernel.
+ * paged_decode_attention_q8; or, where that is estimated to be less (up to 32 queries of a sequence), a few
+ * queries at a time are rows of its kernel.
  * Through rows K's and V's values are rounded once more, to fp16 in units of the largest scale of
  * the (sequence, kv head): off by 2^-11 of themselves, or by 2^-25 of that unit where that is more; a weight
  * by 2^-11 of itself, or by 2^-32 of the largest.
  * One way is taken for the whole call, by its longest chunk: beside one of more than 32 queries single tokens
  * have their contexts read back too, and max_query_len is what the write's and the read's grids go by.  Chunks
  * and single tokens are better called apart (paged_decode_attention_q8 for these).
- * paged_prefill_q8_workspace_size() bytes are enough either way: 4 bytes for each of num_seqs *
- * max_context_len * num_kv_heads * head_dim coordinates, or a few MB where that is less; 0: too many rows.
- * paged_prefill_q8_workspace_size_for() are what a call of just these sizes needs: the few MB where it makes no
- * rows; 0: it would be refused (or has nothing to do).
+ * paged_prefill_q8_workspace_size_for() is the workspace for a call of these sizes: a few MB where few queries
+ * are listed; else rows for all sequences at once, 4 bytes for each of num_seqs * max_context_len *
+ * num_kv_heads * head_dim coordinates, or 8 GB of them if that is less, or one sequence's if that is more.
+ * With less, down to one sequence's rows, the sequences are taken in more groups, one after another (the
+ * same bits, more time).  0: the call would be refused, or has nothing to do.
+ * paged_prefill_q8_workspace_size() is enough for any number of queries, all sequences at once; 0: 2^31 rows or more.
  * max_query_len and max_context_len bound every length; longer ones, and sequences of more queries
  * than tokens, raise PKV_DEVERR_CONTEXT_LEN (they are cut; a query before the first token gives
  * zeros).  Rows of no sequence are not written.  A page of scale NaN (see paged_kv_write_q8) makes

@@ -867,7 +867,8 @@ def paged_prefill_q8_workspace_size(num_seqs: int, num_kv_heads: int, head_dim: 
 
 def paged_prefill_q8_workspace_size_for(num_queries: int, max_query_len: int, num_seqs: int, num_q_heads: int,
                                         num_kv_heads: int, head_dim: int, max_context_len: int) -> int:
-    """For a call of just these sizes: where its few queries need no rows, by their number alone."""
+    """For a call of these sizes: a few MB where its few queries need no rows, else rows for all sequences, or 8 GB
+    of them at a time.  (Less is taken too, down to one sequence's rows.)"""
     return int(_lib.paged_prefill_q8_workspace_size_for(num_queries, max_query_len, num_seqs, num_q_heads, num_kv_heads,
                                                         head_dim, max_context_len))
 

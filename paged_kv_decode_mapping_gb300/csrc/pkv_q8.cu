@@ -936,19 +936,39 @@ size_t list_bytes(int32_t num_seqs, int32_t d, int sms) {
   return up(list_q8_workspace(std::min((int64_t)num_seqs * kMaxListPer, (int64_t)kMaxEntries), d, sms));
 }
 
-// The way that a call takes, and its workspace: 0 bytes where no way can be.
+// The tiles take the sequences in groups, as many at a time as the workspace has rows for.  How many, evenly
+// (0: none), and a group's layout.
+int32_t seqs_at_once(int32_t num_seqs, int32_t hkv, int32_t d, int32_t max_len, size_t bytes, PrefillLayout *p) {
+  const size_t one = (size_t)max_len * hkv * d * 4;
+  int32_t n = (int32_t)std::min<size_t>({(size_t)num_seqs, bytes / one, 0x7fffff00ull / hkv / max_len});
+  while (n > 0 && !(prefill_layout(n, hkv, d, max_len, p) && p->total <= bytes)) --n;  // (the rest is small)
+  if (n == 0) return 0;
+  const int32_t groups = (num_seqs + n - 1) / n;
+  n = (num_seqs + groups - 1) / groups;
+  prefill_layout(n, hkv, d, max_len, p);
+  return n;
+}
+// So much is asked for at most, where one context's rows are not more: 3 % of the GPU's memory.  (Groups cost
+// launches that do not fill the GPU: 64 chunks of 40 to 200, one over 32768 tokens and the others over up to 4000,
+// take 0.66 ms at once, in 8.6 GB, and 1.16 in 0.9; 16 of 512 over 32768 each 2.97 in 2.1 GB and 3.50 in 0.8.)
+constexpr size_t kRowsPlenty = size_t(1) << 33;
+
+// The way that a call takes; the workspace that it is best given, 0 bytes where no way can be.
 struct PrefillWay {
   bool list;
   size_t bytes;
-  PrefillLayout tiles;
 };
 PrefillWay prefill_way(int64_t num_queries, int32_t max_query_len, int32_t num_seqs, int32_t hq, int32_t hkv, int32_t d,
                        int32_t max_len, int sms) {
   PrefillWay w = {};
-  const bool rows = prefill_layout(num_seqs, hkv, d, max_len, &w.tiles);
+  PrefillLayout p;
+  const bool rows = prefill_layout(1, hkv, d, max_len, &p);
   w.list = list_fits(max_query_len, num_seqs, hq / hkv, d) &&
            (!rows || list_pays(num_queries, max_query_len, num_seqs, hq, hkv, d, max_len, sms));
-  w.bytes = w.list ? list_bytes(num_seqs, d, sms) : rows ? w.tiles.total : 0;
+  if (w.list)
+    w.bytes = list_bytes(num_seqs, d, sms);
+  else if (rows && seqs_at_once(num_seqs, hkv, d, max_len, std::max(kRowsPlenty, p.total), &p) > 0)
+    w.bytes = p.total;
   return w;
 }
 
@@ -1007,11 +1027,18 @@ PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t
   const int sms = sms_or(152);
   const PrefillWay way = prefill_way(num_queries, max_query_len, num_seqs, num_q_heads, desc->num_kv_heads, desc->head_dim,
                                      max_context_len, sms);
-  const PrefillLayout &p = way.tiles;
   if (way.bytes == 0)
-    return set_error(PKV_ERR_UNSUPPORTED, "%s: the contexts have more than 2^31 rows of heads", fn);
-  if (!workspace || workspace_bytes < way.bytes)
-    return set_error(PKV_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, workspace_bytes, way.bytes);
+    return set_error(PKV_ERR_UNSUPPORTED, "%s: a context has more than 2^31 rows of heads", fn);
+  PrefillLayout p;
+  int32_t at_once = num_seqs;
+  size_t least = way.bytes;
+  if (!way.list) {
+    prefill_layout(1, desc->num_kv_heads, desc->head_dim, max_context_len, &p);
+    least = p.total;
+    at_once = seqs_at_once(num_seqs, desc->num_kv_heads, desc->head_dim, max_context_len, workspace_bytes, &p);
+  }
+  if (!workspace || workspace_bytes < least || at_once == 0)
+    return set_error(PKV_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu needed", fn, workspace_bytes, least);
   if (!aligned16(workspace)) return set_error(PKV_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char *const ws = static_cast<char *>(workspace);
@@ -1023,7 +1050,6 @@ PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t
   l.num_queries = num_queries;
   l.max_query_len = max_query_len;
   l.max_context = (int32_t)std::min<int64_t>((int64_t)max_blocks_per_seq * desc->block_size, max_context_len);
-  l.kv_rows = p.rows;
   l.num_seqs = num_seqs;
   l.num_q_heads = num_q_heads;
   l.num_kv_heads = desc->num_kv_heads;
@@ -1034,30 +1060,38 @@ PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t
     if (!rc) clear_error();
     return rc;
   }
-  const Span span = span_of(block_tables, max_blocks_per_seq, context_lens, query_start, max_context_len, num_seqs, 0, *desc);
-  UnitArgs u;
-  u.s = span;
-  u.k_scale = cache->k_scale;
-  u.v_scale = cache->v_scale;
-  u.k_unit = reinterpret_cast<float *>(ws + p.k_unit);
-  u.v_unit = reinterpret_cast<float *>(ws + p.v_unit);
-  u.nan_from = reinterpret_cast<int32_t *>(ws + p.nan_from);
-  u.order = reinterpret_cast<int4 *>(ws + p.order);
-  u.num_queries = (int32_t)num_queries;
-  u.max_query_len = max_query_len;
-  const cudaError_t e = q8::launch_early(units_q8_kernel, dim3((unsigned)num_seqs), kUnitThreads, 0, s, u);
-  if (e != cudaSuccess) return cuda_error(e, "units_q8_kernel launch");
   const int64_t stride = (int64_t)desc->num_kv_heads * desc->head_dim;
-  rc = launch_read(span, *cache, *desc, ws + p.k, ws + p.v, stride, stride, p.rows, u.k_unit, u.v_unit,
-                   ((int64_t)max_context_len + desc->block_size - 1) / desc->block_size, s);
-  if (rc) return rc;
-  l.k = reinterpret_cast<const uint16_t *>(ws + p.k);
-  l.v = reinterpret_cast<const uint16_t *>(ws + p.v);
-  l.k_unit = u.k_unit;
-  l.v_unit = u.v_unit;
-  l.nan_from = u.nan_from;
-  l.order = u.order;
-  rc = launch_chunk(l, s);
+  for (int32_t b0 = 0; !rc && b0 < num_seqs; b0 += at_once) {
+    const int32_t n = std::min(at_once, num_seqs - b0);
+    const Span span = span_of(block_tables + (int64_t)b0 * max_blocks_per_seq, max_blocks_per_seq, context_lens + b0,
+                              query_start + b0, max_context_len, n, 0, *desc);
+    UnitArgs u;
+    u.s = span;
+    u.k_scale = cache->k_scale;
+    u.v_scale = cache->v_scale;
+    u.k_unit = reinterpret_cast<float *>(ws + p.k_unit);
+    u.v_unit = reinterpret_cast<float *>(ws + p.v_unit);
+    u.nan_from = reinterpret_cast<int32_t *>(ws + p.nan_from);
+    u.order = reinterpret_cast<int4 *>(ws + p.order);
+    u.num_queries = (int32_t)num_queries;
+    u.max_query_len = max_query_len;
+    const cudaError_t e = q8::launch_early(units_q8_kernel, dim3((unsigned)n), kUnitThreads, 0, s, u);
+    if (e != cudaSuccess) return cuda_error(e, "units_q8_kernel launch");
+    rc = launch_read(span, *cache, *desc, ws + p.k, ws + p.v, stride, stride, p.rows, u.k_unit, u.v_unit,
+                     ((int64_t)max_context_len + desc->block_size - 1) / desc->block_size, s);
+    if (rc) return rc;
+    l.query_start = span.start;
+    l.context_lens = span.lens;
+    l.num_seqs = n;
+    l.kv_rows = p.rows;
+    l.k = reinterpret_cast<const uint16_t *>(ws + p.k);
+    l.v = reinterpret_cast<const uint16_t *>(ws + p.v);
+    l.k_unit = u.k_unit;
+    l.v_unit = u.v_unit;
+    l.nan_from = u.nan_from;
+    l.order = u.order;
+    rc = launch_chunk(l, s);
+  }
   if (!rc) clear_error();
   return rc;
 }

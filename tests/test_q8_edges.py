@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import q8_ref as R
-from test_q8_attention import check, decode, decode_ref
+from test_q8_attention import check, decode, decode_ref, poison
 from test_q8_cache import DEV, Batch, starts
 
 pytestmark = pytest.mark.gpu
@@ -254,3 +254,38 @@ def test_chunks_aimed_at_single_keys(B, dtype, d, lens, new, hq, hkv, bs):
         seen = (at <= own).to(DEV)
         assert bool((off[seen] < 0.05).all()) and bool((off[~seen] > 0.5).all())  # a lost or an extra key would show
     assert B.pkv_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", R.KINDS)
+@pytest.mark.parametrize("lens,new,hq,hkv,d,bs", [
+    ([300, 90, 0, 555, 128, 40, 200], [130, 1, 0, 300, 0, 40, 77], 4, 2, 64, 16), ([1000, 129], [100, 129], 3, 1, 128, 32),
+])
+def test_chunks_in_groups_of_sequences(B, dtype, lens, new, hq, hkv, d, bs):
+    """Workspaces for all sequences and for ever fewer, down to one: the same bits, and nothing behind them."""
+    b = Batch(lens, dtype, hkv, d, bs, seed=87)
+    poison(b)
+    q = b.randn(sum(new) + 3, hq, d)
+    full = B.paged_prefill_q8_workspace_size_for(sum(new) + 3, max(new), len(lens), hq, hkv, d, max(lens))
+    one = B.paged_prefill_q8_workspace_size_for(max(new), max(new), 1, hq, hkv, d, max(lens))
+    assert full >= len(lens) * (one - 4096)
+    want, bound = chunk_ref(b, q[:sum(new)], new, 0.125)
+    first = None
+    for size in [full] + [one * n for n in range(len(lens), 0, -1)]:
+        ws = torch.full((size + 4096,), 0xff, dtype=torch.uint8, device=DEV)
+        out = prefill(B, b, q, new, 0.125, workspace=ws[:size])
+        if first is None:
+            first = out
+            check_chunk(out[:sum(new)], want, bound)
+        assert torch.equal(out, first), f"{size} of {full} bytes"
+        assert bool((ws[size:] == 0xff).all()) and bool((out[sum(new):] == 77).all())
+    assert B.pkv_device_errors() == 0
+    # sequences whose rows overlap are cut and flagged, in whatever group
+    start = starts(new)
+    start[2] = 0
+    for size in (full, one):
+        out = torch.full_like(q, 77.0)
+        B.paged_prefill_attention_q8(out, q, *b.cache(), b.bt, b.cl, max(lens), start, sum(new), 0.125,
+                                     workspace=torch.empty(max(size, one), dtype=torch.uint8, device=DEV))
+        assert B.pkv_device_errors() == 4 and bool(out[:sum(new)].isfinite().all())
+    with pytest.raises(B.PkvError, match="workspace"):
+        prefill(B, b, q, new, 0.125, workspace=torch.empty(one - 1, dtype=torch.uint8, device=DEV))

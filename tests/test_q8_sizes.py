@@ -40,16 +40,19 @@ def test_few_queries_need_no_room_for_the_contexts(B):
     for n, new, hq, hkv, d, longest in ((2, 4, 8, 2, 64, 100), (8, 5, 32, 8, 64, 2000), (4, 2048, 24, 8, 128, 8000),
                                         (3, 33, 5, 1, 64, 40), (64, 32, 8, 8, 64, 4000)):
         assert 0 < size(n * new, new, n, hq, hkv, d, longest) <= B.paged_prefill_q8_workspace_size(n, hkv, d, 16, longest)
-    # over 2^31 rows of heads: few queries alone
+    # over 2^31 rows of heads
     assert B.paged_prefill_q8_workspace_size(1024, 8, 64, 16, 1 << 18) == 0
-    assert 0 < size(1024 * 2, 2, 1024, 8, 8, 64, 1 << 18) < 32 << 20 and size(1024 * 40, 40, 1024, 8, 8, 64, 1 << 18) == 0
+    assert 0 < size(1024 * 2, 2, 1024, 8, 8, 64, 1 << 18) < 32 << 20
+    # chunks: 8 GB of rows at a time, or one context's
+    assert 7 << 30 < size(1024 * 40, 40, 1024, 8, 8, 64, 1 << 18) <= 8 << 30
+    assert 8 << 30 <= size(2 * 40, 40, 2, 8, 8, 64, 1 << 22) < (8 << 30) + (1 << 20) and size(40, 40, 1, 8, 8, 64, 1 << 29) == 0
     for bad in ((0, 1, 1, 1, 1, 64, 9), (1, 0, 1, 1, 1, 64, 9), (1, 1, 0, 1, 1, 64, 9), (1, 1, 1, 0, 1, 64, 9), (1, 1, 1, 1, 0, 64, 9),
                 (1, 1, 1, 1, 1, 96, 9), (1, 10, 1, 1, 1, 64, 9), (1, 1, 1, 9, 1, 64, 9), (1, 1, 1, 3, 2, 64, 9)):
         assert size(*bad) == 0
 
 
 def test_a_chunk_is_refused_without_its_rows(B):
-    """Workspaces one byte short, both ways; rows over 2^31 where queries are not few."""
+    """Workspaces one byte short, both ways; a context of over 2^31 rows where queries are not few."""
     fake = ctypes.c_void_p(1 << 20)  # (never dereferenced: each of these calls is refused)
     cache, desc = B.pkv_q8_cache(fake, fake, fake, fake, 0), B.pkv_cache_desc(64, 16, 2, 64)
 
@@ -57,6 +60,7 @@ def test_a_chunk_is_refused_without_its_rows(B):
         return B.lib().paged_prefill_attention_q8(fake, fake, new * n, ctypes.byref(cache), fake, most // 16 + 1, fake, most, fake,
                                                   new, n, 8, ctypes.byref(desc), 0.1, fake, size, None)
 
-    for new, n, most in ((4, 2, 100), (5, 256, 32768), (70, 3, 4000)):
+    for new, n, most in ((4, 2, 100), (5, 256, 32768), (70, 1, 4000), (70, 1, 1 << 22)):
         assert call(new, n, most, B.paged_prefill_q8_workspace_size_for(new * n, new, n, 8, 2, 64, most) - 1) == -4
-    assert call(40, 65535, 1 << 20, 1 << 40) == -3
+    assert call(70, 3, 4000, B.paged_prefill_q8_workspace_size_for(70, 70, 1, 8, 2, 64, 4000) - 1) == -4  # not one sequence's
+    assert call(40, 3, 1 << 30, 1 << 40) == -3
