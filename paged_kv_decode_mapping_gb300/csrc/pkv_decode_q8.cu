@@ -27,7 +27,7 @@
 // of 128, HBM; short batches, the start: 2.5 us until the first box is asked for and 2 for it to come.
 // Measured (one GPU of 152 SMs; a plain copy runs at 6.8 TB/s): 64 contexts of 128 to 4096 keys, 8 kv
 // heads of 128 e4m3 47.2 us, 6.0 TB/s; 256 of 16 to 8192, 4 of 64 int8 41.0 us, 4.7 TB/s; 4 of 32768, 8
-// of 128 int8 46.0 us, 5.8 TB/s; 16 of 2048, 8 of 64 e4m3 13.4 us; one of 128, 8 of 64 5.0 us.
+// of 128 int8 46.5 us, 5.7 TB/s; 16 of 2048, 8 of 64 e4m3 13.4 us; one of 128, 8 of 64 4.9 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

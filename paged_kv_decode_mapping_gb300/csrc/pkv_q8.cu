@@ -126,7 +126,7 @@ __device__ __forceinline__ uint4 rotate_pairs(const uint4 &x, const Angles &a) {
 // a second time).
 // Bound by its instructions (two thirds of the issue slots; widening, two products and two
 // conversions for each pair of codes) and by HBM: 35000 tokens of 8 heads of 128 take 47 us, 4.6
-// TB/s; with k rotated 84, with 24 heads of q besides 147.  256 tokens of a step: 3.6 us, and 2 more where
+// TB/s; with k rotated 80, with 24 heads of q besides 144.  256 tokens of a step: 3.2 us, and 2 more where
 // pages of 16 all grow (30 more with pages of 256).
 
 struct WriteArgs {
