@@ -424,6 +424,7 @@ struct UnitArgs {
   int32_t *nan_from;  // the first key of a page whose scale is NaN
   int4 *order;
   int32_t num_queries, max_query_len;
+  int32_t ahead;  // sequences of earlier groups: theirs are the entries of s.start below 0
 };
 constexpr int kUnitThreads = 1024;
 __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_constant__ UnitArgs a) {
@@ -437,6 +438,8 @@ __global__ void __launch_bounds__(kUnitThreads) units_q8_kernel(const __grid_con
   const int pages = has_queries(a.s, b) ? (int)(((int64_t)L + a.s.block_size - 1) >> a.s.log2_bs) : 0;
   const int32_t *const row = a.s.tables + (int64_t)b * a.s.max_blocks;
   int before = 0, rank = 0;  // the furthest end of the sequences before b; how many are taken before b
+  for (int i = tid - a.ahead; i < 0; i += kUnitThreads)
+    before = max(before, min(max(q8::ld(a.s.start + i + 1), 0), a.num_queries));
   for (int i = tid; i < a.s.num_seqs; i += kUnitThreads) {
     if (i < b) before = max(before, min(max(q8::ld(a.s.start + i + 1), 0), a.num_queries));
     const int Li = min(max(q8::ld(a.s.lens + i), 0), cap);
@@ -1075,6 +1078,7 @@ PKV_API int paged_prefill_attention_q8(pkv_bf16 *out, const pkv_bf16 *q, int64_t
     u.order = reinterpret_cast<int4 *>(ws + p.order);
     u.num_queries = (int32_t)num_queries;
     u.max_query_len = max_query_len;
+    u.ahead = b0;
     const cudaError_t e = q8::launch_early(units_q8_kernel, dim3((unsigned)n), kUnitThreads, 0, s, u);
     if (e != cudaSuccess) return cuda_error(e, "units_q8_kernel launch");
     rc = launch_read(span, *cache, *desc, ws + p.k, ws + p.v, stride, stride, p.rows, u.k_unit, u.v_unit,

@@ -282,10 +282,13 @@ def test_chunks_in_groups_of_sequences(B, dtype, lens, new, hq, hkv, d, bs):
     # sequences whose rows overlap are cut and flagged, in whatever group
     start = starts(new)
     start[2] = 0
-    for size in (full, one):
+    first = None
+    for size in (full, 2 * one, one):
         out = torch.full_like(q, 77.0)
         B.paged_prefill_attention_q8(out, q, *b.cache(), b.bt, b.cl, max(lens), start, sum(new), 0.125,
                                      workspace=torch.empty(max(size, one), dtype=torch.uint8, device=DEV))
         assert B.pkv_device_errors() == 4 and bool(out[:sum(new)].isfinite().all())
+        first = out if first is None else first
+        assert torch.equal(out, first)
     with pytest.raises(B.PkvError, match="workspace"):
         prefill(B, b, q, new, 0.125, workspace=torch.empty(one - 1, dtype=torch.uint8, device=DEV))
